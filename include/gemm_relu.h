@@ -37,7 +37,9 @@ typedef enum {
     GEMM_ERR_LAUNCH = 5,             /* the kernel launch failed */
     GEMM_ERR_TIMEOUT = 6,            /* a device-side wait exceeded its limit (reported later) */
     GEMM_ERR_CUDA = 7,               /* another CUDA runtime error */
-    GEMM_ERR_TOO_LARGE = 8           /* gemm_relu_noalloc: problem outside its fixed scratch */
+    GEMM_ERR_TOO_LARGE = 8,          /* gemm_relu_noalloc: problem outside its fixed scratch; ragged
+                                        products: more tiles than 32 bits count */
+    GEMM_ERR_INDEX = 9               /* offsets or ids outside their range (reported later) */
 } gemm_status_t;
 
 /* Largest accepted M, N or K (TMA coordinates are signed 32-bit). */
@@ -126,6 +128,7 @@ int gemm_relu_host(const void* A_host, const void* B_host, void* C_host,
  * Synchronizes `stream`, then reads and clears the current device's error
  * word.  Returns GEMM_ERR_TIMEOUT if a kernel of this library gave up a
  * bounded wait since the last check (the split-K counters are then reset),
+ * GEMM_ERR_INDEX if a ragged product met offsets or ids outside their range,
  * GEMM_ERR_CUDA if the stream reports a CUDA error, else GEMM_OK.
  *
  * Every device wait of the kernels is bounded (2 s plus 2 us per k-block);
@@ -206,6 +209,81 @@ int gemm_relu_noalloc(const void* A, const void* B, void* C,
  * GEMM_OK.  Like gemm_relu_noalloc, it has no counterpart on the pages.
  */
 int gemm_relu_noalloc_check_device_error(void* stream);
+
+/* ---- Ragged products: rows of one batch that go through different weights -- */
+
+/* Most groups of one grouped call, and largest rank of an adapter. */
+#define GEMM_RELU_MAX_GROUPS 1024
+#define GEMM_RELU_MAX_RANK 512
+
+/*
+ * Products grouped by expert.  The T rows are sorted by group; offsets is a
+ * DEVICE array of G + 1 int32 values, offsets[g] the first row of group g and
+ * offsets[G] the end of the last, non-decreasing and within [0, T].  The host
+ * never reads it, so a router on the same stream can write it.  Any group may
+ * be empty.  Rows of no group (before offsets[0], from offsets[G] on) belong
+ * to no product: Y and dX get +0 there, dW nothing.
+ *
+ *   gemm_relu_grouped      Y[t]  = ReLU(X[t] . W[g]) (or without the ReLU)
+ *   gemm_relu_grouped_dx   dX[t] = (dY[t] . W[g]^T), and +0 where act[t] is
+ *                          not positive (act null: no gate).  act is the
+ *                          activation that went into this product, X itself:
+ *                          where X came out of a ReLU, dX is then the
+ *                          gradient before that ReLU.  act <= 0 and NaN gate.
+ *   gemm_relu_grouped_dw   dW[g] = X[rows of g]^T . dY[rows of g]; +0 for an
+ *                          empty group.  Rows of other groups do not enter,
+ *                          whatever they hold (NaN included).
+ *
+ * X, dX, act: (T, K) row-major with row pitch ldx, ld_dx, ld_act elements;
+ * Y, dY: (T, N) with pitch ldy, ld_dy.  Pitches are at least the width and
+ * multiples of 8.  W, dW: G dense matrices one after another, each (K, N)
+ * row-major (GEMM_B_KN) or (N, K) (GEMM_B_NK).  All hold `dtype` elements;
+ * pointers are 16-byte aligned (offsets 4-byte), K % 8 == 0 and N % 8 == 0.
+ * Output must not overlap an input (not checked).  0 <= G <=
+ * GEMM_RELU_MAX_GROUPS.  A reduction of length 0 (K, N or no row) gives +0.
+ *
+ * Arithmetic as gemm_relu's: exact products accumulated in fp32, one
+ * rounding to nearest-even at the end; results do not depend on the order in
+ * which CTAs run.  Asynchronous on `stream`; the same workspace rules, error
+ * word and bounded waits as gemm_relu.  Offsets that decrease or leave
+ * [0, T] are clamped (nothing outside the tensors is touched, the values are
+ * then unspecified) and reported as GEMM_ERR_INDEX by the next
+ * gemm_relu_check_device_error.
+ */
+int gemm_relu_grouped(const void* X, const void* W, void* Y, const int32_t* offsets,
+                      int64_t T, int64_t G, int64_t N, int64_t K, int64_t ldx, int64_t ldy,
+                      int apply_relu, int b_layout, int dtype, void* stream);
+
+int gemm_relu_grouped_dx(const void* dY, const void* W, void* dX, const int32_t* offsets, const void* act,
+                         int64_t T, int64_t G, int64_t N, int64_t K,
+                         int64_t ld_dy, int64_t ld_dx, int64_t ld_act,
+                         int b_layout, int dtype, void* stream);
+
+int gemm_relu_grouped_dw(const void* X, const void* dY, void* dW, const int32_t* offsets,
+                         int64_t T, int64_t G, int64_t N, int64_t K, int64_t ldx, int64_t ld_dy,
+                         int b_layout, int dtype, void* stream);
+
+/*
+ * One shared weight with a low-rank adapter per row, for a batch of requests
+ * that use different adapters:
+ *
+ *   Y[t] = ReLU( X[t] . W + scale[i] * (X[t] . A[i]^T) . B[i] ),  i = ids[t]
+ *
+ * ids: DEVICE array of T int32 values in [-1, R), in any order; -1 is a row
+ * without adapter.  A: (R, rank, K), B: (R, rank, N), dense; scale: DEVICE
+ * array of R floats, or null for 1.  1 <= rank <= GEMM_RELU_MAX_RANK, R >= 1.
+ * X, W, Y, pitches, types, alignment and stream as gemm_relu_grouped with one
+ * W.  A row depends on its own adapter only, whatever the others hold.
+ *
+ * scale * (X A^T) is accumulated and scaled in fp32 and rounded once to
+ * `dtype` before it meets B; the rest is accumulated in fp32 and rounded once.
+ * An id outside [-1, R) counts as -1 and is reported as GEMM_ERR_INDEX by
+ * the next gemm_relu_check_device_error.
+ */
+int gemm_relu_adapters(const void* X, const void* W, const void* A, const void* B,
+                       const int32_t* ids, const float* scale, void* Y,
+                       int64_t T, int64_t N, int64_t K, int64_t R, int64_t rank, int64_t ldx, int64_t ldy,
+                       int apply_relu, int b_layout, int dtype, void* stream);
 
 /* ---- Host-only planning interface (no CUDA calls; usable without a GPU) -- */
 

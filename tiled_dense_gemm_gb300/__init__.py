@@ -7,12 +7,15 @@ example to draw the seeded workloads in ``workloads``) needs no GPU.
 """
 import importlib
 
-__all__ = ["gemm_relu", "gemm_relu_host", "binding", "workloads"]
+__all__ = ["gemm_relu", "gemm_relu_host", "gemm_relu_grouped", "gemm_relu_grouped_dx", "gemm_relu_grouped_dw",
+           "gemm_relu_adapters", "binding", "workloads"]
+
+_FUNCTIONS = frozenset(__all__[:6]) | {"check_device_error"}
 
 
 def __getattr__(name):
     if name in ("binding", "build", "workloads"):
         return importlib.import_module(f".{name}", __name__)
-    if name in ("gemm_relu", "gemm_relu_host", "check_device_error"):
+    if name in _FUNCTIONS:
         return getattr(importlib.import_module(".binding", __name__), name)
     raise AttributeError(name)

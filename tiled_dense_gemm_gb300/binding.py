@@ -18,7 +18,7 @@ GEMM_OK = 0
 STATUS_NAMES = {
     0: "GEMM_OK", 1: "GEMM_ERR_INVALID_ARG", 2: "GEMM_ERR_ALIGNMENT",
     3: "GEMM_ERR_UNSUPPORTED_DEVICE", 4: "GEMM_ERR_OUT_OF_MEMORY", 5: "GEMM_ERR_LAUNCH",
-    6: "GEMM_ERR_TIMEOUT", 7: "GEMM_ERR_CUDA", 8: "GEMM_ERR_TOO_LARGE",
+    6: "GEMM_ERR_TIMEOUT", 7: "GEMM_ERR_CUDA", 8: "GEMM_ERR_TOO_LARGE", 9: "GEMM_ERR_INDEX",
 }
 
 
@@ -89,6 +89,14 @@ def lib():
         L.gemm_relu_status_string.argtypes = [i32]
         L.gemm_relu_shutdown.restype = None
         L.gemm_relu_shutdown.argtypes = []
+        L.gemm_relu_grouped.restype = i32
+        L.gemm_relu_grouped.argtypes = [vp] * 4 + [i64] * 6 + [i32] * 3 + [vp]
+        L.gemm_relu_grouped_dx.restype = i32
+        L.gemm_relu_grouped_dx.argtypes = [vp] * 5 + [i64] * 7 + [i32] * 2 + [vp]
+        L.gemm_relu_grouped_dw.restype = i32
+        L.gemm_relu_grouped_dw.argtypes = [vp] * 4 + [i64] * 6 + [i32] * 2 + [vp]
+        L.gemm_relu_adapters.restype = i32
+        L.gemm_relu_adapters.argtypes = [vp] * 7 + [i64] * 7 + [i32] * 3 + [vp]
         L.gemm_relu_plan.restype = i32
         L.gemm_relu_plan.argtypes = [i64, i64, i64, i32, ctypes.POINTER(Plan)]
         p32 = ctypes.POINTER(ctypes.c_int32)
@@ -293,6 +301,196 @@ def noalloc_check_device_error(stream=None, device=None):
         rc = lib().gemm_relu_noalloc_check_device_error(_stream_handle(stream, dev))
     if rc != GEMM_OK:
         raise GemmReluError(rc, "device (noalloc)")
+
+
+_DTYPES = None  # {torch type: gemm_dtype_t}, filled on first use (torch is imported lazily)
+
+
+def _dtype_code(*tensors):
+    """gemm_dtype_t of tensors that all have one of the library's types."""
+    global _DTYPES
+    import torch
+    if _DTYPES is None:
+        _DTYPES = {torch.float16: 0, torch.bfloat16: 1}
+    for t in tensors:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("expected torch tensors")
+    dtype = tensors[0].dtype
+    if dtype not in _DTYPES or any(t.dtype != dtype for t in tensors):
+        raise TypeError("the matrices must all be float16 or all bfloat16")
+    return _DTYPES[dtype]
+
+
+def _rows(name, t, rows, width, device):
+    """Row pitch of a (rows, width) matrix whose rows are contiguous."""
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != width:
+        raise ValueError(f"{name} must be ({rows}, {width}), not {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if t.is_contiguous():
+        return width
+    if t.stride(1) != 1 or t.stride(0) < width:
+        raise ValueError(f"{name} must have contiguous rows that do not overlap (call .contiguous())")
+    return t.stride(0)
+
+
+def _stack(name, t, shape, device):
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {shape}, not {tuple(t.shape)}")
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and on {device}")
+
+
+def _index(name, t, count, device):
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
+        raise TypeError(f"{name} must be an int32 tensor")
+    if t.dim() != 1 or (count is not None and t.shape[0] != count):
+        raise ValueError(f"{name} must hold {count} values" if count is not None else f"{name} must be 1-D")
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and on {device}")
+
+
+def _grouped_sizes(first, w, offsets, b_layout, forward):
+    """(T, G, N, K, device) of a grouped product from its row matrix and weights."""
+    if b_layout not in B_LAYOUTS:
+        raise ValueError(f"b_layout must be 'kn' or 'nk', not {b_layout!r}")
+    if first.dim() != 2 or w.dim() != 3:
+        raise ValueError("the rows must be 2-D and the weights 3-D")
+    if not first.is_cuda:
+        raise ValueError("the operands must be CUDA tensors")
+    G = w.shape[0]
+    K, N = (w.shape[1], w.shape[2]) if b_layout == "kn" else (w.shape[2], w.shape[1])
+    if first.shape[1] != (K if forward else N):
+        raise ValueError(f"bad shapes {tuple(first.shape)} and {tuple(w.shape)} ({b_layout})")
+    device = first.device
+    _stack("w", w, tuple(w.shape), device)
+    _index("offsets", offsets, G + 1, device)
+    return first.shape[0], G, N, K, device
+
+
+def gemm_relu_grouped(x, w, offsets, y=None, apply_relu: bool = True, b_layout: str = "kn", stream=None):
+    """y[t] = ReLU(x[t] @ w[g]) for the rows offsets[g] <= t < offsets[g + 1].
+
+    ``x`` (T, K) and ``y`` (T, N) have contiguous rows (any row pitch that is
+    a multiple of 8), ``w`` is (G, K, N), or (G, N, K) for ``b_layout="nk"``;
+    float16 or bfloat16 CUDA tensors.  ``offsets`` is a CUDA int32 tensor of
+    G + 1 values that the host does not read.  Rows of no group get zeros."""
+    import torch
+    dtype = _dtype_code(x, w)
+    T, G, N, K, device = _grouped_sizes(x, w, offsets, b_layout, True)
+    ldx = _rows("x", x, T, K, device)
+    if y is None:
+        y = torch.empty((T, N), dtype=x.dtype, device=device)
+    elif y.dtype != x.dtype:
+        raise TypeError("y must have x's type")
+    ldy = _rows("y", y, T, N, device)
+    rc = _on_device(device, lib().gemm_relu_grouped, x.data_ptr(), w.data_ptr(), y.data_ptr(), offsets.data_ptr(), T,
+                    G, N, K, ldx, ldy, int(bool(apply_relu)), B_LAYOUTS[b_layout], dtype,
+                    _stream_handle(stream, device))
+    if rc != GEMM_OK:
+        raise GemmReluError(rc, "gemm_relu_grouped")
+    return y
+
+
+def gemm_relu_grouped_dx(dy, w, offsets, act=None, dx=None, b_layout: str = "kn", stream=None):
+    """dx[t] = dy[t] @ w[g].T, and zero where ``act`` is given and not positive.
+
+    ``act`` (T, K) is the activation that went into the product (its x): where
+    that came out of a ReLU, dx is the gradient before that ReLU.  Shapes,
+    types and ``offsets`` as ``gemm_relu_grouped``."""
+    import torch
+    dtype = _dtype_code(dy, w) if act is None else _dtype_code(dy, w, act)
+    T, G, N, K, device = _grouped_sizes(dy, w, offsets, b_layout, False)
+    ld_dy = _rows("dy", dy, T, N, device)
+    if dx is None:
+        dx = torch.empty((T, K), dtype=dy.dtype, device=device)
+    elif dx.dtype != dy.dtype:
+        raise TypeError("dx must have dy's type")
+    ld_dx = _rows("dx", dx, T, K, device)
+    ld_act = 0 if act is None else _rows("act", act, T, K, device)
+    rc = _on_device(device, lib().gemm_relu_grouped_dx, dy.data_ptr(), w.data_ptr(), dx.data_ptr(),
+                    offsets.data_ptr(), None if act is None else act.data_ptr(), T, G, N, K, ld_dy, ld_dx, ld_act,
+                    B_LAYOUTS[b_layout], dtype, _stream_handle(stream, device))
+    if rc != GEMM_OK:
+        raise GemmReluError(rc, "gemm_relu_grouped_dx")
+    return dx
+
+
+def gemm_relu_grouped_dw(x, dy, offsets, dw=None, b_layout: str = "kn", stream=None):
+    """dw[g] = x[rows of g].T @ dy[rows of g], (G, K, N), or its transpose
+    (G, N, K) for ``b_layout="nk"``; zero for an empty group."""
+    import torch
+    dtype = _dtype_code(x, dy)
+    if b_layout not in B_LAYOUTS:
+        raise ValueError(f"b_layout must be 'kn' or 'nk', not {b_layout!r}")
+    if x.dim() != 2 or dy.dim() != 2 or x.shape[0] != dy.shape[0]:
+        raise ValueError(f"bad shapes {tuple(x.shape)} and {tuple(dy.shape)}")
+    if not x.is_cuda:
+        raise ValueError("the operands must be CUDA tensors")
+    device = x.device
+    _index("offsets", offsets, None, device)
+    (T, K), N, G = x.shape, dy.shape[1], offsets.shape[0] - 1
+    if G < 0:
+        raise ValueError("offsets must hold at least one value")
+    ldx, ld_dy = _rows("x", x, T, K, device), _rows("dy", dy, T, N, device)
+    shape = (G, K, N) if b_layout == "kn" else (G, N, K)
+    if dw is None:
+        dw = torch.empty(shape, dtype=x.dtype, device=device)
+    elif dw.dtype != x.dtype:
+        raise TypeError("dw must have x's type")
+    else:
+        _stack("dw", dw, shape, device)
+    rc = _on_device(device, lib().gemm_relu_grouped_dw, x.data_ptr(), dy.data_ptr(), dw.data_ptr(),
+                    offsets.data_ptr(), T, G, N, K, ldx, ld_dy, B_LAYOUTS[b_layout], dtype,
+                    _stream_handle(stream, device))
+    if rc != GEMM_OK:
+        raise GemmReluError(rc, "gemm_relu_grouped_dw")
+    return dw
+
+
+def gemm_relu_adapters(x, w, a, b, ids, scale=None, y=None, apply_relu: bool = True, b_layout: str = "kn",
+                       stream=None):
+    """y[t] = ReLU(x[t] @ w + scale[i] * (x[t] @ a[i].T) @ b[i]), i = ids[t].
+
+    ``x`` (T, K), ``w`` (K, N) or (N, K) for ``b_layout="nk"``, ``a``
+    (R, rank, K), ``b`` (R, rank, N): float16 or bfloat16 CUDA tensors;
+    ``ids`` CUDA int32 (T,), -1 for a row without adapter; ``scale`` CUDA
+    float32 (R,) or None for 1."""
+    import torch
+    dtype = _dtype_code(x, w, a, b)
+    if b_layout not in B_LAYOUTS:
+        raise ValueError(f"b_layout must be 'kn' or 'nk', not {b_layout!r}")
+    if x.dim() != 2 or w.dim() != 2 or a.dim() != 3 or b.dim() != 3:
+        raise ValueError("x and w must be 2-D, a and b 3-D")
+    if not x.is_cuda:
+        raise ValueError("the operands must be CUDA tensors")
+    device = x.device
+    T, K = x.shape
+    N, Kw = (w.shape[1], w.shape[0]) if b_layout == "kn" else (w.shape[0], w.shape[1])
+    if Kw != K:
+        raise ValueError(f"bad shapes {tuple(x.shape)} and {tuple(w.shape)} ({b_layout})")
+    R, rank = a.shape[0], a.shape[1]
+    _stack("w", w, tuple(w.shape), device)
+    _stack("a", a, (R, rank, K), device)
+    _stack("b", b, (R, rank, N), device)
+    _index("ids", ids, T, device)
+    if scale is not None:
+        if not isinstance(scale, torch.Tensor) or scale.dtype != torch.float32:
+            raise TypeError("scale must be a float32 tensor")
+        _stack("scale", scale, (R,), device)
+    ldx = _rows("x", x, T, K, device)
+    if y is None:
+        y = torch.empty((T, N), dtype=x.dtype, device=device)
+    elif y.dtype != x.dtype:
+        raise TypeError("y must have x's type")
+    ldy = _rows("y", y, T, N, device)
+    rc = _on_device(device, lib().gemm_relu_adapters, x.data_ptr(), w.data_ptr(), a.data_ptr(), b.data_ptr(),
+                    ids.data_ptr(), None if scale is None else scale.data_ptr(), y.data_ptr(), T, N, K, R, rank, ldx,
+                    ldy, int(bool(apply_relu)), B_LAYOUTS[b_layout], dtype, _stream_handle(stream, device))
+    if rc != GEMM_OK:
+        raise GemmReluError(rc, "gemm_relu_adapters")
+    return y
 
 
 def shutdown():

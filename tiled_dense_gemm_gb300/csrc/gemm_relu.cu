@@ -457,6 +457,7 @@ int reset_after_error_locked(DeviceState& d) {
     for (auto& s : d.streams) {
         if (s.counters) cudaMemset(s.counters, 0, s.counter_bytes);
         if (s.pack_sync) cudaMemset(s.pack_sync, 0, s.pack_sync_bytes);
+        if (s.rg_flags) cudaMemset(s.rg_flags, 0, s.rg_flags_bytes);
     }
     cudaDeviceSynchronize();
     cudaGetLastError();
@@ -501,13 +502,18 @@ extern "C" int gemm_relu_check_device_error(void* stream) {
     std::lock_guard<std::mutex> lock(g_mu);
     DeviceState& d = g_dev[dev];
     if (!d.inited || !d.d_err) return d.inited ? d.status : GEMM_OK;
-    int32_t err = 0;
-    if (cudaMemcpy(&err, d.d_err, sizeof(err), cudaMemcpyDeviceToHost) != cudaSuccess) {
+    int32_t err[2] = {0, 0};
+    if (cudaMemcpy(err, d.d_err, sizeof(err), cudaMemcpyDeviceToHost) != cudaSuccess) {
         cudaGetLastError();
         return GEMM_ERR_CUDA;
     }
-    if (err == 0) return GEMM_OK;
-    return reset_after_error_locked(d);
+    if (err[0] != 0) return reset_after_error_locked(d);
+    if (err[1] != 0) {
+        cudaMemset(d.d_err, 0, 16);
+        cudaGetLastError();
+        return GEMM_ERR_INDEX;
+    }
+    return GEMM_OK;
 }
 
 extern "C" const char* gemm_relu_status_string(int status) {
@@ -521,6 +527,7 @@ extern "C" const char* gemm_relu_status_string(int status) {
         case GEMM_ERR_TIMEOUT: return "GEMM_ERR_TIMEOUT";
         case GEMM_ERR_CUDA: return "GEMM_ERR_CUDA";
         case GEMM_ERR_TOO_LARGE: return "GEMM_ERR_TOO_LARGE";
+        case GEMM_ERR_INDEX: return "GEMM_ERR_INDEX";
         default: return "GEMM_ERR_UNKNOWN";
     }
 }
@@ -541,6 +548,9 @@ extern "C" void gemm_relu_shutdown(void) {
                 cudaFree(s.counters);
                 cudaFree(s.packed);
                 cudaFree(s.pack_sync);
+                cudaFree(s.rg_ws);
+                cudaFree(s.rg_flags);
+                cudaFree(s.rg_misc);
                 cudaFree(s.hA);
                 cudaFree(s.hB);
                 cudaFree(s.hC);

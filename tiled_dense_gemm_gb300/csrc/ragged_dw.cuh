@@ -1,0 +1,342 @@
+// Weight gradients of ragged groups, for sm_103a:
+//
+//   D[g] (P x Q) = U[rows of g, :]^T V[rows of g, :]
+//
+// a product whose reduction runs over the rows of group g, so its length is
+// known on the device only.  Both operands are read as stored (rows of P or
+// Q contiguous elements): MN-major for the tensor core, no transposition.
+//
+// A group may end anywhere inside a 128-row block.  The rows after it belong
+// to another group and must not enter the sum, whatever they hold (0 x NaN is
+// NaN), so each group reads through its own pair of tensor maps whose row
+// extent ends with the group: the copies fill the rows beyond with zeros and
+// fetch nothing for them.  A small kernel before this one makes the maps from
+// the host's by setting that one extent (one warp per group), and orders the
+// groups by length, longest first, so that the last items of the persistent
+// grid are short ones.
+//
+// Tile 128 x 128 per CTA, or 256 x 256 per CTA pair; stages of 128 rows; roles
+// and waits as in the ragged forward kernel.
+#pragma once
+
+#include "ragged_kernel.cuh"
+
+namespace gr {
+namespace rg {
+
+struct DwGroup {
+    int32_t g, lo, hi, pad;
+};
+
+struct DwMaps {
+    CUtensorMap d;  // the gradients, 3-D
+};
+
+struct DwParams {
+    int32_t T, G, P, Q;
+    int32_t p_tiles, q_tiles;
+    int32_t num_stages;
+    int32_t u3d, v3d;     // one copy per stage of the operand's two 64-column chunks
+    int32_t bf16;
+    const DwGroup* groups;      // by length, longest first
+    const CUtensorMap* maps;    // [2 * position]: U's and V's of that group
+    int32_t* err;
+    uint64_t timeout_ns;
+};
+
+struct DwPrepMaps {
+    CUtensorMap u, v;
+};
+
+// One warp per group g: its position by length, its bounds, its two maps.
+__global__ void __launch_bounds__(32) dw_prep_kernel(const __grid_constant__ DwPrepMaps base, const int32_t* offsets,
+                                                     int32_t G, int32_t T, DwGroup* groups, CUtensorMap* maps,
+                                                     int32_t* err) {
+    __shared__ __align__(128) CUtensorMap edit[2];
+    const int32_t g = (int32_t)blockIdx.x, lane = (int32_t)threadIdx.x;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    // clamped to [0, T] and to be non-decreasing, as the forward kernel reads them
+    const int32_t a = __ldcg(offsets + g), b = __ldcg(offsets + g + 1);
+    const int32_t mine = min(max(b, 0), T) - min(max(a, 0), T);
+    int32_t before = 0, lo = 0;
+    for (int32_t j = lane; j < G; j += 32) {
+        const int32_t x = min(max(__ldcg(offsets + j), 0), T), y = min(max(__ldcg(offsets + j + 1), 0), T);
+        const int32_t len = y - x;
+        before += (len > mine || (len == mine && j < g)) ? 1 : 0;
+        if (j <= g) lo = max(lo, x);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        before += __shfl_xor_sync(0xffffffffu, before, d);
+        lo = max(lo, __shfl_xor_sync(0xffffffffu, lo, d));
+    }
+    const int32_t hi = max(lo, min(max(b, 0), T));
+    if (lane == 0) {
+        if (a != min(max(a, 0), T) || b != min(max(b, 0), T) || b < a) atomicCAS(err + 1, 0, (int32_t)kBadOffsets);
+        DwGroup o;
+        o.g = g;
+        o.lo = lo;
+        o.hi = hi;
+        o.pad = 0;
+        groups[before] = o;
+    }
+    reinterpret_cast<uint32_t*>(&edit[0])[lane] = reinterpret_cast<const uint32_t*>(&base.u)[lane];
+    reinterpret_cast<uint32_t*>(&edit[1])[lane] = reinterpret_cast<const uint32_t*>(&base.v)[lane];
+    __syncwarp();
+    if (lane == 0 && hi > lo) {
+        map_set_rows(smem_u32(&edit[0]), (uint32_t)hi);
+        map_set_rows(smem_u32(&edit[1]), (uint32_t)hi);
+    }
+    __syncwarp();
+    map_publish(maps + 2 * before, smem_u32(&edit[0]));
+    map_publish(maps + 2 * before + 1, smem_u32(&edit[1]));
+}
+
+template <bool kPair>
+__global__ void __launch_bounds__(kThreads, 1)
+    ragged_dw_kernel(const __grid_constant__ DwMaps out, const __grid_constant__ DwParams q) {
+    constexpr int kCG = kPair ? 2 : 1;
+    constexpr uint32_t kTile = kPair ? 256 : 128;  // rows and columns of D per tile
+    constexpr uint32_t kCols = kTile;              // TMEM columns per accumulator
+    constexpr uint32_t kOperand = 128 * kBK * 2;   // bytes per operand, stage and CTA
+    constexpr uint32_t stride = 2 * kOperand;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem);
+    const uint32_t ring = (smem_u32(smem) + (uint32_t)sizeof(Ctrl) + 1023u) & ~1023u;
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = kPair ? cluster_ctarank() : 0u;
+    const uint32_t worker = kPair ? blockIdx.x / 2 : blockIdx.x;
+    const uint32_t workers = kPair ? gridDim.x / 2 : gridDim.x;
+    Params w;  // what wait_phase reads
+    w.err = q.err;
+    w.timeout_ns = q.timeout_ns;
+
+    if (warp == 2 && lane == 0) {
+        for (int s = 0; s < q.num_stages; ++s) {
+            mbar_init(smem_u32(&ctrl->full[s]), 1);
+            mbar_init(smem_u32(&ctrl->empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&ctrl->tmem_full[b]), 1);
+            mbar_init(smem_u32(&ctrl->tmem_empty[b]), (kPair ? 2u : 1u) * (kEpiThreads / 32));
+        }
+        mbar_init(smem_u32(&ctrl->final_bar), 1);
+        ctrl->abort_flag = 0;
+        ctrl->ring_s = ctrl->ring_ph = ctrl->ring_lap = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc<kCG>(smem_u32(&ctrl->tmem_addr), 2 * kCols);
+        tmem_relinquish<kCG>();
+    }
+    __syncwarp();
+    tc_fence_before();
+    if (kPair)
+        cluster_sync();
+    else
+        cta_barrier_sync();
+    tc_fence_after();
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const uint32_t tmem_base = ctrl->tmem_addr;
+    const uint32_t S = (uint32_t)q.num_stages;
+    const uint32_t full0 = smem_u32(&ctrl->full[0]), empty0 = smem_u32(&ctrl->empty[0]);
+    const uint32_t per_group = (uint32_t)(q.p_tiles * q.q_tiles);
+    const uint32_t items = (uint32_t)q.G * per_group;
+
+    // item -> position in the length order, tile; groups without a row have no k-block
+    struct Work {
+        int32_t pos, g, lo, hi, pt, qt;
+    };
+    auto fetch = [&](uint32_t item) {
+        Work k;
+        k.pos = (int32_t)(item / per_group);
+        const uint32_t l = item - (uint32_t)k.pos * per_group;
+        k.qt = (int32_t)(l / (uint32_t)q.p_tiles);
+        k.pt = (int32_t)(l - (uint32_t)k.qt * (uint32_t)q.p_tiles);
+        const int4 d = __ldcg(reinterpret_cast<const int4*>(q.groups + k.pos));
+        k.g = d.x;
+        k.lo = d.y;
+        k.hi = d.z;
+        return k;
+    };
+
+    if (warp == 0 || warp == 6) {
+        // warp 0 copies U's tiles and arms the stages, warp 6 V's
+        if (lane == 0) {
+            const bool is_u = warp == 0;
+            uint32_t s = 0, ph = 0;
+            int32_t issued = 0, seen = -1;
+            bool ok = true;
+            for (uint32_t item = worker; ok && item < items; item += workers) {
+                const Work k = fetch(item);
+                if (k.hi == k.lo) continue;
+                const CUtensorMap* m = q.maps + 2 * k.pos + (is_u ? 0 : 1);
+                if (k.pos != seen) map_acquire(m);
+                seen = k.pos;
+                const int32_t c0 = (is_u ? k.pt : k.qt) * (int32_t)kTile + 128 * (int32_t)rank;
+                for (int32_t r = k.lo; r < k.hi; r += kBK) {
+                    if (!wait_phase(empty0 + 8u * s, ph ^ 1u, ctrl, w, is_u ? kErrTokens : kErrWeights)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t full = full0 + 8u * s;
+                    if (is_u) {
+                        if (!kPair || rank == 0) mbar_arrive_expect_tx(full, (kPair ? 2u : 1u) * stride);
+                        ++issued;
+                    }
+                    const uint32_t bar = kPair ? mapa_shared(full, 0) : full;
+                    const uint32_t dst = ring + s * stride + (is_u ? 0u : kOperand);
+                    if (is_u ? q.u3d : q.v3d) {
+                        load_3d<kPair>(dst, m, bar, 0, r, c0 / 64);
+                    } else {
+                        load_2d<kPair>(dst, m, bar, c0, r);
+                        load_2d<kPair>(dst + (uint32_t)kBK * 128u, m, bar, c0 + 64, r);
+                    }
+                    if (++s == S) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            if (is_u && (!kPair || rank == 0)) {
+                ctrl->ring_s = (int32_t)s;
+                ctrl->ring_ph = (int32_t)ph;
+                ctrl->ring_lap = issued >= (int32_t)S ? 1 : 0;
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0 && (!kPair || rank == 0)) {
+            const uint32_t tfull0 = smem_u32(&ctrl->tmem_full[0]), tempty0 = smem_u32(&ctrl->tmem_empty[0]);
+            const uint32_t idesc = make_idesc_f16_f32(kTile, kTile, true, true, q.bf16 != 0);
+            const uint64_t a_desc0 = make_sw128_desc(ring, (uint32_t)kBK * 128u, 1024);
+            const uint64_t b_desc0 = make_sw128_desc(ring + kOperand, (uint32_t)kBK * 128u, 1024);
+            uint32_t s = 0, ph = 0, local = 0;
+            bool ok = true;
+            for (uint32_t item = worker; ok && item < items; item += workers) {
+                const Work k = fetch(item);
+                if (k.hi == k.lo) continue;
+                const uint32_t buf = local & 1u, bph = (local >> 1) & 1u;
+                if (!wait_phase(tempty0 + 8u * buf, bph ^ 1u, ctrl, w, kErrAccum)) break;
+                tc_fence_after();
+                const uint32_t d = tmem_base + buf * kCols;
+                uint32_t acc = 0;
+                for (int32_t r = k.lo; r < k.hi; r += kBK) {
+                    if (!wait_phase(full0 + 8u * s, ph, ctrl, w, kErrStage)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t a_desc = a_desc0 + (uint64_t)(s * (stride >> 4));
+                    const uint64_t b_desc = b_desc0 + (uint64_t)(s * (stride >> 4));
+                    if (k.hi - r >= kBK) {
+#pragma unroll
+                        for (uint32_t i = 0; i < kBK / 16; ++i)
+                            mma_f16_ss<kCG>(d, a_desc + i * 128u, b_desc + i * 128u, idesc, i > 0 ? 1u : acc);
+                    } else {
+                        const uint32_t steps = (uint32_t)(k.hi - r + 15) / 16;  // the rest of the block is zeros
+                        for (uint32_t i = 0; i < steps; ++i)
+                            mma_f16_ss<kCG>(d, a_desc + i * 128u, b_desc + i * 128u, idesc, i > 0 ? 1u : acc);
+                    }
+                    acc = 1;
+                    mma_commit<kCG>(empty0 + 8u * s, 0x3);
+                    if (++s == S) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                mma_commit<kCG>(tfull0 + 8u * buf, 0x3);
+                ++local;
+            }
+            mma_commit<kCG>(smem_u32(&ctrl->final_bar), 0x1);
+            const uint64_t t0 = globaltimer_ns();
+            while (!mbar_try_wait(smem_u32(&ctrl->final_bar), 0))
+                if (globaltimer_ns() - t0 > q.timeout_ns) {
+                    atomicCAS(q.err, 0, (int32_t)kErrFinal);
+                    break;
+                }
+        }
+        __syncwarp();
+    } else {
+        const uint32_t quarter = warp & 3u;
+        const uint32_t staging = ring + S * stride + quarter * 8192u;  // two 4 KiB buffers per warp
+        uint32_t sbuf = 0, local = 0;
+        for (uint32_t item = worker; item < items; item += workers) {
+            const Work k = fetch(item);
+            const bool some = k.hi > k.lo;
+            const uint32_t buf = local & 1u, bph = (local >> 1) & 1u;
+            if (some) {
+                bool ok = wait_phase(smem_u32(&ctrl->tmem_full[buf]), bph, ctrl, w, kErrEpi);
+                ok = named_bar_and(kEpiBarrier, kEpiThreads, ok);
+                if (!ok) break;
+                tc_fence_after();
+            }
+            const uint32_t taddr = tmem_base + ((quarter * 32u) << 16) + buf * kCols;
+            const int32_t row0 = k.pt * (int32_t)kTile + 128 * (int32_t)rank + 32 * (int32_t)quarter;
+            for (uint32_t c = 0; c < kCols; c += 64) {
+                const int32_t col = k.qt * (int32_t)kTile + (int32_t)c;
+                if (col >= q.Q) break;  // (uniform over the warp)
+                float v[64];
+                if (some) {
+                    __syncwarp();
+                    tmem_load_64cols(taddr + c, v);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) v[j] = 0.0f;
+                }
+                if (row0 >= q.P) continue;
+                // the copy issued from this buffer two chunks ago must have read it
+                if (lane == 0) bulk_wait_group_read<1>();
+                __syncwarp();
+                const uint32_t buf_addr = staging + sbuf * 4096u;
+#pragma unroll
+                for (uint32_t u = 0; u < 8; ++u) {
+                    uint4 x;
+                    x.x = pack16(v[8 * u + 0], v[8 * u + 1], q.bf16);
+                    x.y = pack16(v[8 * u + 2], v[8 * u + 3], q.bf16);
+                    x.z = pack16(v[8 * u + 4], v[8 * u + 5], q.bf16);
+                    x.w = pack16(v[8 * u + 6], v[8 * u + 7], q.bf16);
+                    st_shared_v4(buf_addr + lane * 128u + ((u ^ (lane & 7u)) << 4), x);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    store_3d(&out.d, buf_addr, col, row0, k.g);
+                    bulk_commit_group();
+                }
+                sbuf ^= 1u;
+            }
+            if (some) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (kPair)
+                        mbar_arrive_cluster(mapa_shared(smem_u32(&ctrl->tmem_empty[buf]), 0));
+                    else
+                        mbar_arrive(smem_u32(&ctrl->tmem_empty[buf]));
+                }
+                ++local;
+            }
+        }
+        if (lane == 0) bulk_wait_group_all();
+        __syncwarp();
+    }
+
+    __syncthreads();
+    if (threadIdx.x == 0 && *(volatile int32_t*)&ctrl->abort_flag) drain_ring(ctrl, full0, S);
+    tc_fence_before();
+    if (kPair)
+        cluster_sync_relaxed();
+    else
+        __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc<kCG>(tmem_base, 2 * kCols);
+    }
+}
+
+}  // namespace rg
+}  // namespace gr

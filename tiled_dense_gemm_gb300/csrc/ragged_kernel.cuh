@@ -1,0 +1,813 @@
+// Products of ragged rows with several weights, for sm_103a:
+//
+//   Y[t, :] = epilogue( sum_k X[t, k] W[g(t)][k, :] )
+//
+// where the rows t are sorted by group and only the device knows how many
+// rows each group has (experts' products, forward and data gradient), or
+// where every row shares one W and adds a low-rank part of its own adapter
+// (kAdapters).
+//
+// Operand roles.  The weights are the MMA's M side (128 output columns per
+// CTA, 256 per CTA pair) and the rows its N side: tcgen05's N goes in steps
+// of 16 at run time, so a group of any size costs its rows rounded up to 16
+// (32 for a pair), not to a 128- or 256-row tile, and a group of a few rows
+// streams its weights with next to no MMA work.  D^T sits in tensor memory
+// with an output column per lane and a row per TMEM column, so masking the
+// rows past a group's end is a uniform branch per store.
+//
+// Work list.  Each CTA reads the G + 1 row offsets once and builds two
+// prefix arrays in shared memory (first row, row tiles before the group);
+// item i is then (group, row tile, column tile) by binary search, with no
+// host round trip and no launch of its own.  A group's rows are cut into
+// tiles of equal width, so 260 rows are 144 + 116 and not 256 + 4.
+//
+// Roles (224 threads, one CTA per SM): warp 0 copies row tiles (and builds
+// the adapters' tiles), warp 6 the weights, warp 1 issues the MMAs, warps 2-5
+// drain the accumulators; shared-memory ring of 128-k stages, two TMEM
+// accumulators.  Every wait is bounded.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "ptx.cuh"
+#include "ragged_ptx.cuh"
+
+namespace gr {
+namespace rg {
+
+constexpr int kThreads = 224;
+constexpr uint32_t kEpiThreads = 128;
+constexpr uint32_t kEpiBarrier = 1;
+constexpr int kBK = 128;       // k-rows per ring stage: eight MMAs per wait and commit
+constexpr int kMaxStages = 8;
+constexpr int kTokBoxes = 8;   // row-tile boxes of 16, 32, ..., 128 rows per CTA
+constexpr int kRaster = 8;     // row tiles of one group walked together, column tile by column tile
+constexpr uint32_t kWBytes = 128 * kBK * 2;  // weights per stage and CTA
+
+enum : int32_t {
+    kErrTokens = 0x61,
+    kErrWeights = 0x62,
+    kErrStage = 0x63,
+    kErrAccum = 0x64,
+    kErrEpi = 0x65,
+    kErrFinal = 0x66,
+};
+// codes of the second error word (bad values in an index array)
+enum : int32_t { kBadOffsets = 1, kBadIds = 2 };
+
+struct Maps {
+    CUtensorMap w;             // weights
+    CUtensorMap x[kTokBoxes];  // rows, boxes of 16 (i + 1) rows
+    CUtensorMap b;             // adapters' second factors
+};
+
+struct Params {
+    int32_t T, G;        // rows of X; groups (1: all rows)
+    int32_t N, K;        // output columns, reduction length
+    int32_t num_kb;      // ceil(K / kBK)
+    int32_t n_tiles;     // column tiles (128, or 256 for a pair)
+    int32_t cap;         // most rows of a tile
+    int32_t split;       // 1: the k-blocks of all items are cut into equal contiguous runs, one per CTA
+    int32_t num_stages;
+    int32_t stage_bytes; // stride of a ring stage
+    int32_t table_off;   // shared-memory offset of the prefix arrays, from the ring's start
+    uint32_t tmem_cols;  // allocated; half of them per accumulator
+    int32_t w_kmajor;    // weights stored with the reduction contiguous
+    int32_t w4d;         // one copy per stage and CTA of the weights
+    int32_t x3d;         // one copy per stage of a row tile
+    int32_t apply_relu, bf16;
+    const int32_t* offsets;  // G + 1, or null: one group of all rows
+    uint16_t* Y;
+    int64_t ldy;
+    const uint16_t* act;     // gate: outputs where act <= 0 are set to +0 (null: none)
+    int64_t ld_act;
+    float* ws;               // split: one fp32 partial tile per CTA
+    uint32_t* flags;         // split: that partial is published (zero between launches)
+    int32_t* err;            // err[0] timed-out waits, err[1] bad index arrays
+    uint64_t timeout_ns;
+    // adapters
+    const int32_t* ids;      // adapter of each row, -1 none
+    const uint16_t* low;     // (T, rank_pad): scale * x A^T, rounded to the element type
+    const int32_t* nslots;   // distinct adapters of each row tile
+    const int32_t* slots;    // [tile][cap] their indexes
+    int32_t rank_pad, rank_box, b4d;
+    int32_t R;
+};
+
+struct __align__(8) Ctrl {
+    uint64_t full[kMaxStages];
+    uint64_t empty[kMaxStages];
+    uint64_t tmem_full[2];
+    uint64_t tmem_empty[2];
+    uint64_t final_bar;
+    uint32_t tmem_addr;
+    int32_t abort_flag;
+    int32_t ring_s, ring_ph, ring_lap;
+    int32_t max_extra;  // adapters: most extra k-blocks of a row tile
+};
+static_assert(sizeof(Ctrl) <= 1024, "control block exceeds its reserved 1 KiB");
+
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, Ctrl* ctrl, const Params& p, int32_t site) {
+    if (mbar_try_wait(bar, parity)) return true;
+    volatile int32_t* abort_flag = &ctrl->abort_flag;
+    const uint64_t t0 = globaltimer_ns();
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (*abort_flag) return false;
+        if (globaltimer_ns() - t0 > p.timeout_ns) {
+            *abort_flag = 1;
+            atomicCAS(p.err, 0, site);
+            return false;
+        }
+    }
+}
+
+// Bounded wait (100 us in all) for the copies that an aborting CTA has in
+// flight, before its shared memory is released.
+__device__ __forceinline__ void drain_ring(Ctrl* ctrl, uint32_t full0, uint32_t S) {
+    const uint64_t t0 = globaltimer_ns();
+    const uint32_t ring_s = (uint32_t)ctrl->ring_s, ring_ph = (uint32_t)ctrl->ring_ph;
+    for (uint32_t i = 0; i < S; ++i) {
+        if (i >= ring_s && !ctrl->ring_lap) continue;  // never armed
+        const uint32_t parity = i < ring_s ? ring_ph : ring_ph ^ 1u;
+        while (!mbar_try_wait(full0 + 8u * i, parity))
+            if (globaltimer_ns() - t0 > 100000ull) return;
+    }
+}
+
+// ------------------------------------------------------------------ work list
+
+// Prefix arrays of the groups, by one warp: start[g] = first row of group g
+// (start[G]: end of the last), tiles[g] = row tiles before it.  Offsets are
+// clamped to [0, T] and to be non-decreasing, so no later index can leave the
+// tensors; if that changed any, bad index arrays are reported.
+__device__ __forceinline__ void build_table(const Params& p, int32_t* start, int32_t* tiles, uint32_t lane) {
+    if (!p.offsets) {
+        if (lane == 0) {
+            start[0] = 0;
+            start[1] = p.T;
+            tiles[0] = 0;
+            tiles[1] = (p.T + p.cap - 1) / p.cap;
+        }
+        return;
+    }
+    bool bad = false;
+    int32_t top = 0, count = 0;  // running maximum and tile count before this round
+    for (int32_t g0 = 0; g0 < p.G; g0 += 32) {
+        const int32_t g = g0 + (int32_t)lane;
+        int32_t lo = 0, hi = 0;
+        if (g < p.G) {
+            const int32_t a = __ldcg(p.offsets + g), b = __ldcg(p.offsets + g + 1);
+            lo = min(max(a, 0), p.T);
+            hi = min(max(b, 0), p.T);
+            bad |= a != lo || b != hi || hi < lo;
+        }
+        // inclusive maximum of lo over the lanes, and of every offset before
+        int32_t m = max(lo, top);
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int32_t o = __shfl_up_sync(0xffffffffu, m, d);
+            if ((int)lane >= d) m = max(m, o);
+        }
+        const int32_t end = max(m, hi);
+        int32_t n = g < p.G ? (end - m + p.cap - 1) / p.cap : 0;
+        const int32_t mine = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int32_t o = __shfl_up_sync(0xffffffffu, n, d);
+            if ((int)lane >= d) n += o;
+        }
+        if (g < p.G) {
+            start[g] = m;
+            tiles[g] = count + n - mine;
+            if (g == p.G - 1) {
+                start[p.G] = end;
+                tiles[p.G] = count + n;
+            }
+        }
+        const int32_t last = min(31, p.G - 1 - g0);
+        top = __shfl_sync(0xffffffffu, end, last);
+        count += __shfl_sync(0xffffffffu, n, last);
+    }
+    if (bad) atomicCAS(p.err + 1, 0, (int32_t)kBadOffsets);
+}
+
+struct Item {
+    int32_t g;          // group
+    int32_t tile;       // row tile (over all groups)
+    int32_t row0;       // first row
+    int32_t valid;      // rows of this tile
+    int32_t w;          // rows rounded up to the MMA's granularity
+    int32_t n;          // column tile
+    int32_t kb0, kb1;   // k-blocks [kb0, kb1) of `kb_all`
+    int32_t kb_all;
+    uint32_t index;     // item number
+};
+
+// Extra k-blocks of a row tile: its distinct adapters' ranks side by side.
+__device__ __forceinline__ int32_t extra_blocks(const Params& p, int32_t slots) {
+    return (slots * p.rank_pad + kBK - 1) / kBK;
+}
+
+template <bool kPair, bool kAdapters>
+struct Iter {
+    const Params& p;
+    const int32_t* start;
+    const int32_t* tiles;
+    uint32_t u, u1, step;
+    int32_t kb_all;  // split: k-blocks of every item (adapters: with the most extra ones)
+
+    __device__ __forceinline__ Iter(const Params& p_, const int32_t* start_, const int32_t* tiles_, uint32_t worker,
+                                    uint32_t workers, int32_t max_extra)
+        : p(p_), start(start_), tiles(tiles_) {
+        const uint32_t items = (uint32_t)tiles[p.G] * (uint32_t)p.n_tiles;
+        kb_all = p.num_kb + (kAdapters ? max_extra : 0);
+        if (!kPair && p.split) {
+            const uint32_t units = items * (uint32_t)kb_all;
+            u = begin_of(units, worker, workers);
+            u1 = begin_of(units, worker + 1, workers);
+            step = 0;
+        } else {
+            u = worker;
+            u1 = items;
+            step = workers;
+        }
+    }
+
+    static __device__ __forceinline__ uint32_t begin_of(uint32_t units, uint32_t worker, uint32_t workers) {
+        const uint32_t q = units / workers, r = units - q * workers;
+        return worker * q + min(worker, r);
+    }
+
+    __device__ __forceinline__ bool next(Item& it) {
+        if (u >= u1) return false;
+        uint32_t item;
+        if (!kPair && p.split) {
+            item = u / (uint32_t)kb_all;
+            it.kb0 = (int32_t)(u - item * (uint32_t)kb_all);
+            it.kb1 = (int32_t)min((uint32_t)kb_all, (uint32_t)it.kb0 + (u1 - u));
+            u += (uint32_t)(it.kb1 - it.kb0);
+            it.kb_all = kb_all;
+        } else {
+            item = u;
+            u += step;
+            it.kb0 = 0;
+        }
+        it.index = item;
+        const uint32_t nt = (uint32_t)p.n_tiles;
+        const int32_t rt = (int32_t)(item / nt);
+        int32_t lo = 0, hi = p.G;  // largest g with tiles[g] <= rt
+        while (hi - lo > 1) {
+            const int32_t mid = (lo + hi) >> 1;
+            if (tiles[mid] <= rt) lo = mid; else hi = mid;
+        }
+        it.g = lo;
+        const int32_t first = tiles[lo], cnt = tiles[lo + 1] - first;
+        const uint32_t l = item - (uint32_t)first * nt;
+        const uint32_t band = l / (kRaster * nt);
+        const uint32_t r = l - band * (kRaster * nt);
+        const uint32_t rows = min((uint32_t)kRaster, (uint32_t)cnt - band * kRaster);
+        it.n = (int32_t)(r / rows);
+        const int32_t j = (int32_t)(band * kRaster + r - (uint32_t)it.n * rows);
+        it.tile = first + j;
+        const int32_t s0 = start[lo], len = start[lo + 1] - s0;
+        constexpr int32_t kGran = kPair ? 32 : 16;
+        it.w = ((len + cnt - 1) / cnt + kGran - 1) / kGran * kGran;
+        it.row0 = s0 + j * it.w;
+        it.valid = min(it.w, len - j * it.w);
+        if (kPair || !p.split) {
+            it.kb_all = p.num_kb + (kAdapters ? extra_blocks(p, __ldcg(p.nslots + it.tile)) : 0);
+            it.kb1 = it.kb_all;
+        }
+        return true;
+    }
+};
+
+// ------------------------------------------------------------------ numbers
+
+__device__ __forceinline__ uint16_t round16(float x, int32_t bf16) {
+    if (bf16) return __bfloat16_as_ushort(__float2bfloat16_rn(x));
+    return __half_as_ushort(__float2half_rn(x));
+}
+
+// Two values rounded to nearest-even 16-bit floats, a in the low half.
+__device__ __forceinline__ uint32_t pack16(float a, float b, int32_t bf16) {
+    if (bf16) {
+        __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<uint32_t*>(&h);
+    }
+    __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&h);
+}
+
+// x > 0 for 16-bit floats of either type: sign clear, not zero, not NaN
+__device__ __forceinline__ bool positive16(uint16_t x, int32_t bf16) {
+    return x != 0 && x <= (bf16 ? 0x7F80u : 0x7C00u);
+}
+
+// ------------------------------------------------------------------ kernel
+
+template <bool kPair, bool kAdapters>
+__global__ void __launch_bounds__(kThreads, 1)
+    ragged_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
+    constexpr int kCG = kPair ? 2 : 1;
+    using It = Iter<kPair, kAdapters>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem);
+    const uint32_t ring = (smem_u32(smem) + (uint32_t)sizeof(Ctrl) + 1023u) & ~1023u;
+    int32_t* const start = reinterpret_cast<int32_t*>(smem + (ring - smem_u32(smem)) + p.table_off);
+    int32_t* const tiles = start + p.G + 1;
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = kPair ? cluster_ctarank() : 0u;
+    const uint32_t worker = kPair ? blockIdx.x / 2 : blockIdx.x;
+    const uint32_t workers = kPair ? gridDim.x / 2 : gridDim.x;
+
+    if (warp == 2 && lane == 0) {
+        for (int s = 0; s < p.num_stages; ++s) {
+            // a pair of the adapters' kernel: the peer's row producer arrives too (it may have built its half itself)
+            mbar_init(smem_u32(&ctrl->full[s]), (kPair && kAdapters) ? 2 : 1);
+            mbar_init(smem_u32(&ctrl->empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&ctrl->tmem_full[b]), 1);
+            mbar_init(smem_u32(&ctrl->tmem_empty[b]), (kPair ? 2u : 1u) * (kEpiThreads / 32));
+        }
+        mbar_init(smem_u32(&ctrl->final_bar), 1);
+        ctrl->abort_flag = 0;
+        ctrl->ring_s = ctrl->ring_ph = ctrl->ring_lap = 0;
+        ctrl->max_extra = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc<kCG>(smem_u32(&ctrl->tmem_addr), p.tmem_cols);
+        tmem_relinquish<kCG>();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&maps.w);
+        tma_prefetch_desc(&maps.x[0]);
+    }
+    grid_launch_dependents();
+    grid_dependency_wait();  // nothing before this reads or writes global memory
+    if (warp == 6) build_table(p, start, tiles, lane);
+    __syncwarp();
+    tc_fence_before();
+    if (kPair)
+        cluster_sync();
+    else
+        cta_barrier_sync();
+    tc_fence_after();
+    if constexpr (kAdapters) {
+        if (p.split) {
+            // items of equal length: as many extra k-blocks as the tile with the most adapters
+            int32_t m = 0;
+            for (int32_t i = (int32_t)threadIdx.x; i < tiles[p.G]; i += kThreads) m = max(m, __ldcg(p.nslots + i));
+            atomicMax(&ctrl->max_extra, extra_blocks(p, m));
+            cta_barrier_sync();
+        }
+    }
+    const int32_t max_extra = kAdapters ? ctrl->max_extra : 0;
+    const uint32_t tmem_base = ctrl->tmem_addr;
+    const uint32_t S = (uint32_t)p.num_stages, stride = (uint32_t)p.stage_bytes;
+    const uint32_t full0 = smem_u32(&ctrl->full[0]), empty0 = smem_u32(&ctrl->empty[0]);
+    It iter(p, start, tiles, worker, workers, max_extra);
+    Item it;
+
+    // pieces (boxes of rank_box rows of an adapter's second factor) of extra
+    // k-block e of a tile with `slots` adapters; a box of 8 rows is half of
+    // an MMA's 16, so their number is made even with one of zeros
+    auto pieces_of = [&](int32_t slots, int32_t e) {
+        const int32_t per = kBK / p.rank_box;
+        int32_t n = min(per, slots * (p.rank_pad / p.rank_box) - e * per);
+        if (p.rank_box == 8) n = (n + 1) & ~1;
+        return n;
+    };
+
+    if (warp == 0) {
+        // ---------------------------------------------------------- row tiles
+        uint32_t s = 0, ph = 0;
+        int32_t issued = 0;
+        bool ok = true;
+        auto arm = [&](uint32_t full, uint32_t bytes) {
+            if (!kPair || rank == 0)
+                mbar_arrive_expect_tx(full, (kPair ? 2u : 1u) * bytes);
+            else if (kAdapters)
+                mbar_arrive_cluster(mapa_shared(full, 0));
+        };
+        while (ok && iter.next(it)) {
+            const uint32_t rows = (uint32_t)it.w / (kPair ? 2u : 1u);
+            const int32_t y = it.row0 + (int32_t)(rank * rows);
+            const int32_t kb_end = kAdapters ? min(it.kb1, p.num_kb) : it.kb1;
+            const int32_t n_main = max(0, kb_end - it.kb0);
+            if (lane == 0) {
+                const CUtensorMap* m = &maps.x[rows / 16 - 1];
+                uint32_t ls = s, lph = ph;
+                for (int32_t kb = it.kb0; kb < kb_end; ++kb) {
+                    if (!wait_phase(empty0 + 8u * ls, lph ^ 1u, ctrl, p, kErrTokens)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t full = full0 + 8u * ls;
+                    arm(full, kWBytes + rows * (uint32_t)(kBK * 2));
+                    const uint32_t dst = ring + ls * stride + kWBytes;
+                    const uint32_t bar = kPair ? mapa_shared(full, 0) : full;
+                    if (p.x3d) {
+                        load_3d<kPair>(dst, m, bar, 0, y, kb * (kBK / 64));
+                    } else {
+                        load_2d<kPair>(dst, m, bar, kb * kBK, y);
+                        load_2d<kPair>(dst + rows * 128u, m, bar, kb * kBK + 64, y);
+                    }
+                    ++issued;
+                    if (++ls == S) {
+                        ls = 0;
+                        lph ^= 1u;
+                    }
+                }
+            }
+            if constexpr (kAdapters) {
+                ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+                const uint32_t adv = s + (uint32_t)n_main;
+                ph ^= (adv / S) & 1u;
+                s = adv % S;
+                const int32_t slots = __ldcg(p.nslots + it.tile);
+                const int32_t e1 = min(it.kb1 - p.num_kb, extra_blocks(p, slots));
+                for (int32_t e = max(0, it.kb0 - p.num_kb); ok && e < e1; ++e) {
+                    ok = wait_phase(empty0 + 8u * s, ph ^ 1u, ctrl, p, kErrTokens);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    // The tile's rows of the low-rank products, each only in
+                    // its own adapter's columns: lane = 16-byte vector
+                    // (8 columns) of one of two rows at a time, written at
+                    // the 128-byte swizzle's place.
+                    const int32_t v = (int32_t)lane & 15;
+                    const int32_t col = e * kBK + 8 * v;
+                    const int32_t slot = col / p.rank_pad;
+                    const int32_t id = slot < slots ? __ldcg(p.slots + (int64_t)it.tile * p.cap + slot) : -2;
+                    const uint16_t* src = p.low + (col - slot * p.rank_pad);
+                    const uint32_t dst = ring + s * stride + kWBytes + (uint32_t)(v >> 3) * rows * 128u;
+                    const int32_t row_end = it.row0 + it.valid;
+                    for (uint32_t i0 = lane >> 4; i0 < rows; i0 += 16) {
+                        uint4 q[8];
+                        int32_t who[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int32_t t = y + (int32_t)i0 + 2 * k;
+                            const bool in = i0 + 2 * k < rows && t < row_end && id >= 0;
+                            who[k] = in ? __ldcg(p.ids + t) : -3;
+                            q[k] = in ? __ldcg(reinterpret_cast<const uint4*>(src + (int64_t)t * p.rank_pad))
+                                      : make_uint4(0, 0, 0, 0);
+                        }
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const uint32_t i = i0 + 2 * k;
+                            if (i >= rows) break;
+                            if (who[k] != id) q[k] = make_uint4(0, 0, 0, 0);
+                            st_shared_v4(dst + i * 128u + ((((uint32_t)v & 7u) ^ (i & 7u)) << 4), q[k]);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        arm(full0 + 8u * s, (uint32_t)(pieces_of(slots, e) * p.rank_box) * 256u);
+                        ++issued;
+                    }
+                    if (++s == S) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+            } else {
+                const uint32_t adv = s + (uint32_t)n_main;
+                ph ^= (adv / S) & 1u;
+                s = adv % S;
+                ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+            }
+        }
+        if (lane == 0 && (!kPair || rank == 0)) {
+            // what an aborting CTA waits for before its shared memory is released
+            const uint32_t pos = (uint32_t)issued;
+            ctrl->ring_s = (int32_t)(pos % S);
+            ctrl->ring_ph = (int32_t)((pos / S) & 1u);
+            ctrl->ring_lap = pos >= S ? 1 : 0;
+        }
+        __syncwarp();
+    } else if (warp == 6) {
+        // ------------------------------------------------------------ weights
+        uint32_t s = 0, ph = 0;
+        bool ok = true;
+        while (ok && iter.next(it)) {
+            const int32_t n0 = it.n * (kPair ? 256 : 128) + 128 * (int32_t)rank;
+            const int32_t kb_end = kAdapters ? min(it.kb1, p.num_kb) : it.kb1;
+            const int32_t n_main = max(0, kb_end - it.kb0);
+            if (lane == 0) {
+                uint32_t ls = s, lph = ph;
+                for (int32_t kb = it.kb0; kb < kb_end; ++kb) {
+                    if (!wait_phase(empty0 + 8u * ls, lph ^ 1u, ctrl, p, kErrWeights)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t full = full0 + 8u * ls;
+                    const uint32_t bar = kPair ? mapa_shared(full, 0) : full;
+                    const uint32_t dst = ring + ls * stride;
+                    const int32_t k0 = kb * kBK;
+                    if (p.w4d) {
+                        if (p.w_kmajor)
+                            load_4d<kPair>(dst, &maps.w, bar, 0, n0, k0 / 64, it.g);
+                        else
+                            load_4d<kPair>(dst, &maps.w, bar, 0, k0, n0 / 64, it.g);
+                    } else if (p.w_kmajor) {
+                        load_3d<kPair>(dst, &maps.w, bar, k0, n0, it.g);
+                        load_3d<kPair>(dst + 128u * 128u, &maps.w, bar, k0 + 64, n0, it.g);
+                    } else {
+                        load_3d<kPair>(dst, &maps.w, bar, n0, k0, it.g);
+                        load_3d<kPair>(dst + (uint32_t)kBK * 128u, &maps.w, bar, n0 + 64, k0, it.g);
+                    }
+                    if (++ls == S) {
+                        ls = 0;
+                        lph ^= 1u;
+                    }
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+            const uint32_t adv = s + (uint32_t)n_main;
+            ph ^= (adv / S) & 1u;
+            s = adv % S;
+            if constexpr (kAdapters) {
+                const int32_t slots = __ldcg(p.nslots + it.tile);
+                const int32_t e1 = min(it.kb1 - p.num_kb, extra_blocks(p, slots));
+                const int32_t per = kBK / p.rank_box, per_slot = p.rank_pad / p.rank_box;
+                for (int32_t e = max(0, it.kb0 - p.num_kb); ok && e < e1; ++e) {
+                    ok = wait_phase(empty0 + 8u * s, ph ^ 1u, ctrl, p, kErrWeights);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    const uint32_t full = full0 + 8u * s;
+                    const uint32_t bar = kPair ? mapa_shared(full, 0) : full;
+                    if ((int32_t)lane < pieces_of(slots, e)) {
+                        const int32_t piece = e * per + (int32_t)lane;
+                        const int32_t slot = piece / per_slot;
+                        // (past the last adapter: a box of zeros, beyond the tensor)
+                        const int32_t id = slot < slots ? __ldcg(p.slots + (int64_t)it.tile * p.cap + slot) : p.R;
+                        const int32_t row = (piece - slot * per_slot) * p.rank_box;
+                        const uint32_t dst = ring + s * stride + lane * (uint32_t)p.rank_box * 256u;
+                        if (p.b4d) {
+                            load_4d<kPair>(dst, &maps.b, bar, 0, row, n0 / 64, id);
+                        } else {
+                            load_3d<kPair>(dst, &maps.b, bar, n0, row, id);
+                            load_3d<kPair>(dst + (uint32_t)p.rank_box * 128u, &maps.b, bar, n0 + 64, row, id);
+                        }
+                    }
+                    __syncwarp();
+                    if (++s == S) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- MMA
+        if (lane == 0 && (!kPair || rank == 0)) {
+            const uint32_t tfull0 = smem_u32(&ctrl->tmem_full[0]), tempty0 = smem_u32(&ctrl->tmem_empty[0]);
+            const uint32_t cols = p.tmem_cols / 2;
+            const uint32_t idesc0 = make_idesc_f16_f32(kPair ? 256 : 128, 0, !p.w_kmajor, false, p.bf16 != 0);
+            const uint32_t idesc1 = make_idesc_f16_f32(kPair ? 256 : 128, 0, true, false, p.bf16 != 0);
+            constexpr uint32_t kK = kBK / 16;
+            // weights: MN-major, 64-column chunks of kBK k-rows (16 k-rows =
+            // two 1024-byte atoms per MMA), or K-major, 128 rows per 64 k
+            const uint64_t a_desc0 = p.w_kmajor ? make_sw128_desc(ring, 16, 1024)
+                                                : make_sw128_desc(ring, (uint32_t)kBK * 128u, 1024);
+            const uint64_t b_desc0 = make_sw128_desc(ring + kWBytes, 16, 1024);
+            uint32_t a_off[kK];
+#pragma unroll
+            for (uint32_t k = 0; k < kK; ++k)
+                a_off[k] = p.w_kmajor ? (k / 4) * (128u * 128u >> 4) + (k % 4) * 2u : k * (2048u >> 4);
+            const uint32_t stride16 = stride >> 4;
+            uint32_t s = 0, ph = 0, local = 0;
+            bool ok = true;
+            while (ok && iter.next(it)) {
+                const uint32_t buf = local & 1u, bph = (local >> 1) & 1u;
+                if (!wait_phase(tempty0 + 8u * buf, bph ^ 1u, ctrl, p, kErrAccum)) break;
+                tc_fence_after();
+                const uint32_t d = tmem_base + buf * cols;
+                const uint32_t nbits = ((uint32_t)it.w >> 3) << 17;
+                const uint32_t idesc = idesc0 | nbits;
+                const uint32_t half16 = ((uint32_t)it.w / (kPair ? 2u : 1u)) * 128u >> 4;  // second 64 k of the rows
+                const int32_t kb_end = kAdapters ? min(it.kb1, p.num_kb) : it.kb1;
+                uint32_t acc = 0;
+                for (int32_t kb = it.kb0; kb < kb_end; ++kb) {
+                    if (!wait_phase(full0 + 8u * s, ph, ctrl, p, kErrStage)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t a_desc = a_desc0 + (uint64_t)(s * stride16);
+                    const uint64_t b_desc = b_desc0 + (uint64_t)(s * stride16);
+#pragma unroll
+                    for (uint32_t k = 0; k < kK; ++k)
+                        mma_f16_ss<kCG>(d, a_desc + a_off[k], b_desc + (k / 4) * half16 + (k % 4) * 2u, idesc,
+                                        k > 0 ? 1u : acc);
+                    acc = 1;
+                    mma_commit<kCG>(empty0 + 8u * s, 0x3);
+                    if (++s == S) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+                if constexpr (kAdapters) {
+                    const int32_t slots = __ldcg(p.nslots + it.tile);
+                    const int32_t e1 = min(it.kb1 - p.num_kb, extra_blocks(p, slots));
+                    const uint32_t box = (uint32_t)p.rank_box;
+                    // second factors: boxes of `box` k-rows x two 64-column
+                    // chunks; boxes of 8 rows pair up to an MMA's 16
+                    const uint64_t x_desc0 = box == 8 ? make_sw128_desc(ring, 1024, 2048)
+                                                      : make_sw128_desc(ring, box * 128u, 1024);
+                    for (int32_t e = max(0, it.kb0 - p.num_kb); ok && e < e1; ++e) {
+                        if (!wait_phase(full0 + 8u * s, ph, ctrl, p, kErrStage)) {
+                            ok = false;
+                            break;
+                        }
+                        if (kPair) fence_acq_rel_cluster();  // the peer wrote its rows itself
+                        tc_fence_after();
+                        const uint64_t a_desc = x_desc0 + (uint64_t)(s * stride16);
+                        const uint64_t b_desc = b_desc0 + (uint64_t)(s * stride16);
+                        const uint32_t nk = (uint32_t)pieces_of(slots, e) * box / 16u;
+                        for (uint32_t k = 0; k < nk; ++k) {
+                            const uint32_t r = 16u * k;
+                            const uint32_t off = box == 8 ? k * 4096u : (r / box) * (box * 256u) + (r % box) * 128u;
+                            mma_f16_ss<kCG>(d, a_desc + (off >> 4), b_desc + (k / 4) * half16 + (k % 4) * 2u,
+                                            idesc1 | nbits, acc);
+                            acc = 1;
+                        }
+                        mma_commit<kCG>(empty0 + 8u * s, 0x3);
+                        if (++s == S) {
+                            s = 0;
+                            ph ^= 1u;
+                        }
+                    }
+                }
+                if (!ok) break;
+                mma_commit<kCG>(tfull0 + 8u * buf, 0x3);
+                ++local;
+            }
+            mma_commit<kCG>(smem_u32(&ctrl->final_bar), 0x1);
+            const uint64_t t0 = globaltimer_ns();
+            while (!mbar_try_wait(smem_u32(&ctrl->final_bar), 0))
+                if (globaltimer_ns() - t0 > p.timeout_ns) {
+                    atomicCAS(p.err, 0, (int32_t)kErrFinal);
+                    break;
+                }
+        }
+        __syncwarp();
+    } else {
+        // ----------------------------------------------------------- epilogue
+        const uint32_t quarter = warp & 3u;
+        const uint32_t lane_row = quarter * 32 + lane;
+        const uint32_t cols = p.tmem_cols / 2;
+        const int64_t part = (int64_t)128 * cols;  // floats of one partial tile
+        uint32_t local = 0;
+        float v[32];
+        while (iter.next(it)) {
+            const uint32_t buf = local & 1u, bph = (local >> 1) & 1u;
+            bool ok = wait_phase(smem_u32(&ctrl->tmem_full[buf]), bph, ctrl, p, kErrEpi);
+            ok = named_bar_and(kEpiBarrier, kEpiThreads, ok);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t taddr = tmem_base + ((quarter * 32u) << 16) + buf * cols;
+            auto release = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (kPair)
+                        mbar_arrive_cluster(mapa_shared(smem_u32(&ctrl->tmem_empty[buf]), 0));
+                    else
+                        mbar_arrive(smem_u32(&ctrl->tmem_empty[buf]));
+                }
+            };
+            const int32_t n = it.n * (kPair ? 256 : 128) + 128 * (int32_t)rank + (int32_t)lane_row;
+            const bool in_n = n < p.N;
+            const bool whole = it.kb0 == 0 && it.kb1 == it.kb_all;
+            // an item's share without a k-block (adapters: past a tile's last adapter) has an untouched accumulator
+            const bool none = kAdapters && it.kb0 >= p.num_kb &&
+                              it.kb0 - p.num_kb >= extra_blocks(p, __ldcg(p.nslots + it.tile));
+            if (!kPair && !whole && it.kb0 != 0) {
+                // a share of an item that an earlier CTA began: publish it
+                float4* dst = reinterpret_cast<float4*>(p.ws + (int64_t)blockIdx.x * part) + lane_row;
+                for (int32_t c = 0; c < it.w; c += 32) {
+                    __syncwarp();
+                    tmem_load_32cols(taddr + c, v);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        __stcg(dst + (int64_t)(c / 4 + j) * 128,
+                               none ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                    : make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+                }
+                release();
+                __threadfence();
+                named_bar_sync(kEpiBarrier, kEpiThreads);
+                if (threadIdx.x == 64) atomicExch(p.flags + blockIdx.x, 1u);
+                ++local;
+                continue;
+            }
+            uint32_t others = 0;  // CTAs after this one that hold a share of the item
+            if (!kPair && !whole) {
+                const uint32_t units = (uint32_t)tiles[p.G] * (uint32_t)p.n_tiles * (uint32_t)it.kb_all;
+                const uint32_t end = (it.index + 1) * (uint32_t)it.kb_all;
+                while (blockIdx.x + others + 1 < gridDim.x &&
+                       It::begin_of(units, blockIdx.x + others + 1, gridDim.x) < end)
+                    ++others;
+                bool ready = true;
+                if (threadIdx.x == 64) {
+                    volatile uint32_t* vf = p.flags + blockIdx.x + 1;
+                    volatile int32_t* abort_flag = &ctrl->abort_flag;
+                    const uint64_t t0 = globaltimer_ns();
+                    for (uint32_t o = 0; o < others && ready; ++o)
+                        while (vf[o] == 0u)
+                            if (*abort_flag || globaltimer_ns() - t0 > p.timeout_ns) {
+                                *abort_flag = 1;
+                                atomicCAS(p.err, 0, (int32_t)kErrEpi);
+                                ready = false;
+                                break;
+                            }
+                    __threadfence();
+                }
+                ready = named_bar_and(kEpiBarrier, kEpiThreads, ready);
+                if (!ready) {
+                    release();
+                    break;
+                }
+            }
+            for (int32_t c = 0; c < it.w; c += 32) {
+                __syncwarp();
+                tmem_load_32cols(taddr + c, v);
+                const float4* src = reinterpret_cast<const float4*>(p.ws + (int64_t)(blockIdx.x + 1) * part) + lane_row;
+                for (uint32_t o = 0; o < others; ++o, src += part / 4) {
+                    float4 x[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[j] = __ldcg(src + (int64_t)(c / 4 + j) * 128);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        v[4 * j] += x[j].x;
+                        v[4 * j + 1] += x[j].y;
+                        v[4 * j + 2] += x[j].z;
+                        v[4 * j + 3] += x[j].w;
+                    }
+                }
+                if (in_n) {
+                    const int32_t m = min(32, it.valid - c);
+                    uint16_t* y = p.Y + (int64_t)(it.row0 + c) * p.ldy + n;
+                    uint16_t gate[32];
+                    if (p.act) {
+                        const uint16_t* a = p.act + (int64_t)(it.row0 + c) * p.ld_act + n;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (j < m) gate[j] = __ldcg(a + (int64_t)j * p.ld_act);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        if (j < m) {
+                            float x = v[j];
+                            if (p.apply_relu) x = x > 0.0f ? x : 0.0f;  // -0 and NaN become +0
+                            uint16_t h = round16(x, p.bf16);
+                            if (p.act && !positive16(gate[j], p.bf16)) h = 0;
+                            y[(int64_t)j * p.ldy] = h;
+                        }
+                    }
+                }
+            }
+            release();
+            if (!kPair && !whole) {
+                named_bar_sync(kEpiBarrier, kEpiThreads);  // the partials have been read
+                for (uint32_t o = threadIdx.x - 64; o < others; o += kEpiThreads) p.flags[blockIdx.x + 1 + o] = 0u;
+            }
+            ++local;
+        }
+        // rows of no group: before the first group and past the last one
+        const int32_t head = start[0], tail = start[p.G];
+        const int32_t outside = head + (p.T - tail);
+        const int32_t vecs = p.N / 8;  // 16-byte vectors of an output row
+        for (int32_t r = (int32_t)blockIdx.x; r < outside; r += (int32_t)gridDim.x) {
+            const int32_t t = r < head ? r : tail + (r - head);
+            uint4* y = reinterpret_cast<uint4*>(p.Y + (int64_t)t * p.ldy);
+            for (int32_t i = (int32_t)threadIdx.x - 64; i < vecs; i += (int32_t)kEpiThreads) y[i] = make_uint4(0, 0, 0, 0);
+        }
+    }
+
+    __syncthreads();
+    if (threadIdx.x == 0 && *(volatile int32_t*)&ctrl->abort_flag) drain_ring(ctrl, full0, S);
+    tc_fence_before();
+    if (kPair)
+        cluster_sync_relaxed();
+    else
+        __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc<kCG>(tmem_base, p.tmem_cols);
+    }
+}
+
+}  // namespace rg
+}  // namespace gr

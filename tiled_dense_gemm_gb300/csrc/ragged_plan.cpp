@@ -1,0 +1,85 @@
+#include "ragged_plan.h"
+
+#include <algorithm>
+
+namespace gr {
+namespace rg {
+
+namespace {
+constexpr int64_t kSmem = 227 * 1024;  // per CTA
+constexpr int64_t kCtrl = 1024;
+constexpr int64_t kStageK = 128;       // k-rows per ring stage
+constexpr int64_t kIndexMax = 0x7fffffff;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+}  // namespace
+
+RaggedPlan plan_rows(int64_t T, int64_t G, int64_t N, int64_t K, int64_t R, int64_t rank, int num_sms,
+                     int max_pairs) {
+    RaggedPlan p = {};
+    const int64_t avg = ceil_div(T, G);
+    const int pairs = max_pairs < 0 ? 0 : std::min(max_pairs ? max_pairs : num_sms / 2, num_sms / 2);
+    p.pair = avg > 128 && pairs > 0;
+    int64_t cap;
+    if (p.pair)
+        cap = 256;
+    else if (R > 0 || T <= 64)
+        cap = std::min<int64_t>(128, round_up(T, 16));
+    else
+        cap = avg <= 16 ? 64 : 128;
+    p.cap = (int32_t)cap;
+    p.num_kb = (int32_t)ceil_div(K, kStageK);
+    p.n_tiles = (int32_t)ceil_div(N, p.pair ? 256 : 128);
+    p.stage_bytes = (int32_t)(128 * kStageK * 2 + cap / (p.pair ? 2 : 1) * kStageK * 2);
+    const int64_t table = round_up(2 * (G + 1) * 4, 16);
+    p.num_stages = (int32_t)std::min<int64_t>(8, (kSmem - kCtrl - table) / p.stage_bytes);
+    p.smem_bytes = (int32_t)(kCtrl + (int64_t)p.num_stages * p.stage_bytes + table);
+    // accumulators are read 32 columns at a time; allocations are powers of two
+    int64_t cols = 2 * round_up(cap, 32), alloc = 32;
+    while (alloc < cols) alloc *= 2;
+    p.tmem_cols = (int32_t)alloc;
+    // at most this many row tiles, whatever the groups' sizes are
+    const int64_t tiles = std::min(T, ceil_div(T, cap) + std::min(G, T));
+    const int64_t items = tiles * p.n_tiles;
+    int64_t kb = p.num_kb;
+    if (R > 0) {
+        p.rank_box = 8;
+        while (p.rank_box < 64 && p.rank_box < rank) p.rank_box *= 2;
+        p.rank_pad = (int32_t)round_up(rank, p.rank_box);
+        kb += ceil_div(std::min(R, cap) * p.rank_pad, kStageK);
+        const int64_t nt = ceil_div(T, cap);
+        p.row_width = (int32_t)round_up(ceil_div(T, nt), p.pair ? 32 : 16);
+    }
+    if (items > kIndexMax) {
+        p.status = GEMM_ERR_TOO_LARGE;
+        return p;
+    }
+    p.split = !p.pair && items * kb <= kIndexMax;
+    p.grid = p.pair ? 2 * (int32_t)std::min<int64_t>(pairs, items)
+                    : (int32_t)std::min<int64_t>(num_sms, p.split ? items * kb : items);
+    return p;
+}
+
+DwPlan plan_dw(int64_t T, int64_t G, int64_t P, int64_t Q, int num_sms, int max_pairs) {
+    (void)T;
+    DwPlan p = {};
+    const int pairs = max_pairs < 0 ? 0 : std::min(max_pairs ? max_pairs : num_sms / 2, num_sms / 2);
+    p.pair = pairs > 0 && G * ceil_div(P, 256) * ceil_div(Q, 256) >= pairs;
+    const int64_t tile = p.pair ? 256 : 128;
+    p.p_tiles = (int32_t)ceil_div(P, tile);
+    p.q_tiles = (int32_t)ceil_div(Q, tile);
+    const int64_t stage = 2 * 128 * kStageK * 2;
+    p.num_stages = 3;
+    p.smem_bytes = (int32_t)(kCtrl + 3 * stage + 32 * 1024);
+    const int64_t items = G * p.p_tiles * p.q_tiles;
+    if (items > kIndexMax) {
+        p.status = GEMM_ERR_TOO_LARGE;
+        return p;
+    }
+    p.grid = p.pair ? 2 * (int32_t)std::min<int64_t>(pairs, items) : (int32_t)std::min<int64_t>(num_sms, items);
+    return p;
+}
+
+}  // namespace rg
+}  // namespace gr

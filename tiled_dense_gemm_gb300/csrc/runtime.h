@@ -4,7 +4,9 @@
 // only; every function that takes the state runs with g_mu held.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 #include <stdint.h>
 
 #include <mutex>
@@ -34,6 +36,14 @@ struct StreamBuffers {
     void* hC = nullptr;
     size_t hA_bytes = 0, hB_bytes = 0, hC_bytes = 0;
     int32_t* h_err = nullptr;  // pinned copy of the error word (host-buffer entry point)
+    // ragged products: fp32 partial tiles, their flags (zero between
+    // launches), and what their first kernel hands to the second
+    void* rg_ws = nullptr;
+    size_t rg_ws_bytes = 0;
+    void* rg_flags = nullptr;
+    size_t rg_flags_bytes = 0;
+    void* rg_misc = nullptr;
+    size_t rg_misc_bytes = 0;
     // host-buffer entry point, pipelined: copy-in and copy-out streams and
     // the events that chain them to the compute stream (created on first use)
     bool pipe_ready = false;
@@ -47,14 +57,15 @@ struct DeviceState {
     int status = GEMM_OK;
     int sm_count = 0;
     int max_pairs = 0;  // co-resident CTA pairs of the paired kernel
-    int32_t* d_err = nullptr;
+    int32_t* d_err = nullptr;  // [0] timed-out waits, [1] bad values in an index array
     bool attr_set[6] = {false, false, false, false, false, false};  // per kernel mode
+    bool rg_attr_set[6] = {false, false, false, false, false, false};  // per ragged kernel
     std::vector<StreamBuffers> streams;
 };
 
-
 extern std::mutex g_mu;
 extern DeviceState g_dev[kMaxDevices];
+extern PFN_cuTensorMapEncodeTiled_v12000 g_encode;  // set by init_device_locked
 
 // Argument checks of the C ABI (device_ptrs: the 16-byte alignment rule
 // applies to A, B and C).
