@@ -74,8 +74,9 @@ def grouped_dw(x, dy, offsets, layout):
 
 
 def adapters(x, w, a, b, ids, scale, relu, layout):
-    """The low-rank products are rounded once to the element type on the way:
-    their error (accumulation, scale, rounding) goes through |B|."""
+    """The low-rank products go through two numbers of the element type, hi and
+    the rounded rest: what is left out is the rounding of a rest of at most
+    u |low|.  That and their accumulation and scale go through |B|."""
     X, W, A, B = _f64(x), _f64(w), _f64(a), _f64(b)
     if layout == "nk":
         W = W.T
@@ -88,11 +89,12 @@ def adapters(x, w, a, b, ids, scale, relu, layout):
         if i < 0:
             continue
         low = s[i] * (X[t] @ A[i].T)
-        low_e = rounded(low, (K + 2) * 2.0 ** -23 * abs(s[i]) * (np.abs(X[t]) @ np.abs(A[i]).T), dtype)
+        low_e = (K + 2) * 2.0 ** -23 * abs(s[i]) * (np.abs(X[t]) @ np.abs(A[i]).T)
+        low_e = low_e + UNIT[dtype] ** 2 * (np.abs(low) + low_e) + TINY[dtype]
         y[t] += low @ B[i]
         terms[t] += (np.abs(low) + low_e) @ np.abs(B[i])
         e[t] += low_e @ np.abs(B[i])
-    e += (K + rank) * 2.0 ** -23 * terms
+    e += (K + 2 * rank) * 2.0 ** -23 * terms
     if relu:
         y = np.maximum(y, 0.0)
     return y, rounded(y, e, dtype)

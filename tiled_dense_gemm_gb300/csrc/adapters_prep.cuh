@@ -1,11 +1,15 @@
-// What the adapters' product needs before its main kernel: the rows' low-rank
-// parts and, for each row tile, the list of its distinct adapters.
+// What the adapters' product needs beside its main kernel: the rows' low-rank
+// parts and, where the rows need several tiles, the list of each tile's
+// distinct adapters.
 //
 //   low[t, j] = scale[i] * sum_k X[t, k] A[i][j, k],   i = ids[t]
 //
-// The sums are taken in 32 bits and rounded once, after the scale, to the
-// element type: low is the operand of a tensor-core product next, as the
-// activations between two layers are.
+// The sums are taken in 32 bits, scaled there, and handed on as two numbers
+// of the element type, hi = round(v) and lo = round(v - hi): together they
+// hold v to 2^-16 (bfloat16) or 2^-22 (binary16), so the low-rank part loses
+// nothing that the last rounding of Y would show.  The tensor cores multiply
+// both with the same B, which costs them twice a product that is a few
+// percent of the whole, and no memory traffic.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -17,108 +21,214 @@
 namespace gr {
 namespace rg {
 
-constexpr int kPrepWarps = 8;
+constexpr int kLowWarps = 8;
 
-struct PrepParams {
+struct LowParams {
     const uint16_t* X;   // (T, K), pitch ldx
     const uint16_t* A;   // (R, rank, K)
     const int32_t* ids;  // (T)
     const float* scale;  // (R), or null: 1
-    uint16_t* low;       // (T, rank_pad)
-    int32_t* slots;      // [tile][cap]
-    int32_t* nslots;     // [tile]
+    uint16_t* low;       // (T, 2, rank_pad): hi, lo
     int64_t ldx;
-    int32_t T, K, R, rank, rank_pad, cap, tile_w, tiles, bf16;
+    int32_t T, K, R, rank, rank_pad, bf16;
+    int32_t slot_step;   // CTAs that share a row block's adapters
+    int32_t passes;      // CTAs that share a rank (8 * kNT products each)
     int32_t* err;
 };
 
-__device__ __forceinline__ float2 unpack16(uint32_t x, int32_t bf16) {
-    if (bf16) return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
-    return __half22float2(*reinterpret_cast<const __half2*>(&x));
+struct SlotParams {
+    const int32_t* ids;
+    int32_t* slots;      // [tile][cap]
+    int32_t* nslots;     // [tile]
+    int32_t T, R, cap, tile_w;
+};
+
+// One row tile's distinct adapters, in order of first appearance.  (Indexes
+// outside [0, R) count as no adapter; low_kernel reports them.)
+__global__ void __launch_bounds__(256) adapters_slots_kernel(const __grid_constant__ SlotParams p) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    __shared__ int32_t id[256];
+    __shared__ int32_t count[8];
+    const int32_t i = (int32_t)threadIdx.x, warp = i / 32, lane = i % 32;
+    const int32_t row0 = (int32_t)blockIdx.x * p.tile_w;
+    const int32_t rows = min(p.tile_w, p.T - row0);
+    int32_t mine = -1;
+    if (i < rows) {
+        mine = __ldcg(p.ids + row0 + i);
+        if (mine < 0 || mine >= p.R) mine = -1;
+    }
+    id[i] = mine;
+    __syncthreads();
+    bool first = mine >= 0;
+    for (int32_t j = 0; j < i; ++j) first = first && id[j] != mine;
+    const uint32_t votes = __ballot_sync(0xffffffffu, first);
+    if (lane == 0) count[warp] = __popc(votes);
+    __syncthreads();
+    int32_t at = __popc(votes & ((1u << lane) - 1u));
+    for (int32_t w = 0; w < warp; ++w) at += count[w];
+    if (first) p.slots[(int64_t)blockIdx.x * p.cap + at] = mine;
+    if (i == 0) {
+        int32_t n = 0;
+        for (int32_t w = 0; w < 8; ++w) n += count[w];
+        p.nslots[blockIdx.x] = n;
+    }
 }
 
-// Blocks [0, tiles): one row tile each, its adapters in order of first
-// appearance.  The others: a warp per row and eight of its rank's products.
-__global__ void __launch_bounds__(kPrepWarps * 32) adapters_prep_kernel(const __grid_constant__ PrepParams p) {
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1, int32_t bf16) {
+    if (bf16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
+            " {%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
+            " {%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 16 bytes from global memory, or zeros, without a branch.
+__device__ __forceinline__ uint4 load_or_zero(const uint16_t* src, bool in) {
+    uint4 q;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+        "@p ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "=&r"(q.x), "=&r"(q.y), "=&r"(q.z), "=&r"(q.w)
+        : "l"(reinterpret_cast<uint64_t>(src)), "r"((uint32_t)in));
+    return q;
+}
+
+// low for blocks of 16 kMT rows, one adapter of the block and 8 kNT of its
+// rank per pass; the warps split K.
+//
+// This product is a few percent of the main one's operations and all
+// latency: it runs beside the main kernel (which starts while it runs and
+// needs low only for its last k-blocks) in the registers and shared memory
+// that kernel leaves, which rules out TMEM and a TMA ring; warp-level MMAs
+// with operands straight from global memory fit.  The order of k inside an
+// MMA does not matter as long as both operands agree, so each thread loads
+// 16 contiguous bytes of its row and feeds two MMAs with them.
+template <int kNT, int kMT>
+__global__ void __launch_bounds__(kLowWarps * 32, 2) adapters_low_kernel(const __grid_constant__ LowParams p) {
+    __shared__ float part[kLowWarps / 2][kNT * 4 * 32];
     grid_dependency_wait();
     grid_launch_dependents();
     const int32_t warp = (int32_t)threadIdx.x / 32, lane = (int32_t)threadIdx.x % 32;
-    if ((int32_t)blockIdx.x < p.tiles) {
-        __shared__ int32_t id[256];
-        __shared__ int32_t count[kPrepWarps];
-        const int32_t i = (int32_t)threadIdx.x;
-        const int32_t row0 = (int32_t)blockIdx.x * p.tile_w;
-        const int32_t rows = min(p.tile_w, p.T - row0);
-        int32_t mine = -1;
-        if (i < rows) {
-            mine = __ldcg(p.ids + row0 + i);
-            if (mine < -1 || mine >= p.R) {
-                atomicCAS(p.err + 1, 0, (int32_t)kBadIds);
-                mine = -1;
-            }
-        }
-        id[i] = mine;
-        __syncthreads();
-        bool first = mine >= 0;
-        for (int32_t j = 0; j < i; ++j) first = first && id[j] != mine;
-        const uint32_t votes = __ballot_sync(0xffffffffu, first);
-        if (lane == 0) count[warp] = __popc(votes);
-        __syncthreads();
-        int32_t at = __popc(votes & ((1u << lane) - 1u));
-        for (int32_t w = 0; w < warp; ++w) at += count[w];
-        if (first) p.slots[(int64_t)blockIdx.x * p.cap + at] = mine;
-        if (i == 0) {
-            int32_t n = 0;
-            for (int32_t w = 0; w < kPrepWarps; ++w) n += count[w];
-            p.nslots[blockIdx.x] = n;
-        }
-        return;
-    }
-    const int32_t groups = p.rank_pad / 8;
-    const int64_t job = (int64_t)(blockIdx.x - p.tiles) * kPrepWarps + warp;
-    if (job >= (int64_t)p.T * groups) return;
-    const int32_t t = (int32_t)(job / groups), j0 = (int32_t)(job - (int64_t)t * groups) * 8;
-    const int32_t id = __ldcg(p.ids + t);
-    if (id < 0 || id >= p.R) return;  // no slot of the row's tile matches it: its low row is not read
-    const int32_t nj = min(8, p.rank - j0);
-    const uint16_t* x = p.X + (int64_t)t * p.ldx;
-    const uint16_t* a = p.A + ((int64_t)id * p.rank + j0) * p.K;
-    float sum[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
-    for (int32_t k = lane * 8; k < p.K; k += 256) {
-        const uint4 xv = *reinterpret_cast<const uint4*>(x + k);
-        uint4 av[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            av[j] = j < nj ? *reinterpret_cast<const uint4*>(a + (int64_t)j * p.K + k) : make_uint4(0, 0, 0, 0);
-        const uint32_t xs[4] = {xv.x, xv.y, xv.z, xv.w};
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t as[4] = {av[j].x, av[j].y, av[j].z, av[j].w};
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const float2 xf = unpack16(xs[c], p.bf16), af = unpack16(as[c], p.bf16);
-                sum[j] = fmaf(xf.x, af.x, sum[j]);
-                sum[j] = fmaf(xf.y, af.y, sum[j]);
-            }
+    const int32_t g = lane >> 2, tig = lane & 3;
+    const int32_t pass = (int32_t)blockIdx.x % p.passes;
+    const int32_t rest = (int32_t)blockIdx.x / p.passes;
+    const int32_t y = rest % p.slot_step, row0 = rest / p.slot_step * (16 * kMT);
+    // the block's distinct adapters, in each warp's registers: lane = row
+    int32_t mine = -1;
+    if (lane < 16 * kMT && row0 + lane < p.T) {
+        mine = __ldcg(p.ids + row0 + lane);
+        if (mine < -1 || mine >= p.R) {
+            atomicCAS(p.err + 1, 0, (int32_t)kBadIds);
+            mine = -1;
         }
     }
+    const uint32_t same = __match_any_sync(0xffffffffu, mine);
+    uint32_t firsts = __ballot_sync(0xffffffffu, mine >= 0 && (same & ((1u << lane) - 1u)) == 0);
+    for (int32_t s = 0; firsts; ++s) {
+        const int32_t src = __ffs((int)firsts) - 1;
+        firsts &= firsts - 1;
+        if (s % p.slot_step != y) continue;
+        const int32_t id = __shfl_sync(0xffffffffu, mine, src);
+        const int32_t j0 = pass * 8 * kNT;  // first of the rank's products
+        float acc[kMT][kNT][4];
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
+        for (int m = 0; m < kMT; ++m)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], d);
-    if (lane == 0) {
-        const float s = p.scale ? __ldcg(p.scale + id) : 1.0f;
-        uint4 q;
-        // (columns past the rank are zeros whatever the scale is)
+            for (int n = 0; n < kNT; ++n)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum[j] = j < nj ? sum[j] * s : 0.0f;
-        q.x = pack16(sum[0], sum[1], p.bf16);
-        q.y = pack16(sum[2], sum[3], p.bf16);
-        q.z = pack16(sum[4], sum[5], p.bf16);
-        q.w = pack16(sum[6], sum[7], p.bf16);
-        *reinterpret_cast<uint4*>(p.low + (int64_t)t * p.rank_pad + j0) = q;
+                for (int c = 0; c < 4; ++c) acc[m][n][c] = 0.0f;
+        const uint16_t* xr[2 * kMT];
+        bool xin[2 * kMT];
+#pragma unroll
+        for (int h = 0; h < 2 * kMT; ++h) {
+            const int32_t t = row0 + h * 8 + g;
+            // rows of other adapters are left out (their results are not kept)
+            xin[h] = __shfl_sync(0xffffffffu, mine, h * 8 + g) == id;
+            xr[h] = p.X + (int64_t)(xin[h] ? t : row0) * p.ldx;
+        }
+        const uint16_t* ar = p.A + ((int64_t)id * p.rank + j0 + g) * p.K;
+        // kU chunks of 32 k per warp in flight at once: one round trip to
+        // DRAM for the first 8 x 32 x kU of K
+        constexpr int kU = kMT == 2 ? (kNT == 8 ? 1 : 2) : (kNT == 8 ? 2 : kNT == 4 ? 4 : 6);
+        for (int32_t kw = warp * 32; kw < p.K; kw += kLowWarps * 32 * kU) {
+            uint4 xv[kU][2 * kMT], av[kU][kNT];
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                const int32_t k = kw + u * kLowWarps * 32 + tig * 8;
+                const bool in = k < p.K;
+#pragma unroll
+                for (int h = 0; h < 2 * kMT; ++h) xv[u][h] = load_or_zero(xr[h] + k, in && xin[h]);
+#pragma unroll
+                for (int n = 0; n < kNT; ++n)
+                    av[u][n] = load_or_zero(ar + (int64_t)n * 8 * p.K + k, in && j0 + n * 8 + g < p.rank);
+            }
+#pragma unroll
+            for (int u = 0; u < kU; ++u)
+#pragma unroll
+                for (int m = 0; m < kMT; ++m)
+#pragma unroll
+                    for (int n = 0; n < kNT; ++n) {
+                        const uint4 &x0 = xv[u][2 * m], &x1 = xv[u][2 * m + 1], &a = av[u][n];
+                        mma_16816(acc[m][n], x0.x, x1.x, x0.y, x1.y, a.x, a.y, p.bf16);
+                        mma_16816(acc[m][n], x0.z, x1.z, x0.w, x1.w, a.z, a.w, p.bf16);
+                    }
+        }
+        const float scale = p.scale ? __ldcg(p.scale + id) : 1.0f;
+#pragma unroll
+        for (int m = 0; m < kMT; ++m) {
+            // sum over the warps: halves in turn, in a fixed order
+#pragma unroll
+            for (int half = kLowWarps / 2; half > 0; half /= 2) {
+                __syncthreads();
+                if (warp >= half && warp < 2 * half)
+#pragma unroll
+                    for (int n = 0; n < kNT; ++n)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) part[warp - half][(n * 4 + c) * 32 + lane] = acc[m][n][c];
+                __syncthreads();
+                if (warp < half)
+#pragma unroll
+                    for (int n = 0; n < kNT; ++n)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) acc[m][n][c] += part[warp][(n * 4 + c) * 32 + lane];
+            }
+            if (warp == 0) {
+#pragma unroll
+                for (int n = 0; n < kNT; ++n)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int32_t j = j0 + n * 8 + tig * 2;
+                        if (!xin[2 * m + h] || j >= p.rank_pad) continue;
+                        const int32_t t = row0 + (2 * m + h) * 8 + g;
+                        float v[2], r[2];
+                        uint32_t hi = 0;
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            // columns past the rank are zeros whatever the scale is
+                            v[c] = j + c < p.rank ? acc[m][n][2 * h + c] * scale : 0.0f;
+                            const uint16_t b = round16(v[c], p.bf16);
+                            const float back = p.bf16 ? __uint_as_float((uint32_t)b << 16)
+                                                      : __half2float(__ushort_as_half(b));
+                            r[c] = isfinite(back) ? v[c] - back : 0.0f;
+                            hi |= (uint32_t)b << (16 * c);
+                        }
+                        uint16_t* dst = p.low + (int64_t)t * 2 * p.rank_pad + j;
+                        *reinterpret_cast<uint32_t*>(dst) = hi;
+                        *reinterpret_cast<uint32_t*>(dst + p.rank_pad) = pack16(r[0], r[1], p.bf16);
+                    }
+            }
+        }
     }
 }
 

@@ -148,7 +148,8 @@ static int run_forward(const void* X, const void* W, void* Y, const int32_t* off
     p.split = pl.split;
     p.num_stages = pl.num_stages;
     p.stage_bytes = pl.stage_bytes;
-    p.table_off = pl.num_stages * pl.stage_bytes;
+    p.turn_off = pl.num_stages * pl.stage_bytes;
+    p.table_off = p.turn_off + 4 * 32 * (int)kTurnPitch;
     p.tmem_cols = (uint32_t)pl.tmem_cols;
     p.w_kmajor = w_kmajor ? 1 : 0;
     p.w4d = (w_kmajor ? K : N) % 64 == 0;
@@ -189,39 +190,59 @@ static int run_forward(const void* X, const void* W, void* Y, const int32_t* off
         if (rc != GEMM_OK) return rc;
         const int64_t tiles = (T + pl.cap - 1) / pl.cap;
         // one buffer: the low-rank rows, the tiles' slot lists, their lengths
-        const size_t low_bytes = ((size_t)T * pl.rank_pad * 2 + 255) / 256 * 256;
+        const size_t low_bytes = ((size_t)T * 2 * pl.rank_pad * 2 + 255) / 256 * 256;
         const size_t slot_bytes = (size_t)tiles * pl.cap * 4;
         rc = rt::grow(&sb.rg_misc, &sb.rg_misc_bytes, low_bytes + slot_bytes + (size_t)tiles * 4, st, false);
         if (rc != GEMM_OK) return rc;
         uint8_t* base = reinterpret_cast<uint8_t*>(sb.rg_misc);
-        PrepParams q;
+        if (!pl.own_slots) {
+            SlotParams q;
+            memset(&q, 0, sizeof(q));
+            q.ids = ad->ids;
+            q.slots = reinterpret_cast<int32_t*>(base + low_bytes);
+            q.nslots = reinterpret_cast<int32_t*>(base + low_bytes + slot_bytes);
+            q.T = (int32_t)T;
+            q.R = (int32_t)ad->R;
+            q.cap = pl.cap;
+            q.tile_w = pl.row_width;
+            rc = launch(adapters_slots_kernel, (int)tiles, 256, 0, 1, st, q);
+            if (rc != GEMM_OK) return rc;
+            p.slots = q.slots;
+            p.nslots = q.nslots;
+        }
+        LowParams q;
         memset(&q, 0, sizeof(q));
         q.X = reinterpret_cast<const uint16_t*>(X);
         q.A = reinterpret_cast<const uint16_t*>(ad->A);
         q.ids = ad->ids;
         q.scale = ad->scale;
         q.low = reinterpret_cast<uint16_t*>(base);
-        q.slots = reinterpret_cast<int32_t*>(base + low_bytes);
-        q.nslots = reinterpret_cast<int32_t*>(base + low_bytes + slot_bytes);
+        q.ldx = ldx;
         q.T = (int32_t)T;
         q.K = (int32_t)K;
         q.R = (int32_t)ad->R;
         q.rank = (int32_t)ad->rank;
         q.rank_pad = pl.rank_pad;
-        q.ldx = ldx;
-        q.cap = pl.cap;
-        q.tile_w = pl.row_width;
-        q.tiles = (int32_t)tiles;
         q.bf16 = p.bf16;
         q.err = d.d_err;
-        const int64_t jobs = T * (pl.rank_pad / 8);
-        const int64_t grid = tiles + (jobs + kPrepWarps - 1) / kPrepWarps;
-        if (grid > 0x7fffffff) return GEMM_ERR_TOO_LARGE;
-        rc = launch(adapters_prep_kernel, (int)grid, kPrepWarps * 32, 0, 1, st, q);
-        if (rc != GEMM_OK) return rc;
         p.low = q.low;
-        p.slots = q.slots;
-        p.nslots = q.nslots;
+        // 16-row blocks while they are few; each block's adapters shared by
+        // as many CTAs as it can have (few rows), or by two
+        const int mt = T > 1024 ? 2 : 1;
+        q.slot_step = (int32_t)std::min<int64_t>({T <= 512 ? 16 : 2, T, ad->R});
+        const int nt = std::min(pl.rank_box / 8, mt == 2 ? 4 : 8);
+        q.passes = (pl.rank_pad + 8 * nt - 1) / (8 * nt);
+        const int64_t grid = (T + 16 * mt - 1) / (16 * mt) * q.slot_step * q.passes;
+        if (grid > 0x7fffffff) return GEMM_ERR_TOO_LARGE;
+        auto fn = mt == 2 ? (nt == 4   ? adapters_low_kernel<4, 2>
+                             : nt == 2 ? adapters_low_kernel<2, 2>
+                                       : adapters_low_kernel<1, 2>)
+                          : (nt == 8   ? adapters_low_kernel<8, 1>
+                             : nt == 4 ? adapters_low_kernel<4, 1>
+                             : nt == 2 ? adapters_low_kernel<2, 1>
+                                       : adapters_low_kernel<1, 1>);
+        rc = launch(fn, (int)grid, kLowWarps * 32, 0, 1, st, q);
+        if (rc != GEMM_OK) return rc;
     }
     const size_t smem = (size_t)pl.smem_bytes;
     if (ad) {

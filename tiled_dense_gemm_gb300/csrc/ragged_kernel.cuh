@@ -43,7 +43,9 @@ constexpr uint32_t kEpiBarrier = 1;
 constexpr int kBK = 128;       // k-rows per ring stage: eight MMAs per wait and commit
 constexpr int kMaxStages = 8;
 constexpr int kTokBoxes = 8;   // row-tile boxes of 16, 32, ..., 128 rows per CTA
+constexpr int kXK = 64;        // adapters: products of the rank per extra k-block, each in two parts
 constexpr int kRaster = 8;     // row tiles of one group walked together, column tile by column tile
+constexpr uint32_t kTurnPitch = 80;  // bytes per row of the transposition: 64, + 16 against bank conflicts
 constexpr uint32_t kWBytes = 128 * kBK * 2;  // weights per stage and CTA
 
 enum : int32_t {
@@ -72,7 +74,8 @@ struct Params {
     int32_t split;       // 1: the k-blocks of all items are cut into equal contiguous runs, one per CTA
     int32_t num_stages;
     int32_t stage_bytes; // stride of a ring stage
-    int32_t table_off;   // shared-memory offset of the prefix arrays, from the ring's start
+    int32_t turn_off;    // shared-memory offsets from the ring's start: the epilogue's transposition,
+    int32_t table_off;   // the prefix arrays
     uint32_t tmem_cols;  // allocated; half of them per accumulator
     int32_t w_kmajor;    // weights stored with the reduction contiguous
     int32_t w4d;         // one copy per stage and CTA of the weights
@@ -89,8 +92,8 @@ struct Params {
     uint64_t timeout_ns;
     // adapters
     const int32_t* ids;      // adapter of each row, -1 none
-    const uint16_t* low;     // (T, rank_pad): scale * x A^T, rounded to the element type
-    const int32_t* nslots;   // distinct adapters of each row tile
+    const uint16_t* low;     // (T, 2, rank_pad): scale * x A^T, in two parts of the element type
+    const int32_t* nslots;   // distinct adapters of each row tile; null: one tile, listed by every CTA itself
     const int32_t* slots;    // [tile][cap] their indexes
     int32_t rank_pad, rank_box, b4d;
     int32_t R;
@@ -210,7 +213,27 @@ struct Item {
 
 // Extra k-blocks of a row tile: its distinct adapters' ranks side by side.
 __device__ __forceinline__ int32_t extra_blocks(const Params& p, int32_t slots) {
-    return (slots * p.rank_pad + kBK - 1) / kBK;
+    return (slots * p.rank_pad + kXK - 1) / kXK;
+}
+
+// The distinct adapters of the one row tile of at most 128 rows, in order of
+// first appearance, by 128 threads (i = 0 .. 127).
+__device__ __forceinline__ void list_slots(const Params& p, int32_t* ids, int32_t* slots, int32_t* nslots, int32_t i) {
+    int32_t mine = i < p.T ? __ldcg(p.ids + i) : -1;
+    if (mine < 0 || mine >= p.R) mine = -1;
+    ids[i] = mine;
+    named_bar_sync(kEpiBarrier, kEpiThreads);
+    bool first = mine >= 0;
+    for (int32_t j = 0; j < i; ++j) first = first && ids[j] != mine;
+    const uint32_t votes = __ballot_sync(0xffffffffu, first);
+    const int32_t lane = i % 32;
+    named_bar_sync(kEpiBarrier, kEpiThreads);  // every thread has read the ids
+    if (lane == 0) ids[i / 32] = __popc(votes);
+    named_bar_sync(kEpiBarrier, kEpiThreads);
+    int32_t at = __popc(votes & ((1u << lane) - 1u));
+    for (int32_t w = 0; w < i / 32; ++w) at += ids[w];
+    if (first) slots[at] = mine;
+    if (i == 0) *nslots = ids[0] + ids[1] + ids[2] + ids[3];
 }
 
 template <bool kPair, bool kAdapters>
@@ -218,12 +241,13 @@ struct Iter {
     const Params& p;
     const int32_t* start;
     const int32_t* tiles;
+    const int32_t* nslots;
     uint32_t u, u1, step;
     int32_t kb_all;  // split: k-blocks of every item (adapters: with the most extra ones)
 
-    __device__ __forceinline__ Iter(const Params& p_, const int32_t* start_, const int32_t* tiles_, uint32_t worker,
-                                    uint32_t workers, int32_t max_extra)
-        : p(p_), start(start_), tiles(tiles_) {
+    __device__ __forceinline__ Iter(const Params& p_, const int32_t* start_, const int32_t* tiles_,
+                                    const int32_t* nslots_, uint32_t worker, uint32_t workers, int32_t max_extra)
+        : p(p_), start(start_), tiles(tiles_), nslots(nslots_) {
         const uint32_t items = (uint32_t)tiles[p.G] * (uint32_t)p.n_tiles;
         kb_all = p.num_kb + (kAdapters ? max_extra : 0);
         if (!kPair && p.split) {
@@ -280,7 +304,7 @@ struct Iter {
         it.row0 = s0 + j * it.w;
         it.valid = min(it.w, len - j * it.w);
         if (kPair || !p.split) {
-            it.kb_all = p.num_kb + (kAdapters ? extra_blocks(p, __ldcg(p.nslots + it.tile)) : 0);
+            it.kb_all = p.num_kb + (kAdapters ? extra_blocks(p, nslots[it.tile]) : 0);
             it.kb1 = it.kb_all;
         }
         return true;
@@ -304,15 +328,19 @@ __device__ __forceinline__ uint32_t pack16(float a, float b, int32_t bf16) {
     return *reinterpret_cast<uint32_t*>(&h);
 }
 
-// x > 0 for 16-bit floats of either type: sign clear, not zero, not NaN
-__device__ __forceinline__ bool positive16(uint16_t x, int32_t bf16) {
-    return x != 0 && x <= (bf16 ? 0x7F80u : 0x7C00u);
+// A pair of 16-bit floats, each +0 where its gate is not positive (sign set,
+// zero or NaN), as unsigned compares of the gate's words.
+__device__ __forceinline__ uint32_t gate16(uint32_t x, uint32_t gate, int32_t bf16) {
+    const uint32_t inf = bf16 ? 0x7F80u : 0x7C00u;
+    const uint32_t lo = (gate & 0xFFFFu) - 1u < inf ? 0x0000FFFFu : 0u;
+    const uint32_t hi = (gate >> 16) - 1u < inf ? 0xFFFF0000u : 0u;
+    return x & (lo | hi);
 }
 
 // ------------------------------------------------------------------ kernel
 
 template <bool kPair, bool kAdapters>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room for a block of the adapters' low kernel
     ragged_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
     constexpr int kCG = kPair ? 2 : 1;
     using It = Iter<kPair, kAdapters>;
@@ -351,7 +379,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&maps.x[0]);
     }
     grid_launch_dependents();
-    grid_dependency_wait();  // nothing before this reads or writes global memory
+    // Nothing before this reads or writes global memory.  The adapters' main
+    // kernel goes on: the kernel before it in the stream computes low and
+    // nothing else, and lets this one start only after it has itself waited
+    // for all that came before, so X, W, ids, the slot lists and the
+    // workspace are ready and Y is free; low alone is waited for where it is
+    // read, after the main k-blocks.
+    if (!kAdapters) grid_dependency_wait();
     if (warp == 6) build_table(p, start, tiles, lane);
     __syncwarp();
     tc_fence_before();
@@ -360,12 +394,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     else
         cta_barrier_sync();
     tc_fence_after();
+    const int32_t* nslots = p.nslots;
+    const int32_t* slot_list = p.slots;
     if constexpr (kAdapters) {
+        if (!kPair && !nslots) {
+            int32_t* const own = tiles + p.G + 1;  // 128 scratch, 128 slots, their number
+            if (warp >= 2 && warp <= 5) list_slots(p, own, own + 128, own + 256, (int32_t)threadIdx.x - 64);
+            slot_list = own + 128;
+            nslots = own + 256;
+            __syncwarp();
+            cta_barrier_sync();
+        }
         if (p.split) {
             // items of equal length: as many extra k-blocks as the tile with the most adapters
             int32_t m = 0;
-            for (int32_t i = (int32_t)threadIdx.x; i < tiles[p.G]; i += kThreads) m = max(m, __ldcg(p.nslots + i));
+            for (int32_t i = (int32_t)threadIdx.x; i < tiles[p.G]; i += kThreads) m = max(m, nslots[i]);
             atomicMax(&ctrl->max_extra, extra_blocks(p, m));
+            __syncwarp();
             cta_barrier_sync();
         }
     }
@@ -373,14 +418,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem_base = ctrl->tmem_addr;
     const uint32_t S = (uint32_t)p.num_stages, stride = (uint32_t)p.stage_bytes;
     const uint32_t full0 = smem_u32(&ctrl->full[0]), empty0 = smem_u32(&ctrl->empty[0]);
-    It iter(p, start, tiles, worker, workers, max_extra);
+    It iter(p, start, tiles, nslots, worker, workers, max_extra);
     Item it;
 
     // pieces (boxes of rank_box rows of an adapter's second factor) of extra
     // k-block e of a tile with `slots` adapters; a box of 8 rows is half of
     // an MMA's 16, so their number is made even with one of zeros
     auto pieces_of = [&](int32_t slots, int32_t e) {
-        const int32_t per = kBK / p.rank_box;
+        const int32_t per = kXK / p.rank_box;
         int32_t n = min(per, slots * (p.rank_pad / p.rank_box) - e * per);
         if (p.rank_box == 8) n = (n + 1) & ~1;
         return n;
@@ -432,40 +477,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t adv = s + (uint32_t)n_main;
                 ph ^= (adv / S) & 1u;
                 s = adv % S;
-                const int32_t slots = __ldcg(p.nslots + it.tile);
-                const int32_t e1 = min(it.kb1 - p.num_kb, extra_blocks(p, slots));
-                for (int32_t e = max(0, it.kb0 - p.num_kb); ok && e < e1; ++e) {
+                const int32_t slots = nslots[it.tile];
+                const int32_t e0 = max(0, it.kb0 - p.num_kb), e1 = min(it.kb1 - p.num_kb, extra_blocks(p, slots));
+                int32_t who[4] = {-2, -2, -2, -2};  // adapters of this CTA's rows: lane, lane + 32, ...
+                if (e0 < e1) {
+                    grid_dependency_wait();  // low
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int32_t t = y + 32 * k + (int32_t)lane;
+                        if (32u * k + lane < rows && t < it.row0 + it.valid) who[k] = __ldcg(p.ids + t);
+                    }
+                }
+                for (int32_t e = e0; ok && e < e1; ++e) {
                     ok = wait_phase(empty0 + 8u * s, ph ^ 1u, ctrl, p, kErrTokens);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     // The tile's rows of the low-rank products, each only in
-                    // its own adapter's columns: lane = 16-byte vector
-                    // (8 columns) of one of two rows at a time, written at
-                    // the 128-byte swizzle's place.
+                    // its own adapter's columns: 64 columns of hi, then of
+                    // lo.  Lane = 16-byte vector (8 columns) of one of two
+                    // rows at a time, written at the 128-byte swizzle's place.
                     const int32_t v = (int32_t)lane & 15;
-                    const int32_t col = e * kBK + 8 * v;
+                    const int32_t col = e * kXK + 8 * (v & 7);
                     const int32_t slot = col / p.rank_pad;
-                    const int32_t id = slot < slots ? __ldcg(p.slots + (int64_t)it.tile * p.cap + slot) : -2;
-                    const uint16_t* src = p.low + (col - slot * p.rank_pad);
+                    const int32_t id = slot < slots ? slot_list[(int64_t)it.tile * p.cap + slot] : -3;
+                    const uint16_t* src = p.low + (col - slot * p.rank_pad) + (v >> 3) * p.rank_pad;
                     const uint32_t dst = ring + s * stride + kWBytes + (uint32_t)(v >> 3) * rows * 128u;
-                    const int32_t row_end = it.row0 + it.valid;
-                    for (uint32_t i0 = lane >> 4; i0 < rows; i0 += 16) {
-                        uint4 q[8];
-                        int32_t who[8];
+#pragma unroll 1
+                    for (uint32_t k = 0; 32u * k < rows; ++k) {
+                        const int32_t who_k = k == 0 ? who[0] : k == 1 ? who[1] : k == 2 ? who[2] : who[3];
+#pragma unroll 1
+                        for (uint32_t half = 0; half < 2; ++half) {
+                            uint4 q[8];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int32_t t = y + (int32_t)i0 + 2 * k;
-                            const bool in = i0 + 2 * k < rows && t < row_end && id >= 0;
-                            who[k] = in ? __ldcg(p.ids + t) : -3;
-                            q[k] = in ? __ldcg(reinterpret_cast<const uint4*>(src + (int64_t)t * p.rank_pad))
-                                      : make_uint4(0, 0, 0, 0);
-                        }
+                            for (int j = 0; j < 8; ++j) {
+                                const uint32_t in32 = 16u * half + 2u * j + (lane >> 4);  // row within 32
+                                const int32_t his = __shfl_sync(0xffffffffu, who_k, (int)in32);
+                                q[j] = make_uint4(0, 0, 0, 0);
+                                if (his == id)
+                                    q[j] = __ldcg(reinterpret_cast<const uint4*>(
+                                        src + (int64_t)(y + (int32_t)(32 * k + in32)) * 2 * p.rank_pad));
+                            }
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const uint32_t i = i0 + 2 * k;
-                            if (i >= rows) break;
-                            if (who[k] != id) q[k] = make_uint4(0, 0, 0, 0);
-                            st_shared_v4(dst + i * 128u + ((((uint32_t)v & 7u) ^ (i & 7u)) << 4), q[k]);
+                            for (int j = 0; j < 8; ++j) {
+                                const uint32_t i = 32u * k + 16u * half + 2u * j + (lane >> 4);
+                                if (i < rows)
+                                    st_shared_v4(dst + i * 128u + ((((uint32_t)v & 7u) ^ (i & 7u)) << 4), q[j]);
+                            }
                         }
                     }
                     fence_proxy_async_smem();
@@ -536,9 +593,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             ph ^= (adv / S) & 1u;
             s = adv % S;
             if constexpr (kAdapters) {
-                const int32_t slots = __ldcg(p.nslots + it.tile);
+                const int32_t slots = nslots[it.tile];
                 const int32_t e1 = min(it.kb1 - p.num_kb, extra_blocks(p, slots));
-                const int32_t per = kBK / p.rank_box, per_slot = p.rank_pad / p.rank_box;
+                const int32_t per = kXK / p.rank_box, per_slot = p.rank_pad / p.rank_box;
                 for (int32_t e = max(0, it.kb0 - p.num_kb); ok && e < e1; ++e) {
                     ok = wait_phase(empty0 + 8u * s, ph ^ 1u, ctrl, p, kErrWeights);
                     ok = __all_sync(0xffffffffu, ok);
@@ -549,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int32_t piece = e * per + (int32_t)lane;
                         const int32_t slot = piece / per_slot;
                         // (past the last adapter: a box of zeros, beyond the tensor)
-                        const int32_t id = slot < slots ? __ldcg(p.slots + (int64_t)it.tile * p.cap + slot) : p.R;
+                        const int32_t id = slot < slots ? slot_list[(int64_t)it.tile * p.cap + slot] : p.R;
                         const int32_t row = (piece - slot * per_slot) * p.rank_box;
                         const uint32_t dst = ring + s * stride + lane * (uint32_t)p.rank_box * 256u;
                         if (p.b4d) {
@@ -618,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if constexpr (kAdapters) {
-                    const int32_t slots = __ldcg(p.nslots + it.tile);
+                    const int32_t slots = nslots[it.tile];
                     const int32_t e1 = min(it.kb1 - p.num_kb, extra_blocks(p, slots));
                     const uint32_t box = (uint32_t)p.rank_box;
                     // second factors: boxes of `box` k-rows x two 64-column
@@ -635,13 +692,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint64_t a_desc = x_desc0 + (uint64_t)(s * stride16);
                         const uint64_t b_desc = b_desc0 + (uint64_t)(s * stride16);
                         const uint32_t nk = (uint32_t)pieces_of(slots, e) * box / 16u;
-                        for (uint32_t k = 0; k < nk; ++k) {
-                            const uint32_t r = 16u * k;
-                            const uint32_t off = box == 8 ? k * 4096u : (r / box) * (box * 256u) + (r % box) * 128u;
-                            mma_f16_ss<kCG>(d, a_desc + (off >> 4), b_desc + (k / 4) * half16 + (k % 4) * 2u,
-                                            idesc1 | nbits, acc);
-                            acc = 1;
-                        }
+                        // hi's columns, then lo's, with the same rows of the factors
+                        for (uint32_t h = 0; h < 2; ++h)
+                            for (uint32_t k = 0; k < nk; ++k) {
+                                const uint32_t r = 16u * k;
+                                const uint32_t off =
+                                    box == 8 ? k * 4096u : (r / box) * (box * 256u) + (r % box) * 128u;
+                                mma_f16_ss<kCG>(d, a_desc + (off >> 4), b_desc + h * half16 + k * 2u, idesc1 | nbits,
+                                                acc);
+                                acc = 1;
+                            }
                         mma_commit<kCG>(empty0 + 8u * s, 0x3);
                         if (++s == S) {
                             s = 0;
@@ -670,6 +730,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t part = (int64_t)128 * cols;  // floats of one partial tile
         uint32_t local = 0;
         float v[32];
+        const uint32_t turn = ring + (uint32_t)p.turn_off + quarter * (32u * kTurnPitch);
+        const uint32_t turn_st = turn + (lane & 7u) * kTurnPitch + (lane >> 3) * 16u;
+        const uint32_t turn_ld = turn + (lane >> 2) * kTurnPitch + (lane & 3u) * 16u;
         while (iter.next(it)) {
             const uint32_t buf = local & 1u, bph = (local >> 1) & 1u;
             bool ok = wait_phase(smem_u32(&ctrl->tmem_full[buf]), bph, ctrl, p, kErrEpi);
@@ -687,18 +750,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mbar_arrive(smem_u32(&ctrl->tmem_empty[buf]));
                 }
             };
-            const int32_t n = it.n * (kPair ? 256 : 128) + 128 * (int32_t)rank + (int32_t)lane_row;
+            // this thread's 8 columns of Y (of rows lane / 4, + 8, ...)
+            const int32_t n = it.n * (kPair ? 256 : 128) + 128 * (int32_t)rank + 32 * (int32_t)quarter + 8 * (int32_t)(lane & 3u);
             const bool in_n = n < p.N;
             const bool whole = it.kb0 == 0 && it.kb1 == it.kb_all;
             // an item's share without a k-block (adapters: past a tile's last adapter) has an untouched accumulator
             const bool none = kAdapters && it.kb0 >= p.num_kb &&
-                              it.kb0 - p.num_kb >= extra_blocks(p, __ldcg(p.nslots + it.tile));
+                              it.kb0 - p.num_kb >= extra_blocks(p, nslots[it.tile]);
             if (!kPair && !whole && it.kb0 != 0) {
                 // a share of an item that an earlier CTA began: publish it
                 float4* dst = reinterpret_cast<float4*>(p.ws + (int64_t)blockIdx.x * part) + lane_row;
                 for (int32_t c = 0; c < it.w; c += 32) {
                     __syncwarp();
-                    tmem_load_32cols(taddr + c, v);
+                    tmem_load_fragments(taddr + c, v);
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         __stcg(dst + (int64_t)(c / 4 + j) * 128,
@@ -741,8 +805,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             for (int32_t c = 0; c < it.w; c += 32) {
-                __syncwarp();
-                tmem_load_32cols(taddr + c, v);
+                uint4 gate[4];
+                if (p.act) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int32_t r = c + 8 * i + (int32_t)(lane >> 2);
+                        if (in_n && r < it.valid)
+                            gate[i] = __ldcg(reinterpret_cast<const uint4*>(
+                                p.act + (int64_t)(it.row0 + r) * p.ld_act + n));
+                    }
+                }
+                __syncwarp();  // (also: the last chunk's shared-memory reads are done)
+                tmem_load_fragments(taddr + c, v);
                 const float4* src = reinterpret_cast<const float4*>(p.ws + (int64_t)(blockIdx.x + 1) * part) + lane_row;
                 for (uint32_t o = 0; o < others; ++o, src += part / 4) {
                     float4 x[8];
@@ -756,25 +830,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                         v[4 * j + 3] += x[j].w;
                     }
                 }
-                if (in_n) {
-                    const int32_t m = min(32, it.valid - c);
-                    uint16_t* y = p.Y + (int64_t)(it.row0 + c) * p.ldy + n;
-                    uint16_t gate[32];
-                    if (p.act) {
-                        const uint16_t* a = p.act + (int64_t)(it.row0 + c) * p.ld_act + n;
+                if (p.apply_relu) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (j < m) gate[j] = __ldcg(a + (int64_t)j * p.ld_act);
-                    }
+                    for (int j = 0; j < 32; ++j) v[j] = v[j] > 0.0f ? v[j] : 0.0f;  // -0 and NaN become +0
+                }
+                // transposed through shared memory: 32 rows of Y x this
+                // warp's 32 columns, 64 bytes at a pitch of 80
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        if (j < m) {
-                            float x = v[j];
-                            if (p.apply_relu) x = x > 0.0f ? x : 0.0f;  // -0 and NaN become +0
-                            uint16_t h = round16(x, p.bf16);
-                            if (p.act && !positive16(gate[j], p.bf16)) h = 0;
-                            y[(int64_t)j * p.ldy] = h;
+                for (int i = 0; i < 4; ++i)
+                    st_matrix_trans(turn_st + (uint32_t)i * 8u * kTurnPitch,
+                                    pack16(v[4 * i], v[4 * i + 1], p.bf16), pack16(v[4 * i + 2], v[4 * i + 3], p.bf16),
+                                    pack16(v[16 + 4 * i], v[17 + 4 * i], p.bf16),
+                                    pack16(v[18 + 4 * i], v[19 + 4 * i], p.bf16));
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int32_t r = c + 8 * i + (int32_t)(lane >> 2);
+                    uint4 q = ld_shared_v4(turn_ld + (uint32_t)i * 8u * kTurnPitch);
+                    if (in_n && r < it.valid) {
+                        if (p.act) {
+                            q.x = gate16(q.x, gate[i].x, p.bf16);
+                            q.y = gate16(q.y, gate[i].y, p.bf16);
+                            q.z = gate16(q.z, gate[i].z, p.bf16);
+                            q.w = gate16(q.w, gate[i].w, p.bf16);
                         }
+                        *reinterpret_cast<uint4*>(p.Y + (int64_t)(it.row0 + r) * p.ldy + n) = q;
                     }
                 }
             }
@@ -796,6 +876,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
 
+    // (a later kernel's wait covers this one only: it must not end first)
+    if (kAdapters) grid_dependency_wait();
     __syncthreads();
     if (threadIdx.x == 0 && *(volatile int32_t*)&ctrl->abort_flag) drain_ring(ctrl, full0, S);
     tc_fence_before();

@@ -9,6 +9,9 @@ namespace {
 constexpr int64_t kSmem = 227 * 1024;  // per CTA
 constexpr int64_t kCtrl = 1024;
 constexpr int64_t kStageK = 128;       // k-rows per ring stage
+constexpr int64_t kExtraK = 64;        // products of the adapters' ranks per extra stage
+constexpr int64_t kTurn = 4 * 32 * 80; // the epilogue's transposition
+constexpr int64_t kLowSmem = 18 * 1024;
 constexpr int64_t kIndexMax = 0x7fffffff;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -32,8 +35,11 @@ RaggedPlan plan_rows(int64_t T, int64_t G, int64_t N, int64_t K, int64_t R, int6
     p.num_kb = (int32_t)ceil_div(K, kStageK);
     p.n_tiles = (int32_t)ceil_div(N, p.pair ? 256 : 128);
     p.stage_bytes = (int32_t)(128 * kStageK * 2 + cap / (p.pair ? 2 : 1) * kStageK * 2);
-    const int64_t table = round_up(2 * (G + 1) * 4, 16);
-    p.num_stages = (int32_t)std::min<int64_t>(8, (kSmem - kCtrl - table) / p.stage_bytes);
+    p.own_slots = R > 0 && !p.pair && T <= cap;
+    const int64_t table = kTurn + round_up((2 * (G + 1) + (p.own_slots ? 257 : 0)) * 4, 16);
+    // (adapters: room beside it for a block of the kernel that computes low)
+    const int64_t room = kSmem - kCtrl - table - (R > 0 ? kLowSmem : 0);
+    p.num_stages = (int32_t)std::min<int64_t>(8, room / p.stage_bytes);
     p.smem_bytes = (int32_t)(kCtrl + (int64_t)p.num_stages * p.stage_bytes + table);
     // accumulators are read 32 columns at a time; allocations are powers of two
     int64_t cols = 2 * round_up(cap, 32), alloc = 32;
@@ -47,7 +53,7 @@ RaggedPlan plan_rows(int64_t T, int64_t G, int64_t N, int64_t K, int64_t R, int6
         p.rank_box = 8;
         while (p.rank_box < 64 && p.rank_box < rank) p.rank_box *= 2;
         p.rank_pad = (int32_t)round_up(rank, p.rank_box);
-        kb += ceil_div(std::min(R, cap) * p.rank_pad, kStageK);
+        kb += ceil_div(std::min(R, cap) * p.rank_pad, kExtraK);
         const int64_t nt = ceil_div(T, cap);
         p.row_width = (int32_t)round_up(ceil_div(T, nt), p.pair ? 32 : 16);
     }
