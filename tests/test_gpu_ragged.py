@@ -135,3 +135,16 @@ def test_adapters(rank, layout, dtype):
             y = binding.gemm_relu_adapters(x, w, a, b, ids, s, apply_relu=relu, b_layout=layout)
             binding.check_device_error()
             ref.check(y, ref.adapters(x, w, a, b, ids, s, relu, layout), f"T={T} R={R} {kind} {K}x{N} rank {rank} {layout} {dtype}")
+
+
+@pytest.mark.parametrize("layout,dtype", [("kn", "f16"), ("nk", "bf16")])
+@pytest.mark.parametrize("T,R,rank,kind", [(1025, 3, 16, "runs"), (1500, 40, 12, "mixed"), (2500, 5, 96, "runs")])
+def test_adapters_many_rows(T, R, rank, kind, layout, dtype):
+    K, N = 264, 328
+    x, a, b = normal((T, K), 1, dtype), normal((R, rank, K), 2, dtype, K ** -0.5), normal((R, rank, N), 3, dtype, rank ** -0.5)
+    w = normal((K, N) if layout == "kn" else (N, K), 4, dtype, K ** -0.5)
+    ids = make_ids(T, R, kind, 5)
+    scale = (torch.rand(R, generator=torch.Generator().manual_seed(6)) + 0.5).to(DEV)
+    y = binding.gemm_relu_adapters(x, w, a, b, ids, scale, apply_relu=True, b_layout=layout)
+    binding.check_device_error()
+    ref.check(y, ref.adapters(x, w, a, b, ids, scale, True, layout), f"T={T} R={R} rank {rank} {kind} {layout} {dtype}")

@@ -101,13 +101,25 @@ static int launch(void (*fn)(P...), int grid, int threads, size_t smem, int clus
 }
 
 template <typename F>
-static int allow_smem(DeviceState& d, int which, F fn) {
+static int allow_smem(DeviceState& d, int which, F fn, int bytes = rt::kMaxDynSmem) {
     if (d.rg_attr_set[which]) return GEMM_OK;
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, rt::kMaxDynSmem) != cudaSuccess) {
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
         cudaGetLastError();
         return GEMM_ERR_LAUNCH;
     }
     d.rg_attr_set[which] = true;
+    return GEMM_OK;
+}
+
+template <typename F>
+static int prefer_smem(DeviceState& d, int which, F fn) {
+    if (d.rg_carveout_set[which]) return GEMM_OK;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
+        cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_LAUNCH;
+    }
+    d.rg_carveout_set[which] = true;
     return GEMM_OK;
 }
 
@@ -119,12 +131,85 @@ static int zero_rows(void* y, int64_t ld, int64_t width, int64_t rows, cudaStrea
     return GEMM_OK;
 }
 
+constexpr int kLowTileSmem = rt::kMaxDynSmem - 4096;  // (it has static shared memory too)
+
 struct Adapters {
     const void *A, *B;
     const int32_t* ids;
     const float* scale;
     int64_t R, rank;
 };
+
+// low for all rows: warp-level MMAs beside the main kernel for up to 1024
+// rows, tensor-core tiles before it for more (8192 rows of K = 4096, rank 64:
+// TODO us against TODO us).
+static int run_low(const void* X, const Adapters& ad, uint16_t* low, int64_t T, int64_t K, int64_t ldx,
+                   const RaggedPlan& pl, bool bf16, DeviceState& d, cudaStream_t st) {
+    int rc;
+    if (T > kLowRows) {
+        LowTileMaps m;
+        LowTileParams q;
+        memset(&q, 0, sizeof(q));
+        q.ids = ad.ids;
+        q.scale = ad.scale;
+        q.low = low;
+        q.T = (int32_t)T;
+        q.R = (int32_t)ad.R;
+        q.num_kb = pl.num_kb;
+        // about one block per multiprocessor
+        q.cap = (int32_t)std::min<int64_t>(128, (T + d.sm_count * 16 - 1) / (d.sm_count * 16) * 16);
+        q.rank = (int32_t)ad.rank;
+        q.rank_pad = pl.rank_pad;
+        q.rank_box = pl.rank_box;
+        q.bf16 = bf16 ? 1 : 0;
+        q.x3d = K % 64 == 0;
+        const int stage = (int)kWBytes + q.cap * kBK * 2;
+        q.num_stages = std::min(kMaxStages, (kLowTileSmem - 1024) / stage);
+        q.tmem_cols = q.cap <= 32 ? 64 : q.cap <= 64 ? 128 : 256;
+        q.err = d.d_err;
+        q.timeout_ns = 2000000000ull + 2000ull * (uint64_t)pl.num_kb;
+        rc = encode_rows(&m.x, X, (uint64_t)K, (uint64_t)T, (uint64_t)ldx, (uint32_t)q.cap, q.x3d ? kBK / 64 : 0, bf16);
+        const uint64_t dims[3] = {(uint64_t)K, (uint64_t)ad.rank, (uint64_t)ad.R};
+        const uint64_t strides[2] = {(uint64_t)K, (uint64_t)(K * ad.rank)};
+        const uint32_t box[3] = {64, (uint32_t)pl.rank_box, 1};
+        if (rc == GEMM_OK) rc = encode(&m.a, ad.A, 3, dims, strides, box, bf16);
+        if (rc == GEMM_OK) rc = allow_smem(d, 6, adapters_low_tile_kernel, kLowTileSmem);
+        if (rc != GEMM_OK) return rc;
+        return launch(adapters_low_tile_kernel, (int)((T + q.cap - 1) / q.cap), kThreads,
+                      (size_t)(1024 + q.num_stages * stage), 1, st, m, q);
+    }
+    LowParams q;
+    memset(&q, 0, sizeof(q));
+    q.X = reinterpret_cast<const uint16_t*>(X);
+    q.A = reinterpret_cast<const uint16_t*>(ad.A);
+    q.ids = ad.ids;
+    q.scale = ad.scale;
+    q.low = low;
+    q.ldx = ldx;
+    q.T = (int32_t)T;
+    q.K = (int32_t)K;
+    q.R = (int32_t)ad.R;
+    q.rank = (int32_t)ad.rank;
+    q.rank_pad = pl.rank_pad;
+    q.bf16 = bf16 ? 1 : 0;
+    q.err = d.d_err;
+    // a block's adapters are shared by as many CTAs as it can have
+    q.slot_step = (int32_t)std::min<int64_t>({T <= 512 ? 16 : 2, T, ad.R});
+    const int nt = pl.rank_box / 8;
+    q.passes = pl.rank_pad / pl.rank_box;
+    const int64_t jobs = (T + 15) / 16 * q.slot_step * q.passes;
+    // few jobs share each reduction between the CTAs of a cluster
+    q.k_split = 1;
+    while (q.k_split < 8 && jobs * q.k_split * 2 <= 2 * d.sm_count && K > 256 * q.k_split) q.k_split *= 2;
+    auto fn = nt == 8   ? adapters_low_kernel<8>
+              : nt == 4 ? adapters_low_kernel<4>
+              : nt == 2 ? adapters_low_kernel<2>
+                        : adapters_low_kernel<1>;
+    // the main kernel joins this one on its multiprocessors: the same split
+    // between shared memory and L1
+    if ((rc = prefer_smem(d, nt == 8 ? 3 : nt / 2, fn)) != GEMM_OK) return rc;
+    return launch(fn, (int)jobs * q.k_split, kLowWarps * 32, 0, q.k_split, st, q);
+}
 
 // Y[t] = epilogue(X[t] W[g(t)]): X (T, K), Y (T, N); W[g] (K, N), or (N, K)
 // where w_kmajor.  offsets null: one W for all rows.
@@ -195,7 +280,7 @@ static int run_forward(const void* X, const void* W, void* Y, const int32_t* off
         rc = rt::grow(&sb.rg_misc, &sb.rg_misc_bytes, low_bytes + slot_bytes + (size_t)tiles * 4, st, false);
         if (rc != GEMM_OK) return rc;
         uint8_t* base = reinterpret_cast<uint8_t*>(sb.rg_misc);
-        if (!pl.own_slots) {
+        if (pl.pair) {
             SlotParams q;
             memset(&q, 0, sizeof(q));
             q.ids = ad->ids;
@@ -210,38 +295,8 @@ static int run_forward(const void* X, const void* W, void* Y, const int32_t* off
             p.slots = q.slots;
             p.nslots = q.nslots;
         }
-        LowParams q;
-        memset(&q, 0, sizeof(q));
-        q.X = reinterpret_cast<const uint16_t*>(X);
-        q.A = reinterpret_cast<const uint16_t*>(ad->A);
-        q.ids = ad->ids;
-        q.scale = ad->scale;
-        q.low = reinterpret_cast<uint16_t*>(base);
-        q.ldx = ldx;
-        q.T = (int32_t)T;
-        q.K = (int32_t)K;
-        q.R = (int32_t)ad->R;
-        q.rank = (int32_t)ad->rank;
-        q.rank_pad = pl.rank_pad;
-        q.bf16 = p.bf16;
-        q.err = d.d_err;
-        p.low = q.low;
-        // 16-row blocks while they are few; each block's adapters shared by
-        // as many CTAs as it can have (few rows), or by two
-        const int mt = T > 1024 ? 2 : 1;
-        q.slot_step = (int32_t)std::min<int64_t>({T <= 512 ? 16 : 2, T, ad->R});
-        const int nt = std::min(pl.rank_box / 8, mt == 2 ? 4 : 8);
-        q.passes = (pl.rank_pad + 8 * nt - 1) / (8 * nt);
-        const int64_t grid = (T + 16 * mt - 1) / (16 * mt) * q.slot_step * q.passes;
-        if (grid > 0x7fffffff) return GEMM_ERR_TOO_LARGE;
-        auto fn = mt == 2 ? (nt == 4   ? adapters_low_kernel<4, 2>
-                             : nt == 2 ? adapters_low_kernel<2, 2>
-                                       : adapters_low_kernel<1, 2>)
-                          : (nt == 8   ? adapters_low_kernel<8, 1>
-                             : nt == 4 ? adapters_low_kernel<4, 1>
-                             : nt == 2 ? adapters_low_kernel<2, 1>
-                                       : adapters_low_kernel<1, 1>);
-        rc = launch(fn, (int)grid, kLowWarps * 32, 0, 1, st, q);
+        p.low = reinterpret_cast<const uint16_t*>(base);
+        rc = run_low(X, *ad, reinterpret_cast<uint16_t*>(base), T, K, ldx, pl, bf16, d, st);
         if (rc != GEMM_OK) return rc;
     }
     const size_t smem = (size_t)pl.smem_bytes;

@@ -93,7 +93,7 @@ struct Params {
     // adapters
     const int32_t* ids;      // adapter of each row, -1 none
     const uint16_t* low;     // (T, 2, rank_pad): scale * x A^T, in two parts of the element type
-    const int32_t* nslots;   // distinct adapters of each row tile; null: one tile, listed by every CTA itself
+    const int32_t* nslots;   // distinct adapters of each row tile; null: single CTAs, which list them themselves
     const int32_t* slots;    // [tile][cap] their indexes
     int32_t rank_pad, rank_box, b4d;
     int32_t R;
@@ -108,7 +108,6 @@ struct __align__(8) Ctrl {
     uint32_t tmem_addr;
     int32_t abort_flag;
     int32_t ring_s, ring_ph, ring_lap;
-    int32_t max_extra;  // adapters: most extra k-blocks of a row tile
 };
 static_assert(sizeof(Ctrl) <= 1024, "control block exceeds its reserved 1 KiB");
 
@@ -216,24 +215,38 @@ __device__ __forceinline__ int32_t extra_blocks(const Params& p, int32_t slots) 
     return (slots * p.rank_pad + kXK - 1) / kXK;
 }
 
-// The distinct adapters of the one row tile of at most 128 rows, in order of
-// first appearance, by 128 threads (i = 0 .. 127).
-__device__ __forceinline__ void list_slots(const Params& p, int32_t* ids, int32_t* slots, int32_t* nslots, int32_t i) {
+// The distinct adapters of one row tile of at most 128 rows, in order of
+// first appearance, by 128 threads (i = 0 .. 127); of each also the 16-row
+// window that holds its rows, lo | hi << 16.  Leaves the rows' ids in shared
+// memory and reports indexes outside [-1, R).
+__device__ __forceinline__ void list_slots(const Params& p, int32_t* ids, int32_t* slots, int32_t* windows,
+                                           int32_t* count, int32_t* nslots, int32_t i) {
     int32_t mine = i < p.T ? __ldcg(p.ids + i) : -1;
-    if (mine < 0 || mine >= p.R) mine = -1;
+    if (mine < -1 || mine >= p.R) {
+        atomicCAS(p.err + 1, 0, (int32_t)kBadIds);
+        mine = -1;
+    }
     ids[i] = mine;
     named_bar_sync(kEpiBarrier, kEpiThreads);
     bool first = mine >= 0;
-    for (int32_t j = 0; j < i; ++j) first = first && ids[j] != mine;
+    int32_t last = i;
+    const int32_t n = min(128, p.T);
+    for (int32_t j = 0; j < n; ++j) {
+        const bool same = ids[j] == mine;
+        first = first && !(same && j < i);
+        last = same ? max(last, j) : last;
+    }
     const uint32_t votes = __ballot_sync(0xffffffffu, first);
     const int32_t lane = i % 32;
-    named_bar_sync(kEpiBarrier, kEpiThreads);  // every thread has read the ids
-    if (lane == 0) ids[i / 32] = __popc(votes);
+    if (lane == 0) count[i / 32] = __popc(votes);
     named_bar_sync(kEpiBarrier, kEpiThreads);
     int32_t at = __popc(votes & ((1u << lane) - 1u));
-    for (int32_t w = 0; w < i / 32; ++w) at += ids[w];
-    if (first) slots[at] = mine;
-    if (i == 0) *nslots = ids[0] + ids[1] + ids[2] + ids[3];
+    for (int32_t w = 0; w < i / 32; ++w) at += count[w];
+    if (first) {
+        slots[at] = mine;
+        windows[at] = (i & ~15) | ((last | 15) + 1) << 16;
+    }
+    if (i == 0) *nslots = count[0] + count[1] + count[2] + count[3];
 }
 
 template <bool kPair, bool kAdapters>
@@ -243,7 +256,7 @@ struct Iter {
     const int32_t* tiles;
     const int32_t* nslots;
     uint32_t u, u1, step;
-    int32_t kb_all;  // split: k-blocks of every item (adapters: with the most extra ones)
+    int32_t kb_all;  // split: k-blocks of every item
 
     __device__ __forceinline__ Iter(const Params& p_, const int32_t* start_, const int32_t* tiles_,
                                     const int32_t* nslots_, uint32_t worker, uint32_t workers, int32_t max_extra)
@@ -367,7 +380,6 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
         mbar_init(smem_u32(&ctrl->final_bar), 1);
         ctrl->abort_flag = 0;
         ctrl->ring_s = ctrl->ring_ph = ctrl->ring_lap = 0;
-        ctrl->max_extra = 0;
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -396,25 +408,33 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
     tc_fence_after();
     const int32_t* nslots = p.nslots;
     const int32_t* slot_list = p.slots;
+    int32_t* const row_ids = tiles + p.G + 1;  // single CTAs of adapters: one row tile, listed by each
+    int32_t* const windows = row_ids + 256;
     if constexpr (kAdapters) {
-        if (!kPair && !nslots) {
-            int32_t* const own = tiles + p.G + 1;  // 128 scratch, 128 slots, their number
-            if (warp >= 2 && warp <= 5) list_slots(p, own, own + 128, own + 256, (int32_t)threadIdx.x - 64);
-            slot_list = own + 128;
-            nslots = own + 256;
-            __syncwarp();
-            cta_barrier_sync();
-        }
-        if (p.split) {
-            // items of equal length: as many extra k-blocks as the tile with the most adapters
-            int32_t m = 0;
-            for (int32_t i = (int32_t)threadIdx.x; i < tiles[p.G]; i += kThreads) m = max(m, nslots[i]);
-            atomicMax(&ctrl->max_extra, extra_blocks(p, m));
+        if (!kPair) {
+            if (warp >= 2 && warp <= 5)
+                list_slots(p, row_ids, row_ids + 128, windows, row_ids + 384, row_ids + 388, (int32_t)threadIdx.x - 64);
+            slot_list = row_ids + 128;
+            nslots = row_ids + 388;
             __syncwarp();
             cta_barrier_sync();
         }
     }
-    const int32_t max_extra = kAdapters ? ctrl->max_extra : 0;
+    // (single CTAs: every item has the one row tile's extra k-blocks)
+    const int32_t max_extra = kAdapters && !kPair ? extra_blocks(p, *nslots) : 0;
+    // rows [lo, hi) that the 16 products from column `col` of the extra
+    // k-blocks reach (two adapters of 8 products: both)
+    auto window = [&](int32_t slots, int32_t col, uint32_t& lo, uint32_t& hi) {
+        const int32_t a = col / p.rank_pad, b = (col + 8) / p.rank_pad;
+        const uint32_t wa = (uint32_t)windows[a];
+        lo = wa & 0xFFFFu;
+        hi = wa >> 16;
+        if (b != a && b < slots) {
+            const uint32_t wb = (uint32_t)windows[b];
+            lo = min(lo, wb & 0xFFFFu);
+            hi = max(hi, wb >> 16);
+        }
+    };
     const uint32_t tmem_base = ctrl->tmem_addr;
     const uint32_t S = (uint32_t)p.num_stages, stride = (uint32_t)p.stage_bytes;
     const uint32_t full0 = smem_u32(&ctrl->full[0]), empty0 = smem_u32(&ctrl->empty[0]);
@@ -480,61 +500,77 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                 const int32_t slots = nslots[it.tile];
                 const int32_t e0 = max(0, it.kb0 - p.num_kb), e1 = min(it.kb1 - p.num_kb, extra_blocks(p, slots));
                 int32_t who[4] = {-2, -2, -2, -2};  // adapters of this CTA's rows: lane, lane + 32, ...
-                if (e0 < e1) {
-                    grid_dependency_wait();  // low
+                if (e0 < e1) grid_dependency_wait();  // low
+                if (kPair && e0 < e1) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int32_t t = y + 32 * k + (int32_t)lane;
                         if (32u * k + lane < rows && t < it.row0 + it.valid) who[k] = __ldcg(p.ids + t);
                     }
                 }
-                for (int32_t e = e0; ok && e < e1; ++e) {
-                    ok = wait_phase(empty0 + 8u * s, ph ^ 1u, ctrl, p, kErrTokens);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    // The tile's rows of the low-rank products, each only in
-                    // its own adapter's columns: 64 columns of hi, then of
-                    // lo.  Lane = 16-byte vector (8 columns) of one of two
-                    // rows at a time, written at the 128-byte swizzle's place.
-                    const int32_t v = (int32_t)lane & 15;
-                    const int32_t col = e * kXK + 8 * (v & 7);
-                    const int32_t slot = col / p.rank_pad;
-                    const int32_t id = slot < slots ? slot_list[(int64_t)it.tile * p.cap + slot] : -3;
-                    const uint16_t* src = p.low + (col - slot * p.rank_pad) + (v >> 3) * p.rank_pad;
-                    const uint32_t dst = ring + s * stride + kWBytes + (uint32_t)(v >> 3) * rows * 128u;
+                // The tile's rows of the low-rank products, each only in its
+                // own adapter's columns: 64 columns of hi, then of lo.
+                // Lane = 16-byte vector (8 columns) of one of two rows at a
+                // time, copied (or zeros) to the 128-byte swizzle's place;
+                // the copies of one block fly while the next one's are issued.
+                const uint32_t v = lane & 15u;
+                for (int32_t e = e0; ok && e <= e1 && e0 < e1; ++e) {
+                    if (e < e1) {
+                        const uint32_t adv_s = s + (uint32_t)(e - e0);
+                        const uint32_t bs = adv_s % S, bph = ph ^ ((adv_s / S) & 1u);
+                        ok = wait_phase(empty0 + 8u * bs, bph ^ 1u, ctrl, p, kErrTokens);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        const int32_t col = e * kXK + 8 * (int32_t)(v & 7u);
+                        const int32_t slot = col / p.rank_pad;
+                        const int32_t id = slot < slots ? slot_list[(int64_t)it.tile * p.cap + slot] : -3;
+                        const uint16_t* src = p.low + (int64_t)y * 2 * p.rank_pad + (col - slot * p.rank_pad) +
+                                              (int32_t)(v >> 3) * p.rank_pad;
+                        const uint32_t dst = ring + bs * stride + kWBytes + (v >> 3) * rows * 128u;
+                        if constexpr (kPair) {
 #pragma unroll 1
-                    for (uint32_t k = 0; 32u * k < rows; ++k) {
-                        const int32_t who_k = k == 0 ? who[0] : k == 1 ? who[1] : k == 2 ? who[2] : who[3];
-#pragma unroll 1
-                        for (uint32_t half = 0; half < 2; ++half) {
-                            uint4 q[8];
+                            for (uint32_t k = 0; 32u * k < rows; ++k) {
+                                const int32_t who_k = k == 0 ? who[0] : k == 1 ? who[1] : k == 2 ? who[2] : who[3];
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const uint32_t in32 = 16u * half + 2u * j + (lane >> 4);  // row within 32
-                                const int32_t his = __shfl_sync(0xffffffffu, who_k, (int)in32);
-                                q[j] = make_uint4(0, 0, 0, 0);
-                                if (his == id)
-                                    q[j] = __ldcg(reinterpret_cast<const uint4*>(
-                                        src + (int64_t)(y + (int32_t)(32 * k + in32)) * 2 * p.rank_pad));
+                                for (uint32_t j = 0; j < 16; ++j) {
+                                    const uint32_t in32 = 2u * j + (lane >> 4), i = 32u * k + in32;
+                                    const bool his = __shfl_sync(0xffffffffu, who_k, (int)in32) == id;
+                                    if (i < rows)
+                                        copy_async_16(dst + i * 128u + (((v & 7u) ^ (i & 7u)) << 4),
+                                                      his ? src + (int64_t)i * 2 * p.rank_pad : p.low, his ? 16u : 0u);
+                                }
                             }
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const uint32_t i = 32u * k + 16u * half + 2u * j + (lane >> 4);
-                                if (i < rows)
-                                    st_shared_v4(dst + i * 128u + ((((uint32_t)v & 7u) ^ (i & 7u)) << 4), q[j]);
+                        } else if ((col & ~15) < slots * p.rank_pad) {
+                            // only the rows that the MMAs of these columns
+                            // read (all where they begin an accumulator)
+                            uint32_t lo = 0, hi = rows;
+                            if (e > e0 || it.kb0 < p.num_kb) window(slots, col & ~15, lo, hi);
+                            for (uint32_t i = lo + (lane >> 4); i < hi; i += 2) {
+                                const bool his = row_ids[i] == id;
+                                copy_async_16(dst + i * 128u + (((v & 7u) ^ (i & 7u)) << 4),
+                                              his ? src + (int64_t)i * 2 * p.rank_pad : p.low, his ? 16u : 0u);
                             }
                         }
+                        copy_async_commit();
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        arm(full0 + 8u * s, (uint32_t)(pieces_of(slots, e) * p.rank_box) * 256u);
-                        ++issued;
+                    if (e > e0) {
+                        if (e < e1)
+                            copy_async_wait<1>();
+                        else
+                            copy_async_wait<0>();
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            arm(full0 + 8u * ((s + (uint32_t)(e - 1 - e0)) % S),
+                                (uint32_t)(pieces_of(slots, e - 1) * p.rank_box) * 256u);
+                            ++issued;
+                        }
                     }
-                    if (++s == S) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
+                }
+                if (e0 < e1) {
+                    const uint32_t adv_e = s + (uint32_t)(e1 - e0);
+                    ph ^= (adv_e / S) & 1u;
+                    s = adv_e % S;
                 }
             } else {
                 const uint32_t adv = s + (uint32_t)n_main;
@@ -682,7 +718,8 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                     // chunks; boxes of 8 rows pair up to an MMA's 16
                     const uint64_t x_desc0 = box == 8 ? make_sw128_desc(ring, 1024, 2048)
                                                       : make_sw128_desc(ring, box * 128u, 1024);
-                    for (int32_t e = max(0, it.kb0 - p.num_kb); ok && e < e1; ++e) {
+                    const int32_t e0 = max(0, it.kb0 - p.num_kb);
+                    for (int32_t e = e0; ok && e < e1; ++e) {
                         if (!wait_phase(full0 + 8u * s, ph, ctrl, p, kErrStage)) {
                             ok = false;
                             break;
@@ -693,15 +730,18 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                         const uint64_t b_desc = b_desc0 + (uint64_t)(s * stride16);
                         const uint32_t nk = (uint32_t)pieces_of(slots, e) * box / 16u;
                         // hi's columns, then lo's, with the same rows of the factors
-                        for (uint32_t h = 0; h < 2; ++h)
-                            for (uint32_t k = 0; k < nk; ++k) {
-                                const uint32_t r = 16u * k;
-                                const uint32_t off =
-                                    box == 8 ? k * 4096u : (r / box) * (box * 256u) + (r % box) * 128u;
-                                mma_f16_ss<kCG>(d, a_desc + (off >> 4), b_desc + h * half16 + k * 2u, idesc1 | nbits,
-                                                acc);
-                                acc = 1;
-                            }
+                        for (uint32_t k = 0; k < nk; ++k) {
+                            const uint32_t r = 16u * k;
+                            const uint32_t off = box == 8 ? k * 4096u : (r / box) * (box * 256u) + (r % box) * 128u;
+                            uint32_t lo = 0, hi = (uint32_t)it.w;
+                            if (!kPair && (e > e0 || it.kb0 < p.num_kb))
+                                window(slots, e * kXK + (int32_t)r, lo, hi);
+                            const uint32_t idesc_x = idesc1 | (((hi - lo) >> 3) << 17);
+                            const uint64_t bd = b_desc + (lo * 128u >> 4) + k * 2u;
+                            mma_f16_ss<kCG>(d + lo, a_desc + (off >> 4), bd, idesc_x, acc);
+                            mma_f16_ss<kCG>(d + lo, a_desc + (off >> 4), bd + half16, idesc_x, 1u);
+                            acc = 1;
+                        }
                         mma_commit<kCG>(empty0 + 8u * s, 0x3);
                         if (++s == S) {
                             s = 0;
@@ -754,9 +794,6 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
             const int32_t n = it.n * (kPair ? 256 : 128) + 128 * (int32_t)rank + 32 * (int32_t)quarter + 8 * (int32_t)(lane & 3u);
             const bool in_n = n < p.N;
             const bool whole = it.kb0 == 0 && it.kb1 == it.kb_all;
-            // an item's share without a k-block (adapters: past a tile's last adapter) has an untouched accumulator
-            const bool none = kAdapters && it.kb0 >= p.num_kb &&
-                              it.kb0 - p.num_kb >= extra_blocks(p, nslots[it.tile]);
             if (!kPair && !whole && it.kb0 != 0) {
                 // a share of an item that an earlier CTA began: publish it
                 float4* dst = reinterpret_cast<float4*>(p.ws + (int64_t)blockIdx.x * part) + lane_row;
@@ -766,8 +803,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         __stcg(dst + (int64_t)(c / 4 + j) * 128,
-                               none ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                    : make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+                               make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
                 }
                 release();
                 __threadfence();

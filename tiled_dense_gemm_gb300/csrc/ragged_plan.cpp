@@ -35,8 +35,11 @@ RaggedPlan plan_rows(int64_t T, int64_t G, int64_t N, int64_t K, int64_t R, int6
     p.num_kb = (int32_t)ceil_div(K, kStageK);
     p.n_tiles = (int32_t)ceil_div(N, p.pair ? 256 : 128);
     p.stage_bytes = (int32_t)(128 * kStageK * 2 + cap / (p.pair ? 2 : 1) * kStageK * 2);
-    p.own_slots = R > 0 && !p.pair && T <= cap;
-    const int64_t table = kTurn + round_up((2 * (G + 1) + (p.own_slots ? 257 : 0)) * 4, 16);
+    if (R > 0 && !p.pair && T > cap) {  // single CTAs list the adapters of one row tile
+        p.status = GEMM_ERR_UNSUPPORTED_DEVICE;
+        return p;
+    }
+    const int64_t table = kTurn + round_up((2 * (G + 1) + (R > 0 && !p.pair ? 389 : 0)) * 4, 16);
     // (adapters: room beside it for a block of the kernel that computes low)
     const int64_t room = kSmem - kCtrl - table - (R > 0 ? kLowSmem : 0);
     p.num_stages = (int32_t)std::min<int64_t>(8, room / p.stage_bytes);
