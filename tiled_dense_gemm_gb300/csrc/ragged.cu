@@ -101,9 +101,9 @@ static int launch(void (*fn)(P...), int grid, int threads, size_t smem, int clus
 }
 
 template <typename F>
-static int allow_smem(DeviceState& d, int which, F fn, int bytes = rt::kMaxDynSmem) {
+static int allow_smem(DeviceState& d, int which, F fn) {
     if (d.rg_attr_set[which]) return GEMM_OK;
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, rt::kMaxDynSmem) != cudaSuccess) {
         cudaGetLastError();
         return GEMM_ERR_LAUNCH;
     }
@@ -131,8 +131,6 @@ static int zero_rows(void* y, int64_t ld, int64_t width, int64_t rows, cudaStrea
     return GEMM_OK;
 }
 
-constexpr int kLowTileSmem = rt::kMaxDynSmem - 4096;  // (it has static shared memory too)
-
 struct Adapters {
     const void *A, *B;
     const int32_t* ids;
@@ -140,44 +138,10 @@ struct Adapters {
     int64_t R, rank;
 };
 
-// low for all rows: warp-level MMAs beside the main kernel for up to 1024
-// rows, tensor-core tiles before it for more (8192 rows of K = 4096, rank 64:
-// TODO us against TODO us).
+// low for up to kLowRows rows, beside the main kernel.
 static int run_low(const void* X, const Adapters& ad, uint16_t* low, int64_t T, int64_t K, int64_t ldx,
                    const RaggedPlan& pl, bool bf16, DeviceState& d, cudaStream_t st) {
     int rc;
-    if (T > kLowRows) {
-        LowTileMaps m;
-        LowTileParams q;
-        memset(&q, 0, sizeof(q));
-        q.ids = ad.ids;
-        q.scale = ad.scale;
-        q.low = low;
-        q.T = (int32_t)T;
-        q.R = (int32_t)ad.R;
-        q.num_kb = pl.num_kb;
-        // about one block per multiprocessor
-        q.cap = (int32_t)std::min<int64_t>(128, (T + d.sm_count * 16 - 1) / (d.sm_count * 16) * 16);
-        q.rank = (int32_t)ad.rank;
-        q.rank_pad = pl.rank_pad;
-        q.rank_box = pl.rank_box;
-        q.bf16 = bf16 ? 1 : 0;
-        q.x3d = K % 64 == 0;
-        const int stage = (int)kWBytes + q.cap * kBK * 2;
-        q.num_stages = std::min(kMaxStages, (kLowTileSmem - 1024) / stage);
-        q.tmem_cols = q.cap <= 32 ? 64 : q.cap <= 64 ? 128 : 256;
-        q.err = d.d_err;
-        q.timeout_ns = 2000000000ull + 2000ull * (uint64_t)pl.num_kb;
-        rc = encode_rows(&m.x, X, (uint64_t)K, (uint64_t)T, (uint64_t)ldx, (uint32_t)q.cap, q.x3d ? kBK / 64 : 0, bf16);
-        const uint64_t dims[3] = {(uint64_t)K, (uint64_t)ad.rank, (uint64_t)ad.R};
-        const uint64_t strides[2] = {(uint64_t)K, (uint64_t)(K * ad.rank)};
-        const uint32_t box[3] = {64, (uint32_t)pl.rank_box, 1};
-        if (rc == GEMM_OK) rc = encode(&m.a, ad.A, 3, dims, strides, box, bf16);
-        if (rc == GEMM_OK) rc = allow_smem(d, 6, adapters_low_tile_kernel, kLowTileSmem);
-        if (rc != GEMM_OK) return rc;
-        return launch(adapters_low_tile_kernel, (int)((T + q.cap - 1) / q.cap), kThreads,
-                      (size_t)(1024 + q.num_stages * stage), 1, st, m, q);
-    }
     LowParams q;
     memset(&q, 0, sizeof(q));
     q.X = reinterpret_cast<const uint16_t*>(X);
@@ -277,27 +241,41 @@ static int run_forward(const void* X, const void* W, void* Y, const int32_t* off
         // one buffer: the low-rank rows, the tiles' slot lists, their lengths
         const size_t low_bytes = ((size_t)T * 2 * pl.rank_pad * 2 + 255) / 256 * 256;
         const size_t slot_bytes = (size_t)tiles * pl.cap * 4;
-        rc = rt::grow(&sb.rg_misc, &sb.rg_misc_bytes, low_bytes + slot_bytes + (size_t)tiles * 4, st, false);
+        rc = rt::grow(&sb.rg_misc, &sb.rg_misc_bytes, low_bytes + slot_bytes + (size_t)tiles * 8, st, false);
         if (rc != GEMM_OK) return rc;
         uint8_t* base = reinterpret_cast<uint8_t*>(sb.rg_misc);
+        p.low = reinterpret_cast<const uint16_t*>(base);
         if (pl.pair) {
             SlotParams q;
             memset(&q, 0, sizeof(q));
             q.ids = ad->ids;
             q.slots = reinterpret_cast<int32_t*>(base + low_bytes);
             q.nslots = reinterpret_cast<int32_t*>(base + low_bytes + slot_bytes);
+            q.low_done = reinterpret_cast<uint32_t*>(q.nslots + tiles);
             q.T = (int32_t)T;
             q.R = (int32_t)ad->R;
             q.cap = pl.cap;
             q.tile_w = pl.row_width;
+            q.err = d.d_err;
             rc = launch(adapters_slots_kernel, (int)tiles, 256, 0, 1, st, q);
             if (rc != GEMM_OK) return rc;
             p.slots = q.slots;
             p.nslots = q.nslots;
+            p.low_done = q.low_done;
         }
-        p.low = reinterpret_cast<const uint16_t*>(base);
-        rc = run_low(X, *ad, reinterpret_cast<uint16_t*>(base), T, K, ldx, pl, bf16, d, st);
-        if (rc != GEMM_OK) return rc;
+        if (pl.low_in_main) {
+            const uint64_t dims[3] = {(uint64_t)K, (uint64_t)ad->rank, (uint64_t)ad->R};
+            const uint64_t strides[2] = {(uint64_t)K, (uint64_t)(K * ad->rank)};
+            const uint32_t box[3] = {64, (uint32_t)pl.rank_box, 1};
+            rc = encode(&m.a, ad->A, 3, dims, strides, box, bf16);
+            if (rc != GEMM_OK) return rc;
+            p.low_out = reinterpret_cast<uint16_t*>(base);
+            p.scale = ad->scale;
+            p.rank = (int32_t)ad->rank;
+        } else {
+            rc = run_low(X, *ad, reinterpret_cast<uint16_t*>(base), T, K, ldx, pl, bf16, d, st);
+            if (rc != GEMM_OK) return rc;
+        }
     }
     const size_t smem = (size_t)pl.smem_bytes;
     if (ad) {
@@ -487,7 +465,13 @@ extern "C" int gemm_relu_adapters(const void* X, const void* W, const void* A, c
     if ((rc = rt::init_device_locked(dev)) != GEMM_OK) return rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (K == 0) return zero_rows(Y, ldy, N, T, st);
-    const Adapters ad = {A, B, ids, scale, R, rank};
-    return run_forward(X, W, Y, nullptr, nullptr, T, 1, N, K, ldx, ldy, 0, apply_relu != 0, b_layout == GEMM_B_NK,
-                       dtype == GEMM_DTYPE_BF16, &ad, st, dev);
+    // (a launch lists its row tiles in shared memory: row blocks of what fits)
+    const int64_t block = (int64_t)GEMM_RELU_MAX_GROUPS * 256;
+    for (int64_t t = 0; t < T && rc == GEMM_OK; t += block) {
+        const Adapters ad = {A, B, ids + t, scale, R, rank};
+        rc = run_forward(reinterpret_cast<const uint16_t*>(X) + t * ldx, W, reinterpret_cast<uint16_t*>(Y) + t * ldy,
+                         nullptr, nullptr, std::min(block, T - t), 1, N, K, ldx, ldy, 0, apply_relu != 0,
+                         b_layout == GEMM_B_NK, dtype == GEMM_DTYPE_BF16, &ad, st, dev);
+    }
+    return rc;
 }

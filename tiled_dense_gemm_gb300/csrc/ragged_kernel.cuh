@@ -21,8 +21,8 @@
 // host round trip and no launch of its own.  A group's rows are cut into
 // tiles of equal width, so 260 rows are 144 + 116 and not 256 + 4.
 //
-// Roles (224 threads, one CTA per SM): warp 0 copies row tiles (and builds
-// the adapters' tiles), warp 6 the weights, warp 1 issues the MMAs, warps 2-5
+// Roles (224 threads, one CTA per SM): warp 0 copies row tiles, warp 6 the
+// weights, warp 1 issues the MMAs, warps 2-5
 // drain the accumulators; shared-memory ring of 128-k stages, two TMEM
 // accumulators.  Every wait is bounded.
 #pragma once
@@ -63,6 +63,7 @@ struct Maps {
     CUtensorMap w;             // weights
     CUtensorMap x[kTokBoxes];  // rows, boxes of 16 (i + 1) rows
     CUtensorMap b;             // adapters' second factors
+    CUtensorMap a;             // ... and first ones: boxes of rank_box rows x 64 k
 };
 
 struct Params {
@@ -95,8 +96,11 @@ struct Params {
     const uint16_t* low;     // (T, 2, rank_pad): scale * x A^T, in two parts of the element type
     const int32_t* nslots;   // distinct adapters of each row tile; null: single CTAs, which list them themselves
     const int32_t* slots;    // [tile][cap] their indexes
-    int32_t rank_pad, rank_box, b4d;
+    int32_t rank, rank_pad, rank_box, b4d;
     int32_t R;
+    const float* scale;      // of each adapter, or null: 1
+    uint16_t* low_out;       // pairs: the low-rank products are items of this launch (null: another kernel's)
+    uint32_t* low_done;      // ... and count themselves here, per row tile (zero at the start)
 };
 
 struct __align__(8) Ctrl {
@@ -105,6 +109,7 @@ struct __align__(8) Ctrl {
     uint64_t tmem_full[2];
     uint64_t tmem_empty[2];
     uint64_t final_bar;
+    uint64_t extra[kMaxStages];  // adapters: the stage is free for an extra k-block
     uint32_t tmem_addr;
     int32_t abort_flag;
     int32_t ring_s, ring_ph, ring_lap;
@@ -208,7 +213,11 @@ struct Item {
     int32_t kb0, kb1;   // k-blocks [kb0, kb1) of `kb_all`
     int32_t kb_all;
     uint32_t index;     // item number
+    bool low;           // low-rank products of the row tile (n: which 256 of them), not columns of Y
 };
+
+// Items that compute the low-rank products of a row tile, 256 each.
+__device__ __forceinline__ int32_t low_items(const Params& p, int32_t slots) { return (slots * p.rank_pad + 255) / 256; }
 
 // Extra k-blocks of a row tile: its distinct adapters' ranks side by side.
 __device__ __forceinline__ int32_t extra_blocks(const Params& p, int32_t slots) {
@@ -255,13 +264,17 @@ struct Iter {
     const int32_t* start;
     const int32_t* tiles;
     const int32_t* nslots;
+    const int32_t* lows;  // adapters of pairs: low items before each row tile
+    uint32_t n_low;       // items [0, n_low) are low ones
     uint32_t u, u1, step;
     int32_t kb_all;  // split: k-blocks of every item
 
     __device__ __forceinline__ Iter(const Params& p_, const int32_t* start_, const int32_t* tiles_,
-                                    const int32_t* nslots_, uint32_t worker, uint32_t workers, int32_t max_extra)
-        : p(p_), start(start_), tiles(tiles_), nslots(nslots_) {
+                                    const int32_t* nslots_, const int32_t* lows_, uint32_t worker, uint32_t workers,
+                                    int32_t max_extra)
+        : p(p_), start(start_), tiles(tiles_), nslots(nslots_), lows(lows_) {
         const uint32_t items = (uint32_t)tiles[p.G] * (uint32_t)p.n_tiles;
+        n_low = kPair && kAdapters && p.low_out ? (uint32_t)lows[tiles[p.G]] : 0u;
         kb_all = p.num_kb + (kAdapters ? max_extra : 0);
         if (!kPair && p.split) {
             const uint32_t units = items * (uint32_t)kb_all;
@@ -270,7 +283,7 @@ struct Iter {
             step = 0;
         } else {
             u = worker;
-            u1 = items;
+            u1 = n_low + items;
             step = workers;
         }
     }
@@ -278,6 +291,15 @@ struct Iter {
     static __device__ __forceinline__ uint32_t begin_of(uint32_t units, uint32_t worker, uint32_t workers) {
         const uint32_t q = units / workers, r = units - q * workers;
         return worker * q + min(worker, r);
+    }
+
+    // rows of tile j of the cnt of group g: equal widths, in the MMA's steps
+    __device__ __forceinline__ void row_tile(Item& it, int32_t g, int32_t cnt, int32_t j) {
+        const int32_t s0 = start[g], len = start[g + 1] - s0;
+        constexpr int32_t kGran = kPair ? 32 : 16;
+        it.w = ((len + cnt - 1) / cnt + kGran - 1) / kGran * kGran;
+        it.row0 = s0 + j * it.w;
+        it.valid = min(it.w, len - j * it.w);
     }
 
     __device__ __forceinline__ bool next(Item& it) {
@@ -295,6 +317,24 @@ struct Iter {
             it.kb0 = 0;
         }
         it.index = item;
+        it.low = false;
+        if constexpr (kPair && kAdapters) {
+            if (item < n_low) {
+                int32_t lo = 0, hi = tiles[p.G];  // largest row tile with lows[tile] <= item
+                while (hi - lo > 1) {
+                    const int32_t mid = (lo + hi) >> 1;
+                    if (lows[mid] <= (int32_t)item) lo = mid; else hi = mid;
+                }
+                it.low = true;
+                it.g = 0;
+                it.tile = lo;
+                it.n = (int32_t)item - lows[lo];
+                row_tile(it, 0, tiles[p.G], lo);
+                it.kb_all = it.kb1 = p.num_kb;
+                return true;
+            }
+            item -= n_low;
+        }
         const uint32_t nt = (uint32_t)p.n_tiles;
         const int32_t rt = (int32_t)(item / nt);
         int32_t lo = 0, hi = p.G;  // largest g with tiles[g] <= rt
@@ -311,11 +351,7 @@ struct Iter {
         it.n = (int32_t)(r / rows);
         const int32_t j = (int32_t)(band * kRaster + r - (uint32_t)it.n * rows);
         it.tile = first + j;
-        const int32_t s0 = start[lo], len = start[lo + 1] - s0;
-        constexpr int32_t kGran = kPair ? 32 : 16;
-        it.w = ((len + cnt - 1) / cnt + kGran - 1) / kGran * kGran;
-        it.row0 = s0 + j * it.w;
-        it.valid = min(it.w, len - j * it.w);
+        row_tile(it, lo, cnt, j);
         if (kPair || !p.split) {
             it.kb_all = p.num_kb + (kAdapters ? extra_blocks(p, nslots[it.tile]) : 0);
             it.kb1 = it.kb_all;
@@ -329,6 +365,12 @@ struct Iter {
 __device__ __forceinline__ uint16_t round16(float x, int32_t bf16) {
     if (bf16) return __bfloat16_as_ushort(__float2bfloat16_rn(x));
     return __half_as_ushort(__float2half_rn(x));
+}
+
+// What rounding x to `hi` left out, rounded (nothing where hi is not finite).
+__device__ __forceinline__ uint16_t rest16(float x, uint16_t hi, int32_t bf16) {
+    const float back = bf16 ? __uint_as_float((uint32_t)hi << 16) : __half2float(__ushort_as_half(hi));
+    return round16(isfinite(back) ? x - back : 0.0f, bf16);
 }
 
 // Two values rounded to nearest-even 16-bit floats, a in the low half.
@@ -372,6 +414,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
             // a pair of the adapters' kernel: the peer's row producer arrives too (it may have built its half itself)
             mbar_init(smem_u32(&ctrl->full[s]), (kPair && kAdapters) ? 2 : 1);
             mbar_init(smem_u32(&ctrl->empty[s]), 1);
+            mbar_init(smem_u32(&ctrl->extra[s]), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&ctrl->tmem_full[b]), 1);
@@ -397,8 +440,30 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
     // for all that came before, so X, W, ids, the slot lists and the
     // workspace are ready and Y is free; low alone is waited for where it is
     // read, after the main k-blocks.
-    if (!kAdapters) grid_dependency_wait();
-    if (warp == 6) build_table(p, start, tiles, lane);
+    // Where the low-rank products are this launch's own items, the kernel
+    // before it is any kernel.
+    if (!kAdapters || (kPair && p.low_out)) grid_dependency_wait();
+    int32_t* const lows = tiles + p.G + 1;
+    if (warp == 6) {
+        build_table(p, start, tiles, lane);
+        if (kPair && kAdapters && p.low_out) {
+            __syncwarp();
+            int32_t before = 0;
+            for (int32_t t0 = 0; t0 < tiles[1]; t0 += 32) {
+                const int32_t t = t0 + (int32_t)lane;
+                int32_t n = t < tiles[1] ? low_items(p, __ldcg(p.nslots + t)) : 0;
+                const int32_t mine = n;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int32_t o = __shfl_up_sync(0xffffffffu, n, d);
+                    if ((int)lane >= d) n += o;
+                }
+                if (t < tiles[1]) lows[t] = before + n - mine;
+                before += __shfl_sync(0xffffffffu, n, 31);
+            }
+            if (lane == 0) lows[tiles[1]] = before;
+        }
+    }
     __syncwarp();
     tc_fence_before();
     if (kPair)
@@ -438,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
     const uint32_t tmem_base = ctrl->tmem_addr;
     const uint32_t S = (uint32_t)p.num_stages, stride = (uint32_t)p.stage_bytes;
     const uint32_t full0 = smem_u32(&ctrl->full[0]), empty0 = smem_u32(&ctrl->empty[0]);
-    It iter(p, start, tiles, nslots, worker, workers, max_extra);
+    It iter(p, start, tiles, nslots, lows, worker, workers, max_extra);
     Item it;
 
     // pieces (boxes of rank_box rows of an adapter's second factor) of extra
@@ -451,33 +516,50 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
         return n;
     };
 
+    // an item's extra k-blocks [e0, e1), numbered from 0
+    auto extras_of = [&](const Item& i, int32_t slots, int32_t& e0, int32_t& e1) {
+        e0 = max(0, i.kb0 - p.num_kb);
+        e1 = max(e0, i.low ? 0 : min(i.kb1 - p.num_kb, extra_blocks(p, slots)));
+    };
+    // boxes of rank_box products of a low item that CTA r of the pair holds
+    auto low_pieces = [&](const Item& i, int32_t slots, uint32_t r) {
+        const int32_t per = 128 / p.rank_box;
+        return max(0, min(per, slots * (p.rank_pad / p.rank_box) - (2 * i.n + (int32_t)r) * per));
+    };
+    // expect a stage's bytes (of both CTAs of a pair) on its barrier; of the
+    // adapters' pairs the peer arrives there too
+    auto arm = [&](uint32_t full, uint32_t bytes) {
+        if (!kPair || rank == 0)
+            mbar_arrive_expect_tx(full, bytes);
+        else if (kAdapters)
+            mbar_arrive_cluster(mapa_shared(full, 0));
+    };
+
     if (warp == 0) {
         // ---------------------------------------------------------- row tiles
-        uint32_t s = 0, ph = 0;
-        int32_t issued = 0;
-        bool ok = true;
-        auto arm = [&](uint32_t full, uint32_t bytes) {
-            if (!kPair || rank == 0)
-                mbar_arrive_expect_tx(full, (kPair ? 2u : 1u) * bytes);
-            else if (kAdapters)
-                mbar_arrive_cluster(mapa_shared(full, 0));
-        };
-        while (ok && iter.next(it)) {
-            const uint32_t rows = (uint32_t)it.w / (kPair ? 2u : 1u);
-            const int32_t y = it.row0 + (int32_t)(rank * rows);
-            const int32_t kb_end = kAdapters ? min(it.kb1, p.num_kb) : it.kb1;
-            const int32_t n_main = max(0, kb_end - it.kb0);
-            if (lane == 0) {
+        if (lane == 0) {
+            uint32_t s = 0, ph = 0;
+            uint32_t pos = 0;  // stages passed
+            bool ok = true;
+            while (ok && iter.next(it)) {
+                const uint32_t rows = (uint32_t)it.w / (kPair ? 2u : 1u);
+                const int32_t y = it.row0 + (int32_t)(rank * rows);
+                const int32_t kb_end = kAdapters ? min(it.kb1, p.num_kb) : it.kb1;
+                uint32_t bytes = (kPair ? 2u : 1u) * (kWBytes + rows * (uint32_t)(kBK * 2));
+                if constexpr (kPair && kAdapters) {
+                    if (it.low)
+                        bytes = (uint32_t)((low_pieces(it, nslots[it.tile], 0) + low_pieces(it, nslots[it.tile], 1)) *
+                                           p.rank_box) * 256u + 2u * rows * (uint32_t)(kBK * 2);
+                }
                 const CUtensorMap* m = &maps.x[rows / 16 - 1];
-                uint32_t ls = s, lph = ph;
                 for (int32_t kb = it.kb0; kb < kb_end; ++kb) {
-                    if (!wait_phase(empty0 + 8u * ls, lph ^ 1u, ctrl, p, kErrTokens)) {
+                    if (!wait_phase(empty0 + 8u * s, ph ^ 1u, ctrl, p, kErrTokens)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t full = full0 + 8u * ls;
-                    arm(full, kWBytes + rows * (uint32_t)(kBK * 2));
-                    const uint32_t dst = ring + ls * stride + kWBytes;
+                    const uint32_t full = full0 + 8u * s;
+                    arm(full, bytes);
+                    const uint32_t dst = ring + s * stride + kWBytes;
                     const uint32_t bar = kPair ? mapa_shared(full, 0) : full;
                     if (p.x3d) {
                         load_3d<kPair>(dst, m, bar, 0, y, kb * (kBK / 64));
@@ -485,106 +567,36 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                         load_2d<kPair>(dst, m, bar, kb * kBK, y);
                         load_2d<kPair>(dst + rows * 128u, m, bar, kb * kBK + 64, y);
                     }
-                    ++issued;
-                    if (++ls == S) {
-                        ls = 0;
-                        lph ^= 1u;
+                    ++pos;
+                    if (++s == S) {
+                        s = 0;
+                        ph ^= 1u;
                     }
                 }
-            }
-            if constexpr (kAdapters) {
-                ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-                const uint32_t adv = s + (uint32_t)n_main;
-                ph ^= (adv / S) & 1u;
-                s = adv % S;
-                const int32_t slots = nslots[it.tile];
-                const int32_t e0 = max(0, it.kb0 - p.num_kb), e1 = min(it.kb1 - p.num_kb, extra_blocks(p, slots));
-                int32_t who[4] = {-2, -2, -2, -2};  // adapters of this CTA's rows: lane, lane + 32, ...
-                if (e0 < e1) grid_dependency_wait();  // low
-                if (kPair && e0 < e1) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int32_t t = y + 32 * k + (int32_t)lane;
-                        if (32u * k + lane < rows && t < it.row0 + it.valid) who[k] = __ldcg(p.ids + t);
-                    }
-                }
-                // The tile's rows of the low-rank products, each only in its
-                // own adapter's columns: 64 columns of hi, then of lo.
-                // Lane = 16-byte vector (8 columns) of one of two rows at a
-                // time, copied (or zeros) to the 128-byte swizzle's place;
-                // the copies of one block fly while the next one's are issued.
-                const uint32_t v = lane & 15u;
-                for (int32_t e = e0; ok && e <= e1 && e0 < e1; ++e) {
-                    if (e < e1) {
-                        const uint32_t adv_s = s + (uint32_t)(e - e0);
-                        const uint32_t bs = adv_s % S, bph = ph ^ ((adv_s / S) & 1u);
-                        ok = wait_phase(empty0 + 8u * bs, bph ^ 1u, ctrl, p, kErrTokens);
-                        ok = __all_sync(0xffffffffu, ok);
+                if constexpr (kAdapters) {
+                    // the epilogue's warps fill and arm the extra k-blocks;
+                    // this thread, which is never more than a lap ahead of
+                    // the MMAs, tells them when a stage is free
+                    int32_t e0, e1;
+                    extras_of(it, nslots[it.tile], e0, e1);
+                    for (int32_t e = e0; ok && e < e1; ++e) {
+                        ok = wait_phase(empty0 + 8u * s, ph ^ 1u, ctrl, p, kErrTokens);
                         if (!ok) break;
-                        const int32_t col = e * kXK + 8 * (int32_t)(v & 7u);
-                        const int32_t slot = col / p.rank_pad;
-                        const int32_t id = slot < slots ? slot_list[(int64_t)it.tile * p.cap + slot] : -3;
-                        const uint16_t* src = p.low + (int64_t)y * 2 * p.rank_pad + (col - slot * p.rank_pad) +
-                                              (int32_t)(v >> 3) * p.rank_pad;
-                        const uint32_t dst = ring + bs * stride + kWBytes + (v >> 3) * rows * 128u;
-                        if constexpr (kPair) {
-#pragma unroll 1
-                            for (uint32_t k = 0; 32u * k < rows; ++k) {
-                                const int32_t who_k = k == 0 ? who[0] : k == 1 ? who[1] : k == 2 ? who[2] : who[3];
-#pragma unroll
-                                for (uint32_t j = 0; j < 16; ++j) {
-                                    const uint32_t in32 = 2u * j + (lane >> 4), i = 32u * k + in32;
-                                    const bool his = __shfl_sync(0xffffffffu, who_k, (int)in32) == id;
-                                    if (i < rows)
-                                        copy_async_16(dst + i * 128u + (((v & 7u) ^ (i & 7u)) << 4),
-                                                      his ? src + (int64_t)i * 2 * p.rank_pad : p.low, his ? 16u : 0u);
-                                }
-                            }
-                        } else if ((col & ~15) < slots * p.rank_pad) {
-                            // only the rows that the MMAs of these columns
-                            // read (all where they begin an accumulator)
-                            uint32_t lo = 0, hi = rows;
-                            if (e > e0 || it.kb0 < p.num_kb) window(slots, col & ~15, lo, hi);
-                            for (uint32_t i = lo + (lane >> 4); i < hi; i += 2) {
-                                const bool his = row_ids[i] == id;
-                                copy_async_16(dst + i * 128u + (((v & 7u) ^ (i & 7u)) << 4),
-                                              his ? src + (int64_t)i * 2 * p.rank_pad : p.low, his ? 16u : 0u);
-                            }
-                        }
-                        copy_async_commit();
-                    }
-                    if (e > e0) {
-                        if (e < e1)
-                            copy_async_wait<1>();
-                        else
-                            copy_async_wait<0>();
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            arm(full0 + 8u * ((s + (uint32_t)(e - 1 - e0)) % S),
-                                (uint32_t)(pieces_of(slots, e - 1) * p.rank_box) * 256u);
-                            ++issued;
+                        mbar_arrive(smem_u32(&ctrl->extra[s]));
+                        ++pos;
+                        if (++s == S) {
+                            s = 0;
+                            ph ^= 1u;
                         }
                     }
                 }
-                if (e0 < e1) {
-                    const uint32_t adv_e = s + (uint32_t)(e1 - e0);
-                    ph ^= (adv_e / S) & 1u;
-                    s = adv_e % S;
-                }
-            } else {
-                const uint32_t adv = s + (uint32_t)n_main;
-                ph ^= (adv / S) & 1u;
-                s = adv % S;
-                ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
             }
-        }
-        if (lane == 0 && (!kPair || rank == 0)) {
-            // what an aborting CTA waits for before its shared memory is released
-            const uint32_t pos = (uint32_t)issued;
-            ctrl->ring_s = (int32_t)(pos % S);
-            ctrl->ring_ph = (int32_t)((pos / S) & 1u);
-            ctrl->ring_lap = pos >= S ? 1 : 0;
+            if (!kPair || rank == 0) {
+                // what an aborting CTA waits for before its shared memory is released
+                ctrl->ring_s = (int32_t)(pos % S);
+                ctrl->ring_ph = (int32_t)((pos / S) & 1u);
+                ctrl->ring_lap = pos >= S ? 1 : 0;
+            }
         }
         __syncwarp();
     } else if (warp == 6) {
@@ -595,7 +607,31 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
             const int32_t n0 = it.n * (kPair ? 256 : 128) + 128 * (int32_t)rank;
             const int32_t kb_end = kAdapters ? min(it.kb1, p.num_kb) : it.kb1;
             const int32_t n_main = max(0, kb_end - it.kb0);
-            if (lane == 0) {
+            if (kPair && kAdapters && it.low) {
+                // first factors of the tile's adapters, 128 rows per CTA; a
+                // lane per box of rank_box rows x 64 k
+                const int32_t slots = nslots[it.tile], mine = low_pieces(it, slots, rank);
+                const int32_t piece = (2 * it.n + (int32_t)rank) * (128 / p.rank_box) + (int32_t)(lane >> 1);
+                const int32_t per_slot = p.rank_pad / p.rank_box, slot = piece / per_slot;
+                const bool has = (int32_t)(lane >> 1) < mine;
+                const int32_t id = has ? slot_list[(int64_t)it.tile * p.cap + slot] : 0;
+                uint32_t ls = s, lph = ph;
+                for (int32_t kb = 0; kb < kb_end; ++kb) {
+                    ok = wait_phase(empty0 + 8u * ls, lph ^ 1u, ctrl, p, kErrWeights);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (has)
+                        load_3d<kPair>(ring + ls * stride + (lane & 1u) * (128u * 128u) +
+                                           (lane >> 1) * (uint32_t)p.rank_box * 128u,
+                                       &maps.a, mapa_shared(full0 + 8u * ls, 0), kb * kBK + 64 * (int32_t)(lane & 1u),
+                                       (piece - slot * per_slot) * p.rank_box, id);
+                    __syncwarp();
+                    if (++ls == S) {
+                        ls = 0;
+                        lph ^= 1u;
+                    }
+                }
+            } else if (lane == 0) {
                 uint32_t ls = s, lph = ph;
                 for (int32_t kb = it.kb0; kb < kb_end; ++kb) {
                     if (!wait_phase(empty0 + 8u * ls, lph ^ 1u, ctrl, p, kErrWeights)) {
@@ -630,9 +666,10 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
             s = adv % S;
             if constexpr (kAdapters) {
                 const int32_t slots = nslots[it.tile];
-                const int32_t e1 = min(it.kb1 - p.num_kb, extra_blocks(p, slots));
+                int32_t e0, e1;
+                extras_of(it, slots, e0, e1);
                 const int32_t per = kXK / p.rank_box, per_slot = p.rank_pad / p.rank_box;
-                for (int32_t e = max(0, it.kb0 - p.num_kb); ok && e < e1; ++e) {
+                for (int32_t e = e0; ok && e < e1; ++e) {
                     ok = wait_phase(empty0 + 8u * s, ph ^ 1u, ctrl, p, kErrWeights);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
@@ -667,12 +704,14 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
             const uint32_t tfull0 = smem_u32(&ctrl->tmem_full[0]), tempty0 = smem_u32(&ctrl->tmem_empty[0]);
             const uint32_t cols = p.tmem_cols / 2;
             const uint32_t idesc0 = make_idesc_f16_f32(kPair ? 256 : 128, 0, !p.w_kmajor, false, p.bf16 != 0);
+            const uint32_t idesc_k = make_idesc_f16_f32(kPair ? 256 : 128, 0, false, false, p.bf16 != 0);
             const uint32_t idesc1 = make_idesc_f16_f32(kPair ? 256 : 128, 0, true, false, p.bf16 != 0);
             constexpr uint32_t kK = kBK / 16;
             // weights: MN-major, 64-column chunks of kBK k-rows (16 k-rows =
             // two 1024-byte atoms per MMA), or K-major, 128 rows per 64 k
             const uint64_t a_desc0 = p.w_kmajor ? make_sw128_desc(ring, 16, 1024)
                                                 : make_sw128_desc(ring, (uint32_t)kBK * 128u, 1024);
+            const uint64_t a_desc_k = make_sw128_desc(ring, 16, 1024);
             const uint64_t b_desc0 = make_sw128_desc(ring + kWBytes, 16, 1024);
             uint32_t a_off[kK];
 #pragma unroll
@@ -687,7 +726,9 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                 tc_fence_after();
                 const uint32_t d = tmem_base + buf * cols;
                 const uint32_t nbits = ((uint32_t)it.w >> 3) << 17;
-                const uint32_t idesc = idesc0 | nbits;
+                const bool low = kPair && kAdapters && it.low;
+                const uint32_t idesc = (low ? idesc_k : idesc0) | nbits;
+                const uint64_t a_first = low ? a_desc_k : a_desc0;
                 const uint32_t half16 = ((uint32_t)it.w / (kPair ? 2u : 1u)) * 128u >> 4;  // second 64 k of the rows
                 const int32_t kb_end = kAdapters ? min(it.kb1, p.num_kb) : it.kb1;
                 uint32_t acc = 0;
@@ -697,11 +738,11 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                         break;
                     }
                     tc_fence_after();
-                    const uint64_t a_desc = a_desc0 + (uint64_t)(s * stride16);
+                    const uint64_t a_desc = a_first + (uint64_t)(s * stride16);
                     const uint64_t b_desc = b_desc0 + (uint64_t)(s * stride16);
 #pragma unroll
                     for (uint32_t k = 0; k < kK; ++k)
-                        mma_f16_ss<kCG>(d, a_desc + a_off[k], b_desc + (k / 4) * half16 + (k % 4) * 2u, idesc,
+                        mma_f16_ss<kCG>(d, a_desc + (low ? (k / 4) * (128u * 128u >> 4) + (k % 4) * 2u : a_off[k]), b_desc + (k / 4) * half16 + (k % 4) * 2u, idesc,
                                         k > 0 ? 1u : acc);
                     acc = 1;
                     mma_commit<kCG>(empty0 + 8u * s, 0x3);
@@ -712,13 +753,13 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                 }
                 if constexpr (kAdapters) {
                     const int32_t slots = nslots[it.tile];
-                    const int32_t e1 = min(it.kb1 - p.num_kb, extra_blocks(p, slots));
+                    int32_t e0, e1;
+                    extras_of(it, slots, e0, e1);
                     const uint32_t box = (uint32_t)p.rank_box;
                     // second factors: boxes of `box` k-rows x two 64-column
                     // chunks; boxes of 8 rows pair up to an MMA's 16
                     const uint64_t x_desc0 = box == 8 ? make_sw128_desc(ring, 1024, 2048)
                                                       : make_sw128_desc(ring, box * 128u, 1024);
-                    const int32_t e0 = max(0, it.kb0 - p.num_kb);
                     for (int32_t e = e0; ok && e < e1; ++e) {
                         if (!wait_phase(full0 + 8u * s, ph, ctrl, p, kErrStage)) {
                             ok = false;
@@ -773,7 +814,100 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
         const uint32_t turn = ring + (uint32_t)p.turn_off + quarter * (32u * kTurnPitch);
         const uint32_t turn_st = turn + (lane & 7u) * kTurnPitch + (lane >> 3) * 16u;
         const uint32_t turn_ld = turn + (lane >> 2) * kTurnPitch + (lane & 3u) * 16u;
+        const uint32_t et = threadIdx.x - 64;
+        uint32_t pos = 0;  // adapters: ring stages before the item's extra ones
+        uint32_t extra_ph = 0;  // ... and the phase of each stage's `extra` barrier
+        // Adapters: fill and arm an item's extra k-blocks.  A row tile's
+        // low-rank products, each row only in its own adapter's columns: 64
+        // columns of hi, then of lo.  Thread = 16-byte vector (8 columns) of
+        // one of eight rows at a time, copied (or zeros) to the 128-byte
+        // swizzle's place; one block's copies fly while the next one's are
+        // issued.
+        auto fill_extras = [&]() {
+            const int32_t slots = nslots[it.tile];
+            int32_t e0, e1;
+            extras_of(it, slots, e0, e1);
+            pos += (uint32_t)max(0, min(it.kb1, p.num_kb) - it.kb0);
+            if (e0 == e1) return true;
+            const uint32_t rows = (uint32_t)it.w / (kPair ? 2u : 1u);
+            const int32_t y = it.row0 + (int32_t)(rank * rows);
+            bool ok = true;
+            if (kPair && p.low_out) {
+                // low items come first in every CTA's list: this ends
+                if (et == 0) {
+                    volatile uint32_t* const done = p.low_done + it.tile;
+                    volatile int32_t* const abort_flag = &ctrl->abort_flag;
+                    const uint32_t want = 2u * (uint32_t)low_items(p, slots);
+                    const uint64_t t0 = globaltimer_ns();
+                    while (*done < want)
+                        if (*abort_flag || globaltimer_ns() - t0 > p.timeout_ns) {
+                            *abort_flag = 1;
+                            atomicCAS(p.err, 0, (int32_t)kErrEpi);
+                            ok = false;
+                            break;
+                        }
+                    __threadfence();
+                }
+                ok = named_bar_and(kEpiBarrier, kEpiThreads, ok);
+            } else {
+                grid_dependency_wait();
+            }
+            const uint32_t v = et & 15u, r0 = et >> 4;
+            int32_t who[kPair ? 16 : 1];  // adapters of rows r0, r0 + 8, ...
+            if constexpr (kPair) {
+#pragma unroll
+                for (uint32_t j = 0; j < 16; ++j) {
+                    const int32_t t = y + (int32_t)(r0 + 8u * j);
+                    who[j] = r0 + 8u * j < rows && t < it.row0 + it.valid ? __ldcg(p.ids + t) : -2;
+                }
+            }
+            for (int32_t e = e0; ok && e <= e1; ++e) {
+                if (e < e1) {
+                    const uint32_t at = pos + (uint32_t)(e - e0), st = at % S;
+                    ok = wait_phase(smem_u32(&ctrl->extra[st]), (extra_ph >> st) & 1u, ctrl, p, kErrTokens);
+                    extra_ph ^= 1u << st;
+                    ok = named_bar_and(kEpiBarrier, kEpiThreads, ok);
+                    if (!ok) break;
+                    const int32_t col = e * kXK + 8 * (int32_t)(v & 7u);
+                    const int32_t slot = col / p.rank_pad;
+                    const int32_t id = slot < slots ? slot_list[(int64_t)it.tile * p.cap + slot] : -3;
+                    const uint16_t* src = p.low + (int64_t)y * 2 * p.rank_pad + (col - slot * p.rank_pad) +
+                                          (int32_t)(v >> 3) * p.rank_pad;
+                    const uint32_t dst = ring + st * stride + kWBytes + (v >> 3) * rows * 128u;
+                    auto put = [&](uint32_t i, bool his) {
+                        copy_async_16(dst + i * 128u + (((v & 7u) ^ (i & 7u)) << 4),
+                                      his ? src + (int64_t)i * 2 * p.rank_pad : p.low, his ? 16u : 0u);
+                    };
+                    if constexpr (kPair) {
+#pragma unroll
+                        for (uint32_t j = 0; j < 16; ++j)
+                            if (r0 + 8u * j < rows) put(r0 + 8u * j, who[j] == id);
+                    } else if ((col & ~15) < slots * p.rank_pad) {
+                        // only the rows that the MMAs of these columns read
+                        // (all where they begin an accumulator)
+                        uint32_t lo = 0, hi = rows;
+                        if (e > e0 || it.kb0 < p.num_kb) window(slots, col & ~15, lo, hi);
+                        for (uint32_t i = lo + r0; i < hi; i += 8) put(i, row_ids[i] == id);
+                    }
+                    copy_async_commit();
+                }
+                if (e > e0) {
+                    if (e < e1)
+                        copy_async_wait<1>();
+                    else
+                        copy_async_wait<0>();
+                    fence_proxy_async_smem();
+                    named_bar_sync(kEpiBarrier, kEpiThreads);
+                    if (et == 0)
+                        arm(full0 + 8u * ((pos + (uint32_t)(e - 1 - e0)) % S),
+                            (uint32_t)(pieces_of(slots, e - 1) * p.rank_box) * (kPair ? 512u : 256u));
+                }
+            }
+            pos += (uint32_t)(e1 - e0);
+            return ok;
+        };
         while (iter.next(it)) {
+            if (kAdapters && !fill_extras()) break;
             const uint32_t buf = local & 1u, bph = (local >> 1) & 1u;
             bool ok = wait_phase(smem_u32(&ctrl->tmem_full[buf]), bph, ctrl, p, kErrEpi);
             ok = named_bar_and(kEpiBarrier, kEpiThreads, ok);
@@ -790,6 +924,37 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                         mbar_arrive(smem_u32(&ctrl->tmem_empty[buf]));
                 }
             };
+            if constexpr (kPair && kAdapters) {
+                if (it.low) {
+                    // this lane's product: number j of adapter id's rank
+                    const int32_t r = 256 * it.n + 128 * (int32_t)rank + (int32_t)lane_row;
+                    const int32_t slot = r / p.rank_pad, j = r - slot * p.rank_pad;
+                    const int32_t id = slot < nslots[it.tile] ? slot_list[(int64_t)it.tile * p.cap + slot] : -3;
+                    const float scale = id >= 0 && p.scale ? __ldcg(p.scale + id) : 1.0f;
+                    for (int32_t c = 0; c < it.w; c += 32) {
+                        const int32_t t = it.row0 + c + (int32_t)lane;
+                        const int32_t his = c + (int32_t)lane < it.valid ? __ldcg(p.ids + t) : -2;
+                        __syncwarp();
+                        tmem_load_32cols(taddr + c, v);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            if (__shfl_sync(0xffffffffu, his, i) != id) continue;
+                            // columns past the rank are zeros whatever the scale is
+                            const float x = j < p.rank ? v[i] * scale : 0.0f;
+                            const uint16_t hi = round16(x, p.bf16);
+                            uint16_t* dst = p.low_out + (int64_t)(it.row0 + c + i) * 2 * p.rank_pad + j;
+                            dst[0] = hi;
+                            dst[p.rank_pad] = rest16(x, hi, p.bf16);
+                        }
+                    }
+                    release();
+                    __threadfence();
+                    named_bar_sync(kEpiBarrier, kEpiThreads);
+                    if (et == 0) atomicAdd(p.low_done + it.tile, 1u);
+                    ++local;
+                    continue;
+                }
+            }
             // this thread's 8 columns of Y (of rows lane / 4, + 8, ...)
             const int32_t n = it.n * (kPair ? 256 : 128) + 128 * (int32_t)rank + 32 * (int32_t)quarter + 8 * (int32_t)(lane & 3u);
             const bool in_n = n < p.N;
@@ -913,7 +1078,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
     }
 
     // (a later kernel's wait covers this one only: it must not end first)
-    if (kAdapters) grid_dependency_wait();
+    if (kAdapters && !p.low_out) grid_dependency_wait();
     __syncthreads();
     if (threadIdx.x == 0 && *(volatile int32_t*)&ctrl->abort_flag) drain_ring(ctrl, full0, S);
     tc_fence_before();
