@@ -231,18 +231,13 @@ __global__ void __launch_bounds__(kLowWarps * 32, 2) adapters_low_kernel(const _
                 for (int h = 0; h < 2; ++h) {
                     if (!(h ? in1 : in0)) continue;
                     const int32_t j = j0 + n * 8 + tig * 2;
-                    uint32_t hi = 0, rest = 0;
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        // columns past the rank are zeros whatever the scale is
-                        const float v = j + c < p.rank ? acc[n][2 * h + c] * scale : 0.0f;
-                        const uint16_t b = round16(v, p.bf16);
-                        hi |= (uint32_t)b << (16 * c);
-                        rest |= (uint32_t)rest16(v, b, p.bf16) << (16 * c);
-                    }
+                    // columns past the rank are zeros whatever the scale is
+                    const float v0 = j < p.rank ? acc[n][2 * h] * scale : 0.0f;
+                    const float v1 = j + 1 < p.rank ? acc[n][2 * h + 1] * scale : 0.0f;
+                    const uint32_t hi = pack16(v0, v1, p.bf16);
                     uint16_t* dst = p.low + (int64_t)(row0 + 8 * h + g) * 2 * p.rank_pad + j;
                     *reinterpret_cast<uint32_t*>(dst) = hi;
-                    *reinterpret_cast<uint32_t*>(dst + p.rank_pad) = rest;
+                    *reinterpret_cast<uint32_t*>(dst + p.rank_pad) = rest16x2(v0, v1, hi, p.bf16);
                 }
         }
     }

@@ -233,6 +233,8 @@ static int run_forward(const void* X, const void* W, void* Y, const int32_t* off
         p.R = (int32_t)ad->R;
         p.rank_box = pl.rank_box;
         p.rank_pad = pl.rank_pad;
+        p.box_shift = pl.rank_box == 8 ? 3 : pl.rank_box == 16 ? 4 : pl.rank_box == 32 ? 5 : 6;
+        p.per_slot = pl.rank_pad / pl.rank_box;
         p.b4d = N % 64 == 0;
         rc = encode_stack(&m.b, ad->B, (uint64_t)N, (uint64_t)ad->rank, (uint64_t)ad->R, (uint32_t)pl.rank_box, p.b4d,
                           bf16);
@@ -268,6 +270,10 @@ static int run_forward(const void* X, const void* W, void* Y, const int32_t* off
             const uint64_t strides[2] = {(uint64_t)K, (uint64_t)(K * ad->rank)};
             const uint32_t box[3] = {64, (uint32_t)pl.rank_box, 1};
             rc = encode(&m.a, ad->A, 3, dims, strides, box, bf16);
+            p.a4d = K % 64 == 0;
+            if (rc == GEMM_OK && p.a4d)
+                rc = encode_stack(&m.a4, ad->A, (uint64_t)K, (uint64_t)ad->rank, (uint64_t)ad->R,
+                                  (uint32_t)pl.rank_box, true, bf16);
             if (rc != GEMM_OK) return rc;
             p.low_out = reinterpret_cast<uint16_t*>(base);
             p.scale = ad->scale;

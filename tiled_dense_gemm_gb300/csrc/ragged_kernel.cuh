@@ -63,7 +63,7 @@ struct Maps {
     CUtensorMap w;             // weights
     CUtensorMap x[kTokBoxes];  // rows, boxes of 16 (i + 1) rows
     CUtensorMap b;             // adapters' second factors
-    CUtensorMap a;             // ... and first ones: boxes of rank_box rows x 64 k
+    CUtensorMap a, a4;         // ... and first ones: boxes of rank_box rows x 64 k; a4: x 2 x 64 k
 };
 
 struct Params {
@@ -96,7 +96,9 @@ struct Params {
     const uint16_t* low;     // (T, 2, rank_pad): scale * x A^T, in two parts of the element type
     const int32_t* nslots;   // distinct adapters of each row tile; null: single CTAs, which list them themselves
     const int32_t* slots;    // [tile][cap] their indexes
-    int32_t rank, rank_pad, rank_box, b4d;
+    int32_t rank, rank_pad, rank_box, b4d, a4d;  // rank_box: 8, 16, 32 or 64; rank_pad a multiple of it
+    int32_t box_shift;       // rank_box = 1 << box_shift
+    int32_t per_slot;        // rank_pad / rank_box
     int32_t R;
     const float* scale;      // of each adapter, or null: 1
     uint16_t* low_out;       // pairs: the low-rank products are items of this launch (null: another kernel's)
@@ -110,6 +112,7 @@ struct __align__(8) Ctrl {
     uint64_t tmem_empty[2];
     uint64_t final_bar;
     uint64_t extra[kMaxStages];  // adapters: the stage is free for an extra k-block
+    uint64_t peer[kMaxStages];   // ... and, of a pair's leader, filled by the peer
     uint32_t tmem_addr;
     int32_t abort_flag;
     int32_t ring_s, ring_ph, ring_lap;
@@ -131,6 +134,19 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, Ctrl* 
             return false;
         }
     }
+}
+
+// The same for arrivals from the other CTA of a pair.
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, Ctrl* ctrl, const Params& p) {
+    volatile int32_t* abort_flag = &ctrl->abort_flag;
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait_acq_cluster(bar, parity))
+        if (*abort_flag || globaltimer_ns() - t0 > p.timeout_ns) {
+            *abort_flag = 1;
+            atomicCAS(p.err, 0, (int32_t)kErrEpi);
+            return false;
+        }
+    return true;
 }
 
 // Bounded wait (100 us in all) for the copies that an aborting CTA has in
@@ -216,8 +232,27 @@ struct Item {
     bool low;           // low-rank products of the row tile (n: which 256 of them), not columns of Y
 };
 
-// Items that compute the low-rank products of a row tile, 256 each.
-__device__ __forceinline__ int32_t low_items(const Params& p, int32_t slots) { return (slots * p.rank_pad + 255) / 256; }
+// The slot (position among a row tile's adapters) that box `box` of its
+// ranks belongs to.  (Divisions cost the single-thread roles ~100 cycles
+// each; ranks up to 64 need none.)
+__device__ __forceinline__ int32_t slot_of(const Params& p, int32_t box) {
+    return p.per_slot == 1 ? box : box / p.per_slot;
+}
+
+// Low items compute the low-rank products of a row tile, boxes of rank_box of
+// them at a time: one box per CTA of the pair where the tile has at most two,
+// or boxes are large (64), which takes one copy per stage; else as many as
+// the MMA's 128 rows hold, at two copies per box (copies issue one after
+// another, ~450 cycles each: four per stage made an item of 32 stages 33 us,
+// one makes it TODO).
+__device__ __forceinline__ int32_t low_boxes(const Params& p, int32_t slots) {
+    return p.rank_box == 64 || slots * p.per_slot <= 2 ? 1 : 128 >> p.box_shift;
+}
+
+__device__ __forceinline__ int32_t low_items(const Params& p, int32_t slots) {
+    const int32_t boxes = slots * p.per_slot;
+    return p.rank_box == 64 || boxes <= 2 ? (boxes + 1) / 2 : (boxes + (256 >> p.box_shift) - 1) >> (8 - p.box_shift);
+}
 
 // Extra k-blocks of a row tile: its distinct adapters' ranks side by side.
 __device__ __forceinline__ int32_t extra_blocks(const Params& p, int32_t slots) {
@@ -367,12 +402,6 @@ __device__ __forceinline__ uint16_t round16(float x, int32_t bf16) {
     return __half_as_ushort(__float2half_rn(x));
 }
 
-// What rounding x to `hi` left out, rounded (nothing where hi is not finite).
-__device__ __forceinline__ uint16_t rest16(float x, uint16_t hi, int32_t bf16) {
-    const float back = bf16 ? __uint_as_float((uint32_t)hi << 16) : __half2float(__ushort_as_half(hi));
-    return round16(isfinite(back) ? x - back : 0.0f, bf16);
-}
-
 // Two values rounded to nearest-even 16-bit floats, a in the low half.
 __device__ __forceinline__ uint32_t pack16(float a, float b, int32_t bf16) {
     if (bf16) {
@@ -381,6 +410,18 @@ __device__ __forceinline__ uint32_t pack16(float a, float b, int32_t bf16) {
     }
     __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float2 unpack16(uint32_t x, int32_t bf16) {
+    if (bf16) return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
+    return __half22float2(*reinterpret_cast<const __half2*>(&x));
+}
+
+// What rounding x and y to the pair `hi` left out, rounded (nothing where hi
+// is not finite).
+__device__ __forceinline__ uint32_t rest16x2(float x, float y, uint32_t hi, int32_t bf16) {
+    const float2 back = unpack16(hi, bf16);
+    return pack16(isfinite(back.x) ? x - back.x : 0.0f, isfinite(back.y) ? y - back.y : 0.0f, bf16);
 }
 
 // A pair of 16-bit floats, each +0 where its gate is not positive (sign set,
@@ -411,10 +452,10 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
 
     if (warp == 2 && lane == 0) {
         for (int s = 0; s < p.num_stages; ++s) {
-            // a pair of the adapters' kernel: the peer's row producer arrives too (it may have built its half itself)
-            mbar_init(smem_u32(&ctrl->full[s]), (kPair && kAdapters) ? 2 : 1);
+            mbar_init(smem_u32(&ctrl->full[s]), 1);
             mbar_init(smem_u32(&ctrl->empty[s]), 1);
             mbar_init(smem_u32(&ctrl->extra[s]), 1);
+            mbar_init(smem_u32(&ctrl->peer[s]), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&ctrl->tmem_full[b]), 1);
@@ -490,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
     // rows [lo, hi) that the 16 products from column `col` of the extra
     // k-blocks reach (two adapters of 8 products: both)
     auto window = [&](int32_t slots, int32_t col, uint32_t& lo, uint32_t& hi) {
-        const int32_t a = col / p.rank_pad, b = (col + 8) / p.rank_pad;
+        const int32_t a = slot_of(p, col >> p.box_shift), b = slot_of(p, (col + 8) >> p.box_shift);
         const uint32_t wa = (uint32_t)windows[a];
         lo = wa & 0xFFFFu;
         hi = wa >> 16;
@@ -510,8 +551,8 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
     // k-block e of a tile with `slots` adapters; a box of 8 rows is half of
     // an MMA's 16, so their number is made even with one of zeros
     auto pieces_of = [&](int32_t slots, int32_t e) {
-        const int32_t per = kXK / p.rank_box;
-        int32_t n = min(per, slots * (p.rank_pad / p.rank_box) - e * per);
+        const int32_t per = kXK >> p.box_shift;
+        int32_t n = min(per, slots * p.per_slot - e * per);
         if (p.rank_box == 8) n = (n + 1) & ~1;
         return n;
     };
@@ -523,16 +564,12 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
     };
     // boxes of rank_box products of a low item that CTA r of the pair holds
     auto low_pieces = [&](const Item& i, int32_t slots, uint32_t r) {
-        const int32_t per = 128 / p.rank_box;
-        return max(0, min(per, slots * (p.rank_pad / p.rank_box) - (2 * i.n + (int32_t)r) * per));
+        const int32_t per = low_boxes(p, slots);
+        return max(0, min(per, slots * p.per_slot - (2 * i.n + (int32_t)r) * per));
     };
-    // expect a stage's bytes (of both CTAs of a pair) on its barrier; of the
-    // adapters' pairs the peer arrives there too
+    // expect a stage's bytes (of both CTAs of a pair) on its barrier
     auto arm = [&](uint32_t full, uint32_t bytes) {
-        if (!kPair || rank == 0)
-            mbar_arrive_expect_tx(full, bytes);
-        else if (kAdapters)
-            mbar_arrive_cluster(mapa_shared(full, 0));
+        if (!kPair || rank == 0) mbar_arrive_expect_tx(full, bytes);
     };
 
     if (warp == 0) {
@@ -611,20 +648,26 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                 // first factors of the tile's adapters, 128 rows per CTA; a
                 // lane per box of rank_box rows x 64 k
                 const int32_t slots = nslots[it.tile], mine = low_pieces(it, slots, rank);
-                const int32_t piece = (2 * it.n + (int32_t)rank) * (128 / p.rank_box) + (int32_t)(lane >> 1);
-                const int32_t per_slot = p.rank_pad / p.rank_box, slot = piece / per_slot;
-                const bool has = (int32_t)(lane >> 1) < mine;
+                const int32_t per = low_boxes(p, slots);
+                const int32_t piece = (2 * it.n + (int32_t)rank) * per + (int32_t)(lane >> 1);
+                const int32_t slot = slot_of(p, piece);
+                const bool one = per == 1 && p.a4d;  // both 64-k boxes in one copy
+                const bool has = (int32_t)(lane >> 1) < mine && !(one && (lane & 1u));
+                const uint32_t sub = (per == 1 ? (uint32_t)p.rank_box : 128u) * 128u;  // from one 64 k to the next
                 const int32_t id = has ? slot_list[(int64_t)it.tile * p.cap + slot] : 0;
                 uint32_t ls = s, lph = ph;
                 for (int32_t kb = 0; kb < kb_end; ++kb) {
                     ok = wait_phase(empty0 + 8u * ls, lph ^ 1u, ctrl, p, kErrWeights);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
-                    if (has)
-                        load_3d<kPair>(ring + ls * stride + (lane & 1u) * (128u * 128u) +
-                                           (lane >> 1) * (uint32_t)p.rank_box * 128u,
+                    const int32_t row = (piece - slot * p.per_slot) * p.rank_box;
+                    if (has && one)
+                        load_4d<kPair>(ring + ls * stride, &maps.a4, mapa_shared(full0 + 8u * ls, 0), 0, row,
+                                       kb * (kBK / 64), id);
+                    else if (has)
+                        load_3d<kPair>(ring + ls * stride + (lane & 1u) * sub + (lane >> 1) * (uint32_t)p.rank_box * 128u,
                                        &maps.a, mapa_shared(full0 + 8u * ls, 0), kb * kBK + 64 * (int32_t)(lane & 1u),
-                                       (piece - slot * per_slot) * p.rank_box, id);
+                                       row, id);
                     __syncwarp();
                     if (++ls == S) {
                         ls = 0;
@@ -668,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                 const int32_t slots = nslots[it.tile];
                 int32_t e0, e1;
                 extras_of(it, slots, e0, e1);
-                const int32_t per = kXK / p.rank_box, per_slot = p.rank_pad / p.rank_box;
+                const int32_t per = kXK >> p.box_shift;
                 for (int32_t e = e0; ok && e < e1; ++e) {
                     ok = wait_phase(empty0 + 8u * s, ph ^ 1u, ctrl, p, kErrWeights);
                     ok = __all_sync(0xffffffffu, ok);
@@ -677,10 +720,10 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                     const uint32_t bar = kPair ? mapa_shared(full, 0) : full;
                     if ((int32_t)lane < pieces_of(slots, e)) {
                         const int32_t piece = e * per + (int32_t)lane;
-                        const int32_t slot = piece / per_slot;
+                        const int32_t slot = slot_of(p, piece);
                         // (past the last adapter: a box of zeros, beyond the tensor)
                         const int32_t id = slot < slots ? slot_list[(int64_t)it.tile * p.cap + slot] : p.R;
-                        const int32_t row = (piece - slot * per_slot) * p.rank_box;
+                        const int32_t row = (piece - slot * p.per_slot) * p.rank_box;
                         const uint32_t dst = ring + s * stride + lane * (uint32_t)p.rank_box * 256u;
                         if (p.b4d) {
                             load_4d<kPair>(dst, &maps.b, bar, 0, row, n0 / 64, id);
@@ -726,31 +769,38 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                 tc_fence_after();
                 const uint32_t d = tmem_base + buf * cols;
                 const uint32_t nbits = ((uint32_t)it.w >> 3) << 17;
-                const bool low = kPair && kAdapters && it.low;
-                const uint32_t idesc = (low ? idesc_k : idesc0) | nbits;
-                const uint64_t a_first = low ? a_desc_k : a_desc0;
                 const uint32_t half16 = ((uint32_t)it.w / (kPair ? 2u : 1u)) * 128u >> 4;  // second 64 k of the rows
                 const int32_t kb_end = kAdapters ? min(it.kb1, p.num_kb) : it.kb1;
                 uint32_t acc = 0;
-                for (int32_t kb = it.kb0; kb < kb_end; ++kb) {
-                    if (!wait_phase(full0 + 8u * s, ph, ctrl, p, kErrStage)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint64_t a_desc = a_first + (uint64_t)(s * stride16);
-                    const uint64_t b_desc = b_desc0 + (uint64_t)(s * stride16);
+                // the k-blocks of [it.kb0, kb_end); weights from `a_first`, k-step k at offset(k)
+                auto main_blocks = [&](uint64_t a_first, uint32_t idesc, auto offset) {
+                    for (int32_t kb = it.kb0; kb < kb_end; ++kb) {
+                        if (!wait_phase(full0 + 8u * s, ph, ctrl, p, kErrStage)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint64_t a_desc = a_first + (uint64_t)(s * stride16);
+                        const uint64_t b_desc = b_desc0 + (uint64_t)(s * stride16);
 #pragma unroll
-                    for (uint32_t k = 0; k < kK; ++k)
-                        mma_f16_ss<kCG>(d, a_desc + (low ? (k / 4) * (128u * 128u >> 4) + (k % 4) * 2u : a_off[k]), b_desc + (k / 4) * half16 + (k % 4) * 2u, idesc,
-                                        k > 0 ? 1u : acc);
-                    acc = 1;
-                    mma_commit<kCG>(empty0 + 8u * s, 0x3);
-                    if (++s == S) {
-                        s = 0;
-                        ph ^= 1u;
+                        for (uint32_t k = 0; k < kK; ++k)
+                            mma_f16_ss<kCG>(d, a_desc + offset(k), b_desc + (k / 4) * half16 + (k % 4) * 2u, idesc,
+                                            k > 0 ? 1u : acc);
+                        acc = 1;
+                        mma_commit<kCG>(empty0 + 8u * s, 0x3);
+                        if (++s == S) {
+                            s = 0;
+                            ph ^= 1u;
+                        }
                     }
-                }
+                };
+                if (kPair && kAdapters && it.low) {
+                    // (one box: the MMA's rows past it read what lies there, into lanes that nothing reads)
+                    const uint32_t sub16 =
+                        (low_boxes(p, nslots[it.tile]) == 1 ? (uint32_t)p.rank_box : 128u) * 128u >> 4;
+                    main_blocks(a_desc_k, idesc_k | nbits, [=](uint32_t k) { return (k / 4) * sub16 + (k % 4) * 2u; });
+                } else
+                    main_blocks(a_desc0, idesc0 | nbits, [&](uint32_t k) { return a_off[k]; });
                 if constexpr (kAdapters) {
                     const int32_t slots = nslots[it.tile];
                     int32_t e0, e1;
@@ -769,11 +819,11 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                         tc_fence_after();
                         const uint64_t a_desc = x_desc0 + (uint64_t)(s * stride16);
                         const uint64_t b_desc = b_desc0 + (uint64_t)(s * stride16);
-                        const uint32_t nk = (uint32_t)pieces_of(slots, e) * box / 16u;
+                        const uint32_t nk = (uint32_t)pieces_of(slots, e) << p.box_shift >> 4;
                         // hi's columns, then lo's, with the same rows of the factors
                         for (uint32_t k = 0; k < nk; ++k) {
                             const uint32_t r = 16u * k;
-                            const uint32_t off = box == 8 ? k * 4096u : (r / box) * (box * 256u) + (r % box) * 128u;
+                            const uint32_t off = box == 8 ? k * 4096u : (r & ~(box - 1u)) * 256u + (r & (box - 1u)) * 128u;
                             uint32_t lo = 0, hi = (uint32_t)it.w;
                             if (!kPair && (e > e0 || it.kb0 < p.num_kb))
                                 window(slots, e * kXK + (int32_t)r, lo, hi);
@@ -869,7 +919,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                     ok = named_bar_and(kEpiBarrier, kEpiThreads, ok);
                     if (!ok) break;
                     const int32_t col = e * kXK + 8 * (int32_t)(v & 7u);
-                    const int32_t slot = col / p.rank_pad;
+                    const int32_t slot = slot_of(p, col >> p.box_shift);
                     const int32_t id = slot < slots ? slot_list[(int64_t)it.tile * p.cap + slot] : -3;
                     const uint16_t* src = p.low + (int64_t)y * 2 * p.rank_pad + (col - slot * p.rank_pad) +
                                           (int32_t)(v >> 3) * p.rank_pad;
@@ -898,13 +948,23 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                         copy_async_wait<0>();
                     fence_proxy_async_smem();
                     named_bar_sync(kEpiBarrier, kEpiThreads);
-                    if (et == 0)
-                        arm(full0 + 8u * ((pos + (uint32_t)(e - 1 - e0)) % S),
-                            (uint32_t)(pieces_of(slots, e - 1) * p.rank_box) * (kPair ? 512u : 256u));
+                    if (et == 0) {
+                        const uint32_t st = (pos + (uint32_t)(e - 1 - e0)) % S;
+                        if (kPair && rank != 0) {
+                            mbar_arrive_cluster(mapa_shared(smem_u32(&ctrl->peer[st]), 0));
+                        } else {
+                            // (extra_ph has moved on: once since this block, which is the last use of its stage)
+                            if (kPair)
+                                ok = wait_cluster(smem_u32(&ctrl->peer[st]), ((extra_ph >> st) & 1u) ^ 1u, ctrl, p);
+                            if (ok)
+                                mbar_arrive_expect_tx(full0 + 8u * st, (uint32_t)(pieces_of(slots, e - 1) * p.rank_box) *
+                                                                           (kPair ? 512u : 256u));
+                        }
+                    }
                 }
             }
             pos += (uint32_t)(e1 - e0);
-            return ok;
+            return named_bar_and(kEpiBarrier, kEpiThreads, ok);
         };
         while (iter.next(it)) {
             if (kAdapters && !fill_extras()) break;
@@ -927,24 +987,28 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
             if constexpr (kPair && kAdapters) {
                 if (it.low) {
                     // this lane's product: number j of adapter id's rank
-                    const int32_t r = 256 * it.n + 128 * (int32_t)rank + (int32_t)lane_row;
-                    const int32_t slot = r / p.rank_pad, j = r - slot * p.rank_pad;
-                    const int32_t id = slot < nslots[it.tile] ? slot_list[(int64_t)it.tile * p.cap + slot] : -3;
+                    const int32_t held = low_boxes(p, nslots[it.tile]) * p.rank_box;  // of each CTA
+                    const int32_t r = (2 * it.n + (int32_t)rank) * held + (int32_t)lane_row;
+                    const int32_t slot = slot_of(p, r >> p.box_shift), j = r - slot * p.rank_pad;
+                    const int32_t id = (int32_t)lane_row < held && slot < nslots[it.tile] ? slot_list[(int64_t)it.tile * p.cap + slot] : -3;
                     const float scale = id >= 0 && p.scale ? __ldcg(p.scale + id) : 1.0f;
                     for (int32_t c = 0; c < it.w; c += 32) {
                         const int32_t t = it.row0 + c + (int32_t)lane;
                         const int32_t his = c + (int32_t)lane < it.valid ? __ldcg(p.ids + t) : -2;
                         __syncwarp();
                         tmem_load_32cols(taddr + c, v);
+                        uint16_t* dst = p.low_out + (int64_t)(it.row0 + c) * 2 * p.rank_pad + j;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            if (__shfl_sync(0xffffffffu, his, i) != id) continue;
-                            // columns past the rank are zeros whatever the scale is
-                            const float x = j < p.rank ? v[i] * scale : 0.0f;
-                            const uint16_t hi = round16(x, p.bf16);
-                            uint16_t* dst = p.low_out + (int64_t)(it.row0 + c + i) * 2 * p.rank_pad + j;
-                            dst[0] = hi;
-                            dst[p.rank_pad] = rest16(x, hi, p.bf16);
+                        for (int i = 0; i < 32; i += 2, dst += 4 * p.rank_pad) {
+                            const bool a = __shfl_sync(0xffffffffu, his, i) == id;
+                            const bool b = __shfl_sync(0xffffffffu, his, i + 1) == id;
+                            // (columns past the rank are zeros whatever the scale is)
+                            const float x = j < p.rank ? v[i] * scale : 0.0f, y = j < p.rank ? v[i + 1] * scale : 0.0f;
+                            const uint32_t hi = pack16(x, y, p.bf16), rest = rest16x2(x, y, hi, p.bf16);
+                            if (a) dst[0] = (uint16_t)hi;
+                            if (a) dst[p.rank_pad] = (uint16_t)rest;
+                            if (b) dst[2 * p.rank_pad] = (uint16_t)(hi >> 16);
+                            if (b) dst[3 * p.rank_pad] = (uint16_t)(rest >> 16);
                         }
                     }
                     release();
