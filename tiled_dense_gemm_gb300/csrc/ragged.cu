@@ -139,7 +139,7 @@ struct Adapters {
 };
 
 // low for up to kLowRows rows, beside the main kernel.
-static int run_low(const void* X, const Adapters& ad, uint16_t* low, int64_t T, int64_t K, int64_t ldx,
+static int run_low(const void* X, const Adapters& ad, uint16_t* low, int64_t T, int64_t N, int64_t K, int64_t ldx,
                    const RaggedPlan& pl, bool bf16, DeviceState& d, cudaStream_t st) {
     int rc;
     LowParams q;
@@ -162,9 +162,16 @@ static int run_low(const void* X, const Adapters& ad, uint16_t* low, int64_t T, 
     const int nt = pl.rank_box / 8;
     q.passes = pl.rank_pad / pl.rank_box;
     const int64_t jobs = (T + 15) / 16 * q.slot_step * q.passes;
-    // few jobs share each reduction between the CTAs of a cluster
+    // Beside the main kernel where it reads little: the main kernel's deep
+    // queues of copies starve it of DRAM (48 adapters of rank 32 at K = N =
+    // 8192: low took 32 us beside it, 13 us before it).  Then that kernel starts
+    // when low's loads are in.
+    q.early = std::min(T, ad.R) * ad.rank * 64 <= N ? 1 : 0;
+    // few jobs share each reduction between the CTAs of a cluster (one CTA
+    // per multiprocessor leaves room there for one of the main kernel)
+    const int64_t room = q.early ? d.sm_count : 2 * (int64_t)d.sm_count;
     q.k_split = 1;
-    while (q.k_split < 8 && jobs * q.k_split * 2 <= 2 * d.sm_count && K > 256 * q.k_split) q.k_split *= 2;
+    while (q.k_split < 8 && jobs * q.k_split * 2 <= room && K > 256 * q.k_split) q.k_split *= 2;
     auto fn = nt == 8   ? adapters_low_kernel<8>
               : nt == 4 ? adapters_low_kernel<4>
               : nt == 2 ? adapters_low_kernel<2>
@@ -194,6 +201,7 @@ static int run_forward(const void* X, const void* W, void* Y, const int32_t* off
     p.num_kb = pl.num_kb;
     p.n_tiles = pl.n_tiles;
     p.cap = pl.cap;
+    p.cluster = pl.cluster;
     p.split = pl.split;
     p.num_stages = pl.num_stages;
     p.stage_bytes = pl.stage_bytes;
@@ -279,7 +287,7 @@ static int run_forward(const void* X, const void* W, void* Y, const int32_t* off
             p.scale = ad->scale;
             p.rank = (int32_t)ad->rank;
         } else {
-            rc = run_low(X, *ad, reinterpret_cast<uint16_t*>(base), T, K, ldx, pl, bf16, d, st);
+            rc = run_low(X, *ad, reinterpret_cast<uint16_t*>(base), T, N, K, ldx, pl, bf16, d, st);
             if (rc != GEMM_OK) return rc;
         }
     }
@@ -290,7 +298,7 @@ static int run_forward(const void* X, const void* W, void* Y, const int32_t* off
             return launch(ragged_kernel<true, true>, pl.grid, kThreads, smem, 2, st, m, p);
         }
         if ((rc = allow_smem(d, 1, ragged_kernel<false, true>)) != GEMM_OK) return rc;
-        return launch(ragged_kernel<false, true>, pl.grid, kThreads, smem, 1, st, m, p);
+        return launch(ragged_kernel<false, true>, pl.grid, kThreads, smem, pl.cluster, st, m, p);
     }
     if (pl.pair) {
         if ((rc = allow_smem(d, 2, ragged_kernel<true, false>)) != GEMM_OK) return rc;

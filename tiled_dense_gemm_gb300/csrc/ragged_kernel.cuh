@@ -72,6 +72,7 @@ struct Params {
     int32_t num_kb;      // ceil(K / kBK)
     int32_t n_tiles;     // column tiles (128, or 256 for a pair)
     int32_t cap;         // most rows of a tile
+    int32_t cluster;     // adapters, single CTAs: > 1: an item's k-blocks shared by the CTAs of a cluster
     int32_t split;       // 1: the k-blocks of all items are cut into equal contiguous runs, one per CTA
     int32_t num_stages;
     int32_t stage_bytes; // stride of a ring stage
@@ -306,7 +307,7 @@ struct Iter {
 
     __device__ __forceinline__ Iter(const Params& p_, const int32_t* start_, const int32_t* tiles_,
                                     const int32_t* nslots_, const int32_t* lows_, uint32_t worker, uint32_t workers,
-                                    int32_t max_extra)
+                                    int32_t max_extra, uint32_t share)
         : p(p_), start(start_), tiles(tiles_), nslots(nslots_), lows(lows_) {
         const uint32_t items = (uint32_t)tiles[p.G] * (uint32_t)p.n_tiles;
         n_low = kPair && kAdapters && p.low_out ? (uint32_t)lows[tiles[p.G]] : 0u;
@@ -315,6 +316,11 @@ struct Iter {
             const uint32_t units = items * (uint32_t)kb_all;
             u = begin_of(units, worker, workers);
             u1 = begin_of(units, worker + 1, workers);
+            step = 0;
+        } else if (kAdapters && !kPair && p.cluster > 1) {
+            // one item per cluster, as one share of it per CTA
+            u = worker * (uint32_t)kb_all + share * (uint32_t)kb_all / (uint32_t)p.cluster;
+            u1 = worker < items ? worker * (uint32_t)kb_all + (share + 1) * (uint32_t)kb_all / (uint32_t)p.cluster : u;
             step = 0;
         } else {
             u = worker;
@@ -340,7 +346,7 @@ struct Iter {
     __device__ __forceinline__ bool next(Item& it) {
         if (u >= u1) return false;
         uint32_t item;
-        if (!kPair && p.split) {
+        if (!kPair && step == 0) {
             item = u / (uint32_t)kb_all;
             it.kb0 = (int32_t)(u - item * (uint32_t)kb_all);
             it.kb1 = (int32_t)min((uint32_t)kb_all, (uint32_t)it.kb0 + (u1 - u));
@@ -387,7 +393,7 @@ struct Iter {
         const int32_t j = (int32_t)(band * kRaster + r - (uint32_t)it.n * rows);
         it.tile = first + j;
         row_tile(it, lo, cnt, j);
-        if (kPair || !p.split) {
+        if (kPair || step != 0) {
             it.kb_all = p.num_kb + (kAdapters ? extra_blocks(p, nslots[it.tile]) : 0);
             it.kb1 = it.kb_all;
         }
@@ -447,7 +453,9 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
     int32_t* const tiles = start + p.G + 1;
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = kPair ? cluster_ctarank() : 0u;
-    const uint32_t worker = kPair ? blockIdx.x / 2 : blockIdx.x;
+    const bool clustered = kAdapters && !kPair && p.cluster > 1;
+    const uint32_t share = clustered ? cluster_ctarank() : 0u;
+    const uint32_t worker = kPair ? blockIdx.x / 2 : clustered ? blockIdx.x / (uint32_t)p.cluster : blockIdx.x;
     const uint32_t workers = kPair ? gridDim.x / 2 : gridDim.x;
 
     if (warp == 2 && lane == 0) {
@@ -544,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
     const uint32_t tmem_base = ctrl->tmem_addr;
     const uint32_t S = (uint32_t)p.num_stages, stride = (uint32_t)p.stage_bytes;
     const uint32_t full0 = smem_u32(&ctrl->full[0]), empty0 = smem_u32(&ctrl->empty[0]);
-    It iter(p, start, tiles, nslots, lows, worker, workers, max_extra);
+    It iter(p, start, tiles, nslots, lows, worker, workers, max_extra, share);
     Item it;
 
     // pieces (boxes of rank_box rows of an adapter's second factor) of extra
@@ -881,7 +889,8 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
             if (e0 == e1) return true;
             const uint32_t rows = (uint32_t)it.w / (kPair ? 2u : 1u);
             const int32_t y = it.row0 + (int32_t)(rank * rows);
-            bool ok = true;
+            bool ok = true;     // (alike in all threads)
+            bool armed = true;  // of the thread that arms
             if (kPair && p.low_out) {
                 // low items come first in every CTA's list: this ends
                 if (et == 0) {
@@ -911,14 +920,18 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                     who[j] = r0 + 8u * j < rows && t < it.row0 + it.valid ? __ldcg(p.ids + t) : -2;
                 }
             }
-            for (int32_t e = e0; ok && e <= e1; ++e) {
-                if (e < e1) {
-                    const uint32_t at = pos + (uint32_t)(e - e0), st = at % S;
+            // Blocks in flight: stage e + S - 2 is free while the MMAs work
+            // on block e - 1, in time for e.
+            const int32_t ahead = max(0, min(3, (int32_t)S - 2));
+            int32_t issued = e0;
+            for (int32_t e = e0; ok && e < e1; ++e) {
+                for (; issued < e1 && issued <= e + ahead; ++issued) {
+                    const uint32_t st = (pos + (uint32_t)(issued - e0)) % S;
                     ok = wait_phase(smem_u32(&ctrl->extra[st]), (extra_ph >> st) & 1u, ctrl, p, kErrTokens);
                     extra_ph ^= 1u << st;
                     ok = named_bar_and(kEpiBarrier, kEpiThreads, ok);
                     if (!ok) break;
-                    const int32_t col = e * kXK + 8 * (int32_t)(v & 7u);
+                    const int32_t col = issued * kXK + 8 * (int32_t)(v & 7u);
                     const int32_t slot = slot_of(p, col >> p.box_shift);
                     const int32_t id = slot < slots ? slot_list[(int64_t)it.tile * p.cap + slot] : -3;
                     const uint16_t* src = p.low + (int64_t)y * 2 * p.rank_pad + (col - slot * p.rank_pad) +
@@ -936,43 +949,46 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                         // only the rows that the MMAs of these columns read
                         // (all where they begin an accumulator)
                         uint32_t lo = 0, hi = rows;
-                        if (e > e0 || it.kb0 < p.num_kb) window(slots, col & ~15, lo, hi);
+                        if (issued > e0 || it.kb0 < p.num_kb) window(slots, col & ~15, lo, hi);
                         for (uint32_t i = lo + r0; i < hi; i += 8) put(i, row_ids[i] == id);
                     }
                     copy_async_commit();
                 }
-                if (e > e0) {
-                    if (e < e1)
-                        copy_async_wait<1>();
-                    else
-                        copy_async_wait<0>();
-                    fence_proxy_async_smem();
-                    named_bar_sync(kEpiBarrier, kEpiThreads);
-                    if (et == 0) {
-                        const uint32_t st = (pos + (uint32_t)(e - 1 - e0)) % S;
-                        if (kPair && rank != 0) {
-                            mbar_arrive_cluster(mapa_shared(smem_u32(&ctrl->peer[st]), 0));
-                        } else {
-                            // (extra_ph has moved on: once since this block, which is the last use of its stage)
-                            if (kPair)
-                                ok = wait_cluster(smem_u32(&ctrl->peer[st]), ((extra_ph >> st) & 1u) ^ 1u, ctrl, p);
-                            if (ok)
-                                mbar_arrive_expect_tx(full0 + 8u * st, (uint32_t)(pieces_of(slots, e - 1) * p.rank_box) *
-                                                                           (kPair ? 512u : 256u));
-                        }
+                if (!ok) break;
+                switch (issued - e) {
+                    case 1: copy_async_wait<0>(); break;
+                    case 2: copy_async_wait<1>(); break;
+                    case 3: copy_async_wait<2>(); break;
+                    default: copy_async_wait<3>(); break;
+                }
+                fence_proxy_async_smem();
+                named_bar_sync(kEpiBarrier, kEpiThreads);
+                if (et == 0) {
+                    const uint32_t st = (pos + (uint32_t)(e - e0)) % S;
+                    if (kPair && rank != 0) {
+                        mbar_arrive_cluster(mapa_shared(smem_u32(&ctrl->peer[st]), 0));
+                    } else {
+                        // (extra_ph has moved on once since this block, the last use of its stage)
+                        if (kPair && armed)
+                            armed = wait_cluster(smem_u32(&ctrl->peer[st]), ((extra_ph >> st) & 1u) ^ 1u, ctrl, p);
+                        if (armed)
+                            mbar_arrive_expect_tx(full0 + 8u * st, (uint32_t)(pieces_of(slots, e) * p.rank_box) *
+                                                                       (kPair ? 512u : 256u));
                     }
                 }
             }
             pos += (uint32_t)(e1 - e0);
-            return named_bar_and(kEpiBarrier, kEpiThreads, ok);
+            return named_bar_and(kEpiBarrier, kEpiThreads, ok && armed);
         };
-        while (iter.next(it)) {
-            if (kAdapters && !fill_extras()) break;
+        // the item whose accumulator is the CTA's `local`-th; false: aborting
+        auto drain = [&](const Item& it, uint32_t local) {
             const uint32_t buf = local & 1u, bph = (local >> 1) & 1u;
-            bool ok = wait_phase(smem_u32(&ctrl->tmem_full[buf]), bph, ctrl, p, kErrEpi);
-            ok = named_bar_and(kEpiBarrier, kEpiThreads, ok);
-            if (!ok) break;
-            tc_fence_after();
+            auto ready = [&]() {
+                bool ok = wait_phase(smem_u32(&ctrl->tmem_full[buf]), bph, ctrl, p, kErrEpi);
+                ok = named_bar_and(kEpiBarrier, kEpiThreads, ok);
+                tc_fence_after();
+                return ok;
+            };
             const uint32_t taddr = tmem_base + ((quarter * 32u) << 16) + buf * cols;
             auto release = [&]() {
                 tc_fence_before();
@@ -986,38 +1002,90 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
             };
             if constexpr (kPair && kAdapters) {
                 if (it.low) {
-                    // this lane's product: number j of adapter id's rank
-                    const int32_t held = low_boxes(p, nslots[it.tile]) * p.rank_box;  // of each CTA
-                    const int32_t r = (2 * it.n + (int32_t)rank) * held + (int32_t)lane_row;
-                    const int32_t slot = slot_of(p, r >> p.box_shift), j = r - slot * p.rank_pad;
-                    const int32_t id = (int32_t)lane_row < held && slot < nslots[it.tile] ? slot_list[(int64_t)it.tile * p.cap + slot] : -3;
-                    const float scale = id >= 0 && p.scale ? __ldcg(p.scale + id) : 1.0f;
-                    for (int32_t c = 0; c < it.w; c += 32) {
-                        const int32_t t = it.row0 + c + (int32_t)lane;
-                        const int32_t his = c + (int32_t)lane < it.valid ? __ldcg(p.ids + t) : -2;
-                        __syncwarp();
-                        tmem_load_32cols(taddr + c, v);
-                        uint16_t* dst = p.low_out + (int64_t)(it.row0 + c) * 2 * p.rank_pad + j;
+                    const int32_t slots = nslots[it.tile];
+                    const int32_t held = low_boxes(p, slots) * p.rank_box;  // products of each CTA
+                    const int32_t r0 = (2 * it.n + (int32_t)rank) * held;   // its first
+                    // scale of this thread's fragment rows; columns past the
+                    // rank are zeros whatever the scale is
+                    float scale[4];
+                    bool keep[4];
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2, dst += 4 * p.rank_pad) {
-                            const bool a = __shfl_sync(0xffffffffu, his, i) == id;
-                            const bool b = __shfl_sync(0xffffffffu, his, i + 1) == id;
-                            // (columns past the rank are zeros whatever the scale is)
-                            const float x = j < p.rank ? v[i] * scale : 0.0f, y = j < p.rank ? v[i + 1] * scale : 0.0f;
-                            const uint32_t hi = pack16(x, y, p.bf16), rest = rest16x2(x, y, hi, p.bf16);
-                            if (a) dst[0] = (uint16_t)hi;
-                            if (a) dst[p.rank_pad] = (uint16_t)rest;
-                            if (b) dst[2 * p.rank_pad] = (uint16_t)(hi >> 16);
-                            if (b) dst[3 * p.rank_pad] = (uint16_t)(rest >> 16);
+                    for (int k = 0; k < 4; ++k) {
+                        const int32_t r = r0 + 32 * (int32_t)quarter + 8 * k + (int32_t)(lane >> 2);
+                        const int32_t slot = slot_of(p, r >> p.box_shift);
+                        keep[k] = slot < slots && r - slot * p.rank_pad < p.rank;
+                        scale[k] = keep[k] && p.scale ? __ldcg(p.scale + slot_list[(int64_t)it.tile * p.cap + slot])
+                                                      : 1.0f;
+                    }
+                    // after the transposition: eight products of adapter id, from number j
+                    const int32_t col = 32 * (int32_t)quarter + 8 * (int32_t)(lane & 3u);
+                    const int32_t slot = slot_of(p, (r0 + col) >> p.box_shift), j = r0 + col - slot * p.rank_pad;
+                    const int32_t id = col < held && slot < slots ? slot_list[(int64_t)it.tile * p.cap + slot] : -3;
+                    int32_t who[8];  // adapters of rows lane, lane + 32, ...
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int32_t r = 32 * k + (int32_t)lane;
+                        who[k] = r < it.valid ? __ldcg(p.ids + it.row0 + r) : -2;
+                    }
+                    if (!ready()) return false;
+#pragma unroll
+                    for (int ck = 0; ck < 8; ++ck) {
+                        const int32_t c = 32 * ck;
+                        if (c >= it.w) break;
+                        int32_t his[4];  // adapters of rows c + lane / 4, + 8, ...
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            his[i] = __shfl_sync(0xffffffffu, who[ck], 8 * i + (int)(lane >> 2));
+                        __syncwarp();
+                        tmem_load_fragments(taddr + c, v);
+                        uint32_t hi[16], rest[16];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)  // row of the fragments: 8 k + lane / 4
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int at = 16 * (k >> 1) + 4 * i + 2 * (k & 1);
+                                const float x = keep[k] ? v[at] * scale[k] : 0.0f;
+                                const float y = keep[k] ? v[at + 1] * scale[k] : 0.0f;
+                                hi[4 * i + k] = pack16(x, y, p.bf16);
+                                rest[4 * i + k] = rest16x2(x, y, hi[4 * i + k], p.bf16);
+                            }
+#pragma unroll
+                        for (int part = 0; part < 2; ++part) {
+                            __syncwarp();
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint32_t* q = (part ? rest : hi) + 4 * i;
+                                st_matrix_trans(turn_st + (uint32_t)i * 8u * kTurnPitch, q[0], q[1], q[2], q[3]);
+                            }
+                            __syncwarp();
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (his[i] == id)
+                                    *reinterpret_cast<uint4*>(
+                                        p.low_out + (int64_t)(it.row0 + c + 8 * i + (int32_t)(lane >> 2)) * 2 * p.rank_pad +
+                                        part * p.rank_pad + j) = ld_shared_v4(turn_ld + (uint32_t)i * 8u * kTurnPitch);
                         }
                     }
                     release();
                     __threadfence();
                     named_bar_sync(kEpiBarrier, kEpiThreads);
                     if (et == 0) atomicAdd(p.low_done + it.tile, 1u);
-                    ++local;
-                    continue;
+                    return true;
                 }
+            }
+            if (!ready()) return false;
+            if (clustered) {
+                // this CTA's share, fp32, into its ring (idle by now): rows of
+                // Y x 128 columns; the cluster adds them up below
+                for (int32_t c = 0; c < it.w; c += 32) {
+                    __syncwarp();
+                    tmem_load_32cols(taddr + c, v);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (c + j < it.w) st_shared_f32(ring + (uint32_t)((c + j) * 128 + (int32_t)lane_row) * 4u, v[j]);
+                }
+                release();
+                return true;
             }
             // this thread's 8 columns of Y (of rows lane / 4, + 8, ...)
             const int32_t n = it.n * (kPair ? 256 : 128) + 128 * (int32_t)rank + 32 * (int32_t)quarter + 8 * (int32_t)(lane & 3u);
@@ -1031,15 +1099,15 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                     tmem_load_fragments(taddr + c, v);
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        __stcg(dst + (int64_t)(c / 4 + j) * 128,
-                               make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+                        if ((j & 2) == 0 || it.w - c > 16)  // (a last chunk of 16 columns is every other half)
+                            __stcg(dst + (int64_t)(c / 4 + j) * 128,
+                                   make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
                 }
                 release();
                 __threadfence();
                 named_bar_sync(kEpiBarrier, kEpiThreads);
                 if (threadIdx.x == 64) atomicExch(p.flags + blockIdx.x, 1u);
-                ++local;
-                continue;
+                return true;
             }
             uint32_t others = 0;  // CTAs after this one that hold a share of the item
             if (!kPair && !whole) {
@@ -1048,25 +1116,24 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                 while (blockIdx.x + others + 1 < gridDim.x &&
                        It::begin_of(units, blockIdx.x + others + 1, gridDim.x) < end)
                     ++others;
-                bool ready = true;
+                bool all = true;
                 if (threadIdx.x == 64) {
                     volatile uint32_t* vf = p.flags + blockIdx.x + 1;
                     volatile int32_t* abort_flag = &ctrl->abort_flag;
                     const uint64_t t0 = globaltimer_ns();
-                    for (uint32_t o = 0; o < others && ready; ++o)
+                    for (uint32_t o = 0; o < others && all; ++o)
                         while (vf[o] == 0u)
                             if (*abort_flag || globaltimer_ns() - t0 > p.timeout_ns) {
                                 *abort_flag = 1;
                                 atomicCAS(p.err, 0, (int32_t)kErrEpi);
-                                ready = false;
+                                all = false;
                                 break;
                             }
                     __threadfence();
                 }
-                ready = named_bar_and(kEpiBarrier, kEpiThreads, ready);
-                if (!ready) {
+                if (!named_bar_and(kEpiBarrier, kEpiThreads, all)) {
                     release();
-                    break;
+                    return false;
                 }
             }
             for (int32_t c = 0; c < it.w; c += 32) {
@@ -1083,17 +1150,25 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                 __syncwarp();  // (also: the last chunk's shared-memory reads are done)
                 tmem_load_fragments(taddr + c, v);
                 const float4* src = reinterpret_cast<const float4*>(p.ws + (int64_t)(blockIdx.x + 1) * part) + lane_row;
-                for (uint32_t o = 0; o < others; ++o, src += part / 4) {
-                    float4 x[8];
+                // the others' shares in their order, two on the way at a time
+                for (uint32_t o = 0; o < others; o += 2) {
+                    float4 x[2][8];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] = __ldcg(src + (int64_t)(c / 4 + j) * 128);
+                    for (int q = 0; q < 2; ++q)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        v[4 * j] += x[j].x;
-                        v[4 * j + 1] += x[j].y;
-                        v[4 * j + 2] += x[j].z;
-                        v[4 * j + 3] += x[j].w;
-                    }
+                        for (int j = 0; j < 8; ++j)
+                            x[q][j] = o + q < others && ((j & 2) == 0 || it.w - c > 16)
+                                          ? __ldcg(src + (int64_t)(o + q) * (part / 4) + (int64_t)(c / 4 + j) * 128)
+                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            v[4 * j] += x[q][j].x;
+                            v[4 * j + 1] += x[q][j].y;
+                            v[4 * j + 2] += x[q][j].z;
+                            v[4 * j + 3] += x[q][j].w;
+                        }
                 }
                 if (p.apply_relu) {
 #pragma unroll
@@ -1126,9 +1201,13 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
             release();
             if (!kPair && !whole) {
                 named_bar_sync(kEpiBarrier, kEpiThreads);  // the partials have been read
-                for (uint32_t o = threadIdx.x - 64; o < others; o += kEpiThreads) p.flags[blockIdx.x + 1 + o] = 0u;
+                for (uint32_t o = et; o < others; o += kEpiThreads) p.flags[blockIdx.x + 1 + o] = 0u;
             }
-            ++local;
+            return true;
+        };
+        for (bool ok = true; ok && iter.next(it); ++local) {
+            if (kAdapters) ok = fill_extras();
+            if (ok) ok = drain(it, local);
         }
         // rows of no group: before the first group and past the last one
         const int32_t head = start[0], tail = start[p.G];
@@ -1141,13 +1220,52 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
         }
     }
 
+    if (clustered) {
+        // every CTA of the cluster adds its part of the rows up, the shares
+        // in their order, and writes them: 16 threads per row
+        __syncwarp();
+        cluster_sync();
+        It again(p, start, tiles, nslots, lows, worker, workers, max_extra, 0u);
+        if (again.next(it) && warp >= 2 && warp <= 5) {
+            const uint32_t c = (uint32_t)p.cluster;
+            const int32_t r1 = min(it.valid, (int32_t)((share + 1) * (uint32_t)it.w / c));
+            const uint32_t col = ((threadIdx.x - 64) & 15u) * 8u;
+            const int32_t n = it.n * 128 + (int32_t)col;
+            if (n < p.N) {
+                for (int32_t r = (int32_t)(share * (uint32_t)it.w / c + ((threadIdx.x - 64) >> 4)); r < r1; r += 8) {
+                    float x[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[j] = 0.0f;
+                    for (uint32_t q = 0; q < c; ++q) {
+                        const uint32_t from = mapa_shared(ring + ((uint32_t)r * 128u + col) * 4u, q);
+                        const float4 a = ld_shared_cluster_f4(from), b = ld_shared_cluster_f4(from + 16u);
+                        x[0] += a.x;
+                        x[1] += a.y;
+                        x[2] += a.z;
+                        x[3] += a.w;
+                        x[4] += b.x;
+                        x[5] += b.y;
+                        x[6] += b.z;
+                        x[7] += b.w;
+                    }
+                    if (p.apply_relu) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) x[j] = x[j] > 0.0f ? x[j] : 0.0f;
+                    }
+                    *reinterpret_cast<uint4*>(p.Y + (int64_t)(it.row0 + r) * p.ldy + n) =
+                        make_uint4(pack16(x[0], x[1], p.bf16), pack16(x[2], x[3], p.bf16), pack16(x[4], x[5], p.bf16),
+                                   pack16(x[6], x[7], p.bf16));
+                }
+            }
+        }
+    }
     // (a later kernel's wait covers this one only: it must not end first)
     if (kAdapters && !p.low_out) grid_dependency_wait();
     __syncthreads();
     if (threadIdx.x == 0 && *(volatile int32_t*)&ctrl->abort_flag) drain_ring(ctrl, full0, S);
     tc_fence_before();
-    if (kPair)
-        cluster_sync_relaxed();
+    if (kPair || clustered)
+        cluster_sync_relaxed();  // the other CTAs' accesses to this one's shared memory are done
     else
         __syncthreads();
     if (warp == 1) {

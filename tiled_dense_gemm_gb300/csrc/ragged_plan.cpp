@@ -51,7 +51,7 @@ RaggedPlan plan_rows(int64_t T, int64_t G, int64_t N, int64_t K, int64_t R, int6
     while (alloc < cols) alloc *= 2;
     p.tmem_cols = (int32_t)alloc;
     // at most this many row tiles, whatever the groups' sizes are
-    const int64_t tiles = std::min(T, ceil_div(T, cap) + std::min(G, T));
+    const int64_t tiles = R > 0 ? ceil_div(T, cap) : std::min(T, ceil_div(T, cap) + std::min(G, T));
     const int64_t items = tiles * p.n_tiles;
     int64_t kb = p.num_kb;
     if (R > 0) {
@@ -66,7 +66,16 @@ RaggedPlan plan_rows(int64_t T, int64_t G, int64_t N, int64_t K, int64_t R, int6
         p.status = GEMM_ERR_TOO_LARGE;
         return p;
     }
-    p.split = !p.pair && items * kb <= kIndexMax;
+    // One row tile and few column tiles: clusters share each tile's k-blocks
+    // and add up on chip.  Else the k-blocks of all items are cut evenly.
+    p.cluster = 1;
+    while (R > 0 && !p.pair && p.cluster < 8 && items * p.cluster * 2 <= num_sms && p.cluster * 2 <= p.num_kb)
+        p.cluster *= 2;
+    p.split = !p.pair && p.cluster == 1 && items * kb <= kIndexMax;
+    if (p.cluster > 1) {
+        p.grid = (int32_t)items * p.cluster;
+        return p;
+    }
     p.grid = p.pair ? 2 * (int32_t)std::min<int64_t>(pairs, items)
                     : (int32_t)std::min<int64_t>(num_sms, p.split ? items * kb : items);
     return p;

@@ -106,6 +106,10 @@ __device__ __forceinline__ void st_matrix_trans(uint32_t addr, uint32_t a, uint3
                  : "memory");
 }
 
+__device__ __forceinline__ void st_shared_f32(uint32_t addr, float x) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
+}
+
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
     uint4 q;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
