@@ -138,8 +138,10 @@ __global__ void __launch_bounds__(kLowWarps * 32, 2) adapters_low_kernel(const _
     const int32_t job = (int32_t)blockIdx.x / p.k_split;
     const int32_t j0 = job % p.passes * 8 * kNT;  // first of the rank's products
     const int32_t y = job / p.passes % p.slot_step, row0 = job / p.passes / p.slot_step * 16;
-    // this warp's chunks of 32 k: kw0, kw0 + kw_step, ...
-    const int32_t kw0 = (rank * kLowWarps + warp) * 32, kw_step = p.k_split * kLowWarps * 32;
+    // kU chunks of 32 k per warp in flight at once, side by side: one round
+    // trip to DRAM for each 256 x kU x k_split of K
+    constexpr int kU = kNT == 8 ? 2 : kNT == 4 ? 4 : 6;
+    const int32_t kw0 = (rank * kLowWarps + warp) * (32 * kU), kw_step = p.k_split * kLowWarps * (32 * kU);
     // the block's distinct adapters, in each warp's registers: lane = row
     int32_t mine = -1;
     if (lane < 16 && row0 + lane < p.T) {
@@ -166,14 +168,11 @@ __global__ void __launch_bounds__(kLowWarps * 32, 2) adapters_low_kernel(const _
         const uint16_t* x0 = p.X + (int64_t)(in0 ? row0 + g : row0) * p.ldx;
         const uint16_t* x1 = p.X + (int64_t)(in1 ? row0 + g + 8 : row0) * p.ldx;
         const uint16_t* a = p.A + ((int64_t)id * p.rank + j0 + g) * p.K;
-        // kU chunks of 32 k per warp in flight at once: one round trip to
-        // DRAM for each 256 x kU x k_split of K
-        constexpr int kU = kNT == 8 ? 2 : kNT == 4 ? 4 : 6;
-        for (int32_t kw = kw0; kw < p.K; kw += kw_step * kU) {
+        for (int32_t kw = kw0; kw < p.K; kw += kw_step) {
             uint4 xv[kU][2], av[kU][kNT];
 #pragma unroll
             for (int u = 0; u < kU; ++u) {
-                const int32_t k = kw + u * kw_step + tig * 8;
+                const int32_t k = kw + u * 32 + tig * 8;
                 const bool in = k < p.K;
                 xv[u][0] = load_or_zero(x0 + k, in && in0);
                 xv[u][1] = load_or_zero(x1 + k, in && in1);

@@ -227,8 +227,9 @@ struct Item {
     int32_t valid;      // rows of this tile
     int32_t w;          // rows rounded up to the MMA's granularity
     int32_t n;          // column tile
-    int32_t kb0, kb1;   // k-blocks [kb0, kb1) of `kb_all`
-    int32_t kb_all;
+    int32_t kb0, kb1;   // this CTA's k-blocks [kb0, kb1)
+    int32_t x0, x1;     // ... and extra ones (adapters)
+    bool begins, whole; // they hold the item's first k-block; all of them
     uint32_t index;     // item number
     bool low;           // low-rank products of the row tile (n: which 256 of them), not columns of Y
 };
@@ -303,12 +304,13 @@ struct Iter {
     const int32_t* lows;  // adapters of pairs: low items before each row tile
     uint32_t n_low;       // items [0, n_low) are low ones
     uint32_t u, u1, step;
-    int32_t kb_all;  // split: k-blocks of every item
+    int32_t share;   // this CTA's rank in its cluster
+    int32_t kb_all;  // single CTAs: k-blocks of every item
 
     __device__ __forceinline__ Iter(const Params& p_, const int32_t* start_, const int32_t* tiles_,
                                     const int32_t* nslots_, const int32_t* lows_, uint32_t worker, uint32_t workers,
-                                    int32_t max_extra, uint32_t share)
-        : p(p_), start(start_), tiles(tiles_), nslots(nslots_), lows(lows_) {
+                                    int32_t max_extra, int32_t share_)
+        : p(p_), start(start_), tiles(tiles_), nslots(nslots_), lows(lows_), share(share_) {
         const uint32_t items = (uint32_t)tiles[p.G] * (uint32_t)p.n_tiles;
         n_low = kPair && kAdapters && p.low_out ? (uint32_t)lows[tiles[p.G]] : 0u;
         kb_all = p.num_kb + (kAdapters ? max_extra : 0);
@@ -316,11 +318,6 @@ struct Iter {
             const uint32_t units = items * (uint32_t)kb_all;
             u = begin_of(units, worker, workers);
             u1 = begin_of(units, worker + 1, workers);
-            step = 0;
-        } else if (kAdapters && !kPair && p.cluster > 1) {
-            // one item per cluster, as one share of it per CTA
-            u = worker * (uint32_t)kb_all + share * (uint32_t)kb_all / (uint32_t)p.cluster;
-            u1 = worker < items ? worker * (uint32_t)kb_all + (share + 1) * (uint32_t)kb_all / (uint32_t)p.cluster : u;
             step = 0;
         } else {
             u = worker;
@@ -346,16 +343,34 @@ struct Iter {
     __device__ __forceinline__ bool next(Item& it) {
         if (u >= u1) return false;
         uint32_t item;
+        it.kb0 = it.x0 = it.x1 = 0;
+        it.kb1 = p.num_kb;
+        it.begins = it.whole = true;
         if (!kPair && step == 0) {
             item = u / (uint32_t)kb_all;
-            it.kb0 = (int32_t)(u - item * (uint32_t)kb_all);
-            it.kb1 = (int32_t)min((uint32_t)kb_all, (uint32_t)it.kb0 + (u1 - u));
-            u += (uint32_t)(it.kb1 - it.kb0);
-            it.kb_all = kb_all;
+            const int32_t b0 = (int32_t)(u - item * (uint32_t)kb_all);
+            const int32_t b1 = (int32_t)min((uint32_t)kb_all, (uint32_t)b0 + (u1 - u));
+            u += (uint32_t)(b1 - b0);
+            it.kb0 = min(b0, p.num_kb);
+            it.kb1 = min(b1, p.num_kb);
+            it.x0 = b0 - it.kb0;
+            it.x1 = b1 - it.kb1;
+            it.begins = b0 == 0;
+            it.whole = it.begins && b1 == kb_all;
         } else {
             item = u;
             u += step;
-            it.kb0 = 0;
+            if (kAdapters && !kPair && p.cluster > 1) {
+                // an even share of the main k-blocks (DRAM) and of the extra
+                // ones (latency) for each CTA of the cluster
+                const int32_t extra = kb_all - p.num_kb;
+                it.kb0 = share * p.num_kb / p.cluster;
+                it.kb1 = (share + 1) * p.num_kb / p.cluster;
+                it.x0 = share * extra / p.cluster;
+                it.x1 = (share + 1) * extra / p.cluster;
+            } else if (kAdapters) {
+                it.x1 = -1;  // the row tile's, below
+            }
         }
         it.index = item;
         it.low = false;
@@ -371,7 +386,7 @@ struct Iter {
                 it.tile = lo;
                 it.n = (int32_t)item - lows[lo];
                 row_tile(it, 0, tiles[p.G], lo);
-                it.kb_all = it.kb1 = p.num_kb;
+                it.x1 = 0;
                 return true;
             }
             item -= n_low;
@@ -393,10 +408,7 @@ struct Iter {
         const int32_t j = (int32_t)(band * kRaster + r - (uint32_t)it.n * rows);
         it.tile = first + j;
         row_tile(it, lo, cnt, j);
-        if (kPair || step != 0) {
-            it.kb_all = p.num_kb + (kAdapters ? extra_blocks(p, nslots[it.tile]) : 0);
-            it.kb1 = it.kb_all;
-        }
+        if (kAdapters && it.x1 < 0) it.x1 = extra_blocks(p, nslots[it.tile]);
         return true;
     }
 };
@@ -456,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
     const bool clustered = kAdapters && !kPair && p.cluster > 1;
     const uint32_t share = clustered ? cluster_ctarank() : 0u;
     const uint32_t worker = kPair ? blockIdx.x / 2 : clustered ? blockIdx.x / (uint32_t)p.cluster : blockIdx.x;
-    const uint32_t workers = kPair ? gridDim.x / 2 : gridDim.x;
+    const uint32_t workers = kPair ? gridDim.x / 2 : clustered ? gridDim.x / (uint32_t)p.cluster : gridDim.x;
 
     if (warp == 2 && lane == 0) {
         for (int s = 0; s < p.num_stages; ++s) {
@@ -552,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
     const uint32_t tmem_base = ctrl->tmem_addr;
     const uint32_t S = (uint32_t)p.num_stages, stride = (uint32_t)p.stage_bytes;
     const uint32_t full0 = smem_u32(&ctrl->full[0]), empty0 = smem_u32(&ctrl->empty[0]);
-    It iter(p, start, tiles, nslots, lows, worker, workers, max_extra, share);
+    It iter(p, start, tiles, nslots, lows, worker, workers, max_extra, (int32_t)share);
     Item it;
 
     // pieces (boxes of rank_box rows of an adapter's second factor) of extra
@@ -565,11 +577,6 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
         return n;
     };
 
-    // an item's extra k-blocks [e0, e1), numbered from 0
-    auto extras_of = [&](const Item& i, int32_t slots, int32_t& e0, int32_t& e1) {
-        e0 = max(0, i.kb0 - p.num_kb);
-        e1 = max(e0, i.low ? 0 : min(i.kb1 - p.num_kb, extra_blocks(p, slots)));
-    };
     // boxes of rank_box products of a low item that CTA r of the pair holds
     auto low_pieces = [&](const Item& i, int32_t slots, uint32_t r) {
         const int32_t per = low_boxes(p, slots);
@@ -589,7 +596,6 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
             while (ok && iter.next(it)) {
                 const uint32_t rows = (uint32_t)it.w / (kPair ? 2u : 1u);
                 const int32_t y = it.row0 + (int32_t)(rank * rows);
-                const int32_t kb_end = kAdapters ? min(it.kb1, p.num_kb) : it.kb1;
                 uint32_t bytes = (kPair ? 2u : 1u) * (kWBytes + rows * (uint32_t)(kBK * 2));
                 if constexpr (kPair && kAdapters) {
                     if (it.low)
@@ -597,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                                            p.rank_box) * 256u + 2u * rows * (uint32_t)(kBK * 2);
                 }
                 const CUtensorMap* m = &maps.x[rows / 16 - 1];
-                for (int32_t kb = it.kb0; kb < kb_end; ++kb) {
+                for (int32_t kb = it.kb0; kb < it.kb1; ++kb) {
                     if (!wait_phase(empty0 + 8u * s, ph ^ 1u, ctrl, p, kErrTokens)) {
                         ok = false;
                         break;
@@ -622,9 +628,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                     // the epilogue's warps fill and arm the extra k-blocks;
                     // this thread, which is never more than a lap ahead of
                     // the MMAs, tells them when a stage is free
-                    int32_t e0, e1;
-                    extras_of(it, nslots[it.tile], e0, e1);
-                    for (int32_t e = e0; ok && e < e1; ++e) {
+                    for (int32_t e = it.x0; ok && e < it.x1; ++e) {
                         ok = wait_phase(empty0 + 8u * s, ph ^ 1u, ctrl, p, kErrTokens);
                         if (!ok) break;
                         mbar_arrive(smem_u32(&ctrl->extra[s]));
@@ -650,8 +654,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
         bool ok = true;
         while (ok && iter.next(it)) {
             const int32_t n0 = it.n * (kPair ? 256 : 128) + 128 * (int32_t)rank;
-            const int32_t kb_end = kAdapters ? min(it.kb1, p.num_kb) : it.kb1;
-            const int32_t n_main = max(0, kb_end - it.kb0);
+            const int32_t n_main = it.kb1 - it.kb0;
             if (kPair && kAdapters && it.low) {
                 // first factors of the tile's adapters, 128 rows per CTA; a
                 // lane per box of rank_box rows x 64 k
@@ -664,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                 const uint32_t sub = (per == 1 ? (uint32_t)p.rank_box : 128u) * 128u;  // from one 64 k to the next
                 const int32_t id = has ? slot_list[(int64_t)it.tile * p.cap + slot] : 0;
                 uint32_t ls = s, lph = ph;
-                for (int32_t kb = 0; kb < kb_end; ++kb) {
+                for (int32_t kb = 0; kb < it.kb1; ++kb) {
                     ok = wait_phase(empty0 + 8u * ls, lph ^ 1u, ctrl, p, kErrWeights);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
@@ -684,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                 }
             } else if (lane == 0) {
                 uint32_t ls = s, lph = ph;
-                for (int32_t kb = it.kb0; kb < kb_end; ++kb) {
+                for (int32_t kb = it.kb0; kb < it.kb1; ++kb) {
                     if (!wait_phase(empty0 + 8u * ls, lph ^ 1u, ctrl, p, kErrWeights)) {
                         ok = false;
                         break;
@@ -717,10 +720,8 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
             s = adv % S;
             if constexpr (kAdapters) {
                 const int32_t slots = nslots[it.tile];
-                int32_t e0, e1;
-                extras_of(it, slots, e0, e1);
                 const int32_t per = kXK >> p.box_shift;
-                for (int32_t e = e0; ok && e < e1; ++e) {
+                for (int32_t e = it.x0; ok && e < it.x1; ++e) {
                     ok = wait_phase(empty0 + 8u * s, ph ^ 1u, ctrl, p, kErrWeights);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
@@ -778,11 +779,10 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                 const uint32_t d = tmem_base + buf * cols;
                 const uint32_t nbits = ((uint32_t)it.w >> 3) << 17;
                 const uint32_t half16 = ((uint32_t)it.w / (kPair ? 2u : 1u)) * 128u >> 4;  // second 64 k of the rows
-                const int32_t kb_end = kAdapters ? min(it.kb1, p.num_kb) : it.kb1;
                 uint32_t acc = 0;
-                // the k-blocks of [it.kb0, kb_end); weights from `a_first`, k-step k at offset(k)
+                // the k-blocks; weights from `a_first`, k-step k at offset(k)
                 auto main_blocks = [&](uint64_t a_first, uint32_t idesc, auto offset) {
-                    for (int32_t kb = it.kb0; kb < kb_end; ++kb) {
+                    for (int32_t kb = it.kb0; kb < it.kb1; ++kb) {
                         if (!wait_phase(full0 + 8u * s, ph, ctrl, p, kErrStage)) {
                             ok = false;
                             break;
@@ -811,14 +811,12 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                     main_blocks(a_desc0, idesc0 | nbits, [&](uint32_t k) { return a_off[k]; });
                 if constexpr (kAdapters) {
                     const int32_t slots = nslots[it.tile];
-                    int32_t e0, e1;
-                    extras_of(it, slots, e0, e1);
                     const uint32_t box = (uint32_t)p.rank_box;
                     // second factors: boxes of `box` k-rows x two 64-column
                     // chunks; boxes of 8 rows pair up to an MMA's 16
                     const uint64_t x_desc0 = box == 8 ? make_sw128_desc(ring, 1024, 2048)
                                                       : make_sw128_desc(ring, box * 128u, 1024);
-                    for (int32_t e = e0; ok && e < e1; ++e) {
+                    for (int32_t e = it.x0; ok && e < it.x1; ++e) {
                         if (!wait_phase(full0 + 8u * s, ph, ctrl, p, kErrStage)) {
                             ok = false;
                             break;
@@ -829,11 +827,13 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                         const uint64_t b_desc = b_desc0 + (uint64_t)(s * stride16);
                         const uint32_t nk = (uint32_t)pieces_of(slots, e) << p.box_shift >> 4;
                         // hi's columns, then lo's, with the same rows of the factors
-                        for (uint32_t k = 0; k < nk; ++k) {
+#pragma unroll
+                        for (uint32_t k = 0; k < kXK / 16; ++k) {
+                            if (k >= nk) break;
                             const uint32_t r = 16u * k;
                             const uint32_t off = box == 8 ? k * 4096u : (r & ~(box - 1u)) * 256u + (r & (box - 1u)) * 128u;
                             uint32_t lo = 0, hi = (uint32_t)it.w;
-                            if (!kPair && (e > e0 || it.kb0 < p.num_kb))
+                            if (!kPair && (e > it.x0 || it.kb0 < it.kb1))
                                 window(slots, e * kXK + (int32_t)r, lo, hi);
                             const uint32_t idesc_x = idesc1 | (((hi - lo) >> 3) << 17);
                             const uint64_t bd = b_desc + (lo * 128u >> 4) + k * 2u;
@@ -883,10 +883,9 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
         // issued.
         auto fill_extras = [&]() {
             const int32_t slots = nslots[it.tile];
-            int32_t e0, e1;
-            extras_of(it, slots, e0, e1);
-            pos += (uint32_t)max(0, min(it.kb1, p.num_kb) - it.kb0);
-            if (e0 == e1) return true;
+            const int32_t e0 = it.x0, e1 = it.x1;
+            pos += (uint32_t)(it.kb1 - it.kb0);
+            if (e0 >= e1) return true;
             const uint32_t rows = (uint32_t)it.w / (kPair ? 2u : 1u);
             const int32_t y = it.row0 + (int32_t)(rank * rows);
             bool ok = true;     // (alike in all threads)
@@ -949,7 +948,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                         // only the rows that the MMAs of these columns read
                         // (all where they begin an accumulator)
                         uint32_t lo = 0, hi = rows;
-                        if (issued > e0 || it.kb0 < p.num_kb) window(slots, col & ~15, lo, hi);
+                        if (issued > e0 || it.kb0 < it.kb1) window(slots, col & ~15, lo, hi);
                         for (uint32_t i = lo + r0; i < hi; i += 8) put(i, row_ids[i] == id);
                     }
                     copy_async_commit();
@@ -1090,8 +1089,8 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
             // this thread's 8 columns of Y (of rows lane / 4, + 8, ...)
             const int32_t n = it.n * (kPair ? 256 : 128) + 128 * (int32_t)rank + 32 * (int32_t)quarter + 8 * (int32_t)(lane & 3u);
             const bool in_n = n < p.N;
-            const bool whole = it.kb0 == 0 && it.kb1 == it.kb_all;
-            if (!kPair && !whole && it.kb0 != 0) {
+            const bool whole = it.whole;
+            if (!kPair && !whole && !it.begins) {
                 // a share of an item that an earlier CTA began: publish it
                 float4* dst = reinterpret_cast<float4*>(p.ws + (int64_t)blockIdx.x * part) + lane_row;
                 for (int32_t c = 0; c < it.w; c += 32) {
@@ -1111,8 +1110,8 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
             }
             uint32_t others = 0;  // CTAs after this one that hold a share of the item
             if (!kPair && !whole) {
-                const uint32_t units = (uint32_t)tiles[p.G] * (uint32_t)p.n_tiles * (uint32_t)it.kb_all;
-                const uint32_t end = (it.index + 1) * (uint32_t)it.kb_all;
+                const uint32_t units = (uint32_t)tiles[p.G] * (uint32_t)p.n_tiles * (uint32_t)iter.kb_all;
+                const uint32_t end = (it.index + 1) * (uint32_t)iter.kb_all;
                 while (blockIdx.x + others + 1 < gridDim.x &&
                        It::begin_of(units, blockIdx.x + others + 1, gridDim.x) < end)
                     ++others;
@@ -1205,6 +1204,28 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
             }
             return true;
         };
+        if (kAdapters && !kPair && lane == 0) {
+            // few rows: a stage of an extra k-block holds half the weights of
+            // a main one, too little in flight for DRAM's latency; these
+            // warps, idle so far, ask L2 for them ahead (first items only)
+            It ahead(iter);
+            Item a;
+            for (int i = 0; i < 2 && ahead.next(a); ++i) {
+                const int32_t slots = nslots[a.tile];
+                const int32_t per = kXK >> p.box_shift;
+                const int32_t end = min(a.x1 * per, slots * p.per_slot);
+                for (int32_t piece = a.x0 * per + (int32_t)quarter; piece < end; piece += 4) {
+                    const int32_t slot = slot_of(p, piece), row = (piece - slot * p.per_slot) * p.rank_box;
+                    if (p.b4d) {
+                        prefetch_4d(&maps.b, 0, row, a.n * 2, slot_list[slot]);
+                    } else {
+                        prefetch_3d(&maps.b, a.n * 128, row, slot_list[slot]);
+                        prefetch_3d(&maps.b, a.n * 128 + 64, row, slot_list[slot]);
+                    }
+                }
+            }
+        }
+        __syncwarp();
         for (bool ok = true; ok && iter.next(it); ++local) {
             if (kAdapters) ok = fill_extras();
             if (ok) ok = drain(it, local);
@@ -1225,7 +1246,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
         // in their order, and writes them: 16 threads per row
         __syncwarp();
         cluster_sync();
-        It again(p, start, tiles, nslots, lows, worker, workers, max_extra, 0u);
+        It again(p, start, tiles, nslots, lows, worker, workers, max_extra, 0);
         if (again.next(it) && warp >= 2 && warp <= 5) {
             const uint32_t c = (uint32_t)p.cluster;
             const int32_t r1 = min(it.valid, (int32_t)((share + 1) * (uint32_t)it.w / c));
