@@ -17,5 +17,7 @@ def __getattr__(name):
     if name in ("binding", "build", "workloads"):
         return importlib.import_module(f".{name}", __name__)
     if name in _FUNCTIONS:
-        return getattr(importlib.import_module(".binding", __name__), name)
+        value = getattr(importlib.import_module(".binding", __name__), name)
+        globals()[name] = value  # looked up once
+        return value
     raise AttributeError(name)

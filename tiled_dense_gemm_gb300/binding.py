@@ -303,70 +303,126 @@ def noalloc_check_device_error(stream=None, device=None):
         raise GemmReluError(rc, "device (noalloc)")
 
 
-_DTYPES = None  # {torch type: gemm_dtype_t}, filled on first use (torch is imported lazily)
+# ---- Ragged products.  A small call's GPU time is a few microseconds, so the
+# checks below read each tensor property once and compare plain integers.
+
+_torch = None
+_CODES = {}  # {torch type: gemm_dtype_t}
+
+
+def _load_torch():
+    """torch, imported on first use."""
+    global _torch
+    if _torch is None:
+        import torch
+        _CODES.update({torch.float16: 0, torch.bfloat16: 1})
+        _torch = torch
+    return _torch
 
 
 def _dtype_code(*tensors):
     """gemm_dtype_t of tensors that all have one of the library's types."""
-    global _DTYPES
-    import torch
-    if _DTYPES is None:
-        _DTYPES = {torch.float16: 0, torch.bfloat16: 1}
-    for t in tensors:
-        if not isinstance(t, torch.Tensor):
-            raise TypeError("expected torch tensors")
-    dtype = tensors[0].dtype
-    if dtype not in _DTYPES or any(t.dtype != dtype for t in tensors):
+    _load_torch()
+    try:
+        dtype = tensors[0].dtype
+        code = _CODES.get(dtype)
+        for t in tensors:
+            if t.dtype is not dtype:
+                code = None
+    except AttributeError:
+        raise TypeError("expected torch tensors") from None
+    if code is None:
         raise TypeError("the matrices must all be float16 or all bfloat16")
-    return _DTYPES[dtype]
+    return code
+
+
+def _layout_code(b_layout):
+    try:
+        return B_LAYOUTS[b_layout]
+    except (KeyError, TypeError):
+        raise ValueError(f"b_layout must be 'kn' or 'nk', not {b_layout!r}") from None
+
+
+def _device_of(t):
+    """Index of the tensor's CUDA device."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError("the operands must be CUDA tensors")
+    return index
 
 
 def _rows(name, t, rows, width, device):
     """Row pitch of a (rows, width) matrix whose rows are contiguous."""
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != width:
+    if t.shape != (rows, width):
         raise ValueError(f"{name} must be ({rows}, {width}), not {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on CUDA device {device}")
     if t.is_contiguous():
         return width
-    if t.stride(1) != 1 or t.stride(0) < width:
+    row, col = t.stride()
+    if col != 1 or row < width:
         raise ValueError(f"{name} must have contiguous rows that do not overlap (call .contiguous())")
-    return t.stride(0)
+    return row
 
 
 def _stack(name, t, shape, device):
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must be {shape}, not {tuple(t.shape)}")
-    if t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous and on {device}")
+    if t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and on CUDA device {device}")
 
 
 def _index(name, t, count, device):
-    import torch
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
-        raise TypeError(f"{name} must be an int32 tensor")
+    try:
+        if t.dtype is not _torch.int32:
+            raise TypeError(f"{name} must be an int32 tensor")
+    except AttributeError:
+        raise TypeError(f"{name} must be an int32 tensor") from None
     if t.dim() != 1 or (count is not None and t.shape[0] != count):
         raise ValueError(f"{name} must hold {count} values" if count is not None else f"{name} must be 1-D")
-    if t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous and on {device}")
+    if t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and on CUDA device {device}")
 
 
-def _grouped_sizes(first, w, offsets, b_layout, forward):
+def _output(name, t, like, rows, width, device):
+    """(matrix, row pitch) of an output: the caller's, or a new one."""
+    if t is None:
+        return _torch.empty((rows, width), dtype=like.dtype, device=like.device), width
+    if getattr(t, "dtype", None) is not like.dtype:
+        raise TypeError(f"{name} must be a tensor of the operands' type")
+    return t, _rows(name, t, rows, width, device)
+
+
+def _enqueue(fn, device, stream, *args):
+    """fn(*args, stream) on that CUDA device; raises what it reports."""
+    if stream is None:
+        stream = _torch._C._cuda_getCurrentRawStream(device)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    if device == _torch._C._cuda_getDevice():
+        rc = fn(*args, stream)
+    else:
+        with _torch.cuda.device(device):
+            rc = fn(*args, stream)
+    if rc != GEMM_OK:
+        raise GemmReluError(rc, fn.__name__)
+
+
+def _grouped_sizes(rows, w, offsets, layout, forward):
     """(T, G, N, K, device) of a grouped product from its row matrix and weights."""
-    if b_layout not in B_LAYOUTS:
-        raise ValueError(f"b_layout must be 'kn' or 'nk', not {b_layout!r}")
-    if first.dim() != 2 or w.dim() != 3:
+    if rows.dim() != 2 or w.dim() != 3:
         raise ValueError("the rows must be 2-D and the weights 3-D")
-    if not first.is_cuda:
-        raise ValueError("the operands must be CUDA tensors")
-    G = w.shape[0]
-    K, N = (w.shape[1], w.shape[2]) if b_layout == "kn" else (w.shape[2], w.shape[1])
-    if first.shape[1] != (K if forward else N):
-        raise ValueError(f"bad shapes {tuple(first.shape)} and {tuple(w.shape)} ({b_layout})")
-    device = first.device
-    _stack("w", w, tuple(w.shape), device)
+    device = _device_of(rows)
+    G, K, N = w.shape
+    if layout:
+        K, N = N, K
+    T, width = rows.shape
+    if width != (K if forward else N):
+        raise ValueError(f"bad shapes {tuple(rows.shape)} and {tuple(w.shape)}")
+    if w.get_device() != device or not w.is_contiguous():
+        raise ValueError(f"w must be contiguous and on CUDA device {device}")
     _index("offsets", offsets, G + 1, device)
-    return first.shape[0], G, N, K, device
+    return T, G, N, K, device
 
 
 def gemm_relu_grouped(x, w, offsets, y=None, apply_relu: bool = True, b_layout: str = "kn", stream=None):
@@ -376,20 +432,12 @@ def gemm_relu_grouped(x, w, offsets, y=None, apply_relu: bool = True, b_layout: 
     a multiple of 8), ``w`` is (G, K, N), or (G, N, K) for ``b_layout="nk"``;
     float16 or bfloat16 CUDA tensors.  ``offsets`` is a CUDA int32 tensor of
     G + 1 values that the host does not read.  Rows of no group get zeros."""
-    import torch
-    dtype = _dtype_code(x, w)
-    T, G, N, K, device = _grouped_sizes(x, w, offsets, b_layout, True)
+    dtype, layout = _dtype_code(x, w), _layout_code(b_layout)
+    T, G, N, K, device = _grouped_sizes(x, w, offsets, layout, True)
     ldx = _rows("x", x, T, K, device)
-    if y is None:
-        y = torch.empty((T, N), dtype=x.dtype, device=device)
-    elif y.dtype != x.dtype:
-        raise TypeError("y must have x's type")
-    ldy = _rows("y", y, T, N, device)
-    rc = _on_device(device, lib().gemm_relu_grouped, x.data_ptr(), w.data_ptr(), y.data_ptr(), offsets.data_ptr(), T,
-                    G, N, K, ldx, ldy, int(bool(apply_relu)), B_LAYOUTS[b_layout], dtype,
-                    _stream_handle(stream, device))
-    if rc != GEMM_OK:
-        raise GemmReluError(rc, "gemm_relu_grouped")
+    y, ldy = _output("y", y, x, T, N, device)
+    _enqueue(lib().gemm_relu_grouped, device, stream, x.data_ptr(), w.data_ptr(), y.data_ptr(), offsets.data_ptr(),
+             T, G, N, K, ldx, ldy, 1 if apply_relu else 0, layout, dtype)
     return y
 
 
@@ -399,53 +447,38 @@ def gemm_relu_grouped_dx(dy, w, offsets, act=None, dx=None, b_layout: str = "kn"
     ``act`` (T, K) is the activation that went into the product (its x): where
     that came out of a ReLU, dx is the gradient before that ReLU.  Shapes,
     types and ``offsets`` as ``gemm_relu_grouped``."""
-    import torch
-    dtype = _dtype_code(dy, w) if act is None else _dtype_code(dy, w, act)
-    T, G, N, K, device = _grouped_sizes(dy, w, offsets, b_layout, False)
+    dtype, layout = _dtype_code(dy, w) if act is None else _dtype_code(dy, w, act), _layout_code(b_layout)
+    T, G, N, K, device = _grouped_sizes(dy, w, offsets, layout, False)
     ld_dy = _rows("dy", dy, T, N, device)
-    if dx is None:
-        dx = torch.empty((T, K), dtype=dy.dtype, device=device)
-    elif dx.dtype != dy.dtype:
-        raise TypeError("dx must have dy's type")
-    ld_dx = _rows("dx", dx, T, K, device)
+    dx, ld_dx = _output("dx", dx, dy, T, K, device)
     ld_act = 0 if act is None else _rows("act", act, T, K, device)
-    rc = _on_device(device, lib().gemm_relu_grouped_dx, dy.data_ptr(), w.data_ptr(), dx.data_ptr(),
-                    offsets.data_ptr(), None if act is None else act.data_ptr(), T, G, N, K, ld_dy, ld_dx, ld_act,
-                    B_LAYOUTS[b_layout], dtype, _stream_handle(stream, device))
-    if rc != GEMM_OK:
-        raise GemmReluError(rc, "gemm_relu_grouped_dx")
+    _enqueue(lib().gemm_relu_grouped_dx, device, stream, dy.data_ptr(), w.data_ptr(), dx.data_ptr(),
+             offsets.data_ptr(), None if act is None else act.data_ptr(), T, G, N, K, ld_dy, ld_dx, ld_act, layout,
+             dtype)
     return dx
 
 
 def gemm_relu_grouped_dw(x, dy, offsets, dw=None, b_layout: str = "kn", stream=None):
     """dw[g] = x[rows of g].T @ dy[rows of g], (G, K, N), or its transpose
     (G, N, K) for ``b_layout="nk"``; zero for an empty group."""
-    import torch
-    dtype = _dtype_code(x, dy)
-    if b_layout not in B_LAYOUTS:
-        raise ValueError(f"b_layout must be 'kn' or 'nk', not {b_layout!r}")
+    dtype, layout = _dtype_code(x, dy), _layout_code(b_layout)
     if x.dim() != 2 or dy.dim() != 2 or x.shape[0] != dy.shape[0]:
         raise ValueError(f"bad shapes {tuple(x.shape)} and {tuple(dy.shape)}")
-    if not x.is_cuda:
-        raise ValueError("the operands must be CUDA tensors")
-    device = x.device
+    device = _device_of(x)
     _index("offsets", offsets, None, device)
     (T, K), N, G = x.shape, dy.shape[1], offsets.shape[0] - 1
     if G < 0:
         raise ValueError("offsets must hold at least one value")
     ldx, ld_dy = _rows("x", x, T, K, device), _rows("dy", dy, T, N, device)
-    shape = (G, K, N) if b_layout == "kn" else (G, N, K)
+    shape = (G, N, K) if layout else (G, K, N)
     if dw is None:
-        dw = torch.empty(shape, dtype=x.dtype, device=device)
-    elif dw.dtype != x.dtype:
-        raise TypeError("dw must have x's type")
+        dw = _torch.empty(shape, dtype=x.dtype, device=x.device)
+    elif getattr(dw, "dtype", None) is not x.dtype:
+        raise TypeError("dw must be a tensor of the operands' type")
     else:
         _stack("dw", dw, shape, device)
-    rc = _on_device(device, lib().gemm_relu_grouped_dw, x.data_ptr(), dy.data_ptr(), dw.data_ptr(),
-                    offsets.data_ptr(), T, G, N, K, ldx, ld_dy, B_LAYOUTS[b_layout], dtype,
-                    _stream_handle(stream, device))
-    if rc != GEMM_OK:
-        raise GemmReluError(rc, "gemm_relu_grouped_dw")
+    _enqueue(lib().gemm_relu_grouped_dw, device, stream, x.data_ptr(), dy.data_ptr(), dw.data_ptr(),
+             offsets.data_ptr(), T, G, N, K, ldx, ld_dy, layout, dtype)
     return dw
 
 
@@ -457,39 +490,30 @@ def gemm_relu_adapters(x, w, a, b, ids, scale=None, y=None, apply_relu: bool = T
     (R, rank, K), ``b`` (R, rank, N): float16 or bfloat16 CUDA tensors;
     ``ids`` CUDA int32 (T,), -1 for a row without adapter; ``scale`` CUDA
     float32 (R,) or None for 1."""
-    import torch
-    dtype = _dtype_code(x, w, a, b)
-    if b_layout not in B_LAYOUTS:
-        raise ValueError(f"b_layout must be 'kn' or 'nk', not {b_layout!r}")
+    dtype, layout = _dtype_code(x, w, a, b), _layout_code(b_layout)
     if x.dim() != 2 or w.dim() != 2 or a.dim() != 3 or b.dim() != 3:
         raise ValueError("x and w must be 2-D, a and b 3-D")
-    if not x.is_cuda:
-        raise ValueError("the operands must be CUDA tensors")
-    device = x.device
+    device = _device_of(x)
     T, K = x.shape
-    N, Kw = (w.shape[1], w.shape[0]) if b_layout == "kn" else (w.shape[0], w.shape[1])
+    Kw, N = w.shape
+    if layout:
+        Kw, N = N, Kw
     if Kw != K:
         raise ValueError(f"bad shapes {tuple(x.shape)} and {tuple(w.shape)} ({b_layout})")
     R, rank = a.shape[0], a.shape[1]
-    _stack("w", w, tuple(w.shape), device)
+    _stack("w", w, w.shape, device)
     _stack("a", a, (R, rank, K), device)
     _stack("b", b, (R, rank, N), device)
     _index("ids", ids, T, device)
     if scale is not None:
-        if not isinstance(scale, torch.Tensor) or scale.dtype != torch.float32:
+        if getattr(scale, "dtype", None) is not _torch.float32:
             raise TypeError("scale must be a float32 tensor")
         _stack("scale", scale, (R,), device)
     ldx = _rows("x", x, T, K, device)
-    if y is None:
-        y = torch.empty((T, N), dtype=x.dtype, device=device)
-    elif y.dtype != x.dtype:
-        raise TypeError("y must have x's type")
-    ldy = _rows("y", y, T, N, device)
-    rc = _on_device(device, lib().gemm_relu_adapters, x.data_ptr(), w.data_ptr(), a.data_ptr(), b.data_ptr(),
-                    ids.data_ptr(), None if scale is None else scale.data_ptr(), y.data_ptr(), T, N, K, R, rank, ldx,
-                    ldy, int(bool(apply_relu)), B_LAYOUTS[b_layout], dtype, _stream_handle(stream, device))
-    if rc != GEMM_OK:
-        raise GemmReluError(rc, "gemm_relu_adapters")
+    y, ldy = _output("y", y, x, T, N, device)
+    _enqueue(lib().gemm_relu_adapters, device, stream, x.data_ptr(), w.data_ptr(), a.data_ptr(), b.data_ptr(),
+             ids.data_ptr(), None if scale is None else scale.data_ptr(), y.data_ptr(), T, N, K, R, rank, ldx, ldy,
+             1 if apply_relu else 0, layout, dtype)
     return y
 
 

@@ -5,7 +5,6 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
-#include <stdlib.h>
 #include <string.h>
 
 #include <algorithm>
@@ -168,11 +167,9 @@ static int run_low(const void* X, const Adapters& ad, uint16_t* low, int64_t T, 
     // 8192: low took 32 us beside it, 13 us before it).  Then that kernel starts
     // when low's loads are in.
     q.early = std::min(T, ad.R) * ad.rank * 64 <= N ? 1 : 0;
-    if (getenv("XE")) q.early = atoi(getenv("XE"));  // TMP
     // few jobs share each reduction between the CTAs of a cluster (one CTA
     // per multiprocessor leaves room there for one of the main kernel)
-    int64_t room = q.early ? d.sm_count : 2 * (int64_t)d.sm_count;
-    if (getenv("XR")) room = atoi(getenv("XR"));  // TMP
+    const int64_t room = q.early ? d.sm_count : 2 * (int64_t)d.sm_count;
     q.k_split = 1;
     while (q.k_split < 8 && jobs * q.k_split * 2 <= room && K > 256 * q.k_split) q.k_split *= 2;
     auto fn = nt == 8   ? adapters_low_kernel<8>
