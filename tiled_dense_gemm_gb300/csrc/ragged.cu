@@ -347,10 +347,10 @@ static int run_dw(const void* U, const void* V, void* D, const int32_t* offsets,
     q.timeout_ns = 2000000000ull + 2000ull * (uint64_t)((T + kBK - 1) / kBK);
     if (pl.pair) {
         if ((rc = allow_smem(d, 4, ragged_dw_kernel<true>)) != GEMM_OK) return rc;
-        return launch(ragged_dw_kernel<true>, pl.grid, kThreads, (size_t)pl.smem_bytes, 2, st, out, q);
+        return launch(ragged_dw_kernel<true>, pl.grid, kDwThreads, (size_t)pl.smem_bytes, 2, st, out, q);
     }
     if ((rc = allow_smem(d, 5, ragged_dw_kernel<false>)) != GEMM_OK) return rc;
-    return launch(ragged_dw_kernel<false>, pl.grid, kThreads, (size_t)pl.smem_bytes, 1, st, out, q);
+    return launch(ragged_dw_kernel<false>, pl.grid, kDwThreads, (size_t)pl.smem_bytes, 1, st, out, q);
 }
 
 // ------------------------------------------------------------------ checks

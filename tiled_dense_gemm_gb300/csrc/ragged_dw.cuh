@@ -16,7 +16,10 @@
 // grid are short ones.
 //
 // Tile 128 x 128 per CTA, or 256 x 256 per CTA pair; stages of 128 rows; roles
-// and waits as in the ragged forward kernel.
+// and waits as in the ragged forward kernel, but eight epilogue warps (2-5 and
+// 7-10, each half of a quarter's columns): a group's reduction is often only a
+// few stages long, and with four warps writing a tile took longer than
+// computing it (512 rows per group on average: TODO).
 #pragma once
 
 #include "ragged_kernel.cuh"
@@ -93,8 +96,10 @@ __global__ void __launch_bounds__(32) dw_prep_kernel(const __grid_constant__ DwP
     map_publish(maps + 2 * before + 1, smem_u32(&edit[1]));
 }
 
+constexpr int kDwThreads = 352;
+
 template <bool kPair>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kDwThreads, 1)
     ragged_dw_kernel(const __grid_constant__ DwMaps out, const __grid_constant__ DwParams q) {
     constexpr int kCG = kPair ? 2 : 1;
     constexpr uint32_t kTile = kPair ? 256 : 128;  // rows and columns of D per tile
@@ -119,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&ctrl->tmem_full[b]), 1);
-            mbar_init(smem_u32(&ctrl->tmem_empty[b]), (kPair ? 2u : 1u) * (kEpiThreads / 32));
+            mbar_init(smem_u32(&ctrl->tmem_empty[b]), (kPair ? 2u : 1u) * 8u);
         }
         mbar_init(smem_u32(&ctrl->final_bar), 1);
         ctrl->abort_flag = 0;
@@ -145,22 +150,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t per_group = (uint32_t)(q.p_tiles * q.q_tiles);
     const uint32_t items = (uint32_t)q.G * per_group;
 
-    // item -> position in the length order, tile; groups without a row have no k-block
+    // item -> position in the length order, tile; groups without a row have
+    // no k-block.  The next item's group is on its way while this one runs.
     struct Work {
         int32_t pos, g, lo, hi, pt, qt;
     };
-    auto fetch = [&](uint32_t item) {
-        Work k;
+    uint32_t item = worker;
+    int4 ahead = make_int4(0, 0, 0, 0);
+    auto look = [&]() {
+        if (item < items) ahead = __ldcg(reinterpret_cast<const int4*>(q.groups + item / per_group));
+    };
+    look();
+    auto next = [&](Work& k) {
+        if (item >= items) return false;
         k.pos = (int32_t)(item / per_group);
         const uint32_t l = item - (uint32_t)k.pos * per_group;
         k.qt = (int32_t)(l / (uint32_t)q.p_tiles);
         k.pt = (int32_t)(l - (uint32_t)k.qt * (uint32_t)q.p_tiles);
-        const int4 d = __ldcg(reinterpret_cast<const int4*>(q.groups + k.pos));
-        k.g = d.x;
-        k.lo = d.y;
-        k.hi = d.z;
-        return k;
+        k.g = ahead.x;
+        k.lo = ahead.y;
+        k.hi = ahead.z;
+        item += workers;
+        look();
+        return true;
     };
+    Work k;
 
     if (warp == 0 || warp == 6) {
         // warp 0 copies U's tiles and arms the stages, warp 6 V's
@@ -169,8 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t s = 0, ph = 0;
             int32_t issued = 0, seen = -1;
             bool ok = true;
-            for (uint32_t item = worker; ok && item < items; item += workers) {
-                const Work k = fetch(item);
+            while (ok && next(k)) {
                 if (k.hi == k.lo) continue;
                 const CUtensorMap* m = q.maps + 2 * k.pos + (is_u ? 0 : 1);
                 if (k.pos != seen) map_acquire(m);
@@ -215,8 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t b_desc0 = make_sw128_desc(ring + kOperand, (uint32_t)kBK * 128u, 1024);
             uint32_t s = 0, ph = 0, local = 0;
             bool ok = true;
-            for (uint32_t item = worker; ok && item < items; item += workers) {
-                const Work k = fetch(item);
+            while (ok && next(k)) {
                 if (k.hi == k.lo) continue;
                 const uint32_t buf = local & 1u, bph = (local >> 1) & 1u;
                 if (!wait_phase(tempty0 + 8u * buf, bph ^ 1u, ctrl, w, kErrAccum)) break;
@@ -261,53 +273,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else {
-        const uint32_t quarter = warp & 3u;
-        const uint32_t staging = ring + S * stride + quarter * 8192u;  // two 4 KiB buffers per warp
-        uint32_t sbuf = 0, local = 0;
-        for (uint32_t item = worker; item < items; item += workers) {
-            const Work k = fetch(item);
+        const uint32_t quarter = warp & 3u, half = warp >= 7 ? 1u : 0u;
+        const uint32_t staging = ring + S * stride + (quarter + 4u * half) * 4096u;
+        uint32_t local = 0;
+        while (next(k)) {
             const bool some = k.hi > k.lo;
             const uint32_t buf = local & 1u, bph = (local >> 1) & 1u;
             if (some) {
-                bool ok = wait_phase(smem_u32(&ctrl->tmem_full[buf]), bph, ctrl, w, kErrEpi);
-                ok = named_bar_and(kEpiBarrier, kEpiThreads, ok);
-                if (!ok) break;
+                if (!__all_sync(0xffffffffu, wait_phase(smem_u32(&ctrl->tmem_full[buf]), bph, ctrl, w, kErrEpi))) break;
                 tc_fence_after();
             }
             const uint32_t taddr = tmem_base + ((quarter * 32u) << 16) + buf * kCols;
             const int32_t row0 = k.pt * (int32_t)kTile + 128 * (int32_t)rank + 32 * (int32_t)quarter;
-            for (uint32_t c = 0; c < kCols; c += 64) {
+            for (uint32_t c = half * (kCols / 2); c < (half + 1u) * (kCols / 2); c += 64) {
                 const int32_t col = k.qt * (int32_t)kTile + (int32_t)c;
-                if (col >= q.Q) break;  // (uniform over the warp)
-                float v[64];
+                if (col >= q.Q || row0 >= q.P) break;  // (uniform over the warp)
+                uint32_t x[32];
                 if (some) {
+                    float v[64];
                     __syncwarp();
                     tmem_load_64cols(taddr + c, v);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) x[j] = pack16(v[2 * j], v[2 * j + 1], q.bf16);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) v[j] = 0.0f;
+                    for (int j = 0; j < 32; ++j) x[j] = 0u;
                 }
-                if (row0 >= q.P) continue;
-                // the copy issued from this buffer two chunks ago must have read it
-                if (lane == 0) bulk_wait_group_read<1>();
+                // the copy issued from this buffer before must have read it
+                if (lane == 0) bulk_wait_group_read<0>();
                 __syncwarp();
-                const uint32_t buf_addr = staging + sbuf * 4096u;
 #pragma unroll
-                for (uint32_t u = 0; u < 8; ++u) {
-                    uint4 x;
-                    x.x = pack16(v[8 * u + 0], v[8 * u + 1], q.bf16);
-                    x.y = pack16(v[8 * u + 2], v[8 * u + 3], q.bf16);
-                    x.z = pack16(v[8 * u + 4], v[8 * u + 5], q.bf16);
-                    x.w = pack16(v[8 * u + 6], v[8 * u + 7], q.bf16);
-                    st_shared_v4(buf_addr + lane * 128u + ((u ^ (lane & 7u)) << 4), x);
-                }
+                for (uint32_t u = 0; u < 8; ++u)
+                    st_shared_v4(staging + lane * 128u + ((u ^ (lane & 7u)) << 4),
+                                 make_uint4(x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]));
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    store_3d(&out.d, buf_addr, col, row0, k.g);
+                    store_3d(&out.d, staging, col, row0, k.g);
                     bulk_commit_group();
                 }
-                sbuf ^= 1u;
             }
             if (some) {
                 tc_fence_before();
