@@ -994,7 +994,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                 __syncwarp();
                 if (lane == 0) {
                     if (kPair)
-                        mbar_arrive_cluster(mapa_shared(smem_u32(&ctrl->tmem_empty[buf]), 0));
+                        mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&ctrl->tmem_empty[buf]), 0));
                     else
                         mbar_arrive(smem_u32(&ctrl->tmem_empty[buf]));
                 }

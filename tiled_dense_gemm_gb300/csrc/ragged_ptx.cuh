@@ -87,6 +87,16 @@ __device__ __forceinline__ void copy_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// Arrive on an mbarrier of another CTA of the cluster (its shared::cluster
+// address) without ordering memory: a release at cluster scope waits until
+// this thread's earlier global stores are visible there, which held every
+// tile's accumulator for 3400 cycles after it had been read.  What the
+// accumulator's release has to order is tensor memory only: its loads have
+// completed (tcgen05.wait::ld) and are fenced before the arrival.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 q) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w)
                  : "memory");
