@@ -325,6 +325,8 @@ static int run_dw(const void* U, const void* V, void* D, const int32_t* offsets,
         rc = encode_rows(&base.v, V, (uint64_t)Q, (uint64_t)T, (uint64_t)ldv, kBK, q.v3d ? 2 : 0, bf16);
     if (rc == GEMM_OK) rc = encode_stack(&out.d, D, (uint64_t)Q, (uint64_t)P, (uint64_t)G, 32, false, bf16);
     if (rc != GEMM_OK) return rc;
+    out.u = base.u;
+    out.v = base.v;
     StreamBuffers& sb = rt::buffers_for_locked(d, st);
     const size_t map_bytes = (size_t)G * 2 * sizeof(CUtensorMap);
     rc = rt::grow(&sb.rg_misc, &sb.rg_misc_bytes, map_bytes + (size_t)G * sizeof(DwGroup), st, false);

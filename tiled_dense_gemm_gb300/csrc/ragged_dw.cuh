@@ -8,12 +8,13 @@
 //
 // A group may end anywhere inside a 128-row block.  The rows after it belong
 // to another group and must not enter the sum, whatever they hold (0 x NaN is
-// NaN), so each group reads through its own pair of tensor maps whose row
-// extent ends with the group: the copies fill the rows beyond with zeros and
-// fetch nothing for them.  A small kernel before this one makes the maps from
-// the host's by setting that one extent (one warp per group), and orders the
-// groups by length, longest first, so that the last items of the persistent
-// grid are short ones.
+// NaN), so a group's last block is read through its own pair of tensor maps
+// whose row extent ends with the group: the copies fill the rows beyond with
+// zeros and fetch nothing for them.  (Whole blocks go through the maps of the
+// whole operands: a map's first use costs its fetch.)  A small kernel before
+// this one makes the maps from the host's by setting that one extent (one warp
+// per group), and orders the groups by length, longest first, so that the last
+// items of the persistent grid are short ones.
 //
 // Tile 128 x 128 per CTA, or 256 x 256 per CTA pair; stages of 128 rows; roles
 // and waits as in the ragged forward kernel, but eight epilogue warps (2-5 and
@@ -32,7 +33,8 @@ struct DwGroup {
 };
 
 struct DwMaps {
-    CUtensorMap d;  // the gradients, 3-D
+    CUtensorMap d;     // the gradients, 3-D
+    CUtensorMap u, v;  // the operands
 };
 
 struct DwParams {
@@ -185,8 +187,11 @@ __global__ void __launch_bounds__(kDwThreads, 1)
             bool ok = true;
             while (ok && next(k)) {
                 if (k.hi == k.lo) continue;
-                const CUtensorMap* m = q.maps + 2 * k.pos + (is_u ? 0 : 1);
-                if (k.pos != seen) map_acquire(m);
+                const CUtensorMap* const last = q.maps + 2 * k.pos + (is_u ? 0 : 1);
+                if (k.pos != seen && (k.hi - k.lo) % kBK != 0) {
+                    map_acquire(last);
+                    tma_prefetch_desc(last);
+                }
                 seen = k.pos;
                 const int32_t c0 = (is_u ? k.pt : k.qt) * (int32_t)kTile + 128 * (int32_t)rank;
                 for (int32_t r = k.lo; r < k.hi; r += kBK) {
@@ -201,6 +206,7 @@ __global__ void __launch_bounds__(kDwThreads, 1)
                     }
                     const uint32_t bar = kPair ? mapa_shared(full, 0) : full;
                     const uint32_t dst = ring + s * stride + (is_u ? 0u : kOperand);
+                    const CUtensorMap* const m = k.hi - r < kBK ? last : is_u ? &out.u : &out.v;
                     if (is_u ? q.u3d : q.v3d) {
                         load_3d<kPair>(dst, m, bar, 0, r, c0 / 64);
                     } else {
