@@ -457,7 +457,6 @@ int reset_after_error_locked(DeviceState& d) {
     for (auto& s : d.streams) {
         if (s.counters) cudaMemset(s.counters, 0, s.counter_bytes);
         if (s.pack_sync) cudaMemset(s.pack_sync, 0, s.pack_sync_bytes);
-        if (s.rg_flags) cudaMemset(s.rg_flags, 0, s.rg_flags_bytes);
     }
     cudaDeviceSynchronize();
     cudaGetLastError();
@@ -548,8 +547,6 @@ extern "C" void gemm_relu_shutdown(void) {
                 cudaFree(s.counters);
                 cudaFree(s.packed);
                 cudaFree(s.pack_sync);
-                cudaFree(s.rg_ws);
-                cudaFree(s.rg_flags);
                 cudaFree(s.rg_misc);
                 cudaFree(s.hA);
                 cudaFree(s.hB);

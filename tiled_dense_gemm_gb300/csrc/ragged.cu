@@ -202,7 +202,6 @@ static int run_forward(const void* X, const void* W, void* Y, const int32_t* off
     p.n_tiles = pl.n_tiles;
     p.cap = pl.cap;
     p.cluster = pl.cluster;
-    p.split = pl.split;
     p.num_stages = pl.num_stages;
     p.stage_bytes = pl.stage_bytes;
     p.turn_off = pl.num_stages * pl.stage_bytes;
@@ -229,13 +228,6 @@ static int run_forward(const void* X, const void* W, void* Y, const int32_t* off
                          p.x3d ? kBK / 64 : 0, bf16);
     if (rc != GEMM_OK) return rc;
     StreamBuffers& sb = rt::buffers_for_locked(d, st);
-    if (pl.split) {
-        rc = rt::grow(&sb.rg_ws, &sb.rg_ws_bytes, (size_t)pl.grid * 128 * (size_t)(pl.tmem_cols / 2) * 4, st, false);
-        if (rc == GEMM_OK) rc = rt::grow(&sb.rg_flags, &sb.rg_flags_bytes, (size_t)pl.grid * 4, st, true);
-        if (rc != GEMM_OK) return rc;
-        p.ws = reinterpret_cast<float*>(sb.rg_ws);
-        p.flags = reinterpret_cast<uint32_t*>(sb.rg_flags);
-    }
     if (ad) {
         p.ids = ad->ids;
         p.R = (int32_t)ad->R;
@@ -305,7 +297,7 @@ static int run_forward(const void* X, const void* W, void* Y, const int32_t* off
         return launch(ragged_kernel<true, false>, pl.grid, kThreads, smem, 2, st, m, p);
     }
     if ((rc = allow_smem(d, 3, ragged_kernel<false, false>)) != GEMM_OK) return rc;
-    return launch(ragged_kernel<false, false>, pl.grid, kThreads, smem, 1, st, m, p);
+    return launch(ragged_kernel<false, false>, pl.grid, kThreads, smem, pl.cluster, st, m, p);
 }
 
 // D[g] (P, Q) = U[rows of g]^T V[rows of g]

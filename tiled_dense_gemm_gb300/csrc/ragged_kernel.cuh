@@ -21,6 +21,10 @@
 // host round trip and no launch of its own.  A group's rows are cut into
 // tiles of equal width, so 260 rows are 144 + 116 and not 256 + 4.
 //
+// Column tiles that are few (short calls) are computed by clusters: each CTA
+// takes a share of the tile's k-blocks and the cluster adds the shares up
+// through distributed shared memory.
+//
 // Roles (224 threads, one CTA per SM): warp 0 copies row tiles, warp 6 the
 // weights, warp 1 issues the MMAs, warps 2-5
 // drain the accumulators; shared-memory ring of 128-k stages, two TMEM
@@ -72,8 +76,7 @@ struct Params {
     int32_t num_kb;      // ceil(K / kBK)
     int32_t n_tiles;     // column tiles (128, or 256 for a pair)
     int32_t cap;         // most rows of a tile
-    int32_t cluster;     // adapters, single CTAs: > 1: an item's k-blocks shared by the CTAs of a cluster
-    int32_t split;       // 1: the k-blocks of all items are cut into equal contiguous runs, one per CTA
+    int32_t cluster;     // single CTAs: > 1: each item's k-blocks shared by the CTAs of a cluster
     int32_t num_stages;
     int32_t stage_bytes; // stride of a ring stage
     int32_t turn_off;    // shared-memory offsets from the ring's start: the epilogue's transposition,
@@ -88,8 +91,6 @@ struct Params {
     int64_t ldy;
     const uint16_t* act;     // gate: outputs where act <= 0 are set to +0 (null: none)
     int64_t ld_act;
-    float* ws;               // split: one fp32 partial tile per CTA
-    uint32_t* flags;         // split: that partial is published (zero between launches)
     int32_t* err;            // err[0] timed-out waits, err[1] bad index arrays
     uint64_t timeout_ns;
     // adapters
@@ -229,8 +230,6 @@ struct Item {
     int32_t n;          // column tile
     int32_t kb0, kb1;   // this CTA's k-blocks [kb0, kb1)
     int32_t x0, x1;     // ... and extra ones (adapters)
-    bool begins, whole; // they hold the item's first k-block; all of them
-    uint32_t index;     // item number
     bool low;           // low-rank products of the row tile (n: which 256 of them), not columns of Y
 };
 
@@ -304,31 +303,18 @@ struct Iter {
     const int32_t* lows;  // adapters of pairs: low items before each row tile
     uint32_t n_low;       // items [0, n_low) are low ones
     uint32_t u, u1, step;
-    int32_t share;   // this CTA's rank in its cluster
-    int32_t kb_all;  // single CTAs: k-blocks of every item
+    int32_t share;      // this CTA's rank in its cluster
+    int32_t max_extra;  // single CTAs of adapters: the one row tile's extra k-blocks
 
     __device__ __forceinline__ Iter(const Params& p_, const int32_t* start_, const int32_t* tiles_,
                                     const int32_t* nslots_, const int32_t* lows_, uint32_t worker, uint32_t workers,
-                                    int32_t max_extra, int32_t share_)
-        : p(p_), start(start_), tiles(tiles_), nslots(nslots_), lows(lows_), share(share_) {
+                                    int32_t max_extra_, int32_t share_)
+        : p(p_), start(start_), tiles(tiles_), nslots(nslots_), lows(lows_), share(share_), max_extra(max_extra_) {
         const uint32_t items = (uint32_t)tiles[p.G] * (uint32_t)p.n_tiles;
         n_low = kPair && kAdapters && p.low_out ? (uint32_t)lows[tiles[p.G]] : 0u;
-        kb_all = p.num_kb + (kAdapters ? max_extra : 0);
-        if (!kPair && p.split) {
-            const uint32_t units = items * (uint32_t)kb_all;
-            u = begin_of(units, worker, workers);
-            u1 = begin_of(units, worker + 1, workers);
-            step = 0;
-        } else {
-            u = worker;
-            u1 = n_low + items;
-            step = workers;
-        }
-    }
-
-    static __device__ __forceinline__ uint32_t begin_of(uint32_t units, uint32_t worker, uint32_t workers) {
-        const uint32_t q = units / workers, r = units - q * workers;
-        return worker * q + min(worker, r);
+        u = worker;
+        u1 = n_low + items;
+        step = workers;
     }
 
     // rows of tile j of the cnt of group g: equal widths, in the MMA's steps
@@ -342,37 +328,20 @@ struct Iter {
 
     __device__ __forceinline__ bool next(Item& it) {
         if (u >= u1) return false;
-        uint32_t item;
+        uint32_t item = u;
+        u += step;
         it.kb0 = it.x0 = it.x1 = 0;
         it.kb1 = p.num_kb;
-        it.begins = it.whole = true;
-        if (!kPair && step == 0) {
-            item = u / (uint32_t)kb_all;
-            const int32_t b0 = (int32_t)(u - item * (uint32_t)kb_all);
-            const int32_t b1 = (int32_t)min((uint32_t)kb_all, (uint32_t)b0 + (u1 - u));
-            u += (uint32_t)(b1 - b0);
-            it.kb0 = min(b0, p.num_kb);
-            it.kb1 = min(b1, p.num_kb);
-            it.x0 = b0 - it.kb0;
-            it.x1 = b1 - it.kb1;
-            it.begins = b0 == 0;
-            it.whole = it.begins && b1 == kb_all;
-        } else {
-            item = u;
-            u += step;
-            if (kAdapters && !kPair && p.cluster > 1) {
-                // an even share of the main k-blocks (DRAM) and of the extra
-                // ones (latency) for each CTA of the cluster
-                const int32_t extra = kb_all - p.num_kb;
-                it.kb0 = share * p.num_kb / p.cluster;
-                it.kb1 = (share + 1) * p.num_kb / p.cluster;
-                it.x0 = share * extra / p.cluster;
-                it.x1 = (share + 1) * extra / p.cluster;
-            } else if (kAdapters) {
-                it.x1 = -1;  // the row tile's, below
-            }
+        if (!kPair && p.cluster > 1) {
+            // an even share of the main k-blocks (DRAM) and of the extra ones
+            // (latency) for each CTA of the cluster
+            it.kb0 = share * p.num_kb / p.cluster;
+            it.kb1 = (share + 1) * p.num_kb / p.cluster;
+            it.x0 = share * max_extra / p.cluster;
+            it.x1 = (share + 1) * max_extra / p.cluster;
+        } else if (kAdapters) {
+            it.x1 = kPair ? -1 : max_extra;  // (-1: the row tile's, below)
         }
-        it.index = item;
         it.low = false;
         if constexpr (kPair && kAdapters) {
             if (item < n_low) {
@@ -465,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
     int32_t* const tiles = start + p.G + 1;
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = kPair ? cluster_ctarank() : 0u;
-    const bool clustered = kAdapters && !kPair && p.cluster > 1;
+    const bool clustered = !kPair && p.cluster > 1;
     const uint32_t share = clustered ? cluster_ctarank() : 0u;
     const uint32_t worker = kPair ? blockIdx.x / 2 : clustered ? blockIdx.x / (uint32_t)p.cluster : blockIdx.x;
     const uint32_t workers = kPair ? gridDim.x / 2 : clustered ? gridDim.x / (uint32_t)p.cluster : gridDim.x;
@@ -866,7 +835,6 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
         const uint32_t quarter = warp & 3u;
         const uint32_t lane_row = quarter * 32 + lane;
         const uint32_t cols = p.tmem_cols / 2;
-        const int64_t part = (int64_t)128 * cols;  // floats of one partial tile
         uint32_t local = 0;
         float v[32];
         const uint32_t turn = ring + (uint32_t)p.turn_off + quarter * (32u * kTurnPitch);
@@ -1089,52 +1057,6 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
             // this thread's 8 columns of Y (of rows lane / 4, + 8, ...)
             const int32_t n = it.n * (kPair ? 256 : 128) + 128 * (int32_t)rank + 32 * (int32_t)quarter + 8 * (int32_t)(lane & 3u);
             const bool in_n = n < p.N;
-            const bool whole = it.whole;
-            if (!kPair && !whole && !it.begins) {
-                // a share of an item that an earlier CTA began: publish it
-                float4* dst = reinterpret_cast<float4*>(p.ws + (int64_t)blockIdx.x * part) + lane_row;
-                for (int32_t c = 0; c < it.w; c += 32) {
-                    __syncwarp();
-                    tmem_load_fragments(taddr + c, v);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if ((j & 2) == 0 || it.w - c > 16)  // (a last chunk of 16 columns is every other half)
-                            __stcg(dst + (int64_t)(c / 4 + j) * 128,
-                                   make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
-                }
-                release();
-                __threadfence();
-                named_bar_sync(kEpiBarrier, kEpiThreads);
-                if (threadIdx.x == 64) atomicExch(p.flags + blockIdx.x, 1u);
-                return true;
-            }
-            uint32_t others = 0;  // CTAs after this one that hold a share of the item
-            if (!kPair && !whole) {
-                const uint32_t units = (uint32_t)tiles[p.G] * (uint32_t)p.n_tiles * (uint32_t)iter.kb_all;
-                const uint32_t end = (it.index + 1) * (uint32_t)iter.kb_all;
-                while (blockIdx.x + others + 1 < gridDim.x &&
-                       It::begin_of(units, blockIdx.x + others + 1, gridDim.x) < end)
-                    ++others;
-                bool all = true;
-                if (threadIdx.x == 64) {
-                    volatile uint32_t* vf = p.flags + blockIdx.x + 1;
-                    volatile int32_t* abort_flag = &ctrl->abort_flag;
-                    const uint64_t t0 = globaltimer_ns();
-                    for (uint32_t o = 0; o < others && all; ++o)
-                        while (vf[o] == 0u)
-                            if (*abort_flag || globaltimer_ns() - t0 > p.timeout_ns) {
-                                *abort_flag = 1;
-                                atomicCAS(p.err, 0, (int32_t)kErrEpi);
-                                all = false;
-                                break;
-                            }
-                    __threadfence();
-                }
-                if (!named_bar_and(kEpiBarrier, kEpiThreads, all)) {
-                    release();
-                    return false;
-                }
-            }
             for (int32_t c = 0; c < it.w; c += 32) {
                 uint4 gate[4];
                 if (p.act) {
@@ -1148,27 +1070,6 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                 }
                 __syncwarp();  // (also: the last chunk's shared-memory reads are done)
                 tmem_load_fragments(taddr + c, v);
-                const float4* src = reinterpret_cast<const float4*>(p.ws + (int64_t)(blockIdx.x + 1) * part) + lane_row;
-                // the others' shares in their order, two on the way at a time
-                for (uint32_t o = 0; o < others; o += 2) {
-                    float4 x[2][8];
-#pragma unroll
-                    for (int q = 0; q < 2; ++q)
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            x[q][j] = o + q < others && ((j & 2) == 0 || it.w - c > 16)
-                                          ? __ldcg(src + (int64_t)(o + q) * (part / 4) + (int64_t)(c / 4 + j) * 128)
-                                          : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                    for (int q = 0; q < 2; ++q)
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            v[4 * j] += x[q][j].x;
-                            v[4 * j + 1] += x[q][j].y;
-                            v[4 * j + 2] += x[q][j].z;
-                            v[4 * j + 3] += x[q][j].w;
-                        }
-                }
                 if (p.apply_relu) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = v[j] > 0.0f ? v[j] : 0.0f;  // -0 and NaN become +0
@@ -1198,10 +1099,6 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                 }
             }
             release();
-            if (!kPair && !whole) {
-                named_bar_sync(kEpiBarrier, kEpiThreads);  // the partials have been read
-                for (uint32_t o = et; o < others; o += kEpiThreads) p.flags[blockIdx.x + 1 + o] = 0u;
-            }
             return true;
         };
         if (kAdapters && !kPair && lane == 0) {
@@ -1273,9 +1170,17 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
 #pragma unroll
                         for (int j = 0; j < 8; ++j) x[j] = x[j] > 0.0f ? x[j] : 0.0f;
                     }
-                    *reinterpret_cast<uint4*>(p.Y + (int64_t)(it.row0 + r) * p.ldy + n) =
-                        make_uint4(pack16(x[0], x[1], p.bf16), pack16(x[2], x[3], p.bf16), pack16(x[4], x[5], p.bf16),
-                                   pack16(x[6], x[7], p.bf16));
+                    uint4 q = make_uint4(pack16(x[0], x[1], p.bf16), pack16(x[2], x[3], p.bf16),
+                                         pack16(x[4], x[5], p.bf16), pack16(x[6], x[7], p.bf16));
+                    if (p.act) {
+                        const uint4 gate = __ldcg(
+                            reinterpret_cast<const uint4*>(p.act + (int64_t)(it.row0 + r) * p.ld_act + n));
+                        q.x = gate16(q.x, gate.x, p.bf16);
+                        q.y = gate16(q.y, gate.y, p.bf16);
+                        q.z = gate16(q.z, gate.z, p.bf16);
+                        q.w = gate16(q.w, gate.w, p.bf16);
+                    }
+                    *reinterpret_cast<uint4*>(p.Y + (int64_t)(it.row0 + r) * p.ldy + n) = q;
                 }
             }
         }

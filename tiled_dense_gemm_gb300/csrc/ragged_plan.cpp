@@ -9,7 +9,6 @@ namespace {
 constexpr int64_t kSmem = 227 * 1024;  // per CTA
 constexpr int64_t kCtrl = 1024;
 constexpr int64_t kStageK = 128;       // k-rows per ring stage
-constexpr int64_t kExtraK = 64;        // products of the adapters' ranks per extra stage
 constexpr int64_t kTurn = 4 * 32 * 80; // the epilogue's transposition
 constexpr int64_t kLowRows = 1024;
 constexpr int64_t kLowSmem = 18 * 1024;
@@ -24,14 +23,19 @@ RaggedPlan plan_rows(int64_t T, int64_t G, int64_t N, int64_t K, int64_t R, int6
     RaggedPlan p = {};
     const int64_t avg = ceil_div(T, G);
     const int pairs = max_pairs < 0 ? 0 : std::min(max_pairs ? max_pairs : num_sms / 2, num_sms / 2);
-    p.pair = avg > 128 && pairs > 0;
+    // Up to 64 rows per group the weights' way from DRAM is what counts, and
+    // single CTAs and pairs take the same time (64 groups of 4096 x 2048, 64
+    // rows each: 163 us both; 4 rows: 153 and 154); above, pairs move fewer
+    // bytes per operation into the multiprocessors (128 rows each: 171 us
+    // against 266).  Tiles of at most 128 rows for groups of about that many
+    // (128 rows each: 171 us, with tiles of up to 256: 175; 192 rows: 227
+    // and 185).
+    p.pair = avg > (R > 0 ? 128 : 64) && pairs > 0;
     int64_t cap;
     if (p.pair)
-        cap = 256;
-    else if (R > 0 || T <= 64)
-        cap = std::min<int64_t>(128, round_up(T, 16));
+        cap = avg <= 96 ? 128 : 256;
     else
-        cap = avg <= 16 ? 64 : 128;
+        cap = std::min<int64_t>(R > 0 ? 128 : 64, round_up(T, 16));
     p.cap = (int32_t)cap;
     p.num_kb = (int32_t)ceil_div(K, kStageK);
     p.n_tiles = (int32_t)ceil_div(N, p.pair ? 256 : 128);
@@ -50,15 +54,15 @@ RaggedPlan plan_rows(int64_t T, int64_t G, int64_t N, int64_t K, int64_t R, int6
     int64_t cols = 2 * round_up(cap, 32), alloc = 32;
     while (alloc < cols) alloc *= 2;
     p.tmem_cols = (int32_t)alloc;
-    // at most this many row tiles, whatever the groups' sizes are
-    const int64_t tiles = R > 0 ? ceil_div(T, cap) : std::min(T, ceil_div(T, cap) + std::min(G, T));
+    // at most this many row tiles, whatever the groups' sizes are: one row
+    // in each of as many groups as can have one, the rest in full tiles
+    const int64_t used = std::min(G, T);
+    const int64_t tiles = R > 0 ? ceil_div(T, cap) : used + (T - used) / cap;
     const int64_t items = tiles * p.n_tiles;
-    int64_t kb = p.num_kb;
     if (R > 0) {
         p.rank_box = 8;
         while (p.rank_box < 64 && p.rank_box < rank) p.rank_box *= 2;
         p.rank_pad = (int32_t)round_up(rank, p.rank_box);
-        kb += ceil_div(std::min(R, cap) * p.rank_pad, kExtraK);
         const int64_t nt = ceil_div(T, cap);
         p.row_width = (int32_t)round_up(ceil_div(T, nt), p.pair ? 32 : 16);
     }
@@ -66,18 +70,13 @@ RaggedPlan plan_rows(int64_t T, int64_t G, int64_t N, int64_t K, int64_t R, int6
         p.status = GEMM_ERR_TOO_LARGE;
         return p;
     }
-    // One row tile and few column tiles: clusters share each tile's k-blocks
-    // and add up on chip.  Else the k-blocks of all items are cut evenly.
+    // Fewer tiles than half the multiprocessors: clusters share each tile's
+    // k-blocks and add up on chip (one group of 4096 x 4096, 2 rows: TODO us
+    // against 18.7 without).
     p.cluster = 1;
-    while (R > 0 && !p.pair && p.cluster < 8 && items * p.cluster * 2 <= num_sms && p.cluster * 2 <= p.num_kb)
-        p.cluster *= 2;
-    p.split = !p.pair && p.cluster == 1 && items * kb <= kIndexMax;
-    if (p.cluster > 1) {
-        p.grid = (int32_t)items * p.cluster;
-        return p;
-    }
+    while (!p.pair && p.cluster < 8 && items * p.cluster * 2 <= num_sms && p.cluster * 4 <= p.num_kb) p.cluster *= 2;
     p.grid = p.pair ? 2 * (int32_t)std::min<int64_t>(pairs, items)
-                    : (int32_t)std::min<int64_t>(num_sms, p.split ? items * kb : items);
+                    : (int32_t)std::min<int64_t>(num_sms, items) * p.cluster;
     return p;
 }
 

@@ -36,12 +36,7 @@ struct StreamBuffers {
     void* hC = nullptr;
     size_t hA_bytes = 0, hB_bytes = 0, hC_bytes = 0;
     int32_t* h_err = nullptr;  // pinned copy of the error word (host-buffer entry point)
-    // ragged products: fp32 partial tiles, their flags (zero between
-    // launches), and what their first kernel hands to the second
-    void* rg_ws = nullptr;
-    size_t rg_ws_bytes = 0;
-    void* rg_flags = nullptr;
-    size_t rg_flags_bytes = 0;
+    // ragged products: what their first kernel hands to the second
     void* rg_misc = nullptr;
     size_t rg_misc_bytes = 0;
     // host-buffer entry point, pipelined: copy-in and copy-out streams and
