@@ -556,6 +556,29 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
         if (!kPair || rank == 0) mbar_arrive_expect_tx(full, bytes);
     };
 
+    // The order of an item's k-blocks.  Pairs: all main ones, then the extra
+    // ones.  Single CTAs (few rows): the last main ones in turn with the extra
+    // ones, which wait for latencies and not for DRAM.  Segment j holds main
+    // blocks [k0, k1), then extra ones [e0, e1).
+    auto mains_until = [&](const Item& i, int32_t j) {  // main blocks before extra one j
+        const int32_t n = i.kb1 - i.kb0;
+        return kPair ? n : min(n, max(0, n - (i.x1 - i.x0)) + j + 1);
+    };
+    auto segments = [&](const Item& i) { return kPair || !kAdapters ? 1 : max(1, i.x1 - i.x0); };
+    auto segment = [&](const Item& i, int32_t j, int32_t& k0, int32_t& k1, int32_t& e0, int32_t& e1) {
+        if (kPair || !kAdapters || i.x1 <= i.x0) {
+            k0 = i.kb0;
+            k1 = i.kb1;
+            e0 = i.x0;
+            e1 = i.x1;
+        } else {
+            k0 = i.kb0 + (j > 0 ? mains_until(i, j - 1) : 0);
+            k1 = i.kb0 + mains_until(i, j);
+            e0 = i.x0 + j;
+            e1 = e0 + 1;
+        }
+    };
+
     if (warp == 0) {
         // ---------------------------------------------------------- row tiles
         if (lane == 0) {
@@ -572,7 +595,10 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                                            p.rank_box) * 256u + 2u * rows * (uint32_t)(kBK * 2);
                 }
                 const CUtensorMap* m = &maps.x[rows / 16 - 1];
-                for (int32_t kb = it.kb0; kb < it.kb1; ++kb) {
+                for (int32_t j = 0; ok && j < segments(it); ++j) {
+                int32_t k0, k1, e0, e1;
+                segment(it, j, k0, k1, e0, e1);
+                for (int32_t kb = k0; kb < k1; ++kb) {
                     if (!wait_phase(empty0 + 8u * s, ph ^ 1u, ctrl, p, kErrTokens)) {
                         ok = false;
                         break;
@@ -597,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                     // the epilogue's warps fill and arm the extra k-blocks;
                     // this thread, which is never more than a lap ahead of
                     // the MMAs, tells them when a stage is free
-                    for (int32_t e = it.x0; ok && e < it.x1; ++e) {
+                    for (int32_t e = e0; ok && e < e1; ++e) {
                         ok = wait_phase(empty0 + 8u * s, ph ^ 1u, ctrl, p, kErrTokens);
                         if (!ok) break;
                         mbar_arrive(smem_u32(&ctrl->extra[s]));
@@ -607,6 +633,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                             ph ^= 1u;
                         }
                     }
+                }
                 }
             }
             if (!kPair || rank == 0) {
@@ -623,7 +650,10 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
         bool ok = true;
         while (ok && iter.next(it)) {
             const int32_t n0 = it.n * (kPair ? 256 : 128) + 128 * (int32_t)rank;
-            const int32_t n_main = it.kb1 - it.kb0;
+            for (int32_t j = 0; ok && j < segments(it); ++j) {
+            int32_t kb_first, kb_end, e_first, e_end;
+            segment(it, j, kb_first, kb_end, e_first, e_end);
+            const int32_t n_main = kb_end - kb_first;
             if (kPair && kAdapters && it.low) {
                 // first factors of the tile's adapters, 128 rows per CTA; a
                 // lane per box of rank_box rows x 64 k
@@ -656,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                 }
             } else if (lane == 0) {
                 uint32_t ls = s, lph = ph;
-                for (int32_t kb = it.kb0; kb < it.kb1; ++kb) {
+                for (int32_t kb = kb_first; kb < kb_end; ++kb) {
                     if (!wait_phase(empty0 + 8u * ls, lph ^ 1u, ctrl, p, kErrWeights)) {
                         ok = false;
                         break;
@@ -690,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
             if constexpr (kAdapters) {
                 const int32_t slots = nslots[it.tile];
                 const int32_t per = kXK >> p.box_shift;
-                for (int32_t e = it.x0; ok && e < it.x1; ++e) {
+                for (int32_t e = e_first; ok && e < e_end; ++e) {
                     ok = wait_phase(empty0 + 8u * s, ph ^ 1u, ctrl, p, kErrWeights);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
@@ -716,6 +746,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                         ph ^= 1u;
                     }
                 }
+            }
             }
         }
         __syncwarp();
@@ -750,8 +781,8 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                 const uint32_t half16 = ((uint32_t)it.w / (kPair ? 2u : 1u)) * 128u >> 4;  // second 64 k of the rows
                 uint32_t acc = 0;
                 // the k-blocks; weights from `a_first`, k-step k at offset(k)
-                auto main_blocks = [&](uint64_t a_first, uint32_t idesc, auto offset) {
-                    for (int32_t kb = it.kb0; kb < it.kb1; ++kb) {
+                auto main_blocks = [&](int32_t kb, int32_t kb_end, uint64_t a_first, uint32_t idesc, auto offset) {
+                    for (; kb < kb_end; ++kb) {
                         if (!wait_phase(full0 + 8u * s, ph, ctrl, p, kErrStage)) {
                             ok = false;
                             break;
@@ -771,13 +802,16 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                         }
                     }
                 };
+                for (int32_t j = 0; ok && j < segments(it); ++j) {
+                int32_t k0, k1, e0, e1;
+                segment(it, j, k0, k1, e0, e1);
                 if (kPair && kAdapters && it.low) {
                     // (one box: the MMA's rows past it read what lies there, into lanes that nothing reads)
                     const uint32_t sub16 =
                         (low_boxes(p, nslots[it.tile]) == 1 ? (uint32_t)p.rank_box : 128u) * 128u >> 4;
-                    main_blocks(a_desc_k, idesc_k | nbits, [=](uint32_t k) { return (k / 4) * sub16 + (k % 4) * 2u; });
+                    main_blocks(k0, k1, a_desc_k, idesc_k | nbits, [=](uint32_t k) { return (k / 4) * sub16 + (k % 4) * 2u; });
                 } else
-                    main_blocks(a_desc0, idesc0 | nbits, [&](uint32_t k) { return a_off[k]; });
+                    main_blocks(k0, k1, a_desc0, idesc0 | nbits, [&](uint32_t k) { return a_off[k]; });
                 if constexpr (kAdapters) {
                     const int32_t slots = nslots[it.tile];
                     const uint32_t box = (uint32_t)p.rank_box;
@@ -785,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                     // chunks; boxes of 8 rows pair up to an MMA's 16
                     const uint64_t x_desc0 = box == 8 ? make_sw128_desc(ring, 1024, 2048)
                                                       : make_sw128_desc(ring, box * 128u, 1024);
-                    for (int32_t e = it.x0; ok && e < it.x1; ++e) {
+                    for (int32_t e = e0; ok && e < e1; ++e) {
                         if (!wait_phase(full0 + 8u * s, ph, ctrl, p, kErrStage)) {
                             ok = false;
                             break;
@@ -816,6 +850,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                             ph ^= 1u;
                         }
                     }
+                }
                 }
                 if (!ok) break;
                 mma_commit<kCG>(tfull0 + 8u * buf, 0x3);
@@ -852,8 +887,12 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
         auto fill_extras = [&]() {
             const int32_t slots = nslots[it.tile];
             const int32_t e0 = it.x0, e1 = it.x1;
-            pos += (uint32_t)(it.kb1 - it.kb0);
-            if (e0 >= e1) return true;
+            // ring stages before extra block e
+            auto stage_of = [&](int32_t e) { return pos + (uint32_t)(mains_until(it, e - e0) + e - e0); };
+            if (e0 >= e1) {
+                pos += (uint32_t)(it.kb1 - it.kb0);
+                return true;
+            }
             const uint32_t rows = (uint32_t)it.w / (kPair ? 2u : 1u);
             const int32_t y = it.row0 + (int32_t)(rank * rows);
             bool ok = true;     // (alike in all threads)
@@ -888,12 +927,12 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                 }
             }
             // Blocks in flight: stage e + S - 2 is free while the MMAs work
-            // on block e - 1, in time for e.
-            const int32_t ahead = max(0, min(3, (int32_t)S - 2));
+            // on block e - 1, in time for e (in turn with main ones: half).
+            const int32_t ahead = max(0, min(3, ((int32_t)S - 2) / (kPair ? 1 : 2)));
             int32_t issued = e0;
             for (int32_t e = e0; ok && e < e1; ++e) {
                 for (; issued < e1 && issued <= e + ahead; ++issued) {
-                    const uint32_t st = (pos + (uint32_t)(issued - e0)) % S;
+                    const uint32_t st = stage_of(issued) % S;
                     ok = wait_phase(smem_u32(&ctrl->extra[st]), (extra_ph >> st) & 1u, ctrl, p, kErrTokens);
                     extra_ph ^= 1u << st;
                     ok = named_bar_and(kEpiBarrier, kEpiThreads, ok);
@@ -931,7 +970,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                 fence_proxy_async_smem();
                 named_bar_sync(kEpiBarrier, kEpiThreads);
                 if (et == 0) {
-                    const uint32_t st = (pos + (uint32_t)(e - e0)) % S;
+                    const uint32_t st = stage_of(e) % S;
                     if (kPair && rank != 0) {
                         mbar_arrive_cluster(mapa_shared(smem_u32(&ctrl->peer[st]), 0));
                     } else {
@@ -944,7 +983,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                     }
                 }
             }
-            pos += (uint32_t)(e1 - e0);
+            pos += (uint32_t)(it.kb1 - it.kb0 + e1 - e0);
             return named_bar_and(kEpiBarrier, kEpiThreads, ok && armed);
         };
         // the item whose accumulator is the CTA's `local`-th; false: aborting
