@@ -148,3 +148,397 @@ def test_adapters_many_rows(T, R, rank, kind, layout, dtype):
     y = binding.gemm_relu_adapters(x, w, a, b, ids, scale, apply_relu=True, b_layout=layout)
     binding.check_device_error()
     ref.check(y, ref.adapters(x, w, a, b, ids, scale, True, layout), f"T={T} R={R} rank {rank} {kind} {layout} {dtype}")
+
+
+NAN_GROUPS = [[1, 2, 3], [15, 17, 1], [100, 28, 129], [127, 1, 128, 130], [40, 300, 5]]
+
+
+@pytest.mark.parametrize("sizes", NAN_GROUPS, ids=str)
+@pytest.mark.parametrize("K,N", [(72, 136), (520, 648)])
+def test_rows_of_other_groups_do_not_enter(sizes, K, N):
+    """NaN in one group's rows, in rows of no group and in one group's weights
+    stays in that group's results."""
+    for dtype in ("f16", "bf16"):
+        T = sum(sizes) + 9
+        off = offsets_of(sizes, 4)
+        o = off.cpu().tolist()
+        x, dy = normal((T, K), 1, dtype), normal((T, N), 2, dtype)
+        w = weights(len(sizes), K, N, "kn", 3, dtype, K ** -0.5)
+        for sick in range(len(sizes)):
+            xs, ds, ws = x.clone(), dy.clone(), w.clone()
+            for t in (xs, ds):
+                t[:o[0]] = float("nan")
+                t[o[-1]:] = float("inf")
+                t[o[sick]:o[sick + 1]] = float("nan")
+            ws[sick] = float("nan")
+            y = binding.gemm_relu_grouped(xs, ws, off, apply_relu=False)
+            dx = binding.gemm_relu_grouped_dx(ds, ws, off)
+            dw = binding.gemm_relu_grouped_dw(xs, ds, off)
+            binding.check_device_error()
+            ry, rx, rw = (ref.grouped(x, w, off, False, "kn"), ref.grouped_dx(dy, w, off, None, "kn"),
+                          ref.grouped_dw(x, dy, off, "kn"))
+            rows = np.ones(T, bool)
+            rows[o[sick]:o[sick + 1]] = False
+            assert torch.isnan(y[~torch.from_numpy(rows).to(DEV)]).all()
+            assert torch.isnan(dw[sick]).all()
+            keep = torch.from_numpy(rows).to(DEV)
+            ref.check(y[keep], (ry[0][rows], ry[1][rows]), f"y {sizes} {sick}")
+            ref.check(dx[keep], (rx[0][rows], rx[1][rows]), f"dx {sizes} {sick}")
+            others = [g for g in range(len(sizes)) if g != sick]
+            ref.check(dw[others], (rw[0][others], rw[1][others]), f"dw {sizes} {sick}")
+            assert (y[:o[0]] == 0).all() and (y[o[-1]:] == 0).all()
+
+
+def test_gate_values():
+    """The gate opens for positive numbers and +inf only, and a closed gate
+    gives +0 whatever the product is."""
+    for dtype in ("f16", "bf16"):
+        K, N, T = 64, 64, 40
+        off = offsets_of([17, 23])
+        dy, w = normal((T, N), 1, dtype), weights(2, K, N, "kn", 2, dtype, N ** -0.5)
+        act = normal((T, K), 3, dtype)
+        special = [0.0, -0.0, float("inf"), float("-inf"), float("nan"), -1.0, 2.0 ** -14, -(2.0 ** -14)]
+        for i, v in enumerate(special):
+            act[:, i] = v
+        value, bound = ref.grouped_dx(dy, w, off, None, "kn")
+        dx = binding.gemm_relu_grouped_dx(dy, w, off, act=act)
+        binding.check_device_error()
+        keep = (act.double() > 0).cpu().numpy()
+        ref.check(dx, (np.where(keep, value, 0.0), np.where(keep, bound, 0.0)), dtype)
+        assert not torch.signbit(dx[~torch.from_numpy(keep).to(DEV)]).any()
+        dy[:] = float("nan")
+        dx = binding.gemm_relu_grouped_dx(dy, w, off, act=act)
+        assert torch.isnan(dx[torch.from_numpy(keep).to(DEV)]).all()
+        assert (dx[~torch.from_numpy(keep).to(DEV)] == 0).all()
+
+
+def test_binding_refuses_on_the_gpu():
+    x, w, off = normal((6, 64), 1, "f16"), weights(2, 64, 72, "kn", 2, "f16", 0.1), offsets_of([2, 4])
+    call = binding.gemm_relu_grouped
+    with pytest.raises(TypeError):
+        call(x, w, off.long())
+    with pytest.raises(ValueError):
+        call(x, w, off[:2])
+    with pytest.raises(ValueError):
+        call(x, w, off.cpu())
+    with pytest.raises(ValueError):
+        call(x, w.transpose(1, 2), off, b_layout="nk")  # not contiguous
+    with pytest.raises(ValueError):
+        call(x.t().contiguous().t(), w, off)            # rows not contiguous
+    with pytest.raises(ValueError):
+        call(x, w, off, y=normal((6, 64), 3, "f16"))
+    with pytest.raises(TypeError):
+        call(x, w, off, y=normal((6, 72), 3, "bf16"))
+    with pytest.raises(binding.GemmReluError):          # a pitch that is not a multiple of 16 bytes
+        call(normal((6, 68), 4, "f16")[:, :64], w, off)
+    with pytest.raises(binding.GemmReluError):          # rows that begin off a 16-byte boundary
+        call(normal((6, 80), 4, "f16")[:, 4:68], w, off)
+    with pytest.raises(ValueError):
+        binding.gemm_relu_grouped_dx(normal((6, 72), 5, "f16"), w, off, act=normal((6, 72), 6, "f16"))
+    with pytest.raises(ValueError):
+        binding.gemm_relu_grouped_dw(x, normal((6, 72), 5, "f16"), off, dw=normal((2, 72, 64), 6, "f16"))
+    a, b = normal((3, 4, 64), 7, "f16"), normal((3, 4, 72), 8, "f16")
+    ids = torch.zeros(6, dtype=torch.int32, device=DEV)
+    with pytest.raises(TypeError):
+        binding.gemm_relu_adapters(x, w[0], a, b, ids, torch.ones(3, device=DEV, dtype=torch.float64))
+    with pytest.raises(ValueError):
+        binding.gemm_relu_adapters(x, w[0], a, b, ids, torch.ones(2, device=DEV))
+    with pytest.raises(ValueError):
+        binding.gemm_relu_adapters(x, w[0], a, b, ids[:5])
+    with pytest.raises(ValueError):
+        binding.gemm_relu_adapters(x, w[0], a, b[:, :2], ids)
+    binding.check_device_error()
+
+
+@pytest.mark.parametrize("bad", [[0, 9, 5, 20], [-3, 4, 8, 20], [0, 4, 8, 99], [5, 5, 2, 1]])
+def test_bad_offsets_are_reported(bad):
+    """Offsets that decrease or leave [0, T]: reported once, nothing outside
+    the outputs is written, and the next call is right."""
+    T, K, N = 20, 72, 136
+    x, dy, w = normal((T, K), 1, "f16"), normal((T, N), 2, "f16"), weights(3, K, N, "kn", 3, "f16", 0.1)
+    off = torch.tensor(bad, dtype=torch.int32, device=DEV)
+    good = offsets_of([3, 0, 17])
+    guard = torch.full((3, T, N), 7.0, dtype=torch.float16, device=DEV)
+    for run in (lambda o: binding.gemm_relu_grouped(x, w, o, y=guard[1]),
+                lambda o: binding.gemm_relu_grouped_dx(dy, w, o),
+                lambda o: binding.gemm_relu_grouped_dw(x, dy, o)):
+        run(off)
+        with pytest.raises(binding.GemmReluError, match="GEMM_ERR_INDEX"):
+            binding.check_device_error()
+        run(good)
+        binding.check_device_error()
+    assert (guard[0] == 7).all() and (guard[2] == 7).all()
+    ref.check(guard[1], ref.grouped(x, w, good, True, "kn"), "after")
+
+
+@pytest.mark.parametrize("T", [5, 200, 1300])
+def test_bad_ids_are_reported(T):
+    R, rank, K, N = 3, 8, 64, 72
+    x, a, b, w = normal((T, K), 1, "f16"), normal((R, rank, K), 2, "f16", 0.1), normal((R, rank, N), 3, "f16"), normal((K, N), 4, "f16", 0.1)
+    ids = make_ids(T, R, "mixed", 1)
+    sick = ids.clone()
+    sick[1], sick[T - 1] = R, -2
+    y = binding.gemm_relu_adapters(x, w, a, b, sick)
+    with pytest.raises(binding.GemmReluError, match="GEMM_ERR_INDEX"):
+        binding.check_device_error()
+    none = sick.clone()
+    none[1] = none[T - 1] = -1
+    ref.check(y, ref.adapters(x, w, a, b, none, None, True, "kn"), "as without adapter")
+    y = binding.gemm_relu_adapters(x, w, a, b, ids)
+    binding.check_device_error()
+    ref.check(y, ref.adapters(x, w, a, b, ids, None, True, "kn"), "after")
+
+
+@pytest.mark.parametrize("T", [7, 130, 700, 1100])
+def test_adapters_do_not_mix(T):
+    """A NaN factor or an infinite scale of one adapter stays in its rows."""
+    R, rank, K, N = 5, 20, 136, 200
+    x, a, b, w = normal((T, K), 1, "bf16"), normal((R, rank, K), 2, "bf16", 0.1), normal((R, rank, N), 3, "bf16"), normal((K, N), 4, "bf16", 0.1)
+    scale = torch.ones(R, device=DEV)
+    ids = make_ids(T, R, "mixed", 2)
+    rows = (ids != 1) & (ids != 3) & (ids != 4)
+    value, bound = ref.adapters(x, w, a, b, ids, scale, False, "kn")
+    a[1], b[3], scale[4] = float("nan"), float("nan"), float("inf")
+    y = binding.gemm_relu_adapters(x, w, a, b, ids, scale, apply_relu=False)
+    binding.check_device_error()
+    keep = rows.cpu().numpy()
+    ref.check(y[rows], (value[keep], bound[keep]), f"T={T}")
+    assert torch.isnan(y[(ids == 1) | (ids == 3)]).all()
+
+
+def test_row_pitches():
+    """Rows inside wider matrices, for every row operand; what lies between
+    them is neither read nor written."""
+    T, K, N, sizes = 70, 72, 136, [30, 0, 33]
+    off = offsets_of(sizes, 2)
+    def padded(width, seed, left):
+        wide = torch.full((T, width + 24), float("nan"), dtype=torch.bfloat16, device=DEV)
+        wide[:, left:left + width] = normal((T, width), seed, "bf16")
+        return wide[:, left:left + width], wide
+    x, _ = padded(K, 1, 8)
+    dy, _ = padded(N, 2, 16)
+    act, _ = padded(K, 3, 0)
+    w = weights(3, K, N, "kn", 4, "bf16", 0.1)
+    y, wide_y = padded(N, 5, 8)
+    binding.gemm_relu_grouped(x, w, off, y=y)
+    ref.check(y, ref.grouped(x, w, off, True, "kn"), "y")
+    dx, wide_dx = padded(K, 6, 16)
+    binding.gemm_relu_grouped_dx(dy, w, off, act=act, dx=dx)
+    ref.check(dx, ref.grouped_dx(dy, w, off, act, "kn"), "dx")
+    ref.check(binding.gemm_relu_grouped_dw(x, dy, off), ref.grouped_dw(x, dy, off, "kn"), "dw")
+    a, b = normal((4, 12, K), 7, "bf16", 0.1), normal((4, 12, N), 8, "bf16")
+    ids = make_ids(T, 4, "mixed", 9)
+    y2, wide_y2 = padded(N, 10, 8)
+    binding.gemm_relu_adapters(x, w[0], a, b, ids, y=y2)
+    ref.check(y2, ref.adapters(x, w[0], a, b, ids, None, True, "kn"), "adapters")
+    binding.check_device_error()
+    for wide, left, width in ((wide_y, 8, N), (wide_dx, 16, K), (wide_y2, 8, N)):
+        assert torch.isnan(wide[:, :left]).all() and torch.isnan(wide[:, left + width:]).all()
+
+
+def test_sums_of_nothing_and_of_one():
+    """No group, no reduction, no row: zeros; outputs of stale memory are overwritten."""
+    K, N = 64, 72
+    x, w = normal((5, K), 1, "f16"), weights(2, K, N, "kn", 2, "f16", 0.1)
+    y = torch.full((5, N), 9.0, dtype=torch.float16, device=DEV)
+    binding.gemm_relu_grouped(x, w[:0], offsets_of([]), y=y)
+    assert (y == 0).all()
+    y.fill_(9)
+    binding.gemm_relu_grouped(x[:, :0], w[:, :0].contiguous(), offsets_of([2, 3]), y=y)
+    assert (y == 0).all()
+    dw = torch.full((2, K, N), 9.0, dtype=torch.float16, device=DEV)
+    binding.gemm_relu_grouped_dw(x[:0], y[:0], offsets_of([0, 0]), dw=dw)
+    assert (dw == 0).all()
+    dw.fill_(9)
+    binding.gemm_relu_grouped_dw(x, y, offsets_of([0, 0]), dw=dw)
+    assert (dw == 0).all()
+    assert binding.gemm_relu_grouped(x[:0], w, offsets_of([0, 0])).shape == (0, N)
+    binding.check_device_error()
+
+
+def test_every_group_count():
+    """As many groups as a call takes, one row each but for a few."""
+    G, K, N = 1024, 64, 64
+    rs = np.random.RandomState(0)
+    for sizes in (rs.randint(0, 3, G), rs.randint(0, 2, G) * 0, np.eye(1, G, 700, dtype=int)[0] * 150,
+                  rs.randint(0, 300, G)):
+        T = int(sizes.sum()) + 2
+        off = offsets_of(sizes)
+        x, dy, w = normal((T, K), 1, "f16"), normal((T, N), 2, "f16"), weights(G, K, N, "kn", 3, "f16", 0.1)
+        ref.check(binding.gemm_relu_grouped(x, w, off), ref.grouped(x, w, off, True, "kn"), "y")
+        ref.check(binding.gemm_relu_grouped_dw(x, dy, off), ref.grouped_dw(x, dy, off, "kn"), "dw")
+        binding.check_device_error()
+
+
+def _differences(f, t, h, picks, rs):
+    """Central differences of the scalar f() in a few entries of t (float64)."""
+    out = []
+    flat = t.view(-1)
+    for i in rs.choice(flat.numel(), picks, replace=False):
+        v = flat[i].item()
+        flat[i] = v + h
+        up = f()
+        flat[i] = v - h
+        down = f()
+        flat[i] = v
+        out.append((int(i), (up - down) / (2 * h)))
+    return out
+
+
+def test_gradients_against_differences():
+    """dx (through the ReLU below) and dw of L = sum(c * y), y = x w, x =
+    ReLU(z), against central differences of L in 64 bits.  L is linear in w and
+    piecewise linear in z, so a difference is exact up to rounding where z is
+    further from 0 than the step."""
+    rs = np.random.RandomState(3)
+    T, K, N, sizes = 37, 64, 72, [5, 0, 20, 11]
+    off = offsets_of(sizes)
+    z = normal((T, K), 1, "f16")
+    z[z.abs() < 2.0 ** -6] = 0.25
+    x, w, c = torch.relu(z), weights(4, K, N, "kn", 2, "f16", 0.1), normal((T, N), 3, "f16")
+    dx = binding.gemm_relu_grouped_dx(c, w, off, act=x).double().cpu().view(-1)
+    dw = binding.gemm_relu_grouped_dw(x, c, off).double().cpu().view(-1)
+    binding.check_device_error()
+    z64, w64, c64 = z.double().cpu(), w.double().cpu(), c.double().cpu()
+    bounds = ref.bounds_of(off, T)
+
+    def loss():
+        x64 = torch.relu(z64)
+        return sum(float((c64[lo:hi] * (x64[lo:hi] @ w64[g])).sum()) for g, (lo, hi) in enumerate(bounds))
+
+    _, bx = ref.grouped_dx(c, w, off, x, "kn")
+    _, bw = ref.grouped_dw(x, c, off, "kn")
+    h = 2.0 ** -8
+    slack = 64 * T * N * K * 2.0 ** -53 / h  # rounding of the two sums, of terms of order one
+    for i, d in _differences(loss, z64, h, 60, rs):
+        assert abs(d - dx[i].item()) <= bx.reshape(-1)[i] + slack
+    for i, d in _differences(loss, w64, h, 60, rs):
+        assert abs(d - dw[i].item()) <= bw.reshape(-1)[i] + slack
+
+
+def test_two_streams_and_a_graph():
+    """Calls on two streams at once keep apart; a captured sequence replays on
+    new inputs and offsets in the same buffers."""
+    T, K, N, R, rank = 300, 264, 520, 6, 16
+    w = weights(5, K, N, "kn", 1, "bf16", K ** -0.5)
+    a, b = normal((R, rank, K), 2, "bf16", K ** -0.5), normal((R, rank, N), 3, "bf16", rank ** -0.5)
+
+    def inputs(seed):
+        rs = np.random.RandomState(seed)
+        sizes = rs.multinomial(T - 3, np.ones(5) / 5)
+        return normal((T, K), seed, "bf16"), normal((T, N), seed + 1, "bf16"), offsets_of(sizes, 1), make_ids(T, R, "mixed", seed)
+
+    def run(x, dy, off, ids):
+        return (binding.gemm_relu_grouped(x, w, off), binding.gemm_relu_grouped_dx(dy, w, off, act=x),
+                binding.gemm_relu_grouped_dw(x, dy, off), binding.gemm_relu_adapters(x, w[0], a, b, ids),
+                binding.gemm_relu_adapters(x[:40], w[0], a, b, ids[:40].contiguous()))
+
+    def check(out, x, dy, off, ids, what):
+        ref.check(out[0], ref.grouped(x, w, off, True, "kn"), what)
+        ref.check(out[1], ref.grouped_dx(dy, w, off, x, "kn"), what)
+        ref.check(out[2], ref.grouped_dw(x, dy, off, "kn"), what)
+        ref.check(out[3], ref.adapters(x, w[0], a, b, ids, None, True, "kn"), what)
+        ref.check(out[4], ref.adapters(x[:40], w[0], a, b, ids[:40], None, True, "kn"), what)
+
+    sets = [inputs(10), inputs(20)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[], []]
+    for _ in range(3):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                outs[i].append(run(*sets[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o in outs[i]:
+            check(o, *sets[i], f"stream {i}")
+            assert all(torch.equal(p, q) for p, q in zip(o, outs[i][0]))
+    held = [t.clone() for t in sets[0]]
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        run(*held)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            out = run(*held)
+    for new in (sets[1], sets[0], inputs(30)):
+        for t, n in zip(held, new):
+            t.copy_(n)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        check(out, *new, "replay")
+    binding.check_device_error()
+
+
+def test_results_do_not_change_from_run_to_run():
+    for T, G in ((40, 6), (3000, 9)):
+        K, N = 392, 520
+        rs = np.random.RandomState(T)
+        off = offsets_of(rs.multinomial(T, np.ones(G) / G))
+        x, dy, w = normal((T, K), 1, "f16"), normal((T, N), 2, "f16"), weights(G, K, N, "nk", 3, "f16", K ** -0.5)
+        a, b, ids = normal((7, 24, K), 4, "f16", K ** -0.5), normal((7, 24, N), 5, "f16"), make_ids(T, 7, "mixed", 6)
+        runs = [(binding.gemm_relu_grouped(x, w, off, b_layout="nk"), binding.gemm_relu_grouped_dx(dy, w, off, b_layout="nk"),
+                 binding.gemm_relu_grouped_dw(x, dy, off, b_layout="nk"),
+                 binding.gemm_relu_adapters(x, w[0], a, b, ids, b_layout="nk")) for _ in range(5)]
+        for r in runs[1:]:
+            assert all(torch.equal(p, q) for p, q in zip(r, runs[0]))
+
+
+def test_results_past_32_bit_offsets():
+    """Outputs and weights of more than 2^32 bytes and 2^31 elements: the last
+    rows of Y and the last expert, against those rows alone."""
+    K, N, T = 64, 4096, (1 << 31) // 4096 + 300
+    w = weights(3, K, N, "kn", 1, "f16", K ** -0.5)
+    off = torch.tensor([0, 5, T - 200, T], dtype=torch.int32, device=DEV)
+    x = torch.randn(T, K, generator=torch.Generator(device=DEV).manual_seed(2), device=DEV).half()
+    y = binding.gemm_relu_grouped(x, w, off)
+    binding.check_device_error()
+    tail = x[T - 400:].contiguous()
+    ref.check(y[T - 400:], ref.grouped(tail, w, torch.tensor([0, 0, 200, 400]), True, "kn"), "tail")
+    ref.check(y[:8], ref.grouped(x[:8].contiguous(), w, torch.tensor([0, 5, 8, 8]), True, "kn"), "head")
+    del y, x
+    G, K, N = 600, 1024, 4096  # 2.5e9 elements of weights
+    w = torch.zeros((G, K, N), dtype=torch.float16, device=DEV)
+    w[-1] = normal((K, N), 3, "f16", K ** -0.5)
+    x = normal((40, K), 4, "f16")
+    off = torch.zeros(G + 1, dtype=torch.int32, device=DEV)
+    off[-1] = 40
+    y = binding.gemm_relu_grouped(x, w, off)
+    ref.check(y, ref.grouped(x, w[-1:], torch.tensor([0, 40]), True, "kn"), "last expert")
+    dw = binding.gemm_relu_grouped_dw(x, y, off, dw=w)
+    ref.check(dw[-1:], ref.grouped_dw(x, y, torch.tensor([0, 40]), "kn"), "last gradient")
+    assert not dw[:-1].any()
+    binding.check_device_error()
+
+
+def test_example_block():
+    """The example's block, forward and backward, against plain 64-bit torch
+    with autograd; the library's outputs that are rounded on the way (h, u, z,
+    dz, du) set the tolerance: their unit roundoff, a few times over."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "expert_block.py")
+    spec = importlib.util.spec_from_file_location("expert_block", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    for T in (6, 300):
+        block = mod.ExpertBlock(136, 264, 8, 2, 4, 8, dtype=torch.float16, device=DEV, seed=T)
+        x, dy = normal((T, 136), 1, "f16"), normal((T, 136), 2, "f16")
+        ids = make_ids(T, 4, "mixed", 3)
+        y, kept = block.forward(x, ids)
+        dh, d_up, d_down = block.backward(dy, kept)
+        binding.check_device_error()
+        row, offsets, weight, rows, u, _ = kept
+        h = torch.zeros((T, 136), dtype=torch.float64, device=DEV)
+        h[row] = rows.double()
+        h.requires_grad_()
+        up, down = block.up.double().requires_grad_(), block.down.double().requires_grad_()
+        out = torch.zeros((T, 136), dtype=torch.float64, device=DEV)
+        for g, (lo, hi) in enumerate(ref.bounds_of(offsets, 2 * T)):
+            z = torch.relu(h[row[lo:hi]] @ up[g]) @ down[g]
+            out = out.index_add(0, row[lo:hi], z * weight[lo:hi, None].double())
+        out.backward(dy.double())
+        for got, want in ((y, out.detach()), (dh, h.grad), (d_up, up.grad), (d_down, down.grad)):
+            off = (got.double() - want).norm() / want.norm()
+            assert off < 8 * 2.0 ** -11, float(off)

@@ -230,6 +230,8 @@ static int run_forward(const void* X, const void* W, void* Y, const int32_t* off
     StreamBuffers& sb = rt::buffers_for_locked(d, st);
     if (ad) {
         p.ids = ad->ids;
+        p.B = reinterpret_cast<const uint16_t*>(ad->B);
+        p.rank = (int32_t)ad->rank;
         p.R = (int32_t)ad->R;
         p.rank_box = pl.rank_box;
         p.rank_pad = pl.rank_pad;
@@ -277,7 +279,6 @@ static int run_forward(const void* X, const void* W, void* Y, const int32_t* off
             if (rc != GEMM_OK) return rc;
             p.low_out = reinterpret_cast<uint16_t*>(base);
             p.scale = ad->scale;
-            p.rank = (int32_t)ad->rank;
         } else {
             rc = run_low(X, *ad, reinterpret_cast<uint16_t*>(base), T, N, K, ldx, pl, bf16, d, st);
             if (rc != GEMM_OK) return rc;

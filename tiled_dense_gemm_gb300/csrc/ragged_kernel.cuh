@@ -46,6 +46,7 @@ constexpr uint32_t kEpiThreads = 128;
 constexpr uint32_t kEpiBarrier = 1;
 constexpr int kBK = 128;       // k-rows per ring stage: eight MMAs per wait and commit
 constexpr int kMaxStages = 8;
+constexpr int kMaxBoxes = 2048;  // adapters: boxes of rank_box rows of a row tile's second factors (256 x 512 / 64)
 constexpr int kTokBoxes = 8;   // row-tile boxes of 16, 32, ..., 128 rows per CTA
 constexpr int kXK = 64;        // adapters: products of the rank per extra k-block, each in two parts
 constexpr int kRaster = 8;     // row tiles of one group walked together, column tile by column tile
@@ -98,6 +99,7 @@ struct Params {
     const uint16_t* low;     // (T, 2, rank_pad): scale * x A^T, in two parts of the element type
     const int32_t* nslots;   // distinct adapters of each row tile; null: single CTAs, which list them themselves
     const int32_t* slots;    // [tile][cap] their indexes
+    const uint16_t* B;       // second factors (R, rank, N)
     int32_t rank, rank_pad, rank_box, b4d, a4d;  // rank_box: 8, 16, 32 or 64; rank_pad a multiple of it
     int32_t box_shift;       // rank_box = 1 << box_shift
     int32_t per_slot;        // rank_pad / rank_box
@@ -115,6 +117,8 @@ struct __align__(8) Ctrl {
     uint64_t final_bar;
     uint64_t extra[kMaxStages];  // adapters: the stage is free for an extra k-block
     uint64_t peer[kMaxStages];   // ... and, of a pair's leader, filled by the peer
+    uint32_t sick[kMaxBoxes / 32];  // adapters: boxes of the item's second factors that are not finite
+    int32_t checked;                // ... items whose boxes have been looked at
     uint32_t tmem_addr;
     int32_t abort_flag;
     int32_t ring_s, ring_ph, ring_lap;
@@ -148,6 +152,21 @@ __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, Ctrl
             atomicCAS(p.err, 0, (int32_t)kErrEpi);
             return false;
         }
+    return true;
+}
+
+// The same until a counter in shared memory has reached a value.
+__device__ __forceinline__ bool wait_counter(int32_t* counter, int32_t value, Ctrl* ctrl, const Params& p) {
+    volatile int32_t* const c = counter;
+    volatile int32_t* abort_flag = &ctrl->abort_flag;
+    const uint64_t t0 = globaltimer_ns();
+    while (*c < value)
+        if (*abort_flag || globaltimer_ns() - t0 > p.timeout_ns) {
+            *abort_flag = 1;
+            atomicCAS(p.err, 0, (int32_t)kErrWeights);
+            return false;
+        }
+    __threadfence_block();
     return true;
 }
 
@@ -411,6 +430,12 @@ __device__ __forceinline__ uint32_t rest16x2(float x, float y, uint32_t hi, int3
     return pack16(isfinite(back.x) ? x - back.x : 0.0f, isfinite(back.y) ? y - back.y : 0.0f, bf16);
 }
 
+// v[at] += x for an index that is not a constant (the array stays in registers).
+__device__ __forceinline__ void add_at(float (&v)[32], int at, float x) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] += j == at ? x : 0.0f;
+}
+
 // A pair of 16-bit floats, each +0 where its gate is not positive (sign set,
 // zero or NaN), as unsigned compares of the gate's words.
 __device__ __forceinline__ uint32_t gate16(uint32_t x, uint32_t gate, int32_t bf16) {
@@ -453,6 +478,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
         mbar_init(smem_u32(&ctrl->final_bar), 1);
         ctrl->abort_flag = 0;
         ctrl->ring_s = ctrl->ring_ph = ctrl->ring_lap = 0;
+        ctrl->checked = 0;
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -648,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
         // ------------------------------------------------------------ weights
         uint32_t s = 0, ph = 0;
         bool ok = true;
-        while (ok && iter.next(it)) {
+        for (int32_t items = 1; ok && iter.next(it); ++items) {
             const int32_t n0 = it.n * (kPair ? 256 : 128) + 128 * (int32_t)rank;
             for (int32_t j = 0; ok && j < segments(it); ++j) {
             int32_t kb_first, kb_end, e_first, e_end;
@@ -720,6 +746,10 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
             if constexpr (kAdapters) {
                 const int32_t slots = nslots[it.tile];
                 const int32_t per = kXK >> p.box_shift;
+                if (j == 0 && e_first < e_end) {
+                    ok = wait_counter(&ctrl->checked, items, ctrl, p);
+                    ok = __all_sync(0xffffffffu, ok);
+                }
                 for (int32_t e = e_first; ok && e < e_end; ++e) {
                     ok = wait_phase(empty0 + 8u * s, ph ^ 1u, ctrl, p, kErrWeights);
                     ok = __all_sync(0xffffffffu, ok);
@@ -729,8 +759,10 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                     if ((int32_t)lane < pieces_of(slots, e)) {
                         const int32_t piece = e * per + (int32_t)lane;
                         const int32_t slot = slot_of(p, piece);
-                        // (past the last adapter: a box of zeros, beyond the tensor)
-                        const int32_t id = slot < slots ? slot_list[(int64_t)it.tile * p.cap + slot] : p.R;
+                        // (past the last adapter, and in place of a box that
+                        // is not finite: a box of zeros, beyond the tensor)
+                        const bool sick = ((*(volatile uint32_t*)&ctrl->sick[piece >> 5] >> (piece & 31)) & 1u) != 0;
+                        const int32_t id = slot < slots && !sick ? slot_list[(int64_t)it.tile * p.cap + slot] : p.R;
                         const int32_t row = (piece - slot * p.per_slot) * p.rank_box;
                         const uint32_t dst = ring + s * stride + lane * (uint32_t)p.rank_box * 256u;
                         if (p.b4d) {
@@ -878,6 +910,73 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
         const uint32_t et = threadIdx.x - 64;
         uint32_t pos = 0;  // adapters: ring stages before the item's extra ones
         uint32_t extra_ph = 0;  // ... and the phase of each stage's `extra` barrier
+        // Adapters: look at the second factors that the item's extra k-blocks
+        // will multiply.  A row's columns of other adapters are zeros there,
+        // and zero times an infinity or NaN is not zero: a box that is not
+        // finite is kept out of the MMAs (the copies put zeros in its place)
+        // and its own rows get its products from the epilogue, so that one
+        // adapter's broken weights stay in its rows.  These warps have
+        // nothing else to do while the main k-blocks run, and what they read
+        // is in L2 when the copies come for it.
+        bool any_sick = false;
+        auto check_boxes = [&]() {
+            any_sick = false;
+            if (it.x0 < it.x1) {
+                const int32_t slots = nslots[it.tile], per = kXK >> p.box_shift;
+                const int32_t b0 = it.x0 * per, b1 = min(it.x1 * per, slots * p.per_slot);
+                for (int32_t i = (b0 >> 5) + (int32_t)et; i <= (b1 - 1) >> 5; i += (int32_t)kEpiThreads) ctrl->sick[i] = 0u;
+                named_bar_sync(kEpiBarrier, kEpiThreads);
+                const int32_t n = it.n * (kPair ? 256 : 128) + 128 * (int32_t)rank + 8 * (int32_t)(et & 15u);
+                const uint32_t inf = p.bf16 ? 0x7F807F80u : 0x7C007C00u;
+                bool sick = false;
+                // 16 threads per row of 128 columns, 8 rows apart, 4 rows per thread at a time
+                const int32_t rows = (b1 - b0) << p.box_shift;
+                for (int32_t r = (int32_t)(et >> 4); n < p.N && r < rows; r += 32) {
+                    uint4 q[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int32_t row = r + 8 * i, box = b0 + (row >> p.box_shift), slot = slot_of(p, box);
+                        const int32_t j = (box - slot * p.per_slot) * p.rank_box + (row & (p.rank_box - 1));
+                        q[i] = row < rows && j < p.rank
+                                   ? __ldg(reinterpret_cast<const uint4*>(
+                                         p.B + ((int64_t)slot_list[(int64_t)it.tile * p.cap + slot] * p.rank + j) * p.N + n))
+                                   : make_uint4(0, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t bad = __vcmpeq2(q[i].x & inf, inf) | __vcmpeq2(q[i].y & inf, inf) |
+                                             __vcmpeq2(q[i].z & inf, inf) | __vcmpeq2(q[i].w & inf, inf);
+                        if (bad) {
+                            const int32_t box = b0 + ((r + 8 * i) >> p.box_shift);
+                            atomicOr(&ctrl->sick[box >> 5], 1u << (box & 31));
+                            sick = true;
+                        }
+                    }
+                }
+                any_sick = !named_bar_and(kEpiBarrier, kEpiThreads, !sick);
+            }
+            __threadfence_block();
+            if (et == 0) *(volatile int32_t*)&ctrl->checked = (int32_t)local + 1;
+        };
+        // The products of the boxes kept out, for one of their own rows: what
+        // row t's low-rank part is to have in column n besides.
+        auto sick_part = [&](int32_t t, int32_t n) {
+            float sum = 0.0f;
+            const int32_t his = t < it.row0 + it.valid && n < p.N ? __ldcg(p.ids + t) : -2, per = kXK >> p.box_shift;
+            for (int32_t box = it.x0 * per; his >= 0 && box < min(it.x1 * per, nslots[it.tile] * p.per_slot); ++box) {
+                if (((ctrl->sick[box >> 5] >> (box & 31)) & 1u) == 0) continue;
+                const int32_t slot = slot_of(p, box), j0 = (box - slot * p.per_slot) * p.rank_box;
+                if (slot_list[(int64_t)it.tile * p.cap + slot] != his) continue;
+                const uint16_t* low = p.low + (int64_t)t * 2 * p.rank_pad;
+                for (int32_t j = j0; j < min(j0 + p.rank_box, p.rank); ++j) {
+                    const float2 b = unpack16(p.B[((int64_t)his * p.rank + j) * p.N + n], p.bf16);
+                    const float2 hi = unpack16(__ldcg(low + j), p.bf16), rest = unpack16(__ldcg(low + p.rank_pad + j), p.bf16);
+                    sum = fmaf(hi.x, b.x, sum);
+                    if (rest.x != 0.0f) sum = fmaf(rest.x, b.x, sum);  // (0 x inf would be NaN)
+                }
+            }
+            return sum;
+        };
         // Adapters: fill and arm an item's extra k-blocks.  A row tile's
         // low-rank products, each row only in its own adapter's columns: 64
         // columns of hi, then of lo.  Thread = 16-byte vector (8 columns) of
@@ -1086,6 +1185,9 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                 for (int32_t c = 0; c < it.w; c += 32) {
                     __syncwarp();
                     tmem_load_32cols(taddr + c, v);
+                    if (kAdapters && any_sick)
+#pragma unroll 1
+                        for (int j = 0; j < 32; ++j) add_at(v, j, sick_part(it.row0 + c + j, it.n * 128 + (int32_t)lane_row));
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         if (c + j < it.w) st_shared_f32(ring + (uint32_t)((c + j) * 128 + (int32_t)lane_row) * 4u, v[j]);
@@ -1109,6 +1211,12 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                 }
                 __syncwarp();  // (also: the last chunk's shared-memory reads are done)
                 tmem_load_fragments(taddr + c, v);
+                if (kAdapters && any_sick)
+#pragma unroll 1
+                    for (int j = 0; j < 32; ++j)
+                        add_at(v, j, sick_part(it.row0 + c + 8 * ((j >> 2) & 3) + 2 * (int32_t)(lane & 3u) + (j & 1),
+                                               n - 8 * (int32_t)(lane & 3u) + 16 * (j >> 4) + 8 * ((j >> 1) & 1) +
+                                                   (int32_t)(lane >> 2)));
                 if (p.apply_relu) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = v[j] > 0.0f ? v[j] : 0.0f;  // -0 and NaN become +0
@@ -1140,30 +1248,11 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
             release();
             return true;
         };
-        if (kAdapters && !kPair && lane == 0) {
-            // few rows: a stage of an extra k-block holds half the weights of
-            // a main one, too little in flight for DRAM's latency; these
-            // warps, idle so far, ask L2 for them ahead (first items only)
-            It ahead(iter);
-            Item a;
-            for (int i = 0; i < 2 && ahead.next(a); ++i) {
-                const int32_t slots = nslots[a.tile];
-                const int32_t per = kXK >> p.box_shift;
-                const int32_t end = min(a.x1 * per, slots * p.per_slot);
-                for (int32_t piece = a.x0 * per + (int32_t)quarter; piece < end; piece += 4) {
-                    const int32_t slot = slot_of(p, piece), row = (piece - slot * p.per_slot) * p.rank_box;
-                    if (p.b4d) {
-                        prefetch_4d(&maps.b, 0, row, a.n * 2, slot_list[slot]);
-                    } else {
-                        prefetch_3d(&maps.b, a.n * 128, row, slot_list[slot]);
-                        prefetch_3d(&maps.b, a.n * 128 + 64, row, slot_list[slot]);
-                    }
-                }
-            }
-        }
-        __syncwarp();
         for (bool ok = true; ok && iter.next(it); ++local) {
-            if (kAdapters) ok = fill_extras();
+            if (kAdapters) {
+                check_boxes();
+                ok = fill_extras();
+            }
             if (ok) ok = drain(it, local);
         }
         // rows of no group: before the first group and past the last one
