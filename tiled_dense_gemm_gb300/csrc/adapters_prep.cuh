@@ -34,7 +34,6 @@ struct LowParams {
     int32_t slot_step;   // CTAs that share a row block's adapters
     int32_t passes;      // CTAs that share a rank (8 * kNT products each)
     int32_t k_split;     // CTAs (a cluster) that share a reduction
-    int32_t early;       // the main kernel starts beside this one
     int32_t* err;
 };
 
@@ -121,17 +120,17 @@ __device__ __forceinline__ uint4 load_or_zero(const uint16_t* src, bool in) {
 // per job; the warps, and the CTAs of a cluster where jobs are few, split K.
 //
 // This product is a few percent of the main one's operations and all
-// latency: where it reads little, it runs beside the main kernel (which starts
-// while it runs and needs low only for its last k-blocks) in the registers
-// and shared memory that kernel leaves, which rules out TMEM and a TMA ring;
-// warp-level MMAs with operands straight from global memory fit.  The order of k inside an
+// latency: it runs beside the main kernel (which starts while it runs and
+// needs low only for its last k-blocks) in the registers and shared memory
+// that kernel leaves, which rules out TMEM and a TMA ring; warp-level MMAs
+// with operands straight from global memory fit.  The order of k inside an
 // MMA does not matter as long as both operands agree, so each thread loads
 // 16 contiguous bytes of its row and feeds two MMAs with them.
 template <int kNT>
 __global__ void __launch_bounds__(kLowWarps * 32, 2) adapters_low_kernel(const __grid_constant__ LowParams p) {
     __shared__ float part[kLowWarps / 2][kNT * 4 * 32];
     grid_dependency_wait();
-    if (p.early) grid_launch_dependents();
+    grid_launch_dependents();
     const int32_t warp = (int32_t)threadIdx.x / 32, lane = (int32_t)threadIdx.x % 32;
     const int32_t g = lane >> 2, tig = lane & 3;
     const int32_t rank = p.k_split > 1 ? (int32_t)cluster_ctarank() : 0;
@@ -168,6 +167,13 @@ __global__ void __launch_bounds__(kLowWarps * 32, 2) adapters_low_kernel(const _
         const uint16_t* x0 = p.X + (int64_t)(in0 ? row0 + g : row0) * p.ldx;
         const uint16_t* x1 = p.X + (int64_t)(in1 ? row0 + g + 8 : row0) * p.ldx;
         const uint16_t* a = p.A + ((int64_t)id * p.rank + j0 + g) * p.K;
+        // all of it to L2 first, ahead of the main kernel's copies
+        for (int32_t i = (int32_t)threadIdx.x; i < kNT * 8 * (p.K + 63) / 64; i += kLowWarps * 32) {
+            const int32_t chunk = i / (kNT * 8), row = i % (kNT * 8), k = chunk * 64;
+            // (chunks of 64 k that this CTA of the cluster reads)
+            if (k / (kLowWarps * 32 * kU) % p.k_split == rank && j0 + row < p.rank)
+                prefetch_line(p.A + ((int64_t)id * p.rank + j0 + row) * p.K + k);
+        }
         for (int32_t kw = kw0; kw < p.K; kw += kw_step) {
             uint4 xv[kU][2], av[kU][kNT];
 #pragma unroll
@@ -188,7 +194,6 @@ __global__ void __launch_bounds__(kLowWarps * 32, 2) adapters_low_kernel(const _
                     mma_16816(acc[n], xv[u][0].z, xv[u][1].z, xv[u][0].w, xv[u][1].w, av[u][n].z, av[u][n].w, p.bf16);
                 }
         }
-        if (!p.early && firsts == 0) grid_launch_dependents();
         const float scale = p.scale ? __ldcg(p.scale + id) : 1.0f;
         // sum over the warps: halves in turn, in a fixed order
 #pragma unroll

@@ -139,7 +139,7 @@ struct Adapters {
 };
 
 // low for up to kLowRows rows, beside the main kernel.
-static int run_low(const void* X, const Adapters& ad, uint16_t* low, int64_t T, int64_t N, int64_t K, int64_t ldx,
+static int run_low(const void* X, const Adapters& ad, uint16_t* low, int64_t T, int64_t K, int64_t ldx,
                    const RaggedPlan& pl, bool bf16, DeviceState& d, cudaStream_t st) {
     int rc;
     LowParams q;
@@ -162,16 +162,10 @@ static int run_low(const void* X, const Adapters& ad, uint16_t* low, int64_t T, 
     const int nt = pl.rank_box / 8;
     q.passes = pl.rank_pad / pl.rank_box;
     const int64_t jobs = (T + 15) / 16 * q.slot_step * q.passes;
-    // Beside the main kernel where it reads little: the main kernel's deep
-    // queues of copies starve it of DRAM (48 adapters of rank 32 at K = N =
-    // 8192: low took 32 us beside it, 13 us before it).  Then that kernel starts
-    // when low's loads are in.
-    q.early = std::min(T, ad.R) * ad.rank * 64 <= N ? 1 : 0;
     // few jobs share each reduction between the CTAs of a cluster (one CTA
     // per multiprocessor leaves room there for one of the main kernel)
-    const int64_t room = q.early ? d.sm_count : 2 * (int64_t)d.sm_count;
     q.k_split = 1;
-    while (q.k_split < 8 && jobs * q.k_split * 2 <= room && K > 256 * q.k_split) q.k_split *= 2;
+    while (q.k_split < 8 && jobs * q.k_split * 2 <= d.sm_count && K > 256 * q.k_split) q.k_split *= 2;
     auto fn = nt == 8   ? adapters_low_kernel<8>
               : nt == 4 ? adapters_low_kernel<4>
               : nt == 2 ? adapters_low_kernel<2>
@@ -280,7 +274,7 @@ static int run_forward(const void* X, const void* W, void* Y, const int32_t* off
             p.low_out = reinterpret_cast<uint16_t*>(base);
             p.scale = ad->scale;
         } else {
-            rc = run_low(X, *ad, reinterpret_cast<uint16_t*>(base), T, N, K, ldx, pl, bf16, d, st);
+            rc = run_low(X, *ad, reinterpret_cast<uint16_t*>(base), T, K, ldx, pl, bf16, d, st);
             if (rc != GEMM_OK) return rc;
         }
     }

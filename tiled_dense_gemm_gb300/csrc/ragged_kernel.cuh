@@ -582,29 +582,6 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
         if (!kPair || rank == 0) mbar_arrive_expect_tx(full, bytes);
     };
 
-    // The order of an item's k-blocks.  Pairs: all main ones, then the extra
-    // ones.  Single CTAs (few rows): the last main ones in turn with the extra
-    // ones, which wait for latencies and not for DRAM.  Segment j holds main
-    // blocks [k0, k1), then extra ones [e0, e1).
-    auto mains_until = [&](const Item& i, int32_t j) {  // main blocks before extra one j
-        const int32_t n = i.kb1 - i.kb0;
-        return kPair ? n : min(n, max(0, n - (i.x1 - i.x0)) + j + 1);
-    };
-    auto segments = [&](const Item& i) { return kPair || !kAdapters ? 1 : max(1, i.x1 - i.x0); };
-    auto segment = [&](const Item& i, int32_t j, int32_t& k0, int32_t& k1, int32_t& e0, int32_t& e1) {
-        if (kPair || !kAdapters || i.x1 <= i.x0) {
-            k0 = i.kb0;
-            k1 = i.kb1;
-            e0 = i.x0;
-            e1 = i.x1;
-        } else {
-            k0 = i.kb0 + (j > 0 ? mains_until(i, j - 1) : 0);
-            k1 = i.kb0 + mains_until(i, j);
-            e0 = i.x0 + j;
-            e1 = e0 + 1;
-        }
-    };
-
     if (warp == 0) {
         // ---------------------------------------------------------- row tiles
         if (lane == 0) {
@@ -621,10 +598,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                                            p.rank_box) * 256u + 2u * rows * (uint32_t)(kBK * 2);
                 }
                 const CUtensorMap* m = &maps.x[rows / 16 - 1];
-                for (int32_t j = 0; ok && j < segments(it); ++j) {
-                int32_t k0, k1, e0, e1;
-                segment(it, j, k0, k1, e0, e1);
-                for (int32_t kb = k0; kb < k1; ++kb) {
+                for (int32_t kb = it.kb0; kb < it.kb1; ++kb) {
                     if (!wait_phase(empty0 + 8u * s, ph ^ 1u, ctrl, p, kErrTokens)) {
                         ok = false;
                         break;
@@ -649,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                     // the epilogue's warps fill and arm the extra k-blocks;
                     // this thread, which is never more than a lap ahead of
                     // the MMAs, tells them when a stage is free
-                    for (int32_t e = e0; ok && e < e1; ++e) {
+                    for (int32_t e = it.x0; ok && e < it.x1; ++e) {
                         ok = wait_phase(empty0 + 8u * s, ph ^ 1u, ctrl, p, kErrTokens);
                         if (!ok) break;
                         mbar_arrive(smem_u32(&ctrl->extra[s]));
@@ -659,7 +633,6 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                             ph ^= 1u;
                         }
                     }
-                }
                 }
             }
             if (!kPair || rank == 0) {
@@ -676,10 +649,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
         bool ok = true;
         for (int32_t items = 1; ok && iter.next(it); ++items) {
             const int32_t n0 = it.n * (kPair ? 256 : 128) + 128 * (int32_t)rank;
-            for (int32_t j = 0; ok && j < segments(it); ++j) {
-            int32_t kb_first, kb_end, e_first, e_end;
-            segment(it, j, kb_first, kb_end, e_first, e_end);
-            const int32_t n_main = kb_end - kb_first;
+            const int32_t n_main = it.kb1 - it.kb0;
             if (kPair && kAdapters && it.low) {
                 // first factors of the tile's adapters, 128 rows per CTA; a
                 // lane per box of rank_box rows x 64 k
@@ -712,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                 }
             } else if (lane == 0) {
                 uint32_t ls = s, lph = ph;
-                for (int32_t kb = kb_first; kb < kb_end; ++kb) {
+                for (int32_t kb = it.kb0; kb < it.kb1; ++kb) {
                     if (!wait_phase(empty0 + 8u * ls, lph ^ 1u, ctrl, p, kErrWeights)) {
                         ok = false;
                         break;
@@ -746,11 +716,11 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
             if constexpr (kAdapters) {
                 const int32_t slots = nslots[it.tile];
                 const int32_t per = kXK >> p.box_shift;
-                if (j == 0 && e_first < e_end) {
+                if (ok && it.x0 < it.x1) {
                     ok = wait_counter(&ctrl->checked, items, ctrl, p);
                     ok = __all_sync(0xffffffffu, ok);
                 }
-                for (int32_t e = e_first; ok && e < e_end; ++e) {
+                for (int32_t e = it.x0; ok && e < it.x1; ++e) {
                     ok = wait_phase(empty0 + 8u * s, ph ^ 1u, ctrl, p, kErrWeights);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
@@ -778,7 +748,6 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                         ph ^= 1u;
                     }
                 }
-            }
             }
         }
         __syncwarp();
@@ -813,8 +782,8 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                 const uint32_t half16 = ((uint32_t)it.w / (kPair ? 2u : 1u)) * 128u >> 4;  // second 64 k of the rows
                 uint32_t acc = 0;
                 // the k-blocks; weights from `a_first`, k-step k at offset(k)
-                auto main_blocks = [&](int32_t kb, int32_t kb_end, uint64_t a_first, uint32_t idesc, auto offset) {
-                    for (; kb < kb_end; ++kb) {
+                auto main_blocks = [&](uint64_t a_first, uint32_t idesc, auto offset) {
+                    for (int32_t kb = it.kb0; kb < it.kb1; ++kb) {
                         if (!wait_phase(full0 + 8u * s, ph, ctrl, p, kErrStage)) {
                             ok = false;
                             break;
@@ -834,16 +803,14 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                         }
                     }
                 };
-                for (int32_t j = 0; ok && j < segments(it); ++j) {
-                int32_t k0, k1, e0, e1;
-                segment(it, j, k0, k1, e0, e1);
                 if (kPair && kAdapters && it.low) {
                     // (one box: the MMA's rows past it read what lies there, into lanes that nothing reads)
                     const uint32_t sub16 =
                         (low_boxes(p, nslots[it.tile]) == 1 ? (uint32_t)p.rank_box : 128u) * 128u >> 4;
-                    main_blocks(k0, k1, a_desc_k, idesc_k | nbits, [=](uint32_t k) { return (k / 4) * sub16 + (k % 4) * 2u; });
-                } else
-                    main_blocks(k0, k1, a_desc0, idesc0 | nbits, [&](uint32_t k) { return a_off[k]; });
+                    main_blocks(a_desc_k, idesc_k | nbits, [=](uint32_t k) { return (k / 4) * sub16 + (k % 4) * 2u; });
+                } else {
+                    main_blocks(a_desc0, idesc0 | nbits, [&](uint32_t k) { return a_off[k]; });
+                }
                 if constexpr (kAdapters) {
                     const int32_t slots = nslots[it.tile];
                     const uint32_t box = (uint32_t)p.rank_box;
@@ -851,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                     // chunks; boxes of 8 rows pair up to an MMA's 16
                     const uint64_t x_desc0 = box == 8 ? make_sw128_desc(ring, 1024, 2048)
                                                       : make_sw128_desc(ring, box * 128u, 1024);
-                    for (int32_t e = e0; ok && e < e1; ++e) {
+                    for (int32_t e = it.x0; ok && e < it.x1; ++e) {
                         if (!wait_phase(full0 + 8u * s, ph, ctrl, p, kErrStage)) {
                             ok = false;
                             break;
@@ -882,7 +849,6 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                             ph ^= 1u;
                         }
                     }
-                }
                 }
                 if (!ok) break;
                 mma_commit<kCG>(tfull0 + 8u * buf, 0x3);
@@ -926,24 +892,33 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                 const int32_t b0 = it.x0 * per, b1 = min(it.x1 * per, slots * p.per_slot);
                 for (int32_t i = (b0 >> 5) + (int32_t)et; i <= (b1 - 1) >> 5; i += (int32_t)kEpiThreads) ctrl->sick[i] = 0u;
                 named_bar_sync(kEpiBarrier, kEpiThreads);
-                const int32_t n = it.n * (kPair ? 256 : 128) + 128 * (int32_t)rank + 8 * (int32_t)(et & 15u);
+                const int32_t n0 = it.n * (kPair ? 256 : 128) + 128 * (int32_t)rank;
                 const uint32_t inf = p.bf16 ? 0x7F807F80u : 0x7C007C00u;
                 bool sick = false;
-                // 16 threads per row of 128 columns, 8 rows apart, 4 rows per thread at a time
+                // row r of the item's boxes at column n, or null
                 const int32_t rows = (b1 - b0) << p.box_shift;
-                for (int32_t r = (int32_t)(et >> 4); n < p.N && r < rows; r += 32) {
-                    uint4 q[4];
+                auto row_of = [&](int32_t r, int32_t n) -> const uint16_t* {
+                    const int32_t box = b0 + (r >> p.box_shift), slot = slot_of(p, box);
+                    const int32_t j = ((box - slot * p.per_slot) << p.box_shift) + (r & (p.rank_box - 1));
+                    if (n >= p.N || r >= rows || j >= p.rank) return nullptr;
+                    return p.B + ((int64_t)slot_list[(int64_t)it.tile * p.cap + slot] * p.rank + j) * p.N + n;
+                };
+                // few rows: first to L2 all at once, before the main k-blocks'
+                // copies fill DRAM's queues (a thread per row, two lines)
+                if (!kPair)
+                    for (int32_t r = (int32_t)et; r < rows; r += (int32_t)kEpiThreads)
+                        for (int32_t c = 0; c < 128; c += 64)
+                            if (const uint16_t* q = row_of(r, n0 + c)) prefetch_line(q);
+                // 16 threads per row, 8 rows apart
+                for (int32_t r = (int32_t)(et >> 4); r < rows; r += 64) {
+                    uint4 q[8];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int32_t row = r + 8 * i, box = b0 + (row >> p.box_shift), slot = slot_of(p, box);
-                        const int32_t j = (box - slot * p.per_slot) * p.rank_box + (row & (p.rank_box - 1));
-                        q[i] = row < rows && j < p.rank
-                                   ? __ldg(reinterpret_cast<const uint4*>(
-                                         p.B + ((int64_t)slot_list[(int64_t)it.tile * p.cap + slot] * p.rank + j) * p.N + n))
-                                   : make_uint4(0, 0, 0, 0);
+                    for (int i = 0; i < 8; ++i) {
+                        const uint16_t* from = row_of(r + 8 * i, n0 + 8 * (int32_t)(et & 15u));
+                        q[i] = from ? __ldg(reinterpret_cast<const uint4*>(from)) : make_uint4(0, 0, 0, 0);
                     }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < 8; ++i) {
                         const uint32_t bad = __vcmpeq2(q[i].x & inf, inf) | __vcmpeq2(q[i].y & inf, inf) |
                                              __vcmpeq2(q[i].z & inf, inf) | __vcmpeq2(q[i].w & inf, inf);
                         if (bad) {
@@ -986,12 +961,8 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
         auto fill_extras = [&]() {
             const int32_t slots = nslots[it.tile];
             const int32_t e0 = it.x0, e1 = it.x1;
-            // ring stages before extra block e
-            auto stage_of = [&](int32_t e) { return pos + (uint32_t)(mains_until(it, e - e0) + e - e0); };
-            if (e0 >= e1) {
-                pos += (uint32_t)(it.kb1 - it.kb0);
-                return true;
-            }
+            pos += (uint32_t)(it.kb1 - it.kb0);
+            if (e0 >= e1) return true;
             const uint32_t rows = (uint32_t)it.w / (kPair ? 2u : 1u);
             const int32_t y = it.row0 + (int32_t)(rank * rows);
             bool ok = true;     // (alike in all threads)
@@ -1026,12 +997,12 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                 }
             }
             // Blocks in flight: stage e + S - 2 is free while the MMAs work
-            // on block e - 1, in time for e (in turn with main ones: half).
-            const int32_t ahead = max(0, min(3, ((int32_t)S - 2) / (kPair ? 1 : 2)));
+            // on block e - 1, in time for e.
+            const int32_t ahead = max(0, min(3, (int32_t)S - 2));
             int32_t issued = e0;
             for (int32_t e = e0; ok && e < e1; ++e) {
                 for (; issued < e1 && issued <= e + ahead; ++issued) {
-                    const uint32_t st = stage_of(issued) % S;
+                    const uint32_t st = (pos + (uint32_t)(issued - e0)) % S;
                     ok = wait_phase(smem_u32(&ctrl->extra[st]), (extra_ph >> st) & 1u, ctrl, p, kErrTokens);
                     extra_ph ^= 1u << st;
                     ok = named_bar_and(kEpiBarrier, kEpiThreads, ok);
@@ -1069,7 +1040,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                 fence_proxy_async_smem();
                 named_bar_sync(kEpiBarrier, kEpiThreads);
                 if (et == 0) {
-                    const uint32_t st = stage_of(e) % S;
+                    const uint32_t st = (pos + (uint32_t)(e - e0)) % S;
                     if (kPair && rank != 0) {
                         mbar_arrive_cluster(mapa_shared(smem_u32(&ctrl->peer[st]), 0));
                     } else {
@@ -1082,7 +1053,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                     }
                 }
             }
-            pos += (uint32_t)(it.kb1 - it.kb0 + e1 - e0);
+            pos += (uint32_t)(e1 - e0);
             return named_bar_and(kEpiBarrier, kEpiThreads, ok && armed);
         };
         // the item whose accumulator is the CTA's `local`-th; false: aborting

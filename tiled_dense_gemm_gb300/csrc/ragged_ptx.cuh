@@ -58,19 +58,9 @@ __device__ __forceinline__ void load_4d(uint32_t dst, const CUtensorMap* m, uint
             : "memory");
 }
 
-// L2 prefetches of the box that a copy at the same place would read.
-__device__ __forceinline__ void prefetch_3d(const CUtensorMap* m, int32_t x, int32_t y, int32_t z) {
-    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
-                     reinterpret_cast<uint64_t>(m)),
-                 "r"(x), "r"(y), "r"(z)
-                 : "memory");
-}
-
-__device__ __forceinline__ void prefetch_4d(const CUtensorMap* m, int32_t x, int32_t y, int32_t z, int32_t w) {
-    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
-                     reinterpret_cast<uint64_t>(m)),
-                 "r"(x), "r"(y), "r"(z), "r"(w)
-                 : "memory");
+// L2 prefetch of the line that holds an address.
+__device__ __forceinline__ void prefetch_line(const void* p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
 // Asynchronous 16-byte copy global -> shared; `bytes` (0 or 16) are read, the
