@@ -141,7 +141,9 @@ int gemm_relu_host(const void* A_host, const void* B_host, void* C_host,
  * that the wait for that k-block runs out and the launch ends with the
  * error recorded (its C is incomplete).  A k outside [0, number of
  * k-blocks of the plan) or a plan that runs in clusters is refused with
- * GEMM_ERR_INVALID_ARG.
+ * GEMM_ERR_INVALID_ARG.  The grouped products take the hook too where their
+ * plans are of single CTAs without clusters (gemm_relu_grouped_dw: k = 0, the
+ * first row block).
  */
 int gemm_relu_check_device_error(void* stream);
 
@@ -275,8 +277,10 @@ int gemm_relu_grouped_dw(const void* X, const void* dY, void* dW, const int32_t*
  * X, W, Y, pitches, types, alignment and stream as gemm_relu_grouped with one
  * W.  A row depends on its own adapter only, whatever the others hold.
  *
- * scale * (X A^T) is accumulated and scaled in fp32 and rounded once to
- * `dtype` before it meets B; the rest is accumulated in fp32 and rounded once.
+ * scale * (X A^T) is accumulated and scaled in fp32 and meets B as two numbers
+ * of `dtype`, the rounded value and the rounded rest (together 2^-16 of it in
+ * bfloat16, 2^-22 in binary16; with binary16 it has to stay within that type's
+ * range); everything else is accumulated in fp32 and rounded once.
  * An id outside [-1, R) counts as -1 and is reported as GEMM_ERR_INDEX by
  * the next gemm_relu_check_device_error.
  */

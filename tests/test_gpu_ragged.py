@@ -542,3 +542,57 @@ def test_example_block():
         for got, want in ((y, out.detach()), (dh, h.grad), (d_up, up.grad), (d_down, down.grad)):
             off = (got.double() - want).norm() / want.norm()
             assert off < 8 * 2.0 ** -11, float(off)
+
+
+# Bounded waits, by the library's own hook: the copy of one block of rows is
+# left out, so a wait of the kernel runs out after a millisecond.  The sizes
+# give plans of single CTAs without clusters.
+HOOKED = {
+    "grouped 0": (0, lambda x, w, g, off: binding.gemm_relu_grouped(x, w, off),
+                  lambda x, w, g, off: ref.grouped(x, w, off, True, "kn")),
+    "grouped 2": (2, lambda x, w, g, off: binding.gemm_relu_grouped(x, w, off),
+                  lambda x, w, g, off: ref.grouped(x, w, off, True, "kn")),
+    "dw 0": (0, lambda x, w, g, off: binding.gemm_relu_grouped_dw(x, g, off),
+             lambda x, w, g, off: ref.grouped_dw(x, g, off, "kn")),
+}
+
+
+@pytest.mark.parametrize("what", list(HOOKED))
+def test_timed_out_wait_is_reported_and_the_next_call_is_correct(what, monkeypatch):
+    kb, call, want = HOOKED[what]
+    sizes, K, N = [7, 0, 15, 8, 10], 512, 2048 if kb or "dw" not in what else 256
+    off = offsets_of(sizes)
+    x, w = normal((sum(sizes), K), 1, "f16"), weights(5, K, N, "kn", 2, "f16", K ** -0.5)
+    g = normal((sum(sizes), N), 3, "f16")
+    monkeypatch.setenv("GEMM_RELU_TEST_DROP_KB", str(kb))
+    call(x, w, g, off)
+    with pytest.raises(binding.GemmReluError) as e:
+        binding.check_device_error()
+    assert e.value.status == 6  # GEMM_ERR_TIMEOUT
+    monkeypatch.delenv("GEMM_RELU_TEST_DROP_KB")
+    binding.check_device_error()
+    for _ in range(2):
+        y = call(x, w, g, off)
+        binding.check_device_error()
+        ref.check(y, want(x, w, g, off), what)
+
+
+def test_the_hook_is_refused_where_it_does_not_apply(monkeypatch):
+    def refused(call):
+        with pytest.raises(binding.GemmReluError) as e:
+            call()
+        assert e.value.status == 1  # GEMM_ERR_INVALID_ARG
+
+    x, w = normal((40, 512), 1, "f16"), weights(5, 512, 2048, "kn", 2, "f16", 0.05)
+    off = offsets_of([7, 0, 15, 8, 10])
+    monkeypatch.setenv("GEMM_RELU_TEST_DROP_KB", "4")  # K = 512: k-blocks 0 .. 3
+    refused(lambda: binding.gemm_relu_grouped(x, w, off))
+    monkeypatch.setenv("GEMM_RELU_TEST_DROP_KB", "0")
+    # clusters; pairs; adapters
+    refused(lambda: binding.gemm_relu_grouped(x, w[:, :, :128].contiguous(), off))
+    refused(lambda: binding.gemm_relu_grouped(normal((400, 512), 1, "f16"), w, offsets_of([100, 0, 100, 200, 0])))
+    refused(lambda: binding.gemm_relu_adapters(
+        x, w[0], normal((2, 8, 512), 1, "f16"), normal((2, 8, 2048), 1, "f16"),
+        torch.zeros(40, dtype=torch.int32, device=DEV)))
+    monkeypatch.delenv("GEMM_RELU_TEST_DROP_KB")
+    binding.check_device_error()

@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+#include <stdlib.h>
 #include <string.h>
 
 #include <algorithm>
@@ -131,6 +132,18 @@ static int zero_rows(void* y, int64_t ld, int64_t width, int64_t rows, cudaStrea
     return GEMM_OK;
 }
 
+// The test hook of the bounded waits (GEMM_RELU_TEST_DROP_KB=k): plans of
+// single CTAs, without clusters and with a k-block k, take it; others refuse.
+static int test_hook(bool single, int32_t blocks, int32_t* drop, uint64_t* timeout_ns) {
+    const char* text = getenv("GEMM_RELU_TEST_DROP_KB");
+    if (!text || !*text) return GEMM_OK;
+    const long kb = strtol(text, nullptr, 10);
+    if (kb < 0 || kb >= blocks || !single) return GEMM_ERR_INVALID_ARG;
+    *drop = (int32_t)kb + 1;
+    *timeout_ns = 1000000;  // 1 ms
+    return GEMM_OK;
+}
+
 struct Adapters {
     const void *A, *B;
     const int32_t* ids;
@@ -213,9 +226,11 @@ static int run_forward(const void* X, const void* W, void* Y, const int32_t* off
     p.ld_act = ld_act;
     p.err = d.d_err;
     p.timeout_ns = 2000000000ull + 2000ull * (uint64_t)pl.num_kb;
+    int rc = test_hook(!pl.pair && pl.cluster == 1 && !ad, pl.num_kb, &p.test_drop_kb, &p.timeout_ns);
+    if (rc != GEMM_OK) return rc;
     // weights: K-major, 128 rows x 64 k; else 128 k-rows x 64 columns
-    int rc = w_kmajor ? encode_stack(&m.w, W, (uint64_t)K, (uint64_t)N, (uint64_t)G, 128, p.w4d, bf16)
-                      : encode_stack(&m.w, W, (uint64_t)N, (uint64_t)K, (uint64_t)G, kBK, p.w4d, bf16);
+    rc = w_kmajor ? encode_stack(&m.w, W, (uint64_t)K, (uint64_t)N, (uint64_t)G, 128, p.w4d, bf16)
+                  : encode_stack(&m.w, W, (uint64_t)N, (uint64_t)K, (uint64_t)G, kBK, p.w4d, bf16);
     const int boxes = pl.cap / (pl.pair ? 2 : 1) / 16;
     for (int i = 0; rc == GEMM_OK && i < boxes; ++i)
         rc = encode_rows(&m.x[i], X, (uint64_t)K, (uint64_t)T, (uint64_t)ldx, 16u * (uint32_t)(i + 1),
@@ -307,7 +322,9 @@ static int run_dw(const void* U, const void* V, void* D, const int32_t* offsets,
     memset(&q, 0, sizeof(q));
     q.u3d = P % 64 == 0;
     q.v3d = Q % 64 == 0;
-    int rc = encode_rows(&base.u, U, (uint64_t)P, (uint64_t)T, (uint64_t)ldu, kBK, q.u3d ? 2 : 0, bf16);
+    q.timeout_ns = 2000000000ull + 2000ull * (uint64_t)((T + kBK - 1) / kBK);
+    int rc = test_hook(!pl.pair, 1, &q.test_drop_kb, &q.timeout_ns);
+    if (rc == GEMM_OK) rc = encode_rows(&base.u, U, (uint64_t)P, (uint64_t)T, (uint64_t)ldu, kBK, q.u3d ? 2 : 0, bf16);
     if (rc == GEMM_OK)
         rc = encode_rows(&base.v, V, (uint64_t)Q, (uint64_t)T, (uint64_t)ldv, kBK, q.v3d ? 2 : 0, bf16);
     if (rc == GEMM_OK) rc = encode_stack(&out.d, D, (uint64_t)Q, (uint64_t)P, (uint64_t)G, 32, false, bf16);
@@ -333,7 +350,6 @@ static int run_dw(const void* U, const void* V, void* D, const int32_t* offsets,
     q.groups = groups;
     q.maps = maps;
     q.err = d.d_err;
-    q.timeout_ns = 2000000000ull + 2000ull * (uint64_t)((T + kBK - 1) / kBK);
     if (pl.pair) {
         if ((rc = allow_smem(d, 4, ragged_dw_kernel<true>)) != GEMM_OK) return rc;
         return launch(ragged_dw_kernel<true>, pl.grid, kDwThreads, (size_t)pl.smem_bytes, 2, st, out, q);

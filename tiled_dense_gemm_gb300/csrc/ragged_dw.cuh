@@ -47,6 +47,7 @@ struct DwParams {
     const CUtensorMap* maps;    // [2 * position]: U's and V's of that group
     int32_t* err;
     uint64_t timeout_ns;
+    int32_t test_drop_kb;  // as of the forward kernel: a block of U's rows
 };
 
 struct DwPrepMaps {
@@ -207,7 +208,9 @@ __global__ void __launch_bounds__(kDwThreads, 1)
                     const uint32_t bar = kPair ? mapa_shared(full, 0) : full;
                     const uint32_t dst = ring + s * stride + (is_u ? 0u : kOperand);
                     const CUtensorMap* const m = k.hi - r < kBK ? last : is_u ? &out.u : &out.v;
-                    if (is_u ? q.u3d : q.v3d) {
+                    if (!kPair && is_u && issued == q.test_drop_kb && q.test_drop_kb > 0) {
+                        // (test hook: not copied)
+                    } else if (is_u ? q.u3d : q.v3d) {
                         load_3d<kPair>(dst, m, bar, 0, r, c0 / 64);
                     } else {
                         load_2d<kPair>(dst, m, bar, c0, r);

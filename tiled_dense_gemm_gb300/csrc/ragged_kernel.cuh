@@ -94,6 +94,11 @@ struct Params {
     int64_t ld_act;
     int32_t* err;            // err[0] timed-out waits, err[1] bad index arrays
     uint64_t timeout_ns;
+    // test hook of the bounded waits, 0 in every normal call: k + 1 leaves the
+    // row copy of k-block k of each CTA's first item undone (its stage is
+    // still armed for the bytes); the host pairs it with a short timeout_ns
+    // and plans of single CTAs
+    int32_t test_drop_kb;
     // adapters
     const int32_t* ids;      // adapter of each row, -1 none
     const uint16_t* low;     // (T, 2, rank_pad): scale * x A^T, in two parts of the element type
@@ -607,7 +612,9 @@ __global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room fo
                     arm(full, bytes);
                     const uint32_t dst = ring + s * stride + kWBytes;
                     const uint32_t bar = kPair ? mapa_shared(full, 0) : full;
-                    if (p.x3d) {
+                    if (!kPair && kb == p.test_drop_kb - 1 && pos == (uint32_t)(kb - it.kb0)) {
+                        // (test hook: not copied)
+                    } else if (p.x3d) {
                         load_3d<kPair>(dst, m, bar, 0, y, kb * (kBK / 64));
                     } else {
                         load_2d<kPair>(dst, m, bar, kb * kBK, y);
