@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kLowWarps * 32, 2) adapters_low_kernel(const _
         const uint16_t* x1 = p.X + (int64_t)(in1 ? row0 + g + 8 : row0) * p.ldx;
         const uint16_t* a = p.A + ((int64_t)id * p.rank + j0 + g) * p.K;
         // all of it to L2 first, ahead of the main kernel's copies
-        for (int32_t i = (int32_t)threadIdx.x; i < kNT * 8 * (p.K + 63) / 64; i += kLowWarps * 32) {
+        for (int32_t i = (int32_t)threadIdx.x; i < kNT * 8 * ((p.K + 63) / 64); i += kLowWarps * 32) {
             const int32_t chunk = i / (kNT * 8), row = i % (kNT * 8), k = chunk * 64;
             // (chunks of 64 k that this CTA of the cluster reads)
             if (k / (kLowWarps * 32 * kU) % p.k_split == rank && j0 + row < p.rank)
