@@ -26,9 +26,29 @@
 // through distributed shared memory.
 //
 // Roles (224 threads, one CTA per SM): warp 0 copies row tiles, warp 6 the
-// weights, warp 1 issues the MMAs, warps 2-5
-// drain the accumulators; shared-memory ring of 128-k stages, two TMEM
-// accumulators.  Every wait is bounded.
+// weights, warp 1 issues the MMAs, warps 2-5 drain the accumulators;
+// shared-memory ring of 128-k stages, two TMEM accumulators.  Every wait is
+// bounded.  The epilogue turns D^T round in shared memory (each warp its own
+// 32 x 32 blocks), applies the ReLU or the gate in 32 bits or on the rounded
+// value, and rounds once, to the output's type.
+//
+// What bounds it, and what it measured (bfloat16 or binary16, launches one
+// after another, inputs beyond L2):
+//   few rows per group: the weights' way from DRAM.  64 groups of 4096 x
+//     2048, 256 rows: 152-154 us, 7.0 TB/s.
+//   many: bytes into the multiprocessors.  A pair takes 256 x (rows of the
+//     tile) products per k from L2, and tiles of ragged groups are narrower
+//     than 256: 32 groups of 2048 x 4096, 16384 rows: 187-189 us, 1460
+//     TFLOP/s, with 14.6 TB/s from L2 (159 us with the weights' copies left
+//     out, 157 us with the MMAs left out: neither hides the other wholly).
+//     Stages of 64 k (six of them) instead of 128 (three): 197 us.
+//   row pitches that are not multiples of 128 bytes cost a second copy per
+//     stage and operand and a second line per row: 5000 rows, 12 groups of
+//     2056 x 3000, 66 us.
+//   rows with adapters: as above, and the second factors and the low-rank
+//     products in extra k-blocks at the end of each tile, ~0.6-1.8 us each
+//     (8192 rows, 24 of 32 adapters of rank 64, 4096 x 4096: 205 us, of which
+//     ~150 us are the shared product's).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -267,9 +287,9 @@ __device__ __forceinline__ int32_t slot_of(const Params& p, int32_t box) {
 // Low items compute the low-rank products of a row tile, boxes of rank_box of
 // them at a time: one box per CTA of the pair where the tile has at most two,
 // or boxes are large (64), which takes one copy per stage; else as many as
-// the MMA's 128 rows hold, at two copies per box (copies issue one after
-// another, ~450 cycles each: four per stage made an item of 32 stages 33 us,
-// one makes it TODO).
+// the MMA's 128 rows hold, at two copies per box.  (Copies issue one after
+// another, ~450 cycles each: with four per stage an item of 32 stages took
+// 33 us, most of it waiting for them.)
 __device__ __forceinline__ int32_t low_boxes(const Params& p, int32_t slots) {
     return p.rank_box == 64 || slots * p.per_slot <= 2 ? 1 : 128 >> p.box_shift;
 }
@@ -453,7 +473,7 @@ __device__ __forceinline__ uint32_t gate16(uint32_t x, uint32_t gate, int32_t bf
 // ------------------------------------------------------------------ kernel
 
 template <bool kPair, bool kAdapters>
-__global__ void __launch_bounds__(kThreads, 2)  // 144 registers: leaves room for a block of the adapters' low kernel
+__global__ void __launch_bounds__(kThreads, 2)  // at most 144 registers: room for a block of the adapters' low kernel
     ragged_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
     constexpr int kCG = kPair ? 2 : 1;
     using It = Iter<kPair, kAdapters>;
