@@ -361,13 +361,16 @@ struct Iter {
         step = workers;
     }
 
-    // rows of tile j of the cnt of group g: equal widths, in the MMA's steps
+    // rows of tile j of the cnt of group g: equal widths, in the MMA's steps,
+    // but the last only as wide as what is left for it (32 groups of 512 rows
+    // on average: 4% fewer columns of MMA work than with all equal)
     __device__ __forceinline__ void row_tile(Item& it, int32_t g, int32_t cnt, int32_t j) {
         const int32_t s0 = start[g], len = start[g + 1] - s0;
         constexpr int32_t kGran = kPair ? 32 : 16;
         it.w = ((len + cnt - 1) / cnt + kGran - 1) / kGran * kGran;
         it.row0 = s0 + j * it.w;
         it.valid = min(it.w, len - j * it.w);
+        it.w = (it.valid + kGran - 1) / kGran * kGran;
     }
 
     __device__ __forceinline__ bool next(Item& it) {
