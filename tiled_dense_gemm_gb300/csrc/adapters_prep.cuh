@@ -31,6 +31,7 @@ struct LowParams {
     uint16_t* low;       // (T, 2, rank_pad): hi, lo
     int64_t ldx;
     int32_t T, K, R, rank, rank_pad, bf16;
+    int32_t wide;        // rows of X and A start on 32 bytes
     int32_t slot_step;   // CTAs that share a row block's adapters
     int32_t passes;      // CTAs that share a rank (8 * kNT products each)
     int32_t k_split;     // CTAs (a cluster) that share a reduction
@@ -103,6 +104,23 @@ __device__ __forceinline__ float ld_shared_cluster(uint32_t addr) {
     return v;
 }
 
+// 32 bytes from global memory: in one load where addresses allow it (a whole
+// line for the four lanes of a row: half the requests), else in two.
+__device__ __forceinline__ void load_32(uint4 (&q)[2], const uint16_t* src, bool wide) {
+    if (wide)
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(q[0].x), "=r"(q[0].y), "=r"(q[0].z), "=r"(q[0].w), "=r"(q[1].x), "=r"(q[1].y),
+                       "=r"(q[1].z), "=r"(q[1].w)
+                     : "l"(reinterpret_cast<uint64_t>(src)));
+    else
+        asm volatile(
+            "ld.global.v4.b32 {%0, %1, %2, %3}, [%8];\n\t"
+            "ld.global.v4.b32 {%4, %5, %6, %7}, [%8 + 16];"
+            : "=&r"(q[0].x), "=&r"(q[0].y), "=&r"(q[0].z), "=&r"(q[0].w), "=&r"(q[1].x), "=&r"(q[1].y),
+              "=&r"(q[1].z), "=&r"(q[1].w)
+            : "l"(reinterpret_cast<uint64_t>(src)));
+}
+
 // 16 bytes from global memory, or zeros, without a branch.
 __device__ __forceinline__ uint4 load_or_zero(const uint16_t* src, bool in) {
     uint4 q;
@@ -125,7 +143,7 @@ __device__ __forceinline__ uint4 load_or_zero(const uint16_t* src, bool in) {
 // that kernel leaves, which rules out TMEM and a TMA ring; warp-level MMAs
 // with operands straight from global memory fit.  The order of k inside an
 // MMA does not matter as long as both operands agree, so each thread loads
-// 16 contiguous bytes of its row and feeds two MMAs with them.
+// 32 contiguous bytes of its row and feeds four MMAs with them.
 //
 // Bound: DRAM, which it shares with the main kernel's weights.  64 rows with
 // 48 adapters of rank 32, 8192 x 8192: its 25 MB are in 32-38 us after the
@@ -144,10 +162,15 @@ __global__ void __launch_bounds__(kLowWarps * 32, 2) adapters_low_kernel(const _
     const int32_t job = (int32_t)blockIdx.x / p.k_split;
     const int32_t j0 = job % p.passes * 8 * kNT;  // first of the rank's products
     const int32_t y = job / p.passes % p.slot_step, row0 = job / p.passes / p.slot_step * 16;
-    // kU chunks of 32 k per warp in flight at once, side by side: one round
-    // trip to DRAM for each 256 x kU x k_split of K
-    constexpr int kU = kNT == 8 ? 2 : kNT == 4 ? 4 : 6;
-    const int32_t kw0 = (rank * kLowWarps + warp) * (32 * kU), kw_step = p.k_split * kLowWarps * (32 * kU);
+    // K in chunks of 64 (a line of each row), in turn with the other warps
+    // (and CTAs of the cluster).  kD of them are in flight while one is
+    // multiplied: what 128 registers hold without spilling, and with more a
+    // CTA of the main kernel no longer fits beside (64 rows, 48 adapters of
+    // rank 32, the whole call: 16 products per pass with two chunks 56 us, 32
+    // with two 59, with 136 registers 61).
+    constexpr int kD = kNT == 2 ? 2 : 4;
+    const uint32_t part_of = (uint32_t)(rank * kLowWarps + warp), parts = (uint32_t)(p.k_split * kLowWarps);
+    const uint32_t K = (uint32_t)p.K, whole = K / 64;
     // the block's distinct adapters, in each warp's registers: lane = row
     int32_t mine = -1;
     if (lane < 16 && row0 + lane < p.T) {
@@ -164,94 +187,125 @@ __global__ void __launch_bounds__(kLowWarps * 32, 2) adapters_low_kernel(const _
         firsts &= firsts - 1;
         if (s % p.slot_step != y) continue;
         const int32_t id = __shfl_sync(0xffffffffu, mine, src);
+        const float scale = p.scale ? __ldcg(p.scale + id) : 1.0f;
+        // Every product of the MMAs that is kept has its own row of X and its
+        // own row of A; the others (rows of other adapters, past the rank)
+        // read some row that exists and go nowhere.
+        const uint32_t his = __ballot_sync(0xffffffffu, lane < 16 && mine == id);
+        const uint16_t* const x0 = p.X + (int64_t)(row0 + ((his >> g) & 1u ? g : src)) * p.ldx + tig * 16;
+        const uint16_t* const x1 = p.X + (int64_t)(row0 + ((his >> (g + 8)) & 1u ? g + 8 : src)) * p.ldx + tig * 16;
+        const uint16_t* const a0 = p.A + (int64_t)id * p.rank * p.K + tig * 16;
+        auto a_row = [&](int n) { return a0 + (uint64_t)(uint32_t)min(j0 + n * 8 + g, p.rank - 1) * K; };
+        uint4 xv[kD][2][2], av[kD][kNT][2];
         float acc[kNT][4];
 #pragma unroll
         for (int n = 0; n < kNT; ++n)
 #pragma unroll
             for (int c = 0; c < 4; ++c) acc[n][c] = 0.0f;
-        // rows of other adapters are left out (their results are not kept)
-        const bool in0 = __shfl_sync(0xffffffffu, mine, g) == id, in1 = __shfl_sync(0xffffffffu, mine, g + 8) == id;
-        const uint16_t* x0 = p.X + (int64_t)(in0 ? row0 + g : row0) * p.ldx;
-        const uint16_t* x1 = p.X + (int64_t)(in1 ? row0 + g + 8 : row0) * p.ldx;
-        const uint16_t* a = p.A + ((int64_t)id * p.rank + j0 + g) * p.K;
-        // all of it to L2 first, ahead of the main kernel's copies
-        for (int32_t i = (int32_t)threadIdx.x; i < kNT * 8 * ((p.K + 63) / 64); i += kLowWarps * 32) {
-            const int32_t chunk = i / (kNT * 8), row = i % (kNT * 8), k = chunk * 64;
-            // (chunks of 64 k that this CTA of the cluster reads)
-            if (k / (kLowWarps * 32 * kU) % p.k_split == rank && j0 + row < p.rank)
-                prefetch_line(p.A + ((int64_t)id * p.rank + j0 + row) * p.K + k);
-        }
-        for (int32_t kw = kw0; kw < p.K; kw += kw_step) {
-            uint4 xv[kU][2], av[kU][kNT];
+        auto load = [&](int d, uint32_t c) {
 #pragma unroll
-            for (int u = 0; u < kU; ++u) {
-                const int32_t k = kw + u * 32 + tig * 8;
-                const bool in = k < p.K;
-                xv[u][0] = load_or_zero(x0 + k, in && in0);
-                xv[u][1] = load_or_zero(x1 + k, in && in1);
+            for (int n = 0; n < kNT; ++n) load_32(av[d][n], a_row(n) + 64ull * c, p.wide);
+            load_32(xv[d][0], x0 + 64ull * c, p.wide);
+            load_32(xv[d][1], x1 + 64ull * c, p.wide);
+        };
+        auto multiply = [&](int d) {
 #pragma unroll
-                for (int n = 0; n < kNT; ++n)
-                    av[u][n] = load_or_zero(a + (int64_t)n * 8 * p.K + k, in && j0 + n * 8 + g < p.rank);
-            }
-#pragma unroll
-            for (int u = 0; u < kU; ++u)
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int n = 0; n < kNT; ++n) {
-                    mma_16816(acc[n], xv[u][0].x, xv[u][1].x, xv[u][0].y, xv[u][1].y, av[u][n].x, av[u][n].y, p.bf16);
-                    mma_16816(acc[n], xv[u][0].z, xv[u][1].z, xv[u][0].w, xv[u][1].w, av[u][n].z, av[u][n].w, p.bf16);
+                    const uint4 &xa = xv[d][0][h], &xb = xv[d][1][h], &w = av[d][n][h];
+                    mma_16816(acc[n], xa.x, xb.x, xa.y, xb.y, w.x, w.y, p.bf16);
+                    mma_16816(acc[n], xa.z, xb.z, xa.w, xb.w, w.z, w.w, p.bf16);
                 }
+        };
+#pragma unroll
+        for (int d = 0; d < kD; ++d)
+            if (part_of + d * parts < whole) load(d, part_of + d * parts);
+        // what this warp reads later to L2 first, ahead of the main kernel's
+        // copies: a lane per row and line
+        for (uint32_t c = part_of + kD * parts; c < whole; c += parts)
+            for (int32_t r = lane; r < kNT * 8; r += 32)
+                if (j0 + r < p.rank) prefetch_line(p.A + ((int64_t)id * p.rank + j0 + r) * p.K + 64ull * c);
+        for (uint32_t c0 = part_of; c0 < whole; c0 += kD * parts)
+#pragma unroll
+            for (int d = 0; d < kD; ++d) {
+                const uint32_t c = c0 + d * parts;
+                if (c >= whole) break;
+                multiply(d);
+                if (c + kD * parts < whole) load(d, c + kD * parts);
+            }
+        if (K % 64 != 0 && whole % parts == part_of) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const bool in = whole * 64 + (uint32_t)(tig * 16 + 8 * h) < K;
+#pragma unroll
+                for (int n = 0; n < kNT; ++n) av[0][n][h] = load_or_zero(a_row(n) + 64ull * whole + 8 * h, in);
+                xv[0][0][h] = load_or_zero(x0 + 64ull * whole + 8 * h, in);
+                xv[0][1][h] = load_or_zero(x1 + 64ull * whole + 8 * h, in);
+            }
+            multiply(0);
         }
-        const float scale = p.scale ? __ldcg(p.scale + id) : 1.0f;
-        // sum over the warps: halves in turn, in a fixed order
-#pragma unroll
-        for (int half = kLowWarps / 2; half > 0; half /= 2) {
-            __syncthreads();
-            if (warp >= half && warp < 2 * half)
-#pragma unroll
-                for (int n = 0; n < kNT; ++n)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) part[warp - half][(n * 4 + c) * 32 + lane] = acc[n][c];
-            __syncthreads();
-            if (warp < half)
-#pragma unroll
-                for (int n = 0; n < kNT; ++n)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) acc[n][c] += part[warp][(n * 4 + c) * 32 + lane];
-        }
-        if (p.k_split > 1) {
-            // the cluster's sums, in rank order, by its first CTA
-            __syncthreads();
-            if (warp == 0 && rank != 0)
-#pragma unroll
-                for (int n = 0; n < kNT; ++n)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) part[0][(n * 4 + c) * 32 + lane] = acc[n][c];
-            cluster_sync();
-            if (warp == 0 && rank == 0)
-                for (int32_t r = 1; r < p.k_split; ++r) {
-                    const uint32_t from = mapa_shared(smem_u32(&part[0][lane]), (uint32_t)r);
-#pragma unroll
-                    for (int n = 0; n < kNT; ++n)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) acc[n][c] += ld_shared_cluster(from + (n * 4 + c) * 128u);
-                }
-            cluster_sync();  // its reads are done
-        }
-        if (warp == 0 && rank == 0) {
+        // Sums over the warps and the CTAs of the cluster, in a fixed order:
+        // warps 4-7 to warps 0-3, then a thread per element
+        __syncthreads();
+        if (warp >= kLowWarps / 2)
 #pragma unroll
             for (int n = 0; n < kNT; ++n)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (!(h ? in1 : in0)) continue;
-                    const int32_t j = j0 + n * 8 + tig * 2;
-                    // columns past the rank are zeros whatever the scale is
-                    const float v0 = j < p.rank ? acc[n][2 * h] * scale : 0.0f;
-                    const float v1 = j + 1 < p.rank ? acc[n][2 * h + 1] * scale : 0.0f;
-                    const uint32_t hi = pack16(v0, v1, p.bf16);
-                    uint16_t* dst = p.low + (int64_t)(row0 + 8 * h + g) * 2 * p.rank_pad + j;
-                    *reinterpret_cast<uint32_t*>(dst) = hi;
-                    *reinterpret_cast<uint32_t*>(dst + p.rank_pad) = rest16x2(v0, v1, hi, p.bf16);
+                for (int c = 0; c < 4; ++c) part[warp - kLowWarps / 2][(n * 4 + c) * 32 + lane] = acc[n][c];
+        __syncthreads();
+        if (warp < kLowWarps / 2)
+#pragma unroll
+            for (int n = 0; n < kNT; ++n)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) part[warp][(n * 4 + c) * 32 + lane] += acc[n][c];
+        __syncthreads();
+        constexpr int kE = (kNT * 128 + kLowWarps * 32 - 1) / (kLowWarps * 32);  // elements of a thread
+        float v[kE];
+#pragma unroll
+        for (int i = 0; i < kE; ++i) {
+            const int32_t e = (int32_t)threadIdx.x + i * kLowWarps * 32;
+            v[i] = 0.0f;
+            if (e < kNT * 128) v[i] = (part[0][e] + part[1][e]) + (part[2][e] + part[3][e]);
+        }
+        if (p.k_split > 1) {
+#pragma unroll
+            for (int i = 0; i < kE; ++i) {
+                const int32_t e = (int32_t)threadIdx.x + i * kLowWarps * 32;
+                if (e < kNT * 128) part[0][e] = v[i];
+            }
+            cluster_sync();
+            if (rank == 0) {
+#pragma unroll
+                for (int i = 0; i < kE; ++i) {
+                    const int32_t e = (int32_t)threadIdx.x + i * kLowWarps * 32;
+                    if (e >= kNT * 128) continue;
+                    const uint32_t at = smem_u32(&part[0][e]);
+                    float w[7];
+#pragma unroll
+                    for (int r = 1; r < 8; ++r) w[r - 1] = r < p.k_split ? ld_shared_cluster(mapa_shared(at, (uint32_t)r)) : 0.0f;
+#pragma unroll
+                    for (int r = 1; r < 8; ++r) v[i] += w[r - 1];
                 }
+            }
+            cluster_sync();  // its reads are done
+        }
+        if (rank == 0) {
+#pragma unroll
+            for (int i = 0; i < kE; ++i) {
+                const int32_t e = (int32_t)threadIdx.x + i * kLowWarps * 32;
+                if (e >= kNT * 128) continue;
+                // element (n, c, lane) of the fragments: its row, its product
+                const int32_t l = e & 31, c = (e >> 5) & 3, n = e >> 7;
+                const int32_t row = (l >> 2) + 8 * (c >> 1), j = j0 + n * 8 + (l & 3) * 2 + (c & 1);
+                if (((his >> row) & 1u) == 0) continue;
+                // columns past the rank are zeros whatever the scale is
+                const float low = j < p.rank ? v[i] * scale : 0.0f;
+                const uint32_t hi = pack16(low, 0.0f, p.bf16);
+                uint16_t* dst = p.low + (int64_t)(row0 + row) * 2 * p.rank_pad + j;
+                dst[0] = (uint16_t)hi;
+                dst[p.rank_pad] = (uint16_t)rest16x2(low, 0.0f, hi, p.bf16);
+            }
         }
     }
 }

@@ -132,6 +132,8 @@ static int zero_rows(void* y, int64_t ld, int64_t width, int64_t rows, cudaStrea
     return GEMM_OK;
 }
 
+static bool misaligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) != 0; }
+
 // The test hook of the bounded waits (GEMM_RELU_TEST_DROP_KB=k): plans of
 // single CTAs, without clusters and with a k-block k, take it; others refuse.
 static int test_hook(bool single, int32_t blocks, int32_t* drop, uint64_t* timeout_ns) {
@@ -169,23 +171,20 @@ static int run_low(const void* X, const Adapters& ad, uint16_t* low, int64_t T, 
     q.rank = (int32_t)ad.rank;
     q.rank_pad = pl.rank_pad;
     q.bf16 = bf16 ? 1 : 0;
+    q.wide = K % 16 == 0 && ldx % 16 == 0 && !misaligned(X, 32) && !misaligned(ad.A, 32);
     q.err = d.d_err;
     // a block's adapters are shared by as many CTAs as it can have
     q.slot_step = (int32_t)std::min<int64_t>({T <= 512 ? 16 : 2, T, ad.R});
-    const int nt = pl.rank_box / 8;
-    q.passes = pl.rank_pad / pl.rank_box;
+    const int nt = std::min(pl.rank_box / 8, 2);
+    q.passes = pl.rank_pad / (8 * nt);
     const int64_t jobs = (T + 15) / 16 * q.slot_step * q.passes;
     // few jobs share each reduction between the CTAs of a cluster (one CTA
     // per multiprocessor leaves room there for one of the main kernel)
-    q.k_split = 1;
-    while (q.k_split < 8 && jobs * q.k_split * 2 <= d.sm_count && K > 256 * q.k_split) q.k_split *= 2;
-    auto fn = nt == 8   ? adapters_low_kernel<8>
-              : nt == 4 ? adapters_low_kernel<4>
-              : nt == 2 ? adapters_low_kernel<2>
-                        : adapters_low_kernel<1>;
+    q.k_split = (int32_t)std::max<int64_t>(1, std::min<int64_t>({8, d.sm_count / jobs, (K + 255) / 256}));
+    auto fn = nt == 2 ? adapters_low_kernel<2> : adapters_low_kernel<1>;
     // the main kernel joins this one on its multiprocessors: the same split
     // between shared memory and L1
-    if ((rc = prefer_smem(d, nt == 8 ? 3 : nt / 2, fn)) != GEMM_OK) return rc;
+    if ((rc = prefer_smem(d, nt - 1, fn)) != GEMM_OK) return rc;
     return launch(fn, (int)jobs * q.k_split, kLowWarps * 32, 0, q.k_split, st, q);
 }
 
@@ -361,7 +360,6 @@ static int run_dw(const void* U, const void* V, void* D, const int32_t* offsets,
 // ------------------------------------------------------------------ checks
 
 static bool dim_ok(int64_t v) { return v >= 0 && v <= GEMM_RELU_MAX_DIM; }
-static bool misaligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) != 0; }
 
 // A row-pitched matrix argument of `width` columns.
 static int check_matrix(const void* ptr, int64_t width, int64_t ld) {

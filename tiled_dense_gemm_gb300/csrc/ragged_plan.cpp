@@ -11,7 +11,7 @@ constexpr int64_t kCtrl = 1024;
 constexpr int64_t kStageK = 128;       // k-rows per ring stage
 constexpr int64_t kTurn = 4 * 32 * 80; // the epilogue's transposition
 constexpr int64_t kLowRows = 1024;
-constexpr int64_t kLowSmem = 18 * 1024;
+constexpr int64_t kLowSmem = 6 * 1024;
 constexpr int64_t kIndexMax = 0x7fffffff;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }

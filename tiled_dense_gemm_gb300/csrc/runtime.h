@@ -54,7 +54,7 @@ struct DeviceState {
     int max_pairs = 0;  // co-resident CTA pairs of the paired kernel
     int32_t* d_err = nullptr;  // [0] timed-out waits, [1] bad values in an index array
     bool attr_set[6] = {false, false, false, false, false, false};  // per kernel mode
-    bool rg_carveout_set[4] = {};  // per kernel that runs beside a ragged one
+    bool rg_carveout_set[2] = {};  // per kernel that runs beside a ragged one
     bool rg_attr_set[6] = {};  // per ragged kernel
     std::vector<StreamBuffers> streams;
 };
