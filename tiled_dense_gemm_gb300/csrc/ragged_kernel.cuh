@@ -143,7 +143,7 @@ struct __align__(8) Ctrl {
     uint64_t extra[kMaxStages];  // adapters: the stage is free for an extra k-block
     uint64_t peer[kMaxStages];   // ... and, of a pair's leader, filled by the peer
     uint32_t sick[kMaxBoxes / 32];  // adapters: boxes of the item's second factors that are not finite
-    int32_t checked;                // ... items whose boxes have been looked at
+    uint64_t boxes[kMaxStages];     // ... landed in a stage
     uint32_t tmem_addr;
     int32_t abort_flag;
     int32_t ring_s, ring_ph, ring_lap;
@@ -177,21 +177,6 @@ __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, Ctrl
             atomicCAS(p.err, 0, (int32_t)kErrEpi);
             return false;
         }
-    return true;
-}
-
-// The same until a counter in shared memory has reached a value.
-__device__ __forceinline__ bool wait_counter(int32_t* counter, int32_t value, Ctrl* ctrl, const Params& p) {
-    volatile int32_t* const c = counter;
-    volatile int32_t* abort_flag = &ctrl->abort_flag;
-    const uint64_t t0 = globaltimer_ns();
-    while (*c < value)
-        if (*abort_flag || globaltimer_ns() - t0 > p.timeout_ns) {
-            *abort_flag = 1;
-            atomicCAS(p.err, 0, (int32_t)kErrWeights);
-            return false;
-        }
-    __threadfence_block();
     return true;
 }
 
@@ -498,6 +483,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // at most 144 registers: room f
             mbar_init(smem_u32(&ctrl->empty[s]), 1);
             mbar_init(smem_u32(&ctrl->extra[s]), 1);
             mbar_init(smem_u32(&ctrl->peer[s]), 1);
+            mbar_init(smem_u32(&ctrl->boxes[s]), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&ctrl->tmem_full[b]), 1);
@@ -506,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // at most 144 registers: room f
         mbar_init(smem_u32(&ctrl->final_bar), 1);
         ctrl->abort_flag = 0;
         ctrl->ring_s = ctrl->ring_ph = ctrl->ring_lap = 0;
-        ctrl->checked = 0;
+        for (int i = 0; i < kMaxBoxes / 32; ++i) ctrl->sick[i] = 0u;
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -677,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // at most 144 registers: room f
         // ------------------------------------------------------------ weights
         uint32_t s = 0, ph = 0;
         bool ok = true;
-        for (int32_t items = 1; ok && iter.next(it); ++items) {
+        while (ok && iter.next(it)) {
             const int32_t n0 = it.n * (kPair ? 256 : 128) + 128 * (int32_t)rank;
             const int32_t n_main = it.kb1 - it.kb0;
             if (kPair && kAdapters && it.low) {
@@ -721,7 +707,19 @@ __global__ void __launch_bounds__(kThreads, 2)  // at most 144 registers: room f
                     const uint32_t bar = kPair ? mapa_shared(full, 0) : full;
                     const uint32_t dst = ring + ls * stride;
                     const int32_t k0 = kb * kBK;
-                    if (p.w4d) {
+                    if constexpr (!kPair && kAdapters) {
+                        // read once: not to push the factors out of L2
+                        const uint64_t once = l2_policy_evict_first();
+                        if (p.w4d) {
+                            load_4d_hint(dst, &maps.w, bar, 0, p.w_kmajor ? n0 : k0, (p.w_kmajor ? k0 : n0) / 64, it.g, once);
+                        } else if (p.w_kmajor) {
+                            load_3d_hint(dst, &maps.w, bar, k0, n0, it.g, once);
+                            load_3d_hint(dst + 128u * 128u, &maps.w, bar, k0 + 64, n0, it.g, once);
+                        } else {
+                            load_3d_hint(dst, &maps.w, bar, n0, k0, it.g, once);
+                            load_3d_hint(dst + (uint32_t)kBK * 128u, &maps.w, bar, n0 + 64, k0, it.g, once);
+                        }
+                    } else if (p.w4d) {
                         if (p.w_kmajor)
                             load_4d<kPair>(dst, &maps.w, bar, 0, n0, k0 / 64, it.g);
                         else
@@ -746,30 +744,26 @@ __global__ void __launch_bounds__(kThreads, 2)  // at most 144 registers: room f
             if constexpr (kAdapters) {
                 const int32_t slots = nslots[it.tile];
                 const int32_t per = kXK >> p.box_shift;
-                if (ok && it.x0 < it.x1) {
-                    ok = wait_counter(&ctrl->checked, items, ctrl, p);
-                    ok = __all_sync(0xffffffffu, ok);
-                }
                 for (int32_t e = it.x0; ok && e < it.x1; ++e) {
                     ok = wait_phase(empty0 + 8u * s, ph ^ 1u, ctrl, p, kErrWeights);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
-                    const uint32_t full = full0 + 8u * s;
-                    const uint32_t bar = kPair ? mapa_shared(full, 0) : full;
-                    if ((int32_t)lane < pieces_of(slots, e)) {
+                    const uint32_t bar = smem_u32(&ctrl->boxes[s]);  // (this CTA's own, of a pair too)
+                    const int32_t pieces = pieces_of(slots, e);
+                    if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(pieces * p.rank_box) * 256u);
+                    __syncwarp();
+                    if ((int32_t)lane < pieces) {
                         const int32_t piece = e * per + (int32_t)lane;
                         const int32_t slot = slot_of(p, piece);
-                        // (past the last adapter, and in place of a box that
-                        // is not finite: a box of zeros, beyond the tensor)
-                        const bool sick = ((*(volatile uint32_t*)&ctrl->sick[piece >> 5] >> (piece & 31)) & 1u) != 0;
-                        const int32_t id = slot < slots && !sick ? slot_list[(int64_t)it.tile * p.cap + slot] : p.R;
+                        // (past the last adapter a box of zeros, beyond the tensor)
+                        const int32_t id = slot < slots ? slot_list[(int64_t)it.tile * p.cap + slot] : p.R;
                         const int32_t row = (piece - slot * p.per_slot) * p.rank_box;
                         const uint32_t dst = ring + s * stride + lane * (uint32_t)p.rank_box * 256u;
                         if (p.b4d) {
-                            load_4d<kPair>(dst, &maps.b, bar, 0, row, n0 / 64, id);
+                            load_4d<false>(dst, &maps.b, bar, 0, row, n0 / 64, id);
                         } else {
-                            load_3d<kPair>(dst, &maps.b, bar, n0, row, id);
-                            load_3d<kPair>(dst + (uint32_t)p.rank_box * 128u, &maps.b, bar, n0 + 64, row, id);
+                            load_3d<false>(dst, &maps.b, bar, n0, row, id);
+                            load_3d<false>(dst + (uint32_t)p.rank_box * 128u, &maps.b, bar, n0 + 64, row, id);
                         }
                     }
                     __syncwarp();
@@ -906,62 +900,65 @@ __global__ void __launch_bounds__(kThreads, 2)  // at most 144 registers: room f
         const uint32_t et = threadIdx.x - 64;
         uint32_t pos = 0;  // adapters: ring stages before the item's extra ones
         uint32_t extra_ph = 0;  // ... and the phase of each stage's `extra` barrier
-        // Adapters: look at the second factors that the item's extra k-blocks
-        // will multiply.  A row's columns of other adapters are zeros there,
-        // and zero times an infinity or NaN is not zero: a box that is not
-        // finite is kept out of the MMAs (the copies put zeros in its place)
-        // and its own rows get its products from the epilogue, so that one
-        // adapter's broken weights stay in its rows.  These warps have
-        // nothing else to do while the main k-blocks run, and what they read
-        // is in L2 when the copies come for it.
-        bool any_sick = false;
-        auto check_boxes = [&]() {
-            any_sick = false;
-            if (it.x0 < it.x1) {
-                const int32_t slots = nslots[it.tile], per = kXK >> p.box_shift;
-                const int32_t b0 = it.x0 * per, b1 = min(it.x1 * per, slots * p.per_slot);
-                for (int32_t i = (b0 >> 5) + (int32_t)et; i <= (b1 - 1) >> 5; i += (int32_t)kEpiThreads) ctrl->sick[i] = 0u;
-                named_bar_sync(kEpiBarrier, kEpiThreads);
-                const int32_t n0 = it.n * (kPair ? 256 : 128) + 128 * (int32_t)rank;
-                const uint32_t inf = p.bf16 ? 0x7F807F80u : 0x7C007C00u;
-                bool sick = false;
-                // row r of the item's boxes at column n, or null
-                const int32_t rows = (b1 - b0) << p.box_shift;
-                auto row_of = [&](int32_t r, int32_t n) -> const uint16_t* {
-                    const int32_t box = b0 + (r >> p.box_shift), slot = slot_of(p, box);
-                    const int32_t j = ((box - slot * p.per_slot) << p.box_shift) + (r & (p.rank_box - 1));
-                    if (n >= p.N || r >= rows || j >= p.rank) return nullptr;
-                    return p.B + ((int64_t)slot_list[(int64_t)it.tile * p.cap + slot] * p.rank + j) * p.N + n;
-                };
-                // few rows: first to L2 all at once, before the main k-blocks'
-                // copies fill DRAM's queues (a thread per row, two lines)
-                if (!kPair)
-                    for (int32_t r = (int32_t)et; r < rows; r += (int32_t)kEpiThreads)
-                        for (int32_t c = 0; c < 128; c += 64)
-                            if (const uint16_t* q = row_of(r, n0 + c)) prefetch_line(q);
-                // 16 threads per row, 8 rows apart
-                for (int32_t r = (int32_t)(et >> 4); r < rows; r += 64) {
-                    uint4 q[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint16_t* from = row_of(r + 8 * i, n0 + 8 * (int32_t)(et & 15u));
-                        q[i] = from ? __ldg(reinterpret_cast<const uint4*>(from)) : make_uint4(0, 0, 0, 0);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint32_t bad = __vcmpeq2(q[i].x & inf, inf) | __vcmpeq2(q[i].y & inf, inf) |
-                                             __vcmpeq2(q[i].z & inf, inf) | __vcmpeq2(q[i].w & inf, inf);
-                        if (bad) {
-                            const int32_t box = b0 + ((r + 8 * i) >> p.box_shift);
-                            atomicOr(&ctrl->sick[box >> 5], 1u << (box & 31));
-                            sick = true;
-                        }
-                    }
-                }
-                any_sick = !named_bar_and(kEpiBarrier, kEpiThreads, !sick);
+        bool any_sick = false;  // ... and whether any of the item's boxes is kept out of the MMAs
+        // Adapters, few rows: the item's second factors to L2 before the main
+        // k-blocks' copies fill DRAM's queues (a thread per row, two lines).
+        auto ask_for_boxes = [&]() {
+            const int32_t slots = nslots[it.tile], per = kXK >> p.box_shift;
+            const int32_t b0 = it.x0 * per, rows = (min(it.x1 * per, slots * p.per_slot) - b0) << p.box_shift;
+            for (int32_t r = (int32_t)et; r < rows; r += (int32_t)kEpiThreads) {
+                const int32_t box = b0 + (r >> p.box_shift), slot = slot_of(p, box);
+                const int32_t j = ((box - slot * p.per_slot) << p.box_shift) + (r & (p.rank_box - 1));
+                if (j >= p.rank) continue;
+                const int64_t row = (int64_t)slot_list[(int64_t)it.tile * p.cap + slot] * p.rank + j;
+                for (int32_t n = it.n * 128; n < min(it.n * 128 + 128, p.N); n += 64) prefetch_line(p.B + row * p.N + n);
             }
-            __threadfence_block();
-            if (et == 0) *(volatile int32_t*)&ctrl->checked = (int32_t)local + 1;
+        };
+        // The second factors of an extra k-block, once they have landed: a
+        // row's columns of other adapters are zeros in its low-rank part, and
+        // zero times an infinity or NaN is not zero, so a box that is not
+        // finite is made zeros here and its own rows get its products from the
+        // epilogue: one adapter's broken weights stay in its rows.  Looked at
+        // in shared memory: a read of them in global memory, ahead of the copies,
+        // stood in DRAM's queues behind the weights (64 rows, 48 adapters of
+        // rank 32, 8192 x 8192: 56.5 us, so 47.3).
+        // (exponent all ones: adding its lowest bit carries into the sign's place)
+        const uint32_t inf = p.bf16 ? 0x7F807F80u : 0x7C007C00u, low_bit = p.bf16 ? 0x00800080u : 0x04000400u;
+        auto carries = [&](const uint4& q) {
+            return ((q.x & inf) + low_bit) | ((q.y & inf) + low_bit) | ((q.z & inf) + low_bit) | ((q.w & inf) + low_bit);
+        };
+        auto vec_finite = [&](const uint4& q) { return (carries(q) & 0x80008000u) == 0u; };
+        auto boxes_finite = [&](uint32_t at, int32_t vecs) {
+            constexpr int32_t kEach = kXK * 16 / (int32_t)kEpiThreads;  // vectors of a thread
+            uint32_t bad = 0;
+#pragma unroll
+            for (int32_t i0 = 0; i0 < kEach; i0 += 4) {
+                uint4 q[4];
+#pragma unroll
+                for (int32_t i = 0; i < 4; ++i) {
+                    const int32_t v = (int32_t)et + (i0 + i) * (int32_t)kEpiThreads;
+                    q[i] = ld_shared_v4(at + 16u * (uint32_t)min(v, vecs - 1));
+                }
+#pragma unroll
+                for (int32_t i = 0; i < 4; ++i) bad |= carries(q[i]);
+            }
+            return (bad & 0x80008000u) == 0u;
+        };
+        // ... and the boxes of block e that are not finite to zeros (all threads)
+        auto clear_boxes = [&](uint32_t at, int32_t vecs, int32_t e) {
+            const int32_t b0 = e * (kXK >> p.box_shift), shift = p.box_shift + 4;  // vectors of a box, as a power of two
+            for (int32_t v = (int32_t)et; v < vecs; v += (int32_t)kEpiThreads)
+                if (!vec_finite(ld_shared_v4(at + 16u * (uint32_t)v))) {
+                    const int32_t box = b0 + (v >> shift);
+                    atomicOr(&ctrl->sick[box >> 5], 1u << (box & 31));
+                }
+            named_bar_sync(kEpiBarrier, kEpiThreads);
+            for (int32_t v = (int32_t)et; v < vecs; v += (int32_t)kEpiThreads) {
+                const int32_t box = b0 + (v >> shift);
+                if ((ctrl->sick[box >> 5] >> (box & 31)) & 1u) st_shared_v4(at + 16u * (uint32_t)v, make_uint4(0, 0, 0, 0));
+            }
+            fence_proxy_async_smem();
+            named_bar_sync(kEpiBarrier, kEpiThreads);
         };
         // The products of the boxes kept out, for one of their own rows: what
         // row t's low-rank part is to have in column n besides.
@@ -1068,18 +1065,23 @@ __global__ void __launch_bounds__(kThreads, 2)  // at most 144 registers: room f
                     default: copy_async_wait<3>(); break;
                 }
                 fence_proxy_async_smem();
-                named_bar_sync(kEpiBarrier, kEpiThreads);
+                // (extra_ph has moved on once since this block, the last use of its stage)
+                const uint32_t st = (pos + (uint32_t)(e - e0)) % S, phase = ((extra_ph >> st) & 1u) ^ 1u;
+                const uint32_t at = ring + st * stride;
+                const int32_t vecs = pieces_of(slots, e) * p.rank_box * 16;
+                const bool landed = wait_phase(smem_u32(&ctrl->boxes[st]), phase, ctrl, p, kErrEpi);
+                if (!named_bar_and(kEpiBarrier, kEpiThreads, landed && boxes_finite(at, vecs))) {
+                    ok = named_bar_and(kEpiBarrier, kEpiThreads, landed);
+                    if (!ok) break;
+                    clear_boxes(at, vecs, e);
+                    any_sick = true;
+                }
                 if (et == 0) {
-                    const uint32_t st = (pos + (uint32_t)(e - e0)) % S;
                     if (kPair && rank != 0) {
                         mbar_arrive_cluster(mapa_shared(smem_u32(&ctrl->peer[st]), 0));
                     } else {
-                        // (extra_ph has moved on once since this block, the last use of its stage)
-                        if (kPair && armed)
-                            armed = wait_cluster(smem_u32(&ctrl->peer[st]), ((extra_ph >> st) & 1u) ^ 1u, ctrl, p);
-                        if (armed)
-                            mbar_arrive_expect_tx(full0 + 8u * st, (uint32_t)(pieces_of(slots, e) * p.rank_box) *
-                                                                       (kPair ? 512u : 256u));
+                        if (kPair && armed) armed = wait_cluster(smem_u32(&ctrl->peer[st]), phase, ctrl, p);
+                        if (armed) mbar_arrive(full0 + 8u * st);
                     }
                 }
             }
@@ -1251,10 +1253,15 @@ __global__ void __launch_bounds__(kThreads, 2)  // at most 144 registers: room f
         };
         for (bool ok = true; ok && iter.next(it); ++local) {
             if (kAdapters) {
-                check_boxes();
+                if (!kPair) ask_for_boxes();
                 ok = fill_extras();
             }
             if (ok) ok = drain(it, local);
+            if (kAdapters && any_sick) {
+                named_bar_sync(kEpiBarrier, kEpiThreads);  // (all have drained it)
+                for (int32_t i = (int32_t)et; i < kMaxBoxes / 32; i += (int32_t)kEpiThreads) ctrl->sick[i] = 0u;
+                any_sick = false;
+            }
         }
         // rows of no group: before the first group and past the last one
         const int32_t head = start[0], tail = start[p.G];

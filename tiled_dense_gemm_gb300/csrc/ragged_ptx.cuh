@@ -58,6 +58,25 @@ __device__ __forceinline__ void load_4d(uint32_t dst, const CUtensorMap* m, uint
             : "memory");
 }
 
+// The same for single CTAs, with an L2 cache policy.
+__device__ __forceinline__ void load_3d_hint(uint32_t dst, const CUtensorMap* m, uint32_t bar, int32_t x, int32_t y,
+                                             int32_t z, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x),
+        "r"(y), "r"(z), "l"(policy)
+        : "memory");
+}
+
+__device__ __forceinline__ void load_4d_hint(uint32_t dst, const CUtensorMap* m, uint32_t bar, int32_t x, int32_t y,
+                                             int32_t z, int32_t w, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x),
+        "r"(y), "r"(z), "r"(w), "l"(policy)
+        : "memory");
+}
+
 // L2 prefetch of the line that holds an address.
 __device__ __forceinline__ void prefetch_line(const void* p) {
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
