@@ -1129,21 +1129,20 @@ __global__ void __launch_bounds__(kThreads, 2)  // at most 144 registers: room f
                     const int32_t col = 32 * (int32_t)quarter + 8 * (int32_t)(lane & 3u);
                     const int32_t slot = slot_of(p, (r0 + col) >> p.box_shift), j = r0 + col - slot * p.rank_pad;
                     const int32_t id = col < held && slot < slots ? slot_list[(int64_t)it.tile * p.cap + slot] : -3;
-                    int32_t who[8];  // adapters of rows lane, lane + 32, ...
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int32_t r = 32 * k + (int32_t)lane;
-                        who[k] = r < it.valid ? __ldcg(p.ids + it.row0 + r) : -2;
-                    }
+                    // adapter of row c + lane, asked for a chunk ahead
+                    auto who_at = [&](int32_t r) { return r < it.valid ? __ldcg(p.ids + it.row0 + r) : -2; };
+                    int32_t who = who_at((int32_t)lane);
                     if (!ready()) return false;
-#pragma unroll
-                    for (int ck = 0; ck < 8; ++ck) {
-                        const int32_t c = 32 * ck;
-                        if (c >= it.w) break;
+                    // (not unrolled: it runs once per item, and the code of all
+                    // chunks came from memory, 16 us for eight of them)
+#pragma unroll 1
+                    for (int32_t c = 0; c < it.w; c += 32) {
+                        const int32_t coming = who_at(c + 32 + (int32_t)lane);
                         int32_t his[4];  // adapters of rows c + lane / 4, + 8, ...
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            his[i] = __shfl_sync(0xffffffffu, who[ck], 8 * i + (int)(lane >> 2));
+                            his[i] = __shfl_sync(0xffffffffu, who, 8 * i + (int)(lane >> 2));
+                        who = coming;
                         __syncwarp();
                         tmem_load_fragments(taddr + c, v);
                         uint32_t hi[16], rest[16];
