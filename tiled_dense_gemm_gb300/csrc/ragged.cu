@@ -211,7 +211,7 @@ static int run_forward(const void* X, const void* W, void* Y, const int32_t* off
     p.num_stages = pl.num_stages;
     p.stage_bytes = pl.stage_bytes;
     p.turn_off = pl.num_stages * pl.stage_bytes;
-    p.table_off = p.turn_off + 4 * 32 * (int)kTurnPitch;
+    p.table_off = p.turn_off + (int)epi_threads(ad != nullptr) * (int)kTurnPitch;
     p.tmem_cols = (uint32_t)pl.tmem_cols;
     p.w_kmajor = w_kmajor ? 1 : 0;
     p.w4d = (w_kmajor ? K : N) % 64 == 0;
@@ -296,17 +296,17 @@ static int run_forward(const void* X, const void* W, void* Y, const int32_t* off
     if (ad) {
         if (pl.pair) {
             if ((rc = allow_smem(d, 0, ragged_kernel<true, true>)) != GEMM_OK) return rc;
-            return launch(ragged_kernel<true, true>, pl.grid, kThreads, smem, 2, st, m, p);
+            return launch(ragged_kernel<true, true>, pl.grid, row_threads(true), smem, 2, st, m, p);
         }
         if ((rc = allow_smem(d, 1, ragged_kernel<false, true>)) != GEMM_OK) return rc;
-        return launch(ragged_kernel<false, true>, pl.grid, kThreads, smem, pl.cluster, st, m, p);
+        return launch(ragged_kernel<false, true>, pl.grid, row_threads(true), smem, pl.cluster, st, m, p);
     }
     if (pl.pair) {
         if ((rc = allow_smem(d, 2, ragged_kernel<true, false>)) != GEMM_OK) return rc;
-        return launch(ragged_kernel<true, false>, pl.grid, kThreads, smem, 2, st, m, p);
+        return launch(ragged_kernel<true, false>, pl.grid, row_threads(false), smem, 2, st, m, p);
     }
     if ((rc = allow_smem(d, 3, ragged_kernel<false, false>)) != GEMM_OK) return rc;
-    return launch(ragged_kernel<false, false>, pl.grid, kThreads, smem, pl.cluster, st, m, p);
+    return launch(ragged_kernel<false, false>, pl.grid, row_threads(false), smem, pl.cluster, st, m, p);
 }
 
 // D[g] (P, Q) = U[rows of g]^T V[rows of g]

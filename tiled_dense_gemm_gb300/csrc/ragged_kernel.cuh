@@ -25,8 +25,9 @@
 // takes a share of the tile's k-blocks and the cluster adds the shares up
 // through distributed shared memory.
 //
-// Roles (224 threads, one CTA per SM): warp 0 copies row tiles, warp 6 the
-// weights, warp 1 issues the MMAs, warps 2-5 drain the accumulators;
+// Roles (352 threads, 224 with adapters; one CTA per SM): warp 0 copies row
+// tiles, warp 6 the weights, warp 1 issues the MMAs, warps 2-5 and 7-10 (2-5)
+// drain the accumulators;
 // shared-memory ring of 128-k stages, two TMEM accumulators.  Every wait is
 // bounded.  The epilogue turns D^T round in shared memory (each warp its own
 // 32 x 32 blocks), applies the ReLU or the gate in 32 bits or on the rounded
@@ -61,8 +62,14 @@
 namespace gr {
 namespace rg {
 
-constexpr int kThreads = 224;
+// Epilogue warps: eight, each half of a quarter's 32-row chunks (one warp per
+// scheduler takes 0.7 us per chunk, which shows where the last tile's epilogue
+// has nothing to hide behind: 3000 rows, 8 groups, 4096 -> 1024: 32.9 us with
+// four warps, 30.0 with eight); four in the adapters' kernels, which share the
+// registers with the low-rank kernel.
 constexpr uint32_t kEpiThreads = 128;
+__host__ __device__ constexpr uint32_t epi_threads(bool adapters) { return adapters ? kEpiThreads : 2 * kEpiThreads; }
+__host__ __device__ constexpr int row_threads(bool adapters) { return 96 + (int)epi_threads(adapters); }
 constexpr uint32_t kEpiBarrier = 1;
 constexpr int kBK = 128;       // k-rows per ring stage: eight MMAs per wait and commit
 constexpr int kMaxStages = 8;
@@ -461,9 +468,10 @@ __device__ __forceinline__ uint32_t gate16(uint32_t x, uint32_t gate, int32_t bf
 // ------------------------------------------------------------------ kernel
 
 template <bool kPair, bool kAdapters>
-__global__ void __launch_bounds__(kThreads, 2)  // at most 144 registers: room for a block of the adapters' low kernel
+__global__ void __launch_bounds__(row_threads(kAdapters), kAdapters ? 2 : 1)  // (2: room for a block of the low kernel)
     ragged_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
     constexpr int kCG = kPair ? 2 : 1;
+    constexpr uint32_t kEpi = epi_threads(kAdapters);
     using It = Iter<kPair, kAdapters>;
     extern __shared__ __align__(1024) uint8_t smem[];
     Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem);
@@ -487,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // at most 144 registers: room f
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&ctrl->tmem_full[b]), 1);
-            mbar_init(smem_u32(&ctrl->tmem_empty[b]), (kPair ? 2u : 1u) * (kEpiThreads / 32));
+            mbar_init(smem_u32(&ctrl->tmem_empty[b]), (kPair ? 2u : 1u) * (kEpi / 32));
         }
         mbar_init(smem_u32(&ctrl->final_bar), 1);
         ctrl->abort_flag = 0;
@@ -889,15 +897,16 @@ __global__ void __launch_bounds__(kThreads, 2)  // at most 144 registers: room f
         __syncwarp();
     } else {
         // ----------------------------------------------------------- epilogue
-        const uint32_t quarter = warp & 3u;
+        const uint32_t quarter = warp & 3u, half = warp > 6 ? 1u : 0u;
+        constexpr int32_t kChunkStep = (int32_t)kEpi / 4;  // from one of a warp's chunks of 32 rows to its next
         const uint32_t lane_row = quarter * 32 + lane;
         const uint32_t cols = p.tmem_cols / 2;
         uint32_t local = 0;
         float v[32];
-        const uint32_t turn = ring + (uint32_t)p.turn_off + quarter * (32u * kTurnPitch);
+        const uint32_t turn = ring + (uint32_t)p.turn_off + (quarter + 4u * half) * (32u * kTurnPitch);
         const uint32_t turn_st = turn + (lane & 7u) * kTurnPitch + (lane >> 3) * 16u;
         const uint32_t turn_ld = turn + (lane >> 2) * kTurnPitch + (lane & 3u) * 16u;
-        const uint32_t et = threadIdx.x - 64;
+        const uint32_t et = threadIdx.x - 64 - 32 * half;  // (warp 6 has another role)
         uint32_t pos = 0;  // adapters: ring stages before the item's extra ones
         uint32_t extra_ph = 0;  // ... and the phase of each stage's `extra` barrier
         bool any_sick = false;  // ... and whether any of the item's boxes is kept out of the MMAs
@@ -906,7 +915,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // at most 144 registers: room f
         auto ask_for_boxes = [&]() {
             const int32_t slots = nslots[it.tile], per = kXK >> p.box_shift;
             const int32_t b0 = it.x0 * per, rows = (min(it.x1 * per, slots * p.per_slot) - b0) << p.box_shift;
-            for (int32_t r = (int32_t)et; r < rows; r += (int32_t)kEpiThreads) {
+            for (int32_t r = (int32_t)et; r < rows; r += (int32_t)kEpi) {
                 const int32_t box = b0 + (r >> p.box_shift), slot = slot_of(p, box);
                 const int32_t j = ((box - slot * p.per_slot) << p.box_shift) + (r & (p.rank_box - 1));
                 if (j >= p.rank) continue;
@@ -929,14 +938,14 @@ __global__ void __launch_bounds__(kThreads, 2)  // at most 144 registers: room f
         };
         auto vec_finite = [&](const uint4& q) { return (carries(q) & 0x80008000u) == 0u; };
         auto boxes_finite = [&](uint32_t at, int32_t vecs) {
-            constexpr int32_t kEach = kXK * 16 / (int32_t)kEpiThreads;  // vectors of a thread
+            constexpr int32_t kEach = kXK * 16 / (int32_t)kEpi;  // vectors of a thread
             uint32_t bad = 0;
 #pragma unroll
             for (int32_t i0 = 0; i0 < kEach; i0 += 4) {
                 uint4 q[4];
 #pragma unroll
                 for (int32_t i = 0; i < 4; ++i) {
-                    const int32_t v = (int32_t)et + (i0 + i) * (int32_t)kEpiThreads;
+                    const int32_t v = (int32_t)et + (i0 + i) * (int32_t)kEpi;
                     q[i] = ld_shared_v4(at + 16u * (uint32_t)min(v, vecs - 1));
                 }
 #pragma unroll
@@ -947,18 +956,18 @@ __global__ void __launch_bounds__(kThreads, 2)  // at most 144 registers: room f
         // ... and the boxes of block e that are not finite to zeros (all threads)
         auto clear_boxes = [&](uint32_t at, int32_t vecs, int32_t e) {
             const int32_t b0 = e * (kXK >> p.box_shift), shift = p.box_shift + 4;  // vectors of a box, as a power of two
-            for (int32_t v = (int32_t)et; v < vecs; v += (int32_t)kEpiThreads)
+            for (int32_t v = (int32_t)et; v < vecs; v += (int32_t)kEpi)
                 if (!vec_finite(ld_shared_v4(at + 16u * (uint32_t)v))) {
                     const int32_t box = b0 + (v >> shift);
                     atomicOr(&ctrl->sick[box >> 5], 1u << (box & 31));
                 }
-            named_bar_sync(kEpiBarrier, kEpiThreads);
-            for (int32_t v = (int32_t)et; v < vecs; v += (int32_t)kEpiThreads) {
+            named_bar_sync(kEpiBarrier, kEpi);
+            for (int32_t v = (int32_t)et; v < vecs; v += (int32_t)kEpi) {
                 const int32_t box = b0 + (v >> shift);
                 if ((ctrl->sick[box >> 5] >> (box & 31)) & 1u) st_shared_v4(at + 16u * (uint32_t)v, make_uint4(0, 0, 0, 0));
             }
             fence_proxy_async_smem();
-            named_bar_sync(kEpiBarrier, kEpiThreads);
+            named_bar_sync(kEpiBarrier, kEpi);
         };
         // The products of the boxes kept out, for one of their own rows: what
         // row t's low-rank part is to have in column n besides.
@@ -1010,7 +1019,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // at most 144 registers: room f
                         }
                     __threadfence();
                 }
-                ok = named_bar_and(kEpiBarrier, kEpiThreads, ok);
+                ok = named_bar_and(kEpiBarrier, kEpi, ok);
             } else {
                 grid_dependency_wait();
             }
@@ -1032,7 +1041,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // at most 144 registers: room f
                     const uint32_t st = (pos + (uint32_t)(issued - e0)) % S;
                     ok = wait_phase(smem_u32(&ctrl->extra[st]), (extra_ph >> st) & 1u, ctrl, p, kErrTokens);
                     extra_ph ^= 1u << st;
-                    ok = named_bar_and(kEpiBarrier, kEpiThreads, ok);
+                    ok = named_bar_and(kEpiBarrier, kEpi, ok);
                     if (!ok) break;
                     const int32_t col = issued * kXK + 8 * (int32_t)(v & 7u);
                     const int32_t slot = slot_of(p, col >> p.box_shift);
@@ -1070,8 +1079,8 @@ __global__ void __launch_bounds__(kThreads, 2)  // at most 144 registers: room f
                 const uint32_t at = ring + st * stride;
                 const int32_t vecs = pieces_of(slots, e) * p.rank_box * 16;
                 const bool landed = wait_phase(smem_u32(&ctrl->boxes[st]), phase, ctrl, p, kErrEpi);
-                if (!named_bar_and(kEpiBarrier, kEpiThreads, landed && boxes_finite(at, vecs))) {
-                    ok = named_bar_and(kEpiBarrier, kEpiThreads, landed);
+                if (!named_bar_and(kEpiBarrier, kEpi, landed && boxes_finite(at, vecs))) {
+                    ok = named_bar_and(kEpiBarrier, kEpi, landed);
                     if (!ok) break;
                     clear_boxes(at, vecs, e);
                     any_sick = true;
@@ -1086,14 +1095,14 @@ __global__ void __launch_bounds__(kThreads, 2)  // at most 144 registers: room f
                 }
             }
             pos += (uint32_t)(e1 - e0);
-            return named_bar_and(kEpiBarrier, kEpiThreads, ok && armed);
+            return named_bar_and(kEpiBarrier, kEpi, ok && armed);
         };
         // the item whose accumulator is the CTA's `local`-th; false: aborting
         auto drain = [&](const Item& it, uint32_t local) {
             const uint32_t buf = local & 1u, bph = (local >> 1) & 1u;
             auto ready = [&]() {
                 bool ok = wait_phase(smem_u32(&ctrl->tmem_full[buf]), bph, ctrl, p, kErrEpi);
-                ok = named_bar_and(kEpiBarrier, kEpiThreads, ok);
+                ok = named_bar_and(kEpiBarrier, kEpi, ok);
                 tc_fence_after();
                 return ok;
             };
@@ -1175,7 +1184,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // at most 144 registers: room f
                     }
                     release();
                     __threadfence();
-                    named_bar_sync(kEpiBarrier, kEpiThreads);
+                    named_bar_sync(kEpiBarrier, kEpi);
                     if (et == 0) atomicAdd(p.low_done + it.tile, 1u);
                     return true;
                 }
@@ -1184,7 +1193,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // at most 144 registers: room f
             if (clustered) {
                 // this CTA's share, fp32, into its ring (idle by now): rows of
                 // Y x 128 columns; the cluster adds them up below
-                for (int32_t c = 0; c < it.w; c += 32) {
+                for (int32_t c = 32 * (int32_t)half; c < it.w; c += kChunkStep) {
                     __syncwarp();
                     tmem_load_32cols(taddr + c, v);
                     if (kAdapters && any_sick)
@@ -1200,7 +1209,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // at most 144 registers: room f
             // this thread's 8 columns of Y (of rows lane / 4, + 8, ...)
             const int32_t n = it.n * (kPair ? 256 : 128) + 128 * (int32_t)rank + 32 * (int32_t)quarter + 8 * (int32_t)(lane & 3u);
             const bool in_n = n < p.N;
-            for (int32_t c = 0; c < it.w; c += 32) {
+            for (int32_t c = 32 * (int32_t)half; c < it.w; c += kChunkStep) {
                 uint4 gate[4];
                 if (p.act) {
 #pragma unroll
@@ -1257,8 +1266,8 @@ __global__ void __launch_bounds__(kThreads, 2)  // at most 144 registers: room f
             }
             if (ok) ok = drain(it, local);
             if (kAdapters && any_sick) {
-                named_bar_sync(kEpiBarrier, kEpiThreads);  // (all have drained it)
-                for (int32_t i = (int32_t)et; i < kMaxBoxes / 32; i += (int32_t)kEpiThreads) ctrl->sick[i] = 0u;
+                named_bar_sync(kEpiBarrier, kEpi);  // (all have drained it)
+                for (int32_t i = (int32_t)et; i < kMaxBoxes / 32; i += (int32_t)kEpi) ctrl->sick[i] = 0u;
                 any_sick = false;
             }
         }
@@ -1269,7 +1278,7 @@ __global__ void __launch_bounds__(kThreads, 2)  // at most 144 registers: room f
         for (int32_t r = (int32_t)blockIdx.x; r < outside; r += (int32_t)gridDim.x) {
             const int32_t t = r < head ? r : tail + (r - head);
             uint4* y = reinterpret_cast<uint4*>(p.Y + (int64_t)t * p.ldy);
-            for (int32_t i = (int32_t)threadIdx.x - 64; i < vecs; i += (int32_t)kEpiThreads) y[i] = make_uint4(0, 0, 0, 0);
+            for (int32_t i = (int32_t)et; i < vecs; i += (int32_t)kEpi) y[i] = make_uint4(0, 0, 0, 0);
         }
     }
 
