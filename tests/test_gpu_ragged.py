@@ -544,6 +544,31 @@ def test_example_block():
             assert off < 8 * 2.0 ** -11, float(off)
 
 
+# Groups of many rows with many column tiles: CTA pairs (few tiles run as single
+# CTAs), with the columns' last tile partial.
+WIDE = [([255, 257, 0, 300], 0, 1), ([512, 1, 0, 513], 7, 0), ([600], 0, 0), ([33, 0, 410, 96, 31], 2, 2)]
+
+
+@pytest.mark.parametrize("layout,dtype", [("kn", "f16"), ("nk", "f16"), ("kn", "bf16"), ("nk", "bf16")])
+@pytest.mark.parametrize("groups", WIDE, ids=lambda g: "-".join(map(str, g[0])))
+@pytest.mark.parametrize("K,N", [(136, 8200), (520, 5000), (1024, 4096)])
+def test_grouped_wide(K, N, groups, layout, dtype):
+    sizes, head, tail = groups
+    T = head + sum(sizes) + tail
+    off = offsets_of(sizes, head)
+    x, w = normal((T, K), 31, dtype), weights(len(sizes), K, N, layout, 32, dtype, K ** -0.5)
+    y = binding.gemm_relu_grouped(x, w, off, b_layout=layout)
+    binding.check_device_error()
+    ref.check(y, ref.grouped(x, w, off, True, layout), f"{sizes} {K}x{N} {layout} {dtype}")
+    # the gradient with the same many columns: its reduction is the short side
+    other = "nk" if layout == "kn" else "kn"
+    w = weights(len(sizes), N, K, other, 33, dtype, K ** -0.5)
+    act = normal((T, N), 34, dtype)
+    dx = binding.gemm_relu_grouped_dx(x, w, off, act=act, b_layout=other)
+    binding.check_device_error()
+    ref.check(dx, ref.grouped_dx(x, w, off, act, other), f"dx {sizes} {K}x{N} {other} {dtype}")
+
+
 # Bounded waits, by the library's own hook: the copy of one block of rows is
 # left out, so a wait of the kernel runs out after a millisecond.  The sizes
 # give plans of single CTAs without clusters.

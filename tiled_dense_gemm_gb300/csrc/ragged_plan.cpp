@@ -30,7 +30,14 @@ RaggedPlan plan_rows(int64_t T, int64_t G, int64_t N, int64_t K, int64_t R, int6
     // against 266).  Tiles of at most 128 rows for groups of about that many
     // (128 rows each: 171 us, with tiles of up to 256: 175; 192 rows: 227
     // and 185).
-    p.pair = avg > (R > 0 ? 128 : 64) && pairs > 0;
+    // But a few pairs' tiles leave most multiprocessors idle, each with all of a
+    // long reduction: up to two tiles for every five pairs, single CTAs, whose
+    // clusters share the reduction, are faster (one group of 4096 x 1024, 512
+    // rows, 8 tiles: 14.5 us against 24.2; 1024 rows, 16: 19.4 and 24.1; 2048
+    // rows, 32: 33.7 and 24.4; 8 groups of 4096 x 512, 256 rows each, 30: 19.7
+    // and 25.5).
+    const int64_t pair_tiles = (std::min(G, T) + (T - std::min(G, T)) / 256) * ceil_div(N, 256);
+    p.pair = avg > (R > 0 ? 128 : 64) && pairs > 0 && (R > 0 || pair_tiles * 5 > (int64_t)pairs * 2);
     int64_t cap;
     if (p.pair)
         cap = avg <= 96 ? 128 : 256;
