@@ -211,7 +211,8 @@ static int run_forward(const void* X, const void* W, void* Y, const int32_t* off
     p.num_stages = pl.num_stages;
     p.stage_bytes = pl.stage_bytes;
     p.turn_off = pl.num_stages * pl.stage_bytes;
-    p.table_off = p.turn_off + (int)epi_threads(ad != nullptr) * (int)kTurnPitch;
+    const int threads = pl.low_in_main ? kHelped : row_threads(ad != nullptr);
+    p.table_off = p.turn_off + (threads - 96) * (int)kTurnPitch;
     p.tmem_cols = (uint32_t)pl.tmem_cols;
     p.w_kmajor = w_kmajor ? 1 : 0;
     p.w4d = (w_kmajor ? K : N) % 64 == 0;
@@ -296,7 +297,7 @@ static int run_forward(const void* X, const void* W, void* Y, const int32_t* off
     if (ad) {
         if (pl.pair) {
             if ((rc = allow_smem(d, 0, ragged_kernel<true, true>)) != GEMM_OK) return rc;
-            return launch(ragged_kernel<true, true>, pl.grid, row_threads(true), smem, 2, st, m, p);
+            return launch(ragged_kernel<true, true>, pl.grid, threads, smem, 2, st, m, p);
         }
         if ((rc = allow_smem(d, 1, ragged_kernel<false, true>)) != GEMM_OK) return rc;
         return launch(ragged_kernel<false, true>, pl.grid, row_threads(true), smem, pl.cluster, st, m, p);

@@ -62,11 +62,16 @@
 namespace gr {
 namespace rg {
 
+constexpr int kHelped = 352;  // threads of the adapters' pair kernel with four more warps for its main tiles' epilogue
+
 // Epilogue warps: eight, each half of a quarter's 32-row chunks (one warp per
 // scheduler takes 0.7 us per chunk, which shows where the last tile's epilogue
 // has nothing to hide behind: 3000 rows, 8 groups, 4096 -> 1024: 32.9 us with
 // four warps, 30.0 with eight); four in the adapters' kernels, which share the
-// registers with the low-rank kernel.
+// registers with the low-rank kernel, and where there is none four more, which
+// drain the main tiles while the first four fill the next one's extra k-blocks
+// (12153 rows, 296 x 6608, rank 8: 152 -> 120 us; 8192 rows of 4096 x 4096, whose
+// main k-blocks are longer than both, 200 either way).
 constexpr uint32_t kEpiThreads = 128;
 __host__ __device__ constexpr uint32_t epi_threads(bool adapters) { return adapters ? kEpiThreads : 2 * kEpiThreads; }
 __host__ __device__ constexpr int row_threads(bool adapters) { return 96 + (int)epi_threads(adapters); }
@@ -151,6 +156,8 @@ struct __align__(8) Ctrl {
     uint64_t peer[kMaxStages];   // ... and, of a pair's leader, filled by the peer
     uint32_t sick[kMaxBoxes / 32];  // adapters: boxes of the item's second factors that are not finite
     uint64_t boxes[kMaxStages];     // ... landed in a stage
+    int32_t helped;                 // ... items that the helping warps have drained, times their number
+    int32_t sick_item;              // ... 1 + the CTA's item some of whose boxes are kept out
     uint32_t tmem_addr;
     int32_t abort_flag;
     int32_t ring_s, ring_ph, ring_lap;
@@ -184,6 +191,21 @@ __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, Ctrl
             atomicCAS(p.err, 0, (int32_t)kErrEpi);
             return false;
         }
+    return true;
+}
+
+// The same until a counter in shared memory has reached a value.
+__device__ __forceinline__ bool wait_counter(int32_t* counter, int32_t value, Ctrl* ctrl, const Params& p) {
+    volatile int32_t* const c = counter;
+    volatile int32_t* abort_flag = &ctrl->abort_flag;
+    const uint64_t t0 = globaltimer_ns();
+    while (*c < value)
+        if (*abort_flag || globaltimer_ns() - t0 > p.timeout_ns) {
+            *abort_flag = 1;
+            atomicCAS(p.err, 0, (int32_t)kErrEpi);
+            return false;
+        }
+    __threadfence_block();
     return true;
 }
 
@@ -468,7 +490,7 @@ __device__ __forceinline__ uint32_t gate16(uint32_t x, uint32_t gate, int32_t bf
 // ------------------------------------------------------------------ kernel
 
 template <bool kPair, bool kAdapters>
-__global__ void __launch_bounds__(row_threads(kAdapters), kAdapters ? 2 : 1)  // (2: room for a block of the low kernel)
+__global__ void __maxnreg__(128)  // (adapters: leaves room for a block of the low kernel)
     ragged_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
     constexpr int kCG = kPair ? 2 : 1;
     constexpr uint32_t kEpi = epi_threads(kAdapters);
@@ -481,6 +503,7 @@ __global__ void __launch_bounds__(row_threads(kAdapters), kAdapters ? 2 : 1)  //
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = kPair ? cluster_ctarank() : 0u;
     const bool clustered = !kPair && p.cluster > 1;
+    const bool helpers = kPair && kAdapters && blockDim.x == kHelped;
     const uint32_t share = clustered ? cluster_ctarank() : 0u;
     const uint32_t worker = kPair ? blockIdx.x / 2 : clustered ? blockIdx.x / (uint32_t)p.cluster : blockIdx.x;
     const uint32_t workers = kPair ? gridDim.x / 2 : clustered ? gridDim.x / (uint32_t)p.cluster : gridDim.x;
@@ -498,6 +521,7 @@ __global__ void __launch_bounds__(row_threads(kAdapters), kAdapters ? 2 : 1)  //
             mbar_init(smem_u32(&ctrl->tmem_empty[b]), (kPair ? 2u : 1u) * (kEpi / 32));
         }
         mbar_init(smem_u32(&ctrl->final_bar), 1);
+        ctrl->helped = ctrl->sick_item = 0;
         ctrl->abort_flag = 0;
         ctrl->ring_s = ctrl->ring_ph = ctrl->ring_lap = 0;
         for (int i = 0; i < kMaxBoxes / 32; ++i) ctrl->sick[i] = 0u;
@@ -899,6 +923,8 @@ __global__ void __launch_bounds__(row_threads(kAdapters), kAdapters ? 2 : 1)  //
         // ----------------------------------------------------------- epilogue
         const uint32_t quarter = warp & 3u, half = warp > 6 ? 1u : 0u;
         constexpr int32_t kChunkStep = (int32_t)kEpi / 4;  // from one of a warp's chunks of 32 rows to its next
+        const int32_t chunk0 = kAdapters ? 0 : 32 * (int32_t)half;
+        const uint32_t group_barrier = kEpiBarrier + (kAdapters ? half : 0u);
         const uint32_t lane_row = quarter * 32 + lane;
         const uint32_t cols = p.tmem_cols / 2;
         uint32_t local = 0;
@@ -906,7 +932,7 @@ __global__ void __launch_bounds__(row_threads(kAdapters), kAdapters ? 2 : 1)  //
         const uint32_t turn = ring + (uint32_t)p.turn_off + (quarter + 4u * half) * (32u * kTurnPitch);
         const uint32_t turn_st = turn + (lane & 7u) * kTurnPitch + (lane >> 3) * 16u;
         const uint32_t turn_ld = turn + (lane >> 2) * kTurnPitch + (lane & 3u) * 16u;
-        const uint32_t et = threadIdx.x - 64 - 32 * half;  // (warp 6 has another role)
+        const uint32_t et = threadIdx.x - 64 - (kAdapters ? 160 : 32) * half;  // (warp 6 has another role)
         uint32_t pos = 0;  // adapters: ring stages before the item's extra ones
         uint32_t extra_ph = 0;  // ... and the phase of each stage's `extra` barrier
         bool any_sick = false;  // ... and whether any of the item's boxes is kept out of the MMAs
@@ -1084,6 +1110,7 @@ __global__ void __launch_bounds__(row_threads(kAdapters), kAdapters ? 2 : 1)  //
                     if (!ok) break;
                     clear_boxes(at, vecs, e);
                     any_sick = true;
+                    if (et == 0) *(volatile int32_t*)&ctrl->sick_item = (int32_t)local + 1;
                 }
                 if (et == 0) {
                     if (kPair && rank != 0) {
@@ -1102,8 +1129,9 @@ __global__ void __launch_bounds__(row_threads(kAdapters), kAdapters ? 2 : 1)  //
             const uint32_t buf = local & 1u, bph = (local >> 1) & 1u;
             auto ready = [&]() {
                 bool ok = wait_phase(smem_u32(&ctrl->tmem_full[buf]), bph, ctrl, p, kErrEpi);
-                ok = named_bar_and(kEpiBarrier, kEpi, ok);
+                ok = named_bar_and(group_barrier, kEpi, ok);
                 tc_fence_after();
+                if (kAdapters && half) any_sick = *(volatile int32_t*)&ctrl->sick_item == (int32_t)local + 1;
                 return ok;
             };
             const uint32_t taddr = tmem_base + ((quarter * 32u) << 16) + buf * cols;
@@ -1118,6 +1146,7 @@ __global__ void __launch_bounds__(row_threads(kAdapters), kAdapters ? 2 : 1)  //
                 }
             };
             if constexpr (kPair && kAdapters) {
+                if (it.low && half) return ready();  // (only to keep up with the accumulators' phases)
                 if (it.low) {
                     const int32_t slots = nslots[it.tile];
                     const int32_t held = low_boxes(p, slots) * p.rank_box;  // products of each CTA
@@ -1193,7 +1222,7 @@ __global__ void __launch_bounds__(row_threads(kAdapters), kAdapters ? 2 : 1)  //
             if (clustered) {
                 // this CTA's share, fp32, into its ring (idle by now): rows of
                 // Y x 128 columns; the cluster adds them up below
-                for (int32_t c = 32 * (int32_t)half; c < it.w; c += kChunkStep) {
+                for (int32_t c = chunk0; c < it.w; c += kChunkStep) {
                     __syncwarp();
                     tmem_load_32cols(taddr + c, v);
                     if (kAdapters && any_sick)
@@ -1209,7 +1238,7 @@ __global__ void __launch_bounds__(row_threads(kAdapters), kAdapters ? 2 : 1)  //
             // this thread's 8 columns of Y (of rows lane / 4, + 8, ...)
             const int32_t n = it.n * (kPair ? 256 : 128) + 128 * (int32_t)rank + 32 * (int32_t)quarter + 8 * (int32_t)(lane & 3u);
             const bool in_n = n < p.N;
-            for (int32_t c = 32 * (int32_t)half; c < it.w; c += kChunkStep) {
+            for (int32_t c = chunk0; c < it.w; c += kChunkStep) {
                 uint4 gate[4];
                 if (p.act) {
 #pragma unroll
@@ -1260,14 +1289,23 @@ __global__ void __launch_bounds__(row_threads(kAdapters), kAdapters ? 2 : 1)  //
             return true;
         };
         for (bool ok = true; ok && iter.next(it); ++local) {
-            if (kAdapters) {
+            if (kAdapters && !half) {
                 if (!kPair) ask_for_boxes();
                 ok = fill_extras();
             }
-            if (ok) ok = drain(it, local);
-            if (kAdapters && any_sick) {
-                named_bar_sync(kEpiBarrier, kEpi);  // (all have drained it)
+            // with helping warps these fill the next item's extra k-blocks while
+            // those drain this one
+            if (ok && (!helpers || half || it.low)) ok = drain(it, local);
+            if (kAdapters && half) {
+                __threadfence_block();
+                __syncwarp();
+                if (lane == 0) atomicAdd(&ctrl->helped, 1);
+            } else if (kAdapters && any_sick) {
+                // (all have drained it)
+                if (helpers) ok = ok && wait_counter(&ctrl->helped, 4 * ((int32_t)local + 1), ctrl, p);
+                ok = named_bar_and(kEpiBarrier, kEpi, ok);
                 for (int32_t i = (int32_t)et; i < kMaxBoxes / 32; i += (int32_t)kEpi) ctrl->sick[i] = 0u;
+                if (et == 0) ctrl->sick_item = 0;
                 any_sick = false;
             }
         }

@@ -52,7 +52,7 @@ RaggedPlan plan_rows(int64_t T, int64_t G, int64_t N, int64_t K, int64_t R, int6
         return p;
     }
     p.low_in_main = R > 0 && p.pair && T > kLowRows;
-    const int64_t table = (R > 0 ? 1 : 2) * kTurn + round_up((2 * (G + 1) + (R == 0 ? 0 : p.pair ? ceil_div(T, cap) + 1 : 389)) * 4, 16);
+    const int64_t table = (R > 0 && !p.low_in_main ? 1 : 2) * kTurn + round_up((2 * (G + 1) + (R == 0 ? 0 : p.pair ? ceil_div(T, cap) + 1 : 389)) * 4, 16);
     // (adapters: room beside it for a block of the kernel that computes low)
     const int64_t room = kSmem - kCtrl - table - (R > 0 && !p.low_in_main ? kLowSmem : 0);
     p.num_stages = (int32_t)std::min<int64_t>(8, room / p.stage_bytes);
