@@ -544,6 +544,33 @@ def test_example_block():
             assert off < 8 * 2.0 ** -11, float(off)
 
 
+@pytest.mark.parametrize("rank", [8, 40])
+def test_adapters_do_not_mix_from_tile_to_tile(rank):
+    """Many tiles per CTA, some with a factor that is not finite and some
+    without: what one tile keeps out of its products the next does not."""
+    T, K, N, R = 2304, 136, 8200, 6
+    x, a, b, w = normal((T, K), 1, "bf16"), normal((R, rank, K), 2, "bf16", 0.1), normal((R, rank, N), 3, "bf16"), normal((K, N), 4, "bf16", 0.1)
+    b[1, rank - 1, ::3] = float("inf")
+    b[4, 0, 5000:] = float("nan")
+    ids = (torch.arange(T, device=DEV) // 100 % R).int()
+    ids[7::50] = 1
+    ids[512:768] = 2
+    ids[1500:1800] = -1
+    y = binding.gemm_relu_adapters(x, w, a, b, ids, apply_relu=False)
+    binding.check_device_error()
+    rows = (ids != 1) & (ids != 4)
+    value, bound = ref.adapters(x, w, a, torch.nan_to_num(b.float(), nan=0.0, posinf=0.0, neginf=0.0).to(b.dtype), ids, None, False, "kn")
+    keep = rows.cpu().numpy()
+    ref.check(y[rows], (value[keep], bound[keep]), f"rank {rank}")
+    # and the broken rows have their own finite columns
+    mine = (ids == 1).cpu().numpy()
+    fine = np.ones(N, dtype=bool)
+    fine[::3] = False
+    ref.check(y[ids == 1][:, torch.from_numpy(fine).to(DEV)], (value[mine][:, fine], bound[mine][:, fine]), f"rank {rank}, finite columns")
+    assert not torch.isfinite(y[ids == 1][:, ::3].float()).any()
+    assert torch.isnan(y[ids == 4][:, 5000:].float()).all()
+
+
 # Groups of many rows with many column tiles: CTA pairs (few tiles run as single
 # CTAs), with the columns' last tile partial.
 WIDE = [([255, 257, 0, 300], 0, 1), ([512, 1, 0, 513], 7, 0), ([600], 0, 0), ([33, 0, 410, 96, 31], 2, 2)]

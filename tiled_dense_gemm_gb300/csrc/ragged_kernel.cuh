@@ -228,7 +228,7 @@ __device__ __forceinline__ void drain_ring(Ctrl* ctrl, uint32_t full0, uint32_t 
 // (start[G]: end of the last), tiles[g] = row tiles before it.  Offsets are
 // clamped to [0, T] and to be non-decreasing, so no later index can leave the
 // tensors; if that changed any, bad index arrays are reported.
-__device__ __forceinline__ void build_table(const Params& p, int32_t* start, int32_t* tiles, uint32_t lane) {
+__device__ __forceinline__ void build_table(const Params& p, int32_t* start, int32_t* tiles, uint32_t lane, uint32_t workers) {
     if (!p.offsets) {
         if (lane == 0) {
             start[0] = 0;
@@ -277,6 +277,58 @@ __device__ __forceinline__ void build_table(const Params& p, int32_t* start, int
         count += __shfl_sync(0xffffffffu, n, last);
     }
     if (bad) atomicCAS(p.err + 1, 0, (int32_t)kBadOffsets);
+    if (p.cap != 256) return;
+    // Pairs with tiles of up to 256 rows: the last of few waves may be nearly
+    // empty.  A wave takes about as long as its copies, 128 weights and half a
+    // tile's rows per k and CTA; of tiles of up to 256, 224, ..., 128 rows the
+    // ones whose waves take the shortest time, if that is 5% less (4 groups of
+    // 2583 rows, 5440 x 512: 61.1 us with tiles of 240, 54.1 with 160; 4 of 1030,
+    // 4096 x 1024: 41.4 and 38.4).
+    __syncwarp();
+    int32_t rows = 0, cnt[5] = {0, 0, 0, 0, 0};  // in steps of 32 rows; tiles for each width
+    for (int32_t g = (int32_t)lane; g < p.G; g += 32) {
+        const int32_t units = (start[g + 1] - start[g] + 31) >> 5;
+        rows += units;
+        cnt[0] += (units + 7) / 8;
+        cnt[1] += (units + 6) / 7;
+        cnt[2] += (units + 5) / 6;
+        cnt[3] += (units + 4) / 5;
+        cnt[4] += (units + 3) / 4;
+    }
+    rows = __reduce_add_sync(0xffffffffu, rows);
+    int32_t n_here = 1;  // lane k: the k-th width's tiles
+#pragma unroll
+    for (int k = 0; k < 5; ++k) {
+        cnt[k] = __reduce_add_sync(0xffffffffu, cnt[k]);
+        if ((int)lane == k) n_here = max(cnt[k], 1);
+    }
+    const uint32_t waves = ((uint32_t)n_here * (uint32_t)p.n_tiles + workers - 1u) / workers;
+    const float cost = (float)waves * (128.0f + __fdividef(16.0f * (float)rows, (float)n_here));
+    int32_t best = 8;
+    float least = __shfl_sync(0xffffffffu, cost, 0);
+#pragma unroll
+    for (int k = 1; k < 5; ++k) {
+        const float c = __shfl_sync(0xffffffffu, cost, k);
+        if (c < 0.95f * least) {
+            least = c;
+            best = 8 - k;
+        }
+    }
+    if (best == 8) return;
+    count = 0;
+    for (int32_t g0 = 0; g0 < p.G; g0 += 32) {
+        const int32_t g = g0 + (int32_t)lane;
+        const int32_t mine = g < p.G ? (((start[g + 1] - start[g] + 31) >> 5) + best - 1) / best : 0;
+        int32_t n = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int32_t o = __shfl_up_sync(0xffffffffu, n, d);
+            if ((int)lane >= d) n += o;
+        }
+        if (g < p.G) tiles[g] = count + n - mine;
+        count += __shfl_sync(0xffffffffu, n, 31);
+    }
+    if (lane == 0) tiles[p.G] = count;
 }
 
 struct Item {
@@ -547,7 +599,7 @@ __global__ void __maxnreg__(128)  // (adapters: leaves room for a block of the l
     if (!kAdapters || (kPair && p.low_out)) grid_dependency_wait();
     int32_t* const lows = tiles + p.G + 1;
     if (warp == 6) {
-        build_table(p, start, tiles, lane);
+        build_table(p, start, tiles, lane, workers);
         if (kPair && kAdapters && p.low_out) {
             __syncwarp();
             int32_t before = 0;

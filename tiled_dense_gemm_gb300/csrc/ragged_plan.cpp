@@ -73,7 +73,8 @@ RaggedPlan plan_rows(int64_t T, int64_t G, int64_t N, int64_t K, int64_t R, int6
         const int64_t nt = ceil_div(T, cap);
         p.row_width = (int32_t)round_up(ceil_div(T, nt), p.pair ? 32 : 16);
     }
-    if (items > kIndexMax) {
+    // (the kernel may cut pairs' groups into tiles of half that)
+    if (items > kIndexMax / 2) {
         p.status = GEMM_ERR_TOO_LARGE;
         return p;
     }
