@@ -146,11 +146,11 @@ __device__ __forceinline__ uint4 load_or_zero(const uint16_t* src, bool in) {
 // 32 contiguous bytes of its row and feeds four MMAs with them.
 //
 // Bound: DRAM, which it shares with the main kernel's weights.  64 rows with
-// 48 adapters of rank 32, 8192 x 8192: its 25 MB are in 32-38 us after the
-// start, with the main kernel's 134 MB beside them.  Asking for both
+// 48 adapters of rank 32, 8192 x 8192: its 25 MB are in and multiplied 23 us
+// after the main kernel's start, with that one's 134 MB beside them.  Asking for both
 // factors in L2 first (this one here, the second in the main kernel) keeps
-// them from queueing behind the weights (16 rows with 16 adapters: 43 us for
-// the whole call without, 37 with).
+// them from queueing behind the weights (16 rows with 16 adapters, the whole
+// call: 43 us without, 37 with; 32 with whole lines per load as well).
 template <int kNT>
 __global__ void __launch_bounds__(kLowWarps * 32, 2) adapters_low_kernel(const __grid_constant__ LowParams p) {
     __shared__ float part[kLowWarps / 2][kNT * 4 * 32];

@@ -39,17 +39,18 @@
 //     2048, 256 rows: 152-154 us, 7.0 TB/s.
 //   many: bytes into the multiprocessors.  A pair takes 256 x (rows of the
 //     tile) products per k from L2, and tiles of ragged groups are narrower
-//     than 256: 32 groups of 2048 x 4096, 16384 rows: 186 us, 1480
-//     TFLOP/s, with 14.6 TB/s from L2 (159 us with the weights' copies left
+//     than 256: 32 groups of 2048 x 4096, 16384 rows: 186-189 us,
+//     1470 TFLOP/s, with 14.6 TB/s from L2 (159 us with the weights' copies left
 //     out, 157 us with the MMAs left out: neither hides the other wholly).
 //     Stages of 64 k (six of them) instead of 128 (three): 197 us.
 //   row pitches that are not multiples of 128 bytes cost a second copy per
 //     stage and operand and a second line per row: 5000 rows, 12 groups of
 //     2056 x 3000, 65 us.
 //   rows with adapters: as above, and the second factors and the low-rank
-//     products in extra k-blocks at the end of each tile, ~0.6-1.8 us each
-//     (8192 rows, 24 of 32 adapters of rank 64, 4096 x 4096: 207 us, of which
-//     ~150 us are the shared product's).
+//     products in extra k-blocks at the end of each tile, ~0.9 us each
+//     (64 rows, 48 adapters of rank 32, 8192 x 8192: 48 us, of which DRAM
+//     takes 32; 8192 rows, 24 adapters of rank 64, 4096 x 4096: 200 us, of
+//     which ~150 us are the shared product's and ~30 the wait for low).
 #pragma once
 
 #include <cuda_bf16.h>
