@@ -51,7 +51,7 @@ struct SlotParams {
 __global__ void __launch_bounds__(256) adapters_slots_kernel(const __grid_constant__ SlotParams p) {
     grid_dependency_wait();
     grid_launch_dependents();
-    __shared__ int32_t id[256];
+    __shared__ __align__(16) int32_t id[256];
     __shared__ int32_t count[8];
     const int32_t i = (int32_t)threadIdx.x, warp = i / 32, lane = i % 32;
     const int32_t row0 = (int32_t)blockIdx.x * p.tile_w;
@@ -66,8 +66,14 @@ __global__ void __launch_bounds__(256) adapters_slots_kernel(const __grid_consta
     }
     id[i] = mine;
     __syncthreads();
-    bool first = mine >= 0;
-    for (int32_t j = 0; j < i; ++j) first = first && id[j] != mine;
+    // the first of its own warp, and in none of the warps before
+    const uint32_t same = __match_any_sync(0xffffffffu, mine);
+    bool first = mine >= 0 && (same & ((1u << lane) - 1u)) == 0;
+#pragma unroll 8
+    for (int32_t j = 0; j < 8 * warp; ++j) {
+        const int4 q = reinterpret_cast<const int4*>(id)[j];
+        first = first & (q.x != mine) & (q.y != mine) & (q.z != mine) & (q.w != mine);
+    }
     const uint32_t votes = __ballot_sync(0xffffffffu, first);
     if (lane == 0) count[warp] = __popc(votes);
     __syncthreads();

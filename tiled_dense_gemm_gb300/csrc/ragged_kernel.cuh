@@ -384,16 +384,24 @@ __device__ __forceinline__ void list_slots(const Params& p, int32_t* ids, int32_
     }
     ids[i] = mine;
     named_bar_sync(kEpiBarrier, kEpiThreads);
-    bool first = mine >= 0;
-    int32_t last = i;
-    const int32_t n = min(128, p.T);
-    for (int32_t j = 0; j < n; ++j) {
-        const bool same = ids[j] == mine;
-        first = first && !(same && j < i);
-        last = same ? max(last, j) : last;
+    // the rows of the same adapter, warp by warp (ids is 16-byte aligned)
+    const int32_t lane = i % 32;
+    const uint32_t own = __match_any_sync(0xffffffffu, mine);
+    bool first = mine >= 0 && (own & ((1u << lane) - 1u)) == 0;
+    int32_t last = i / 32 * 32 + 31 - __clz((int)own);
+    for (int32_t w = 0; w < (min(128, p.T) + 31) / 32; ++w) {
+        if (w == i / 32) continue;
+        uint32_t same = 0;
+#pragma unroll
+        for (int32_t j = 0; j < 8; ++j) {
+            const int4 q = reinterpret_cast<const int4*>(ids)[8 * w + j];
+            same |= ((uint32_t)(q.x == mine) | (uint32_t)(q.y == mine) << 1 | (uint32_t)(q.z == mine) << 2 |
+                     (uint32_t)(q.w == mine) << 3) << (4 * j);
+        }
+        if (same && w < i / 32) first = false;
+        if (same) last = max(last, 32 * w + 31 - __clz((int)same));
     }
     const uint32_t votes = __ballot_sync(0xffffffffu, first);
-    const int32_t lane = i % 32;
     if (lane == 0) count[i / 32] = __popc(votes);
     named_bar_sync(kEpiBarrier, kEpiThreads);
     int32_t at = __popc(votes & ((1u << lane) - 1u));
