@@ -49,7 +49,7 @@
 //   rows with adapters: as above, and the second factors and the low-rank
 //     products in extra k-blocks at the end of each tile, ~0.9 us each
 //     (64 rows, 48 adapters of rank 32, 8192 x 8192: 48 us, of which DRAM
-//     takes 32; 8192 rows, 24 adapters of rank 64, 4096 x 4096: 200 us, of
+//     takes 32; 8192 rows, 24 adapters of rank 64, 4096 x 4096: 196 us, of
 //     which ~150 us are the shared product's and ~30 the wait for low).
 #pragma once
 
@@ -71,8 +71,8 @@ constexpr int kHelped = 352;  // threads of the adapters' pair kernel with four 
 // four warps, 30.0 with eight); four in the adapters' kernels, which share the
 // registers with the low-rank kernel, and where there is none four more, which
 // drain the main tiles while the first four fill the next one's extra k-blocks
-// (12153 rows, 296 x 6608, rank 8: 152 -> 120 us; 8192 rows of 4096 x 4096, whose
-// main k-blocks are longer than both, 200 either way).
+// (12153 rows, 296 x 6608, rank 8: 152 us without, 120 with; 8192 rows of 4096 x
+// 4096, whose main k-blocks are longer than both: the same).
 constexpr uint32_t kEpiThreads = 128;
 __host__ __device__ constexpr uint32_t epi_threads(bool adapters) { return adapters ? kEpiThreads : 2 * kEpiThreads; }
 __host__ __device__ constexpr int row_threads(bool adapters) { return 96 + (int)epi_threads(adapters); }
