@@ -240,6 +240,7 @@ static int run_forward(const void* X, const void* W, void* Y, const int32_t* off
     if (ad) {
         p.ids = ad->ids;
         p.B = reinterpret_cast<const uint16_t*>(ad->B);
+        p.row_tiles = pl.row_tiles;
         p.rank = (int32_t)ad->rank;
         p.R = (int32_t)ad->R;
         p.rank_box = pl.rank_box;
@@ -250,7 +251,7 @@ static int run_forward(const void* X, const void* W, void* Y, const int32_t* off
         rc = encode_stack(&m.b, ad->B, (uint64_t)N, (uint64_t)ad->rank, (uint64_t)ad->R, (uint32_t)pl.rank_box, p.b4d,
                           bf16);
         if (rc != GEMM_OK) return rc;
-        const int64_t tiles = (T + pl.cap - 1) / pl.cap;
+        const int64_t tiles = pl.row_tiles;
         // one buffer: the low-rank rows, the tiles' slot lists, their lengths
         const size_t low_bytes = ((size_t)T * 2 * pl.rank_pad * 2 + 255) / 256 * 256;
         const size_t slot_bytes = (size_t)tiles * pl.cap * 4;

@@ -133,6 +133,7 @@ struct Params {
     // and plans of single CTAs
     int32_t test_drop_kb;
     // adapters
+    int32_t row_tiles;       // of equal widths
     const int32_t* ids;      // adapter of each row, -1 none
     const uint16_t* low;     // (T, 2, rank_pad): scale * x A^T, in two parts of the element type
     const int32_t* nslots;   // distinct adapters of each row tile; null: single CTAs, which list them themselves
@@ -235,7 +236,7 @@ __device__ __forceinline__ void build_table(const Params& p, int32_t* start, int
             start[0] = 0;
             start[1] = p.T;
             tiles[0] = 0;
-            tiles[1] = (p.T + p.cap - 1) / p.cap;
+            tiles[1] = p.row_tiles;
         }
         return;
     }

@@ -18,6 +18,18 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 }  // namespace
 
+// T rows in tiles of at most `width`, of equal widths in steps of `step` (the
+// kernel finds the same width from their number): the number of tiles.
+static int64_t equal_tiles(int64_t T, int64_t width, int64_t step, int64_t* w) {
+    int64_t n = ceil_div(T, width);
+    while (true) {
+        *w = round_up(ceil_div(T, n), step);
+        const int64_t fewer = ceil_div(T, *w);
+        if (fewer == n) return n;
+        n = fewer;
+    }
+}
+
 RaggedPlan plan_rows(int64_t T, int64_t G, int64_t N, int64_t K, int64_t R, int64_t rank, int num_sms,
                      int max_pairs) {
     RaggedPlan p = {};
@@ -52,7 +64,27 @@ RaggedPlan plan_rows(int64_t T, int64_t G, int64_t N, int64_t K, int64_t R, int6
         return p;
     }
     p.low_in_main = R > 0 && p.pair && T > kLowRows;
-    const int64_t table = (R > 0 && !p.low_in_main ? 1 : 2) * kTurn + round_up((2 * (G + 1) + (R == 0 ? 0 : p.pair ? ceil_div(T, cap) + 1 : 389)) * 4, 16);
+    if (R > 0) {
+        // As the kernel does for groups: tiles of the width whose waves take the
+        // shortest time, if that is 5% less than with up to 256 rows (1500 rows,
+        // 4096 x 4096, rank 32: 81.8 us with tiles of 256, 74.0; 2827 rows, 576 x
+        // 320, rank 16: 24.2 and 18.8; 255 rows, 1728 x 360, rank 4: 19.8 and 17.3).
+        int64_t width = 0;
+        p.row_tiles = (int32_t)equal_tiles(T, cap, p.pair ? 32 : 16, &width);
+        p.row_width = (int32_t)width;
+        double least = 0;
+        for (int64_t most = 256; p.pair && most >= 128; most -= 32) {
+            const int64_t n = equal_tiles(T, most, 32, &width);
+            const double cost = (double)ceil_div(n * p.n_tiles, pairs) * (128.0 + 0.5 * (double)width);
+            if (most == 256 || (cost < 0.95 * least && n <= GEMM_RELU_MAX_GROUPS)) {
+                least = cost;
+                p.row_tiles = (int32_t)n;
+                p.row_width = (int32_t)width;
+            }
+        }
+    }
+    const int64_t table = (R > 0 && !p.low_in_main ? 1 : 2) * kTurn +
+                          round_up((2 * (G + 1) + (R == 0 ? 0 : p.pair ? p.row_tiles + 1 : 389)) * 4, 16);
     // (adapters: room beside it for a block of the kernel that computes low)
     const int64_t room = kSmem - kCtrl - table - (R > 0 && !p.low_in_main ? kLowSmem : 0);
     p.num_stages = (int32_t)std::min<int64_t>(8, room / p.stage_bytes);
@@ -64,14 +96,12 @@ RaggedPlan plan_rows(int64_t T, int64_t G, int64_t N, int64_t K, int64_t R, int6
     // at most this many row tiles, whatever the groups' sizes are: one row
     // in each of as many groups as can have one, the rest in full tiles
     const int64_t used = std::min(G, T);
-    const int64_t tiles = R > 0 ? ceil_div(T, cap) : used + (T - used) / cap;
+    const int64_t tiles = R > 0 ? p.row_tiles : used + (T - used) / cap;
     const int64_t items = tiles * p.n_tiles;
     if (R > 0) {
         p.rank_box = 8;
         while (p.rank_box < 64 && p.rank_box < rank) p.rank_box *= 2;
         p.rank_pad = (int32_t)round_up(rank, p.rank_box);
-        const int64_t nt = ceil_div(T, cap);
-        p.row_width = (int32_t)round_up(ceil_div(T, nt), p.pair ? 32 : 16);
     }
     // (the kernel may cut pairs' groups into tiles of half that)
     if (items > kIndexMax / 2) {

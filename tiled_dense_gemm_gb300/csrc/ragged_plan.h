@@ -13,7 +13,8 @@ struct RaggedPlan {
     int32_t status;
     int32_t pair;        // CTA pairs (256 columns per tile) instead of single CTAs (128)
     int32_t cap;         // most rows of a tile
-    int32_t row_width;   // adapters of pairs: rows of each row tile
+    int32_t row_tiles;   // adapters: row tiles,
+    int32_t row_width;   // ... and rows of each
     int32_t cluster;     // single CTAs: CTAs (a cluster) that share each item's k-blocks
     int32_t num_kb, n_tiles;
     int32_t stage_bytes, num_stages, smem_bytes, tmem_cols;
