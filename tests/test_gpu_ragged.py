@@ -571,6 +571,26 @@ def test_adapters_do_not_mix_from_tile_to_tile(rank):
     assert torch.isnan(y[ids == 4][:, 5000:].float()).all()
 
 
+# Long groups with few tiles: clusters share the reduction, with shares that
+# are empty (a short group beside long ones), and rows of no group that must not
+# enter.
+@pytest.mark.parametrize("layout,dtype", [("kn", "f16"), ("nk", "bf16")])
+@pytest.mark.parametrize("sizes,head,tail", [([2100], 0, 0), ([1500, 0, 1700], 5, 9), ([4111], 1, 0), ([3, 5000], 0, 130),
+                                             ([130, 1, 3000, 700], 2, 0)], ids=str)
+def test_grouped_dw_long(sizes, head, tail, layout, dtype):
+    T = head + sum(sizes) + tail
+    off = offsets_of(sizes, head)
+    for i, (K, N) in enumerate([(8, 8), (136, 520), (392, 72), (256, 384), (1000, 264)]):
+        x, dy = normal((T, K), 40 + i, dtype), normal((T, N), 50 + i, dtype)
+        x[:head], dy[:head] = float("nan"), float("inf")
+        x[T - tail:], dy[T - tail:] = float("inf"), float("nan")
+        dw = binding.gemm_relu_grouped_dw(x, dy, off, b_layout=layout)
+        binding.check_device_error()
+        ref.check(dw, ref.grouped_dw(x, dy, off, layout), f"{sizes} {K}x{N} {layout} {dtype}")
+        again = binding.gemm_relu_grouped_dw(x, dy, off, b_layout=layout)
+        assert torch.equal(dw, again)
+
+
 # Groups of many rows with many column tiles: CTA pairs (few tiles run as single
 # CTAs), with the columns' last tile partial.
 WIDE = [([255, 257, 0, 300], 0, 1), ([512, 1, 0, 513], 7, 0), ([600], 0, 0), ([33, 0, 410, 96, 31], 2, 2)]

@@ -104,12 +104,6 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ float ld_shared_cluster(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
-}
-
 // 32 bytes from global memory: in one load where addresses allow it (a whole
 // line for the four lanes of a row: half the requests), else in two.
 __device__ __forceinline__ void load_32(uint4 (&q)[2], const uint16_t* src, bool wide) {

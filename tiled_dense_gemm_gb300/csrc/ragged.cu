@@ -324,7 +324,7 @@ static int run_dw(const void* U, const void* V, void* D, const int32_t* offsets,
     q.u3d = P % 64 == 0;
     q.v3d = Q % 64 == 0;
     q.timeout_ns = 2000000000ull + 2000ull * (uint64_t)((T + kBK - 1) / kBK);
-    int rc = test_hook(!pl.pair, 1, &q.test_drop_kb, &q.timeout_ns);
+    int rc = test_hook(!pl.pair && pl.cluster == 1, 1, &q.test_drop_kb, &q.timeout_ns);
     if (rc == GEMM_OK) rc = encode_rows(&base.u, U, (uint64_t)P, (uint64_t)T, (uint64_t)ldu, kBK, q.u3d ? 2 : 0, bf16);
     if (rc == GEMM_OK)
         rc = encode_rows(&base.v, V, (uint64_t)Q, (uint64_t)T, (uint64_t)ldv, kBK, q.v3d ? 2 : 0, bf16);
@@ -348,6 +348,8 @@ static int run_dw(const void* U, const void* V, void* D, const int32_t* offsets,
     q.q_tiles = pl.q_tiles;
     q.num_stages = pl.num_stages;
     q.bf16 = bf16 ? 1 : 0;
+    q.cluster = pl.cluster;
+    q.D = reinterpret_cast<uint16_t*>(D);
     q.groups = groups;
     q.maps = maps;
     q.err = d.d_err;
@@ -356,7 +358,7 @@ static int run_dw(const void* U, const void* V, void* D, const int32_t* offsets,
         return launch(ragged_dw_kernel<true>, pl.grid, kDwThreads, (size_t)pl.smem_bytes, 2, st, out, q);
     }
     if ((rc = allow_smem(d, 5, ragged_dw_kernel<false>)) != GEMM_OK) return rc;
-    return launch(ragged_dw_kernel<false>, pl.grid, kDwThreads, (size_t)pl.smem_bytes, 1, st, out, q);
+    return launch(ragged_dw_kernel<false>, pl.grid, kDwThreads, (size_t)pl.smem_bytes, pl.cluster, st, out, q);
 }
 
 // ------------------------------------------------------------------ checks

@@ -24,6 +24,10 @@
 // 239 us with four, 216 with eight; 199 with the accumulator released before
 // the stores behind it are visible).
 //
+// Few tiles of long groups are computed by clusters, whose CTAs take shares of
+// the group's blocks and add them up through distributed shared memory, in
+// their order.
+//
 // Bound.  Sums are in 32 bits, rounded once.  At the tensor rate a CTA of a
 // pair takes in 64 bytes per clock, close to what copies reach, and a tile's
 // start and end hide only behind its neighbours' four blocks: that case runs
@@ -52,6 +56,8 @@ struct DwParams {
     int32_t num_stages;
     int32_t u3d, v3d;     // one copy per stage of the operand's two 64-column chunks
     int32_t bf16;
+    int32_t cluster;      // single CTAs: > 1: the CTAs of a cluster share each tile's rows
+    uint16_t* D;
     const DwGroup* groups;      // by length, longest first
     const CUtensorMap* maps;    // [2 * position]: U's and V's of that group
     int32_t* err;
@@ -123,8 +129,10 @@ __global__ void __launch_bounds__(kDwThreads, 1)
     const uint32_t ring = (smem_u32(smem) + (uint32_t)sizeof(Ctrl) + 1023u) & ~1023u;
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = kPair ? cluster_ctarank() : 0u;
-    const uint32_t worker = kPair ? blockIdx.x / 2 : blockIdx.x;
-    const uint32_t workers = kPair ? gridDim.x / 2 : gridDim.x;
+    const bool clustered = !kPair && q.cluster > 1;  // (one item per cluster)
+    const uint32_t share = clustered ? cluster_ctarank() : 0u;
+    const uint32_t worker = kPair ? blockIdx.x / 2 : blockIdx.x / (uint32_t)q.cluster;
+    const uint32_t workers = kPair ? gridDim.x / 2 : gridDim.x / (uint32_t)q.cluster;
     Params w;  // what wait_phase reads
     w.err = q.err;
     w.timeout_ns = q.timeout_ns;
@@ -182,6 +190,12 @@ __global__ void __launch_bounds__(kDwThreads, 1)
         k.g = ahead.x;
         k.lo = ahead.y;
         k.hi = ahead.z;
+        if (clustered) {
+            // an even share of the group's blocks
+            const int32_t blocks = (k.hi - k.lo + kBK - 1) / kBK, c = q.cluster, lo = k.lo;
+            k.lo = lo + (int32_t)share * blocks / c * kBK;
+            k.hi = min(k.hi, lo + ((int32_t)share + 1) * blocks / c * kBK);
+        }
         item += workers;
         look();
         return true;
@@ -294,7 +308,23 @@ __global__ void __launch_bounds__(kDwThreads, 1)
         const uint32_t quarter = warp & 3u, half = warp >= 7 ? 1u : 0u;
         const uint32_t staging = ring + S * stride + (quarter + 4u * half) * 4096u;
         uint32_t local = 0;
-        while (next(k)) {
+        if (clustered && next(k)) {
+            // this CTA's share in 32 bits into its ring (idle by now), column
+            // by column; the cluster adds the shares up below
+            const bool some = k.hi > k.lo;
+            float v[64];
+#pragma unroll
+            for (int j = 0; j < 64; ++j) v[j] = 0.0f;
+            if (some && __all_sync(0xffffffffu, wait_phase(smem_u32(&ctrl->tmem_full[0]), 0, ctrl, w, kErrEpi))) {
+                tc_fence_after();
+                tmem_load_64cols(tmem_base + ((quarter * 32u) << 16) + 64u * half, v);
+                tc_fence_before();
+            }
+#pragma unroll
+            for (int j = 0; j < 64; ++j)
+                st_shared_f32(ring + ((64u * half + (uint32_t)j) * 128u + 32u * quarter + lane) * 4u, v[j]);
+        }
+        while (!clustered && next(k)) {
             const bool some = k.hi > k.lo;
             const uint32_t buf = local & 1u, bph = (local >> 1) & 1u;
             if (some) {
@@ -347,11 +377,40 @@ __global__ void __launch_bounds__(kDwThreads, 1)
         __syncwarp();
     }
 
+    if (clustered) {
+        // sums of the shares, in their order: a warp for 32 rows x 16 columns
+        __syncwarp();
+        cluster_sync();
+        item = worker;
+        look();
+        if (warp >= 2 && warp != 6 && next(k)) {
+            for (uint32_t task = share * 8u + (warp < 6 ? warp - 2u : warp - 3u); task < 32u; task += 8u * (uint32_t)q.cluster) {
+                const uint32_t at = 32u * (task & 3u) + lane, c0 = 16u * (task >> 2);
+                float x[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) x[j] = 0.0f;
+                for (uint32_t r = 0; r < (uint32_t)q.cluster; ++r) {
+                    const uint32_t from = mapa_shared(ring + (c0 * 128u + at) * 4u, r);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) x[j] += ld_shared_cluster(from + (uint32_t)j * 512u);
+                }
+                const int32_t row = k.pt * (int32_t)kTile + (int32_t)at, col = k.qt * (int32_t)kTile + (int32_t)c0;
+                uint16_t* const d = q.D + ((int64_t)k.g * q.P + row) * q.Q + col;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (row < q.P && col + 8 * h < q.Q)
+                        *reinterpret_cast<uint4*>(d + 8 * h) =
+                            make_uint4(pack16(x[8 * h], x[8 * h + 1], q.bf16), pack16(x[8 * h + 2], x[8 * h + 3], q.bf16),
+                                       pack16(x[8 * h + 4], x[8 * h + 5], q.bf16),
+                                       pack16(x[8 * h + 6], x[8 * h + 7], q.bf16));
+            }
+        }
+    }
     __syncthreads();
     if (threadIdx.x == 0 && *(volatile int32_t*)&ctrl->abort_flag) drain_ring(ctrl, full0, S);
     tc_fence_before();
-    if (kPair)
-        cluster_sync_relaxed();
+    if (kPair || clustered)
+        cluster_sync_relaxed();  // the other CTAs' accesses to this one's shared memory are done
     else
         __syncthreads();
     if (warp == 1) {

@@ -25,7 +25,7 @@ struct RaggedPlan {
 
 struct DwPlan {
     int32_t status;
-    int32_t pair, p_tiles, q_tiles, num_stages, smem_bytes, grid;
+    int32_t pair, cluster, p_tiles, q_tiles, num_stages, smem_bytes, grid;
 };
 
 // R == 0: experts' products over G groups; else adapters (G is 1).

@@ -144,6 +144,12 @@ __device__ __forceinline__ void st_shared_f32(uint32_t addr, float x) {
     asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
 }
 
+__device__ __forceinline__ float ld_shared_cluster(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
     uint4 q;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
