@@ -214,8 +214,12 @@ int gemm_relu_noalloc_check_device_error(void* stream);
 
 /* ---- Ragged products: rows of one batch that go through different weights -- */
 
-/* Most groups of one grouped call, and largest rank of an adapter. */
+/* Most groups and most rows of one grouped call, and largest rank of an
+ * adapter.  (Rows: 2^31 - 2^26.  The kernels find tiles and their rows in 32
+ * bits; a row number, a tile count of at least 64 rows each and a tile's
+ * rounding have to fit there together.) */
 #define GEMM_RELU_MAX_GROUPS 1024
+#define GEMM_RELU_MAX_ROWS 2080374784LL
 #define GEMM_RELU_MAX_RANK 512
 
 /*
@@ -242,7 +246,7 @@ int gemm_relu_noalloc_check_device_error(void* stream);
  * row-major (GEMM_B_KN) or (N, K) (GEMM_B_NK).  All hold `dtype` elements;
  * pointers are 16-byte aligned (offsets 4-byte), K % 8 == 0 and N % 8 == 0.
  * Output must not overlap an input (not checked).  0 <= G <=
- * GEMM_RELU_MAX_GROUPS.  A reduction of length 0 (K, N or no row) gives +0.
+ * GEMM_RELU_MAX_GROUPS, 0 <= T <= GEMM_RELU_MAX_ROWS.  A reduction of length 0 (K, N or no row) gives +0.
  *
  * Arithmetic as gemm_relu's: exact products accumulated in fp32, one
  * rounding to nearest-even at the end; results do not depend on the order in

@@ -60,6 +60,33 @@ def test_row_matrices(gemm_lib, call, rows):
         assert call(L, act=GOOD, ld_act=0) == 1
 
 
+MAX_ROWS = 2 ** 31 - 2 ** 26  # GEMM_RELU_MAX_ROWS
+
+
+@pytest.mark.parametrize("call", [grouped, grouped_dx, grouped_dw], ids=lambda f: f.__name__)
+def test_rows_whose_tiles_leave_32_bits(gemm_lib, call):
+    """Row counts from which tile counts, widths or loop ends pass 2^31 on the
+    device are refused before any launch, for any group count."""
+    L = gemm_lib.lib()
+    for T in (MAX_ROWS + 1, 2 ** 31 - 2 ** 23, 2 ** 31 - 128, 2 ** 31 - 1):
+        for G in (1, 80, 1024):
+            assert call(L, T=T, G=G) == 1, (T, G)
+    if not torch.cuda.is_available():  # the checks pass, no device is found
+        assert call(L, T=MAX_ROWS) == 3
+    # what the kernels add to a row number, a group's length or its end: its
+    # tiles (64 rows at least), a tile's width, a block of 128 rows, a grid
+    assert MAX_ROWS + -(-MAX_ROWS // 64) + 256 < 2 ** 31
+
+
+def test_adapters_take_rows_in_blocks(gemm_lib):
+    """Adapters' rows go in blocks of their own, so their number is bounded by
+    the dimensions' limit alone."""
+    L = gemm_lib.lib()
+    assert adapters(L, T=1 << 31) == 1
+    if not torch.cuda.is_available():
+        assert adapters(L, T=2 ** 31 - 1) == 3
+
+
 def test_nothing_to_do_needs_no_pointer(gemm_lib):
     L = gemm_lib.lib()
     none = dict(X=None, W=None)

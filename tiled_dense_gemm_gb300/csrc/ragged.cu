@@ -372,6 +372,10 @@ static int check_matrix(const void* ptr, int64_t width, int64_t ld) {
     return GEMM_OK;
 }
 
+// Grouped products: no row number of a call, nor a sum of one with a tile count
+// or a tile's width, leaves 32 bits on the device.
+static bool rows_ok(int64_t T) { return T <= GEMM_RELU_MAX_ROWS; }
+
 static int check_common(int64_t T, int64_t G, int64_t N, int64_t K, int b_layout, int dtype) {
     if (!dim_ok(T) || !dim_ok(N) || !dim_ok(K) || G < 0 || G > GEMM_RELU_MAX_GROUPS) return GEMM_ERR_INVALID_ARG;
     if ((b_layout != GEMM_B_KN && b_layout != GEMM_B_NK) || (dtype != GEMM_DTYPE_F16 && dtype != GEMM_DTYPE_BF16))
@@ -396,6 +400,7 @@ extern "C" int gemm_relu_grouped(const void* X, const void* W, void* Y, const in
                                  int dtype, void* stream) {
     int rc = check_common(T, G, N, K, b_layout, dtype);
     if (rc != GEMM_OK) return rc;
+    if (!rows_ok(T)) return GEMM_ERR_INVALID_ARG;
     if (T == 0 || N == 0) return GEMM_OK;
     if ((rc = check_matrix(Y, N, ldy)) != GEMM_OK) return rc;
     const bool empty = G == 0 || K == 0;
@@ -419,6 +424,7 @@ extern "C" int gemm_relu_grouped_dx(const void* dY, const void* W, void* dX, con
                                     int64_t ld_act, int b_layout, int dtype, void* stream) {
     int rc = check_common(T, G, N, K, b_layout, dtype);
     if (rc != GEMM_OK) return rc;
+    if (!rows_ok(T)) return GEMM_ERR_INVALID_ARG;
     if (T == 0 || K == 0) return GEMM_OK;
     if ((rc = check_matrix(dX, K, ld_dx)) != GEMM_OK) return rc;
     const bool empty = G == 0 || N == 0;
@@ -445,6 +451,7 @@ extern "C" int gemm_relu_grouped_dw(const void* X, const void* dY, void* dW, con
                                     int dtype, void* stream) {
     int rc = check_common(T, G, N, K, b_layout, dtype);
     if (rc != GEMM_OK) return rc;
+    if (!rows_ok(T)) return GEMM_ERR_INVALID_ARG;
     if (G == 0 || N == 0 || K == 0) return GEMM_OK;
     if ((rc = check_matrix(dW, 0, 0)) != GEMM_OK) return rc;
     if (T > 0) {
