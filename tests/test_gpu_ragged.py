@@ -668,3 +668,50 @@ def test_the_hook_is_refused_where_it_does_not_apply(monkeypatch):
         torch.zeros(40, dtype=torch.int32, device=DEV)))
     monkeypatch.delenv("GEMM_RELU_TEST_DROP_KB")
     binding.check_device_error()
+
+
+def test_adapters_of_many_rows_on_two_streams_and_in_a_graph():
+    """Calls whose low-rank products are tiles of their own, on two streams of
+    unequal priority while a third one holds part of the GPU: each call ends
+    whatever share of the GPU it gets, and its result is the one it has alone.
+    Then the same calls captured, and replayed on other inputs."""
+    K, N, R, rank = 264, 1032, 40, 40
+    w, a, b = normal((K, N), 1, "bf16", K ** -0.5), normal((R, rank, K), 2, "bf16", K ** -0.5), normal((R, rank, N), 3, "bf16", rank ** -0.5)
+    sets = [(normal((T, K), T, "bf16"), make_ids(T, R, "mixed", T)) for T in (1100, 2600)]
+    alone = [binding.gemm_relu_adapters(x, w, a, b, ids) for x, ids in sets]
+    binding.check_device_error()
+    for (x, ids), y in zip(sets, alone):
+        ref.check(y, ref.adapters(x, w, a, b, ids, None, True, "kn"), f"{len(ids)} rows")
+    xd, wd = normal((2048, 2048), 4, "f16"), normal((2048, 1024), 5, "f16", 0.02)
+    low, high = torch.cuda.Stream.priority_range()
+    streams = [torch.cuda.Stream(priority=low), torch.cuda.Stream(priority=high)]
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(20):
+        with torch.cuda.stream(other):
+            binding.gemm_relu(xd, wd)
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                outs[i].append(binding.gemm_relu_adapters(sets[i][0], w, a, b, sets[i][1]))
+    torch.cuda.synchronize()
+    binding.check_device_error()
+    for i in range(2):
+        assert all(torch.equal(y, alone[i]) for y in outs[i])
+    x, ids = (t.clone() for t in sets[0])
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        binding.gemm_relu_adapters(x, w, a, b, ids)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            y = binding.gemm_relu_adapters(x, w, a, b, ids)
+            z = binding.gemm_relu_adapters(x, w, a, b, ids, apply_relu=False)
+    x.copy_(sets[1][0][:1100])
+    ids.copy_(sets[1][1][:1100])
+    torch.cuda.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    binding.check_device_error()
+    ref.check(y, ref.adapters(x, w, a, b, ids, None, True, "kn"), "replayed")
+    ref.check(z, ref.adapters(x, w, a, b, ids, None, False, "kn"), "replayed, no ReLU")

@@ -42,7 +42,6 @@ struct SlotParams {
     const int32_t* ids;
     int32_t* slots;      // [tile][cap]
     int32_t* nslots;     // [tile]
-    uint32_t* low_done;  // [tile], set to zero
     int32_t T, R, cap, tile_w;
     int32_t* err;
 };
@@ -84,7 +83,6 @@ __global__ void __launch_bounds__(256) adapters_slots_kernel(const __grid_consta
         int32_t n = 0;
         for (int32_t w = 0; w < 8; ++w) n += count[w];
         p.nslots[blockIdx.x] = n;
-        p.low_done[blockIdx.x] = 0u;
     }
 }
 

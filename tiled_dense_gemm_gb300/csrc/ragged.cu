@@ -211,7 +211,7 @@ static int run_forward(const void* X, const void* W, void* Y, const int32_t* off
     p.num_stages = pl.num_stages;
     p.stage_bytes = pl.stage_bytes;
     p.turn_off = pl.num_stages * pl.stage_bytes;
-    const int threads = pl.low_in_main ? kHelped : row_threads(ad != nullptr);
+    const int threads = pl.low_grid ? kHelped : row_threads(ad != nullptr);
     p.table_off = p.turn_off + (threads - 96) * (int)kTurnPitch;
     p.tmem_cols = (uint32_t)pl.tmem_cols;
     p.w_kmajor = w_kmajor ? 1 : 0;
@@ -255,7 +255,7 @@ static int run_forward(const void* X, const void* W, void* Y, const int32_t* off
         // one buffer: the low-rank rows, the tiles' slot lists, their lengths
         const size_t low_bytes = ((size_t)T * 2 * pl.rank_pad * 2 + 255) / 256 * 256;
         const size_t slot_bytes = (size_t)tiles * pl.cap * 4;
-        rc = rt::grow(&sb.rg_misc, &sb.rg_misc_bytes, low_bytes + slot_bytes + (size_t)tiles * 8, st, false);
+        rc = rt::grow(&sb.rg_misc, &sb.rg_misc_bytes, low_bytes + slot_bytes + (size_t)tiles * 4, st, false);
         if (rc != GEMM_OK) return rc;
         uint8_t* base = reinterpret_cast<uint8_t*>(sb.rg_misc);
         p.low = reinterpret_cast<const uint16_t*>(base);
@@ -265,7 +265,6 @@ static int run_forward(const void* X, const void* W, void* Y, const int32_t* off
             q.ids = ad->ids;
             q.slots = reinterpret_cast<int32_t*>(base + low_bytes);
             q.nslots = reinterpret_cast<int32_t*>(base + low_bytes + slot_bytes);
-            q.low_done = reinterpret_cast<uint32_t*>(q.nslots + tiles);
             q.T = (int32_t)T;
             q.R = (int32_t)ad->R;
             q.cap = pl.cap;
@@ -275,9 +274,8 @@ static int run_forward(const void* X, const void* W, void* Y, const int32_t* off
             if (rc != GEMM_OK) return rc;
             p.slots = q.slots;
             p.nslots = q.nslots;
-            p.low_done = q.low_done;
         }
-        if (pl.low_in_main) {
+        if (pl.low_grid) {
             const uint64_t dims[3] = {(uint64_t)K, (uint64_t)ad->rank, (uint64_t)ad->R};
             const uint64_t strides[2] = {(uint64_t)K, (uint64_t)(K * ad->rank)};
             const uint32_t box[3] = {64, (uint32_t)pl.rank_box, 1};
@@ -287,8 +285,14 @@ static int run_forward(const void* X, const void* W, void* Y, const int32_t* off
                 rc = encode_stack(&m.a4, ad->A, (uint64_t)K, (uint64_t)ad->rank, (uint64_t)ad->R,
                                   (uint32_t)pl.rank_box, true, bf16);
             if (rc != GEMM_OK) return rc;
+            // the low-rank products as items of the same kernel, in a launch of their
+            // own: tiles of Y wait for it as a whole, never for other CTAs of theirs
             p.low_out = reinterpret_cast<uint16_t*>(base);
             p.scale = ad->scale;
+            if ((rc = allow_smem(d, 0, ragged_kernel<true, true>)) != GEMM_OK) return rc;
+            rc = launch(ragged_kernel<true, true>, pl.low_grid, row_threads(true), (size_t)pl.smem_bytes, 2, st, m, p);
+            if (rc != GEMM_OK) return rc;
+            p.low_out = nullptr;
         } else {
             rc = run_low(X, *ad, reinterpret_cast<uint16_t*>(base), T, K, ldx, pl, bf16, d, st);
             if (rc != GEMM_OK) return rc;

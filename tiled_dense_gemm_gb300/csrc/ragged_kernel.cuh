@@ -144,8 +144,7 @@ struct Params {
     int32_t per_slot;        // rank_pad / rank_box
     int32_t R;
     const float* scale;      // of each adapter, or null: 1
-    uint16_t* low_out;       // pairs: the low-rank products are items of this launch (null: another kernel's)
-    uint32_t* low_done;      // ... and count themselves here, per row tile (zero at the start)
+    uint16_t* low_out;       // pairs: this launch's items are the low-rank products (null: columns of Y)
 };
 
 struct __align__(8) Ctrl {
@@ -342,7 +341,7 @@ struct Item {
     int32_t n;          // column tile
     int32_t kb0, kb1;   // this CTA's k-blocks [kb0, kb1)
     int32_t x0, x1;     // ... and extra ones (adapters)
-    bool low;           // low-rank products of the row tile (n: which 256 of them), not columns of Y
+    bool low;           // low-rank products of the row tile (n: which of them), not columns of Y
 };
 
 // The slot (position among a row tile's adapters) that box `box` of its
@@ -420,8 +419,7 @@ struct Iter {
     const int32_t* start;
     const int32_t* tiles;
     const int32_t* nslots;
-    const int32_t* lows;  // adapters of pairs: low items before each row tile
-    uint32_t n_low;       // items [0, n_low) are low ones
+    const int32_t* lows;  // a launch of low items: those before each row tile
     uint32_t u, u1, step;
     int32_t share;      // this CTA's rank in its cluster
     int32_t max_extra;  // single CTAs of adapters: the one row tile's extra k-blocks
@@ -430,10 +428,8 @@ struct Iter {
                                     const int32_t* nslots_, const int32_t* lows_, uint32_t worker, uint32_t workers,
                                     int32_t max_extra_, int32_t share_)
         : p(p_), start(start_), tiles(tiles_), nslots(nslots_), lows(lows_), share(share_), max_extra(max_extra_) {
-        const uint32_t items = (uint32_t)tiles[p.G] * (uint32_t)p.n_tiles;
-        n_low = kPair && kAdapters && p.low_out ? (uint32_t)lows[tiles[p.G]] : 0u;
         u = worker;
-        u1 = n_low + items;
+        u1 = kPair && kAdapters && p.low_out ? (uint32_t)lows[tiles[p.G]] : (uint32_t)tiles[p.G] * (uint32_t)p.n_tiles;
         step = workers;
     }
 
@@ -451,7 +447,7 @@ struct Iter {
 
     __device__ __forceinline__ bool next(Item& it) {
         if (u >= u1) return false;
-        uint32_t item = u;
+        const uint32_t item = u;
         u += step;
         it.kb0 = it.x0 = it.x1 = 0;
         it.kb1 = p.num_kb;
@@ -467,7 +463,7 @@ struct Iter {
         }
         it.low = false;
         if constexpr (kPair && kAdapters) {
-            if (item < n_low) {
+            if (p.low_out) {
                 int32_t lo = 0, hi = tiles[p.G];  // largest row tile with lows[tile] <= item
                 while (hi - lo > 1) {
                     const int32_t mid = (lo + hi) >> 1;
@@ -481,7 +477,6 @@ struct Iter {
                 it.x1 = 0;
                 return true;
             }
-            item -= n_low;
         }
         const uint32_t nt = (uint32_t)p.n_tiles;
         const int32_t rt = (int32_t)(item / nt);
@@ -597,20 +592,22 @@ __global__ void __maxnreg__(128)  // (adapters: leaves room for a block of the l
         tma_prefetch_desc(&maps.w);
         tma_prefetch_desc(&maps.x[0]);
     }
-    grid_launch_dependents();
     // Nothing before this reads or writes global memory.  The adapters' main
-    // kernel goes on: the kernel before it in the stream computes low and
+    // launch goes on: the one before it in the stream computes low and
     // nothing else, and lets this one start only after it has itself waited
     // for all that came before, so X, W, ids, the slot lists and the
     // workspace are ready and Y is free; low alone is waited for where it is
-    // read, after the main k-blocks.
-    // Where the low-rank products are this launch's own items, the kernel
-    // before it is any kernel.
-    if (!kAdapters || (kPair && p.low_out)) grid_dependency_wait();
+    // read, after the main k-blocks.  (So a launch of low items waits first.
+    // The main one starts only once all its CTAs have, that is, are resident
+    // or done: what the main CTAs wait for never waits for a place of theirs.)
+    const bool lows_only = kPair && kAdapters && p.low_out;
+    if (lows_only) grid_dependency_wait();
+    grid_launch_dependents();
+    if (!kAdapters) grid_dependency_wait();
     int32_t* const lows = tiles + p.G + 1;
     if (warp == 6) {
         build_table(p, start, tiles, lane, workers);
-        if (kPair && kAdapters && p.low_out) {
+        if (lows_only) {
             __syncwarp();
             int32_t before = 0;
             for (int32_t t0 = 0; t0 < tiles[1]; t0 += 32) {
@@ -1091,26 +1088,7 @@ __global__ void __maxnreg__(128)  // (adapters: leaves room for a block of the l
             const int32_t y = it.row0 + (int32_t)(rank * rows);
             bool ok = true;     // (alike in all threads)
             bool armed = true;  // of the thread that arms
-            if (kPair && p.low_out) {
-                // low items come first in every CTA's list: this ends
-                if (et == 0) {
-                    volatile uint32_t* const done = p.low_done + it.tile;
-                    volatile int32_t* const abort_flag = &ctrl->abort_flag;
-                    const uint32_t want = 2u * (uint32_t)low_items(p, slots);
-                    const uint64_t t0 = globaltimer_ns();
-                    while (*done < want)
-                        if (*abort_flag || globaltimer_ns() - t0 > p.timeout_ns) {
-                            *abort_flag = 1;
-                            atomicCAS(p.err, 0, (int32_t)kErrEpi);
-                            ok = false;
-                            break;
-                        }
-                    __threadfence();
-                }
-                ok = named_bar_and(kEpiBarrier, kEpi, ok);
-            } else {
-                grid_dependency_wait();
-            }
+            grid_dependency_wait();  // low is complete
             const uint32_t v = et & 15u, r0 = et >> 4;
             int32_t who[kPair ? 16 : 1];  // adapters of rows r0, r0 + 8, ...
             if constexpr (kPair) {
@@ -1208,7 +1186,6 @@ __global__ void __maxnreg__(128)  // (adapters: leaves room for a block of the l
                 }
             };
             if constexpr (kPair && kAdapters) {
-                if (it.low && half) return ready();  // (only to keep up with the accumulators' phases)
                 if (it.low) {
                     const int32_t slots = nslots[it.tile];
                     const int32_t held = low_boxes(p, slots) * p.rank_box;  // products of each CTA
@@ -1274,9 +1251,6 @@ __global__ void __maxnreg__(128)  // (adapters: leaves room for a block of the l
                         }
                     }
                     release();
-                    __threadfence();
-                    named_bar_sync(kEpiBarrier, kEpi);
-                    if (et == 0) atomicAdd(p.low_done + it.tile, 1u);
                     return true;
                 }
             }
@@ -1357,7 +1331,7 @@ __global__ void __maxnreg__(128)  // (adapters: leaves room for a block of the l
             }
             // with helping warps these fill the next item's extra k-blocks while
             // those drain this one
-            if (ok && (!helpers || half || it.low)) ok = drain(it, local);
+            if (ok && (!helpers || half)) ok = drain(it, local);
             if (kAdapters && half) {
                 __threadfence_block();
                 __syncwarp();
@@ -1430,7 +1404,7 @@ __global__ void __maxnreg__(128)  // (adapters: leaves room for a block of the l
         }
     }
     // (a later kernel's wait covers this one only: it must not end first)
-    if (kAdapters && !p.low_out) grid_dependency_wait();
+    if (kAdapters && !lows_only) grid_dependency_wait();
     __syncthreads();
     if (threadIdx.x == 0 && *(volatile int32_t*)&ctrl->abort_flag) drain_ring(ctrl, full0, S);
     tc_fence_before();

@@ -63,7 +63,7 @@ RaggedPlan plan_rows(int64_t T, int64_t G, int64_t N, int64_t K, int64_t R, int6
         p.status = GEMM_ERR_UNSUPPORTED_DEVICE;
         return p;
     }
-    p.low_in_main = R > 0 && p.pair && T > kLowRows;
+    const bool low_tiles = R > 0 && p.pair && T > kLowRows;
     if (R > 0) {
         // As the kernel does for groups: tiles of the width whose waves take the
         // shortest time, if that is 5% less than with up to 256 rows (1500 rows,
@@ -83,10 +83,10 @@ RaggedPlan plan_rows(int64_t T, int64_t G, int64_t N, int64_t K, int64_t R, int6
             }
         }
     }
-    const int64_t table = (R > 0 && !p.low_in_main ? 1 : 2) * kTurn +
+    const int64_t table = (R > 0 && !low_tiles ? 1 : 2) * kTurn +
                           round_up((2 * (G + 1) + (R == 0 ? 0 : p.pair ? p.row_tiles + 1 : 389)) * 4, 16);
     // (adapters: room beside it for a block of the kernel that computes low)
-    const int64_t room = kSmem - kCtrl - table - (R > 0 && !p.low_in_main ? kLowSmem : 0);
+    const int64_t room = kSmem - kCtrl - table - (R > 0 && !low_tiles ? kLowSmem : 0);
     p.num_stages = (int32_t)std::min<int64_t>(8, room / p.stage_bytes);
     p.smem_bytes = (int32_t)(kCtrl + (int64_t)p.num_stages * p.stage_bytes + table);
     // accumulators are read 32 columns at a time; allocations are powers of two
@@ -102,6 +102,12 @@ RaggedPlan plan_rows(int64_t T, int64_t G, int64_t N, int64_t K, int64_t R, int6
         p.rank_box = 8;
         while (p.rank_box < 64 && p.rank_box < rank) p.rank_box *= 2;
         p.rank_pad = (int32_t)round_up(rank, p.rank_box);
+    }
+    if (low_tiles) {
+        // (pairs have no more to do than every row tile with an adapter per row)
+        const int64_t boxes = std::min<int64_t>(p.row_width, R) * (p.rank_pad / p.rank_box);
+        const int64_t most = p.rank_box == 64 ? ceil_div(boxes, 2) : ceil_div(boxes * p.rank_box, 256);
+        p.low_grid = 2 * (int32_t)std::min<int64_t>(pairs, p.row_tiles * most);
     }
     // (the kernel may cut pairs' groups into tiles of half that)
     if (items > kIndexMax / 2) {

@@ -20,7 +20,7 @@ struct RaggedPlan {
     int32_t stage_bytes, num_stages, smem_bytes, tmem_cols;
     int32_t grid;        // CTAs
     int32_t rank_box, rank_pad;
-    int32_t low_in_main; // adapters: the low-rank products are items of the main launch
+    int32_t low_grid;    // adapters: > 0: the low-rank products come from a launch of tensor-core tiles, its CTAs
 };
 
 struct DwPlan {
