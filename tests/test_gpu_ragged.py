@@ -715,3 +715,20 @@ def test_adapters_of_many_rows_on_two_streams_and_in_a_graph():
     binding.check_device_error()
     ref.check(y, ref.adapters(x, w, a, b, ids, None, True, "kn"), "replayed")
     ref.check(z, ref.adapters(x, w, a, b, ids, None, False, "kn"), "replayed, no ReLU")
+
+
+@pytest.mark.parametrize("T,R,rank,kind", [(1100, 200, 512, "mixed"), (1400, 90, 136, "mixed"), (3000, 256, 8, "mixed"), (2300, 64, 24, "runs")])
+def test_adapters_with_many_low_rank_tiles_per_block(T, R, rank, kind):
+    """Tens of tiles of low-rank products on each pair of CTAs (200 adapters of
+    rank 512 in each row tile), then several tiles of Y with as many extra
+    k-blocks: every accumulator's turn is taken by the warps that release it.
+    Five calls give the same bits."""
+    K, N = 136, 72 if rank > 100 else 4104
+    x, a, b = normal((T, K), 1, "bf16"), normal((R, rank, K), 2, "bf16", K ** -0.5), normal((R, rank, N), 3, "bf16", rank ** -0.5)
+    w, ids = normal((K, N), 4, "bf16", K ** -0.5), make_ids(T, R, kind, 5)
+    y = binding.gemm_relu_adapters(x, w, a, b, ids, apply_relu=False)
+    binding.check_device_error()
+    ref.check(y, ref.adapters(x, w, a, b, ids, None, False, "kn"), f"T={T} R={R} rank {rank}")
+    for _ in range(4):
+        assert torch.equal(y, binding.gemm_relu_adapters(x, w, a, b, ids, apply_relu=False))
+    binding.check_device_error()

@@ -560,6 +560,10 @@ __global__ void __maxnreg__(128)  // (adapters: leaves room for a block of the l
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = kPair ? cluster_ctarank() : 0u;
     const bool clustered = !kPair && p.cluster > 1;
+    // A launch of low items has no helping warps.  They wait on an
+    // accumulator's phase parity, so they have to be the ones that release
+    // every accumulator they pass: were one released by other warps, two more
+    // items could end before they look, and the parity would be that of a later one.
     const bool helpers = kPair && kAdapters && blockDim.x == kHelped;
     const uint32_t share = clustered ? cluster_ctarank() : 0u;
     const uint32_t worker = kPair ? blockIdx.x / 2 : clustered ? blockIdx.x / (uint32_t)p.cluster : blockIdx.x;
