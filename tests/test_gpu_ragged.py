@@ -732,3 +732,29 @@ def test_adapters_with_many_low_rank_tiles_per_block(T, R, rank, kind):
     for _ in range(4):
         assert torch.equal(y, binding.gemm_relu_adapters(x, w, a, b, ids, apply_relu=False))
     binding.check_device_error()
+
+
+# (T > 128: pairs; rank 8 and an odd number of adapters in a row tile: a box of
+# zeros pads the last extra k-block's products)
+@pytest.mark.parametrize("T", [7, 128, 200, 1000, 1300])
+@pytest.mark.parametrize("rank", [8, 5, 16, 24])
+def test_ids_outside_the_range_count_as_none(T, rank):
+    """Whatever value an id outside [-1, R) has, its row is one without
+    adapter, also where an earlier call left NaN in the workspace."""
+    for R in (1, 3):
+        K, N = 64, 72
+        for dtype in ("f16", "bf16"):
+            x, a, b, w = normal((T, K), 1, dtype), normal((R, rank, K), 2, dtype, 0.1), normal((R, rank, N), 3, dtype), normal((K, N), 4, dtype, 0.1)
+            ids = (torch.arange(T, device=DEV) % R).int()
+            sick = ids.clone()
+            bad = torch.tensor([-2, -3, -4, -5, R, R + 1, -(2 ** 31), 2 ** 31 - 1, -3, -3], dtype=torch.int32, device=DEV)
+            at = torch.arange(T, device=DEV)[1::5]
+            sick[at] = bad[torch.arange(len(at), device=DEV) % len(bad)]
+            if T > 200:
+                sick[40:90] = -3
+            none = torch.where((sick >= 0) & (sick < R), sick, torch.full_like(sick, -1))
+            binding.gemm_relu_adapters(x, w, torch.full_like(a, float("nan")), b, ids)  # NaN in every row's low-rank part
+            y = binding.gemm_relu_adapters(x, w, a, b, sick, apply_relu=False)
+            with pytest.raises(binding.GemmReluError, match="GEMM_ERR_INDEX"):
+                binding.check_device_error()
+            ref.check(y, ref.adapters(x, w, a, b, none, None, False, "kn"), f"T={T} R={R} rank {rank} {dtype}")

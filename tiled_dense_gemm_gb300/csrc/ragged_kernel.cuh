@@ -1062,7 +1062,7 @@ __global__ void __maxnreg__(128)  // (adapters: leaves room for a block of the l
         // row t's low-rank part is to have in column n besides.
         auto sick_part = [&](int32_t t, int32_t n) {
             float sum = 0.0f;
-            const int32_t his = t < it.row0 + it.valid && n < p.N ? __ldcg(p.ids + t) : -2, per = kXK >> p.box_shift;
+            const int32_t his = t < it.row0 + it.valid && n < p.N ? __ldcg(p.ids + t) : -1, per = kXK >> p.box_shift;
             for (int32_t box = it.x0 * per; his >= 0 && box < min(it.x1 * per, nslots[it.tile] * p.per_slot); ++box) {
                 if (((ctrl->sick[box >> 5] >> (box & 31)) & 1u) == 0) continue;
                 const int32_t slot = slot_of(p, box), j0 = (box - slot * p.per_slot) * p.rank_box;
@@ -1099,7 +1099,7 @@ __global__ void __maxnreg__(128)  // (adapters: leaves room for a block of the l
 #pragma unroll
                 for (uint32_t j = 0; j < 16; ++j) {
                     const int32_t t = y + (int32_t)(r0 + 8u * j);
-                    who[j] = r0 + 8u * j < rows && t < it.row0 + it.valid ? __ldcg(p.ids + t) : -2;
+                    who[j] = r0 + 8u * j < rows && t < it.row0 + it.valid ? __ldcg(p.ids + t) : -1;
                 }
             }
             // Blocks in flight: stage e + S - 2 is free while the MMAs work
@@ -1115,7 +1115,9 @@ __global__ void __maxnreg__(128)  // (adapters: leaves room for a block of the l
                     if (!ok) break;
                     const int32_t col = issued * kXK + 8 * (int32_t)(v & 7u);
                     const int32_t slot = slot_of(p, col >> p.box_shift);
-                    const int32_t id = slot < slots ? slot_list[(int64_t)it.tile * p.cap + slot] : -3;
+                    // (no row's where no adapter's: rows' ids, as they are, may be anything)
+                    const bool real = slot < slots;
+                    const int32_t id = real ? slot_list[(int64_t)it.tile * p.cap + slot] : -1;
                     const uint16_t* src = p.low + (int64_t)y * 2 * p.rank_pad + (col - slot * p.rank_pad) +
                                           (int32_t)(v >> 3) * p.rank_pad;
                     const uint32_t dst = ring + st * stride + kWBytes + (v >> 3) * rows * 128u;
@@ -1126,13 +1128,13 @@ __global__ void __maxnreg__(128)  // (adapters: leaves room for a block of the l
                     if constexpr (kPair) {
 #pragma unroll
                         for (uint32_t j = 0; j < 16; ++j)
-                            if (r0 + 8u * j < rows) put(r0 + 8u * j, who[j] == id);
+                            if (r0 + 8u * j < rows) put(r0 + 8u * j, real && who[j] == id);
                     } else if ((col & ~15) < slots * p.rank_pad) {
                         // only the rows that the MMAs of these columns read
                         // (all where they begin an accumulator)
                         uint32_t lo = 0, hi = rows;
                         if (issued > e0 || it.kb0 < it.kb1) window(slots, col & ~15, lo, hi);
-                        for (uint32_t i = lo + r0; i < hi; i += 8) put(i, row_ids[i] == id);
+                        for (uint32_t i = lo + r0; i < hi; i += 8) put(i, real && row_ids[i] == id);
                     }
                     copy_async_commit();
                 }
@@ -1209,9 +1211,12 @@ __global__ void __maxnreg__(128)  // (adapters: leaves room for a block of the l
                     // after the transposition: eight products of adapter id, from number j
                     const int32_t col = 32 * (int32_t)quarter + 8 * (int32_t)(lane & 3u);
                     const int32_t slot = slot_of(p, (r0 + col) >> p.box_shift), j = r0 + col - slot * p.rank_pad;
-                    const int32_t id = col < held && slot < slots ? slot_list[(int64_t)it.tile * p.cap + slot] : -3;
+                    // (no row's where this thread holds no adapter's products:
+                    // rows' ids, as they are, may be anything)
+                    const bool real = col < held && slot < slots;
+                    const int32_t id = real ? slot_list[(int64_t)it.tile * p.cap + slot] : -1;
                     // adapter of row c + lane, asked for a chunk ahead
-                    auto who_at = [&](int32_t r) { return r < it.valid ? __ldcg(p.ids + it.row0 + r) : -2; };
+                    auto who_at = [&](int32_t r) { return r < it.valid ? __ldcg(p.ids + it.row0 + r) : -1; };
                     int32_t who = who_at((int32_t)lane);
                     if (!ready()) return false;
                     // (not unrolled: it runs once per item, and the code of all
@@ -1248,7 +1253,7 @@ __global__ void __maxnreg__(128)  // (adapters: leaves room for a block of the l
                             __syncwarp();
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
-                                if (his[i] == id)
+                                if (real && his[i] == id)
                                     *reinterpret_cast<uint4*>(
                                         p.low_out + (int64_t)(it.row0 + c + 8 * i + (int32_t)(lane >> 2)) * 2 * p.rank_pad +
                                         part * p.rank_pad + j) = ld_shared_v4(turn_ld + (uint32_t)i * 8u * kTurnPitch);
