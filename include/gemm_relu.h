@@ -125,8 +125,9 @@ int gemm_relu_host(const void* A_host, const void* B_host, void* C_host,
                    int64_t M, int64_t N, int64_t K, int apply_relu, void* stream);
 
 /*
- * Synchronizes `stream`, then reads and clears the current device's error
- * word.  Returns GEMM_ERR_TIMEOUT if a kernel of this library gave up a
+ * Synchronizes `stream`, then reads the current device's error words and
+ * clears the one it reports (of both, the timeout first and the indexes at the
+ * next check).  Returns GEMM_ERR_TIMEOUT if a kernel of this library gave up a
  * bounded wait since the last check (the split-K counters are then reset),
  * GEMM_ERR_INDEX if a ragged product met offsets or ids outside their range,
  * GEMM_ERR_CUDA if the stream reports a CUDA error, else GEMM_OK.

@@ -758,3 +758,27 @@ def test_ids_outside_the_range_count_as_none(T, rank):
             with pytest.raises(binding.GemmReluError, match="GEMM_ERR_INDEX"):
                 binding.check_device_error()
             ref.check(y, ref.adapters(x, w, a, b, none, None, False, "kn"), f"T={T} R={R} rank {rank} {dtype}")
+
+
+@pytest.mark.parametrize("what", ["grouped 0", "dw 0"])
+def test_a_timeout_does_not_hide_bad_offsets(what, monkeypatch):
+    """A launch whose wait runs out and that met offsets outside [0, T]: both
+    are reported, the timeout first, each once."""
+    kb, call, want = HOOKED[what]
+    sizes, K, N = [7, 0, 15, 8, 10], 512, 2048 if "dw" not in what else 256
+    off = offsets_of(sizes)
+    x, w = normal((sum(sizes), K), 1, "f16"), weights(5, K, N, "kn", 2, "f16", K ** -0.5)
+    g = normal((sum(sizes), N), 3, "f16")
+    bad = off.clone()
+    bad[-1] = 41  # one row more than there are
+    monkeypatch.setenv("GEMM_RELU_TEST_DROP_KB", str(kb))
+    call(x, w, g, bad)
+    monkeypatch.delenv("GEMM_RELU_TEST_DROP_KB")
+    for status in (6, 9):  # GEMM_ERR_TIMEOUT, GEMM_ERR_INDEX
+        with pytest.raises(binding.GemmReluError) as e:
+            binding.check_device_error()
+        assert e.value.status == status
+    binding.check_device_error()
+    y = call(x, w, g, off)
+    binding.check_device_error()
+    ref.check(y, want(x, w, g, off), what)

@@ -453,7 +453,7 @@ int run_device(const void* A, const void* B, void* C, int64_t M, int64_t N, int6
 // counter, and report the timeout.  Caller holds g_mu.
 int reset_after_error_locked(DeviceState& d) {
     cudaDeviceSynchronize();
-    cudaMemset(d.d_err, 0, 16);
+    cudaMemset(d.d_err, 0, 4);  // (bad indexes, if any, are the next check's)
     for (auto& s : d.streams) {
         if (s.counters) cudaMemset(s.counters, 0, s.counter_bytes);
         if (s.pack_sync) cudaMemset(s.pack_sync, 0, s.pack_sync_bytes);
@@ -508,7 +508,7 @@ extern "C" int gemm_relu_check_device_error(void* stream) {
     }
     if (err[0] != 0) return reset_after_error_locked(d);
     if (err[1] != 0) {
-        cudaMemset(d.d_err, 0, 16);
+        cudaMemset(d.d_err + 1, 0, 4);
         cudaGetLastError();
         return GEMM_ERR_INDEX;
     }

@@ -77,7 +77,7 @@ int grow(void** buf, size_t* have, size_t need, cudaStream_t stream, bool zero);
 // Enqueue C = ReLU(A . B) on device buffers (plan, workspace, maps, launch).
 int run_device(const void* A, const void* B, void* C, int64_t M, int64_t N, int64_t K, int apply_relu, bool b_nk,
                bool bf16, cudaStream_t st, int dev);
-// A launch gave up part-way: clear the error word and every counter.
+// A launch gave up part-way: clear the word of timed-out waits and every counter.
 int reset_after_error_locked(DeviceState& d);
 // Release the side streams and events of the host-buffer pipeline.
 void pipe_release(StreamBuffers& sb);
