@@ -282,10 +282,14 @@ int gemm_relu_grouped_dw(const void* X, const void* dY, void* dW, const int32_t*
  * X, W, Y, pitches, types, alignment and stream as gemm_relu_grouped with one
  * W.  A row depends on its own adapter only, whatever the others hold.
  *
- * scale * (X A^T) is accumulated and scaled in fp32 and meets B as two numbers
- * of `dtype`, the rounded value and the rounded rest (together 2^-16 of it in
- * bfloat16, 2^-22 in binary16; with binary16 it has to stay within that type's
- * range); everything else is accumulated in fp32 and rounded once.
+ * low = scale * (X A^T) is accumulated and scaled in fp32 and meets B as two
+ * numbers of `dtype`, the rounded value and the rounded rest: together within
+ * 2^-16 |low| in bfloat16, and in binary16 within 2^-22 |low| or 2^-25, whichever
+ * is larger (its smallest step is 2^-24: the relative bound holds from 2^-3 up,
+ * 2^-14 is held to 2^-11 of itself, and values below 2^-25 are lost).  From
+ * 65520 up low is infinite in binary16.  So with binary16 keep scale where low
+ * is of ordinary size, and the rest of the factor in B.  Everything else is
+ * accumulated in fp32 and rounded once.
  * An id outside [-1, R) counts as -1 and is reported as GEMM_ERR_INDEX by
  * the next gemm_relu_check_device_error.
  */

@@ -782,3 +782,40 @@ def test_a_timeout_does_not_hide_bad_offsets(what, monkeypatch):
     y = call(x, w, g, off)
     binding.check_device_error()
     ref.check(y, want(x, w, g, off), what)
+
+
+@pytest.mark.parametrize("T", [5, 200, 1300])
+@pytest.mark.parametrize("power", [-20, -14, -8, 12])
+def test_small_and_large_low_rank_parts(T, power):
+    """Scales of 2^power with second factors of 2^-power (2^12 at most: binary16): low is held to
+    u^2 |low| or half the type's smallest step, and no better is promised; the
+    bound takes that through |B|."""
+    K, N, R, rank = 136, 264, 3, 12
+    for dtype in ("f16", "bf16"):
+        x, a, w = normal((T, K), 1, dtype), normal((R, rank, K), 2, dtype, K ** -0.5), normal((K, N), 4, dtype, 0.1)
+        b = normal((R, rank, N), 3, dtype, 2.0 ** min(-power, 12))
+        ids, scale = make_ids(T, R, "mixed", 5), torch.full((R,), 2.0 ** power, device=DEV)
+        y = binding.gemm_relu_adapters(x, w, a, b, ids, scale, apply_relu=False)
+        binding.check_device_error()
+        ref.check(y, ref.adapters(x, w, a, b, ids, scale, False, "kn"), f"T={T} 2^{power} {dtype}")
+
+
+def test_low_rank_parts_beyond_binary16():
+    """From 65520 up low is infinite in binary16, for the rows of that adapter
+    alone; bfloat16 holds it."""
+    T, K, N, R, rank = 300, 64, 72, 2, 4
+    for dtype in ("f16", "bf16"):
+        x, a, w = normal((T, K), 1, dtype), normal((R, rank, K), 2, dtype, K ** -0.5), normal((K, N), 4, dtype, 0.1)
+        x[:, 0], a[:, :, 0] = 1.0, 8.0  # low > 0 but for a few rows
+        b = normal((R, rank, N), 3, dtype, 2.0 ** -14)
+        ids = (torch.arange(T, device=DEV) % R).int()
+        scale = torch.tensor([1.0, 2.0 ** 16], device=DEV)
+        y = binding.gemm_relu_adapters(x, w, a, b, ids, scale, apply_relu=False)
+        binding.check_device_error()
+        value, bound = ref.adapters(x, w, a, b, ids, scale, False, "kn")
+        if dtype == "bf16":
+            ref.check(y, (value, bound), "bfloat16")
+            continue
+        ref.check(y[ids == 0], (value[::2], bound[::2]), "the other rows")
+        low = (x.double() @ a[1].double().t() * 2.0 ** 16).abs()
+        assert not torch.isfinite(y[(ids == 1) & (low > 65536).any(1)]).any()

@@ -6,8 +6,11 @@
 //
 // The sums are taken in 32 bits, scaled there, and handed on as two numbers
 // of the element type, hi = round(v) and lo = round(v - hi): together they
-// hold v to 2^-16 (bfloat16) or 2^-22 (binary16), so the low-rank part loses
-// nothing that the last rounding of Y would show.  The tensor cores multiply
+// hold v to 2^-16 |v| (bfloat16), or to 2^-22 |v| or 2^-25, whichever is larger
+// (binary16, whose smallest step is 2^-24 and whose values end at 65504).  For
+// values of ordinary size the low-rank part so loses nothing that the last
+// rounding of Y would show; small ones lose in binary16 (2^-14: 2^-11 of it),
+// since the scale is in v.  The tensor cores multiply
 // both with the same B, which costs them twice a product that is a few
 // percent of the whole, and no memory traffic.
 #pragma once
