@@ -261,7 +261,8 @@ def gemm_relu_host(a, b, c=None, apply_relu: bool = True, stream=None, device=No
 
 def check_device_error(stream=None, device=None):
     """Synchronize ``stream`` and raise if a kernel of this library reported
-    a timed-out wait since the last check."""
+    a timed-out wait, or offsets or ids outside their range, since the last
+    check (of both, the timeout first)."""
     import torch
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     with torch.cuda.device(dev):

@@ -81,7 +81,8 @@ static int launch(void (*fn)(P...), int grid, int threads, size_t smem, int clus
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     // set-up may overlap the previous kernel of the stream (every kernel here
-    // waits for it before it touches global memory)
+    // waits for it before it touches global memory; the adapters' main one goes
+    // by the wait of the launch before it)
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     unsigned n = 1;
@@ -173,7 +174,12 @@ static int run_low(const void* X, const Adapters& ad, uint16_t* low, int64_t T, 
     q.bf16 = bf16 ? 1 : 0;
     q.wide = K % 16 == 0 && ldx % 16 == 0 && !misaligned(X, 32) && !misaligned(ad.A, 32);
     q.err = d.d_err;
-    // a block's adapters are shared by as many CTAs as it can have
+    // A block's adapters are shared by as many CTAs as it can have, or by two,
+    // which take them in turn, where the row blocks are many (times with 2 / 16;
+    // 4096 x 4096, 32 adapters of rank 64, another one from row to row: 64 rows 45
+    // / 30 us, 128 56 / 42, 400 104 / 109, 512 104 / 116, 1000 147 / 160; 1024 x
+    // 1024, 16 of rank 16: 300 rows 27 / 20, 700 25 / 25, 1000 25 / 28; twenty
+    // requests in runs, 700 rows, 4096 x 4096: 44 / 51).
     q.slot_step = (int32_t)std::min<int64_t>({T <= 512 ? 16 : 2, T, ad.R});
     const int nt = std::min(pl.rank_box / 8, 2);
     q.passes = pl.rank_pad / (8 * nt);

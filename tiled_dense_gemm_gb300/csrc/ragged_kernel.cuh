@@ -19,28 +19,28 @@
 // prefix arrays in shared memory (first row, row tiles before the group);
 // item i is then (group, row tile, column tile) by binary search, with no
 // host round trip and no launch of its own.  A group's rows are cut into
-// tiles of equal width, so 260 rows are 144 + 116 and not 256 + 4.
+// tiles of equal width, so a pair's 260 rows are 160 + 100 and not 256 + 4.
 //
 // Column tiles that are few (short calls) are computed by clusters: each CTA
 // takes a share of the tile's k-blocks and the cluster adds the shares up
 // through distributed shared memory.
 //
-// Roles (352 threads, 224 with adapters; one CTA per SM): warp 0 copies row
-// tiles, warp 6 the weights, warp 1 issues the MMAs, warps 2-5 and 7-10 (2-5)
-// drain the accumulators;
-// shared-memory ring of 128-k stages, two TMEM accumulators.  Every wait is
+// Roles (352 threads; 224 with adapters, but 352 where warps 7-10 help; one CTA
+// per SM): warp 0 copies row tiles, warp 6 the weights, warp 1 issues the MMAs,
+// warps 2-5 and 7-10 (2-5) drain the accumulators; shared-memory ring of 128-k stages, two TMEM accumulators.  Every wait is
 // bounded.  The epilogue turns D^T round in shared memory (each warp its own
 // 32 x 32 blocks), applies the ReLU or the gate in 32 bits or on the rounded
 // value, and rounds once, to the output's type.
 //
-// What bounds it, and what it measured (bfloat16 or binary16, launches one
-// after another, inputs beyond L2):
+// What bounds it, and what it measured (bfloat16 or binary16; the GPU's time
+// alone, of calls in a CUDA graph whose inputs rotate beyond L2.  Long runs of
+// single calls settle at a lower clock: the large cases take 10-15% more there):
 //   few rows per group: the weights' way from DRAM.  64 groups of 4096 x
 //     2048, 256 rows: 152-154 us, 7.0 TB/s.
 //   many: bytes into the multiprocessors.  A pair takes 256 x (rows of the
 //     tile) products per k from L2, and tiles of ragged groups are narrower
-//     than 256: 32 groups of 2048 x 4096, 16384 rows: 186-189 us,
-//     1470 TFLOP/s, with 14.6 TB/s from L2 (159 us with the weights' copies left
+//     than 256: 32 groups of 2048 x 4096, 16384 rows: 184-189 us,
+//     1480 TFLOP/s, with 13.2 TB/s from L2 (159 us with the weights' copies left
 //     out, 157 us with the MMAs left out: neither hides the other wholly).
 //     Stages of 64 k (six of them) instead of 128 (three): 197 us.
 //   row pitches that are not multiples of 128 bytes cost a second copy per
@@ -48,9 +48,9 @@
 //     2056 x 3000, 65 us.
 //   rows with adapters: as above, and the second factors and the low-rank
 //     products in extra k-blocks at the end of each tile, ~0.9 us each
-//     (64 rows, 48 adapters of rank 32, 8192 x 8192: 48 us, of which DRAM
-//     takes 32; 8192 rows, 24 adapters of rank 64, 4096 x 4096: 196 us, of
-//     which ~150 us are the shared product's and ~30 the wait for low).
+//     (64 rows, 48 adapters of rank 32, 8192 x 8192: 48-49 us, of which DRAM
+//     takes 32; 8192 rows, 24 adapters of rank 64, 4096 x 4096: 202 us, of
+//     which ~150 us are the shared product's and ~35 the launch of low before).
 #pragma once
 
 #include <cuda_bf16.h>

@@ -10,6 +10,16 @@ constexpr int64_t kSmem = 227 * 1024;  // per CTA
 constexpr int64_t kCtrl = 1024;
 constexpr int64_t kStageK = 128;       // k-rows per ring stage
 constexpr int64_t kTurn = 128 * 80;    // the epilogue's transposition, four warps
+// Adapters of pairs: up to this many rows the low-rank products come from the
+// warp-level kernel beside the main one, beyond from a launch of tensor-core
+// tiles.  The first reads a row block's own adapters only, the second every
+// adapter of a row tile for all its rows, so which is faster goes by how the
+// rows mix, which the host does not know (times so / with tiles).  Twenty
+// requests in runs: 1024 x 1024, 16 adapters of rank 16, 1000 rows 15.4 / 19.5 us,
+// 3000 rows 19.3 / 26.3; 4096 x 4096, 32 of rank 64, 300 rows 43.7 / 42.4, 1000
+// 51.0 / 47.0, 2000 73.8 / 78.6, 3000 101.8 / 101.0.  Another adapter from row to
+// row, same sizes: 1000 rows 25.4 / 24.9, 3000 38.6 / 30.8; 300 rows 100 / 93, 1000
+// 147 / 105, 3000 386 / 265.
 constexpr int64_t kLowRows = 1024;
 constexpr int64_t kLowSmem = 6 * 1024;
 constexpr int64_t kIndexMax = 0x7fffffff;
@@ -39,9 +49,11 @@ RaggedPlan plan_rows(int64_t T, int64_t G, int64_t N, int64_t K, int64_t R, int6
     // single CTAs and pairs take the same time (64 groups of 4096 x 2048, 64
     // rows each: 163 us both; 4 rows: 153 and 154); above, pairs move fewer
     // bytes per operation into the multiprocessors (128 rows each: 171 us
-    // against 266).  Tiles of at most 128 rows for groups of about that many
-    // (128 rows each: 171 us, with tiles of up to 256: 175; 192 rows: 227
-    // and 185).
+    // against 266).  Tiles of at most 128 rows where groups have up to 96 on
+    // average, else of 256: equal groups gain 2% by the first as long as they fit
+    // (times with at most 128 / 256: 80 rows each 166 / 170 us, 96 168 / 172, 128
+    // 172 / 176) and lose 27% once they do not (160 rows: 229 / 180), and groups
+    // of more than 96 on average are seldom all below 128.
     // But a few pairs' tiles leave most multiprocessors idle, each with all of a
     // long reduction: up to two tiles for every five pairs, single CTAs, whose
     // clusters share the reduction, are faster (one group of 4096 x 1024, 512
@@ -127,6 +139,11 @@ RaggedPlan plan_rows(int64_t T, int64_t G, int64_t N, int64_t K, int64_t R, int6
 DwPlan plan_dw(int64_t T, int64_t G, int64_t P, int64_t Q, int num_sms, int max_pairs) {
     DwPlan p = {};
     const int pairs = max_pairs < 0 ? 0 : std::min(max_pairs ? max_pairs : num_sms / 2, num_sms / 2);
+    // Pairs from one tile for each of them on (single CTAs read an operand twice
+    // as often): with little more than a wave, 13129 rows, 704 x 6408, 78 tiles for
+    // 76 pairs, 133 us and 165 with single CTAs; 4000 rows, 4096 x 4864, 304 tiles, 85
+    // and 127; 4 groups of 2000, 2048 x 1280, 160 tiles, 38 and 47; 24 groups of
+    // 42, 1032 x 520, 15.6 and 17.7.
     p.pair = pairs > 0 && G * ceil_div(P, 256) * ceil_div(Q, 256) >= pairs;
     const int64_t tile = p.pair ? 256 : 128;
     p.p_tiles = (int32_t)ceil_div(P, tile);
