@@ -819,3 +819,19 @@ def test_low_rank_parts_beyond_binary16():
         ref.check(y[ids == 0], (value[::2], bound[::2]), "the other rows")
         low = (x.double() @ a[1].double().t() * 2.0 ** 16).abs()
         assert not torch.isfinite(y[(ids == 1) & (low > 65536).any(1)]).any()
+
+
+@pytest.mark.parametrize("T", [262144, 262144 + 300])
+def test_adapters_of_a_whole_block_of_rows_and_more(T):
+    """As many row tiles as one launch lists, and rows that go on in a second
+    block of them: the rows at both ends and on both sides of the seam."""
+    K, N, R, rank = 64, 72, 5, 8
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.randn(T, K, generator=g, device=DEV).half()
+    a, b, w = normal((R, rank, K), 2, "f16", K ** -0.5), normal((R, rank, N), 3, "f16", rank ** -0.5), normal((K, N), 4, "f16", K ** -0.5)
+    ids = make_ids(T, R, "mixed", 5)
+    y = binding.gemm_relu_adapters(x, w, a, b, ids)
+    binding.check_device_error()
+    for lo in (0, 131000, 262144 - 200, T - 400):
+        rows = slice(lo, min(lo + 400, T))
+        ref.check(y[rows], ref.adapters(x[rows], w, a, b, ids[rows], None, True, "kn"), f"rows from {lo}")
