@@ -298,6 +298,98 @@ int gemm_relu_adapters(const void* X, const void* W, const void* A, const void* 
                        int64_t T, int64_t N, int64_t K, int64_t R, int64_t rank, int64_t ldx, int64_t ldy,
                        int apply_relu, int b_layout, int dtype, void* stream);
 
+/* ---- Losses over a vocabulary ------------------------------------------- */
+
+/* Most rows and words of one call, and most words of a teacher per row. */
+#define GEMM_RELU_MAX_LOSS_ROWS 16777216LL
+#define GEMM_RELU_MAX_WORDS 16777216LL
+#define GEMM_RELU_MAX_TEACHER_WORDS 1024
+
+/* Types of a teacher's logits. */
+typedef enum {
+    GEMM_LOGITS_F16 = 0,
+    GEMM_LOGITS_BF16 = 1,
+    GEMM_LOGITS_F32 = 2
+} gemm_logits_t;
+
+/*
+ * The product of T rows with the output weights of a vocabulary of V words,
+ * and what is wanted of it, in one pass over the weights and with no logits
+ * kept.  With z[t, v] = sum_d X[t, d] W[d, v]:
+ *
+ *   gemm_relu_xent          lse[t]  = log sum_v exp z[t, v]
+ *                           loss[t] = lse[t] - z[t, y],  y = targets[t]
+ *   gemm_relu_xent_grad     g[t, v] = dloss[t] (exp(z[t, v] - lse[t]) - [v = y])
+ *                           dX = g W^T,  dW = X^T g (laid out as W)
+ *   gemm_relu_distill       a teacher's k best words of each row, ids and logits;
+ *                           q = softmax over them of logits / temperature (tau):
+ *                           lse[t]  = log sum_v exp(z[t, v] / tau)
+ *                           loss[t] = tau^2 sum_j q_j (log q_j - z[t, id_j] / tau + lse[t])
+ *                           (tau^2 times the divergence of the row's softmax at
+ *                           tau from the teacher's words)
+ *   gemm_relu_distill_grad  g[t, v] = dloss[t] tau (exp(z[t, v] / tau - lse[t])
+ *                           - sum of q_j with id_j = v); dX, dW as above
+ *
+ * targets: DEVICE array of T int32; negative: the row has none.  ids: DEVICE
+ * (T, k) int32 in any order, row pitch ld_ids >= k; negative: no word there (its
+ * logit is not looked at).  The same word twice is two entries.  logits: DEVICE
+ * (T, k) of logits_type, pitch ld_logits >= k; a logit of -infinity has weight 0.
+ * A target or id of V or more counts as none and is reported as GEMM_ERR_INDEX
+ * by the next gemm_relu_check_device_error.  1 <= k <=
+ * GEMM_RELU_MAX_TEACHER_WORDS; temperature is positive, and it and its inverse
+ * are finite.
+ *
+ * A row with no target, or no word of a weight, has loss and lse +0 and a dX of
+ * +0, and enters dW in no way, whatever X holds there.  Such rows are left out of
+ * the products (from more than 128 rows on, and in the gradients always), so a
+ * batch that is half prompts takes half the time.
+ *
+ * X: (T, D) row-major, pitch ldx; W, dW: dense (D, V) for GEMM_B_KN (V % 8 ==
+ * 0) or (V, D) for GEMM_B_NK (any V); dX (T, D), pitch ld_dx.  These hold `dtype`
+ * elements, are 16-byte aligned, D % 8 == 0, pitches at least D and multiples of
+ * 8.  loss, lse, dloss: DEVICE floats.  lse of the gradients is what the forward
+ * call returned.  dloss_stride 1: dloss[t] per row (the gradient of a weighted sum
+ * of the losses); 0: dloss[0] for all.  dX or dW null: not computed.  Outputs must
+ * not overlap inputs (not checked).  T == 0: nothing but dW = +0.
+ *
+ * Arithmetic: z, the softmax and both sums in fp32; g is rounded to `dtype` once
+ * before the gradients' products, dX and dW once at the end.  In binary16 g is
+ * held times a power of two that brings the largest |dloss tau| to [2^14, 2^15):
+ * terms below 2^-39 of that are lost, below 2^-29 they lose bits.  Results do not
+ * depend on the order in which CTAs run.  Logits that are not finite follow IEEE
+ * 754: an infinite lse, or NaN, in that row.
+ *
+ * workspace: DEVICE memory of at least gemm_relu_loss_workspace(...) bytes,
+ * 256-byte aligned, that belongs to this call until it has run: calls that may
+ * overlap (two streams, two captured graphs) need one each.  Nothing in it has to
+ * be set, and nothing is kept in it.  gemm_relu_loss_workspace (host only) returns
+ * bytes, or minus a gemm_status_t; k = 0 for targets.  The gradients' is about
+ * T V 2 bytes or 512 MiB, whichever is less, + T D 4 (once or for up to 16 shares).
+ * Asynchronous on `stream`; bounded waits and the error word as gemm_relu.
+ */
+int64_t gemm_relu_loss_workspace(int64_t T, int64_t V, int64_t D, int64_t k, int gradient);
+
+int gemm_relu_xent(const void* X, const void* W, const int32_t* targets, float* loss, float* lse,
+                   int64_t T, int64_t V, int64_t D, int64_t ldx, int b_layout, int dtype,
+                   void* workspace, int64_t workspace_bytes, void* stream);
+
+int gemm_relu_xent_grad(const void* X, const void* W, const int32_t* targets, const float* lse,
+                        const float* dloss, int64_t dloss_stride, void* dX, void* dW,
+                        int64_t T, int64_t V, int64_t D, int64_t ldx, int64_t ld_dx, int b_layout, int dtype,
+                        void* workspace, int64_t workspace_bytes, void* stream);
+
+int gemm_relu_distill(const void* X, const void* W, const int32_t* ids, const void* logits, float temperature,
+                      float* loss, float* lse, int64_t T, int64_t V, int64_t D, int64_t k,
+                      int64_t ldx, int64_t ld_ids, int64_t ld_logits, int b_layout, int dtype, int logits_type,
+                      void* workspace, int64_t workspace_bytes, void* stream);
+
+int gemm_relu_distill_grad(const void* X, const void* W, const int32_t* ids, const void* logits, float temperature,
+                           const float* lse, const float* dloss, int64_t dloss_stride, void* dX, void* dW,
+                           int64_t T, int64_t V, int64_t D, int64_t k,
+                           int64_t ldx, int64_t ld_ids, int64_t ld_logits, int64_t ld_dx,
+                           int b_layout, int dtype, int logits_type,
+                           void* workspace, int64_t workspace_bytes, void* stream);
+
 /* ---- Host-only planning interface (no CUDA calls; usable without a GPU) -- */
 
 typedef struct {

@@ -8,9 +8,10 @@ example to draw the seeded workloads in ``workloads``) needs no GPU.
 import importlib
 
 __all__ = ["gemm_relu", "gemm_relu_host", "gemm_relu_grouped", "gemm_relu_grouped_dx", "gemm_relu_grouped_dw",
-           "gemm_relu_adapters", "binding", "workloads"]
+           "gemm_relu_adapters", "gemm_relu_xent", "gemm_relu_xent_grad", "gemm_relu_distill", "gemm_relu_distill_grad",
+           "binding", "workloads"]
 
-_FUNCTIONS = frozenset(__all__[:6]) | {"check_device_error"}
+_FUNCTIONS = frozenset(__all__[:10]) | {"check_device_error"}
 
 
 def __getattr__(name):

@@ -7,6 +7,7 @@ library is missing or the device is not a GB300 (sm_103a), calls raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -97,6 +98,17 @@ def lib():
         L.gemm_relu_grouped_dw.argtypes = [vp] * 4 + [i64] * 6 + [i32] * 2 + [vp]
         L.gemm_relu_adapters.restype = i32
         L.gemm_relu_adapters.argtypes = [vp] * 7 + [i64] * 7 + [i32] * 3 + [vp]
+        f32 = ctypes.c_float
+        L.gemm_relu_loss_workspace.restype = i64
+        L.gemm_relu_loss_workspace.argtypes = [i64] * 4 + [i32]
+        L.gemm_relu_xent.restype = i32
+        L.gemm_relu_xent.argtypes = [vp] * 5 + [i64] * 4 + [i32] * 2 + [vp, i64, vp]
+        L.gemm_relu_xent_grad.restype = i32
+        L.gemm_relu_xent_grad.argtypes = [vp] * 5 + [i64, vp, vp] + [i64] * 5 + [i32] * 2 + [vp, i64, vp]
+        L.gemm_relu_distill.restype = i32
+        L.gemm_relu_distill.argtypes = [vp] * 4 + [f32, vp, vp] + [i64] * 7 + [i32] * 3 + [vp, i64, vp]
+        L.gemm_relu_distill_grad.restype = i32
+        L.gemm_relu_distill_grad.argtypes = [vp] * 4 + [f32, vp, vp, i64, vp, vp] + [i64] * 8 + [i32] * 3 + [vp, i64, vp]
         L.gemm_relu_plan.restype = i32
         L.gemm_relu_plan.argtypes = [i64, i64, i64, i32, ctypes.POINTER(Plan)]
         p32 = ctypes.POINTER(ctypes.c_int32)
@@ -516,6 +528,186 @@ def gemm_relu_adapters(x, w, a, b, ids, scale=None, y=None, apply_relu: bool = T
              ids.data_ptr(), None if scale is None else scale.data_ptr(), y.data_ptr(), T, N, K, R, rank, ldx, ldy,
              1 if apply_relu else 0, layout, dtype)
     return y
+
+
+# ---- Losses over a vocabulary.  The workspace is a tensor of the caching
+# allocator's, taken and given back on the call's stream: calls on two streams,
+# or captured in two graphs, never share one.
+
+_LOGIT_CODES = {}  # {torch type: gemm_logits_t}
+
+
+def _head_sizes(x, w, layout):
+    """(T, V, D, row pitch of x, device) of rows and a vocabulary's weights."""
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x and w must be 2-D")
+    device = _device_of(x)
+    T, D = x.shape
+    V, Dw = w.shape
+    if not layout:
+        V, Dw = Dw, V
+    if Dw != D:
+        raise ValueError(f"bad shapes {tuple(x.shape)} and {tuple(w.shape)}")
+    if w.get_device() != device or not w.is_contiguous():
+        raise ValueError(f"w must be contiguous and on CUDA device {device}")
+    return T, V, D, _rows("x", x, T, D, device), device
+
+
+def _floats(name, t, T, device):
+    if getattr(t, "dtype", None) is not _torch.float32:
+        raise TypeError(f"{name} must be a float32 tensor")
+    _stack(name, t, (T,), device)
+
+
+def _dloss(t, T, device):
+    """Stride of the losses' gradient: 1, or 0 where all rows share one value."""
+    if getattr(t, "dtype", None) is not _torch.float32:
+        raise TypeError("dloss must be a float32 tensor")
+    if t.get_device() != device:
+        raise ValueError(f"dloss must be on CUDA device {device}")
+    if t.dim() <= 1 and t.numel() == 1:
+        return 0
+    if t.shape != (T,) or (T > 1 and t.stride(0) not in (0, 1)):
+        raise ValueError(f"dloss must hold one value, or {T} contiguous ones")
+    return t.stride(0) if T > 1 else 1
+
+
+def _teacher(ids, logits, T, device):
+    """(k, pitch of ids, pitch of logits, type of logits)"""
+    if not _LOGIT_CODES:
+        _LOGIT_CODES.update({_torch.float16: 0, _torch.bfloat16: 1, _torch.float32: 2})
+    if getattr(ids, "dtype", None) is not _torch.int32:
+        raise TypeError("ids must be an int32 tensor")
+    code = _LOGIT_CODES.get(getattr(logits, "dtype", None))
+    if code is None:
+        raise TypeError("logits must be a float16, bfloat16 or float32 tensor")
+    if ids.dim() != 2:
+        raise ValueError("ids must be 2-D")
+    k = ids.shape[1]
+    return k, _rows("ids", ids, T, k, device), _rows("logits", logits, T, k, device), code
+
+
+def _on_stream(stream, device):
+    """The context in which a call's tensors are allocated, and the stream's handle."""
+    if stream is None:
+        return contextlib.nullcontext(), None
+    if not hasattr(stream, "cuda_stream"):
+        stream = _torch.cuda.ExternalStream(stream, device=device)
+    return _torch.cuda.stream(stream), stream.cuda_stream
+
+
+def _loss_call(fn, x, device, stream, T, V, D, k, gradient, allocate, args):
+    """fn(*args(outputs), workspace, bytes, stream), the outputs from allocate()."""
+    context, handle = _on_stream(stream, device)
+    need = lib().gemm_relu_loss_workspace(T, V, D, k, gradient)
+    if need < 0:
+        raise GemmReluError(-need, fn.__name__)
+    with context:
+        out = allocate()
+        space = _torch.empty((need,), dtype=_torch.uint8, device=x.device)
+        _enqueue(fn, device, handle, *args(out), space.data_ptr(), need)
+    return out
+
+
+def _losses(loss, lse, x, T, device):
+    if loss is not None:
+        _floats("loss", loss, T, device)
+    if lse is not None:
+        _floats("lse", lse, T, device)
+    new = lambda t: _torch.empty((T,), dtype=_torch.float32, device=x.device) if t is None else t  # noqa: E731
+    return lambda: (new(loss), new(lse))
+
+
+def _gradients(dx, dw, x, w, T, D, device, want_dx, want_dw):
+    """What allocates (dx, dw, pitch of dx); None for one that is not wanted."""
+    ld = D
+    if want_dx and dx is not None:
+        dx, ld = _output("dx", dx, x, T, D, device)
+    if want_dw and dw is not None:
+        if getattr(dw, "dtype", None) is not x.dtype:
+            raise TypeError("dw must be a tensor of the operands' type")
+        _stack("dw", dw, w.shape, device)
+
+    def allocate():
+        a = dx if want_dx else None
+        if want_dx and a is None:
+            a = _torch.empty((T, D), dtype=x.dtype, device=x.device)
+        b = dw if want_dw else None
+        if want_dw and b is None:
+            b = _torch.empty(w.shape, dtype=x.dtype, device=x.device)
+        return a, b
+    return allocate, ld
+
+
+def _pointer(t):
+    return None if t is None else t.data_ptr()
+
+
+def gemm_relu_xent(x, w, targets, loss=None, lse=None, b_layout: str = "kn", stream=None):
+    """(loss, lse) of a cross entropy over a vocabulary, without its logits:
+    lse[t] = log sum_v exp z[t, v], loss[t] = lse[t] - z[t, targets[t]], z = x @ w.
+
+    ``x`` (T, D) has contiguous rows, ``w`` is (D, V), or (V, D) for
+    ``b_layout="nk"``; float16 or bfloat16 CUDA tensors.  ``targets``: CUDA
+    int32 (T,), negative for a row without one, whose loss and lse are 0.
+    ``loss`` and ``lse`` are float32 (T,), written in place when given."""
+    dtype, layout = _dtype_code(x, w), _layout_code(b_layout)
+    T, V, D, ldx, device = _head_sizes(x, w, layout)
+    _index("targets", targets, T, device)
+    return _loss_call(lib().gemm_relu_xent, x, device, stream, T, V, D, 0, 0, _losses(loss, lse, x, T, device),
+                      lambda o: (x.data_ptr(), w.data_ptr(), targets.data_ptr(), o[0].data_ptr(), o[1].data_ptr(), T, V,
+                                 D, ldx, layout, dtype))
+
+
+def gemm_relu_xent_grad(x, w, targets, lse, dloss, dx=None, dw=None, want_dx: bool = True, want_dw: bool = True,
+                        b_layout: str = "kn", stream=None):
+    """(dx, dw) of ``gemm_relu_xent``, from its ``lse`` and the gradient of its
+    losses, ``dloss``: float32 (T,), or one value for all rows (a mean's).
+
+    ``want_dx=False`` or ``want_dw=False`` leaves that one out (None)."""
+    dtype, layout = _dtype_code(x, w), _layout_code(b_layout)
+    T, V, D, ldx, device = _head_sizes(x, w, layout)
+    _index("targets", targets, T, device)
+    _floats("lse", lse, T, device)
+    step = _dloss(dloss, T, device)
+    allocate, ld_dx = _gradients(dx, dw, x, w, T, D, device, want_dx, want_dw)
+    return _loss_call(lib().gemm_relu_xent_grad, x, device, stream, T, V, D, 0, 1, allocate,
+                      lambda o: (x.data_ptr(), w.data_ptr(), targets.data_ptr(), lse.data_ptr(), dloss.data_ptr(), step,
+                                 _pointer(o[0]), _pointer(o[1]), T, V, D, ldx, ld_dx, layout, dtype))
+
+
+def gemm_relu_distill(x, w, ids, logits, temperature: float = 1.0, loss=None, lse=None, b_layout: str = "kn",
+                      stream=None):
+    """(loss, lse) of a distillation from a teacher's k best words of each row,
+    ``ids`` (T, k) int32, negative for none, and their ``logits`` (T, k) of a
+    16- or 32-bit floating type:
+
+    q = softmax(logits / tau), lse[t] = log sum_v exp(z[t, v] / tau),
+    loss[t] = tau^2 sum_j q_j (log q_j - z[t, ids_j] / tau + lse[t]), z = x @ w.
+
+    The rest as ``gemm_relu_xent``."""
+    dtype, layout = _dtype_code(x, w), _layout_code(b_layout)
+    T, V, D, ldx, device = _head_sizes(x, w, layout)
+    k, ld_ids, ld_logits, code = _teacher(ids, logits, T, device)
+    return _loss_call(lib().gemm_relu_distill, x, device, stream, T, V, D, k, 0, _losses(loss, lse, x, T, device),
+                      lambda o: (x.data_ptr(), w.data_ptr(), ids.data_ptr(), logits.data_ptr(), temperature,
+                                 o[0].data_ptr(), o[1].data_ptr(), T, V, D, k, ldx, ld_ids, ld_logits, layout, dtype,
+                                 code))
+
+
+def gemm_relu_distill_grad(x, w, ids, logits, lse, dloss, temperature: float = 1.0, dx=None, dw=None,
+                           want_dx: bool = True, want_dw: bool = True, b_layout: str = "kn", stream=None):
+    """(dx, dw) of ``gemm_relu_distill``, as ``gemm_relu_xent_grad``."""
+    dtype, layout = _dtype_code(x, w), _layout_code(b_layout)
+    T, V, D, ldx, device = _head_sizes(x, w, layout)
+    k, ld_ids, ld_logits, code = _teacher(ids, logits, T, device)
+    _floats("lse", lse, T, device)
+    step = _dloss(dloss, T, device)
+    allocate, ld_dx = _gradients(dx, dw, x, w, T, D, device, want_dx, want_dw)
+    return _loss_call(lib().gemm_relu_distill_grad, x, device, stream, T, V, D, k, 1, allocate,
+                      lambda o: (x.data_ptr(), w.data_ptr(), ids.data_ptr(), logits.data_ptr(), temperature,
+                                 lse.data_ptr(), dloss.data_ptr(), step, _pointer(o[0]), _pointer(o[1]), T, V, D, k, ldx,
+                                 ld_ids, ld_logits, ld_dx, layout, dtype, code))
 
 
 def shutdown():

@@ -1,0 +1,498 @@
+// C entry points of the losses over a vocabulary: cross entropy and
+// distillation from a teacher's best words, each with its gradients.  Argument
+// checks, plan, tensor maps, launches; the kernels are in loss_kernel.cuh and
+// loss_rows.cuh.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "gemm_relu.h"
+#include "launch.h"
+#include "loss_kernel.cuh"
+#include "loss_plan.h"
+#include "loss_rows.cuh"
+#include "runtime.h"
+
+namespace gr {
+namespace ls {
+
+using rt::DeviceState;
+using rt::encode_rows;
+using rt::launch;
+using rt::misaligned;
+
+// What a call is given.
+struct Call {
+    const void *X, *W;
+    int64_t T, V, D, ldx;
+    bool nk, bf16;
+    const int32_t* targets;  // or
+    const int32_t* ids;      // a teacher's words
+    const void* logits;
+    int64_t k, ld_ids, ld_logits;
+    int logits_type;
+    float tau;
+    float *loss, *lse_out;   // forward
+    const float *lse, *dloss;  // backward
+    int64_t dloss_stride;
+    void *dX, *dW;
+    int64_t ld_dx;
+    uint8_t* ws;
+    cudaStream_t st;
+};
+
+// Sums in 32 bits, a plane per share: boxes of 32 x 32.
+static int encode_sums(CUtensorMap* map, void* ptr, int64_t D, int64_t T, int64_t splits) {
+    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)T, (cuuint64_t)splits};
+    cuuint64_t strides[2] = {(cuuint64_t)D * 4, (cuuint64_t)(D * T) * 4};
+    cuuint32_t box[3] = {32, 32, 1}, step[3] = {1, 1, 1};
+    const CUresult r = rt::g_encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, ptr, dims, strides, box, step,
+                                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_INVALID_ARG;
+}
+
+template <bool kPair, int kMode>
+static int launch_tiles(DeviceState& d, const TilePlan& t, const LossMaps& m, const LossParams& q, cudaStream_t st) {
+    auto fn = loss_kernel<kPair, kMode>;
+    bool& set = d.ls_attr_set[2 * kMode + (kPair ? 1 : 0)];
+    if (!set) {
+        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, rt::kMaxDynSmem) != cudaSuccess) {
+            cudaGetLastError();
+            return GEMM_ERR_LAUNCH;
+        }
+        set = true;
+    }
+    return launch(fn, t.grid, kThreads, (size_t)t.smem_bytes, kPair ? 2 : 1, st, m, q);
+}
+
+template <int kMode>
+static int launch_mode(DeviceState& d, const TilePlan& t, const LossMaps& m, LossParams& q, cudaStream_t st) {
+    q.width = t.width;
+    q.n_tiles = t.n_tiles;
+    q.group_m = t.group_m;
+    q.splits = t.splits;
+    q.a_bytes = (uint32_t)t.a_bytes;
+    q.stage_bytes = (uint32_t)t.stage_bytes;
+    q.num_stages = t.num_stages;
+    q.tmem_cols = (uint32_t)t.tmem_cols;
+    q.err = d.d_err;
+    const int64_t blocks = ((int64_t)q.K + kBK - 1) / kBK;
+    q.timeout_ns = 2000000000ull + 2000ull * (uint64_t)blocks;
+    if (kMode == kStats) {
+        const int rc = rt::test_hook(!t.pair, (int32_t)std::min<int64_t>(blocks, kNone), &q.test_drop_kb, &q.timeout_ns);
+        if (rc != GEMM_OK) return rc;
+    }
+    return t.pair ? launch_tiles<true, kMode>(d, t, m, q, st) : launch_tiles<false, kMode>(d, t, m, q, st);
+}
+
+// The rows' kernels for rows [b0, b0 + T): the teacher's words, which rows are
+// in use, a copy of those.
+static int run_rows(const Call& c, const LossPlan& p, int64_t b0, int64_t T, DeviceState& d) {
+    int rc;
+    if (c.ids) {
+        TeacherParams q;
+        memset(&q, 0, sizeof(q));
+        q.ids = c.ids + b0 * c.ld_ids;
+        q.logits = reinterpret_cast<const uint8_t*>(c.logits) + b0 * c.ld_logits * (c.logits_type == GEMM_LOGITS_F32 ? 4 : 2);
+        q.ld_ids = c.ld_ids;
+        q.ld_logits = c.ld_logits;
+        q.logits_type = c.logits_type;
+        q.T = (int32_t)T;
+        q.k = (int32_t)c.k;
+        q.V = (int32_t)c.V;
+        q.inv_tau = 1.0f / c.tau;
+        q.sorted = reinterpret_cast<int32_t*>(c.ws + p.sorted);
+        q.weights = reinterpret_cast<float*>(c.ws + p.weights);
+        q.flags = reinterpret_cast<int32_t*>(c.ws + p.flags);
+        q.entropy = reinterpret_cast<float*>(c.ws + p.entropy);
+        q.err = d.d_err;
+        const int grid = (int)std::min<int64_t>((T + kTeacherWarps - 1) / kTeacherWarps, 16 * d.sm_count);
+        rc = launch(loss_teacher_kernel, grid, 32 * kTeacherWarps, (size_t)kTeacherWarps * ((c.k + 3) / 4 * 4) * 8, 1, c.st, q);
+        if (rc != GEMM_OK) return rc;
+    }
+    if (!p.gather) return GEMM_OK;
+    RowsParams q;
+    memset(&q, 0, sizeof(q));
+    q.flags = c.ids ? reinterpret_cast<const int32_t*>(c.ws + p.flags) : c.targets + b0;
+    q.limit = c.ids ? 1 : (int32_t)c.V;
+    q.T = (int32_t)T;
+    q.D = (int32_t)c.D;
+    q.X = reinterpret_cast<const uint16_t*>(c.X) + b0 * c.ldx;
+    q.ldx = c.ldx;
+    q.gathered = reinterpret_cast<uint16_t*>(c.ws + p.gathered);
+    q.index = reinterpret_cast<int32_t*>(c.ws + p.index);
+    q.rows = reinterpret_cast<RowsHeader*>(c.ws + p.header);
+    q.dloss = c.dloss;
+    q.dloss_stride = c.dloss_stride;
+    q.grad_scale = c.ids ? c.tau : 1.0f;
+    q.scaled = c.dloss && !c.bf16 ? 1 : 0;
+    q.err = d.d_err;
+    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>((T + 31) / 32, 2 * d.sm_count));
+    return launch(loss_rows_kernel, grid, kRowsThreads, 0, 1, c.st, q);
+}
+
+// The wanted words and the rows, for kStats and kGrad.
+static void wanted(const Call& c, const LossPlan& p, int64_t b0, LossParams& q) {
+    q.rows = p.gather ? reinterpret_cast<const RowsHeader*>(c.ws + p.header) : nullptr;
+    q.rows_m = p.gather ? 1 : 0;
+    q.index = reinterpret_cast<const int32_t*>(c.ws + p.index);
+    if (c.ids) {
+        q.ids = reinterpret_cast<const int32_t*>(c.ws + p.sorted);
+        q.weights = reinterpret_cast<const float*>(c.ws + p.weights);
+        q.k = (int32_t)c.k;
+    } else {
+        q.targets = c.targets + b0;
+    }
+    q.V = (int32_t)c.V;
+    q.log2_scale = 1.4426950408889634f / c.tau;
+}
+
+// W as B's side of the logits (reduction D), `width` words per CTA.
+static int encode_words(CUtensorMap* m, const Call& c, int32_t width, LossParams& q) {
+    q.b_mn = c.nk ? 0 : 1;
+    q.b_3d = c.V % 64 == 0;
+    return c.nk ? encode_rows(m, c.W, (uint64_t)c.D, (uint64_t)c.V, (uint64_t)c.D, (uint32_t)width, 0, c.bf16)
+                : encode_rows(m, c.W, (uint64_t)c.V, (uint64_t)c.D, (uint64_t)c.V, kBK, q.b_3d ? (uint32_t)width / 64 : 0, c.bf16);
+}
+
+// X's rows and their gathered copy, read as boxes of `box` rows (`chunks`: mn-major, in one copy).
+static int encode_x(CUtensorMap* m, const Call& c, const LossPlan& p, int64_t b0, int64_t T, uint32_t box, uint32_t chunks) {
+    int rc = encode_rows(&m[0], reinterpret_cast<const uint16_t*>(c.X) + b0 * c.ldx, (uint64_t)c.D, (uint64_t)T, (uint64_t)c.ldx,
+                         box, chunks, c.bf16);
+    m[1] = m[0];
+    if (rc == GEMM_OK && p.gather)
+        rc = encode_rows(&m[1], c.ws + p.gathered, (uint64_t)c.D, (uint64_t)T, (uint64_t)c.D, box, chunks, c.bf16);
+    return rc;
+}
+
+static int run_forward(const Call& c, const LossPlan& p, DeviceState& d) {
+    for (int64_t b0 = 0; b0 < c.T; b0 += p.rows) {
+        const int64_t T = std::min(p.rows, c.T - b0);
+        int rc = run_rows(c, p, b0, T, d);
+        if (rc != GEMM_OK) return rc;
+        const TilePlan t = plan_logits(T, c.V, c.D, !c.nk, false, d.sm_count, d.max_pairs);
+        LossMaps m;
+        LossParams q;
+        memset(&q, 0, sizeof(q));
+        q.M = (int32_t)T;
+        q.N = (int32_t)c.V;
+        q.K = (int32_t)c.D;
+        q.bf16 = c.bf16 ? 1 : 0;
+        wanted(c, p, b0, q);
+        q.stats = reinterpret_cast<float*>(c.ws + p.stats);
+        q.stats_pitch = (p.rows + 31) / 32 * 32;
+        rc = encode_x(m.a, c, p, b0, T, (uint32_t)t.a_rows, 0);
+        if (rc == GEMM_OK) rc = encode_words(&m.b[0], c, t.width / (t.pair ? 2 : 1), q);
+        if (rc != GEMM_OK) return rc;
+        m.b[1] = m.b[0];
+        m.d = m.a[0];
+        rc = launch_mode<kStats>(d, t, m, q, c.st);
+        if (rc != GEMM_OK) return rc;
+        CombineParams o;
+        memset(&o, 0, sizeof(o));
+        o.stats = q.stats;
+        o.pitch = q.stats_pitch;
+        o.parts = t.n_tiles * std::min(t.width / 64, 2);
+        o.T = (int32_t)T;
+        o.rows = q.rows;
+        o.index = q.index;
+        o.flags = c.ids ? reinterpret_cast<const int32_t*>(c.ws + p.flags) : c.targets + b0;
+        o.limit = c.ids ? 1 : (int32_t)c.V;
+        o.entropy = c.ids ? reinterpret_cast<const float*>(c.ws + p.entropy) : nullptr;
+        o.tau = c.tau;
+        o.log2_scale = q.log2_scale;
+        o.loss = c.loss + b0;
+        o.lse = c.lse_out + b0;
+        o.err = d.d_err;
+        const int blocks = (int)((T + 31) / 32);
+        rc = blocks < 2 * d.sm_count ? launch(loss_combine_kernel<32>, blocks, 1024, 0, 1, c.st, o)
+                                     : launch(loss_combine_kernel<8>, blocks, 256, 0, 1, c.st, o);
+        if (rc != GEMM_OK) return rc;
+    }
+    return GEMM_OK;
+}
+
+static int run_backward(const Call& c, const LossPlan& p, DeviceState& d) {
+    int rc = run_rows(c, p, 0, c.T, d);
+    if (rc != GEMM_OK) return rc;
+    const RowsHeader* rows = reinterpret_cast<const RowsHeader*>(c.ws + p.header);
+    uint16_t* const G = reinterpret_cast<uint16_t*>(c.ws + p.grad);
+    float* const sums = reinterpret_cast<float*>(c.ws + p.sums);
+    for (int64_t p0 = 0; p0 < c.V; p0 += p.piece) {
+        const int64_t vp = std::min(p.piece, c.V - p0);
+        LossMaps m;
+        LossParams q;
+        {  // G of the piece
+            const TilePlan t = plan_logits(c.T, vp, c.D, !c.nk, true, d.sm_count, d.max_pairs);
+            memset(&q, 0, sizeof(q));
+            q.M = (int32_t)c.T;
+            q.N = (int32_t)vp;
+            q.K = (int32_t)c.D;
+            q.bf16 = c.bf16 ? 1 : 0;
+            wanted(c, p, 0, q);
+            q.w_row = (int32_t)p0;
+            q.lse = c.lse;
+            q.dloss = c.dloss;
+            q.dloss_stride = c.dloss_stride;
+            q.grad_scale = c.ids ? c.tau : 1.0f;
+            rc = encode_x(m.a, c, p, 0, c.T, (uint32_t)t.a_rows, 0);
+            if (rc == GEMM_OK) rc = encode_words(&m.b[0], c, t.width / (t.pair ? 2 : 1), q);
+            if (rc == GEMM_OK)
+                rc = encode_rows(&m.d, G, (uint64_t)p.piece, (uint64_t)c.T, (uint64_t)p.piece, 32, 0, c.bf16);
+            m.b[1] = m.b[0];
+            if (rc == GEMM_OK) rc = launch_mode<kGrad>(d, t, m, q, c.st);
+            if (rc != GEMM_OK) return rc;
+        }
+        if (c.dX) {  // sums += G W
+            const TilePlan t = plan_sum(c.T, c.D, vp, p.sum_splits, c.nk, d.sm_count, d.max_pairs);
+            const uint32_t width = (uint32_t)(t.width / (t.pair ? 2 : 1));
+            memset(&q, 0, sizeof(q));
+            q.M = (int32_t)c.T;
+            q.N = (int32_t)c.D;
+            q.K = (int32_t)vp;
+            q.bf16 = c.bf16 ? 1 : 0;
+            q.rows = rows;
+            q.rows_m = 1;
+            q.first = p0 == 0;
+            q.w_k = (int32_t)p0;
+            q.b_mn = c.nk ? 1 : 0;
+            q.b_3d = c.D % 64 == 0;
+            rc = encode_rows(&m.a[0], G, (uint64_t)((vp + 7) / 8 * 8), (uint64_t)c.T, (uint64_t)p.piece, (uint32_t)t.a_rows, 0, c.bf16);
+            if (rc == GEMM_OK)
+                rc = c.nk ? encode_rows(&m.b[0], c.W, (uint64_t)c.D, (uint64_t)c.V, (uint64_t)c.D, kBK, q.b_3d ? width / 64 : 0, c.bf16)
+                          : encode_rows(&m.b[0], c.W, (uint64_t)c.V, (uint64_t)c.D, (uint64_t)c.V, width, 0, c.bf16);
+            if (rc == GEMM_OK) rc = encode_sums(&m.d, sums, c.D, c.T, p.sum_splits);
+            m.a[1] = m.a[0];
+            m.b[1] = m.b[0];
+            if (rc == GEMM_OK) rc = launch_mode<kSum>(d, t, m, q, c.st);
+            if (rc != GEMM_OK) return rc;
+        }
+        if (c.dW) {  // dW[piece] = G^T X, or its transpose
+            const int64_t M = c.nk ? vp : c.D, N = c.nk ? c.D : vp;
+            const TilePlan t = plan_weight(M, N, c.T, d.sm_count, d.max_pairs);
+            const uint32_t chunks = (uint32_t)(t.width / (t.pair ? 2 : 1)) / 64;
+            const bool x3d = c.D % 64 == 0;
+            memset(&q, 0, sizeof(q));
+            q.M = (int32_t)M;
+            q.N = (int32_t)N;
+            q.K = (int32_t)c.T;
+            q.bf16 = c.bf16 ? 1 : 0;
+            q.rows = rows;
+            q.rows_k = 1;
+            q.a_mn = q.b_mn = 1;
+            q.a_3d = c.nk || x3d;
+            q.b_3d = !c.nk || x3d;
+            (c.nk ? q.d_row : q.d_col) = (int32_t)p0;
+            CUtensorMap* const mg = c.nk ? m.a : m.b;
+            CUtensorMap* const mx = c.nk ? m.b : m.a;
+            rc = encode_rows(&mg[0], G, (uint64_t)p.piece, (uint64_t)c.T, (uint64_t)p.piece, kBK, c.nk ? 2 : chunks, c.bf16);
+            mg[1] = mg[0];
+            if (rc == GEMM_OK) rc = encode_x(mx, c, p, 0, c.T, kBK, !x3d ? 0 : c.nk ? chunks : 2);
+            if (rc == GEMM_OK)
+                rc = c.nk ? encode_rows(&m.d, c.dW, (uint64_t)c.D, (uint64_t)c.V, (uint64_t)c.D, 32, 0, c.bf16)
+                          : encode_rows(&m.d, c.dW, (uint64_t)c.V, (uint64_t)c.D, (uint64_t)c.V, 32, 0, c.bf16);
+            if (rc == GEMM_OK) rc = launch_mode<kWeight>(d, t, m, q, c.st);
+            if (rc != GEMM_OK) return rc;
+        }
+    }
+    if (!c.dX) return GEMM_OK;
+    FinishParams f;
+    memset(&f, 0, sizeof(f));
+    f.sums = sums;
+    f.splits = p.sum_splits;
+    f.T = (int32_t)c.T;
+    f.D = (int32_t)c.D;
+    f.bf16 = c.bf16 ? 1 : 0;
+    f.rows = rows;
+    f.index = reinterpret_cast<const int32_t*>(c.ws + p.index);
+    f.dX = reinterpret_cast<uint16_t*>(c.dX);
+    f.ld_dx = c.ld_dx;
+    const int64_t vecs = c.T * (c.D / 8);
+    return launch(loss_finish_kernel, (int)std::min<int64_t>((vecs + 255) / 256, 8 * d.sm_count), 256, 0, 1, c.st, f);
+}
+
+// ------------------------------------------------------------------ checks
+
+static int check_sizes(int64_t T, int64_t V, int64_t D, int64_t k) {
+    if (T < 0 || T > GEMM_RELU_MAX_LOSS_ROWS || V < 1 || V > GEMM_RELU_MAX_WORDS || D < 1 || !rt::dim_ok(D) || k < 0 ||
+        k > GEMM_RELU_MAX_TEACHER_WORDS)
+        return GEMM_ERR_INVALID_ARG;
+    return D % 8 != 0 ? GEMM_ERR_ALIGNMENT : GEMM_OK;
+}
+
+static int check_floats(const void* p) {
+    if (!p) return GEMM_ERR_INVALID_ARG;
+    return misaligned(p, 4) ? GEMM_ERR_ALIGNMENT : GEMM_OK;
+}
+
+// Everything but the outputs.
+static int check_call(const Call& c, int b_layout, int dtype) {
+    int rc = check_sizes(c.T, c.V, c.D, c.k);
+    if (rc != GEMM_OK) return rc;
+    if ((b_layout != GEMM_B_KN && b_layout != GEMM_B_NK) || (dtype != GEMM_DTYPE_F16 && dtype != GEMM_DTYPE_BF16))
+        return GEMM_ERR_INVALID_ARG;
+    if (b_layout == GEMM_B_KN && c.V % 8 != 0) return GEMM_ERR_ALIGNMENT;
+    if (c.T == 0) return GEMM_OK;
+    if ((rc = rt::check_matrix(c.X, c.D, c.ldx)) != GEMM_OK) return rc;
+    return rt::check_matrix(c.W, 0, 0);
+}
+
+static int check_teacher(const Call& c) {
+    if (c.k < 1 || !(c.tau > 0.0f) || !isfinite(c.tau) || !isfinite(1.0f / c.tau)) return GEMM_ERR_INVALID_ARG;
+    if (c.logits_type != GEMM_LOGITS_F16 && c.logits_type != GEMM_LOGITS_BF16 && c.logits_type != GEMM_LOGITS_F32)
+        return GEMM_ERR_INVALID_ARG;
+    if (c.T == 0) return GEMM_OK;
+    if (!c.ids || !c.logits || c.ld_ids < c.k || c.ld_logits < c.k || c.ld_ids > GEMM_RELU_MAX_DIM || c.ld_logits > GEMM_RELU_MAX_DIM)
+        return GEMM_ERR_INVALID_ARG;
+    return misaligned(c.ids, 4) || misaligned(c.logits, c.logits_type == GEMM_LOGITS_F32 ? 4 : 2) ? GEMM_ERR_ALIGNMENT : GEMM_OK;
+}
+
+static int run(Call& c, void* workspace, int64_t workspace_bytes, bool gradient, void* stream) {
+    const LossPlan p = plan_loss(c.T, c.V, c.D, c.k, gradient);
+    if (p.status != GEMM_OK) return p.status;
+    if (!workspace || workspace_bytes < p.bytes) return GEMM_ERR_INVALID_ARG;
+    if (misaligned(workspace, 256)) return GEMM_ERR_ALIGNMENT;
+    c.ws = reinterpret_cast<uint8_t*>(workspace);
+    c.st = reinterpret_cast<cudaStream_t>(stream);
+    int dev, rc;
+    if ((rc = rt::current_device(&dev)) != GEMM_OK) return rc;
+    std::lock_guard<std::mutex> lock(rt::g_mu);
+    if ((rc = rt::init_device_locked(dev)) != GEMM_OK) return rc;
+    return gradient ? run_backward(c, p, rt::g_dev[dev]) : run_forward(c, p, rt::g_dev[dev]);
+}
+
+static int forward(Call& c, void* workspace, int64_t workspace_bytes, void* stream) {
+    if (c.T == 0) return GEMM_OK;
+    int rc;
+    if ((rc = check_floats(c.loss)) != GEMM_OK || (rc = check_floats(c.lse_out)) != GEMM_OK) return rc;
+    return run(c, workspace, workspace_bytes, false, stream);
+}
+
+static int backward(Call& c, void* workspace, int64_t workspace_bytes, void* stream) {
+    int rc;
+    if (c.dloss_stride != 0 && c.dloss_stride != 1) return GEMM_ERR_INVALID_ARG;
+    if (c.dW && misaligned(c.dW, 16)) return GEMM_ERR_ALIGNMENT;
+    if (c.T == 0) {
+        if (!c.dW) return GEMM_OK;
+        int dev;
+        if ((rc = rt::current_device(&dev)) != GEMM_OK) return rc;
+        if (cudaMemsetAsync(c.dW, 0, (size_t)c.V * c.D * 2, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) {
+            cudaGetLastError();
+            return GEMM_ERR_CUDA;
+        }
+        return GEMM_OK;
+    }
+    if ((rc = check_floats(c.lse)) != GEMM_OK || (rc = check_floats(c.dloss)) != GEMM_OK) return rc;
+    if (c.dX && (rc = rt::check_matrix(c.dX, c.D, c.ld_dx)) != GEMM_OK) return rc;
+    if (!c.dX && !c.dW) return GEMM_OK;
+    return run(c, workspace, workspace_bytes, true, stream);
+}
+
+static Call call_of(const void* X, const void* W, int64_t T, int64_t V, int64_t D, int64_t ldx, int b_layout, int dtype) {
+    Call c;
+    memset(&c, 0, sizeof(c));
+    c.X = X;
+    c.W = W;
+    c.T = T;
+    c.V = V;
+    c.D = D;
+    c.ldx = ldx;
+    c.nk = b_layout == GEMM_B_NK;
+    c.bf16 = dtype == GEMM_DTYPE_BF16;
+    c.tau = 1.0f;
+    return c;
+}
+
+}  // namespace ls
+}  // namespace gr
+
+using namespace gr;
+using namespace gr::ls;
+
+extern "C" int64_t gemm_relu_loss_workspace(int64_t T, int64_t V, int64_t D, int64_t k, int gradient) {
+    const int rc = check_sizes(T, V, D, k);
+    if (rc != GEMM_OK) return -rc;
+    if (T == 0) return 0;
+    const LossPlan p = plan_loss(T, V, D, k, gradient != 0);
+    return p.status == GEMM_OK ? p.bytes : -p.status;
+}
+
+extern "C" int gemm_relu_xent(const void* X, const void* W, const int32_t* targets, float* loss, float* lse, int64_t T,
+                              int64_t V, int64_t D, int64_t ldx, int b_layout, int dtype, void* workspace,
+                              int64_t workspace_bytes, void* stream) {
+    Call c = call_of(X, W, T, V, D, ldx, b_layout, dtype);
+    c.targets = targets;
+    c.loss = loss;
+    c.lse_out = lse;
+    int rc = check_call(c, b_layout, dtype);
+    if (rc != GEMM_OK) return rc;
+    if (T > 0 && (rc = check_floats(targets)) != GEMM_OK) return rc;
+    return forward(c, workspace, workspace_bytes, stream);
+}
+
+extern "C" int gemm_relu_xent_grad(const void* X, const void* W, const int32_t* targets, const float* lse, const float* dloss,
+                                   int64_t dloss_stride, void* dX, void* dW, int64_t T, int64_t V, int64_t D, int64_t ldx,
+                                   int64_t ld_dx, int b_layout, int dtype, void* workspace, int64_t workspace_bytes,
+                                   void* stream) {
+    Call c = call_of(X, W, T, V, D, ldx, b_layout, dtype);
+    c.targets = targets;
+    c.lse = lse;
+    c.dloss = dloss;
+    c.dloss_stride = dloss_stride;
+    c.dX = dX;
+    c.dW = dW;
+    c.ld_dx = ld_dx;
+    int rc = check_call(c, b_layout, dtype);
+    if (rc != GEMM_OK) return rc;
+    if (T > 0 && (rc = check_floats(targets)) != GEMM_OK) return rc;
+    return backward(c, workspace, workspace_bytes, stream);
+}
+
+extern "C" int gemm_relu_distill(const void* X, const void* W, const int32_t* ids, const void* logits, float temperature,
+                                 float* loss, float* lse, int64_t T, int64_t V, int64_t D, int64_t k, int64_t ldx,
+                                 int64_t ld_ids, int64_t ld_logits, int b_layout, int dtype, int logits_type,
+                                 void* workspace, int64_t workspace_bytes, void* stream) {
+    Call c = call_of(X, W, T, V, D, ldx, b_layout, dtype);
+    c.ids = ids;
+    c.logits = logits;
+    c.k = k;
+    c.ld_ids = ld_ids;
+    c.ld_logits = ld_logits;
+    c.logits_type = logits_type;
+    c.tau = temperature;
+    c.loss = loss;
+    c.lse_out = lse;
+    int rc = check_call(c, b_layout, dtype);
+    if (rc == GEMM_OK) rc = check_teacher(c);
+    return rc != GEMM_OK ? rc : forward(c, workspace, workspace_bytes, stream);
+}
+
+extern "C" int gemm_relu_distill_grad(const void* X, const void* W, const int32_t* ids, const void* logits, float temperature,
+                                      const float* lse, const float* dloss, int64_t dloss_stride, void* dX, void* dW,
+                                      int64_t T, int64_t V, int64_t D, int64_t k, int64_t ldx, int64_t ld_ids,
+                                      int64_t ld_logits, int64_t ld_dx, int b_layout, int dtype, int logits_type,
+                                      void* workspace, int64_t workspace_bytes, void* stream) {
+    Call c = call_of(X, W, T, V, D, ldx, b_layout, dtype);
+    c.ids = ids;
+    c.logits = logits;
+    c.k = k;
+    c.ld_ids = ld_ids;
+    c.ld_logits = ld_logits;
+    c.logits_type = logits_type;
+    c.tau = temperature;
+    c.lse = lse;
+    c.dloss = dloss;
+    c.dloss_stride = dloss_stride;
+    c.dX = dX;
+    c.dW = dW;
+    c.ld_dx = ld_dx;
+    int rc = check_call(c, b_layout, dtype);
+    if (rc == GEMM_OK) rc = check_teacher(c);
+    return rc != GEMM_OK ? rc : backward(c, workspace, workspace_bytes, stream);
+}

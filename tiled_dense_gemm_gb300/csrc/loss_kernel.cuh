@@ -1,0 +1,514 @@
+// The products behind the losses over a vocabulary, for sm_103a.  With z[t, v]
+// = sum_d X[t, d] W[v, d] the logits of T rows over V words, c = log2(e) / tau,
+// and the wanted words of a row (a target of weight 1, or a teacher's best
+// words with weights q):
+//
+//   kStats   per row and piece of a tile's columns: m = max z, s = sum 2^(c (z - m)),
+//            t = sum of q z over the wanted words among them        (no z is kept)
+//   kGrad    G[t, v] = a_t (2^(c z - log2(e) lse_t) - sum of q of the wanted word v)
+//            over a piece of the vocabulary, rounded to the 16-bit type
+//   kSum     dX += G W over the piece, in 32 bits, split along the piece
+//   kWeight  dW[piece] = G^T X
+//
+// One kernel, four epilogues: D = A B^T in tiles of 128 rows x `width` columns
+// per CTA, or 256 x `width` per CTA pair, over k-blocks of 64.  An operand's
+// reduction index is contiguous ("k-major": boxes of 64 k x rows) or its rows'
+// index is ("mn-major": chunks of 64 rows x 64 k), as the matrices are stored;
+// nothing is transposed in memory.  Rows of X are A's rows in kStats, kGrad and
+// kSum, so that a row's logits sit in one lane of tensor memory: the running
+// maximum and sum of the softmax never leave a thread.
+//
+// The rows in use (those with a wanted word) may have been gathered to the
+// front of a copy of X; only the device knows how many there are.  The row
+// tiles, the reduction of kWeight and the choice between X and its copy go by
+// that count.
+//
+// Roles (352 threads, one CTA per SM): warp 0 copies A's tiles and arms the
+// stages, warp 6 B's, warp 1 issues the MMAs, warps 2-5 and 7-10 drain the two
+// accumulators (a quarter of the rows each, every other chunk of 64 columns).
+// Every wait is bounded.
+#pragma once
+
+#include "ragged_kernel.cuh"
+
+namespace gr {
+namespace ls {
+
+using rg::Ctrl;
+using rg::pack16;
+using rg::wait_phase;
+
+enum Mode : int { kStats = 0, kGrad = 1, kSum = 2, kWeight = 3 };
+
+constexpr int kBK = 64;  // k per ring stage
+constexpr int kThreads = 352;
+constexpr uint32_t kStaging = 4096;  // bytes per epilogue warp
+constexpr int32_t kNone = 0x7fffffff;
+
+// What the device knows of the rows.
+struct RowsHeader {
+    int32_t valid;    // rows in use
+    int32_t compact;  // 1: they are gathered in the copy of X
+    float scale;      // of G (binary16: brings the largest a_t below 2^15), a power of two
+    float unscale;
+};
+
+struct LossMaps {
+    CUtensorMap a[2], b[2];  // (the second: where the rows are gathered)
+    CUtensorMap d;
+};
+
+struct LossParams {
+    int32_t M, N, K;       // D is M x N, K the reduction (bounds, where the rows' count replaces them)
+    int32_t rows_m;        // M is the rows' count
+    int32_t rows_k;        // K is the rows' count
+    int32_t width;         // columns of a tile
+    int32_t n_tiles;
+    int32_t group_m;       // row tiles walked together
+    int32_t splits;        // kSum: shares of the reduction, each summed apart
+    int32_t a_mn, b_mn;    // operand is mn-major
+    int32_t a_3d, b_3d;    // ... and its chunks come in one copy
+    uint32_t a_bytes;      // of a stage (the box's)
+    uint32_t stage_bytes;
+    int32_t num_stages;
+    uint32_t tmem_cols;    // allocated; half per accumulator
+    int32_t bf16;
+    int32_t w_row, w_k;    // first word of the piece, added to B's row or to its k
+    int32_t d_row, d_col;  // ... or to the output's row or column
+    int32_t first;         // kSum: 1: set, 0: add
+    const RowsHeader* rows;  // null: all T rows, as given
+    const int32_t* index;    // row of the batch of each gathered row
+    // the wanted words: a target per row, or (ids != null) k sorted ones with weights
+    const int32_t* targets;
+    const int32_t* ids;
+    const float* weights;
+    int32_t k, V;
+    float log2_scale;        // c
+    float* stats;            // kStats: [tile][half][3][stats_pitch]
+    int64_t stats_pitch;
+    const float* lse;        // kGrad
+    const float* dloss;
+    int64_t dloss_stride;    // 0 or 1
+    float grad_scale;        // tau
+    int32_t* err;
+    uint64_t timeout_ns;
+    int32_t test_drop_kb;    // as of the ragged kernels: a block of A's rows (single CTAs)
+};
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 3-D tiled add shared -> global (bulk-group completion).
+__device__ __forceinline__ void reduce_add_3d(const CUtensorMap* m, uint32_t src, int32_t x, int32_t y, int32_t z) {
+    asm volatile(
+        "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+            reinterpret_cast<uint64_t>(m)),
+        "r"(src), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+// A row's wanted words in rising order, from the first at or behind some column.
+struct Wanted {
+    const int32_t* ids;
+    const float* weights;
+    int32_t next;  // word, kNone: no more
+    int32_t left;  // words behind it
+
+    __device__ __forceinline__ void start(const LossParams& q, int32_t row, bool live, int32_t col) {
+        left = 0;
+        next = kNone;
+        if (!live) return;
+        if (!q.ids) {
+            const int32_t y = __ldcg(q.targets + row);
+            if (y >= col && y < q.V) next = y;
+            return;
+        }
+        ids = q.ids + (int64_t)row * q.k;
+        weights = q.weights + (int64_t)row * q.k;
+        int32_t lo = 0, hi = q.k;
+        while (lo < hi) {
+            const int32_t mid = (lo + hi) >> 1;
+            if (__ldcg(ids + mid) < col)
+                lo = mid + 1;
+            else
+                hi = mid;
+        }
+        ids += lo;
+        weights += lo;
+        left = q.k - lo;
+        next = left > 0 ? __ldcg(ids) : kNone;
+    }
+
+    __device__ __forceinline__ float weight() const { return ids ? __ldcg(weights) : 1.0f; }
+
+    __device__ __forceinline__ void advance() {
+        if (left > 1) {
+            ++ids;
+            ++weights;
+            --left;
+            next = __ldcg(ids);
+        } else {
+            left = 0;
+            next = kNone;
+        }
+    }
+};
+
+template <bool kPair, int kMode>
+__global__ void __launch_bounds__(kThreads, 1)
+    loss_kernel(const __grid_constant__ LossMaps maps, const __grid_constant__ LossParams q) {
+    constexpr int kCG = kPair ? 2 : 1;
+    constexpr int32_t kTileM = kPair ? 256 : 128;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem);
+    const uint32_t ring = (smem_u32(smem) + (uint32_t)sizeof(Ctrl) + 1023u) & ~1023u;
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = kPair ? cluster_ctarank() : 0u;
+    const uint32_t worker = kPair ? blockIdx.x / 2 : blockIdx.x;
+    const uint32_t workers = kPair ? gridDim.x / 2 : gridDim.x;
+    rg::Params w;  // what wait_phase reads
+    w.err = q.err;
+    w.timeout_ns = q.timeout_ns;
+
+    if (warp == 2 && lane == 0) {
+        for (int s = 0; s < q.num_stages; ++s) {
+            mbar_init(smem_u32(&ctrl->full[s]), 1);
+            mbar_init(smem_u32(&ctrl->empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&ctrl->tmem_full[b]), 1);
+            mbar_init(smem_u32(&ctrl->tmem_empty[b]), (kPair ? 2u : 1u) * 8u);
+        }
+        mbar_init(smem_u32(&ctrl->final_bar), 1);
+        ctrl->abort_flag = 0;
+        ctrl->ring_s = ctrl->ring_ph = ctrl->ring_lap = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc<kCG>(smem_u32(&ctrl->tmem_addr), q.tmem_cols);
+        tmem_relinquish<kCG>();
+    }
+    __syncwarp();
+    tc_fence_before();
+    if (kPair)
+        cluster_sync();
+    else
+        cta_barrier_sync();
+    tc_fence_after();
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const uint32_t tmem_base = ctrl->tmem_addr;
+    const uint32_t S = (uint32_t)q.num_stages, stride = q.stage_bytes;
+    const uint32_t full0 = smem_u32(&ctrl->full[0]), empty0 = smem_u32(&ctrl->empty[0]);
+    const uint32_t buf_cols = q.tmem_cols / 2;
+    const int32_t valid = q.rows ? __ldcg(&q.rows->valid) : 0;
+    const int32_t gathered = q.rows ? __ldcg(&q.rows->compact) : 0;
+    const int32_t M = q.rows_m && q.rows ? valid : q.M, K = q.rows_k ? valid : q.K;
+    const int32_t m_tiles = (M + kTileM - 1) / kTileM, blocks = (K + kBK - 1) / kBK;
+    const uint32_t tiles = (uint32_t)m_tiles * (uint32_t)q.n_tiles;
+    const uint32_t items = tiles * (uint32_t)q.splits;
+
+    // item -> share of the reduction, row tile, column tile
+    struct Work {
+        int32_t split, mt, nt, kb0, kb1;
+    };
+    uint32_t item = worker;
+    auto next = [&](Work& k) {
+        if (item >= items) return false;
+        uint32_t l = item;
+        k.split = 0;
+        k.kb0 = 0;
+        k.kb1 = blocks;
+        if (q.splits > 1) {
+            k.split = (int32_t)(item / tiles);
+            l = item - (uint32_t)k.split * tiles;
+            k.kb0 = (int32_t)((int64_t)k.split * blocks / q.splits);
+            k.kb1 = (int32_t)((int64_t)(k.split + 1) * blocks / q.splits);
+        }
+        const uint32_t per_group = (uint32_t)q.group_m * (uint32_t)q.n_tiles;
+        const uint32_t g = l / per_group, r = l - g * per_group;
+        const uint32_t first = g * (uint32_t)q.group_m;
+        const uint32_t gm = min((uint32_t)q.group_m, (uint32_t)m_tiles - first);
+        const uint32_t n = r / gm;
+        k.nt = (int32_t)n;
+        k.mt = (int32_t)(first + r - n * gm);
+        item += workers;
+        return true;
+    };
+    Work k;
+
+    if (warp == 0 || warp == 6) {
+        // warp 0 copies A's tiles and arms the stages, warp 6 B's
+        if (lane == 0) {
+            const bool is_a = warp == 0;
+            const CUtensorMap* const m = is_a ? &maps.a[gathered] : &maps.b[gathered];
+            const int32_t width = q.width / kCG;
+            uint32_t s = 0, ph = 0;
+            int32_t issued = 0;
+            bool ok = true;
+            const bool mn = is_a ? q.a_mn : q.b_mn, one = is_a ? q.a_3d : q.b_3d;
+            const int32_t chunks = is_a ? 2 : width / 64;
+            while (ok && next(k)) {
+                const int32_t r0 = is_a ? k.mt * kTileM + 128 * (int32_t)rank : k.nt * q.width + width * (int32_t)rank + q.w_row;
+                for (int32_t kb = k.kb0; kb < k.kb1; ++kb) {
+                    if (!wait_phase(empty0 + 8u * s, ph ^ 1u, ctrl, w, is_a ? rg::kErrTokens : rg::kErrWeights)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t full = full0 + 8u * s;
+                    if (is_a) {
+                        if (!kPair || rank == 0) mbar_arrive_expect_tx(full, (kPair ? 2u : 1u) * stride);
+                        ++issued;
+                    }
+                    const uint32_t bar = kPair ? mapa_shared(full, 0) : full;
+                    const uint32_t dst = ring + s * stride + (is_a ? 0u : q.a_bytes);
+                    const int32_t k0 = kb * kBK + (is_a ? 0 : q.w_k);
+                    if (!kPair && is_a && issued == q.test_drop_kb && q.test_drop_kb > 0) {
+                        // (test hook: not copied)
+                    } else if (!mn) {
+                        rg::load_2d<kPair>(dst, m, bar, k0, r0);
+                    } else if (one) {
+                        rg::load_3d<kPair>(dst, m, bar, 0, k0, r0 / 64);
+                    } else {
+                        for (int32_t j = 0; j < chunks; ++j)
+                            rg::load_2d<kPair>(dst + (uint32_t)j * (kBK * 128u), m, bar, r0 + 64 * j, k0);
+                    }
+                    if (++s == S) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            if (is_a && (!kPair || rank == 0)) {
+                ctrl->ring_s = (int32_t)s;
+                ctrl->ring_ph = (int32_t)ph;
+                ctrl->ring_lap = issued >= (int32_t)S ? 1 : 0;
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0 && (!kPair || rank == 0)) {
+            const uint32_t tfull0 = smem_u32(&ctrl->tmem_full[0]), tempty0 = smem_u32(&ctrl->tmem_empty[0]);
+            const uint32_t idesc = make_idesc_f16_f32((uint32_t)kTileM, (uint32_t)q.width, q.a_mn != 0, q.b_mn != 0, q.bf16 != 0);
+            // k-major: 32 bytes per 16 k inside the swizzled rows; mn-major: 16 rows of k
+            const uint64_t a_desc0 = make_sw128_desc(ring, q.a_mn ? kBK * 128u : 16u, 1024);
+            const uint64_t b_desc0 = make_sw128_desc(ring + q.a_bytes, q.b_mn ? kBK * 128u : 16u, 1024);
+            const uint64_t a_step = q.a_mn ? 128u : 2u, b_step = q.b_mn ? 128u : 2u;
+            uint32_t s = 0, ph = 0, local = 0;
+            bool ok = true;
+            while (ok && next(k)) {
+                if (k.kb0 == k.kb1) continue;
+                const uint32_t buf = local & 1u, bph = (local >> 1) & 1u;
+                if (!wait_phase(tempty0 + 8u * buf, bph ^ 1u, ctrl, w, rg::kErrAccum)) break;
+                tc_fence_after();
+                const uint32_t d = tmem_base + buf * buf_cols;
+                for (int32_t kb = k.kb0; kb < k.kb1; ++kb) {
+                    if (!wait_phase(full0 + 8u * s, ph, ctrl, w, rg::kErrStage)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t a_desc = a_desc0 + (uint64_t)(s * (stride >> 4));
+                    const uint64_t b_desc = b_desc0 + (uint64_t)(s * (stride >> 4));
+                    const uint32_t acc = kb > k.kb0 ? 1u : 0u;
+#pragma unroll
+                    for (uint32_t i = 0; i < kBK / 16; ++i)
+                        mma_f16_ss<kCG>(d, a_desc + i * a_step, b_desc + i * b_step, idesc, i > 0 ? 1u : acc);
+                    mma_commit<kCG>(empty0 + 8u * s, 0x3);
+                    if (++s == S) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                mma_commit<kCG>(tfull0 + 8u * buf, 0x3);
+                ++local;
+            }
+            mma_commit<kCG>(smem_u32(&ctrl->final_bar), 0x1);
+            const uint64_t t0 = globaltimer_ns();
+            while (!mbar_try_wait(smem_u32(&ctrl->final_bar), 0))
+                if (globaltimer_ns() - t0 > q.timeout_ns) {
+                    atomicCAS(q.err, 0, (int32_t)rg::kErrFinal);
+                    break;
+                }
+        }
+        __syncwarp();
+    } else {
+        const uint32_t quarter = warp & 3u, half = warp >= 7 ? 1u : 0u;
+        const uint32_t staging = ring + S * stride + (quarter + 4u * half) * kStaging;
+        const int32_t chunks = q.width / 64;
+        // (G's rows are kWeight's reduction: zeros up to the end of its last k-block)
+        const int32_t row_end = kMode == kGrad ? (M + kBK - 1) / kBK * kBK : M;
+        uint32_t local = 0;
+        while (next(k)) {
+            const bool some = k.kb1 > k.kb0;
+            const uint32_t buf = local & 1u, bph = (local >> 1) & 1u;
+            const int32_t row0 = k.mt * kTileM + 128 * (int32_t)rank + 32 * (int32_t)quarter;
+            const int32_t r = row0 + (int32_t)lane, n0 = k.nt * q.width;
+            const bool live = r < M;
+            // what the row's epilogue reads, before the accumulator is waited for
+            Wanted want = {nullptr, nullptr, kNone, 0};
+            float coef = 0.0f, shift = 0.0f;
+            if constexpr (kMode == kStats || kMode == kGrad) {
+                const int32_t t = live && gathered ? __ldcg(q.index + r) : r;
+                want.start(q, t, live, n0 + q.w_row);
+                if constexpr (kMode == kGrad) {
+                    if (live) {
+                        shift = -1.4426950408889634f * __ldg(q.lse + t);
+                        coef = __ldg(q.dloss + (int64_t)t * q.dloss_stride) * q.grad_scale * __ldcg(&q.rows->scale);
+                    }
+                }
+            }
+            if (some) {
+                if (!__all_sync(0xffffffffu, wait_phase(smem_u32(&ctrl->tmem_full[buf]), bph, ctrl, w, rg::kErrEpi))) break;
+                tc_fence_after();
+            }
+            const uint32_t taddr = tmem_base + ((quarter * 32u) << 16) + buf * buf_cols;
+            const float c = q.log2_scale;
+            float m_run = -INFINITY, s_run = 0.0f, t_run = 0.0f;
+            for (int32_t ch = (int32_t)half; ch < chunks; ch += 2) {
+                const int32_t col = n0 + 64 * ch;
+                if (col >= q.N || row0 >= row_end) break;  // (uniform over the warp)
+                float v[64];
+                if (some) {
+                    __syncwarp();
+                    tmem_load_64cols(taddr + 64u * (uint32_t)ch, v);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) v[j] = 0.0f;
+                }
+                if constexpr (kMode == kStats || kMode == kGrad) {
+                    const int32_t c0 = col + q.w_row;  // the chunk's first word
+                    while (want.next < c0) want.advance();  // (of the other half's chunk)
+                    if constexpr (kMode == kStats) {
+                        while (__any_sync(0xffffffffu, want.next - c0 < 64)) {
+                            const int32_t at = want.next - c0;
+                            float z = 0.0f;
+#pragma unroll
+                            for (int j = 0; j < 64; ++j) z = j == at ? v[j] : z;
+                            if (at < 64) {
+                                const float p = want.weight();
+                                if (p != 0.0f) t_run = fmaf(p, z, t_run);
+                                want.advance();
+                            }
+                        }
+                        if (col + 64 > q.N) {
+#pragma unroll
+                            for (int j = 0; j < 64; ++j) v[j] = col + j < q.N ? v[j] : -INFINITY;
+                        }
+                        float top[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+                        for (int j = 4; j < 64; ++j) top[j % 4] = fmaxf(top[j % 4], v[j]);
+                        const float m_new = fmaxf(fmaxf(m_run, fmaxf(top[0], top[1])), fmaxf(top[2], top[3]));
+                        // (infinite maxima: the terms are taken as they are, so that the sum says what the row holds)
+                        const float ref = fabsf(m_new) == INFINITY ? 0.0f : m_new;
+                        const float off = -ref * c;
+                        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                        for (int j = 0; j < 64; ++j) sum[j % 4] += exp2_fast(fmaf(v[j], c, off));
+                        s_run = fmaf(s_run, exp2_fast(fmaf(m_run, c, off)), (sum[0] + sum[1]) + (sum[2] + sum[3]));
+                        m_run = m_new;
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 64; ++j) {
+                            const float p = coef * exp2_fast(fmaf(v[j], c, shift));
+                            v[j] = live && col + j < q.N ? p : 0.0f;
+                        }
+                        while (__any_sync(0xffffffffu, want.next - c0 < 64)) {
+                            const int32_t at = want.next - c0;
+                            if (at < 64) {
+                                const float p = coef * want.weight();
+#pragma unroll
+                                for (int j = 0; j < 64; ++j) v[j] = j == at ? v[j] - p : v[j];
+                                want.advance();
+                            }
+                        }
+                    }
+                }
+                if constexpr (kMode == kGrad || kMode == kWeight) {
+                    const float u = kMode == kWeight ? __ldcg(&q.rows->unscale) : 1.0f;
+                    uint32_t x[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) x[j] = pack16(u * v[2 * j], u * v[2 * j + 1], q.bf16);
+                    // the copy issued from this buffer before must have read it
+                    if (lane == 0) bulk_wait_group_read<0>();
+                    __syncwarp();
+#pragma unroll
+                    for (uint32_t i = 0; i < 8; ++i)
+                        rg::st_shared_v4(staging + lane * 128u + ((i ^ (lane & 7u)) << 4),
+                                         make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]));
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_2d(&maps.d, staging, col + q.d_col, row0 + q.d_row);
+                        bulk_commit_group();
+                    }
+                }
+                if constexpr (kMode == kSum) {
+                    if (!some && !q.first) break;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (col + 32 * h >= q.N) break;
+                        if (lane == 0) bulk_wait_group_read<0>();
+                        __syncwarp();
+#pragma unroll
+                        for (uint32_t i = 0; i < 8; ++i)
+                            rg::st_shared_v4(staging + lane * 128u + ((i ^ (lane & 7u)) << 4),
+                                             make_uint4(__float_as_uint(v[32 * h + 4 * i]), __float_as_uint(v[32 * h + 4 * i + 1]),
+                                                        __float_as_uint(v[32 * h + 4 * i + 2]),
+                                                        __float_as_uint(v[32 * h + 4 * i + 3])));
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (q.first)
+                                rg::store_3d(&maps.d, staging, col + 32 * h, row0, k.split);
+                            else
+                                reduce_add_3d(&maps.d, staging, col + 32 * h, row0, k.split);
+                            bulk_commit_group();
+                        }
+                    }
+                }
+            }
+            if constexpr (kMode == kStats) {
+                const int32_t halves = min(chunks, 2);
+                if (live && (int32_t)half < halves) {
+                    float* const o = q.stats + (int64_t)(k.nt * halves + (int32_t)half) * 3 * q.stats_pitch + r;
+                    o[0] = m_run;
+                    o[q.stats_pitch] = s_run;
+                    o[2 * q.stats_pitch] = t_run;
+                }
+            }
+            if (some) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (kPair)
+                        rg::mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&ctrl->tmem_empty[buf]), 0));
+                    else
+                        mbar_arrive(smem_u32(&ctrl->tmem_empty[buf]));
+                }
+                ++local;
+            }
+        }
+        if (lane == 0) bulk_wait_group_all();
+        __syncwarp();
+    }
+
+    __syncthreads();
+    if (threadIdx.x == 0 && *(volatile int32_t*)&ctrl->abort_flag) rg::drain_ring(ctrl, full0, S);
+    tc_fence_before();
+    if (kPair)
+        cluster_sync_relaxed();  // the other CTA's accesses to this one's shared memory are done
+    else
+        __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc<kCG>(tmem_base, q.tmem_cols);
+    }
+}
+
+}  // namespace ls
+}  // namespace gr

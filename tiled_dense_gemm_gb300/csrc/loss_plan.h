@@ -1,0 +1,44 @@
+// Host planning of the losses over a vocabulary (pure host code): pieces of
+// the vocabulary, tile shapes, shares of the reductions, workspace.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "gemm_relu.h"
+
+namespace gr {
+namespace ls {
+
+// One product's tiles.
+struct TilePlan {
+    int32_t pair;     // CTA pairs
+    int32_t width;    // columns of a tile
+    int32_t m_tiles, n_tiles, splits, group_m;
+    int32_t a_rows;   // rows of A's box (k-major)
+    int32_t a_bytes, stage_bytes, num_stages, smem_bytes, tmem_cols, grid;
+};
+
+struct LossPlan {
+    int32_t status;
+    int64_t rows;        // forward: rows of a block; backward: all
+    int64_t piece;       // backward: words of a piece, a multiple of 256 (the last one may be shorter)
+    int32_t pieces;
+    int32_t gather;      // the rows' kernel runs
+    int32_t parts;       // forward: statistics per row
+    int32_t sum_splits;  // backward: shares of dX's reduction
+    // workspace, in bytes from its start
+    int64_t header, index, flags, entropy, sorted, weights, gathered, stats, grad, sums, bytes;
+};
+
+// T x N products of the forward pass and of G; K the reduction.  b_mn: B's
+// chunks are of 64 columns.
+TilePlan plan_logits(int64_t T, int64_t N, int64_t K, bool b_mn, bool staged, int num_sms, int max_pairs);
+TilePlan plan_sum(int64_t T, int64_t N, int64_t K, int splits, bool b_mn, int num_sms, int max_pairs);
+TilePlan plan_weight(int64_t M, int64_t N, int64_t K, int num_sms, int max_pairs);
+
+// k: words of a teacher per row, 0: targets.
+LossPlan plan_loss(int64_t T, int64_t V, int64_t D, int64_t k, bool gradient);
+
+}  // namespace ls
+}  // namespace gr
