@@ -353,9 +353,10 @@ typedef enum {
  * not overlap inputs (not checked).  T == 0: nothing but dW = +0.
  *
  * Arithmetic: z, the softmax and both sums in fp32; g is rounded to `dtype` once
- * before the gradients' products, dX and dW once at the end.  In binary16 g is
- * held times a power of two that brings the largest |dloss tau| to [2^14, 2^15):
- * terms below 2^-39 of that are lost, below 2^-29 they lose bits.  Results do not
+ * before the gradients' products, dX and dW once at the end.  g is held times a
+ * factor that brings the largest |dloss tau| to the top of a binade, in binary16
+ * just below 2^15: there terms below 2^-40 of that are lost, and those below
+ * 2^-29 lose bits.  (Outside 1e-30 .. 1e30 the factor is 1.)  Results do not
  * depend on the order in which CTAs run.  Logits that are not finite follow IEEE
  * 754: an infinite lse, or NaN, in that row.
  *

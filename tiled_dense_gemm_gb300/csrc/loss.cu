@@ -131,7 +131,11 @@ static int run_rows(const Call& c, const LossPlan& p, int64_t b0, int64_t T, Dev
     q.dloss = c.dloss;
     q.dloss_stride = c.dloss_stride;
     q.grad_scale = c.ids ? c.tau : 1.0f;
-    q.scaled = c.dloss && !c.bf16 ? 1 : 0;
+    // The largest entries of G, a (p - 1) of wanted words that are not foreseen,
+    // are near the top of a binade, where a 16-bit type rounds finest, and the
+    // limit itself is exact; binary16 besides keeps what it can of small ones
+    // (relative error of bfloat16 gradients: PLACEHOLDER).
+    q.top = c.bf16 ? 255.0f / 128.0f : 2047.0f / 1024.0f * 16384.0f;
     q.err = d.d_err;
     const int grid = (int)std::max<int64_t>(1, std::min<int64_t>((T + 31) / 32, 2 * d.sm_count));
     return launch(loss_rows_kernel, grid, kRowsThreads, 0, 1, c.st, q);

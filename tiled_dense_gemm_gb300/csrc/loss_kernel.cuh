@@ -49,7 +49,7 @@ constexpr int32_t kNone = 0x7fffffff;
 struct RowsHeader {
     int32_t valid;    // rows in use
     int32_t compact;  // 1: they are gathered in the copy of X
-    float scale;      // of G (binary16: brings the largest a_t below 2^15), a power of two
+    float scale;      // of G, and its inverse: brings the largest |a_t| to the top of a binade
     float unscale;
 };
 
@@ -117,12 +117,14 @@ struct Wanted {
     int32_t next;  // word, kNone: no more
     int32_t left;  // words behind it
 
-    __device__ __forceinline__ void start(const LossParams& q, int32_t row, bool live, int32_t col) {
+    // `y`: the row's target where there is no teacher
+    __device__ __forceinline__ void start(const LossParams& q, int32_t row, int32_t y, bool live, int32_t col) {
         left = 0;
         next = kNone;
+        ids = nullptr;
+        weights = nullptr;
         if (!live) return;
         if (!q.ids) {
-            const int32_t y = __ldcg(q.targets + row);
             if (y >= col && y < q.V) next = y;
             return;
         }
@@ -156,6 +158,16 @@ struct Wanted {
         }
     }
 };
+
+// kStats: the reduction in parts of at most this many k-blocks, each in an
+// accumulator of its own, added up in registers.  The tensor core truncates its
+// sums in 32 bits, 16 products at a time, always towards zero: over 4096 that was
+// 2.4e-6 of the losses (against 6e-7 of a sum that rounds), in parts of 1024 it
+// is PLACEHOLDER.  The epilogue's warps have the time.
+constexpr int32_t kPartBlocks = 16;
+
+__device__ __forceinline__ int32_t part_count(int32_t blocks) { return (blocks + kPartBlocks - 1) / kPartBlocks; }
+__device__ __forceinline__ int32_t part_end(int32_t blocks, int32_t part, int32_t parts) { return part * blocks / parts; }
 
 template <bool kPair, int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -301,31 +313,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             while (ok && next(k)) {
                 if (k.kb0 == k.kb1) continue;
-                const uint32_t buf = local & 1u, bph = (local >> 1) & 1u;
-                if (!wait_phase(tempty0 + 8u * buf, bph ^ 1u, ctrl, w, rg::kErrAccum)) break;
-                tc_fence_after();
-                const uint32_t d = tmem_base + buf * buf_cols;
-                for (int32_t kb = k.kb0; kb < k.kb1; ++kb) {
-                    if (!wait_phase(full0 + 8u * s, ph, ctrl, w, rg::kErrStage)) {
+                const int32_t parts = kMode == kStats ? part_count(k.kb1) : 1;
+                int32_t kb = k.kb0;
+                for (int32_t part = 1; ok && part <= parts; ++part) {
+                    const int32_t begin = kb, end = kMode == kStats ? part_end(k.kb1, part, parts) : k.kb1;
+                    const uint32_t buf = local & 1u, bph = (local >> 1) & 1u;
+                    if (!wait_phase(tempty0 + 8u * buf, bph ^ 1u, ctrl, w, rg::kErrAccum)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint64_t a_desc = a_desc0 + (uint64_t)(s * (stride >> 4));
-                    const uint64_t b_desc = b_desc0 + (uint64_t)(s * (stride >> 4));
-                    const uint32_t acc = kb > k.kb0 ? 1u : 0u;
+                    const uint32_t d = tmem_base + buf * buf_cols;
+                    for (; kb < end; ++kb) {
+                        if (!wait_phase(full0 + 8u * s, ph, ctrl, w, rg::kErrStage)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint64_t a_desc = a_desc0 + (uint64_t)(s * (stride >> 4));
+                        const uint64_t b_desc = b_desc0 + (uint64_t)(s * (stride >> 4));
+                        const uint32_t acc = kb > begin ? 1u : 0u;
 #pragma unroll
-                    for (uint32_t i = 0; i < kBK / 16; ++i)
-                        mma_f16_ss<kCG>(d, a_desc + i * a_step, b_desc + i * b_step, idesc, i > 0 ? 1u : acc);
-                    mma_commit<kCG>(empty0 + 8u * s, 0x3);
-                    if (++s == S) {
-                        s = 0;
-                        ph ^= 1u;
+                        for (uint32_t i = 0; i < kBK / 16; ++i)
+                            mma_f16_ss<kCG>(d, a_desc + i * a_step, b_desc + i * b_step, idesc, i > 0 ? 1u : acc);
+                        mma_commit<kCG>(empty0 + 8u * s, 0x3);
+                        if (++s == S) {
+                            s = 0;
+                            ph ^= 1u;
+                        }
                     }
+                    if (!ok) break;
+                    mma_commit<kCG>(tfull0 + 8u * buf, 0x3);
+                    ++local;
                 }
-                if (!ok) break;
-                mma_commit<kCG>(tfull0 + 8u * buf, 0x3);
-                ++local;
             }
             mma_commit<kCG>(smem_u32(&ctrl->final_bar), 0x1);
             const uint64_t t0 = globaltimer_ns();
@@ -345,16 +365,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t local = 0;
         while (next(k)) {
             const bool some = k.kb1 > k.kb0;
-            const uint32_t buf = local & 1u, bph = (local >> 1) & 1u;
             const int32_t row0 = k.mt * kTileM + 128 * (int32_t)rank + 32 * (int32_t)quarter;
             const int32_t r = row0 + (int32_t)lane, n0 = k.nt * q.width;
             const bool live = r < M;
             // what the row's epilogue reads, before the accumulator is waited for
-            Wanted want = {nullptr, nullptr, kNone, 0};
+            int32_t t = 0, y = kNone;
             float coef = 0.0f, shift = 0.0f;
             if constexpr (kMode == kStats || kMode == kGrad) {
-                const int32_t t = live && gathered ? __ldcg(q.index + r) : r;
-                want.start(q, t, live, n0 + q.w_row);
+                t = live && gathered ? __ldcg(q.index + r) : r;
+                if (live && !q.ids) y = __ldcg(q.targets + t);
                 if constexpr (kMode == kGrad) {
                     if (live) {
                         shift = -1.4426950408889634f * __ldg(q.lse + t);
@@ -362,13 +381,103 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
+            auto release = [&](uint32_t buf) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (kPair)
+                        rg::mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&ctrl->tmem_empty[buf]), 0));
+                    else
+                        mbar_arrive(smem_u32(&ctrl->tmem_empty[buf]));
+                }
+            };
+            const float c = q.log2_scale;
+            if constexpr (kMode == kStats) {
+                // z of this warp's chunks, summed over the parts of the reduction
+                float z[2][64];
+#pragma unroll
+                for (int j = 0; j < 64; ++j) z[0][j] = z[1][j] = 0.0f;
+                const int32_t parts = part_count(k.kb1);
+                bool ok = true;
+#pragma unroll 1
+                for (int32_t part = 0; part < parts; ++part) {
+                    const uint32_t buf = local & 1u, bph = (local >> 1) & 1u;
+                    if (!__all_sync(0xffffffffu, wait_phase(smem_u32(&ctrl->tmem_full[buf]), bph, ctrl, w, rg::kErrEpi))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t taddr = tmem_base + ((quarter * 32u) << 16) + buf * buf_cols;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int32_t ch = (int32_t)half + 2 * i;
+                        if (ch >= chunks) break;
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            float v[16];
+                            __syncwarp();
+                            tmem_load_16cols(taddr + 64u * (uint32_t)ch + 16u * h, v);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) z[i][16 * h + j] += v[j];
+                        }
+                    }
+                    release(buf);
+                    ++local;
+                }
+                if (!ok) break;
+                Wanted want;
+                want.start(q, t, y, live, n0);
+                float m_run = -INFINITY, s_run = 0.0f, t_run = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int32_t ch = (int32_t)half + 2 * i, col = n0 + 64 * ch;
+                    if (ch >= chunks || col >= q.N || row0 >= M) break;  // (uniform over the warp)
+                    float(&v)[64] = z[i];
+                    while (want.next < col) want.advance();  // (of the other half's chunk)
+                    while (__any_sync(0xffffffffu, want.next - col < 64)) {
+                        const int32_t at = want.next - col;
+                        float x = 0.0f;
+#pragma unroll
+                        for (int j = 0; j < 64; ++j) x = j == at ? v[j] : x;
+                        if (at < 64) {
+                            const float p = want.weight();
+                            if (p != 0.0f) t_run = fmaf(p, x, t_run);
+                            want.advance();
+                        }
+                    }
+                    if (col + 64 > q.N) {
+#pragma unroll
+                        for (int j = 0; j < 64; ++j) v[j] = col + j < q.N ? v[j] : -INFINITY;
+                    }
+                    float top[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+                    for (int j = 4; j < 64; ++j) top[j % 4] = fmaxf(top[j % 4], v[j]);
+                    const float m_new = fmaxf(fmaxf(m_run, fmaxf(top[0], top[1])), fmaxf(top[2], top[3]));
+                    // (infinite maxima: the terms are taken as they are, so that the sum says what the row holds)
+                    const float off = fabsf(m_new) == INFINITY ? 0.0f : -m_new * c;
+                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) sum[j % 4] += exp2_fast(fmaf(v[j], c, off));
+                    s_run = fmaf(s_run, exp2_fast(fmaf(m_run, c, off)), (sum[0] + sum[1]) + (sum[2] + sum[3]));
+                    m_run = m_new;
+                }
+                const int32_t halves = min(chunks, 2);
+                if (live && (int32_t)half < halves) {
+                    float* const o = q.stats + (int64_t)(k.nt * halves + (int32_t)half) * 3 * q.stats_pitch + r;
+                    o[0] = m_run;
+                    o[q.stats_pitch] = s_run;
+                    o[2 * q.stats_pitch] = t_run;
+                }
+                continue;
+            }
+            Wanted want;
+            if constexpr (kMode == kGrad) want.start(q, t, y, live, n0 + q.w_row);
+            const uint32_t buf = local & 1u, bph = (local >> 1) & 1u;
             if (some) {
                 if (!__all_sync(0xffffffffu, wait_phase(smem_u32(&ctrl->tmem_full[buf]), bph, ctrl, w, rg::kErrEpi))) break;
                 tc_fence_after();
             }
             const uint32_t taddr = tmem_base + ((quarter * 32u) << 16) + buf * buf_cols;
-            const float c = q.log2_scale;
-            float m_run = -INFINITY, s_run = 0.0f, t_run = 0.0f;
             for (int32_t ch = (int32_t)half; ch < chunks; ch += 2) {
                 const int32_t col = n0 + 64 * ch;
                 if (col >= q.N || row0 >= row_end) break;  // (uniform over the warp)
@@ -380,51 +489,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 64; ++j) v[j] = 0.0f;
                 }
-                if constexpr (kMode == kStats || kMode == kGrad) {
+                if constexpr (kMode == kGrad) {
                     const int32_t c0 = col + q.w_row;  // the chunk's first word
                     while (want.next < c0) want.advance();  // (of the other half's chunk)
-                    if constexpr (kMode == kStats) {
-                        while (__any_sync(0xffffffffu, want.next - c0 < 64)) {
-                            const int32_t at = want.next - c0;
-                            float z = 0.0f;
 #pragma unroll
-                            for (int j = 0; j < 64; ++j) z = j == at ? v[j] : z;
-                            if (at < 64) {
-                                const float p = want.weight();
-                                if (p != 0.0f) t_run = fmaf(p, z, t_run);
-                                want.advance();
-                            }
-                        }
-                        if (col + 64 > q.N) {
+                    for (int j = 0; j < 64; ++j) {
+                        const float p = coef * exp2_fast(fmaf(v[j], c, shift));
+                        v[j] = live && col + j < q.N ? p : 0.0f;
+                    }
+                    while (__any_sync(0xffffffffu, want.next - c0 < 64)) {
+                        const int32_t at = want.next - c0;
+                        if (at < 64) {
+                            const float p = coef * want.weight();
 #pragma unroll
-                            for (int j = 0; j < 64; ++j) v[j] = col + j < q.N ? v[j] : -INFINITY;
-                        }
-                        float top[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-                        for (int j = 4; j < 64; ++j) top[j % 4] = fmaxf(top[j % 4], v[j]);
-                        const float m_new = fmaxf(fmaxf(m_run, fmaxf(top[0], top[1])), fmaxf(top[2], top[3]));
-                        // (infinite maxima: the terms are taken as they are, so that the sum says what the row holds)
-                        const float ref = fabsf(m_new) == INFINITY ? 0.0f : m_new;
-                        const float off = -ref * c;
-                        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                        for (int j = 0; j < 64; ++j) sum[j % 4] += exp2_fast(fmaf(v[j], c, off));
-                        s_run = fmaf(s_run, exp2_fast(fmaf(m_run, c, off)), (sum[0] + sum[1]) + (sum[2] + sum[3]));
-                        m_run = m_new;
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 64; ++j) {
-                            const float p = coef * exp2_fast(fmaf(v[j], c, shift));
-                            v[j] = live && col + j < q.N ? p : 0.0f;
-                        }
-                        while (__any_sync(0xffffffffu, want.next - c0 < 64)) {
-                            const int32_t at = want.next - c0;
-                            if (at < 64) {
-                                const float p = coef * want.weight();
-#pragma unroll
-                                for (int j = 0; j < 64; ++j) v[j] = j == at ? v[j] - p : v[j];
-                                want.advance();
-                            }
+                            for (int j = 0; j < 64; ++j) v[j] = j == at ? v[j] - p : v[j];
+                            want.advance();
                         }
                     }
                 }
@@ -472,24 +551,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if constexpr (kMode == kStats) {
-                const int32_t halves = min(chunks, 2);
-                if (live && (int32_t)half < halves) {
-                    float* const o = q.stats + (int64_t)(k.nt * halves + (int32_t)half) * 3 * q.stats_pitch + r;
-                    o[0] = m_run;
-                    o[q.stats_pitch] = s_run;
-                    o[2 * q.stats_pitch] = t_run;
-                }
-            }
             if (some) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if (kPair)
-                        rg::mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&ctrl->tmem_empty[buf]), 0));
-                    else
-                        mbar_arrive(smem_u32(&ctrl->tmem_empty[buf]));
-                }
+                release(buf);
                 ++local;
             }
         }

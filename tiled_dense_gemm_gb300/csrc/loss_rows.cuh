@@ -126,7 +126,7 @@ struct RowsParams {
     const float* dloss;     // null: no scale wanted
     int64_t dloss_stride;
     float grad_scale;
-    int32_t scaled;         // binary16
+    float top;              // what the largest |dloss grad_scale| is scaled to
     int32_t* err;
 };
 
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kRowsThreads) loss_rows_kernel(const __grid_co
         for (int64_t c = i; c < n; c += kRowsThreads) dst[c] = make_uint4(0, 0, 0, 0);
     }
     float scale = 1.0f;
-    if (p.scaled) {
+    if (p.dloss) {
         float top = 0.0f;
         if (p.dloss_stride == 0) {
             top = fabsf(__ldg(p.dloss));
@@ -223,8 +223,7 @@ __global__ void __launch_bounds__(kRowsThreads) loss_rows_kernel(const __grid_co
         top = 0.0f;
         for (int32_t j = 0; j < kRowsThreads / 32; ++j) top = fmaxf(top, parts[j]);
         top *= p.grad_scale;
-        // |top| < 2^(e + 1): scaled below 2^15
-        if (top > 0.0f && top < INFINITY) scale = exp2f((float)max(-100, min(100, 14 - ilogbf(top))));
+        if (top > 1e-30f && top < 1e30f) scale = p.top / top;
     }
     if (i == 0) {
         p.rows->valid = total;
