@@ -74,6 +74,8 @@ static int launch_tiles(DeviceState& d, const TilePlan& t, const LossMaps& m, co
 template <int kMode>
 static int launch_mode(DeviceState& d, const TilePlan& t, const LossMaps& m, LossParams& q, cudaStream_t st) {
     q.width = t.width;
+    q.bk = t.bk;
+    q.bufs = t.bufs;
     q.n_tiles = t.n_tiles;
     q.group_m = t.group_m;
     q.splits = t.splits;
@@ -82,7 +84,7 @@ static int launch_mode(DeviceState& d, const TilePlan& t, const LossMaps& m, Los
     q.num_stages = t.num_stages;
     q.tmem_cols = (uint32_t)t.tmem_cols;
     q.err = d.d_err;
-    const int64_t blocks = ((int64_t)q.K + kBK - 1) / kBK;
+    const int64_t blocks = ((int64_t)q.K + q.bk - 1) / q.bk;
     q.timeout_ns = 2000000000ull + 2000ull * (uint64_t)blocks;
     if (kMode == kStats) {
         const int rc = rt::test_hook(!t.pair, (int32_t)std::min<int64_t>(blocks, kNone), &q.test_drop_kb, &q.timeout_ns);
@@ -126,6 +128,11 @@ static int run_rows(const Call& c, const LossPlan& p, int64_t b0, int64_t T, Dev
     q.X = reinterpret_cast<const uint16_t*>(c.X) + b0 * c.ldx;
     q.ldx = c.ldx;
     q.gathered = reinterpret_cast<uint16_t*>(c.ws + p.gathered);
+    q.pitch = (int32_t)p.pitch;
+    // A box row of a matrix whose pitch is not a multiple of 128 bytes lies in two
+    // lines; one such operand of two costs little, both a fifth (PLACEHOLDER).  W
+    // stays as it is.
+    q.always = T > 128 && (c.ldx % 64 != 0 || misaligned(q.X, 128));
     q.index = reinterpret_cast<int32_t*>(c.ws + p.index);
     q.rows = reinterpret_cast<RowsHeader*>(c.ws + p.header);
     q.dloss = c.dloss;
@@ -137,7 +144,7 @@ static int run_rows(const Call& c, const LossPlan& p, int64_t b0, int64_t T, Dev
     // (relative error of bfloat16 gradients: PLACEHOLDER).
     q.top = c.bf16 ? 255.0f / 128.0f : 2047.0f / 1024.0f * 16384.0f;
     q.err = d.d_err;
-    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>((T + 31) / 32, 2 * d.sm_count));
+    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>((T + 7) / 8, 4 * d.sm_count));
     return launch(loss_rows_kernel, grid, kRowsThreads, 0, 1, c.st, q);
 }
 
@@ -157,21 +164,22 @@ static void wanted(const Call& c, const LossPlan& p, int64_t b0, LossParams& q) 
     q.log2_scale = 1.4426950408889634f / c.tau;
 }
 
-// W as B's side of the logits (reduction D), `width` words per CTA.
-static int encode_words(CUtensorMap* m, const Call& c, int32_t width, LossParams& q) {
+// W as B's side of the logits (reduction D).
+static int encode_words(CUtensorMap* m, const Call& c, const TilePlan& t, LossParams& q) {
+    const uint32_t width = (uint32_t)(t.width / (t.pair ? 2 : 1));
     q.b_mn = c.nk ? 0 : 1;
-    q.b_3d = c.V % 64 == 0;
-    return c.nk ? encode_rows(m, c.W, (uint64_t)c.D, (uint64_t)c.V, (uint64_t)c.D, (uint32_t)width, 0, c.bf16)
-                : encode_rows(m, c.W, (uint64_t)c.V, (uint64_t)c.D, (uint64_t)c.V, kBK, q.b_3d ? (uint32_t)width / 64 : 0, c.bf16);
+    q.b_3d = (c.nk ? c.D : c.V) % 64 == 0;
+    return c.nk ? encode_rows(m, c.W, (uint64_t)c.D, (uint64_t)c.V, (uint64_t)c.D, width, q.b_3d ? (uint32_t)t.bk / 64 : 0, c.bf16)
+                : encode_rows(m, c.W, (uint64_t)c.V, (uint64_t)c.D, (uint64_t)c.V, (uint32_t)t.bk, q.b_3d ? width / 64 : 0, c.bf16);
 }
 
-// X's rows and their gathered copy, read as boxes of `box` rows (`chunks`: mn-major, in one copy).
-static int encode_x(CUtensorMap* m, const Call& c, const LossPlan& p, int64_t b0, int64_t T, uint32_t box, uint32_t chunks) {
+// X's rows and their gathered copy, read as boxes of `box` rows, `blocks` of 64 columns in one copy (0: one by one).
+static int encode_x(CUtensorMap* m, const Call& c, const LossPlan& p, int64_t b0, int64_t T, uint32_t box, uint32_t blocks) {
     int rc = encode_rows(&m[0], reinterpret_cast<const uint16_t*>(c.X) + b0 * c.ldx, (uint64_t)c.D, (uint64_t)T, (uint64_t)c.ldx,
-                         box, chunks, c.bf16);
+                         box, blocks, c.bf16);
     m[1] = m[0];
     if (rc == GEMM_OK && p.gather)
-        rc = encode_rows(&m[1], c.ws + p.gathered, (uint64_t)c.D, (uint64_t)T, (uint64_t)c.D, box, chunks, c.bf16);
+        rc = encode_rows(&m[1], c.ws + p.gathered, (uint64_t)c.D, (uint64_t)T, (uint64_t)p.pitch, box, blocks, c.bf16);
     return rc;
 }
 
@@ -180,7 +188,7 @@ static int run_forward(const Call& c, const LossPlan& p, DeviceState& d) {
         const int64_t T = std::min(p.rows, c.T - b0);
         int rc = run_rows(c, p, b0, T, d);
         if (rc != GEMM_OK) return rc;
-        const TilePlan t = plan_logits(T, c.V, c.D, !c.nk, false, d.sm_count, d.max_pairs);
+        const TilePlan t = plan_logits(T, c.V, c.D, !c.nk, true, d.sm_count, d.max_pairs);
         LossMaps m;
         LossParams q;
         memset(&q, 0, sizeof(q));
@@ -191,8 +199,9 @@ static int run_forward(const Call& c, const LossPlan& p, DeviceState& d) {
         wanted(c, p, b0, q);
         q.stats = reinterpret_cast<float*>(c.ws + p.stats);
         q.stats_pitch = (p.rows + 31) / 32 * 32;
-        rc = encode_x(m.a, c, p, b0, T, (uint32_t)t.a_rows, 0);
-        if (rc == GEMM_OK) rc = encode_words(&m.b[0], c, t.width / (t.pair ? 2 : 1), q);
+        q.a_3d = c.D % 64 == 0;
+        rc = encode_x(m.a, c, p, b0, T, (uint32_t)t.a_rows, q.a_3d ? (uint32_t)t.bk / 64 : 0);
+        if (rc == GEMM_OK) rc = encode_words(&m.b[0], c, t, q);
         if (rc != GEMM_OK) return rc;
         m.b[1] = m.b[0];
         m.d = m.a[0];
@@ -202,7 +211,7 @@ static int run_forward(const Call& c, const LossPlan& p, DeviceState& d) {
         memset(&o, 0, sizeof(o));
         o.stats = q.stats;
         o.pitch = q.stats_pitch;
-        o.parts = t.n_tiles * std::min(t.width / 64, 2);
+        o.parts = t.n_tiles;
         o.T = (int32_t)T;
         o.rows = q.rows;
         o.index = q.index;
@@ -214,9 +223,8 @@ static int run_forward(const Call& c, const LossPlan& p, DeviceState& d) {
         o.loss = c.loss + b0;
         o.lse = c.lse_out + b0;
         o.err = d.d_err;
-        const int blocks = (int)((T + 31) / 32);
-        rc = blocks < 2 * d.sm_count ? launch(loss_combine_kernel<32>, blocks, 1024, 0, 1, c.st, o)
-                                     : launch(loss_combine_kernel<8>, blocks, 256, 0, 1, c.st, o);
+        rc = T <= 2048 ? launch(loss_combine_kernel<8, 32>, (int)((T + 7) / 8), 1024, 0, 1, c.st, o)
+                       : launch(loss_combine_kernel<32, 16>, (int)((T + 31) / 32), 512, 0, 1, c.st, o);
         if (rc != GEMM_OK) return rc;
     }
     return GEMM_OK;
@@ -233,7 +241,7 @@ static int run_backward(const Call& c, const LossPlan& p, DeviceState& d) {
         LossMaps m;
         LossParams q;
         {  // G of the piece
-            const TilePlan t = plan_logits(c.T, vp, c.D, !c.nk, true, d.sm_count, d.max_pairs);
+            const TilePlan t = plan_logits(c.T, vp, c.D, !c.nk, false, d.sm_count, d.max_pairs);
             memset(&q, 0, sizeof(q));
             q.M = (int32_t)c.T;
             q.N = (int32_t)vp;
@@ -245,8 +253,9 @@ static int run_backward(const Call& c, const LossPlan& p, DeviceState& d) {
             q.dloss = c.dloss;
             q.dloss_stride = c.dloss_stride;
             q.grad_scale = c.ids ? c.tau : 1.0f;
-            rc = encode_x(m.a, c, p, 0, c.T, (uint32_t)t.a_rows, 0);
-            if (rc == GEMM_OK) rc = encode_words(&m.b[0], c, t.width / (t.pair ? 2 : 1), q);
+            q.a_3d = c.D % 64 == 0;
+            rc = encode_x(m.a, c, p, 0, c.T, (uint32_t)t.a_rows, q.a_3d ? (uint32_t)t.bk / 64 : 0);
+            if (rc == GEMM_OK) rc = encode_words(&m.b[0], c, t, q);
             if (rc == GEMM_OK)
                 rc = encode_rows(&m.d, G, (uint64_t)p.piece, (uint64_t)c.T, (uint64_t)p.piece, 32, 0, c.bf16);
             m.b[1] = m.b[0];
@@ -254,7 +263,7 @@ static int run_backward(const Call& c, const LossPlan& p, DeviceState& d) {
             if (rc != GEMM_OK) return rc;
         }
         if (c.dX) {  // sums += G W
-            const TilePlan t = plan_sum(c.T, c.D, vp, p.sum_splits, c.nk, d.sm_count, d.max_pairs);
+            const TilePlan t = plan_sum(c.T, c.D, p.sum_splits, p.sum_width, c.nk, d.sm_count, d.max_pairs);
             const uint32_t width = (uint32_t)(t.width / (t.pair ? 2 : 1));
             memset(&q, 0, sizeof(q));
             q.M = (int32_t)c.T;
@@ -266,11 +275,13 @@ static int run_backward(const Call& c, const LossPlan& p, DeviceState& d) {
             q.first = p0 == 0;
             q.w_k = (int32_t)p0;
             q.b_mn = c.nk ? 1 : 0;
-            q.b_3d = c.D % 64 == 0;
-            rc = encode_rows(&m.a[0], G, (uint64_t)((vp + 7) / 8 * 8), (uint64_t)c.T, (uint64_t)p.piece, (uint32_t)t.a_rows, 0, c.bf16);
+            q.b_3d = (c.nk ? c.D : c.V) % 64 == 0;
+            q.a_3d = 1;  // (G is zero from its last word to the end of that chunk)
+            rc = encode_rows(&m.a[0], G, (uint64_t)((vp + 63) / 64 * 64), (uint64_t)c.T, (uint64_t)p.piece, (uint32_t)t.a_rows,
+                             (uint32_t)t.bk / 64, c.bf16);
             if (rc == GEMM_OK)
-                rc = c.nk ? encode_rows(&m.b[0], c.W, (uint64_t)c.D, (uint64_t)c.V, (uint64_t)c.D, kBK, q.b_3d ? width / 64 : 0, c.bf16)
-                          : encode_rows(&m.b[0], c.W, (uint64_t)c.V, (uint64_t)c.D, (uint64_t)c.V, width, 0, c.bf16);
+                rc = c.nk ? encode_rows(&m.b[0], c.W, (uint64_t)c.D, (uint64_t)c.V, (uint64_t)c.D, (uint32_t)t.bk, q.b_3d ? width / 64 : 0, c.bf16)
+                          : encode_rows(&m.b[0], c.W, (uint64_t)c.V, (uint64_t)c.D, (uint64_t)c.V, width, q.b_3d ? (uint32_t)t.bk / 64 : 0, c.bf16);
             if (rc == GEMM_OK) rc = encode_sums(&m.d, sums, c.D, c.T, p.sum_splits);
             m.a[1] = m.a[0];
             m.b[1] = m.b[0];
@@ -295,9 +306,9 @@ static int run_backward(const Call& c, const LossPlan& p, DeviceState& d) {
             (c.nk ? q.d_row : q.d_col) = (int32_t)p0;
             CUtensorMap* const mg = c.nk ? m.a : m.b;
             CUtensorMap* const mx = c.nk ? m.b : m.a;
-            rc = encode_rows(&mg[0], G, (uint64_t)p.piece, (uint64_t)c.T, (uint64_t)p.piece, kBK, c.nk ? 2 : chunks, c.bf16);
+            rc = encode_rows(&mg[0], G, (uint64_t)p.piece, (uint64_t)c.T, (uint64_t)p.piece, (uint32_t)t.bk, c.nk ? 2 : chunks, c.bf16);
             mg[1] = mg[0];
-            if (rc == GEMM_OK) rc = encode_x(mx, c, p, 0, c.T, kBK, !x3d ? 0 : c.nk ? chunks : 2);
+            if (rc == GEMM_OK) rc = encode_x(mx, c, p, 0, c.T, (uint32_t)t.bk, !x3d ? 0 : c.nk ? chunks : 2);
             if (rc == GEMM_OK)
                 rc = c.nk ? encode_rows(&m.d, c.dW, (uint64_t)c.D, (uint64_t)c.V, (uint64_t)c.D, 32, 0, c.bf16)
                           : encode_rows(&m.d, c.dW, (uint64_t)c.V, (uint64_t)c.D, (uint64_t)c.V, 32, 0, c.bf16);
@@ -318,7 +329,9 @@ static int run_backward(const Call& c, const LossPlan& p, DeviceState& d) {
     f.dX = reinterpret_cast<uint16_t*>(c.dX);
     f.ld_dx = c.ld_dx;
     const int64_t vecs = c.T * (c.D / 8);
-    return launch(loss_finish_kernel, (int)std::min<int64_t>((vecs + 255) / 256, 8 * d.sm_count), 256, 0, 1, c.st, f);
+    if (f.splits >= 8)
+        return launch(loss_finish_kernel<8>, (int)std::min<int64_t>((vecs + 31) / 32, 8 * d.sm_count), 256, 0, 1, c.st, f);
+    return launch(loss_finish_kernel<1>, (int)std::min<int64_t>((vecs + 255) / 256, 8 * d.sm_count), 256, 0, 1, c.st, f);
 }
 
 // ------------------------------------------------------------------ checks

@@ -3,7 +3,7 @@
 // and the wanted words of a row (a target of weight 1, or a teacher's best
 // words with weights q):
 //
-//   kStats   per row and piece of a tile's columns: m = max z, s = sum 2^(c (z - m)),
+//   kStats   per row and tile: m = max z, s = sum 2^(c (z - m)),
 //            t = sum of q z over the wanted words among them        (no z is kept)
 //   kGrad    G[t, v] = a_t (2^(c z - log2(e) lse_t) - sum of q of the wanted word v)
 //            over a piece of the vocabulary, rounded to the 16-bit type
@@ -40,9 +40,9 @@ using rg::wait_phase;
 
 enum Mode : int { kStats = 0, kGrad = 1, kSum = 2, kWeight = 3 };
 
-constexpr int kBK = 64;  // k per ring stage
 constexpr int kThreads = 352;
-constexpr uint32_t kStaging = 4096;  // bytes per epilogue warp
+constexpr uint32_t kStaging = 4096;  // bytes per epilogue warp and buffer
+constexpr int32_t kRowPad = 128;     // rows in use, and G's, end in zeros up to a multiple of this
 constexpr int32_t kNone = 0x7fffffff;
 
 // What the device knows of the rows.
@@ -63,14 +63,16 @@ struct LossParams {
     int32_t rows_m;        // M is the rows' count
     int32_t rows_k;        // K is the rows' count
     int32_t width;         // columns of a tile
+    int32_t bk;            // k per ring stage: 64 or 128
     int32_t n_tiles;
     int32_t group_m;       // row tiles walked together
     int32_t splits;        // kSum: shares of the reduction, each summed apart
     int32_t a_mn, b_mn;    // operand is mn-major
-    int32_t a_3d, b_3d;    // ... and its chunks come in one copy
+    int32_t a_3d, b_3d;    // a stage's boxes or chunks come in one copy
     uint32_t a_bytes;      // of a stage (the box's)
     uint32_t stage_bytes;
     int32_t num_stages;
+    int32_t bufs;          // staging buffers of an epilogue warp: 1 or 2
     uint32_t tmem_cols;    // allocated; half per accumulator
     int32_t bf16;
     int32_t w_row, w_k;    // first word of the piece, added to B's row or to its k
@@ -84,7 +86,7 @@ struct LossParams {
     const float* weights;
     int32_t k, V;
     float log2_scale;        // c
-    float* stats;            // kStats: [tile][half][3][stats_pitch]
+    float* stats;            // kStats: [tile][3][stats_pitch]
     int64_t stats_pitch;
     const float* lse;        // kGrad
     const float* dloss;
@@ -159,15 +161,25 @@ struct Wanted {
     }
 };
 
-// kStats: the reduction in parts of at most this many k-blocks, each in an
-// accumulator of its own, added up in registers.  The tensor core truncates its
-// sums in 32 bits, 16 products at a time, always towards zero: over 4096 that was
-// 2.4e-6 of the losses (against 6e-7 of a sum that rounds), in parts of 1024 it
-// is PLACEHOLDER.  The epilogue's warps have the time.
-constexpr int32_t kPartBlocks = 16;
+// kStats: the reduction in parts of at most this many k, each in an accumulator
+// of its own, added up in registers.  The tensor core truncates its sums in 32
+// bits, 16 products at a time, always towards zero: over 4096 that was 2.4e-6 of
+// the losses (against 6e-7 of a sum that rounds), in parts of 1024 it is
+// PLACEHOLDER.  The epilogue's warps have the time.
+constexpr int32_t kPart = 1024;
 
-__device__ __forceinline__ int32_t part_count(int32_t blocks) { return (blocks + kPartBlocks - 1) / kPartBlocks; }
 __device__ __forceinline__ int32_t part_end(int32_t blocks, int32_t part, int32_t parts) { return part * blocks / parts; }
+
+// Two parts of a row's statistics as one.
+__device__ __forceinline__ void merge_stats(float& m, float& s, float m1, float s1, float c) {
+    const float top = fmaxf(m, m1);
+    const float ref = fabsf(top) == INFINITY ? 0.0f : top;
+    // (a sum taken at an infinite maximum is itself infinite or zero and needs no other reference)
+    const float f0 = fabsf(m) == INFINITY ? 1.0f : exp2_fast((m - ref) * c);
+    const float f1 = fabsf(m1) == INFINITY ? 1.0f : exp2_fast((m1 - ref) * c);
+    s = s * f0 + s1 * f1;
+    m = top;
+}
 
 template <bool kPair, int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -195,6 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&ctrl->tmem_empty[b]), (kPair ? 2u : 1u) * 8u);
         }
         mbar_init(smem_u32(&ctrl->final_bar), 1);
+        for (int b = 0; b < 8; ++b) mbar_init(smem_u32(&ctrl->extra[b]), 1);
         ctrl->abort_flag = 0;
         ctrl->ring_s = ctrl->ring_ph = ctrl->ring_lap = 0;
         fence_mbar_init();
@@ -219,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int32_t valid = q.rows ? __ldcg(&q.rows->valid) : 0;
     const int32_t gathered = q.rows ? __ldcg(&q.rows->compact) : 0;
     const int32_t M = q.rows_m && q.rows ? valid : q.M, K = q.rows_k ? valid : q.K;
-    const int32_t m_tiles = (M + kTileM - 1) / kTileM, blocks = (K + kBK - 1) / kBK;
+    const int32_t m_tiles = (M + kTileM - 1) / kTileM, blocks = (K + q.bk - 1) / q.bk;
     const uint32_t tiles = (uint32_t)m_tiles * (uint32_t)q.n_tiles;
     const uint32_t items = tiles * (uint32_t)q.splits;
 
@@ -262,7 +275,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             int32_t issued = 0;
             bool ok = true;
             const bool mn = is_a ? q.a_mn : q.b_mn, one = is_a ? q.a_3d : q.b_3d;
-            const int32_t chunks = is_a ? 2 : width / 64;
+            // copies of a stage where it takes several, and the bytes of one: 64 k of
+            // all rows, or 64 rows of all k
+            const int32_t copies = mn ? (is_a ? 2 : width / 64) : q.bk / 64;
+            const uint32_t piece = mn ? (uint32_t)q.bk * 128u : is_a ? q.a_bytes / (uint32_t)copies : (uint32_t)width * 128u;
             while (ok && next(k)) {
                 const int32_t r0 = is_a ? k.mt * kTileM + 128 * (int32_t)rank : k.nt * q.width + width * (int32_t)rank + q.w_row;
                 for (int32_t kb = k.kb0; kb < k.kb1; ++kb) {
@@ -277,16 +293,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const uint32_t bar = kPair ? mapa_shared(full, 0) : full;
                     const uint32_t dst = ring + s * stride + (is_a ? 0u : q.a_bytes);
-                    const int32_t k0 = kb * kBK + (is_a ? 0 : q.w_k);
+                    const int32_t k0 = kb * q.bk + (is_a ? 0 : q.w_k);
                     if (!kPair && is_a && issued == q.test_drop_kb && q.test_drop_kb > 0) {
                         // (test hook: not copied)
-                    } else if (!mn) {
-                        rg::load_2d<kPair>(dst, m, bar, k0, r0);
                     } else if (one) {
-                        rg::load_3d<kPair>(dst, m, bar, 0, k0, r0 / 64);
+                        rg::load_3d<kPair>(dst, m, bar, 0, mn ? k0 : r0, (mn ? r0 : k0) / 64);
                     } else {
-                        for (int32_t j = 0; j < chunks; ++j)
-                            rg::load_2d<kPair>(dst + (uint32_t)j * (kBK * 128u), m, bar, r0 + 64 * j, k0);
+                        for (int32_t j = 0; j < copies; ++j)
+                            rg::load_2d<kPair>(dst + (uint32_t)j * piece, m, bar, mn ? r0 + 64 * j : k0 + 64 * j, mn ? k0 : r0);
                     }
                     if (++s == S) {
                         s = 0;
@@ -305,15 +319,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0 && (!kPair || rank == 0)) {
             const uint32_t tfull0 = smem_u32(&ctrl->tmem_full[0]), tempty0 = smem_u32(&ctrl->tmem_empty[0]);
             const uint32_t idesc = make_idesc_f16_f32((uint32_t)kTileM, (uint32_t)q.width, q.a_mn != 0, q.b_mn != 0, q.bf16 != 0);
-            // k-major: 32 bytes per 16 k inside the swizzled rows; mn-major: 16 rows of k
-            const uint64_t a_desc0 = make_sw128_desc(ring, q.a_mn ? kBK * 128u : 16u, 1024);
-            const uint64_t b_desc0 = make_sw128_desc(ring + q.a_bytes, q.b_mn ? kBK * 128u : 16u, 1024);
+            // k-major: 32 bytes per 16 k inside the swizzled rows, the next 64 k behind
+            // all rows; mn-major: 16 rows of k, chunks of 64 rows apart by the k-block
+            const uint32_t b_rows = (uint32_t)q.width / kCG;
+            const uint64_t a_desc0 = make_sw128_desc(ring, q.a_mn ? (uint32_t)q.bk * 128u : 16u, 1024);
+            const uint64_t b_desc0 = make_sw128_desc(ring + q.a_bytes, q.b_mn ? (uint32_t)q.bk * 128u : 16u, 1024);
             const uint64_t a_step = q.a_mn ? 128u : 2u, b_step = q.b_mn ? 128u : 2u;
+            const uint64_t a_next = q.a_mn ? 512u : (q.a_bytes / 2) >> 4, b_next = q.b_mn ? 512u : (b_rows * 128u) >> 4;
+            const bool two = q.bk == 128;
+            const int32_t parts = kMode == kStats ? (q.K + kPart - 1) / kPart : 1;
             uint32_t s = 0, ph = 0, local = 0;
             bool ok = true;
             while (ok && next(k)) {
                 if (k.kb0 == k.kb1) continue;
-                const int32_t parts = kMode == kStats ? part_count(k.kb1) : 1;
                 int32_t kb = k.kb0;
                 for (int32_t part = 1; ok && part <= parts; ++part) {
                     const int32_t begin = kb, end = kMode == kStats ? part_end(k.kb1, part, parts) : k.kb1;
@@ -334,8 +352,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint64_t b_desc = b_desc0 + (uint64_t)(s * (stride >> 4));
                         const uint32_t acc = kb > begin ? 1u : 0u;
 #pragma unroll
-                        for (uint32_t i = 0; i < kBK / 16; ++i)
+                        for (uint32_t i = 0; i < 4; ++i)
                             mma_f16_ss<kCG>(d, a_desc + i * a_step, b_desc + i * b_step, idesc, i > 0 ? 1u : acc);
+                        if (two) {
+#pragma unroll
+                            for (uint32_t i = 0; i < 4; ++i)
+                                mma_f16_ss<kCG>(d, a_desc + a_next + i * a_step, b_desc + b_next + i * b_step, idesc, 1u);
+                        }
                         mma_commit<kCG>(empty0 + 8u * s, 0x3);
                         if (++s == S) {
                             s = 0;
@@ -358,11 +381,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else {
         const uint32_t quarter = warp & 3u, half = warp >= 7 ? 1u : 0u;
-        const uint32_t staging = ring + S * stride + (quarter + 4u * half) * kStaging;
-        const int32_t chunks = q.width / 64;
+        const uint32_t staging0 = ring + S * stride + (quarter + 4u * half) * (uint32_t)q.bufs * kStaging;
+        const int32_t chunks = (q.width + 63) / 64;
         // (G's rows are kWeight's reduction: zeros up to the end of its last k-block)
-        const int32_t row_end = kMode == kGrad ? (M + kBK - 1) / kBK * kBK : M;
-        uint32_t local = 0;
+        const int32_t row_end = kMode == kGrad ? (M + kRowPad - 1) / kRowPad * kRowPad : M;
+        uint32_t local = 0, tile = 0, staging = staging0;
+        // the staging buffer to write next, once the copy out of it has been read
+        auto turn = [&]() {
+            if (q.bufs == 2) {
+                staging = staging == staging0 ? staging0 + kStaging : staging0;
+                if (lane == 0) bulk_wait_group_read<1>();
+            } else if (lane == 0) {
+                bulk_wait_group_read<0>();
+            }
+            __syncwarp();
+        };
         while (next(k)) {
             const bool some = k.kb1 > k.kb0;
             const int32_t row0 = k.mt * kTileM + 128 * (int32_t)rank + 32 * (int32_t)quarter;
@@ -397,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float z[2][64];
 #pragma unroll
                 for (int j = 0; j < 64; ++j) z[0][j] = z[1][j] = 0.0f;
-                const int32_t parts = part_count(k.kb1);
+                const int32_t parts = (q.K + kPart - 1) / kPart;
                 bool ok = true;
 #pragma unroll 1
                 for (int32_t part = 0; part < parts; ++part) {
@@ -427,27 +460,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 Wanted want;
                 want.start(q, t, y, live, n0);
+                const int32_t n_end = min(q.N, n0 + q.width);
                 float m_run = -INFINITY, s_run = 0.0f, t_run = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int32_t ch = (int32_t)half + 2 * i, col = n0 + 64 * ch;
                     if (ch >= chunks || col >= q.N || row0 >= M) break;  // (uniform over the warp)
+                    const int32_t here = min(64, n_end - col);           // of the chunk's columns
                     float(&v)[64] = z[i];
                     while (want.next < col) want.advance();  // (of the other half's chunk)
-                    while (__any_sync(0xffffffffu, want.next - col < 64)) {
+                    while (__any_sync(0xffffffffu, want.next - col < here)) {
                         const int32_t at = want.next - col;
                         float x = 0.0f;
 #pragma unroll
                         for (int j = 0; j < 64; ++j) x = j == at ? v[j] : x;
-                        if (at < 64) {
+                        if (at < here) {
                             const float p = want.weight();
                             if (p != 0.0f) t_run = fmaf(p, x, t_run);
                             want.advance();
                         }
                     }
-                    if (col + 64 > q.N) {
+                    if (here < 64) {
 #pragma unroll
-                        for (int j = 0; j < 64; ++j) v[j] = col + j < q.N ? v[j] : -INFINITY;
+                        for (int j = 0; j < 64; ++j) v[j] = j < here ? v[j] : -INFINITY;
                     }
                     float top[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
@@ -461,13 +496,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                     s_run = fmaf(s_run, exp2_fast(fmaf(m_run, c, off)), (sum[0] + sum[1]) + (sum[2] + sum[3]));
                     m_run = m_new;
                 }
-                const int32_t halves = min(chunks, 2);
-                if (live && (int32_t)half < halves) {
-                    float* const o = q.stats + (int64_t)(k.nt * halves + (int32_t)half) * 3 * q.stats_pitch + r;
-                    o[0] = m_run;
-                    o[q.stats_pitch] = s_run;
-                    o[2 * q.stats_pitch] = t_run;
+                // the two halves' as one: the second hands its numbers to the first in one
+                // of two buffers (it is at most one tile ahead: the accumulators of the
+                // tile after that are not filled before the first has read this one's)
+                float* const hand = reinterpret_cast<float*>(smem + (ring - smem_u32(smem)) + S * stride) + (tile & 1u) * 384u + quarter * 96u + lane;
+                const uint32_t bar = smem_u32(&ctrl->extra[2u * quarter + (tile & 1u)]);
+                if (half == 1) {
+                    hand[0] = m_run;
+                    hand[32] = s_run;
+                    hand[64] = t_run;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar);
+                } else {
+                    if (!__all_sync(0xffffffffu, wait_phase(bar, (tile >> 1) & 1u, ctrl, w, rg::kErrEpi))) break;
+                    merge_stats(m_run, s_run, hand[0], hand[32], c);
+                    t_run += hand[64];
+                    if (live) {
+                        float* const o = q.stats + (int64_t)k.nt * 3 * q.stats_pitch + r;
+                        o[0] = m_run;
+                        o[q.stats_pitch] = s_run;
+                        o[2 * q.stats_pitch] = t_run;
+                    }
                 }
+                ++tile;
                 continue;
             }
             Wanted want;
@@ -512,9 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t x[32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) x[j] = pack16(u * v[2 * j], u * v[2 * j + 1], q.bf16);
-                    // the copy issued from this buffer before must have read it
-                    if (lane == 0) bulk_wait_group_read<0>();
-                    __syncwarp();
+                    turn();
 #pragma unroll
                     for (uint32_t i = 0; i < 8; ++i)
                         rg::st_shared_v4(staging + lane * 128u + ((i ^ (lane & 7u)) << 4),
@@ -531,8 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         if (col + 32 * h >= q.N) break;
-                        if (lane == 0) bulk_wait_group_read<0>();
-                        __syncwarp();
+                        turn();
 #pragma unroll
                         for (uint32_t i = 0; i < 8; ++i)
                             rg::st_shared_v4(staging + lane * 128u + ((i ^ (lane & 7u)) << 4),

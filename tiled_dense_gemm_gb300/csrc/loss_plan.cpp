@@ -7,7 +7,6 @@ namespace gr {
 namespace ls {
 
 namespace {
-constexpr int64_t kBlockK = 64;
 constexpr int64_t kSmem = 227 * 1024;
 constexpr int64_t kCtrl = 2048;  // control block and alignment
 constexpr int64_t kStagingBytes = 8 * 4096;
@@ -23,21 +22,33 @@ int pairs_of(int num_sms, int max_pairs) {
     return max_pairs < 0 ? 0 : std::min(max_pairs ? max_pairs : num_sms / 2, num_sms / 2);
 }
 
-void finish_plan(TilePlan& p, int64_t M, int64_t N, bool a_mn, bool staged, int num_sms, int max_pairs) {
+// Clocks that a tile of `w` columns takes per 64 k.  A pair: the tensor core's,
+// but no less than its commands take (about 300 in stages of 128 k).  A single
+// CTA streams B from memory at its share of it, 24 bytes a clock, and takes in
+// `rows` rows of A besides, at most 41 bytes a clock in all.
+double block_clocks(int64_t w, int64_t rows, bool pair) {
+    if (pair) return std::max(2.0 * (double)w, 300.0);
+    return std::max(128.0 * (double)w / 24, 128.0 * (double)(w + rows) / 41);
+}
+
+// bufs 0: statistics (the epilogue's halves hand over a few numbers)
+void finish_plan(TilePlan& p, int64_t M, int64_t N, bool a_mn, bool b_mn, int bufs, int num_sms, int max_pairs) {
     const int64_t tile_m = p.pair ? 256 : 128, per_cta = p.width / (p.pair ? 2 : 1);
     p.m_tiles = (int32_t)ceil_div(M, tile_m);
     p.n_tiles = (int32_t)ceil_div(N, p.width);
     // (rows of A that the batch does not have are not copied: what the MMA then
     // reads there ends in lanes that nothing looks at)
     p.a_rows = (int32_t)(a_mn ? 128 : std::min<int64_t>(128, round_up(M, 8)));
-    p.a_bytes = p.a_rows * 128;
-    p.stage_bytes = (int32_t)(p.a_bytes + per_cta * 128);
-    const int64_t staging = staged ? kStagingBytes : 0;
-    // (the MMA reads 128 rows of A from the last stage's start)
-    const int64_t tail = std::max<int64_t>(0, 128 * 128 - p.stage_bytes - staging);
+    const int64_t blocks = p.bk / 64;
+    p.a_bytes = (int32_t)(a_mn ? 2 * 128 * p.bk : p.a_rows * 128 * blocks);
+    p.stage_bytes = (int32_t)(p.a_bytes + (b_mn ? per_cta / 64 * 128 * p.bk : per_cta * 128 * blocks));
+    p.bufs = bufs;
+    const int64_t staging = bufs ? bufs * kStagingBytes : 4096;
+    // (the MMA reads 128 rows of A's last 64 k, from the last stage's start on)
+    const int64_t tail = std::max<int64_t>(0, p.a_bytes / blocks * (blocks - 1) + 128 * 128 - p.stage_bytes - staging);
     p.num_stages = (int32_t)std::min<int64_t>(kMaxRing, (kSmem - kCtrl - staging - tail) / p.stage_bytes);
     p.smem_bytes = (int32_t)(kCtrl + (int64_t)p.num_stages * p.stage_bytes + staging + tail);
-    int32_t cols = 32;
+    int32_t cols = 64;
     while (cols < p.width) cols *= 2;
     p.tmem_cols = 2 * cols;
     const int64_t items = (int64_t)p.m_tiles * p.n_tiles * p.splits;
@@ -45,52 +56,52 @@ void finish_plan(TilePlan& p, int64_t M, int64_t N, bool a_mn, bool staged, int 
                     : (int32_t)std::min<int64_t>(num_sms, items);
     p.group_m = (int32_t)std::min<int64_t>(p.m_tiles, 8);
 }
-
-// The width whose waves take the shortest time.
-int32_t best_width(int64_t m_tiles, int64_t N, bool pair, bool b_mn, int64_t workers) {
-    int32_t best = 256;
-    double least = 0;
-    for (int32_t w : {256, 192, 128, 64}) {
-        if (pair && (w == 64 || (w == 192 && b_mn))) continue;  // (whole chunks per CTA)
-        const double cost = (double)ceil_div(m_tiles * ceil_div(N, w), workers) * (w + 24);
-        if (w == 256 || cost < least * 0.98) {
-            best = w;
-            least = cost;
-        }
-    }
-    return best;
-}
 }  // namespace
 
-TilePlan plan_logits(int64_t T, int64_t N, int64_t K, bool b_mn, bool staged, int num_sms, int max_pairs) {
-    (void)K;
+TilePlan plan_logits(int64_t T, int64_t N, int64_t K, bool b_mn, bool stats, int num_sms, int max_pairs) {
     TilePlan p = {};
     const int pairs = pairs_of(num_sms, max_pairs);
     p.pair = T > 128 && pairs > 0;
     p.splits = 1;
-    p.width = best_width(ceil_div(T, p.pair ? 256 : 128), N, p.pair != 0, b_mn, p.pair ? pairs : num_sms);
-    finish_plan(p, T, N, false, staged, num_sms, max_pairs);
+    // The width whose waves take the shortest time, the widest of equals.  Whole
+    // chunks of 64 columns where they are copied as such, in or out; a pair's CTAs
+    // take half each.
+    const int64_t m_tiles = ceil_div(T, p.pair ? 256 : 128), workers = p.pair ? pairs : num_sms;
+    const int32_t step = (b_mn || !stats ? 64 : 16) * (p.pair && (b_mn || stats) ? 2 : 1);
+    const int64_t rows = std::min<int64_t>(128, T);
+    double least = 0;
+    for (int32_t w = 256; w >= 64; w -= step) {
+        const double tile = block_clocks(w, rows, p.pair != 0) * (double)ceil_div(K, 64) + 400;
+        const double cost = (double)ceil_div(m_tiles * ceil_div(N, w), workers) * tile;
+        if (w == 256 || cost < least * 0.98) {
+            p.width = w;
+            least = cost;
+        }
+    }
+    p.bk = p.pair ? (p.width > 192 ? 64 : 128) : (rows <= 64 ? 128 : 64);
+    finish_plan(p, T, N, false, b_mn, stats ? 0 : 1, num_sms, max_pairs);
     return p;
 }
 
-TilePlan plan_sum(int64_t T, int64_t N, int64_t K, int splits, bool b_mn, int num_sms, int max_pairs) {
-    (void)K;
-    (void)b_mn;
+TilePlan plan_sum(int64_t T, int64_t N, int splits, int width, bool b_mn, int num_sms, int max_pairs) {
     TilePlan p = {};
     p.pair = T > 128 && pairs_of(num_sms, max_pairs) > 0;
     p.splits = splits;
-    p.width = N > 128 ? 256 : 128;
-    finish_plan(p, T, N, false, true, num_sms, max_pairs);
+    p.width = width;
+    p.bk = p.pair && width > 192 ? 64 : 128;
+    finish_plan(p, T, N, false, b_mn, 1, num_sms, max_pairs);
     return p;
 }
 
-TilePlan plan_weight(int64_t M, int64_t N, int64_t K, int num_sms, int max_pairs) {
-    (void)K;
+TilePlan plan_weight(int64_t M, int64_t N, int64_t T, int num_sms, int max_pairs) {
     TilePlan p = {};
     p.pair = pairs_of(num_sms, max_pairs) > 0;
     p.splits = 1;
     p.width = N > 128 ? 256 : 128;
-    finish_plan(p, M, N, true, true, num_sms, max_pairs);
+    p.bk = 64;
+    // Two staging buffers per warp where a tile's reduction is so short that its
+    // stores are what takes time (PLACEHOLDER).
+    finish_plan(p, M, N, true, true, T <= 1024 ? 2 : 1, num_sms, max_pairs);
     return p;
 }
 
@@ -114,37 +125,42 @@ LossPlan plan_loss(int64_t T, int64_t V, int64_t D, int64_t k, bool gradient) {
         p.sorted = take(4 * rows * k);
         p.weights = take(4 * rows * k);
     }
-    if (p.gather) p.gathered = take(2 * rows * D);
+    p.pitch = round_up(D, 64);
+    if (p.gather) p.gathered = take(2 * rows * p.pitch);
     if (!gradient) {
-        // (one or two parts per tile, whatever its width)
-        p.parts = (int32_t)(2 * ceil_div(V, 128));
+        // (of the narrowest tiles)
+        p.parts = (int32_t)ceil_div(V, 64);
         if (ceil_div(V, 64) * ceil_div(rows, 128) > 2000000000ll) p.status = GEMM_ERR_TOO_LARGE;
         p.stats = take(4 * 3 * round_up(rows, 32) * p.parts);
     } else {
-        int64_t piece = round_up(V, 256);
         const int64_t most = std::max<int64_t>(256, kGradBytes / (2 * rows) / 256 * 256);
-        p.pieces = (int32_t)ceil_div(piece, most);
-        p.piece = round_up(ceil_div(piece, p.pieces), 256);
+        p.piece = round_up(ceil_div(V, ceil_div(V, most)), 256);
         p.pieces = (int32_t)ceil_div(V, p.piece);
-        // Shares of dX's reduction: as many as fill the last wave best, of at least 16 k-blocks.
+        // Tiles and shares of dX's reduction by the time of their waves, their start
+        // and end (3000 clocks) and the shares' way to memory and back.
         const bool pair = rows > 128;
-        const int64_t workers = pair ? kPlanSms / 2 : kPlanSms;
-        const int64_t tiles = ceil_div(rows, pair ? 256 : 128) * ceil_div(D, D > 128 ? 256 : 128);
-        const int64_t blocks = ceil_div(std::min(p.piece, V), kBlockK);
+        const int64_t workers = pair ? kPlanSms / 2 : kPlanSms, m_tiles = ceil_div(rows, pair ? 256 : 128);
+        const int64_t blocks = ceil_div(std::min(p.piece, V), 64);
         double least = 0;
-        for (int32_t s = 1; s <= 16; ++s) {
-            if (s > 1 && blocks / s < 16) break;
-            // waves of k-blocks, plus the tile's start and end, plus the shares' way to memory and back
-            const double cost = (double)ceil_div(tiles * s, workers) * ((double)blocks / s + 6) + 0.5 * s;
-            if (s == 1 || cost < least * 0.97) {
-                least = cost;
-                p.sum_splits = s;
+        for (int32_t w : {256, 128}) {
+            if (w == 256 && D <= 128) continue;
+            const double clocks = block_clocks(w, std::min<int64_t>(128, rows), pair);
+            const int64_t tiles = m_tiles * ceil_div(D, w);
+            for (int32_t s = 1; s <= 64; ++s) {
+                if (s > 1 && blocks / s < 8) break;
+                const double cost = (double)ceil_div(tiles * s, workers) * (clocks * (double)ceil_div(blocks, s) + 3000) +
+                                    8.0 * (double)s * (double)rows * (double)D / 2600;
+                if (p.sum_splits == 0 || cost < least * 0.98) {
+                    least = cost;
+                    p.sum_splits = s;
+                    p.sum_width = w;
+                }
             }
         }
         p.grad = take(2 * rows * p.piece);
         p.sums = take(4 * rows * D * p.sum_splits);
-        if (ceil_div(rows, 128) * ceil_div(p.piece, 64) > 2000000000ll || ceil_div(p.piece, 128) * ceil_div(D, 64) > 2000000000ll ||
-            tiles * p.sum_splits > 2000000000ll)
+        if (m_tiles * ceil_div(p.piece, 64) > 2000000000ll || ceil_div(p.piece, 128) * ceil_div(D, 64) > 2000000000ll ||
+            m_tiles * ceil_div(D, 64) * p.sum_splits > 2000000000ll)
             p.status = GEMM_ERR_TOO_LARGE;
     }
     p.bytes = at;

@@ -14,6 +14,8 @@ namespace ls {
 struct TilePlan {
     int32_t pair;     // CTA pairs
     int32_t width;    // columns of a tile
+    int32_t bk;       // k per stage
+    int32_t bufs;     // staging buffers of an epilogue warp
     int32_t m_tiles, n_tiles, splits, group_m;
     int32_t a_rows;   // rows of A's box (k-major)
     int32_t a_bytes, stage_bytes, num_stages, smem_bytes, tmem_cols, grid;
@@ -26,16 +28,20 @@ struct LossPlan {
     int32_t pieces;
     int32_t gather;      // the rows' kernel runs
     int32_t parts;       // forward: statistics per row
-    int32_t sum_splits;  // backward: shares of dX's reduction
+    int32_t sum_splits;  // backward: shares of dX's reduction,
+    int32_t sum_width;   // ... and its tiles' columns
+    int64_t pitch;       // of the gathered rows
     // workspace, in bytes from its start
     int64_t header, index, flags, entropy, sorted, weights, gathered, stats, grad, sums, bytes;
 };
 
-// T x N products of the forward pass and of G; K the reduction.  b_mn: B's
-// chunks are of 64 columns.
-TilePlan plan_logits(int64_t T, int64_t N, int64_t K, bool b_mn, bool staged, int num_sms, int max_pairs);
-TilePlan plan_sum(int64_t T, int64_t N, int64_t K, int splits, bool b_mn, int num_sms, int max_pairs);
-TilePlan plan_weight(int64_t M, int64_t N, int64_t K, int num_sms, int max_pairs);
+// The logits (T x N, reduction K): `stats` of the forward pass, else G.  b_mn: B
+// comes in chunks of 64 columns.
+TilePlan plan_logits(int64_t T, int64_t N, int64_t K, bool b_mn, bool stats, int num_sms, int max_pairs);
+// Sums of dX (T x N) in `splits` shares, tiles of `width`.
+TilePlan plan_sum(int64_t T, int64_t N, int splits, int width, bool b_mn, int num_sms, int max_pairs);
+// dW (M x N, reduction T).
+TilePlan plan_weight(int64_t M, int64_t N, int64_t T, int num_sms, int max_pairs);
 
 // k: words of a teacher per row, 0: targets.
 LossPlan plan_loss(int64_t T, int64_t V, int64_t D, int64_t k, bool gradient);

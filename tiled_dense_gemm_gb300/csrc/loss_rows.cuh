@@ -65,11 +65,12 @@ __global__ void __launch_bounds__(32 * kTeacherWarps) loss_teacher_kernel(const 
             float l = -INFINITY;
             if (j < p.k) {
                 id = __ldg(p.ids + t * p.ld_ids + j);
+                l = load_logit(p, t * p.ld_logits + j);
                 if (id >= p.V) {
                     atomicCAS(p.err + 1, 0, (int32_t)rg::kBadIds);
                     id = -1;
                 }
-                if (id >= 0) l = load_logit(p, t * p.ld_logits + j);
+                if (id < 0) l = -INFINITY;
             }
             key[j] = id < 0 ? kNone : id;
             e[j] = l;
@@ -120,13 +121,15 @@ struct RowsParams {
     int32_t T, D;
     const uint16_t* X;
     int64_t ldx;
-    uint16_t* gathered;     // (T, D)
+    uint16_t* gathered;     // (T, pitch)
     int32_t* index;         // the rows in use, then the others
     RowsHeader* rows;
     const float* dloss;     // null: no scale wanted
     int64_t dloss_stride;
     float grad_scale;
     float top;              // what the largest |dloss grad_scale| is scaled to
+    int32_t pitch;          // of the copy: D rounded up to 64
+    int32_t always;         // gather even if all rows are in use (X's pitch is not one of 128 bytes)
     int32_t* err;
 };
 
@@ -147,12 +150,20 @@ __global__ void __launch_bounds__(kRowsThreads) loss_rows_kernel(const __grid_co
     const int32_t r0 = min(p.T, (int32_t)blockIdx.x * each), r1 = min(p.T, r0 + each);
     int32_t before = 0, total = 0;
     bool bad = false;
-    for (int32_t t = i; t < p.T; t += kRowsThreads) {
-        const int32_t y = __ldcg(p.flags + t);
-        const bool in = y >= 0 && y < p.limit;
-        bad |= y >= p.limit;
-        total += in;
-        before += in && t < r0;
+    for (int32_t t0 = i; t0 < p.T; t0 += 8 * kRowsThreads) {
+        int32_t y[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int32_t t = t0 + u * kRowsThreads;
+            y[u] = t < p.T ? __ldcg(p.flags + t) : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const bool in = y[u] >= 0 && y[u] < p.limit;
+            bad |= y[u] >= p.limit;
+            total += in;
+            before += in && t0 + u * kRowsThreads < r0;
+        }
     }
     if (bad && blockIdx.x == 0) atomicCAS(p.err + 1, 0, (int32_t)rg::kBadIds);
     before = __reduce_add_sync(0xffffffffu, before);
@@ -168,7 +179,7 @@ __global__ void __launch_bounds__(kRowsThreads) loss_rows_kernel(const __grid_co
         total += part[1][j];
     }
     __syncthreads();
-    const bool gather = total < p.T;
+    const bool gather = total < p.T || p.always;
     for (int32_t b = r0; b < r1; b += kRowsThreads) {
         const int32_t t = b + i;
         bool in = false;
@@ -191,8 +202,16 @@ __global__ void __launch_bounds__(kRowsThreads) loss_rows_kernel(const __grid_co
                 const int32_t to = where[j];
                 if (to < 0) continue;
                 const uint4* const src = reinterpret_cast<const uint4*>(p.X + (int64_t)(b + j) * p.ldx);
-                uint4* const dst = reinterpret_cast<uint4*>(p.gathered + (int64_t)to * p.D);
-                for (int32_t c = lane; c < vecs; c += 32) dst[c] = __ldg(src + c);
+                uint4* const dst = reinterpret_cast<uint4*>(p.gathered + (int64_t)to * p.pitch);
+                for (int32_t c0 = lane; c0 < vecs; c0 += 8 * 32) {
+                    uint4 x[8];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        if (c0 + 32 * u < vecs) x[u] = __ldcs(src + c0 + 32 * u);
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        if (c0 + 32 * u < vecs) dst[c0 + 32 * u] = x[u];
+                }
             }
         }
         __syncthreads();
@@ -201,9 +220,9 @@ __global__ void __launch_bounds__(kRowsThreads) loss_rows_kernel(const __grid_co
     // the last block: zeros up to the end of the reduction's last k-block, and
     // what the later kernels read of the rows
     if (gather) {
-        const int32_t end = min(p.T, (total + kBK - 1) / kBK * kBK);
-        const int64_t n = (int64_t)(end - total) * (p.D / 8);
-        uint4* const dst = reinterpret_cast<uint4*>(p.gathered + (int64_t)total * p.D);
+        const int32_t end = min(p.T, (total + kRowPad - 1) / kRowPad * kRowPad);
+        const int64_t n = (int64_t)(end - total) * (p.pitch / 8);
+        uint4* const dst = reinterpret_cast<uint4*>(p.gathered + (int64_t)total * p.pitch);
         for (int64_t c = i; c < n; c += kRowsThreads) dst[c] = make_uint4(0, 0, 0, 0);
     }
     float scale = 1.0f;
@@ -212,9 +231,11 @@ __global__ void __launch_bounds__(kRowsThreads) loss_rows_kernel(const __grid_co
         if (p.dloss_stride == 0) {
             top = fabsf(__ldg(p.dloss));
         } else {
+#pragma unroll 8
             for (int32_t t = i; t < p.T; t += kRowsThreads) {
                 const int32_t y = __ldcg(p.flags + t);
-                if (y >= 0 && y < p.limit) top = fmaxf(top, fabsf(__ldg(p.dloss + t)));
+                const float d = __ldg(p.dloss + t);
+                if (y >= 0 && y < p.limit) top = fmaxf(top, fabsf(d));
             }
         }
         top = warp_max(top);
@@ -250,39 +271,58 @@ struct CombineParams {
     int32_t* err;
 };
 
-// A block for 32 rows, a lane for each; its warps take the parts in turn and
-// are merged in their order.
-template <int kWarps>
+// A block for kRows rows.  Its threads take a row's parts in turn and are
+// merged in a fixed order.  Eight rows where there are few, so that a row's parts
+// are in flight at once (64 rows, 512 parts: PLACEHOLDER us).
+template <int kRows, int kWarps>
 __global__ void __launch_bounds__(32 * kWarps) loss_combine_kernel(const __grid_constant__ CombineParams p) {
-    __shared__ float part[3][kWarps][32];
+    constexpr int kLanes = 32 / kRows;  // of a warp, per row
+    __shared__ float part[3][kWarps][kRows];
     const int32_t warp = (int32_t)threadIdx.x / 32, lane = (int32_t)threadIdx.x % 32;
+    const int32_t row = lane % kRows;
     grid_launch_dependents();
     grid_dependency_wait();
-    const int32_t r = (int32_t)blockIdx.x * 32 + lane;
+    const int32_t r = (int32_t)blockIdx.x * kRows + row;
     const int32_t valid = p.rows ? __ldcg(&p.rows->valid) : p.T;
     const float c = p.log2_scale;
     float m = -INFINITY, s = 0.0f, z = 0.0f;
-    auto merge = [&](float m1, float s1, float z1) {
-        const float top = fmaxf(m, m1);
-        const float ref = fabsf(top) == INFINITY ? 0.0f : top;
-        // (a sum taken at an infinite maximum is itself infinite or zero and needs no other reference)
-        const float f0 = fabsf(m) == INFINITY ? 1.0f : exp2_fast((m - ref) * c);
-        const float f1 = fabsf(m1) == INFINITY ? 1.0f : exp2_fast((m1 - ref) * c);
-        s = s * f0 + s1 * f1;
-        z += z1;
-        m = top;
-    };
     if (r < valid) {
-        const float* at = p.stats + r + (int64_t)warp * 3 * p.pitch;
+        const float* const at = p.stats + r;
 #pragma unroll 4
-        for (int32_t j = warp; j < p.parts; j += kWarps, at += 3 * kWarps * p.pitch)
-            merge(__ldcg(at), __ldcg(at + p.pitch), __ldcg(at + 2 * p.pitch));
+        for (int32_t j = kLanes * warp + lane / kRows; j < p.parts; j += kLanes * kWarps) {
+            const float* const x = at + (int64_t)j * 3 * p.pitch;
+            merge_stats(m, s, __ldcg(x), __ldcg(x + p.pitch), c);
+            z += __ldcg(x + 2 * p.pitch);
+        }
     }
-    part[0][warp][lane] = m;
-    part[1][warp][lane] = s;
-    part[2][warp][lane] = z;
+    auto across = [&]() {  // the lanes of a row
+#pragma unroll
+        for (int d = kRows; d < 32; d <<= 1) {
+            const float m1 = __shfl_xor_sync(0xffffffffu, m, d), s1 = __shfl_xor_sync(0xffffffffu, s, d);
+            // (both lanes merge in the same order: the lower lane's first)
+            float a = lane & d ? m1 : m, b = lane & d ? s1 : s;
+            merge_stats(a, b, lane & d ? m : m1, lane & d ? s : s1, c);
+            m = a;
+            s = b;
+            z += __shfl_xor_sync(0xffffffffu, z, d);
+        }
+    };
+    across();
+    if (lane < kRows) {
+        part[0][warp][row] = m;
+        part[1][warp][row] = s;
+        part[2][warp][row] = z;
+    }
     __syncthreads();
-    if (warp != 0 || r >= p.T) return;
+    if (warp != 0) return;
+    m = -INFINITY;
+    s = z = 0.0f;
+    for (int32_t j = lane / kRows; j < kWarps; j += kLanes) {
+        merge_stats(m, s, part[0][j][row], part[1][j][row], c);
+        z += part[2][j][row];
+    }
+    across();
+    if (r >= p.T || lane >= kRows) return;
     const int32_t t = p.rows ? __ldcg(p.index + r) : r;
     bool in = r < valid;
     if (!p.rows) {
@@ -292,9 +332,6 @@ __global__ void __launch_bounds__(32 * kWarps) loss_combine_kernel(const __grid_
     }
     float loss = 0.0f, lse = 0.0f;
     if (in) {
-        m = -INFINITY;
-        s = z = 0.0f;
-        for (int32_t j = 0; j < kWarps; ++j) merge(part[0][j][lane], part[1][j][lane], part[2][j][lane]);
         lse = (fabsf(m) == INFINITY ? 0.0f : m / p.tau) + logf(s);
         loss = p.entropy ? p.tau * p.tau * (__ldcg(p.entropy + t) - z / p.tau + lse) : lse - z;
     }
@@ -313,30 +350,45 @@ struct FinishParams {
     int64_t ld_dx;
 };
 
-// dX[row] from its shares, in their order, rounded once; +0 in the rows that are not in use.
+// dX[row] from its shares, rounded once; +0 in the rows that are not in use.
+// kLanes threads per eight columns take the shares in turn and are added up in a
+// fixed order (many shares of few rows: PLACEHOLDER us with one thread, with eight).
+template <int kLanes>
 __global__ void __launch_bounds__(256) loss_finish_kernel(const __grid_constant__ FinishParams p) {
     grid_launch_dependents();
     grid_dependency_wait();
     const int32_t valid = __ldcg(&p.rows->valid);
     const float u = __ldcg(&p.rows->unscale);
-    const int32_t vecs = p.D / 8;
+    const int32_t vecs = p.D / 8, lane = (int32_t)threadIdx.x % kLanes;
     const int64_t total = (int64_t)p.T * vecs, share = (int64_t)p.T * p.D;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int32_t r = (int32_t)(i / vecs), c = (int32_t)(i - (int64_t)r * vecs);
-        uint4 o = make_uint4(0, 0, 0, 0);
-        if (r < valid) {
-            float4 a = make_float4(0, 0, 0, 0), b = a;
-            const float4* src = reinterpret_cast<const float4*>(p.sums + (int64_t)r * p.D) + 2 * c;
-            for (int32_t k = 0; k < p.splits; ++k, src += share / 4) {
-                const float4 x = __ldcs(src), y = __ldcs(src + 1);
+    const int64_t step = (int64_t)gridDim.x * (256 / kLanes), rounds = (total + step - 1) / step;
+    int64_t i = (int64_t)blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;
+    for (int64_t n = 0; n < rounds; ++n, i += step) {
+        const int32_t r = i < total ? (int32_t)(i / vecs) : 0, c = (int32_t)(i - (int64_t)r * vecs);
+        float4 a = make_float4(0, 0, 0, 0), b = a;
+        if (i < total && r < valid) {
+            const float4* const src = reinterpret_cast<const float4*>(p.sums + (int64_t)r * p.D) + 2 * c;
+#pragma unroll 4
+            for (int32_t k = lane; k < p.splits; k += kLanes) {
+                const float4 x = __ldcs(src + k * (share / 4)), y = __ldcs(src + k * (share / 4) + 1);
                 a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
                 b.x += y.x, b.y += y.y, b.z += y.z, b.w += y.w;
             }
-            o = make_uint4(pack16(a.x * u, a.y * u, p.bf16), pack16(a.z * u, a.w * u, p.bf16),
-                           pack16(b.x * u, b.y * u, p.bf16), pack16(b.z * u, b.w * u, p.bf16));
         }
-        const int32_t t = __ldcg(p.index + r);
-        reinterpret_cast<uint4*>(p.dX + (int64_t)t * p.ld_dx)[c] = o;
+#pragma unroll
+        for (int d = 1; d < kLanes; d <<= 1) {
+            a.x += __shfl_xor_sync(0xffffffffu, a.x, d), a.y += __shfl_xor_sync(0xffffffffu, a.y, d);
+            a.z += __shfl_xor_sync(0xffffffffu, a.z, d), a.w += __shfl_xor_sync(0xffffffffu, a.w, d);
+            b.x += __shfl_xor_sync(0xffffffffu, b.x, d), b.y += __shfl_xor_sync(0xffffffffu, b.y, d);
+            b.z += __shfl_xor_sync(0xffffffffu, b.z, d), b.w += __shfl_xor_sync(0xffffffffu, b.w, d);
+        }
+        if (i < total && lane == 0) {
+            uint4 o = make_uint4(0, 0, 0, 0);
+            if (r < valid)
+                o = make_uint4(pack16(a.x * u, a.y * u, p.bf16), pack16(a.z * u, a.w * u, p.bf16),
+                               pack16(b.x * u, b.y * u, p.bf16), pack16(b.z * u, b.w * u, p.bf16));
+            reinterpret_cast<uint4*>(p.dX + (int64_t)__ldcg(p.index + r) * p.ld_dx)[c] = o;
+        }
     }
 }
 
