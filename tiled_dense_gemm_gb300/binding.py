@@ -7,7 +7,6 @@ library is missing or the device is not a GB300 (sm_103a), calls raise.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import re
@@ -66,6 +65,8 @@ def lib():
     """Load libgemmrelu.so (built by ``__graft_entry__.build()`` or
     ``python -m tiled_dense_gemm_gb300.build``).  Raises if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -587,56 +588,52 @@ def _teacher(ids, logits, T, device):
     return k, _rows("ids", ids, T, k, device), _rows("logits", logits, T, k, device), code
 
 
+_loss_space = {}  # {(T, V, D, k, gradient): workspace bytes}
+
+
+def _workspace(what, x, *sizes):
+    need = _loss_space.get(sizes)
+    if need is None:
+        need = lib().gemm_relu_loss_workspace(*sizes)
+        if need < 0:
+            raise GemmReluError(-need, what)
+        if len(_loss_space) >= 4096:
+            _loss_space.clear()
+        _loss_space[sizes] = need
+    return _torch.empty(need, dtype=_torch.uint8, device=x.device)
+
+
 def _on_stream(stream, device):
-    """The context in which a call's tensors are allocated, and the stream's handle."""
-    if stream is None:
-        return contextlib.nullcontext(), None
+    """The context of a call's stream: what the call allocates belongs to it."""
     if not hasattr(stream, "cuda_stream"):
         stream = _torch.cuda.ExternalStream(stream, device=device)
-    return _torch.cuda.stream(stream), stream.cuda_stream
+    return _torch.cuda.stream(stream)
 
 
-def _loss_call(fn, x, device, stream, T, V, D, k, gradient, allocate, args):
-    """fn(*args(outputs), workspace, bytes, stream), the outputs from allocate()."""
-    context, handle = _on_stream(stream, device)
-    need = lib().gemm_relu_loss_workspace(T, V, D, k, gradient)
-    if need < 0:
-        raise GemmReluError(-need, fn.__name__)
-    with context:
-        out = allocate()
-        space = _torch.empty((need,), dtype=_torch.uint8, device=x.device)
-        _enqueue(fn, device, handle, *args(out), space.data_ptr(), need)
-    return out
-
-
-def _losses(loss, lse, x, T, device):
-    if loss is not None:
-        _floats("loss", loss, T, device)
-    if lse is not None:
-        _floats("lse", lse, T, device)
-    new = lambda t: _torch.empty((T,), dtype=_torch.float32, device=x.device) if t is None else t  # noqa: E731
-    return lambda: (new(loss), new(lse))
+def _row_floats(name, t, T, x, device):
+    """A loss's output: the caller's, or a new one."""
+    if t is None:
+        return _torch.empty(T, dtype=_torch.float32, device=x.device)
+    _floats(name, t, T, device)
+    return t
 
 
 def _gradients(dx, dw, x, w, T, D, device, want_dx, want_dw):
-    """What allocates (dx, dw, pitch of dx); None for one that is not wanted."""
+    """(dx, its pitch, dw), the caller's or new ones; None for one that is not wanted."""
     ld = D
-    if want_dx and dx is not None:
+    if not want_dx:
+        dx = None
+    else:
         dx, ld = _output("dx", dx, x, T, D, device)
-    if want_dw and dw is not None:
+    if not want_dw:
+        dw = None
+    elif dw is None:
+        dw = _torch.empty_like(w)
+    else:
         if getattr(dw, "dtype", None) is not x.dtype:
             raise TypeError("dw must be a tensor of the operands' type")
         _stack("dw", dw, w.shape, device)
-
-    def allocate():
-        a = dx if want_dx else None
-        if want_dx and a is None:
-            a = _torch.empty((T, D), dtype=x.dtype, device=x.device)
-        b = dw if want_dw else None
-        if want_dw and b is None:
-            b = _torch.empty(w.shape, dtype=x.dtype, device=x.device)
-        return a, b
-    return allocate, ld
+    return dx, ld, dw
 
 
 def _pointer(t):
@@ -653,10 +650,15 @@ def gemm_relu_xent(x, w, targets, loss=None, lse=None, b_layout: str = "kn", str
     ``loss`` and ``lse`` are float32 (T,), written in place when given."""
     dtype, layout = _dtype_code(x, w), _layout_code(b_layout)
     T, V, D, ldx, device = _head_sizes(x, w, layout)
+    if stream is not None:
+        with _on_stream(stream, device):
+            return gemm_relu_xent(x, w, targets, loss, lse, b_layout)
     _index("targets", targets, T, device)
-    return _loss_call(lib().gemm_relu_xent, x, device, stream, T, V, D, 0, 0, _losses(loss, lse, x, T, device),
-                      lambda o: (x.data_ptr(), w.data_ptr(), targets.data_ptr(), o[0].data_ptr(), o[1].data_ptr(), T, V,
-                                 D, ldx, layout, dtype))
+    loss, lse = _row_floats("loss", loss, T, x, device), _row_floats("lse", lse, T, x, device)
+    space = _workspace("gemm_relu_xent", x, T, V, D, 0, 0)
+    _enqueue(lib().gemm_relu_xent, device, None, x.data_ptr(), w.data_ptr(), targets.data_ptr(), loss.data_ptr(),
+             lse.data_ptr(), T, V, D, ldx, layout, dtype, space.data_ptr(), space.shape[0])
+    return loss, lse
 
 
 def gemm_relu_xent_grad(x, w, targets, lse, dloss, dx=None, dw=None, want_dx: bool = True, want_dw: bool = True,
@@ -667,13 +669,18 @@ def gemm_relu_xent_grad(x, w, targets, lse, dloss, dx=None, dw=None, want_dx: bo
     ``want_dx=False`` or ``want_dw=False`` leaves that one out (None)."""
     dtype, layout = _dtype_code(x, w), _layout_code(b_layout)
     T, V, D, ldx, device = _head_sizes(x, w, layout)
+    if stream is not None:
+        with _on_stream(stream, device):
+            return gemm_relu_xent_grad(x, w, targets, lse, dloss, dx, dw, want_dx, want_dw, b_layout)
     _index("targets", targets, T, device)
     _floats("lse", lse, T, device)
     step = _dloss(dloss, T, device)
-    allocate, ld_dx = _gradients(dx, dw, x, w, T, D, device, want_dx, want_dw)
-    return _loss_call(lib().gemm_relu_xent_grad, x, device, stream, T, V, D, 0, 1, allocate,
-                      lambda o: (x.data_ptr(), w.data_ptr(), targets.data_ptr(), lse.data_ptr(), dloss.data_ptr(), step,
-                                 _pointer(o[0]), _pointer(o[1]), T, V, D, ldx, ld_dx, layout, dtype))
+    dx, ld_dx, dw = _gradients(dx, dw, x, w, T, D, device, want_dx, want_dw)
+    space = _workspace("gemm_relu_xent_grad", x, T, V, D, 0, 1)
+    _enqueue(lib().gemm_relu_xent_grad, device, None, x.data_ptr(), w.data_ptr(), targets.data_ptr(), lse.data_ptr(),
+             dloss.data_ptr(), step, _pointer(dx), _pointer(dw), T, V, D, ldx, ld_dx, layout, dtype, space.data_ptr(),
+             space.shape[0])
+    return dx, dw
 
 
 def gemm_relu_distill(x, w, ids, logits, temperature: float = 1.0, loss=None, lse=None, b_layout: str = "kn",
@@ -688,11 +695,16 @@ def gemm_relu_distill(x, w, ids, logits, temperature: float = 1.0, loss=None, ls
     The rest as ``gemm_relu_xent``."""
     dtype, layout = _dtype_code(x, w), _layout_code(b_layout)
     T, V, D, ldx, device = _head_sizes(x, w, layout)
+    if stream is not None:
+        with _on_stream(stream, device):
+            return gemm_relu_distill(x, w, ids, logits, temperature, loss, lse, b_layout)
     k, ld_ids, ld_logits, code = _teacher(ids, logits, T, device)
-    return _loss_call(lib().gemm_relu_distill, x, device, stream, T, V, D, k, 0, _losses(loss, lse, x, T, device),
-                      lambda o: (x.data_ptr(), w.data_ptr(), ids.data_ptr(), logits.data_ptr(), temperature,
-                                 o[0].data_ptr(), o[1].data_ptr(), T, V, D, k, ldx, ld_ids, ld_logits, layout, dtype,
-                                 code))
+    loss, lse = _row_floats("loss", loss, T, x, device), _row_floats("lse", lse, T, x, device)
+    space = _workspace("gemm_relu_distill", x, T, V, D, k, 0)
+    _enqueue(lib().gemm_relu_distill, device, None, x.data_ptr(), w.data_ptr(), ids.data_ptr(), logits.data_ptr(),
+             temperature, loss.data_ptr(), lse.data_ptr(), T, V, D, k, ldx, ld_ids, ld_logits, layout, dtype, code,
+             space.data_ptr(), space.shape[0])
+    return loss, lse
 
 
 def gemm_relu_distill_grad(x, w, ids, logits, lse, dloss, temperature: float = 1.0, dx=None, dw=None,
@@ -700,14 +712,19 @@ def gemm_relu_distill_grad(x, w, ids, logits, lse, dloss, temperature: float = 1
     """(dx, dw) of ``gemm_relu_distill``, as ``gemm_relu_xent_grad``."""
     dtype, layout = _dtype_code(x, w), _layout_code(b_layout)
     T, V, D, ldx, device = _head_sizes(x, w, layout)
+    if stream is not None:
+        with _on_stream(stream, device):
+            return gemm_relu_distill_grad(x, w, ids, logits, lse, dloss, temperature, dx, dw, want_dx, want_dw,
+                                          b_layout)
     k, ld_ids, ld_logits, code = _teacher(ids, logits, T, device)
     _floats("lse", lse, T, device)
     step = _dloss(dloss, T, device)
-    allocate, ld_dx = _gradients(dx, dw, x, w, T, D, device, want_dx, want_dw)
-    return _loss_call(lib().gemm_relu_distill_grad, x, device, stream, T, V, D, k, 1, allocate,
-                      lambda o: (x.data_ptr(), w.data_ptr(), ids.data_ptr(), logits.data_ptr(), temperature,
-                                 lse.data_ptr(), dloss.data_ptr(), step, _pointer(o[0]), _pointer(o[1]), T, V, D, k, ldx,
-                                 ld_ids, ld_logits, ld_dx, layout, dtype, code))
+    dx, ld_dx, dw = _gradients(dx, dw, x, w, T, D, device, want_dx, want_dw)
+    space = _workspace("gemm_relu_distill_grad", x, T, V, D, k, 1)
+    _enqueue(lib().gemm_relu_distill_grad, device, None, x.data_ptr(), w.data_ptr(), ids.data_ptr(), logits.data_ptr(),
+             temperature, lse.data_ptr(), dloss.data_ptr(), step, _pointer(dx), _pointer(dw), T, V, D, k, ldx, ld_ids,
+             ld_logits, ld_dx, layout, dtype, code, space.data_ptr(), space.shape[0])
+    return dx, dw
 
 
 def shutdown():

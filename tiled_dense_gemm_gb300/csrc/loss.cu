@@ -76,6 +76,7 @@ static int launch_mode(DeviceState& d, const TilePlan& t, const LossMaps& m, Los
     q.width = t.width;
     q.bk = t.bk;
     q.bufs = t.bufs;
+    q.warm = 8;
     q.n_tiles = t.n_tiles;
     q.group_m = t.group_m;
     q.splits = t.splits;
@@ -93,9 +94,15 @@ static int launch_mode(DeviceState& d, const TilePlan& t, const LossMaps& m, Los
     return t.pair ? launch_tiles<true, kMode>(d, t, m, q, st) : launch_tiles<false, kMode>(d, t, m, q, st);
 }
 
-// The rows' kernels for rows [b0, b0 + T): the teacher's words, which rows are
-// in use, a copy of those.
-static int run_rows(const Call& c, const LossPlan& p, int64_t b0, int64_t T, DeviceState& d) {
+// A row is in use where its flag is in [0, limit).
+static const int32_t* flags_of(const Call& c, const LossPlan& p, int64_t b0) {
+    return c.ids ? reinterpret_cast<const int32_t*>(c.ws + p.flags) : c.targets + b0;
+}
+
+static int32_t limit_of(const Call& c) { return c.ids ? 1 : (int32_t)c.V; }
+
+// The teacher's words of rows [b0, b0 + T).
+static int run_teacher(const Call& c, const LossPlan& p, int64_t b0, int64_t T, DeviceState& d) {
     int rc;
     if (c.ids) {
         TeacherParams q;
@@ -118,11 +125,21 @@ static int run_rows(const Call& c, const LossPlan& p, int64_t b0, int64_t T, Dev
         rc = launch(loss_teacher_kernel, grid, 32 * kTeacherWarps, (size_t)kTeacherWarps * ((c.k + 3) / 4 * 4) * 8, 1, c.st, q);
         if (rc != GEMM_OK) return rc;
     }
-    if (!p.gather) return GEMM_OK;
+    return GEMM_OK;
+}
+
+// What the largest |dloss tau| is scaled to.  The largest entries of G, a (p - 1)
+// of wanted words that are not foreseen, are near the top of a binade, where a
+// 16-bit type rounds finest, and the limit itself is exact; binary16 besides keeps
+// what it can of small ones (relative error of bfloat16 gradients: PLACEHOLDER).
+static float top_of(const Call& c) { return c.bf16 ? 255.0f / 128.0f : 2047.0f / 1024.0f * 16384.0f; }
+
+// Which rows [b0, b0 + T) are in use, and a copy of those.
+static int run_rows(const Call& c, const LossPlan& p, int64_t b0, int64_t T, DeviceState& d) {
     RowsParams q;
     memset(&q, 0, sizeof(q));
-    q.flags = c.ids ? reinterpret_cast<const int32_t*>(c.ws + p.flags) : c.targets + b0;
-    q.limit = c.ids ? 1 : (int32_t)c.V;
+    q.flags = flags_of(c, p, b0);
+    q.limit = limit_of(c);
     q.T = (int32_t)T;
     q.D = (int32_t)c.D;
     q.X = reinterpret_cast<const uint16_t*>(c.X) + b0 * c.ldx;
@@ -138,12 +155,9 @@ static int run_rows(const Call& c, const LossPlan& p, int64_t b0, int64_t T, Dev
     q.dloss = c.dloss;
     q.dloss_stride = c.dloss_stride;
     q.grad_scale = c.ids ? c.tau : 1.0f;
-    // The largest entries of G, a (p - 1) of wanted words that are not foreseen,
-    // are near the top of a binade, where a 16-bit type rounds finest, and the
-    // limit itself is exact; binary16 besides keeps what it can of small ones
-    // (relative error of bfloat16 gradients: PLACEHOLDER).
-    q.top = c.bf16 ? 255.0f / 128.0f : 2047.0f / 1024.0f * 16384.0f;
+    q.top = top_of(c);
     q.err = d.d_err;
+    if (p.masked) return launch(loss_mask_kernel, (int)T, kRowsThreads, 0, 1, c.st, q);
     const int grid = (int)std::max<int64_t>(1, std::min<int64_t>((T + 7) / 8, 4 * d.sm_count));
     return launch(loss_rows_kernel, grid, kRowsThreads, 0, 1, c.st, q);
 }
@@ -178,7 +192,7 @@ static int encode_x(CUtensorMap* m, const Call& c, const LossPlan& p, int64_t b0
     int rc = encode_rows(&m[0], reinterpret_cast<const uint16_t*>(c.X) + b0 * c.ldx, (uint64_t)c.D, (uint64_t)T, (uint64_t)c.ldx,
                          box, blocks, c.bf16);
     m[1] = m[0];
-    if (rc == GEMM_OK && p.gather)
+    if (rc == GEMM_OK && (p.gather || p.masked))
         rc = encode_rows(&m[1], c.ws + p.gathered, (uint64_t)c.D, (uint64_t)T, (uint64_t)p.pitch, box, blocks, c.bf16);
     return rc;
 }
@@ -186,7 +200,8 @@ static int encode_x(CUtensorMap* m, const Call& c, const LossPlan& p, int64_t b0
 static int run_forward(const Call& c, const LossPlan& p, DeviceState& d) {
     for (int64_t b0 = 0; b0 < c.T; b0 += p.rows) {
         const int64_t T = std::min(p.rows, c.T - b0);
-        int rc = run_rows(c, p, b0, T, d);
+        int rc = run_teacher(c, p, b0, T, d);
+        if (rc == GEMM_OK && p.gather) rc = run_rows(c, p, b0, T, d);
         if (rc != GEMM_OK) return rc;
         const TilePlan t = plan_logits(T, c.V, c.D, !c.nk, true, d.sm_count, d.max_pairs);
         LossMaps m;
@@ -215,25 +230,44 @@ static int run_forward(const Call& c, const LossPlan& p, DeviceState& d) {
         o.T = (int32_t)T;
         o.rows = q.rows;
         o.index = q.index;
-        o.flags = c.ids ? reinterpret_cast<const int32_t*>(c.ws + p.flags) : c.targets + b0;
-        o.limit = c.ids ? 1 : (int32_t)c.V;
+        o.flags = flags_of(c, p, b0);
+        o.limit = limit_of(c);
         o.entropy = c.ids ? reinterpret_cast<const float*>(c.ws + p.entropy) : nullptr;
         o.tau = c.tau;
         o.log2_scale = q.log2_scale;
         o.loss = c.loss + b0;
         o.lse = c.lse_out + b0;
         o.err = d.d_err;
-        rc = T <= 2048 ? launch(loss_combine_kernel<8, 32>, (int)((T + 7) / 8), 1024, 0, 1, c.st, o)
-                       : launch(loss_combine_kernel<32, 16>, (int)((T + 31) / 32), 512, 0, 1, c.st, o);
+        rc = T <= 1024 ? launch(loss_combine_kernel<32>, (int)((T + 7) / 8), 1024, 0, 1, c.st, o)
+                       : launch(loss_combine_kernel<16>, (int)((T + 7) / 8), 512, 0, 1, c.st, o);
         if (rc != GEMM_OK) return rc;
     }
     return GEMM_OK;
 }
 
+static FinishParams finish_of(const Call& c, const LossPlan& p) {
+    FinishParams f;
+    memset(&f, 0, sizeof(f));
+    f.sums = reinterpret_cast<const float*>(c.ws + p.sums);
+    f.splits = p.sum_splits;
+    f.T = (int32_t)c.T;
+    f.D = (int32_t)c.D;
+    f.bf16 = c.bf16 ? 1 : 0;
+    f.rows = reinterpret_cast<const RowsHeader*>(c.ws + p.header);
+    f.index = p.masked ? nullptr : reinterpret_cast<const int32_t*>(c.ws + p.index);
+    f.flags = flags_of(c, p, 0);
+    f.limit = limit_of(c);
+    f.dX = reinterpret_cast<uint16_t*>(c.dX);
+    f.ld_dx = c.ld_dx;
+    return f;
+}
+
 static int run_backward(const Call& c, const LossPlan& p, DeviceState& d) {
-    int rc = run_rows(c, p, 0, c.T, d);
+    int rc = run_teacher(c, p, 0, c.T, d);
+    if (rc == GEMM_OK && p.gather) rc = run_rows(c, p, 0, c.T, d);
     if (rc != GEMM_OK) return rc;
     const RowsHeader* rows = reinterpret_cast<const RowsHeader*>(c.ws + p.header);
+    const RowsHeader* counted = p.masked ? nullptr : rows;
     uint16_t* const G = reinterpret_cast<uint16_t*>(c.ws + p.grad);
     float* const sums = reinterpret_cast<float*>(c.ws + p.sums);
     for (int64_t p0 = 0; p0 < c.V; p0 += p.piece) {
@@ -249,6 +283,12 @@ static int run_backward(const Call& c, const LossPlan& p, DeviceState& d) {
             q.bf16 = c.bf16 ? 1 : 0;
             wanted(c, p, 0, q);
             q.w_row = (int32_t)p0;
+            q.scale = p.masked ? nullptr : rows;
+            q.top = top_of(c);
+            if (p.masked) {
+                q.flags = flags_of(c, p, 0);
+                q.limit = limit_of(c);
+            }
             q.lse = c.lse;
             q.dloss = c.dloss;
             q.dloss_stride = c.dloss_stride;
@@ -260,6 +300,7 @@ static int run_backward(const Call& c, const LossPlan& p, DeviceState& d) {
                 rc = encode_rows(&m.d, G, (uint64_t)p.piece, (uint64_t)c.T, (uint64_t)p.piece, 32, 0, c.bf16);
             m.b[1] = m.b[0];
             if (rc == GEMM_OK) rc = launch_mode<kGrad>(d, t, m, q, c.st);
+            if (rc == GEMM_OK && p.masked && p0 == 0) rc = run_rows(c, p, 0, c.T, d);
             if (rc != GEMM_OK) return rc;
         }
         if (c.dX) {  // sums += G W
@@ -270,8 +311,8 @@ static int run_backward(const Call& c, const LossPlan& p, DeviceState& d) {
             q.N = (int32_t)c.D;
             q.K = (int32_t)vp;
             q.bf16 = c.bf16 ? 1 : 0;
-            q.rows = rows;
-            q.rows_m = 1;
+            q.rows = counted;
+            q.rows_m = counted ? 1 : 0;
             q.first = p0 == 0;
             q.w_k = (int32_t)p0;
             q.b_mn = c.nk ? 1 : 0;
@@ -298,8 +339,11 @@ static int run_backward(const Call& c, const LossPlan& p, DeviceState& d) {
             q.N = (int32_t)N;
             q.K = (int32_t)c.T;
             q.bf16 = c.bf16 ? 1 : 0;
-            q.rows = rows;
-            q.rows_k = 1;
+            q.rows = counted;
+            q.rows_k = counted ? 1 : 0;
+            q.scale = rows;
+            q.late = c.dX ? 1 : 0;  // (beside the end of kSum, which has waited for G)
+            if (c.dX && p0 + p.piece >= c.V) q.finish = finish_of(c, p);
             q.a_mn = q.b_mn = 1;
             q.a_3d = c.nk || x3d;
             q.b_3d = !c.nk || x3d;
@@ -309,6 +353,7 @@ static int run_backward(const Call& c, const LossPlan& p, DeviceState& d) {
             rc = encode_rows(&mg[0], G, (uint64_t)p.piece, (uint64_t)c.T, (uint64_t)p.piece, (uint32_t)t.bk, c.nk ? 2 : chunks, c.bf16);
             mg[1] = mg[0];
             if (rc == GEMM_OK) rc = encode_x(mx, c, p, 0, c.T, (uint32_t)t.bk, !x3d ? 0 : c.nk ? chunks : 2);
+            if (p.masked) mx[0] = mx[1];
             if (rc == GEMM_OK)
                 rc = c.nk ? encode_rows(&m.d, c.dW, (uint64_t)c.D, (uint64_t)c.V, (uint64_t)c.D, 32, 0, c.bf16)
                           : encode_rows(&m.d, c.dW, (uint64_t)c.V, (uint64_t)c.D, (uint64_t)c.V, 32, 0, c.bf16);
@@ -316,22 +361,9 @@ static int run_backward(const Call& c, const LossPlan& p, DeviceState& d) {
             if (rc != GEMM_OK) return rc;
         }
     }
-    if (!c.dX) return GEMM_OK;
-    FinishParams f;
-    memset(&f, 0, sizeof(f));
-    f.sums = sums;
-    f.splits = p.sum_splits;
-    f.T = (int32_t)c.T;
-    f.D = (int32_t)c.D;
-    f.bf16 = c.bf16 ? 1 : 0;
-    f.rows = rows;
-    f.index = reinterpret_cast<const int32_t*>(c.ws + p.index);
-    f.dX = reinterpret_cast<uint16_t*>(c.dX);
-    f.ld_dx = c.ld_dx;
+    if (!c.dX || c.dW) return GEMM_OK;
     const int64_t vecs = c.T * (c.D / 8);
-    if (f.splits >= 8)
-        return launch(loss_finish_kernel<8>, (int)std::min<int64_t>((vecs + 31) / 32, 8 * d.sm_count), 256, 0, 1, c.st, f);
-    return launch(loss_finish_kernel<1>, (int)std::min<int64_t>((vecs + 255) / 256, 8 * d.sm_count), 256, 0, 1, c.st, f);
+    return launch(loss_finish_kernel, (int)std::min<int64_t>((vecs + 255) / 256, 8 * d.sm_count), 256, 0, 1, c.st, finish_of(c, p));
 }
 
 // ------------------------------------------------------------------ checks

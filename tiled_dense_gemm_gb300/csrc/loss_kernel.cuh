@@ -58,6 +58,18 @@ struct LossMaps {
     CUtensorMap d;
 };
 
+// dX from its sums.
+struct FinishParams {
+    const float* sums;       // [splits][T][D]
+    int32_t splits, T, D, bf16;
+    const RowsHeader* rows;
+    const int32_t* index;    // null: all rows in their places,
+    const int32_t* flags;    // ... in use where in [0, limit)
+    int32_t limit;
+    uint16_t* dX;
+    int64_t ld_dx;
+};
+
 struct LossParams {
     int32_t M, N, K;       // D is M x N, K the reduction (bounds, where the rows' count replaces them)
     int32_t rows_m;        // M is the rows' count
@@ -72,13 +84,23 @@ struct LossParams {
     uint32_t a_bytes;      // of a stage (the box's)
     uint32_t stage_bytes;
     int32_t num_stages;
+    // This launch goes by its predecessor's wait: it reads nothing of what that
+    // one writes, and that one lets it start only once it has itself waited for all
+    // before.  It waits for its predecessor before it ends, so that its end says
+    // that all before it is done.
+    int32_t late;
+    int32_t warm;          // single CTAs: k-blocks of B asked for in L2 ahead
     int32_t bufs;          // staging buffers of an epilogue warp: 1 or 2
     uint32_t tmem_cols;    // allocated; half per accumulator
     int32_t bf16;
     int32_t w_row, w_k;    // first word of the piece, added to B's row or to its k
     int32_t d_row, d_col;  // ... or to the output's row or column
     int32_t first;         // kSum: 1: set, 0: add
-    const RowsHeader* rows;  // null: all T rows, as given
+    const RowsHeader* rows;  // the rows' count; null: all rows, as given
+    const RowsHeader* scale;  // kGrad: null: to be found from `top` (up to 128 rows)
+    float top;
+    const int32_t* flags;    // kGrad, rows null: a row is in use if its flag is in [0, limit)
+    int32_t limit;
     const int32_t* index;    // row of the batch of each gathered row
     // the wanted words: a target per row, or (ids != null) k sorted ones with weights
     const int32_t* targets;
@@ -92,6 +114,7 @@ struct LossParams {
     const float* dloss;
     int64_t dloss_stride;    // 0 or 1
     float grad_scale;        // tau
+    FinishParams finish;     // kWeight: dX != null: to be done at the end
     int32_t* err;
     uint64_t timeout_ns;
     int32_t test_drop_kb;    // as of the ragged kernels: a block of A's rows (single CTAs)
@@ -101,6 +124,29 @@ __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+    return x;
+}
+
+// The largest |dloss| of the rows in use, by one warp (few rows).
+__device__ __forceinline__ float largest_dloss(const int32_t* flags, int32_t limit, const float* dloss, int64_t stride, int32_t T) {
+    float top = 0.0f;
+    for (int32_t t = (int32_t)threadIdx.x % 32; t < T; t += 32) {
+        const int32_t y = __ldcg(flags + t);
+        const float d = __ldg(dloss + (int64_t)t * stride);
+        if (y >= 0 && y < limit) top = fmaxf(top, fabsf(d));
+    }
+    return warp_max(top);
+}
+
+// The scale of G that brings the largest |dloss grad_scale| to `top`.
+__device__ __forceinline__ float scale_of(float top, float grad_scale, float largest) {
+    largest *= grad_scale;
+    return largest > 1e-30f && largest < 1e30f ? top / largest : 1.0f;
 }
 
 // 3-D tiled add shared -> global (bulk-group completion).
@@ -181,6 +227,58 @@ __device__ __forceinline__ void merge_stats(float& m, float& s, float m1, float 
     m = top;
 }
 
+// dX[row] from its shares, rounded once; +0 in the rows that are not in use.
+// kLanes threads per eight columns take the shares in turn and are added up in a
+// fixed order.  By all blocks of a launch, `threads` each.
+template <int kLanes>
+__device__ __forceinline__ void finish_lanes(const FinishParams& p, int32_t threads) {
+    const int32_t valid = p.index ? __ldcg(&p.rows->valid) : p.T;
+    const float u = __ldcg(&p.rows->unscale);
+    const int32_t vecs = p.D / 8, lane = (int32_t)threadIdx.x % kLanes;
+    const int64_t total = (int64_t)p.T * vecs, share = (int64_t)p.T * p.D;
+    const int64_t step = (int64_t)gridDim.x * (threads / kLanes), rounds = (total + step - 1) / step;
+    int64_t i = (int64_t)blockIdx.x * (threads / kLanes) + threadIdx.x / kLanes;
+    for (int64_t n = 0; n < rounds; ++n, i += step) {
+        const int32_t r = i < total ? (int32_t)(i / vecs) : 0, c = (int32_t)(i - (int64_t)r * vecs);
+        float4 a = make_float4(0, 0, 0, 0), b = a;
+        if (i < total && r < valid) {
+            const float4* const src = reinterpret_cast<const float4*>(p.sums + (int64_t)r * p.D) + 2 * c;
+#pragma unroll 4
+            for (int32_t k = lane; k < p.splits; k += kLanes) {
+                const float4 x = __ldcs(src + k * (share / 4)), y = __ldcs(src + k * (share / 4) + 1);
+                a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
+                b.x += y.x, b.y += y.y, b.z += y.z, b.w += y.w;
+            }
+        }
+#pragma unroll
+        for (int d = 1; d < kLanes; d <<= 1) {
+            a.x += __shfl_xor_sync(0xffffffffu, a.x, d), a.y += __shfl_xor_sync(0xffffffffu, a.y, d);
+            a.z += __shfl_xor_sync(0xffffffffu, a.z, d), a.w += __shfl_xor_sync(0xffffffffu, a.w, d);
+            b.x += __shfl_xor_sync(0xffffffffu, b.x, d), b.y += __shfl_xor_sync(0xffffffffu, b.y, d);
+            b.z += __shfl_xor_sync(0xffffffffu, b.z, d), b.w += __shfl_xor_sync(0xffffffffu, b.w, d);
+        }
+        if (i < total && lane == 0) {
+            uint4 o = make_uint4(0, 0, 0, 0);
+            bool in = r < valid;
+            if (!p.index) {
+                const int32_t f = __ldcg(p.flags + r);
+                in = f >= 0 && f < p.limit;
+            }
+            if (in)
+                o = make_uint4(pack16(a.x * u, a.y * u, p.bf16), pack16(a.z * u, a.w * u, p.bf16),
+                               pack16(b.x * u, b.y * u, p.bf16), pack16(b.z * u, b.w * u, p.bf16));
+            reinterpret_cast<uint4*>(p.dX + (int64_t)(p.index ? __ldcg(p.index + r) : r) * p.ld_dx)[c] = o;
+        }
+    }
+}
+
+__device__ __forceinline__ void finish_dx(const FinishParams& p, int32_t threads) {
+    if (p.splits >= 8)
+        finish_lanes<4>(p, threads);
+    else
+        finish_lanes<1>(p, threads);
+}
+
 template <bool kPair, int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
     loss_kernel(const __grid_constant__ LossMaps maps, const __grid_constant__ LossParams q) {
@@ -223,8 +321,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     else
         cta_barrier_sync();
     tc_fence_after();
-    grid_launch_dependents();
-    grid_dependency_wait();
+    if constexpr (!kPair && kMode != kWeight) {
+        // Few rows: the weights' way from memory is all there is, so the first item's
+        // are asked for in L2 before the kernel before is waited for (a line that it
+        // still writes is current there).  PLACEHOLDER
+        if (warp == 6 && lane == 0) {
+            const uint32_t split = worker / (uint32_t)q.n_tiles, nt = worker - split * (uint32_t)q.n_tiles;
+            const int32_t blocks = (q.K + q.bk - 1) / q.bk;
+            const int32_t r0 = (int32_t)nt * q.width + q.w_row, kb0 = (int32_t)((int64_t)split * blocks / q.splits);
+            for (int32_t i = 0; i < q.warm && kb0 + i < blocks; ++i) {
+                const int32_t k0 = (kb0 + i) * q.bk + q.w_k;
+                if (q.b_3d) {
+                    tma_prefetch_3d(&maps.b[0], 0, q.b_mn ? k0 : r0, (q.b_mn ? r0 : k0) / 64);
+                } else {
+                    for (int32_t j = 0; j < (q.b_mn ? q.width : q.bk) / 64; ++j)
+                        tma_prefetch_2d(&maps.b[0], q.b_mn ? r0 + 64 * j : k0 + 64 * j, q.b_mn ? k0 : r0);
+                }
+            }
+        }
+        __syncwarp();
+    }
+    if (kMode == kStats) grid_launch_dependents();
+    if (!q.late) grid_dependency_wait();
+    if (kMode != kStats) grid_launch_dependents();  // (what follows may go by this wait)
     const uint32_t tmem_base = ctrl->tmem_addr;
     const uint32_t S = (uint32_t)q.num_stages, stride = q.stage_bytes;
     const uint32_t full0 = smem_u32(&ctrl->full[0]), empty0 = smem_u32(&ctrl->empty[0]);
@@ -386,6 +505,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (G's rows are kWeight's reduction: zeros up to the end of its last k-block)
         const int32_t row_end = kMode == kGrad ? (M + kRowPad - 1) / kRowPad * kRowPad : M;
         uint32_t local = 0, tile = 0, staging = staging0;
+        float scale = 1.0f;
+        if constexpr (kMode == kGrad) scale = q.scale ? __ldcg(&q.scale->scale) : scale_of(q.top, q.grad_scale, largest_dloss(q.flags, q.limit, q.dloss, q.dloss_stride, q.M));
         // the staging buffer to write next, once the copy out of it has been read
         auto turn = [&]() {
             if (q.bufs == 2) {
@@ -400,17 +521,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool some = k.kb1 > k.kb0;
             const int32_t row0 = k.mt * kTileM + 128 * (int32_t)rank + 32 * (int32_t)quarter;
             const int32_t r = row0 + (int32_t)lane, n0 = k.nt * q.width;
-            const bool live = r < M;
+            bool live = r < M;
             // what the row's epilogue reads, before the accumulator is waited for
             int32_t t = 0, y = kNone;
             float coef = 0.0f, shift = 0.0f;
             if constexpr (kMode == kStats || kMode == kGrad) {
                 t = live && gathered ? __ldcg(q.index + r) : r;
+                if (kMode == kGrad && live && q.flags) {
+                    const int32_t f = __ldcg(q.flags + t);
+                    live = f >= 0 && f < q.limit;
+                }
                 if (live && !q.ids) y = __ldcg(q.targets + t);
                 if constexpr (kMode == kGrad) {
                     if (live) {
                         shift = -1.4426950408889634f * __ldg(q.lse + t);
-                        coef = __ldg(q.dloss + (int64_t)t * q.dloss_stride) * q.grad_scale * __ldcg(&q.rows->scale);
+                        coef = __ldg(q.dloss + (int64_t)t * q.dloss_stride) * q.grad_scale * scale;
                     }
                 }
             }
@@ -559,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if constexpr (kMode == kGrad || kMode == kWeight) {
-                    const float u = kMode == kWeight ? __ldcg(&q.rows->unscale) : 1.0f;
+                    const float u = kMode == kWeight ? __ldcg(&q.scale->unscale) : 1.0f;
                     uint32_t x[32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) x[j] = pack16(u * v[2 * j], u * v[2 * j + 1], q.bf16);
@@ -608,6 +733,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     }
 
+    if (q.late) grid_dependency_wait();
+    if constexpr (kMode == kWeight) {
+        if (q.finish.dX) finish_dx(q.finish, kThreads);  // the sums are complete
+    }
     __syncthreads();
     if (threadIdx.x == 0 && *(volatile int32_t*)&ctrl->abort_flag) rg::drain_ring(ctrl, full0, S);
     tc_fence_before();

@@ -109,7 +109,8 @@ LossPlan plan_loss(int64_t T, int64_t V, int64_t D, int64_t k, bool gradient) {
     LossPlan p = {};
     p.rows = gradient ? T : std::min(T, kBlockRows);
     // forward: rows in use are gathered where that saves tiles
-    p.gather = gradient || T > 128;
+    p.gather = T > 128;
+    p.masked = gradient && !p.gather;
     const int64_t rows = p.rows;
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
@@ -126,7 +127,7 @@ LossPlan plan_loss(int64_t T, int64_t V, int64_t D, int64_t k, bool gradient) {
         p.weights = take(4 * rows * k);
     }
     p.pitch = round_up(D, 64);
-    if (p.gather) p.gathered = take(2 * rows * p.pitch);
+    if (p.gather || p.masked) p.gathered = take(2 * rows * p.pitch);
     if (!gradient) {
         // (of the narrowest tiles)
         p.parts = (int32_t)ceil_div(V, 64);

@@ -31,12 +31,6 @@ __device__ __forceinline__ float load_logit(const TeacherParams& p, int64_t at) 
     return p.logits_type == 1 ? __uint_as_float((uint32_t)x << 16) : __half2float(__ushort_as_half(x));
 }
 
-__device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-    return x;
-}
-
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
@@ -135,6 +129,15 @@ struct RowsParams {
 
 constexpr int kRowsThreads = 256;
 
+// top: the largest |dloss|
+__device__ __forceinline__ void write_header(const RowsParams& p, int32_t valid, int32_t compact, float top) {
+    const float scale = scale_of(p.top, p.grad_scale, top);
+    p.rows->valid = valid;
+    p.rows->compact = compact;
+    p.rows->scale = scale;
+    p.rows->unscale = 1.0f / scale;
+}
+
 // Which rows have a wanted word, gathered to the front where some have none.
 // Each block counts for itself what lies before its rows (T flags out of L2, a
 // few microseconds beside products of milliseconds), so no block waits for
@@ -225,9 +228,8 @@ __global__ void __launch_bounds__(kRowsThreads) loss_rows_kernel(const __grid_co
         uint4* const dst = reinterpret_cast<uint4*>(p.gathered + (int64_t)total * p.pitch);
         for (int64_t c = i; c < n; c += kRowsThreads) dst[c] = make_uint4(0, 0, 0, 0);
     }
-    float scale = 1.0f;
+    float top = 0.0f;
     if (p.dloss) {
-        float top = 0.0f;
         if (p.dloss_stride == 0) {
             top = fabsf(__ldg(p.dloss));
         } else {
@@ -243,15 +245,30 @@ __global__ void __launch_bounds__(kRowsThreads) loss_rows_kernel(const __grid_co
         __syncthreads();
         top = 0.0f;
         for (int32_t j = 0; j < kRowsThreads / 32; ++j) top = fmaxf(top, parts[j]);
-        top *= p.grad_scale;
-        if (top > 1e-30f && top < 1e30f) scale = p.top / top;
     }
-    if (i == 0) {
-        p.rows->valid = total;
-        p.rows->compact = gather ? 1 : 0;
-        p.rows->scale = scale;
-        p.rows->unscale = 1.0f / scale;
+    if (i == 0) write_header(p, total, gather ? 1 : 0, top);
+}
+
+// Up to 128 rows: nothing is gathered (there is one row tile).  A copy of X with
+// zeros in the rows that are not in use, for dW, and the scale, beside the kernel
+// of G (`late`, as there: that one has waited for X and the flags).
+__global__ void __launch_bounds__(kRowsThreads) loss_mask_kernel(const __grid_constant__ RowsParams p) {
+    const int32_t i = (int32_t)threadIdx.x;
+    grid_launch_dependents();
+    const int32_t vecs = p.D / 8;
+    for (int32_t t = (int32_t)blockIdx.x; t < p.T; t += (int32_t)gridDim.x) {
+        const int32_t y = __ldcg(p.flags + t);
+        if (y >= p.limit && i == 0) atomicCAS(p.err + 1, 0, (int32_t)rg::kBadIds);
+        const bool in = y >= 0 && y < p.limit;
+        const uint4* const src = reinterpret_cast<const uint4*>(p.X + (int64_t)t * p.ldx);
+        uint4* const dst = reinterpret_cast<uint4*>(p.gathered + (int64_t)t * p.pitch);
+        for (int32_t c = i; c < vecs; c += kRowsThreads) dst[c] = in ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
     }
+    if (blockIdx.x == 0 && i < 32) {
+        const float top = largest_dloss(p.flags, p.limit, p.dloss, p.dloss_stride, p.T);
+        if (i == 0) write_header(p, p.T, 0, top);
+    }
+    grid_dependency_wait();
 }
 
 // ------------------------------------------------------------------ losses
@@ -271,12 +288,12 @@ struct CombineParams {
     int32_t* err;
 };
 
-// A block for kRows rows.  Its threads take a row's parts in turn and are
-// merged in a fixed order.  Eight rows where there are few, so that a row's parts
-// are in flight at once (64 rows, 512 parts: PLACEHOLDER us).
-template <int kRows, int kWarps>
+// A block for eight rows (a sector of the statistics), so that a row's parts are
+// in flight at once: its threads take them in turn and are merged in a fixed
+// order.
+template <int kWarps>
 __global__ void __launch_bounds__(32 * kWarps) loss_combine_kernel(const __grid_constant__ CombineParams p) {
-    constexpr int kLanes = 32 / kRows;  // of a warp, per row
+    constexpr int kRows = 8, kLanes = 32 / kRows;  // lanes of a warp per row
     __shared__ float part[3][kWarps][kRows];
     const int32_t warp = (int32_t)threadIdx.x / 32, lane = (int32_t)threadIdx.x % 32;
     const int32_t row = lane % kRows;
@@ -341,55 +358,10 @@ __global__ void __launch_bounds__(32 * kWarps) loss_combine_kernel(const __grid_
 
 // ------------------------------------------------------------------ dX
 
-struct FinishParams {
-    const float* sums;       // [splits][T][D]
-    int32_t splits, T, D, bf16;
-    const RowsHeader* rows;
-    const int32_t* index;
-    uint16_t* dX;
-    int64_t ld_dx;
-};
-
-// dX[row] from its shares, rounded once; +0 in the rows that are not in use.
-// kLanes threads per eight columns take the shares in turn and are added up in a
-// fixed order (many shares of few rows: PLACEHOLDER us with one thread, with eight).
-template <int kLanes>
 __global__ void __launch_bounds__(256) loss_finish_kernel(const __grid_constant__ FinishParams p) {
     grid_launch_dependents();
     grid_dependency_wait();
-    const int32_t valid = __ldcg(&p.rows->valid);
-    const float u = __ldcg(&p.rows->unscale);
-    const int32_t vecs = p.D / 8, lane = (int32_t)threadIdx.x % kLanes;
-    const int64_t total = (int64_t)p.T * vecs, share = (int64_t)p.T * p.D;
-    const int64_t step = (int64_t)gridDim.x * (256 / kLanes), rounds = (total + step - 1) / step;
-    int64_t i = (int64_t)blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;
-    for (int64_t n = 0; n < rounds; ++n, i += step) {
-        const int32_t r = i < total ? (int32_t)(i / vecs) : 0, c = (int32_t)(i - (int64_t)r * vecs);
-        float4 a = make_float4(0, 0, 0, 0), b = a;
-        if (i < total && r < valid) {
-            const float4* const src = reinterpret_cast<const float4*>(p.sums + (int64_t)r * p.D) + 2 * c;
-#pragma unroll 4
-            for (int32_t k = lane; k < p.splits; k += kLanes) {
-                const float4 x = __ldcs(src + k * (share / 4)), y = __ldcs(src + k * (share / 4) + 1);
-                a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
-                b.x += y.x, b.y += y.y, b.z += y.z, b.w += y.w;
-            }
-        }
-#pragma unroll
-        for (int d = 1; d < kLanes; d <<= 1) {
-            a.x += __shfl_xor_sync(0xffffffffu, a.x, d), a.y += __shfl_xor_sync(0xffffffffu, a.y, d);
-            a.z += __shfl_xor_sync(0xffffffffu, a.z, d), a.w += __shfl_xor_sync(0xffffffffu, a.w, d);
-            b.x += __shfl_xor_sync(0xffffffffu, b.x, d), b.y += __shfl_xor_sync(0xffffffffu, b.y, d);
-            b.z += __shfl_xor_sync(0xffffffffu, b.z, d), b.w += __shfl_xor_sync(0xffffffffu, b.w, d);
-        }
-        if (i < total && lane == 0) {
-            uint4 o = make_uint4(0, 0, 0, 0);
-            if (r < valid)
-                o = make_uint4(pack16(a.x * u, a.y * u, p.bf16), pack16(a.z * u, a.w * u, p.bf16),
-                               pack16(b.x * u, b.y * u, p.bf16), pack16(b.z * u, b.w * u, p.bf16));
-            reinterpret_cast<uint4*>(p.dX + (int64_t)__ldcg(p.index + r) * p.ld_dx)[c] = o;
-        }
-    }
+    finish_dx(p, 256);
 }
 
 }  // namespace ls
