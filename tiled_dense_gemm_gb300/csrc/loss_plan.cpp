@@ -32,7 +32,7 @@ double block_clocks(int64_t w, int64_t rows, bool pair) {
 }
 
 // bufs 0: statistics (the epilogue's halves hand over a few numbers)
-void finish_plan(TilePlan& p, int64_t M, int64_t N, bool a_mn, bool b_mn, int bufs, int num_sms, int max_pairs) {
+void finish_plan(TilePlan& p, int64_t M, int64_t N, bool a_mn, bool b_mn, int bufs, bool logits, int num_sms, int max_pairs) {
     const int64_t tile_m = p.pair ? 256 : 128, per_cta = p.width / (p.pair ? 2 : 1);
     p.m_tiles = (int32_t)ceil_div(M, tile_m);
     p.n_tiles = (int32_t)ceil_div(N, p.width);
@@ -54,7 +54,13 @@ void finish_plan(TilePlan& p, int64_t M, int64_t N, bool a_mn, bool b_mn, int bu
     const int64_t items = (int64_t)p.m_tiles * p.n_tiles * p.splits;
     p.grid = p.pair ? 2 * (int32_t)std::min<int64_t>(pairs_of(num_sms, max_pairs), items)
                     : (int32_t)std::min<int64_t>(num_sms, items);
-    p.group_m = (int32_t)std::min<int64_t>(p.m_tiles, 8);
+    // Row tiles walked together, column tile by column tile.  Logits: their rows of
+    // X stay in L2 while the weights pass, so the more the fewer passes (8192 rows,
+    // 131072 words of 4096: 4 together 5.53 ms, 8 5.32, 16 5.19, 32 5.48; 4096
+    // rows, 65536 of 2048: 702, 685, 665, 664 us).  Elsewhere both operands of a
+    // group are long: 8 (the gradients of 4096 rows, 131072 words of 4096, with 8 for
+    // all products 7.97 ms, with 16 8.10).
+    p.group_m = (int32_t)std::min<int64_t>(p.m_tiles, logits ? 16 : 8);
 }
 }  // namespace
 
@@ -79,7 +85,7 @@ TilePlan plan_logits(int64_t T, int64_t N, int64_t K, bool b_mn, bool stats, int
         }
     }
     p.bk = p.pair ? (p.width > 192 ? 64 : 128) : (rows <= 64 ? 128 : 64);
-    finish_plan(p, T, N, false, b_mn, stats ? 0 : 1, num_sms, max_pairs);
+    finish_plan(p, T, N, false, b_mn, stats ? 0 : 1, true, num_sms, max_pairs);
     return p;
 }
 
@@ -89,7 +95,7 @@ TilePlan plan_sum(int64_t T, int64_t N, int splits, int width, bool b_mn, int nu
     p.splits = splits;
     p.width = width;
     p.bk = p.pair && width > 192 ? 64 : 128;
-    finish_plan(p, T, N, false, b_mn, 1, num_sms, max_pairs);
+    finish_plan(p, T, N, false, b_mn, 1, false, num_sms, max_pairs);
     return p;
 }
 
@@ -101,7 +107,7 @@ TilePlan plan_weight(int64_t M, int64_t N, int64_t T, int num_sms, int max_pairs
     p.bk = 64;
     // Two staging buffers per warp where a tile's reduction is so short that its
     // stores are what takes time (PLACEHOLDER).
-    finish_plan(p, M, N, true, true, T <= 1024 ? 2 : 1, num_sms, max_pairs);
+    finish_plan(p, M, N, true, true, T <= 1024 ? 2 : 1, false, num_sms, max_pairs);
     return p;
 }
 
