@@ -149,6 +149,10 @@ __device__ __forceinline__ float scale_of(float top, float grad_scale, float lar
     return largest > 1e-30f && largest < 1e30f ? top / largest : 1.0f;
 }
 
+__device__ __forceinline__ void st_shared_u16(uint32_t addr, uint16_t x) {
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(x) : "memory");
+}
+
 // 3-D tiled add shared -> global (bulk-group completion).
 __device__ __forceinline__ void reduce_add_3d(const CUtensorMap* m, uint32_t src, int32_t x, int32_t y, int32_t z) {
     asm volatile(
@@ -159,25 +163,27 @@ __device__ __forceinline__ void reduce_add_3d(const CUtensorMap* m, uint32_t src
 }
 
 // A row's wanted words in rising order, from the first at or behind some column.
+// Frequent words come close together, so the word after the next one is on its
+// way while that is dealt with.
 struct Wanted {
-    const int32_t* ids;
-    const float* weights;
-    int32_t next;  // word, kNone: no more
-    int32_t left;  // words behind it
+    int64_t at;      // place of the word after `next` in the lists
+    int64_t end;
+    int32_t next;    // word, kNone: no more
+    float weight;    // its
+    int32_t next2;
+    float weight2;
 
     // `y`: the row's target where there is no teacher
     __device__ __forceinline__ void start(const LossParams& q, int32_t row, int32_t y, bool live, int32_t col) {
-        left = 0;
-        next = kNone;
-        ids = nullptr;
-        weights = nullptr;
+        at = end = 0;
+        next = next2 = kNone;
+        weight = weight2 = 1.0f;
         if (!live) return;
         if (!q.ids) {
             if (y >= col && y < q.V) next = y;
             return;
         }
-        ids = q.ids + (int64_t)row * q.k;
-        weights = q.weights + (int64_t)row * q.k;
+        const int32_t* const ids = q.ids + (int64_t)row * q.k;
         int32_t lo = 0, hi = q.k;
         while (lo < hi) {
             const int32_t mid = (lo + hi) >> 1;
@@ -186,26 +192,38 @@ struct Wanted {
             else
                 hi = mid;
         }
-        ids += lo;
-        weights += lo;
-        left = q.k - lo;
-        next = left > 0 ? __ldcg(ids) : kNone;
+        at = (int64_t)row * q.k + lo;
+        end = (int64_t)(row + 1) * q.k;
+        fetch(q, next, weight);
+        fetch(q, next2, weight2);
     }
 
-    __device__ __forceinline__ float weight() const { return ids ? __ldcg(weights) : 1.0f; }
-
-    __device__ __forceinline__ void advance() {
-        if (left > 1) {
-            ++ids;
-            ++weights;
-            --left;
-            next = __ldcg(ids);
-        } else {
-            left = 0;
-            next = kNone;
+    __device__ __forceinline__ void fetch(const LossParams& q, int32_t& id, float& w) {
+        id = kNone;
+        if (at < end) {
+            id = __ldcg(q.ids + at);
+            w = __ldcg(q.weights + at);
+            ++at;
         }
     }
+
+    __device__ __forceinline__ void advance(const LossParams& q) {
+        next = next2;
+        weight = weight2;
+        fetch(q, next2, weight2);
+    }
 };
+
+// v[at], halving.
+template <int kFrom, int kCount, int kSize>
+__device__ __forceinline__ float pick(const float (&v)[kSize], int32_t at) {
+    if constexpr (kCount == 1) {
+        return v[kFrom];
+    } else {
+        const float low = pick<kFrom, kCount / 2>(v, at), high = pick<kFrom + kCount / 2, kCount / 2>(v, at);
+        return at & (kCount / 2) ? high : low;
+    }
+}
 
 // kStats: the reduction in parts of at most this many k, each in an accumulator
 // of its own, added up in registers.  The tensor core truncates its sums in 32
@@ -593,16 +611,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (ch >= chunks || col >= q.N || row0 >= M) break;  // (uniform over the warp)
                     const int32_t here = min(64, n_end - col);           // of the chunk's columns
                     float(&v)[64] = z[i];
-                    while (want.next < col) want.advance();  // (of the other half's chunk)
+                    while (want.next < col) want.advance(q);  // (of the other half's chunk)
                     while (__any_sync(0xffffffffu, want.next - col < here)) {
                         const int32_t at = want.next - col;
-                        float x = 0.0f;
-#pragma unroll
-                        for (int j = 0; j < 64; ++j) x = j == at ? v[j] : x;
+                        const float x = pick<0, 64>(v, at);
                         if (at < here) {
-                            const float p = want.weight();
-                            if (p != 0.0f) t_run = fmaf(p, x, t_run);
-                            want.advance();
+                            if (want.weight != 0.0f) t_run = fmaf(want.weight, x, t_run);
+                            want.advance(q);
                         }
                     }
                     if (here < 64) {
@@ -667,20 +682,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if constexpr (kMode == kGrad) {
                     const int32_t c0 = col + q.w_row;  // the chunk's first word
-                    while (want.next < c0) want.advance();  // (of the other half's chunk)
+                    while (want.next < c0) want.advance(q);  // (of the other half's chunk)
 #pragma unroll
                     for (int j = 0; j < 64; ++j) {
                         const float p = coef * exp2_fast(fmaf(v[j], c, shift));
                         v[j] = live && col + j < q.N ? p : 0.0f;
-                    }
-                    while (__any_sync(0xffffffffu, want.next - c0 < 64)) {
-                        const int32_t at = want.next - c0;
-                        if (at < 64) {
-                            const float p = coef * want.weight();
-#pragma unroll
-                            for (int j = 0; j < 64; ++j) v[j] = j == at ? v[j] - p : v[j];
-                            want.advance();
-                        }
                     }
                 }
                 if constexpr (kMode == kGrad || kMode == kWeight) {
@@ -693,6 +699,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (uint32_t i = 0; i < 8; ++i)
                         rg::st_shared_v4(staging + lane * 128u + ((i ^ (lane & 7u)) << 4),
                                          make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]));
+                    if constexpr (kMode == kGrad) {
+                        // the wanted words, over what the row's thread has just written
+                        const int32_t c0 = col + q.w_row;
+                        int32_t last = kNone;
+                        float g = 0.0f;
+                        while (__any_sync(0xffffffffu, want.next - c0 < 64)) {
+                            const int32_t at = want.next - c0;
+                            const float p = pick<0, 64>(v, at);
+                            if (at < 64) {
+                                g = (at == last ? g : p) - coef * want.weight;  // (a word may come twice)
+                                last = at;
+                                st_shared_u16(staging + lane * 128u + ((((uint32_t)at >> 3) ^ (lane & 7u)) << 4) + ((uint32_t)at & 7u) * 2u,
+                                              rg::round16(g, q.bf16));
+                                want.advance(q);
+                            }
+                        }
+                    }
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
