@@ -75,7 +75,6 @@ template <int kMode>
 static int launch_mode(DeviceState& d, const TilePlan& t, const LossMaps& m, LossParams& q, cudaStream_t st) {
     q.width = t.width;
     q.bk = t.bk;
-    q.bufs = t.bufs;
     q.warm = 8;
     q.n_tiles = t.n_tiles;
     q.group_m = t.group_m;
@@ -145,11 +144,6 @@ static int run_rows(const Call& c, const LossPlan& p, int64_t b0, int64_t T, Dev
     q.X = reinterpret_cast<const uint16_t*>(c.X) + b0 * c.ldx;
     q.ldx = c.ldx;
     q.gathered = reinterpret_cast<uint16_t*>(c.ws + p.gathered);
-    q.pitch = (int32_t)p.pitch;
-    // A box row of a matrix whose pitch is not a multiple of 128 bytes lies in two
-    // lines; one such operand of two costs little, both a fifth (PLACEHOLDER).  W
-    // stays as it is.
-    q.always = T > 128 && (c.ldx % 64 != 0 || misaligned(q.X, 128));
     q.index = reinterpret_cast<int32_t*>(c.ws + p.index);
     q.rows = reinterpret_cast<RowsHeader*>(c.ws + p.header);
     q.dloss = c.dloss;
@@ -193,7 +187,7 @@ static int encode_x(CUtensorMap* m, const Call& c, const LossPlan& p, int64_t b0
                          box, blocks, c.bf16);
     m[1] = m[0];
     if (rc == GEMM_OK && (p.gather || p.masked))
-        rc = encode_rows(&m[1], c.ws + p.gathered, (uint64_t)c.D, (uint64_t)T, (uint64_t)p.pitch, box, blocks, c.bf16);
+        rc = encode_rows(&m[1], c.ws + p.gathered, (uint64_t)c.D, (uint64_t)T, (uint64_t)c.D, box, blocks, c.bf16);
     return rc;
 }
 
@@ -331,7 +325,7 @@ static int run_backward(const Call& c, const LossPlan& p, DeviceState& d) {
         }
         if (c.dW) {  // dW[piece] = G^T X, or its transpose
             const int64_t M = c.nk ? vp : c.D, N = c.nk ? c.D : vp;
-            const TilePlan t = plan_weight(M, N, c.T, d.sm_count, d.max_pairs);
+            const TilePlan t = plan_weight(M, N, d.sm_count, d.max_pairs);
             const uint32_t chunks = (uint32_t)(t.width / (t.pair ? 2 : 1)) / 64;
             const bool x3d = c.D % 64 == 0;
             memset(&q, 0, sizeof(q));

@@ -41,7 +41,7 @@ using rg::wait_phase;
 enum Mode : int { kStats = 0, kGrad = 1, kSum = 2, kWeight = 3 };
 
 constexpr int kThreads = 352;
-constexpr uint32_t kStaging = 4096;  // bytes per epilogue warp and buffer
+constexpr uint32_t kStaging = 4096;  // bytes per epilogue warp
 constexpr int32_t kRowPad = 128;     // rows in use, and G's, end in zeros up to a multiple of this
 constexpr int32_t kNone = 0x7fffffff;
 
@@ -90,7 +90,6 @@ struct LossParams {
     // that all before it is done.
     int32_t late;
     int32_t warm;          // single CTAs: k-blocks of B asked for in L2 ahead
-    int32_t bufs;          // staging buffers of an epilogue warp: 1 or 2
     uint32_t tmem_cols;    // allocated; half per accumulator
     int32_t bf16;
     int32_t w_row, w_k;    // first word of the piece, added to B's row or to its k
@@ -518,21 +517,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else {
         const uint32_t quarter = warp & 3u, half = warp >= 7 ? 1u : 0u;
-        const uint32_t staging0 = ring + S * stride + (quarter + 4u * half) * (uint32_t)q.bufs * kStaging;
+        const uint32_t staging = ring + S * stride + (quarter + 4u * half) * kStaging;
         const int32_t chunks = (q.width + 63) / 64;
         // (G's rows are kWeight's reduction: zeros up to the end of its last k-block)
         const int32_t row_end = kMode == kGrad ? (M + kRowPad - 1) / kRowPad * kRowPad : M;
-        uint32_t local = 0, tile = 0, staging = staging0;
+        uint32_t local = 0, tile = 0;
         float scale = 1.0f;
         if constexpr (kMode == kGrad) scale = q.scale ? __ldcg(&q.scale->scale) : scale_of(q.top, q.grad_scale, largest_dloss(q.flags, q.limit, q.dloss, q.dloss_stride, q.M));
-        // the staging buffer to write next, once the copy out of it has been read
+        // the copy issued from the staging buffer before must have read it
         auto turn = [&]() {
-            if (q.bufs == 2) {
-                staging = staging == staging0 ? staging0 + kStaging : staging0;
-                if (lane == 0) bulk_wait_group_read<1>();
-            } else if (lane == 0) {
-                bulk_wait_group_read<0>();
-            }
+            if (lane == 0) bulk_wait_group_read<0>();
             __syncwarp();
         };
         while (next(k)) {

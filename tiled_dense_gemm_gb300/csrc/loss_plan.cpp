@@ -31,8 +31,8 @@ double block_clocks(int64_t w, int64_t rows, bool pair) {
     return std::max(128.0 * (double)w / 24, 128.0 * (double)(w + rows) / 41);
 }
 
-// bufs 0: statistics (the epilogue's halves hand over a few numbers)
-void finish_plan(TilePlan& p, int64_t M, int64_t N, bool a_mn, bool b_mn, int bufs, bool logits, int num_sms, int max_pairs) {
+// not staged: statistics (the epilogue's halves hand over a few numbers)
+void finish_plan(TilePlan& p, int64_t M, int64_t N, bool a_mn, bool b_mn, bool staged, bool logits, int num_sms, int max_pairs) {
     const int64_t tile_m = p.pair ? 256 : 128, per_cta = p.width / (p.pair ? 2 : 1);
     p.m_tiles = (int32_t)ceil_div(M, tile_m);
     p.n_tiles = (int32_t)ceil_div(N, p.width);
@@ -42,8 +42,7 @@ void finish_plan(TilePlan& p, int64_t M, int64_t N, bool a_mn, bool b_mn, int bu
     const int64_t blocks = p.bk / 64;
     p.a_bytes = (int32_t)(a_mn ? 2 * 128 * p.bk : p.a_rows * 128 * blocks);
     p.stage_bytes = (int32_t)(p.a_bytes + (b_mn ? per_cta / 64 * 128 * p.bk : per_cta * 128 * blocks));
-    p.bufs = bufs;
-    const int64_t staging = bufs ? bufs * kStagingBytes : 4096;
+    const int64_t staging = staged ? kStagingBytes : 4096;
     // (the MMA reads 128 rows of A's last 64 k, from the last stage's start on)
     const int64_t tail = std::max<int64_t>(0, p.a_bytes / blocks * (blocks - 1) + 128 * 128 - p.stage_bytes - staging);
     p.num_stages = (int32_t)std::min<int64_t>(kMaxRing, (kSmem - kCtrl - staging - tail) / p.stage_bytes);
@@ -85,7 +84,7 @@ TilePlan plan_logits(int64_t T, int64_t N, int64_t K, bool b_mn, bool stats, int
         }
     }
     p.bk = p.pair ? (p.width > 192 ? 64 : 128) : (rows <= 64 ? 128 : 64);
-    finish_plan(p, T, N, false, b_mn, stats ? 0 : 1, true, num_sms, max_pairs);
+    finish_plan(p, T, N, false, b_mn, !stats, true, num_sms, max_pairs);
     return p;
 }
 
@@ -95,19 +94,17 @@ TilePlan plan_sum(int64_t T, int64_t N, int splits, int width, bool b_mn, int nu
     p.splits = splits;
     p.width = width;
     p.bk = p.pair && width > 192 ? 64 : 128;
-    finish_plan(p, T, N, false, b_mn, 1, false, num_sms, max_pairs);
+    finish_plan(p, T, N, false, b_mn, true, false, num_sms, max_pairs);
     return p;
 }
 
-TilePlan plan_weight(int64_t M, int64_t N, int64_t T, int num_sms, int max_pairs) {
+TilePlan plan_weight(int64_t M, int64_t N, int num_sms, int max_pairs) {
     TilePlan p = {};
     p.pair = pairs_of(num_sms, max_pairs) > 0;
     p.splits = 1;
     p.width = N > 128 ? 256 : 128;
     p.bk = 64;
-    // Two staging buffers per warp where a tile's reduction is so short that its
-    // stores are what takes time (PLACEHOLDER).
-    finish_plan(p, M, N, true, true, T <= 1024 ? 2 : 1, false, num_sms, max_pairs);
+    finish_plan(p, M, N, true, true, true, false, num_sms, max_pairs);
     return p;
 }
 
@@ -132,8 +129,7 @@ LossPlan plan_loss(int64_t T, int64_t V, int64_t D, int64_t k, bool gradient) {
         p.sorted = take(4 * rows * k);
         p.weights = take(4 * rows * k);
     }
-    p.pitch = round_up(D, 64);
-    if (p.gather || p.masked) p.gathered = take(2 * rows * p.pitch);
+    if (p.gather || p.masked) p.gathered = take(2 * rows * D);
     if (!gradient) {
         // (of the narrowest tiles)
         p.parts = (int32_t)ceil_div(V, 64);

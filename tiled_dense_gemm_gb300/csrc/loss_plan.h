@@ -15,7 +15,6 @@ struct TilePlan {
     int32_t pair;     // CTA pairs
     int32_t width;    // columns of a tile
     int32_t bk;       // k per stage
-    int32_t bufs;     // staging buffers of an epilogue warp
     int32_t m_tiles, n_tiles, splits, group_m;
     int32_t a_rows;   // rows of A's box (k-major)
     int32_t a_bytes, stage_bytes, num_stages, smem_bytes, tmem_cols, grid;
@@ -31,7 +30,6 @@ struct LossPlan {
     int32_t parts;       // forward: statistics per row
     int32_t sum_splits;  // backward: shares of dX's reduction,
     int32_t sum_width;   // ... and its tiles' columns
-    int64_t pitch;       // of the gathered rows
     // workspace, in bytes from its start
     int64_t header, index, flags, entropy, sorted, weights, gathered, stats, grad, sums, bytes;
 };
@@ -41,8 +39,8 @@ struct LossPlan {
 TilePlan plan_logits(int64_t T, int64_t N, int64_t K, bool b_mn, bool stats, int num_sms, int max_pairs);
 // Sums of dX (T x N) in `splits` shares, tiles of `width`.
 TilePlan plan_sum(int64_t T, int64_t N, int splits, int width, bool b_mn, int num_sms, int max_pairs);
-// dW (M x N, reduction T).
-TilePlan plan_weight(int64_t M, int64_t N, int64_t T, int num_sms, int max_pairs);
+// dW (M x N).
+TilePlan plan_weight(int64_t M, int64_t N, int num_sms, int max_pairs);
 
 // k: words of a teacher per row, 0: targets.
 LossPlan plan_loss(int64_t T, int64_t V, int64_t D, int64_t k, bool gradient);

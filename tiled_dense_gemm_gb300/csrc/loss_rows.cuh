@@ -115,15 +115,13 @@ struct RowsParams {
     int32_t T, D;
     const uint16_t* X;
     int64_t ldx;
-    uint16_t* gathered;     // (T, pitch)
+    uint16_t* gathered;     // (T, D)
     int32_t* index;         // the rows in use, then the others
     RowsHeader* rows;
     const float* dloss;     // null: no scale wanted
     int64_t dloss_stride;
     float grad_scale;
     float top;              // what the largest |dloss grad_scale| is scaled to
-    int32_t pitch;          // of the copy: D rounded up to 64
-    int32_t always;         // gather even if all rows are in use (X's pitch is not one of 128 bytes)
     int32_t* err;
 };
 
@@ -182,7 +180,7 @@ __global__ void __launch_bounds__(kRowsThreads) loss_rows_kernel(const __grid_co
         total += part[1][j];
     }
     __syncthreads();
-    const bool gather = total < p.T || p.always;
+    const bool gather = total < p.T;
     for (int32_t b = r0; b < r1; b += kRowsThreads) {
         const int32_t t = b + i;
         bool in = false;
@@ -205,7 +203,7 @@ __global__ void __launch_bounds__(kRowsThreads) loss_rows_kernel(const __grid_co
                 const int32_t to = where[j];
                 if (to < 0) continue;
                 const uint4* const src = reinterpret_cast<const uint4*>(p.X + (int64_t)(b + j) * p.ldx);
-                uint4* const dst = reinterpret_cast<uint4*>(p.gathered + (int64_t)to * p.pitch);
+                uint4* const dst = reinterpret_cast<uint4*>(p.gathered + (int64_t)to * p.D);
                 for (int32_t c0 = lane; c0 < vecs; c0 += 8 * 32) {
                     uint4 x[8];
 #pragma unroll
@@ -224,8 +222,8 @@ __global__ void __launch_bounds__(kRowsThreads) loss_rows_kernel(const __grid_co
     // what the later kernels read of the rows
     if (gather) {
         const int32_t end = min(p.T, (total + kRowPad - 1) / kRowPad * kRowPad);
-        const int64_t n = (int64_t)(end - total) * (p.pitch / 8);
-        uint4* const dst = reinterpret_cast<uint4*>(p.gathered + (int64_t)total * p.pitch);
+        const int64_t n = (int64_t)(end - total) * (p.D / 8);
+        uint4* const dst = reinterpret_cast<uint4*>(p.gathered + (int64_t)total * p.D);
         for (int64_t c = i; c < n; c += kRowsThreads) dst[c] = make_uint4(0, 0, 0, 0);
     }
     float top = 0.0f;
@@ -261,7 +259,7 @@ __global__ void __launch_bounds__(kRowsThreads) loss_mask_kernel(const __grid_co
         if (y >= p.limit && i == 0) atomicCAS(p.err + 1, 0, (int32_t)rg::kBadIds);
         const bool in = y >= 0 && y < p.limit;
         const uint4* const src = reinterpret_cast<const uint4*>(p.X + (int64_t)t * p.ldx);
-        uint4* const dst = reinterpret_cast<uint4*>(p.gathered + (int64_t)t * p.pitch);
+        uint4* const dst = reinterpret_cast<uint4*>(p.gathered + (int64_t)t * p.D);
         for (int32_t c = i; c < vecs; c += kRowsThreads) dst[c] = in ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
     }
     if (blockIdx.x == 0 && i < 32) {
