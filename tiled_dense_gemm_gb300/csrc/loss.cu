@@ -71,11 +71,21 @@ static int launch_tiles(DeviceState& d, const TilePlan& t, const LossMaps& m, co
     return launch(fn, t.grid, kThreads, (size_t)t.smem_bytes, kPair ? 2 : 1, st, m, q);
 }
 
+// Up to so many rows (four row tiles of a pair) the weights are read from memory,
+// and their gradients written, with lines that leave L2 first: they are met once
+// or by CTAs that run together, and otherwise push out what is reused (us, without
+// / with; 32768 words of 1024: one row 17.9 / 16.5, gradients 48.6 / 46.2; 65536 of
+// 2048: 16 rows 51.6 / 45.4, 152 / 150; 100 rows 53.7 / 49.9, 161 / 153; 300 98 /
+// 93, 258 / 252; 32768 of 1024, 1000 rows: 57 / 56, 151.5 / 149.9; but 65536 of
+// 4096, 4096 rows: 1280 / 1302, 3974 / 4050).
+constexpr int64_t kStreamRows = 1024;
+
 template <int kMode>
-static int launch_mode(DeviceState& d, const TilePlan& t, const LossMaps& m, LossParams& q, cudaStream_t st) {
+static int launch_mode(DeviceState& d, const TilePlan& t, const LossMaps& m, LossParams& q, int64_t rows, cudaStream_t st) {
     q.width = t.width;
     q.bk = t.bk;
     q.warm = 8;
+    q.once = rows <= kStreamRows;
     q.n_tiles = t.n_tiles;
     q.group_m = t.group_m;
     q.splits = t.splits;
@@ -214,7 +224,7 @@ static int run_forward(const Call& c, const LossPlan& p, DeviceState& d) {
         if (rc != GEMM_OK) return rc;
         m.b[1] = m.b[0];
         m.d = m.a[0];
-        rc = launch_mode<kStats>(d, t, m, q, c.st);
+        rc = launch_mode<kStats>(d, t, m, q, T, c.st);
         if (rc != GEMM_OK) return rc;
         CombineParams o;
         memset(&o, 0, sizeof(o));
@@ -293,7 +303,7 @@ static int run_backward(const Call& c, const LossPlan& p, DeviceState& d) {
             if (rc == GEMM_OK)
                 rc = encode_rows(&m.d, G, (uint64_t)p.piece, (uint64_t)c.T, (uint64_t)p.piece, 32, 0, c.bf16);
             m.b[1] = m.b[0];
-            if (rc == GEMM_OK) rc = launch_mode<kGrad>(d, t, m, q, c.st);
+            if (rc == GEMM_OK) rc = launch_mode<kGrad>(d, t, m, q, c.T, c.st);
             if (rc == GEMM_OK && p.masked && p0 == 0) rc = run_rows(c, p, 0, c.T, d);
             if (rc != GEMM_OK) return rc;
         }
@@ -320,7 +330,7 @@ static int run_backward(const Call& c, const LossPlan& p, DeviceState& d) {
             if (rc == GEMM_OK) rc = encode_sums(&m.d, sums, c.D, c.T, p.sum_splits);
             m.a[1] = m.a[0];
             m.b[1] = m.b[0];
-            if (rc == GEMM_OK) rc = launch_mode<kSum>(d, t, m, q, c.st);
+            if (rc == GEMM_OK) rc = launch_mode<kSum>(d, t, m, q, c.T, c.st);
             if (rc != GEMM_OK) return rc;
         }
         if (c.dW) {  // dW[piece] = G^T X, or its transpose
@@ -351,7 +361,7 @@ static int run_backward(const Call& c, const LossPlan& p, DeviceState& d) {
             if (rc == GEMM_OK)
                 rc = c.nk ? encode_rows(&m.d, c.dW, (uint64_t)c.D, (uint64_t)c.V, (uint64_t)c.D, 32, 0, c.bf16)
                           : encode_rows(&m.d, c.dW, (uint64_t)c.V, (uint64_t)c.D, (uint64_t)c.V, 32, 0, c.bf16);
-            if (rc == GEMM_OK) rc = launch_mode<kWeight>(d, t, m, q, c.st);
+            if (rc == GEMM_OK) rc = launch_mode<kWeight>(d, t, m, q, c.T, c.st);
             if (rc != GEMM_OK) return rc;
         }
     }

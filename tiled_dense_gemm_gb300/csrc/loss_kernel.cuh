@@ -89,6 +89,7 @@ struct LossParams {
     // before.  It waits for its predecessor before it ends, so that its end says
     // that all before it is done.
     int32_t late;
+    int32_t once;          // the weights' lines (B; kWeight: its output's) leave L2 first
     int32_t warm;          // single CTAs: k-blocks of B asked for in L2 ahead
     uint32_t tmem_cols;    // allocated; half per accumulator
     int32_t bf16;
@@ -150,6 +151,41 @@ __device__ __forceinline__ float scale_of(float top, float grad_scale, float lar
 
 __device__ __forceinline__ void st_shared_u16(uint32_t addr, uint16_t x) {
     asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(x) : "memory");
+}
+
+// Tensor copies global -> shared with an L2 policy; of a pair's, `bar` is the leader's.
+template <bool kPair>
+__device__ __forceinline__ void load_2d_hint(uint32_t dst, const CUtensorMap* m, uint32_t bar, int32_t x, int32_t y,
+                                             uint64_t policy) {
+    if constexpr (kPair)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+            " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y),
+            "l"(policy)
+            : "memory");
+    else
+        tma_load_2d_hint(dst, m, bar, x, y, policy);
+}
+
+template <bool kPair>
+__device__ __forceinline__ void load_3d_hint(uint32_t dst, const CUtensorMap* m, uint32_t bar, int32_t x, int32_t y,
+                                             int32_t z, uint64_t policy) {
+    if constexpr (kPair)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+            " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x),
+            "r"(y), "r"(z), "l"(policy)
+            : "memory");
+    else
+        rg::load_3d_hint(dst, m, bar, x, y, z, policy);
+}
+
+__device__ __forceinline__ void store_2d_hint(const CUtensorMap* m, uint32_t src, int32_t x, int32_t y, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group.L2::cache_hint [%0, {%2, %3}], [%1], %4;" ::"l"(
+            reinterpret_cast<uint64_t>(m)),
+        "r"(src), "r"(x), "r"(y), "l"(policy)
+        : "memory");
 }
 
 // 3-D tiled add shared -> global (bulk-group completion).
@@ -410,6 +446,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t s = 0, ph = 0;
             int32_t issued = 0;
             bool ok = true;
+            const bool once = kMode != kWeight && !is_a && q.once;
+            const uint64_t policy = l2_policy_evict_first();
             const bool mn = is_a ? q.a_mn : q.b_mn, one = is_a ? q.a_3d : q.b_3d;
             // copies of a stage where it takes several, and the bytes of one: 64 k of
             // all rows, or 64 rows of all k
@@ -433,10 +471,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!kPair && is_a && issued == q.test_drop_kb && q.test_drop_kb > 0) {
                         // (test hook: not copied)
                     } else if (one) {
-                        rg::load_3d<kPair>(dst, m, bar, 0, mn ? k0 : r0, (mn ? r0 : k0) / 64);
+                        if (once)
+                            load_3d_hint<kPair>(dst, m, bar, 0, mn ? k0 : r0, (mn ? r0 : k0) / 64, policy);
+                        else
+                            rg::load_3d<kPair>(dst, m, bar, 0, mn ? k0 : r0, (mn ? r0 : k0) / 64);
                     } else {
-                        for (int32_t j = 0; j < copies; ++j)
-                            rg::load_2d<kPair>(dst + (uint32_t)j * piece, m, bar, mn ? r0 + 64 * j : k0 + 64 * j, mn ? k0 : r0);
+                        for (int32_t j = 0; j < copies; ++j) {
+                            const uint32_t to = dst + (uint32_t)j * piece;
+                            const int32_t x = mn ? r0 + 64 * j : k0 + 64 * j, y = mn ? k0 : r0;
+                            if (once)
+                                load_2d_hint<kPair>(to, m, bar, x, y, policy);
+                            else
+                                rg::load_2d<kPair>(to, m, bar, x, y);
+                        }
                     }
                     if (++s == S) {
                         s = 0;
@@ -713,7 +760,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        tma_store_2d(&maps.d, staging, col + q.d_col, row0 + q.d_row);
+                        if (kMode == kWeight && q.once)
+                            store_2d_hint(&maps.d, staging, col + q.d_col, row0 + q.d_row, l2_policy_evict_first());
+                        else
+                            tma_store_2d(&maps.d, staging, col + q.d_col, row0 + q.d_row);
                         bulk_commit_group();
                     }
                 }
