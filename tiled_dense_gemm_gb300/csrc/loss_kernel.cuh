@@ -11,11 +11,11 @@
 //   kWeight  dW[piece] = G^T X
 //
 // One kernel, four epilogues: D = A B^T in tiles of 128 rows x `width` columns
-// per CTA, or 256 x `width` per CTA pair, over k-blocks of 64.  An operand's
+// per CTA, or 256 x `width` per CTA pair, over k-blocks of 64 or 128.  An operand's
 // reduction index is contiguous ("k-major": boxes of 64 k x rows) or its rows'
-// index is ("mn-major": chunks of 64 rows x 64 k), as the matrices are stored;
-// nothing is transposed in memory.  Rows of X are A's rows in kStats, kGrad and
-// kSum, so that a row's logits sit in one lane of tensor memory: the running
+// index is ("mn-major": chunks of 64 rows x the k-block), as the matrices are
+// stored; nothing is transposed in memory.  Rows of X are A's rows in kStats, kGrad
+// and kSum, so that a row's logits sit in one lane of tensor memory: the running
 // maximum and sum of the softmax never leave a thread.
 //
 // The rows in use (those with a wanted word) may have been gathered to the
@@ -27,6 +27,22 @@
 // stages, warp 6 B's, warp 1 issues the MMAs, warps 2-5 and 7-10 drain the two
 // accumulators (a quarter of the rows each, every other chunk of 64 columns).
 // Every wait is bounded.
+//
+// What bounds it, and what it measured (the GPU's time alone, in a CUDA graph
+// whose inputs rotate beyond L2):
+//   up to 128 rows: the weights' way from memory.  64 rows, 131072 words of 4096:
+//     162 us, 6.6 TB/s of weights; 16 rows, 65536 of 2048: 45 us; one row, 32000
+//     of 1024: 16.0 us, of which 6.4 are left with next to no words.  (Boxes of 256
+//     k: 5-15% slower; tiles of 64 to 112 words 5-60%.)  The gradients pass the
+//     weights three times (G, dX, dW): 16 rows, 65536 of 2048: 150 us.
+//   many rows, alone: bytes from L2 into the multiprocessors, 13.4-14.2 TB/s in
+//     every product (a pair takes in 64 KB per 512 clocks of the tensor core, which
+//     at 1.8 GHz would be 17.5 TB/s): the tensor pipe is active 72-81% of the time.
+//   many rows, back to back: the power cap.  8192 rows, 131072 words of 4096: 5.1-
+//     5.3 ms, 1660-1730 TFLOP/s at 1.5 GHz, what the library product sustains; the
+//     gradients of 4096 rows 7.7-7.9 ms.
+//   rows whose pitch is not a multiple of 128 bytes cost a second line per box
+//     row: 50021 words of 2056, 1800 of 3000 rows in use, 262 (bfloat16) - 280 us.
 #pragma once
 
 #include "ragged_kernel.cuh"
@@ -263,8 +279,8 @@ __device__ __forceinline__ float pick(const float (&v)[kSize], int32_t at) {
 // kStats: the reduction in parts of at most this many k, each in an accumulator
 // of its own, added up in registers.  The tensor core truncates its sums in 32
 // bits, 16 products at a time, always towards zero: over 4096 that was 2.4e-6 of
-// the losses (against 6e-7 of a sum that rounds), in parts of 1024 it is
-// PLACEHOLDER.  The epilogue's warps have the time.
+// the losses (6e-7 for a sum that rounds), in parts of 1024 it is 5.4e-7.  The
+// epilogue's warps have the time.
 constexpr int32_t kPart = 1024;
 
 __device__ __forceinline__ int32_t part_end(int32_t blocks, int32_t part, int32_t parts) { return part * blocks / parts; }
@@ -377,7 +393,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (!kPair && kMode != kWeight) {
         // Few rows: the weights' way from memory is all there is, so the first item's
         // are asked for in L2 before the kernel before is waited for (a line that it
-        // still writes is current there).  PLACEHOLDER
+        // still writes is current there): one row, 32000 words of 1024, 19.0 us without,
+        // 17.6 with.
         if (warp == 6 && lane == 0) {
             const uint32_t split = worker / (uint32_t)q.n_tiles, nt = worker - split * (uint32_t)q.n_tiles;
             const int32_t blocks = (q.K + q.bk - 1) / q.bk;

@@ -30,6 +30,7 @@ struct LossPlan {
     int32_t parts;       // forward: statistics per row
     int32_t sum_splits;  // backward: shares of dX's reduction,
     int32_t sum_width;   // ... and its tiles' columns
+    int64_t pitch;       // of the rows' copy
     // workspace, in bytes from its start
     int64_t header, index, flags, entropy, sorted, weights, gathered, stats, grad, sums, bytes;
 };

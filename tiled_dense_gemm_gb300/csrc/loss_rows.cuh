@@ -90,6 +90,7 @@ __global__ void __launch_bounds__(32 * kTeacherWarps) loss_teacher_kernel(const 
             if (q != 0.0f) h += q * (x - log_sum);
             const int32_t mine = key[j];
             int32_t at = 0;
+#pragma unroll 4
             for (int32_t i = 0; i < padded; i += 4) {
                 const int4 o = *reinterpret_cast<const int4*>(key + i);
                 at += (o.x < mine || (o.x == mine && i < j)) + (o.y < mine || (o.y == mine && i + 1 < j)) +
@@ -115,13 +116,15 @@ struct RowsParams {
     int32_t T, D;
     const uint16_t* X;
     int64_t ldx;
-    uint16_t* gathered;     // (T, D)
+    uint16_t* gathered;     // (T, pitch)
     int32_t* index;         // the rows in use, then the others
     RowsHeader* rows;
     const float* dloss;     // null: no scale wanted
     int64_t dloss_stride;
     float grad_scale;
     float top;              // what the largest |dloss grad_scale| is scaled to
+    int32_t pitch;          // of the copy: D rounded up to 64
+    int32_t always;         // gather even if all rows are in use
     int32_t* err;
 };
 
@@ -180,7 +183,7 @@ __global__ void __launch_bounds__(kRowsThreads) loss_rows_kernel(const __grid_co
         total += part[1][j];
     }
     __syncthreads();
-    const bool gather = total < p.T;
+    const bool gather = total < p.T || p.always;
     for (int32_t b = r0; b < r1; b += kRowsThreads) {
         const int32_t t = b + i;
         bool in = false;
@@ -203,7 +206,7 @@ __global__ void __launch_bounds__(kRowsThreads) loss_rows_kernel(const __grid_co
                 const int32_t to = where[j];
                 if (to < 0) continue;
                 const uint4* const src = reinterpret_cast<const uint4*>(p.X + (int64_t)(b + j) * p.ldx);
-                uint4* const dst = reinterpret_cast<uint4*>(p.gathered + (int64_t)to * p.D);
+                uint4* const dst = reinterpret_cast<uint4*>(p.gathered + (int64_t)to * p.pitch);
                 for (int32_t c0 = lane; c0 < vecs; c0 += 8 * 32) {
                     uint4 x[8];
 #pragma unroll
@@ -217,15 +220,16 @@ __global__ void __launch_bounds__(kRowsThreads) loss_rows_kernel(const __grid_co
         }
         __syncthreads();
     }
-    if (blockIdx.x != gridDim.x - 1) return;
-    // the last block: zeros up to the end of the reduction's last k-block, and
-    // what the later kernels read of the rows
+    // zeros up to the end of the reduction's last k-block
     if (gather) {
         const int32_t end = min(p.T, (total + kRowPad - 1) / kRowPad * kRowPad);
-        const int64_t n = (int64_t)(end - total) * (p.D / 8);
-        uint4* const dst = reinterpret_cast<uint4*>(p.gathered + (int64_t)total * p.D);
-        for (int64_t c = i; c < n; c += kRowsThreads) dst[c] = make_uint4(0, 0, 0, 0);
+        for (int32_t r = total + (int32_t)blockIdx.x; r < end; r += (int32_t)gridDim.x) {
+            uint4* const dst = reinterpret_cast<uint4*>(p.gathered + (int64_t)r * p.pitch);
+            for (int32_t c = i; c < p.pitch / 8; c += kRowsThreads) dst[c] = make_uint4(0, 0, 0, 0);
+        }
     }
+    // the last block: what the later kernels read of the rows
+    if (blockIdx.x != gridDim.x - 1) return;
     float top = 0.0f;
     if (p.dloss) {
         if (p.dloss_stride == 0) {
@@ -259,7 +263,7 @@ __global__ void __launch_bounds__(kRowsThreads) loss_mask_kernel(const __grid_co
         if (y >= p.limit && i == 0) atomicCAS(p.err + 1, 0, (int32_t)rg::kBadIds);
         const bool in = y >= 0 && y < p.limit;
         const uint4* const src = reinterpret_cast<const uint4*>(p.X + (int64_t)t * p.ldx);
-        uint4* const dst = reinterpret_cast<uint4*>(p.gathered + (int64_t)t * p.D);
+        uint4* const dst = reinterpret_cast<uint4*>(p.gathered + (int64_t)t * p.pitch);
         for (int32_t c = i; c < vecs; c += kRowsThreads) dst[c] = in ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
     }
     if (blockIdx.x == 0 && i < 32) {
