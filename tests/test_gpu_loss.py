@@ -375,6 +375,31 @@ def test_more_rows_than_a_block():
     binding.check_device_error()
 
 
+def test_many_words_and_blocks_of_rows():
+    """A vocabulary so large that a forward call's rows go in blocks of 2048, the last one shorter."""
+    T, V, D = 2048 + 2048 + 77, 1 << 20, 16
+    x, w = _big(T, V, D, "bf16", "nk", 1)
+    y = ref.make_targets(T, V, 3, 0.2).to(DEV)
+    loss, lse = binding.gemm_relu_xent(x, w, y, b_layout="nk")
+    ids, logits = (t.to(DEV) for t in ref.make_words(T, V, 3, 4, 0.2))
+    soft, lse_tau = binding.gemm_relu_distill(x, w, ids, logits, 2.0, b_layout="nk")
+    binding.check_device_error()
+    at = torch.tensor([0, 1, 1500, 2047, 2048, 2100, 4095, 4096, T - 1], device=DEV)
+    z = x[at].double() @ w.double().T
+    live = y[at] >= 0
+    want = torch.where(live, torch.logsumexp(z, 1), 0.0)
+    assert (lse[at].double() - want).abs().max() < 1e-4
+    zy = z.gather(1, y[at].clamp(min=0).long()[:, None])[:, 0]
+    assert (loss[at].double() - torch.where(live, want - zy, 0.0)).abs().max() < 1e-4
+    live = (ids[at] >= 0).any(1)
+    assert (lse_tau[at].double() - torch.where(live, torch.logsumexp(z / 2, 1), 0.0)).abs().max() < 1e-4
+    has = ids[at] >= 0
+    q = torch.softmax(torch.where(has, logits[at].double() / 2, -1e30), 1) * has
+    p = (torch.log_softmax(z / 2, 1)).gather(1, ids[at].clamp(min=0).long())
+    want = 4 * (torch.xlogy(q, q) - q * p).sum(1)
+    assert (soft[at].double() - torch.where(live, want, 0.0)).abs().max() < 1e-3
+
+
 def test_weights_past_32_bit_offsets():
     """2.5e9 weights: the words at the end count as those at the start."""
     T, V, D = 3, 600001, 4096
@@ -432,7 +457,9 @@ def test_two_streams_and_graphs():
     # ... and by the stream argument
     loss, lse = binding.gemm_relu_xent(sets[0][0], w, sets[0][1], b_layout="nk", stream=streams[0])
     raw = binding.gemm_relu_xent(sets[0][0], w, sets[0][1], b_layout="nk", stream=streams[1].cuda_stream)
+    default = binding.gemm_relu_xent(sets[0][0], w, sets[0][1], b_layout="nk", stream=0)
     torch.cuda.synchronize()
+    assert torch.equal(default[0], want[0][0])
     assert torch.equal(loss, want[0][0]) and torch.equal(lse, want[0][1]) and torch.equal(raw[0], loss)
     for i in range(2):
         for o in got[i]:

@@ -95,8 +95,9 @@ def test_workspace(gemm_lib):
     # the logits of 8192 rows would be 2 GiB: the gradients take a piece of them and dX in 32 bits
     assert size(8192, 131072, 4096, 0, 1) < (1 << 29) + 2 * 8192 * 4096 * 4
     assert size(8192, 131072, 4096, 0, 0) < 1 << 29
-    # a forward call's rows come in blocks
+    # a forward call's rows come in blocks, shorter ones for many words
     assert size(1 << 20, 131072, 4096, 0, 0) == size(16384, 131072, 4096, 0, 0)
+    assert size(1 << 20, 1 << 20, 4096, 0, 0) < 2 * size(2048, 1 << 20, 4096, 0, 0)
 
 
 def test_binding_without_a_gpu(gemm_lib):

@@ -11,7 +11,9 @@ constexpr int64_t kSmem = 227 * 1024;
 constexpr int64_t kCtrl = 2048;  // control block and alignment
 constexpr int64_t kStagingBytes = 8 * 4096;
 constexpr int kMaxRing = 8;
-constexpr int64_t kBlockRows = 16384;         // of a forward call's block
+constexpr int64_t kStatBytes = 384ll << 20;   // of a forward call's statistics: its rows go in blocks,
+constexpr int64_t kLeastRows = 2048;          // ... of at least so many and
+constexpr int64_t kMostRows = 16384;          // at most so many rows
 constexpr int64_t kGradBytes = 512ll << 20;   // of G
 constexpr int64_t kPlanSms = 152;             // the device's (plans fix the workspace before one is asked)
 
@@ -110,7 +112,10 @@ TilePlan plan_weight(int64_t M, int64_t N, int num_sms, int max_pairs) {
 
 LossPlan plan_loss(int64_t T, int64_t V, int64_t D, int64_t k, bool gradient) {
     LossPlan p = {};
-    p.rows = gradient ? T : std::min(T, kBlockRows);
+    // (statistics of the narrowest tiles)
+    const int64_t parts = ceil_div(V, 64);
+    const int64_t most_rows = std::max(kLeastRows, std::min(kMostRows, kStatBytes / (12 * parts) / 256 * 256));
+    p.rows = gradient || T <= most_rows ? T : round_up(ceil_div(T, ceil_div(T, most_rows)), 256);
     // forward: rows in use are gathered where that saves tiles
     p.gather = T > 128;
     p.masked = gradient && !p.gather;
@@ -134,10 +139,8 @@ LossPlan plan_loss(int64_t T, int64_t V, int64_t D, int64_t k, bool gradient) {
     p.pitch = round_up(D, 64);
     if (p.gather || p.masked) p.gathered = take(2 * rows * p.pitch);
     if (!gradient) {
-        // (of the narrowest tiles)
-        p.parts = (int32_t)ceil_div(V, 64);
-        if (ceil_div(V, 64) * ceil_div(rows, 128) > 2000000000ll) p.status = GEMM_ERR_TOO_LARGE;
-        p.stats = take(4 * 3 * round_up(rows, 32) * p.parts);
+        if (parts * ceil_div(rows, 128) > 2000000000ll) p.status = GEMM_ERR_TOO_LARGE;
+        p.stats = take(12 * round_up(rows, 32) * parts);
     } else {
         const int64_t most = std::max<int64_t>(256, kGradBytes / (2 * rows) / 256 * 256);
         p.piece = round_up(ceil_div(V, ceil_div(V, most)), 256);

@@ -27,7 +27,6 @@ struct LossPlan {
     int32_t pieces;
     int32_t gather;      // the rows in use are counted, and gathered if some are not
     int32_t masked;      // backward, up to 128 rows: a copy of X with zeros for those that are not
-    int32_t parts;       // forward: statistics per row
     int32_t sum_splits;  // backward: shares of dX's reduction,
     int32_t sum_width;   // ... and its tiles' columns
     int64_t pitch;       // of the rows' copy
