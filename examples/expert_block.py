@@ -4,10 +4,13 @@
     u_e = ReLU(h_rows-of-e up_e),  y_e = u_e down_e   top-k experts e per row
     y   = sum of its experts' y_e, weighted by the router
 
+    z   = y out^T, a cross entropy with the rows' next words, or with a teacher's best ones
+
 Serving runs ``forward``; ``backward`` gives the gradients of the experts'
-weights and of h for a training step.  The products are the library's; the
-routing (top-k, sort, gather, weighted sum) is plain torch on the same stream,
-and no step reads a size back to the host.
+weights and of h for a training step, ``Head`` the losses over the vocabulary
+and the y gradient that the step begins with.  The products are the library's;
+the routing (top-k, sort, gather, weighted sum) is plain torch on the same
+stream, and no step reads a size back to the host.
 
     python examples/expert_block.py [--rows 4096] [--steps 10]
 """
@@ -76,6 +79,27 @@ class ExpertBlock:
         return dh.to(dy.dtype), d_up, d_down
 
 
+class Head:
+    """Output weights (words, d) and the losses over them; targets and a
+    teacher's ids are negative where a row has none."""
+
+    def __init__(self, d: int, words: int, dtype=torch.bfloat16, device="cuda", seed: int = 1):
+        gen = torch.Generator(device=device).manual_seed(seed)
+        self.out = (torch.randn(words, d, generator=gen, device=device) * d ** -0.5).to(dtype)
+
+    def step(self, y, targets):
+        """(mean loss, its gradients of y and of the output weights)."""
+        loss, lse = fw.gemm_relu_xent(y, self.out, targets, b_layout="nk")
+        share = 1.0 / (targets >= 0).sum().clamp(min=1).float().reshape(1)
+        return (loss * share).sum(), *fw.gemm_relu_xent_grad(y, self.out, targets, lse, share, b_layout="nk")
+
+    def distill(self, y, ids, logits, temperature: float = 1.0):
+        """The same with a teacher's best words of each row."""
+        loss, lse = fw.gemm_relu_distill(y, self.out, ids, logits, temperature, b_layout="nk")
+        share = 1.0 / (ids >= 0).any(dim=1).sum().clamp(min=1).float().reshape(1)
+        return (loss * share).sum(), *fw.gemm_relu_distill_grad(y, self.out, ids, logits, lse, share, temperature, b_layout="nk")
+
+
 def main():
     p = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     p.add_argument("--rows", type=int, default=4096)
@@ -86,14 +110,21 @@ def main():
     p.add_argument("--top-k", type=int, default=2)
     p.add_argument("--adapters", type=int, default=16)
     p.add_argument("--rank", type=int, default=16)
+    p.add_argument("--words", type=int, default=32768)
     a = p.parse_args()
     block = ExpertBlock(a.width, a.hidden, a.experts, a.top_k, a.adapters, a.rank)
     gen = torch.Generator(device="cuda").manual_seed(1)
     x = torch.randn(a.rows, a.width, generator=gen, device="cuda").to(torch.bfloat16)
-    dy = torch.randn(a.rows, a.width, generator=gen, device="cuda").to(torch.bfloat16)
+    head = Head(a.width, a.words)
+    targets = torch.randint(0, a.words, (a.rows,), generator=gen, device="cuda", dtype=torch.int32)
     ids = torch.randint(-1, a.adapters, (a.rows,), generator=gen, device="cuda", dtype=torch.int32)
-    for name, step in (("forward", lambda: block.forward(x, ids)),
-                       ("forward + backward", lambda: block.backward(dy, block.forward(x, ids)[1]))):
+
+    def train():
+        y, kept = block.forward(x, ids)
+        loss, dy, d_out = head.step(y, targets)
+        return loss, d_out, block.backward(dy, kept)
+
+    for name, step in (("forward", lambda: block.forward(x, ids)), ("forward, loss and backward", train)):
         for _ in range(3):
             step()
         begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)

@@ -39,7 +39,7 @@ typedef enum {
     GEMM_ERR_CUDA = 7,               /* another CUDA runtime error */
     GEMM_ERR_TOO_LARGE = 8,          /* gemm_relu_noalloc: problem outside its fixed scratch; ragged
                                         products: more tiles than 32 bits count */
-    GEMM_ERR_INDEX = 9               /* offsets or ids outside their range (reported later) */
+    GEMM_ERR_INDEX = 9               /* offsets, ids or targets outside their range (reported later) */
 } gemm_status_t;
 
 /* Largest accepted M, N or K (TMA coordinates are signed 32-bit). */
@@ -129,8 +129,9 @@ int gemm_relu_host(const void* A_host, const void* B_host, void* C_host,
  * clears the one it reports (of both, the timeout first and the indexes at the
  * next check).  Returns GEMM_ERR_TIMEOUT if a kernel of this library gave up a
  * bounded wait since the last check (the split-K counters are then reset),
- * GEMM_ERR_INDEX if a ragged product met offsets or ids outside their range,
- * GEMM_ERR_CUDA if the stream reports a CUDA error, else GEMM_OK.
+ * GEMM_ERR_INDEX if a ragged product or a loss met offsets, ids or targets
+ * outside their range, GEMM_ERR_CUDA if the stream reports a CUDA error, else
+ * GEMM_OK.
  *
  * Every device wait of the kernels is bounded (2 s plus 2 us per k-block);
  * a CTA whose wait runs out records the error, stops its other roles, lets
@@ -144,7 +145,7 @@ int gemm_relu_host(const void* A_host, const void* B_host, void* C_host,
  * k-blocks of the plan) or a plan that runs in clusters is refused with
  * GEMM_ERR_INVALID_ARG.  The grouped products take the hook too where their
  * plans are of single CTAs without clusters (gemm_relu_grouped_dw: k = 0, the
- * first row block).
+ * first row block), and gemm_relu_xent and gemm_relu_distill with up to 128 rows.
  */
 int gemm_relu_check_device_error(void* stream);
 

@@ -608,6 +608,45 @@ def test_a_step_of_both_losses():
         assert (got - want).norm() <= 4 * 2.0 ** -8 * want.norm()
 
 
+def test_example_step():
+    """The example's step, block and head, against 64-bit torch with autograd; what the library rounds on the
+    way (y, g, dz, du and the gradients themselves) sets the tolerance: their unit roundoff, a few times over."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "expert_block.py")
+    spec = importlib.util.spec_from_file_location("expert_block", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    for T in (6, 300):
+        block, head_ = mod.ExpertBlock(136, 264, 8, 2, 4, 8, dtype=torch.float16, device=DEV, seed=T), mod.Head(136, 500, torch.float16, DEV)
+        x = normal((T, 136), 1, "f16")
+        y, kept = block.forward(x, torch.zeros(T, dtype=torch.int32, device=DEV))
+        targets = ref.make_targets(T, 500, 2, 0.3).to(DEV)
+        ids, logits = (t.to(DEV) for t in ref.make_words(T, 500, 5, 3, 0.2))
+        for soft in (False, True):
+            loss, dy, d_out = head_.distill(y, ids, logits, 2.0) if soft else head_.step(y, targets)
+            dh, d_up, d_down = block.backward(dy, kept)
+            binding.check_device_error()
+            y64, out = y.double().requires_grad_(), head_.out.double().requires_grad_()
+            z = y64 @ out.T
+            if soft:
+                has = ids >= 0
+                q = torch.softmax(torch.where(has, logits.double() / 2, -1e30), 1) * has
+                each = 4 * (torch.xlogy(q, q) - q * torch.log_softmax(z / 2, 1).gather(1, ids.clamp(min=0).long())).sum(1)
+                n = has.any(1).sum()
+            else:
+                n = (targets >= 0).sum()
+                each = torch.where(targets >= 0, torch.logsumexp(z, 1) - z.gather(1, targets.clamp(min=0).long()[:, None])[:, 0], 0.0)
+            want = each.sum() / n
+            want.backward()
+            assert abs(loss.double() - want) < 1e-5 * abs(want)
+            for got, grad in ((dy, y64.grad), (d_out, out.grad)):
+                # (half of the smallest step per element: gradients of a mean are small numbers in binary16)
+                floor = 2.0 ** -25 * got.numel() ** 0.5
+                assert (got.double() - grad).norm() <= 8 * 2.0 ** -11 * grad.norm() + floor
+            assert all(torch.isfinite(t.float()).all() for t in (dh, d_up, d_down)) and dh.any()
+
+
 @pytest.mark.parametrize("kb", [0, 2])
 def test_timed_out_wait_is_reported_and_the_next_call_is_correct(kb, monkeypatch):
     T, V, D = 50, 3000, 264
