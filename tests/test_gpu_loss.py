@@ -183,6 +183,21 @@ def test_many_words(k):
     distill(x, w, ids.to(DEV), logits.to(DEV), 2.0, "nk", f"k {k}, the same words")
 
 
+@pytest.mark.parametrize("T", [30, 260])
+def test_words_in_one_half_of_every_tile(T):
+    """Short reductions and words in every other chunk of 64 columns: one half of the epilogue's warps has all
+    of them to deal with and falls behind the other by several tiles."""
+    V, D, k = 20000, 8, 1024
+    x, w = normal((T, D), 1, "bf16"), head(V, D, "nk", 2, "bf16")
+    rs = np.random.RandomState(3)
+    for first in (0, 64):
+        ids = (rs.randint(0, V // 128, (T, k)) * 128 + first + rs.randint(0, 64, (T, k))).astype(np.int32)
+        ids[:, : k // 2] = first + rs.randint(0, 64, (T, k // 2))  # half of them in the first tile
+        ids = torch.from_numpy(np.minimum(ids, V - 1))
+        logits = torch.from_numpy(rs.standard_normal((T, k)).astype(np.float32))
+        distill(x, w, ids.to(DEV), logits.to(DEV), 1.5, "nk", f"T {T} from {first}")
+
+
 def test_teacher_logits():
     """Logits of -infinity have no weight; of the type's lowest value, alone or with others, they do as any;
     16-bit types, pitches."""

@@ -374,7 +374,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&ctrl->tmem_empty[b]), (kPair ? 2u : 1u) * 8u);
         }
         mbar_init(smem_u32(&ctrl->final_bar), 1);
-        for (int b = 0; b < 8; ++b) mbar_init(smem_u32(&ctrl->extra[b]), 1);
+        for (int b = 0; b < 8; ++b) {
+            mbar_init(smem_u32(&ctrl->extra[b]), 1);
+            mbar_init(smem_u32(&ctrl->peer[b]), 1);
+        }
         ctrl->abort_flag = 0;
         ctrl->ring_s = ctrl->ring_ph = ctrl->ring_lap = 0;
         fence_mbar_init();
@@ -694,21 +697,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                     s_run = fmaf(s_run, exp2_fast(fmaf(m_run, c, off)), (sum[0] + sum[1]) + (sum[2] + sum[3]));
                     m_run = m_new;
                 }
-                // the two halves' as one: the second hands its numbers to the first in one
-                // of two buffers (it is at most one tile ahead: the accumulators of the
-                // tile after that are not filled before the first has read this one's)
+                // The two halves' as one: the second hands its numbers to the first in one
+                // of two buffers.  (It may be two tiles ahead, whose accumulators are
+                // filled once the first has read this tile's, not these numbers: it waits
+                // for the buffer.)
                 float* const hand = reinterpret_cast<float*>(smem + (ring - smem_u32(smem)) + S * stride) + (tile & 1u) * 384u + quarter * 96u + lane;
-                const uint32_t bar = smem_u32(&ctrl->extra[2u * quarter + (tile & 1u)]);
+                const uint32_t given = smem_u32(&ctrl->extra[2u * quarter + (tile & 1u)]);
+                const uint32_t taken = smem_u32(&ctrl->peer[2u * quarter + (tile & 1u)]);
+                const uint32_t phase = (tile >> 1) & 1u;
                 if (half == 1) {
+                    if (!__all_sync(0xffffffffu, wait_phase(taken, phase ^ 1u, ctrl, w, rg::kErrEpi))) break;
                     hand[0] = m_run;
                     hand[32] = s_run;
                     hand[64] = t_run;
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar);
+                    if (lane == 0) mbar_arrive(given);
                 } else {
-                    if (!__all_sync(0xffffffffu, wait_phase(bar, (tile >> 1) & 1u, ctrl, w, rg::kErrEpi))) break;
+                    if (!__all_sync(0xffffffffu, wait_phase(given, phase, ctrl, w, rg::kErrEpi))) break;
                     merge_stats(m_run, s_run, hand[0], hand[32], c);
                     t_run += hand[64];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(taken);
                     if (live) {
                         float* const o = q.stats + (int64_t)k.nt * 3 * q.stats_pitch + r;
                         o[0] = m_run;
