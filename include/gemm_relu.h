@@ -301,9 +301,11 @@ int gemm_relu_adapters(const void* X, const void* W, const void* A, const void* 
 
 /* ---- Losses over a vocabulary ------------------------------------------- */
 
-/* Most rows and words of one call, and most words of a teacher per row. */
+/* Most rows and words of one call, largest width of a row (D), and most words of
+ * a teacher per row. */
 #define GEMM_RELU_MAX_LOSS_ROWS 16777216LL
 #define GEMM_RELU_MAX_WORDS 16777216LL
+#define GEMM_RELU_MAX_LOSS_WIDTH 1048576LL
 #define GEMM_RELU_MAX_TEACHER_WORDS 1024
 
 /* Types of a teacher's logits. */

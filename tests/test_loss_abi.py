@@ -38,7 +38,7 @@ TEACHER = [distill, distill_grad]
 @pytest.mark.parametrize("call", CALLS, ids=lambda f: f.__name__)
 def test_sizes_types_and_layouts(gemm_lib, call):
     L = gemm_lib.lib()
-    for bad in (dict(T=-1), dict(T=(1 << 24) + 1), dict(V=0), dict(V=-8), dict(V=(1 << 24) + 1), dict(D=0), dict(D=-8), dict(D=1 << 31),
+    for bad in (dict(T=-1), dict(T=(1 << 24) + 1), dict(V=0), dict(V=-8), dict(V=(1 << 24) + 1), dict(D=0), dict(D=-8), dict(D=(1 << 20) + 8), dict(D=1 << 31),
                 dict(layout=2), dict(layout=-1), dict(dtype=2), dict(dtype=-1), dict(X=None), dict(W=None), dict(ws=None), dict(size=0), dict(size=100),
                 dict(ldx=0)):
         assert call(L, **bad) == 1, bad

@@ -84,7 +84,6 @@ template <int kMode>
 static int launch_mode(DeviceState& d, const TilePlan& t, const LossMaps& m, LossParams& q, int64_t rows, cudaStream_t st) {
     q.width = t.width;
     q.bk = t.bk;
-    q.warm = 8;
     q.once = rows <= kStreamRows;
     q.n_tiles = t.n_tiles;
     q.group_m = t.group_m;
@@ -377,8 +376,8 @@ static int run_backward(const Call& c, const LossPlan& p, DeviceState& d) {
 // ------------------------------------------------------------------ checks
 
 static int check_sizes(int64_t T, int64_t V, int64_t D, int64_t k) {
-    if (T < 0 || T > GEMM_RELU_MAX_LOSS_ROWS || V < 1 || V > GEMM_RELU_MAX_WORDS || D < 1 || !rt::dim_ok(D) || k < 0 ||
-        k > GEMM_RELU_MAX_TEACHER_WORDS)
+    if (T < 0 || T > GEMM_RELU_MAX_LOSS_ROWS || V < 1 || V > GEMM_RELU_MAX_WORDS || D < 1 ||
+        D > GEMM_RELU_MAX_LOSS_WIDTH || k < 0 || k > GEMM_RELU_MAX_TEACHER_WORDS)
         return GEMM_ERR_INVALID_ARG;
     return D % 8 != 0 ? GEMM_ERR_ALIGNMENT : GEMM_OK;
 }

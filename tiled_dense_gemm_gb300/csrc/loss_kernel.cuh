@@ -60,6 +60,7 @@ constexpr int kThreads = 352;
 constexpr uint32_t kStaging = 4096;  // bytes per epilogue warp
 constexpr int32_t kRowPad = 128;     // rows in use, and G's, end in zeros up to a multiple of this
 constexpr int32_t kNone = 0x7fffffff;
+constexpr int32_t kAhead = 8;        // k-blocks of B asked for in L2 ahead of a launch's turn
 
 // What the device knows of the rows.
 struct RowsHeader {
@@ -106,7 +107,6 @@ struct LossParams {
     // that all before it is done.
     int32_t late;
     int32_t once;          // the weights' lines (B; kWeight: its output's) leave L2 first
-    int32_t warm;          // single CTAs: k-blocks of B asked for in L2 ahead
     uint32_t tmem_cols;    // allocated; half per accumulator
     int32_t bf16;
     int32_t w_row, w_k;    // first word of the piece, added to B's row or to its k
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t split = worker / (uint32_t)q.n_tiles, nt = worker - split * (uint32_t)q.n_tiles;
             const int32_t blocks = (q.K + q.bk - 1) / q.bk;
             const int32_t r0 = (int32_t)nt * q.width + q.w_row, kb0 = (int32_t)((int64_t)split * blocks / q.splits);
-            for (int32_t i = 0; i < q.warm && kb0 + i < blocks; ++i) {
+            for (int32_t i = 0; i < kAhead && kb0 + i < blocks; ++i) {
                 const int32_t k0 = (kb0 + i) * q.bk + q.w_k;
                 if (q.b_3d) {
                     tma_prefetch_3d(&maps.b[0], 0, q.b_mn ? k0 : r0, (q.b_mn ? r0 : k0) / 64);
