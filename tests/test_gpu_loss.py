@@ -501,6 +501,43 @@ def test_two_streams_and_graphs():
     binding.check_device_error()
 
 
+def test_two_threads():
+    """Two host threads, each on its own stream, with calls of several launches between each other's."""
+    import threading
+    V, D = 1003, 136
+    w = head(V, D, "nk", 1, "f16")
+    sets = []
+    for i, T in enumerate((100, 300)):
+        sets.append((normal((T, D), i, "f16"), ref.make_targets(T, V, i, 0.3).to(DEV), dloss_of(T, i)))
+
+    def run(x, y, d):
+        loss, lse = binding.gemm_relu_xent(x, w, y, b_layout="nk")
+        return (loss, lse, *binding.gemm_relu_xent_grad(x, w, y, lse, d, b_layout="nk"))
+
+    want = [run(*s) for s in sets]
+    torch.cuda.synchronize()
+    got, wrong = [[], []], []
+
+    def work(i):
+        try:
+            with torch.cuda.device(DEV), torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    got[i].append(run(*sets[i]))
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # noqa: BLE001
+            wrong.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
+    for i in range(2):
+        assert len(got[i]) == 20 and all(torch.equal(p, q) for o in got[i] for p, q in zip(o, want[i]))
+    binding.check_device_error()
+
+
 def test_results_do_not_change_from_run_to_run():
     for T, V, D in ((3, 5000, 264), (700, 3000, 520)):
         x, w, y = normal((T, D), 1, "bf16"), head(V, D, "nk", 2, "bf16"), ref.make_targets(T, V, 3, 0.3).to(DEV)

@@ -279,9 +279,17 @@ __device__ __forceinline__ float pick(const float (&v)[kSize], int32_t at) {
 // kStats: the reduction in parts of at most this many k, each in an accumulator
 // of its own, added up in registers.  The tensor core truncates its sums in 32
 // bits, 16 products at a time, always towards zero: over 4096 that was 2.4e-6 of
-// the losses (6e-7 for a sum that rounds), in parts of 1024 it is 5.4e-7.  The
-// epilogue's warps have the time.
-constexpr int32_t kPart = 1024;
+// the losses (6e-7 for a sum that rounds).  Pairs: 5.4e-7 in parts of 1024, which
+// cost nothing; parts of 512 3e-7, at 4096 rows, 65536 words of 2048 682 us for
+// 645.  Single CTAs, which wait for memory: 1.3e-7 in parts of 256 (64 rows, 131072
+// words of 4096: 162.1 -> 163.5 us), 9e-8 in parts of 128 (169.4).
+constexpr int32_t kPartPair = 1024, kPartSingle = 256;
+
+template <bool kPair>
+__device__ __forceinline__ int32_t part_count(const LossParams& q) {
+    constexpr int32_t kPart = kPair ? kPartPair : kPartSingle;
+    return (q.K + kPart - 1) / kPart;
+}
 
 __device__ __forceinline__ int32_t part_end(int32_t blocks, int32_t part, int32_t parts) { return part * blocks / parts; }
 
@@ -530,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t a_step = q.a_mn ? 128u : 2u, b_step = q.b_mn ? 128u : 2u;
             const uint64_t a_next = q.a_mn ? 512u : (q.a_bytes / 2) >> 4, b_next = q.b_mn ? 512u : (b_rows * 128u) >> 4;
             const bool two = q.bk == 128;
-            const int32_t parts = kMode == kStats ? (q.K + kPart - 1) / kPart : 1;
+            const int32_t parts = kMode == kStats ? part_count<kPair>(q) : 1;
             uint32_t s = 0, ph = 0, local = 0;
             bool ok = true;
             while (ok && next(k)) {
@@ -634,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float z[2][64];
 #pragma unroll
                 for (int j = 0; j < 64; ++j) z[0][j] = z[1][j] = 0.0f;
-                const int32_t parts = (q.K + kPart - 1) / kPart;
+                const int32_t parts = part_count<kPair>(q);
                 bool ok = true;
 #pragma unroll 1
                 for (int32_t part = 0; part < parts; ++part) {

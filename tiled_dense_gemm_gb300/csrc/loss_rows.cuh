@@ -351,8 +351,11 @@ __global__ void __launch_bounds__(32 * kWarps) loss_combine_kernel(const __grid_
     }
     float loss = 0.0f, lse = 0.0f;
     if (in) {
-        lse = (fabsf(m) == INFINITY ? 0.0f : m / p.tau) + logf(s);
-        loss = p.entropy ? p.tau * p.tau * (__ldcg(p.entropy + t) - z / p.tau + lse) : lse - z;
+        // (the maximum meets the wanted logit before the logarithm is added: where a
+        // word is nearly certain they are equal, and the loss is the logarithm)
+        const float ref = fabsf(m) == INFINITY ? 0.0f : m, log_s = logf(s);
+        lse = ref / p.tau + log_s;
+        loss = p.entropy ? p.tau * p.tau * (__ldcg(p.entropy + t) + (ref - z) / p.tau + log_s) : (ref - z) + log_s;
     }
     p.loss[t] = loss;
     p.lse[t] = lse;
