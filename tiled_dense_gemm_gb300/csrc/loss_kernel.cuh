@@ -293,6 +293,34 @@ __device__ __forceinline__ int32_t part_count(const LossParams& q) {
 
 __device__ __forceinline__ int32_t part_end(int32_t blocks, int32_t part, int32_t parts) { return part * blocks / parts; }
 
+// Division by a number that many items share.
+struct Divider {
+    uint32_t d, inverse;
+
+    __device__ __forceinline__ explicit Divider(uint32_t by) : d(by), inverse(0xffffffffu / by) {}
+
+    __device__ __forceinline__ uint32_t operator()(uint32_t x, uint32_t& rest) const {
+        uint32_t q = __umulhi(x, inverse);  // at most one too small, for x below 2^31
+        rest = x - q * d;
+        if (rest >= d) {
+            ++q;
+            rest -= d;
+        }
+        return q;
+    }
+};
+
+// 64 numbers times a factor, rounded to the 16-bit type.
+__device__ __forceinline__ void pack_64(uint32_t (&x)[32], const float (&v)[64], float u, int32_t bf16) {
+    if (bf16) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) x[j] = pack16(u * v[2 * j], u * v[2 * j + 1], 1);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) x[j] = pack16(u * v[2 * j], u * v[2 * j + 1], 0);
+    }
+}
+
 // Two parts of a row's statistics as one.
 __device__ __forceinline__ void merge_stats(float& m, float& s, float m1, float s1, float c) {
     const float top = fmaxf(m, m1);
@@ -422,6 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     }
+    const Divider by_group((uint32_t)q.group_m * (uint32_t)q.n_tiles), by_rows((uint32_t)q.group_m);
     if (kMode == kStats) grid_launch_dependents();
     if (!q.late) grid_dependency_wait();
     if (kMode != kStats) grid_launch_dependents();  // (what follows may go by this wait)
@@ -440,26 +469,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     struct Work {
         int32_t split, mt, nt, kb0, kb1;
     };
+    // (three divisions per item cost 450 clocks in every role)
     uint32_t item = worker;
+    const uint32_t whole = (uint32_t)m_tiles / (uint32_t)q.group_m;
+    const Divider by_share(max(tiles, 1u)), by_last(max((uint32_t)m_tiles - whole * (uint32_t)q.group_m, 1u));
     auto next = [&](Work& k) {
         if (item >= items) return false;
-        uint32_t l = item;
+        uint32_t l = item, r, m;
         k.split = 0;
         k.kb0 = 0;
         k.kb1 = blocks;
         if (q.splits > 1) {
-            k.split = (int32_t)(item / tiles);
-            l = item - (uint32_t)k.split * tiles;
+            k.split = (int32_t)by_share(item, l);
             k.kb0 = (int32_t)((int64_t)k.split * blocks / q.splits);
             k.kb1 = (int32_t)((int64_t)(k.split + 1) * blocks / q.splits);
         }
-        const uint32_t per_group = (uint32_t)q.group_m * (uint32_t)q.n_tiles;
-        const uint32_t g = l / per_group, r = l - g * per_group;
-        const uint32_t first = g * (uint32_t)q.group_m;
-        const uint32_t gm = min((uint32_t)q.group_m, (uint32_t)m_tiles - first);
-        const uint32_t n = r / gm;
-        k.nt = (int32_t)n;
-        k.mt = (int32_t)(first + r - n * gm);
+        const uint32_t g = by_group(l, r);
+        k.nt = (int32_t)(g < whole ? by_rows(r, m) : by_last(r, m));
+        k.mt = (int32_t)(g * (uint32_t)q.group_m + m);
         item += workers;
         return true;
     };
@@ -599,6 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t local = 0, tile = 0;
         float scale = 1.0f;
         if constexpr (kMode == kGrad) scale = q.scale ? __ldcg(&q.scale->scale) : scale_of(q.top, q.grad_scale, largest_dloss(q.flags, q.limit, q.dloss, q.dloss_stride, q.M));
+        if constexpr (kMode == kWeight) scale = __ldcg(&q.scale->unscale);
         // the copy issued from the staging buffer before must have read it
         auto turn = [&]() {
             if (lane == 0) bulk_wait_group_read<0>();
@@ -765,10 +793,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if constexpr (kMode == kGrad || kMode == kWeight) {
-                    const float u = kMode == kWeight ? __ldcg(&q.scale->unscale) : 1.0f;
                     uint32_t x[32];
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) x[j] = pack16(u * v[2 * j], u * v[2 * j + 1], q.bf16);
+                    pack_64(x, v, kMode == kWeight ? scale : 1.0f, q.bf16);
                     turn();
 #pragma unroll
                     for (uint32_t i = 0; i < 8; ++i)
