@@ -198,6 +198,23 @@ def test_words_in_one_half_of_every_tile(T):
         distill(x, w, ids.to(DEV), logits.to(DEV), 1.5, "nk", f"T {T} from {first}")
 
 
+@pytest.mark.parametrize("layout", ["nk", "kn"])
+@pytest.mark.parametrize("T", [5, 100, 130, 300])
+def test_tiles_of_every_width(T, layout):
+    """Vocabularies whose tiles are as wide as fills the waves: ends inside a chunk of 64 words, and a last tile
+    of any width; words at the tiles' edges."""
+    D, k = 16, 12
+    for V in (8008, 9744, 12345, 17000, 19001, 22000, 30011, 40000):
+        V = V // 8 * 8 if layout == "kn" else V
+        x, w = normal((T, D), 1, "f16"), head(V, D, layout, 2, "f16")
+        y = ref.make_targets(T, V, 3, 0.1)
+        y[0], y[-1] = V - 1, 0
+        xent(x, w, y.to(DEV), layout, f"T {T} V {V}")
+        ids, logits = ref.make_words(T, V, k, 4, 0.1)
+        ids[1::2] = torch.arange(k, dtype=torch.int32) * 16 + (torch.arange(T, dtype=torch.int32)[1::2, None] * 61) % (V - 16 * k)
+        distill(x, w, ids.to(DEV), logits.to(DEV), 2.0, layout, f"T {T} V {V}")
+
+
 def test_teacher_logits():
     """Logits of -infinity have no weight; of the type's lowest value, alone or with others, they do as any;
     16-bit types, pitches."""

@@ -300,6 +300,8 @@ static int run_backward(const Call& c, const LossPlan& p, DeviceState& d) {
             q.dloss = c.dloss;
             q.dloss_stride = c.dloss_stride;
             q.grad_scale = c.ids ? c.tau : 1.0f;
+            q.grad = G;
+            q.grad_pitch = p.piece;
             q.a_3d = c.D % 64 == 0;
             rc = encode_x(m.a, c, p, 0, c.T, (uint32_t)t.a_rows, q.a_3d ? (uint32_t)t.bk / 64 : 0);
             if (rc == GEMM_OK) rc = encode_words(&m.b[0], c, t, q);

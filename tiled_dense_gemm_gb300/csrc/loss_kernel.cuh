@@ -130,6 +130,8 @@ struct LossParams {
     const float* dloss;
     int64_t dloss_stride;    // 0 or 1
     float grad_scale;        // tau
+    uint16_t* grad;          // G, for tiles that end inside a chunk
+    int64_t grad_pitch;
     FinishParams finish;     // kWeight: dX != null: to be done at the end
     int32_t* err;
     uint64_t timeout_ns;
@@ -772,11 +774,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
             }
             const uint32_t taddr = tmem_base + ((quarter * 32u) << 16) + buf * buf_cols;
-            for (int32_t ch = (int32_t)half; ch < chunks; ch += 2) {
-                const int32_t col = n0 + 64 * ch;
-                if (col >= q.N || row0 >= row_end) break;  // (uniform over the warp)
+            // kGrad: the last tile's zeros go on to the end of a chunk of 64 columns of G,
+            // the others stop where the next one begins, inside a chunk perhaps
+            const int32_t stop = kMode != kGrad ? min(q.N, n0 + 64 * chunks) : n0 + q.width >= q.N ? (q.N + 63) & ~63 : n0 + q.width;
+            for (int32_t ch = (int32_t)half;; ch += 2) {
+                const int32_t col = n0 + 64 * ch, c0 = col + q.w_row;  // (c0: its first word)
+                if (col >= stop || row0 >= row_end) break;             // (uniform over the warp)
+                const int32_t here = kMode == kGrad ? min(64, stop - col) : 64;
                 float v[64];
-                if (some) {
+                if (some && ch < chunks) {
                     __syncwarp();
                     tmem_load_64cols(taddr + 64u * (uint32_t)ch, v);
                 } else {
@@ -784,12 +790,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int j = 0; j < 64; ++j) v[j] = 0.0f;
                 }
                 if constexpr (kMode == kGrad) {
-                    const int32_t c0 = col + q.w_row;  // the chunk's first word
                     while (want.next < c0) want.advance(q);  // (of the other half's chunk)
 #pragma unroll
                     for (int j = 0; j < 64; ++j) {
                         const float p = coef * exp2_fast(fmaf(v[j], c, shift));
                         v[j] = live && col + j < q.N ? p : 0.0f;
+                    }
+                    if (here < 64) {
+                        // part of a chunk: straight from the registers
+                        while (__any_sync(0xffffffffu, want.next - c0 < here)) {
+                            const int32_t at = want.next - c0;
+                            if (at < here) {
+                                const float p = coef * want.weight;
+#pragma unroll
+                                for (int j = 0; j < 64; ++j) v[j] = j == at ? v[j] - p : v[j];
+                                want.advance(q);
+                            }
+                        }
+                        uint32_t x[32];
+                        pack_64(x, v, 1.0f, q.bf16);
+                        uint4* const dst = reinterpret_cast<uint4*>(q.grad + (int64_t)r * q.grad_pitch + col);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (8 * i < here && r < q.M) dst[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                        break;  // (the last)
                     }
                 }
                 if constexpr (kMode == kGrad || kMode == kWeight) {
@@ -802,7 +826,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                                          make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]));
                     if constexpr (kMode == kGrad) {
                         // the wanted words, over what the row's thread has just written
-                        const int32_t c0 = col + q.w_row;
                         int32_t last = kNone;
                         float g = 0.0f;
                         while (__any_sync(0xffffffffu, want.next - c0 < 64)) {

@@ -70,11 +70,11 @@ TilePlan plan_logits(int64_t T, int64_t N, int64_t K, bool b_mn, bool stats, int
     const int pairs = pairs_of(num_sms, max_pairs);
     p.pair = T > 128 && pairs > 0;
     p.splits = 1;
-    // The width whose waves take the shortest time, the widest of equals.  Whole
-    // chunks of 64 columns where they are copied as such, in or out; a pair's CTAs
+    // The width whose waves take the shortest time, the widest of equals, in the
+    // MMA's steps; in whole chunks of 64 columns where B comes in such.  A pair's CTAs
     // take half each.
     const int64_t m_tiles = ceil_div(T, p.pair ? 256 : 128), workers = p.pair ? pairs : num_sms;
-    const int32_t step = (b_mn || !stats ? 64 : 16) * (p.pair && (b_mn || stats) ? 2 : 1);
+    const int32_t step = (b_mn ? 64 : 16) * (p.pair ? 2 : 1);
     const int64_t rows = std::min<int64_t>(128, T);
     double least = 0;
     for (int32_t w = 256; w >= 64; w -= step) {
