@@ -185,22 +185,46 @@ static void wanted(const Call& c, const LossPlan& p, int64_t b0, LossParams& q) 
     q.log2_scale = 1.4426950408889634f / c.tau;
 }
 
-// W as B's side of the logits (reduction D).
-static int encode_words(CUtensorMap* m, const Call& c, const TilePlan& t, LossParams& q) {
-    const uint32_t width = (uint32_t)(t.width / (t.pair ? 2 : 1));
-    q.b_mn = c.nk ? 0 : 1;
-    q.b_3d = (c.nk ? c.D : c.V) % 64 == 0;
-    return c.nk ? encode_rows(m, c.W, (uint64_t)c.D, (uint64_t)c.V, (uint64_t)c.D, width, q.b_3d ? (uint32_t)t.bk / 64 : 0, c.bf16)
-                : encode_rows(m, c.W, (uint64_t)c.V, (uint64_t)c.D, (uint64_t)c.V, (uint32_t)t.bk, q.b_3d ? width / 64 : 0, c.bf16);
+// An mn-major operand of `rows` x `width` (k and its rows' index): the chunks of a
+// stage in one copy, but chunk by chunk through `edge` where a row's end cuts
+// through the last.  (Copies issue one after another, 450 clocks each: two of 64
+// columns per stage held a pair's k-block of 64 at 900.)
+static int encode_chunks(CUtensorMap* map, CUtensorMap* edge, const void* ptr, int64_t width, int64_t rows, int64_t pitch, int bk,
+                         int chunks, bool bf16, int32_t* in_one, int32_t* blocks) {
+    *in_one = width >= 64;
+    *blocks = width % 64 == 0 ? kNone : (int32_t)(width / 64);
+    int rc = encode_rows(edge, ptr, (uint64_t)width, (uint64_t)rows, (uint64_t)pitch, (uint32_t)bk, 0, bf16);
+    if (rc != GEMM_OK) return rc;
+    if (*in_one) return encode_rows(map, ptr, (uint64_t)width, (uint64_t)rows, (uint64_t)pitch, (uint32_t)bk, (uint32_t)chunks, bf16);
+    *map = *edge;
+    return GEMM_OK;
 }
 
-// X's rows and their gathered copy, read as boxes of `box` rows, `blocks` of 64 columns in one copy (0: one by one).
-static int encode_x(CUtensorMap* m, const Call& c, const LossPlan& p, int64_t b0, int64_t T, uint32_t box, uint32_t blocks) {
-    int rc = encode_rows(&m[0], reinterpret_cast<const uint16_t*>(c.X) + b0 * c.ldx, (uint64_t)c.D, (uint64_t)T, (uint64_t)c.ldx,
-                         box, blocks, c.bf16);
-    m[1] = m[0];
-    if (rc == GEMM_OK && (p.gather || p.masked))
-        rc = encode_rows(&m[1], c.ws + p.gathered, (uint64_t)c.D, (uint64_t)T, (uint64_t)p.pitch, box, blocks, c.bf16);
+// W as B's side of the logits (reduction D).
+static int encode_words(LossMaps& m, const Call& c, const TilePlan& t, LossParams& q) {
+    const int width = t.width / (t.pair ? 2 : 1);
+    q.b_mn = c.nk ? 0 : 1;
+    int rc;
+    if (c.nk) {
+        q.b_3d = c.D % 64 == 0;
+        rc = encode_rows(&m.b[0], c.W, (uint64_t)c.D, (uint64_t)c.V, (uint64_t)c.D, (uint32_t)width, q.b_3d ? (uint32_t)t.bk / 64 : 0, c.bf16);
+    } else {
+        rc = encode_chunks(&m.b[0], &m.edge[0], c.W, c.V, c.D, c.V, t.bk, width / 64, c.bf16, &q.b_3d, &q.b_blocks);
+        m.edge[1] = m.edge[0];
+    }
+    m.b[1] = m.b[0];
+    return rc;
+}
+
+// X's rows and their gathered copy as A's side of the logits.
+static int encode_rows_of_x(LossMaps& m, const Call& c, const LossPlan& p, int64_t b0, int64_t T, const TilePlan& t, LossParams& q) {
+    q.a_3d = c.D % 64 == 0;
+    const uint32_t blocks = q.a_3d ? (uint32_t)t.bk / 64 : 0;
+    int rc = encode_rows(&m.a[0], reinterpret_cast<const uint16_t*>(c.X) + b0 * c.ldx, (uint64_t)c.D, (uint64_t)T, (uint64_t)c.ldx,
+                         (uint32_t)t.a_rows, blocks, c.bf16);
+    m.a[1] = m.a[0];
+    if (rc == GEMM_OK && p.gather)
+        rc = encode_rows(&m.a[1], c.ws + p.gathered, (uint64_t)c.D, (uint64_t)T, (uint64_t)p.pitch, (uint32_t)t.a_rows, blocks, c.bf16);
     return rc;
 }
 
@@ -221,11 +245,9 @@ static int run_forward(const Call& c, const LossPlan& p, DeviceState& d) {
         wanted(c, p, b0, q);
         q.stats = reinterpret_cast<float*>(c.ws + p.stats);
         q.stats_pitch = (p.rows + 31) / 32 * 32;
-        q.a_3d = c.D % 64 == 0;
-        rc = encode_x(m.a, c, p, b0, T, (uint32_t)t.a_rows, q.a_3d ? (uint32_t)t.bk / 64 : 0);
-        if (rc == GEMM_OK) rc = encode_words(&m.b[0], c, t, q);
+        rc = encode_rows_of_x(m, c, p, b0, T, t, q);
+        if (rc == GEMM_OK) rc = encode_words(m, c, t, q);
         if (rc != GEMM_OK) return rc;
-        m.b[1] = m.b[0];
         m.d = m.a[0];
         rc = launch_mode<kStats>(d, t, m, q, T, c.st);
         if (rc != GEMM_OK) return rc;
@@ -302,12 +324,10 @@ static int run_backward(const Call& c, const LossPlan& p, DeviceState& d) {
             q.grad_scale = c.ids ? c.tau : 1.0f;
             q.grad = G;
             q.grad_pitch = p.piece;
-            q.a_3d = c.D % 64 == 0;
-            rc = encode_x(m.a, c, p, 0, c.T, (uint32_t)t.a_rows, q.a_3d ? (uint32_t)t.bk / 64 : 0);
-            if (rc == GEMM_OK) rc = encode_words(&m.b[0], c, t, q);
+            rc = encode_rows_of_x(m, c, p, 0, c.T, t, q);
+            if (rc == GEMM_OK) rc = encode_words(m, c, t, q);
             if (rc == GEMM_OK)
                 rc = encode_rows(&m.d, G, (uint64_t)p.piece, (uint64_t)c.T, (uint64_t)p.piece, 32, 0, c.bf16);
-            m.b[1] = m.b[0];
             if (rc == GEMM_OK) rc = launch_mode<kGrad>(d, t, m, q, c.T, c.st);
             if (rc == GEMM_OK && p.masked && p0 == 0) rc = run_rows(c, p, 0, c.T, d);
             if (rc != GEMM_OK) return rc;
@@ -325,24 +345,26 @@ static int run_backward(const Call& c, const LossPlan& p, DeviceState& d) {
             q.first = p0 == 0;
             q.w_k = (int32_t)p0;
             q.b_mn = c.nk ? 1 : 0;
-            q.b_3d = (c.nk ? c.D : c.V) % 64 == 0;
             q.a_3d = 1;  // (G is zero from its last word to the end of that chunk)
             rc = encode_rows(&m.a[0], G, (uint64_t)((vp + 63) / 64 * 64), (uint64_t)c.T, (uint64_t)p.piece, (uint32_t)t.a_rows,
                              (uint32_t)t.bk / 64, c.bf16);
-            if (rc == GEMM_OK)
-                rc = c.nk ? encode_rows(&m.b[0], c.W, (uint64_t)c.D, (uint64_t)c.V, (uint64_t)c.D, (uint32_t)t.bk, q.b_3d ? width / 64 : 0, c.bf16)
-                          : encode_rows(&m.b[0], c.W, (uint64_t)c.V, (uint64_t)c.D, (uint64_t)c.V, width, q.b_3d ? (uint32_t)t.bk / 64 : 0, c.bf16);
+            if (rc == GEMM_OK && c.nk) {
+                rc = encode_chunks(&m.b[0], &m.edge[0], c.W, c.D, c.V, c.D, t.bk, (int)width / 64, c.bf16, &q.b_3d, &q.b_blocks);
+            } else if (rc == GEMM_OK) {
+                q.b_3d = c.V % 64 == 0;
+                rc = encode_rows(&m.b[0], c.W, (uint64_t)c.V, (uint64_t)c.D, (uint64_t)c.V, width, q.b_3d ? (uint32_t)t.bk / 64 : 0, c.bf16);
+            }
             if (rc == GEMM_OK) rc = encode_sums(&m.d, sums, c.D, c.T, p.sum_splits);
             m.a[1] = m.a[0];
             m.b[1] = m.b[0];
+            m.edge[1] = m.edge[0];
             if (rc == GEMM_OK) rc = launch_mode<kSum>(d, t, m, q, c.T, c.st);
             if (rc != GEMM_OK) return rc;
         }
         if (c.dW) {  // dW[piece] = G^T X, or its transpose
             const int64_t M = c.nk ? vp : c.D, N = c.nk ? c.D : vp;
             const TilePlan t = plan_weight(M, N, d.sm_count, d.max_pairs);
-            const uint32_t chunks = (uint32_t)(t.width / (t.pair ? 2 : 1)) / 64;
-            const bool x3d = c.D % 64 == 0;
+            const int b_chunks = t.width / (t.pair ? 2 : 1) / 64, g_chunks = c.nk ? 2 : b_chunks, x_chunks = c.nk ? b_chunks : 2;
             memset(&q, 0, sizeof(q));
             q.M = (int32_t)M;
             q.N = (int32_t)N;
@@ -354,15 +376,22 @@ static int run_backward(const Call& c, const LossPlan& p, DeviceState& d) {
             q.late = c.dX ? 1 : 0;  // (beside the end of kSum, which has waited for G)
             if (c.dX && p0 + p.piece >= c.V) q.finish = finish_of(c, p);
             q.a_mn = q.b_mn = 1;
-            q.a_3d = c.nk || x3d;
-            q.b_3d = !c.nk || x3d;
             (c.nk ? q.d_row : q.d_col) = (int32_t)p0;
             CUtensorMap* const mg = c.nk ? m.a : m.b;
             CUtensorMap* const mx = c.nk ? m.b : m.a;
-            rc = encode_rows(&mg[0], G, (uint64_t)p.piece, (uint64_t)c.T, (uint64_t)p.piece, (uint32_t)t.bk, c.nk ? 2 : chunks, c.bf16);
+            (c.nk ? q.a_3d : q.b_3d) = 1;
+            (c.nk ? q.a_blocks : q.b_blocks) = kNone;
+            int32_t* const x_in_one = c.nk ? &q.b_3d : &q.a_3d;
+            int32_t* const x_blocks = c.nk ? &q.b_blocks : &q.a_blocks;
+            rc = encode_rows(&mg[0], G, (uint64_t)p.piece, (uint64_t)c.T, (uint64_t)p.piece, (uint32_t)t.bk, (uint32_t)g_chunks, c.bf16);
             mg[1] = mg[0];
-            if (rc == GEMM_OK) rc = encode_x(mx, c, p, 0, c.T, (uint32_t)t.bk, !x3d ? 0 : c.nk ? chunks : 2);
-            if (p.masked) mx[0] = mx[1];
+            // the copy: where rows are masked, the only one (the kernel takes the first map then)
+            if (rc == GEMM_OK)
+                rc = encode_chunks(&mx[1], &m.edge[1], c.ws + p.gathered, c.D, c.T, p.pitch, t.bk, x_chunks, c.bf16, x_in_one, x_blocks);
+            mx[0] = mx[1];
+            m.edge[0] = m.edge[1];
+            if (rc == GEMM_OK && !p.masked)
+                rc = encode_chunks(&mx[0], &m.edge[0], c.X, c.D, c.T, c.ldx, t.bk, x_chunks, c.bf16, x_in_one, x_blocks);
             if (rc == GEMM_OK)
                 rc = c.nk ? encode_rows(&m.d, c.dW, (uint64_t)c.D, (uint64_t)c.V, (uint64_t)c.D, 32, 0, c.bf16)
                           : encode_rows(&m.d, c.dW, (uint64_t)c.V, (uint64_t)c.D, (uint64_t)c.V, 32, 0, c.bf16);

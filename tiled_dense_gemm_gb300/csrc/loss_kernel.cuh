@@ -72,6 +72,7 @@ struct RowsHeader {
 
 struct LossMaps {
     CUtensorMap a[2], b[2];  // (the second: where the rows are gathered)
+    CUtensorMap edge[2];     // of an mn-major operand, chunk by chunk, where its rows' end cuts through one
     CUtensorMap d;
 };
 
@@ -98,6 +99,7 @@ struct LossParams {
     int32_t splits;        // kSum: shares of the reduction, each summed apart
     int32_t a_mn, b_mn;    // operand is mn-major
     int32_t a_3d, b_3d;    // a stage's boxes or chunks come in one copy
+    int32_t a_blocks, b_blocks;  // ... up to this many chunks of the operand, beyond through `edge`
     uint32_t a_bytes;      // of a stage (the box's)
     uint32_t stage_bytes;
     int32_t num_stages;
@@ -498,20 +500,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         // warp 0 copies A's tiles and arms the stages, warp 6 B's
         if (lane == 0) {
             const bool is_a = warp == 0;
-            const CUtensorMap* const m = is_a ? &maps.a[gathered] : &maps.b[gathered];
+            const CUtensorMap* const maps_of = is_a ? &maps.a[gathered] : &maps.b[gathered];
             const int32_t width = q.width / kCG;
             uint32_t s = 0, ph = 0;
             int32_t issued = 0;
             bool ok = true;
             const bool once = kMode != kWeight && !is_a && q.once;
             const uint64_t policy = l2_policy_evict_first();
-            const bool mn = is_a ? q.a_mn : q.b_mn, one = is_a ? q.a_3d : q.b_3d;
+            const bool mn = is_a ? q.a_mn : q.b_mn, in_one = is_a ? q.a_3d : q.b_3d;
             // copies of a stage where it takes several, and the bytes of one: 64 k of
             // all rows, or 64 rows of all k
             const int32_t copies = mn ? (is_a ? 2 : width / 64) : q.bk / 64;
             const uint32_t piece = mn ? (uint32_t)q.bk * 128u : is_a ? q.a_bytes / (uint32_t)copies : (uint32_t)width * 128u;
             while (ok && next(k)) {
                 const int32_t r0 = is_a ? k.mt * kTileM + 128 * (int32_t)rank : k.nt * q.width + width * (int32_t)rank + q.w_row;
+                const bool inside = !mn || r0 / 64 + copies <= (is_a ? q.a_blocks : q.b_blocks);
+                const bool one = in_one && inside;
+                const CUtensorMap* const m = inside ? maps_of : &maps.edge[gathered];
                 for (int32_t kb = k.kb0; kb < k.kb1; ++kb) {
                     if (!wait_phase(empty0 + 8u * s, ph ^ 1u, ctrl, w, is_a ? rg::kErrTokens : rg::kErrWeights)) {
                         ok = false;
