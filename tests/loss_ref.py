@@ -14,7 +14,10 @@ to 24 bits):
              through: 64 in its chunk, one per chunk of 64 words, one per part) + 4 e32 |lse|
     q        its argument 4 e32 (1 + |x|), exp and the sum of k terms: eq = (4 |x| + 8 + k) e32, relatively
     g        |a| (p et + q eq) + 4 e32 |a| (p + q), then rounded to the type
-             (binary16: held times a power of two that brings max |a| to at least 2^14)
+             (binary16: held times a power of two that brings max |a| to at least 2^14);
+             up to 32 rows held in two numbers of the type, the second the rounded
+             rest of at most u |g|.  Up to 128 rows, at a wanted word of p > 1/2, z is summed
+             with ceil(D / 2048) terms in each number of 32 bits: ez = that many e32 sum |x w|
     dX, dW   those through |W| and |X|, n e32 sum |g| |w| for the accumulation, rounded to the type
 """
 from __future__ import annotations
@@ -93,6 +96,11 @@ def gradients(x, w, words, lse, dloss, layout, tau=1.0, cross=True):
     a = np.where(valid, np.broadcast_to(np.nan_to_num(_f64(dloss)), (T,)), 0.0)[:, None] * (1.0 if cross else tau)
     p = np.exp(z - r)
     e = p * (ez + 2 * E32 * (np.abs(z) + np.abs(r)) + 2 * E32)
+    rows = np.arange(T)[:, None]
+    sure = (ids >= 0) & (p[rows, np.maximum(ids, 0)] > 0.501) & (T <= 128)  # (of half: either)
+    rows, at = np.broadcast_to(rows, ids.shape)[sure], ids[sure]
+    ez[rows, at] *= math.ceil(X.shape[1] / 2048) / X.shape[1]
+    e[rows, at] = p[rows, at] * (ez[rows, at] + 2 * E32)
     g, size = p.copy(), p.copy()
     for j in range(ids.shape[1]):
         rows = np.flatnonzero(ids[:, j] >= 0)
@@ -103,7 +111,7 @@ def gradients(x, w, words, lse, dloss, layout, tau=1.0, cross=True):
     tiny = TINY[dtype]
     if dtype == torch.float16:
         tiny = 2.0 ** -25 * 2.0 ** -14 * np.abs(a).max(initial=0.0)
-    e = e + UNIT[dtype] * (np.abs(g) + e) + np.where(valid, tiny, 0.0)[:, None]
+    e = e + UNIT[dtype] ** (2 if T <= 32 else 1) * (np.abs(g) + e) + np.where(valid, tiny, 0.0)[:, None]
     g, e = g * valid[:, None], e * valid[:, None]
     n = np.abs(g) + e
     dx, ex = g @ W.T, e @ np.abs(W).T + (V + 32) * E32 * (n @ np.abs(W).T)

@@ -281,6 +281,36 @@ def test_gradient_of_broadcast_losses():
     binding.check_device_error()
 
 
+@pytest.mark.parametrize("layout,dtype", BOTH)
+@pytest.mark.parametrize("T", [1, 20, 100, 300])
+def test_words_that_are_all_but_certain(T, layout, dtype):
+    """exp(z - lse) - 1 is far below what a truncated sum of z is off by."""
+    V, D, k = 1000, 2048, 4
+    w = head(V, D, "nk", 60 + T, dtype)
+    y = ref.make_targets(T, V, 61 + T)
+    rows = w[y.cuda().long()].float()
+    x = (24 * rows / rows.pow(2).sum(dim=1, keepdim=True)).to(w.dtype)
+    w = w if layout == "nk" else w.t().contiguous()
+    W = w.double() if layout == "kn" else w.double().t()
+    dloss = dloss_of(T, 62)
+    for tau, words, call in (
+            (1.0, ref.words_of(targets=y), lambda s: binding.gemm_relu_xent_grad(x, w, y.cuda(), s, dloss, b_layout=layout)),
+            (0.75, None, None)):
+        if words is None:
+            ids, logits = ref.make_words(T, V, k, 63, few=0.0)
+            ids[:, 0] = ids[:, 2] = y  # (q near 1, in two places)
+            logits[:, 0], logits[:, 2], logits[:, 1], logits[:, 3] = 9.0, 9.5, -1.0, -2.0
+            words = ref.words_of(ids=ids, logits=logits, tau=tau)
+            i, l = ids.cuda(), logits.cuda()
+            call = lambda s: binding.gemm_relu_distill_grad(x, w, i, l, s, dloss, tau, b_layout=layout)  # noqa: E731
+        lse = torch.logsumexp(x.double() @ W / tau, dim=1).float()
+        dx, dw = call(lse)
+        binding.check_device_error()
+        rx, rw = ref.gradients(x, w, words, lse, dloss, layout, tau, cross=tau == 1.0)
+        ref.check(dx, rx, f"dx, tau {tau}")
+        ref.check(dw, rw, f"dw, tau {tau}")
+
+
 @pytest.mark.parametrize("size", [1e-20, 1e-8, 1.0, 1e4])
 def test_sizes_of_the_losses_gradient(size):
     """Binary16 holds g times a power of two: small and large gradients lose nothing but what dx and dw round."""
@@ -387,6 +417,39 @@ def test_several_pieces(layout, V):
     # g and the results are rounded to 8 bits: 2^-8 of the terms' sizes each
     for got, want, size in ((dx, g @ W, g.abs() @ W.abs()), (dw if layout == "nk" else dw.T, g.T @ x.double(), g.abs().T @ x.double().abs())):
         assert ((got.double() - want).abs() <= 2.0 ** -7 * size + 2.0 ** -8 * want.abs() + 1e-12).all()
+
+
+@pytest.mark.parametrize("T", [31, 128])
+def test_several_pieces_of_few_rows(T):
+    """More words than G has room for at up to 128 rows, certain ones among them in every piece."""
+    V, D = 4200008 if T < 128 else 2200008, 16
+    w, x = head(V, D, "nk", 70, "bf16"), normal((T, D), 71, "bf16")
+    y = ref.make_targets(T, V, 72).cuda()
+    y[: T // 2] = torch.linspace(0, V - 1, T // 2, device=DEV).int()
+    x[: T // 2] = (40 * w[y[: T // 2].long()].float() / w[y[: T // 2].long()].float().pow(2).sum(dim=1, keepdim=True)).to(x.dtype)
+    z = x.double() @ w.double().t()
+    lse = torch.logsumexp(z, dim=1).float()
+    dloss = dloss_of(T, 73)
+    dx, dw = binding.gemm_relu_xent_grad(x, w, y, lse, dloss, b_layout="nk")
+    binding.check_device_error()
+    rows, a = torch.arange(T, device=DEV), dloss.double()[:, None]
+    ez = D * ref.E32 * (x.double().abs() @ w.double().abs().t())
+    p = torch.exp(z - lse.double()[:, None])
+    e = p * (ez + 2 * ref.E32 * (z.abs() + lse.double().abs()[:, None]) + 2 * ref.E32)
+    e[rows, y.long()] = torch.where(p[rows, y.long()] > 0.501, ez[rows, y.long()] / D + 2 * ref.E32, e[rows, y.long()])
+    size = p.clone()
+    size[rows, y.long()] += 1
+    p[rows, y.long()] -= 1
+    u = 2.0 ** -8
+    g, e = a * p, a * (e + 4 * ref.E32 * size)
+    e += u ** (2 if T <= 32 else 1) * (g.abs() + e) + 2.0 ** -134
+    del z, ez, p, size
+    X, W, n = x.double(), w.double(), g.abs() + e
+    # (dX's sums: 16 products and one truncation at a time)
+    for out, value, bound in ((dw, g.t() @ X, e.t() @ X.abs() + T * ref.E32 * (n.t() @ X.abs())),
+                              (dx, g @ W, e @ W.abs() + V / 16 * ref.E32 * (n @ W.abs()))):
+        off = (out.double() - value).abs() - (bound + u * (value.abs() + bound) + 2.0 ** -134)
+        assert off.max().item() <= 0.0
 
 
 def test_more_rows_than_a_block():

@@ -99,7 +99,9 @@ static int launch_mode(DeviceState& d, const TilePlan& t, const LossMaps& m, Los
         const int rc = rt::test_hook(!t.pair, (int32_t)std::min<int64_t>(blocks, kNone), &q.test_drop_kb, &q.timeout_ns);
         if (rc != GEMM_OK) return rc;
     }
-    return t.pair ? launch_tiles<true, kMode>(d, t, m, q, st) : launch_tiles<false, kMode>(d, t, m, q, st);
+    if constexpr (kMode != kGradLow)
+        if (t.pair) return launch_tiles<true, kMode>(d, t, m, q, st);
+    return launch_tiles<false, kMode>(d, t, m, q, st);  // (few rows: never pairs)
 }
 
 // A row is in use where its flag is in [0, limit).
@@ -143,7 +145,7 @@ static int run_teacher(const Call& c, const LossPlan& p, int64_t b0, int64_t T, 
 static float top_of(const Call& c) { return c.bf16 ? 255.0f / 128.0f : 2047.0f / 1024.0f * 16384.0f; }
 
 // Which rows [b0, b0 + T) are in use, and a copy of those.
-static int run_rows(const Call& c, const LossPlan& p, int64_t b0, int64_t T, DeviceState& d) {
+static int run_rows(const Call& c, const LossPlan& p, int64_t b0, int64_t T, DeviceState& d, int64_t p0 = 0) {
     RowsParams q;
     memset(&q, 0, sizeof(q));
     q.flags = flags_of(c, p, b0);
@@ -164,7 +166,27 @@ static int run_rows(const Call& c, const LossPlan& p, int64_t b0, int64_t T, Dev
     q.grad_scale = c.ids ? c.tau : 1.0f;
     q.top = top_of(c);
     q.err = d.d_err;
-    if (p.masked) return launch(loss_mask_kernel, (int)T, kRowsThreads, 0, 1, c.st, q);
+    if (p.masked) {
+        q.rows_of = (int32_t)p.g_rows;
+        q.period = p.low ? p.low : (int32_t)T;
+        q.W = reinterpret_cast<const uint16_t*>(c.W);
+        q.w_word = c.nk ? c.D : 1;
+        q.w_depth = c.nk ? 1 : c.V;
+        if (c.ids) {
+            q.ids = reinterpret_cast<const int32_t*>(c.ws + p.sorted);
+            q.weights = reinterpret_cast<const float*>(c.ws + p.weights);
+            q.k = (int32_t)c.k;
+        }
+        q.bf16 = c.bf16 ? 1 : 0;
+        q.tau = c.ids ? c.tau : 1.0f;
+        q.lse = c.lse;
+        q.grad = reinterpret_cast<uint16_t*>(c.ws + p.grad);
+        q.grad_pitch = p.piece;
+        q.from = (int32_t)p0;
+        q.words = (int32_t)std::min(p.piece, c.V - p0);
+        q.low = p.low;
+        return launch(loss_mask_kernel, q.rows_of, kRowsThreads, 0, 1, c.st, q);
+    }
     const int grid = (int)std::max<int64_t>(1, std::min<int64_t>((T + 7) / 8, 4 * d.sm_count));
     return launch(loss_rows_kernel, grid, kRowsThreads, 0, 1, c.st, q);
 }
@@ -280,6 +302,8 @@ static FinishParams finish_of(const Call& c, const LossPlan& p) {
     f.sums = reinterpret_cast<const float*>(c.ws + p.sums);
     f.splits = p.sum_splits;
     f.T = (int32_t)c.T;
+    f.rows_of = (int32_t)p.g_rows;
+    f.low = p.low;
     f.D = (int32_t)c.D;
     f.bf16 = c.bf16 ? 1 : 0;
     f.rows = reinterpret_cast<const RowsHeader*>(c.ws + p.header);
@@ -304,7 +328,10 @@ static int run_backward(const Call& c, const LossPlan& p, DeviceState& d) {
         LossMaps m;
         LossParams q;
         {  // G of the piece
-            const TilePlan t = plan_logits(c.T, vp, c.D, !c.nk, false, d.sm_count, d.max_pairs);
+            // (the rows' kernel beside it, eight blocks on an SM: 65536 words of 2048, 64
+            // rows 139 us with none left for it, 136 so; 16 rows 137 and 132)
+            const int sms = p.masked ? std::max(d.sm_count - (int)((p.g_rows + 7) / 8), d.sm_count / 2) : d.sm_count;
+            const TilePlan t = plan_logits(c.T, vp, c.D, !c.nk, false, sms, d.max_pairs);
             memset(&q, 0, sizeof(q));
             q.M = (int32_t)c.T;
             q.N = (int32_t)vp;
@@ -327,16 +354,19 @@ static int run_backward(const Call& c, const LossPlan& p, DeviceState& d) {
             rc = encode_rows_of_x(m, c, p, 0, c.T, t, q);
             if (rc == GEMM_OK) rc = encode_words(m, c, t, q);
             if (rc == GEMM_OK)
-                rc = encode_rows(&m.d, G, (uint64_t)p.piece, (uint64_t)c.T, (uint64_t)p.piece, 32, 0, c.bf16);
-            if (rc == GEMM_OK) rc = launch_mode<kGrad>(d, t, m, q, c.T, c.st);
-            if (rc == GEMM_OK && p.masked && p0 == 0) rc = run_rows(c, p, 0, c.T, d);
+                rc = encode_rows(&m.d, G, (uint64_t)p.piece, (uint64_t)(p.low ? p.low : c.T), (uint64_t)p.piece, 32, 0, c.bf16);
+            if (rc == GEMM_OK && p.low)
+                rc = encode_rows(&m.low, G + p.low * p.piece, (uint64_t)p.piece, (uint64_t)p.low, (uint64_t)p.piece, 32, 0, c.bf16);
+            q.low = p.low;
+            if (rc == GEMM_OK) rc = p.low ? launch_mode<kGradLow>(d, t, m, q, c.T, c.st) : launch_mode<kGrad>(d, t, m, q, c.T, c.st);
+            if (rc == GEMM_OK && p.masked) rc = run_rows(c, p, 0, c.T, d, p0);
             if (rc != GEMM_OK) return rc;
         }
         if (c.dX) {  // sums += G W
-            const TilePlan t = plan_sum(c.T, c.D, p.sum_splits, p.sum_width, c.nk, d.sm_count, d.max_pairs);
+            const TilePlan t = plan_sum(p.g_rows, c.D, p.sum_splits, p.sum_width, c.nk, d.sm_count, d.max_pairs);
             const uint32_t width = (uint32_t)(t.width / (t.pair ? 2 : 1));
             memset(&q, 0, sizeof(q));
-            q.M = (int32_t)c.T;
+            q.M = (int32_t)p.g_rows;
             q.N = (int32_t)c.D;
             q.K = (int32_t)vp;
             q.bf16 = c.bf16 ? 1 : 0;
@@ -346,7 +376,7 @@ static int run_backward(const Call& c, const LossPlan& p, DeviceState& d) {
             q.w_k = (int32_t)p0;
             q.b_mn = c.nk ? 1 : 0;
             q.a_3d = 1;  // (G is zero from its last word to the end of that chunk)
-            rc = encode_rows(&m.a[0], G, (uint64_t)((vp + 63) / 64 * 64), (uint64_t)c.T, (uint64_t)p.piece, (uint32_t)t.a_rows,
+            rc = encode_rows(&m.a[0], G, (uint64_t)((vp + 63) / 64 * 64), (uint64_t)p.g_rows, (uint64_t)p.piece, (uint32_t)t.a_rows,
                              (uint32_t)t.bk / 64, c.bf16);
             if (rc == GEMM_OK && c.nk) {
                 rc = encode_chunks(&m.b[0], &m.edge[0], c.W, c.D, c.V, c.D, t.bk, (int)width / 64, c.bf16, &q.b_3d, &q.b_blocks);
@@ -354,7 +384,7 @@ static int run_backward(const Call& c, const LossPlan& p, DeviceState& d) {
                 q.b_3d = c.V % 64 == 0;
                 rc = encode_rows(&m.b[0], c.W, (uint64_t)c.V, (uint64_t)c.D, (uint64_t)c.V, width, q.b_3d ? (uint32_t)t.bk / 64 : 0, c.bf16);
             }
-            if (rc == GEMM_OK) rc = encode_sums(&m.d, sums, c.D, c.T, p.sum_splits);
+            if (rc == GEMM_OK) rc = encode_sums(&m.d, sums, c.D, p.g_rows, p.sum_splits);
             m.a[1] = m.a[0];
             m.b[1] = m.b[0];
             m.edge[1] = m.edge[0];
@@ -368,7 +398,7 @@ static int run_backward(const Call& c, const LossPlan& p, DeviceState& d) {
             memset(&q, 0, sizeof(q));
             q.M = (int32_t)M;
             q.N = (int32_t)N;
-            q.K = (int32_t)c.T;
+            q.K = (int32_t)p.g_rows;
             q.bf16 = c.bf16 ? 1 : 0;
             q.rows = counted;
             q.rows_k = counted ? 1 : 0;
@@ -383,11 +413,11 @@ static int run_backward(const Call& c, const LossPlan& p, DeviceState& d) {
             (c.nk ? q.a_blocks : q.b_blocks) = kNone;
             int32_t* const x_in_one = c.nk ? &q.b_3d : &q.a_3d;
             int32_t* const x_blocks = c.nk ? &q.b_blocks : &q.a_blocks;
-            rc = encode_rows(&mg[0], G, (uint64_t)p.piece, (uint64_t)c.T, (uint64_t)p.piece, (uint32_t)t.bk, (uint32_t)g_chunks, c.bf16);
+            rc = encode_rows(&mg[0], G, (uint64_t)p.piece, (uint64_t)p.g_rows, (uint64_t)p.piece, (uint32_t)t.bk, (uint32_t)g_chunks, c.bf16);
             mg[1] = mg[0];
             // the copy: where rows are masked, the only one (the kernel takes the first map then)
             if (rc == GEMM_OK)
-                rc = encode_chunks(&mx[1], &m.edge[1], c.ws + p.gathered, c.D, c.T, p.pitch, t.bk, x_chunks, c.bf16, x_in_one, x_blocks);
+                rc = encode_chunks(&mx[1], &m.edge[1], c.ws + p.gathered, c.D, p.g_rows, p.pitch, t.bk, x_chunks, c.bf16, x_in_one, x_blocks);
             mx[0] = mx[1];
             m.edge[0] = m.edge[1];
             if (rc == GEMM_OK && !p.masked)

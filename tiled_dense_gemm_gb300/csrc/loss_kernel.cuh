@@ -54,7 +54,7 @@ using rg::Ctrl;
 using rg::pack16;
 using rg::wait_phase;
 
-enum Mode : int { kStats = 0, kGrad = 1, kSum = 2, kWeight = 3 };
+enum Mode : int { kStats = 0, kGrad = 1, kSum = 2, kWeight = 3, kGradLow = 4 };  // (kGradLow: G in two parts)
 
 constexpr int kThreads = 352;
 constexpr uint32_t kStaging = 4096;  // bytes per epilogue warp
@@ -73,13 +73,14 @@ struct RowsHeader {
 struct LossMaps {
     CUtensorMap a[2], b[2];  // (the second: where the rows are gathered)
     CUtensorMap edge[2];     // of an mn-major operand, chunk by chunk, where its rows' end cuts through one
-    CUtensorMap d;
+    CUtensorMap d, low;      // (low: of G's second part)
 };
 
 // dX from its sums.
 struct FinishParams {
-    const float* sums;       // [splits][T][D]
+    const float* sums;       // [splits][rows][D]
     int32_t splits, T, D, bf16;
+    int32_t rows_of, low;    // rows of a plane; > 0: those from here on are added to the first
     const RowsHeader* rows;
     const int32_t* index;    // null: all rows in their places,
     const int32_t* flags;    // ... in use where in [0, limit)
@@ -134,6 +135,7 @@ struct LossParams {
     float grad_scale;        // tau
     uint16_t* grad;          // G, for tiles that end inside a chunk
     int64_t grad_pitch;
+    int32_t low;             // > 0: G's rows from here on take what rounding left of the first
     FinishParams finish;     // kWeight: dX != null: to be done at the end
     int32_t* err;
     uint64_t timeout_ns;
@@ -325,6 +327,17 @@ __device__ __forceinline__ void pack_64(uint32_t (&x)[32], const float (&v)[64],
     }
 }
 
+// What that rounding left of them, rounded.
+__device__ __forceinline__ void rest_64(uint32_t (&x)[32], const float (&v)[64], int32_t bf16) {
+    if (bf16) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) x[j] = rg::rest16x2(v[2 * j], v[2 * j + 1], x[j], 1);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) x[j] = rg::rest16x2(v[2 * j], v[2 * j + 1], x[j], 0);
+    }
+}
+
 // Two parts of a row's statistics as one.
 __device__ __forceinline__ void merge_stats(float& m, float& s, float m1, float s1, float c) {
     const float top = fmaxf(m, m1);
@@ -344,7 +357,7 @@ __device__ __forceinline__ void finish_lanes(const FinishParams& p, int32_t thre
     const int32_t valid = p.index ? __ldcg(&p.rows->valid) : p.T;
     const float u = __ldcg(&p.rows->unscale);
     const int32_t vecs = p.D / 8, lane = (int32_t)threadIdx.x % kLanes;
-    const int64_t total = (int64_t)p.T * vecs, share = (int64_t)p.T * p.D;
+    const int64_t total = (int64_t)p.T * vecs, share = (int64_t)p.rows_of * p.D, low = (int64_t)p.low * p.D;
     const int64_t step = (int64_t)gridDim.x * (threads / kLanes), rounds = (total + step - 1) / step;
     int64_t i = (int64_t)blockIdx.x * (threads / kLanes) + threadIdx.x / kLanes;
     for (int64_t n = 0; n < rounds; ++n, i += step) {
@@ -357,6 +370,11 @@ __device__ __forceinline__ void finish_lanes(const FinishParams& p, int32_t thre
                 const float4 x = __ldcs(src + k * (share / 4)), y = __ldcs(src + k * (share / 4) + 1);
                 a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
                 b.x += y.x, b.y += y.y, b.z += y.z, b.w += y.w;
+                if (low) {
+                    const float4 x2 = __ldcs(src + k * (share / 4) + low / 4), y2 = __ldcs(src + k * (share / 4) + low / 4 + 1);
+                    a.x += x2.x, a.y += x2.y, a.z += x2.z, a.w += x2.w;
+                    b.x += y2.x, b.y += y2.y, b.z += y2.z, b.w += y2.w;
+                }
             }
         }
 #pragma unroll
@@ -393,6 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     loss_kernel(const __grid_constant__ LossMaps maps, const __grid_constant__ LossParams q) {
     constexpr int kCG = kPair ? 2 : 1;
     constexpr int32_t kTileM = kPair ? 256 : 128;
+    constexpr bool kLow = kMode == kGradLow, kAnyGrad = kMode == kGrad || kLow;
     extern __shared__ __align__(1024) uint8_t smem[];
     Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem);
     const uint32_t ring = (smem_u32(smem) + (uint32_t)sizeof(Ctrl) + 1023u) & ~1023u;
@@ -629,10 +648,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t staging = ring + S * stride + (quarter + 4u * half) * kStaging;
         const int32_t chunks = (q.width + 63) / 64;
         // (G's rows are kWeight's reduction: zeros up to the end of its last k-block)
-        const int32_t row_end = kMode == kGrad ? (M + kRowPad - 1) / kRowPad * kRowPad : M;
+        const int32_t row_end = !kAnyGrad ? M : kLow ? q.low : (M + kRowPad - 1) / kRowPad * kRowPad;
         uint32_t local = 0, tile = 0;
         float scale = 1.0f;
-        if constexpr (kMode == kGrad) scale = q.scale ? __ldcg(&q.scale->scale) : scale_of(q.top, q.grad_scale, largest_dloss(q.flags, q.limit, q.dloss, q.dloss_stride, q.M));
+        if constexpr (kAnyGrad) scale = q.scale ? __ldcg(&q.scale->scale) : scale_of(q.top, q.grad_scale, largest_dloss(q.flags, q.limit, q.dloss, q.dloss_stride, q.M));
         if constexpr (kMode == kWeight) scale = __ldcg(&q.scale->unscale);
         // the copy issued from the staging buffer before must have read it
         auto turn = [&]() {
@@ -647,14 +666,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             // what the row's epilogue reads, before the accumulator is waited for
             int32_t t = 0, y = kNone;
             float coef = 0.0f, shift = 0.0f;
-            if constexpr (kMode == kStats || kMode == kGrad) {
+            if constexpr (kMode == kStats || kAnyGrad) {
                 t = live && gathered ? __ldcg(q.index + r) : r;
-                if (kMode == kGrad && live && q.flags) {
+                if (kAnyGrad && live && q.flags) {
                     const int32_t f = __ldcg(q.flags + t);
                     live = f >= 0 && f < q.limit;
                 }
                 if (live && !q.ids) y = __ldcg(q.targets + t);
-                if constexpr (kMode == kGrad) {
+                if constexpr (kAnyGrad) {
                     if (live) {
                         shift = -1.4426950408889634f * __ldg(q.lse + t);
                         coef = __ldg(q.dloss + (int64_t)t * q.dloss_stride) * q.grad_scale * scale;
@@ -772,7 +791,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 continue;
             }
             Wanted want;
-            if constexpr (kMode == kGrad) want.start(q, t, y, live, n0 + q.w_row);
+            if constexpr (kAnyGrad) want.start(q, t, y, live, n0 + q.w_row);
             const uint32_t buf = local & 1u, bph = (local >> 1) & 1u;
             if (some) {
                 if (!__all_sync(0xffffffffu, wait_phase(smem_u32(&ctrl->tmem_full[buf]), bph, ctrl, w, rg::kErrEpi))) break;
@@ -781,11 +800,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t taddr = tmem_base + ((quarter * 32u) << 16) + buf * buf_cols;
             // kGrad: the last tile's zeros go on to the end of a chunk of 64 columns of G,
             // the others stop where the next one begins, inside a chunk perhaps
-            const int32_t stop = kMode != kGrad ? min(q.N, n0 + 64 * chunks) : n0 + q.width >= q.N ? (q.N + 63) & ~63 : n0 + q.width;
+            const int32_t stop = !kAnyGrad ? min(q.N, n0 + 64 * chunks) : n0 + q.width >= q.N ? (q.N + 63) & ~63 : n0 + q.width;
             for (int32_t ch = (int32_t)half;; ch += 2) {
                 const int32_t col = n0 + 64 * ch, c0 = col + q.w_row;  // (c0: its first word)
                 if (col >= stop || row0 >= row_end) break;             // (uniform over the warp)
-                const int32_t here = kMode == kGrad ? min(64, stop - col) : 64;
+                const int32_t here = kAnyGrad ? min(64, stop - col) : 64;
                 float v[64];
                 if (some && ch < chunks) {
                     __syncwarp();
@@ -794,15 +813,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 64; ++j) v[j] = 0.0f;
                 }
-                if constexpr (kMode == kGrad) {
+                if constexpr (kAnyGrad) {
                     while (want.next < c0) want.advance(q);  // (of the other half's chunk)
 #pragma unroll
                     for (int j = 0; j < 64; ++j) {
                         const float p = coef * exp2_fast(fmaf(v[j], c, shift));
                         v[j] = live && col + j < q.N ? p : 0.0f;
                     }
-                    if (here < 64) {
-                        // part of a chunk: straight from the registers
+                    if (here < 64 || kLow) {
+                        // the wanted words, where the row does not go through shared memory in one part
                         while (__any_sync(0xffffffffu, want.next - c0 < here)) {
                             const int32_t at = want.next - c0;
                             if (at < here) {
@@ -812,47 +831,61 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 want.advance(q);
                             }
                         }
+                    }
+                    if (here < 64) {
+                        // part of a chunk (the tile's last): straight from the registers
                         uint32_t x[32];
                         pack_64(x, v, 1.0f, q.bf16);
-                        uint4* const dst = reinterpret_cast<uint4*>(q.grad + (int64_t)r * q.grad_pitch + col);
+                        uint16_t* dst = q.grad + (int64_t)r * q.grad_pitch + col;
+                        const bool write = r < (kLow ? q.low : q.M);
+                        for (int part = 0;; ++part) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (8 * i < here && r < q.M) dst[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-                        break;  // (the last)
+                            for (int i = 0; i < 8; ++i)
+                                if (8 * i < here && write)
+                                    reinterpret_cast<uint4*>(dst)[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                            if (part == 1 || !kLow) break;
+                            dst += (int64_t)q.low * q.grad_pitch;
+                            rest_64(x, v, q.bf16);
+                        }
+                        break;
                     }
                 }
-                if constexpr (kMode == kGrad || kMode == kWeight) {
+                if constexpr (kAnyGrad || kMode == kWeight) {
                     uint32_t x[32];
                     pack_64(x, v, kMode == kWeight ? scale : 1.0f, q.bf16);
-                    turn();
+                    for (int part = 0;; ++part) {
+                        turn();
 #pragma unroll
-                    for (uint32_t i = 0; i < 8; ++i)
-                        rg::st_shared_v4(staging + lane * 128u + ((i ^ (lane & 7u)) << 4),
-                                         make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]));
-                    if constexpr (kMode == kGrad) {
-                        // the wanted words, over what the row's thread has just written
-                        int32_t last = kNone;
-                        float g = 0.0f;
-                        while (__any_sync(0xffffffffu, want.next - c0 < 64)) {
-                            const int32_t at = want.next - c0;
-                            const float p = pick<0, 64>(v, at);
-                            if (at < 64) {
-                                g = (at == last ? g : p) - coef * want.weight;  // (a word may come twice)
-                                last = at;
-                                st_shared_u16(staging + lane * 128u + ((((uint32_t)at >> 3) ^ (lane & 7u)) << 4) + ((uint32_t)at & 7u) * 2u,
-                                              rg::round16(g, q.bf16));
-                                want.advance(q);
+                        for (uint32_t i = 0; i < 8; ++i)
+                            rg::st_shared_v4(staging + lane * 128u + ((i ^ (lane & 7u)) << 4),
+                                             make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]));
+                        if constexpr (kMode == kGrad) {
+                            // the wanted words, over what the row's thread has just written
+                            int32_t last = kNone;
+                            float g = 0.0f;
+                            while (__any_sync(0xffffffffu, want.next - c0 < 64)) {
+                                const int32_t at = want.next - c0;
+                                const float p = pick<0, 64>(v, at);
+                                if (at < 64) {
+                                    g = (at == last ? g : p) - coef * want.weight;  // (a word may come twice)
+                                    last = at;
+                                    st_shared_u16(staging + lane * 128u + ((((uint32_t)at >> 3) ^ (lane & 7u)) << 4) + ((uint32_t)at & 7u) * 2u,
+                                                  rg::round16(g, q.bf16));
+                                    want.advance(q);
+                                }
                             }
                         }
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (kMode == kWeight && q.once)
-                            store_2d_hint(&maps.d, staging, col + q.d_col, row0 + q.d_row, l2_policy_evict_first());
-                        else
-                            tma_store_2d(&maps.d, staging, col + q.d_col, row0 + q.d_row);
-                        bulk_commit_group();
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (kMode == kWeight && q.once)
+                                store_2d_hint(&maps.d, staging, col + q.d_col, row0 + q.d_row, l2_policy_evict_first());
+                            else
+                                tma_store_2d(kLow && part == 1 ? &maps.low : &maps.d, staging, col + q.d_col, row0 + q.d_row);
+                            bulk_commit_group();
+                        }
+                        if (!kLow || part == 1) break;
+                        rest_64(x, v, q.bf16);
                     }
                 }
                 if constexpr (kMode == kSum) {

@@ -119,6 +119,12 @@ LossPlan plan_loss(int64_t T, int64_t V, int64_t D, int64_t k, bool gradient) {
     // forward: rows in use are gathered where that saves tiles
     p.gather = T > 128;
     p.masked = gradient && !p.gather;
+    // Up to 32 rows G has two parts, the rounded values and what that left, in rows
+    // of their own: a tile of 128 rows holds both, and dX and dW are as exact as their
+    // own rounding (one rounding of G, which averages out over many rows, doubled the
+    // error of a single one).
+    p.low = p.masked && T <= 32 ? (int32_t)round_up(T, 8) : 0;
+    p.g_rows = p.low ? 2 * p.low : T;
     const int64_t rows = p.rows;
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
@@ -137,12 +143,12 @@ LossPlan plan_loss(int64_t T, int64_t V, int64_t D, int64_t k, bool gradient) {
     // The copy's rows start at multiples of 128 bytes, so that a box row lies in one
     // line (1800 of 3000 rows, 50021 words of 2056: 305 us at X's pitch, 280 so).
     p.pitch = round_up(D, 64);
-    if (p.gather || p.masked) p.gathered = take(2 * rows * p.pitch);
+    if (p.gather || p.masked) p.gathered = take(2 * std::max(rows, p.masked ? p.g_rows : 0) * p.pitch);
     if (!gradient) {
         if (parts * ceil_div(rows, 128) > 2000000000ll) p.status = GEMM_ERR_TOO_LARGE;
         p.stats = take(12 * round_up(rows, 32) * parts);
     } else {
-        const int64_t most = std::max<int64_t>(256, kGradBytes / (2 * rows) / 256 * 256);
+        const int64_t most = std::max<int64_t>(256, kGradBytes / (2 * p.g_rows) / 256 * 256);
         p.piece = round_up(ceil_div(V, ceil_div(V, most)), 256);
         p.pieces = (int32_t)ceil_div(V, p.piece);
         // Tiles and shares of dX's reduction by the time of their waves, their start
@@ -153,12 +159,12 @@ LossPlan plan_loss(int64_t T, int64_t V, int64_t D, int64_t k, bool gradient) {
         double least = 0;
         for (int32_t w : {256, 128}) {
             if (w == 256 && D <= 128) continue;
-            const double clocks = block_clocks(w, std::min<int64_t>(128, rows), pair);
+            const double clocks = block_clocks(w, std::min<int64_t>(128, p.g_rows), pair);
             const int64_t tiles = m_tiles * ceil_div(D, w);
             for (int32_t s = 1; s <= 64; ++s) {
                 if (s > 1 && blocks / s < 8) break;
                 const double cost = (double)ceil_div(tiles * s, workers) * (clocks * (double)ceil_div(blocks, s) + 3000) +
-                                    8.0 * (double)s * (double)rows * (double)D / 2600;
+                                    8.0 * (double)s * (double)p.g_rows * (double)D / 2600;
                 if (p.sum_splits == 0 || cost < least * 0.98) {
                     least = cost;
                     p.sum_splits = s;
@@ -166,8 +172,8 @@ LossPlan plan_loss(int64_t T, int64_t V, int64_t D, int64_t k, bool gradient) {
                 }
             }
         }
-        p.grad = take(2 * rows * p.piece);
-        p.sums = take(4 * rows * D * p.sum_splits);
+        p.grad = take(2 * p.g_rows * p.piece);
+        p.sums = take(4 * p.g_rows * D * p.sum_splits);
         if (m_tiles * ceil_div(p.piece, 64) > 2000000000ll || ceil_div(p.piece, 128) * ceil_div(D, 64) > 2000000000ll ||
             m_tiles * ceil_div(D, 64) * p.sum_splits > 2000000000ll)
             p.status = GEMM_ERR_TOO_LARGE;

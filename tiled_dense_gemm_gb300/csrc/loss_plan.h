@@ -27,6 +27,8 @@ struct LossPlan {
     int32_t pieces;
     int32_t gather;      // the rows in use are counted, and gathered if some are not
     int32_t masked;      // backward, up to 128 rows: a copy of X with zeros for those that are not
+    int32_t low;         // backward, up to 32 rows: > 0: G's rows from here on hold what rounding left of the first
+    int64_t g_rows;      // rows of G
     int32_t sum_splits;  // backward: shares of dX's reduction,
     int32_t sum_width;   // ... and its tiles' columns
     int64_t pitch;       // of the rows' copy

@@ -125,6 +125,20 @@ struct RowsParams {
     float top;              // what the largest |dloss grad_scale| is scaled to
     int32_t pitch;          // of the copy: D rounded up to 64
     int32_t always;         // gather even if all rows are in use
+    // masked: rows of the copy, X's over and over after so many (of G's two parts), and
+    // what the gradient at a certain word is found from
+    int32_t rows_of, period;
+    const uint16_t* W;
+    int64_t w_word, w_depth;  // from one word to the next, and from one k: one of them 1
+    const int32_t* ids;       // (T, k) of a teacher; null: the flags
+    const float* weights;
+    int32_t k, bf16;
+    float tau;
+    const float* lse;
+    uint16_t* grad;           // G
+    int64_t grad_pitch;
+    int32_t from, words;      // its piece's words
+    int32_t low;              // > 0: G's rows from here on take what rounding left
     int32_t* err;
 };
 
@@ -251,26 +265,135 @@ __global__ void __launch_bounds__(kRowsThreads) loss_rows_kernel(const __grid_co
     if (i == 0) write_header(p, total, gather ? 1 : 0, top);
 }
 
-// Up to 128 rows: nothing is gathered (there is one row tile).  A copy of X with
-// zeros in the rows that are not in use, for dW, and the scale, beside the kernel
-// of G (`late`, as there: that one has waited for X and the flags).
-__global__ void __launch_bounds__(kRowsThreads) loss_mask_kernel(const __grid_constant__ RowsParams p) {
-    const int32_t i = (int32_t)threadIdx.x;
-    grid_launch_dependents();
-    const int32_t vecs = p.D / 8;
-    for (int32_t t = (int32_t)blockIdx.x; t < p.T; t += (int32_t)gridDim.x) {
-        const int32_t y = __ldcg(p.flags + t);
-        if (y >= p.limit && i == 0) atomicCAS(p.err + 1, 0, (int32_t)rg::kBadIds);
-        const bool in = y >= 0 && y < p.limit;
-        const uint4* const src = reinterpret_cast<const uint4*>(p.X + (int64_t)t * p.ldx);
-        uint4* const dst = reinterpret_cast<uint4*>(p.gathered + (int64_t)t * p.pitch);
-        for (int32_t c = i; c < vecs; c += kRowsThreads) dst[c] = in ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+// The wanted word of a row that weighs most, and its weight, by one warp.
+__device__ __forceinline__ int32_t main_word(const RowsParams& p, int32_t t, int32_t flag, float& weight) {
+    weight = 1.0f;
+    if (!p.ids) return flag;
+    const int32_t lane = (int32_t)threadIdx.x % 32;
+    const int32_t* const ids = p.ids + (int64_t)t * p.k;
+    const float* const weights = p.weights + (int64_t)t * p.k;
+    float most = 0.0f;
+    int32_t word = kNone;
+    for (int32_t j = lane; j < p.k; j += 32) {
+        const float q = __ldcg(weights + j);
+        if (q > most) {
+            most = q;
+            word = __ldcg(ids + j);
+        }
     }
-    if (blockIdx.x == 0 && i < 32) {
-        const float top = largest_dloss(p.flags, p.limit, p.dloss, p.dloss_stride, p.T);
-        if (i == 0) write_header(p, p.T, 0, top);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        const float q = __shfl_xor_sync(0xffffffffu, most, d);
+        const int32_t y = __shfl_xor_sync(0xffffffffu, word, d);
+        if (q > most || (q == most && y < word)) {
+            most = q;
+            word = y;
+        }
+    }
+    float all = 0.0f;  // (it may come more than once)
+    for (int32_t j = lane; j < p.k; j += 32)
+        if (__ldcg(ids + j) == word) all += __ldcg(weights + j);
+    weight = warp_sum(all);
+    return word;
+}
+
+// This thread's products of X's row with a word's weights, of all the block's.
+__device__ __forceinline__ double some_products(const RowsParams& p, int32_t t, int32_t word) {
+    const uint16_t* const x = p.X + (int64_t)t * p.ldx;
+    const uint16_t* const w = p.W + (int64_t)word * p.w_word;
+    float sum[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    for (int32_t d = 8 * (int32_t)threadIdx.x; d < p.D; d += 8 * kRowsThreads) {  // (D a multiple of 8)
+        const uint4 a = __ldg(reinterpret_cast<const uint4*>(x + d));
+        uint4 b;
+        if (p.w_depth == 1) {
+            b = __ldg(reinterpret_cast<const uint4*>(w + d));
+        } else {
+            uint32_t e[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) e[j] = __ldg(w + (int64_t)(d + j) * p.w_depth);
+            b = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+        }
+        const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 m = rg::unpack16(av[j], p.bf16), n = rg::unpack16(bv[j], p.bf16);
+            sum[2 * j] = fmaf(m.x, n.x, sum[2 * j]);
+            sum[2 * j + 1] = fmaf(m.y, n.y, sum[2 * j + 1]);
+        }
+    }
+    double z = 0.0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) z += (double)sum[j];
+    return z;
+}
+
+// Up to 128 rows: nothing is gathered (there is one row tile).  Beside the kernel of
+// G (`late`, as there: that one has waited for X and the flags), a block per row:
+//
+// * a copy of X with zeros in the rows that are not in use, for dW, and the scale;
+// * the gradient at the row's main word, if that is all but certain.  Little is
+//   left of p - q there, while the tensor core's z, whose sums it truncates, is off
+//   by up to 1e-4.  So z is summed once more, 1/2048 of the products in each number
+//   of 32 bits and those in 64, and 1 + expm1(z / tau - lse) taken for p; that goes
+//   over G's entry when the kernel of G is done.  (One row of 576, binary16, 1 - p =
+//   0.003: dX off by 2.4e-4, its own rounding; 6.7e-3 without.)
+//
+// Of more rows the certain ones have little part in dX's and dW's size, and no
+// kernel runs beside G's: 300 rows, 32008 words of 1000, 83 us without, 94 with one
+// in front of it.
+__global__ void __launch_bounds__(kRowsThreads) loss_mask_kernel(const __grid_constant__ RowsParams p) {
+    __shared__ double part[kRowsThreads / 32];
+    __shared__ int32_t main;
+    const int32_t i = (int32_t)threadIdx.x, r = (int32_t)blockIdx.x, warp = i / 32, lane = i % 32;
+    grid_launch_dependents();
+    const int32_t t = r % p.period;
+    const int32_t y = t < p.T ? __ldcg(p.flags + t) : -1;
+    if (y >= p.limit && i == 0) atomicCAS(p.err + 1, 0, (int32_t)rg::kBadIds);
+    const bool in = y >= 0 && y < p.limit;
+    float weight = 0.0f;
+    if (warp == 0) {
+        const int32_t word = in && r < p.T ? main_word(p, t, y, weight) : kNone;
+        if (lane == 0) main = word - p.from >= 0 && word - p.from < p.words ? word : kNone;
+    }
+    const int32_t vecs = p.D / 8;
+    if (in) {
+        const uint4* const src = reinterpret_cast<const uint4*>(p.X + (int64_t)t * p.ldx);
+        uint4* const dst = reinterpret_cast<uint4*>(p.gathered + (int64_t)r * p.pitch);
+        for (int32_t c = i; c < vecs; c += kRowsThreads) dst[c] = __ldg(src + c);
+    } else {
+        uint4* const dst = reinterpret_cast<uint4*>(p.gathered + (int64_t)r * p.pitch);
+        for (int32_t c = i; c < vecs; c += kRowsThreads) dst[c] = make_uint4(0, 0, 0, 0);
+    }
+    __syncthreads();
+    const int32_t word = main;
+    if (word != kNone) {
+        double z = some_products(p, t, word);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
+        if (lane == 0) part[warp] = z;
+        __syncthreads();
+    }
+    float top = 0.0f, g = 0.0f;
+    bool sure = false;
+    if (warp == 0) {
+        top = largest_dloss(p.flags, p.limit, p.dloss, p.dloss_stride, p.T);
+        if (word != kNone && lane == 0) {
+            double z = 0.0;
+            for (int32_t j = 0; j < kRowsThreads / 32; ++j) z += part[j];
+            if (p.tau != 1.0f) z /= (double)p.tau;
+            const float rest = expm1f((float)(z - (double)__ldg(p.lse + t)));
+            sure = rest > -0.5f;  // (that leaves one word of a row)
+            g = __ldg(p.dloss + (int64_t)t * p.dloss_stride) * p.grad_scale * scale_of(p.top, p.grad_scale, top) * (rest + (1.0f - weight));
+        }
+        if (r == 0 && lane == 0) write_header(p, p.T, 0, top);
     }
     grid_dependency_wait();
+    if (sure) {
+        uint16_t* const at = p.grad + (int64_t)t * p.grad_pitch + (word - p.from);
+        const uint32_t x = rg::pack16(g, 0.0f, p.bf16);
+        at[0] = (uint16_t)x;
+        if (p.low) at[(int64_t)p.low * p.grad_pitch] = (uint16_t)rg::rest16x2(g, 0.0f, x, p.bf16);
+    }
 }
 
 // ------------------------------------------------------------------ losses
