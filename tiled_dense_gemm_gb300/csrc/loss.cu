@@ -125,6 +125,7 @@ static int run_teacher(const Call& c, const LossPlan& p, int64_t b0, int64_t T, 
         q.T = (int32_t)T;
         q.k = (int32_t)c.k;
         q.V = (int32_t)c.V;
+        q.before = p.masked;
         q.inv_tau = 1.0f / c.tau;
         q.sorted = reinterpret_cast<int32_t*>(c.ws + p.sorted);
         q.weights = reinterpret_cast<float*>(c.ws + p.weights);
@@ -338,6 +339,7 @@ static int run_backward(const Call& c, const LossPlan& p, DeviceState& d) {
             q.K = (int32_t)c.D;
             q.bf16 = c.bf16 ? 1 : 0;
             wanted(c, p, 0, q);
+            q.early = c.ids && p.masked && p0 == 0;  // (behind the teacher's kernel)
             q.w_row = (int32_t)p0;
             q.scale = p.masked ? nullptr : rows;
             q.top = top_of(c);

@@ -109,6 +109,12 @@ struct LossParams {
     // before.  It waits for its predecessor before it ends, so that its end says
     // that all before it is done.
     int32_t late;
+    // kGrad: only the epilogue waits for the predecessor, which lets this launch start
+    // once it has itself waited for all before: the rest reads nothing of what that
+    // one writes (100 rows with a teacher, 32768 words of 1024: 76 us without, 71 with;
+    // kStats is better started before that one's wait, with its first words on their
+    // way into L2: 16 rows, 32000 of 1024, 20.4 and 21.7).
+    int32_t early;
     int32_t once;          // the weights' lines (B; kWeight: its output's) leave L2 first
     uint32_t tmem_cols;    // allocated; half per accumulator
     int32_t bf16;
@@ -475,8 +481,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const Divider by_group((uint32_t)q.group_m * (uint32_t)q.n_tiles), by_rows((uint32_t)q.group_m);
     if (kMode == kStats) grid_launch_dependents();
-    if (!q.late) grid_dependency_wait();
-    if (kMode != kStats) grid_launch_dependents();  // (what follows may go by this wait)
+    const bool early = kAnyGrad && q.early;
+    if (!q.late && !early) grid_dependency_wait();
+    if (kMode != kStats && !early) grid_launch_dependents();  // (what follows may go by this wait)
     const uint32_t tmem_base = ctrl->tmem_addr;
     const uint32_t S = (uint32_t)q.num_stages, stride = q.stage_bytes;
     const uint32_t full0 = smem_u32(&ctrl->full[0]), empty0 = smem_u32(&ctrl->empty[0]);
@@ -650,6 +657,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (G's rows are kWeight's reduction: zeros up to the end of its last k-block)
         const int32_t row_end = !kAnyGrad ? M : kLow ? q.low : (M + kRowPad - 1) / kRowPad * kRowPad;
         uint32_t local = 0, tile = 0;
+        if (early) {
+            grid_dependency_wait();
+            grid_launch_dependents();
+        }
         float scale = 1.0f;
         if constexpr (kAnyGrad) scale = q.scale ? __ldcg(&q.scale->scale) : scale_of(q.top, q.grad_scale, largest_dloss(q.flags, q.limit, q.dloss, q.dloss_stride, q.M));
         if constexpr (kMode == kWeight) scale = __ldcg(&q.scale->unscale);

@@ -17,6 +17,7 @@ struct TeacherParams {
     int64_t ld_ids, ld_logits;
     int32_t logits_type;   // 0 binary16, 1 bfloat16, 2 32 bits
     int32_t T, k, V;
+    int32_t before;        // what follows goes by this kernel's wait
     float inv_tau;
     int32_t* sorted;       // (T, k), kNone behind the last
     float* weights;        // (T, k) q
@@ -49,8 +50,9 @@ __global__ void __launch_bounds__(32 * kTeacherWarps) loss_teacher_kernel(const 
     const int32_t padded = (p.k + 3) & ~3;
     int32_t* const key = reinterpret_cast<int32_t*>(smem) + 2 * warp * padded;
     float* const e = reinterpret_cast<float*>(key + padded);
-    grid_launch_dependents();
+    if (!p.before) grid_launch_dependents();
     grid_dependency_wait();
+    if (p.before) grid_launch_dependents();
     for (int64_t t = (int64_t)blockIdx.x * kTeacherWarps + warp; t < p.T; t += (int64_t)gridDim.x * kTeacherWarps) {
         float top = -INFINITY;
         bool some = false;
