@@ -227,7 +227,10 @@ __device__ __forceinline__ void reduce_add_3d(const CUtensorMap* m, uint32_t src
 
 // A row's wanted words in rising order, from the first at or behind some column.
 // Frequent words come close together, so the word after the next one is on its
-// way while that is dealt with.
+// way while that is dealt with, and they are read through L1: the first tiles hold
+// tens of a row's words, one after another (100 rows, 64 words each, 32768 words of
+// 1024: 34 us from L2, 29 so, the gradients 70 and 61; 4096 rows of 65536 of 2048:
+// 645 and 632).
 struct Wanted {
     int64_t at;      // place of the word after `next` in the lists
     int64_t end;
@@ -250,7 +253,7 @@ struct Wanted {
         int32_t lo = 0, hi = q.k;
         while (lo < hi) {
             const int32_t mid = (lo + hi) >> 1;
-            if (__ldcg(ids + mid) < col)
+            if (ids[mid] < col)
                 lo = mid + 1;
             else
                 hi = mid;
@@ -264,8 +267,8 @@ struct Wanted {
     __device__ __forceinline__ void fetch(const LossParams& q, int32_t& id, float& w) {
         id = kNone;
         if (at < end) {
-            id = __ldcg(q.ids + at);
-            w = __ldcg(q.weights + at);
+            id = q.ids[at];
+            w = q.weights[at];
             ++at;
         }
     }
