@@ -581,6 +581,44 @@ def test_two_streams_and_graphs():
     binding.check_device_error()
 
 
+@pytest.mark.parametrize("T,k", [(1, 3), (30, 40), (100, 7), (200, 40)])
+def test_replays_follow_new_inputs(T, k):
+    """One call behind another in the same memory, nothing waited for in between: each reads its own inputs."""
+    V, D = 2003, 136
+    w = head(V, D, "nk", 1, "bf16")
+
+    def inputs(seed):
+        ids, logits = ref.make_words(T, V, k, seed, 0.1)
+        return [normal((T, D), seed, "bf16"), ref.make_targets(T, V, seed, 0.1).to(DEV), ids.to(DEV), logits.to(DEV), dloss_of(T, seed)]
+
+    def run(x, y, ids, logits, d):
+        a = binding.gemm_relu_xent(x, w, y, b_layout="nk")
+        b = binding.gemm_relu_distill(x, w, ids, logits, 1.5, b_layout="nk")
+        return (*a, *binding.gemm_relu_xent_grad(x, w, y, a[1], d, b_layout="nk"), *b,
+                *binding.gemm_relu_distill_grad(x, w, ids, logits, b[1], d, 1.5, b_layout="nk"))
+
+    sets = [inputs(s) for s in range(40, 48)]
+    want = []
+    for s in sets:
+        want.append(run(*s))
+        torch.cuda.synchronize()
+    held = [t.clone() for t in sets[0]]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        outs = run(*held)
+    got = []
+    for _ in range(3):
+        for s in sets:
+            for t, n in zip(held, s):
+                t.copy_(n)
+            g.replay()
+            got.append([o.clone() for o in outs])
+    torch.cuda.synchronize()
+    binding.check_device_error()
+    for i, o in enumerate(got):
+        assert all(torch.equal(p, q) for p, q in zip(o, want[i % len(sets)])), i
+
+
 def test_two_threads():
     """Two host threads, each on its own stream, with calls of several launches between each other's."""
     import threading

@@ -165,7 +165,7 @@ __device__ __forceinline__ float largest_dloss(const int32_t* flags, int32_t lim
     float top = 0.0f;
     for (int32_t t = (int32_t)threadIdx.x % 32; t < T; t += 32) {
         const int32_t y = __ldcg(flags + t);
-        const float d = __ldg(dloss + (int64_t)t * stride);
+        const float d = dloss[(int64_t)t * stride];
         if (y >= 0 && y < limit) top = fmaxf(top, fabsf(d));
     }
     return warp_max(top);
@@ -689,8 +689,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (live && !q.ids) y = __ldcg(q.targets + t);
                 if constexpr (kAnyGrad) {
                     if (live) {
-                        shift = -1.4426950408889634f * __ldg(q.lse + t);
-                        coef = __ldg(q.dloss + (int64_t)t * q.dloss_stride) * q.grad_scale * scale;
+                        shift = -1.4426950408889634f * q.lse[t];
+                        coef = q.dloss[(int64_t)t * q.dloss_stride] * q.grad_scale * scale;
                     }
                 }
             }

@@ -249,12 +249,12 @@ __global__ void __launch_bounds__(kRowsThreads) loss_rows_kernel(const __grid_co
     float top = 0.0f;
     if (p.dloss) {
         if (p.dloss_stride == 0) {
-            top = fabsf(__ldg(p.dloss));
+            top = fabsf(p.dloss[0]);
         } else {
 #pragma unroll 8
             for (int32_t t = i; t < p.T; t += kRowsThreads) {
                 const int32_t y = __ldcg(p.flags + t);
-                const float d = __ldg(p.dloss + t);
+                const float d = p.dloss[t];
                 if (y >= 0 && y < p.limit) top = fmaxf(top, fabsf(d));
             }
         }
@@ -383,9 +383,9 @@ __global__ void __launch_bounds__(kRowsThreads) loss_mask_kernel(const __grid_co
             double z = 0.0;
             for (int32_t j = 0; j < kRowsThreads / 32; ++j) z += part[j];
             if (p.tau != 1.0f) z /= (double)p.tau;
-            const float rest = expm1f((float)(z - (double)__ldg(p.lse + t)));
+            const float rest = expm1f((float)(z - (double)p.lse[t]));
             sure = rest > -0.5f;  // (that leaves one word of a row)
-            g = __ldg(p.dloss + (int64_t)t * p.dloss_stride) * p.grad_scale * scale_of(p.top, p.grad_scale, top) * (rest + (1.0f - weight));
+            g = p.dloss[(int64_t)t * p.dloss_stride] * p.grad_scale * scale_of(p.top, p.grad_scale, top) * (rest + (1.0f - weight));
         }
         if (r == 0 && lane == 0) write_header(p, p.T, 0, top);
     }
