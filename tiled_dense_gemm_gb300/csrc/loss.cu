@@ -74,10 +74,10 @@ static int launch_tiles(DeviceState& d, const TilePlan& t, const LossMaps& m, co
 // Up to so many rows (four row tiles of a pair) the weights are read from memory,
 // and their gradients written, with lines that leave L2 first: they are met once
 // or by CTAs that run together, and otherwise push out what is reused (us, without
-// / with; 32768 words of 1024: one row 17.9 / 16.5, gradients 48.6 / 46.2; 65536 of
-// 2048: 16 rows 51.6 / 45.4, 152 / 150; 100 rows 53.7 / 49.9, 161 / 153; 300 98 /
-// 93, 258 / 252; 32768 of 1024, 1000 rows: 57 / 56, 151.5 / 149.9; but 65536 of
-// 4096, 4096 rows: 1280 / 1302, 3974 / 4050).
+// / with; 32768 words of 1024: one row 18.0 / 16.6, gradients 50.3 / 46.6; 65536 of
+// 2048: 16 rows 52.2 / 46.1, 147 / 132; 100 rows 54.5 / 50.6, 158 / 146; 300 97 /
+// 93, 259 / 249; 32768 of 1024, 1000 rows: 56 / 56, 155.5 / 152.8; but 65536 of
+// 4096, 4096 rows: 1185 / 1188, 3903 / 3947).
 constexpr int64_t kStreamRows = 1024;
 
 template <int kMode>
@@ -157,7 +157,7 @@ static int run_rows(const Call& c, const LossPlan& p, int64_t b0, int64_t T, Dev
     q.ldx = c.ldx;
     q.pitch = (int32_t)p.pitch;
     // X's pitch not a multiple of 128 bytes: the copy's is (5000 rows, 50021 words of
-    // 1544: 516 us from X, 494 from the copy; the gradients 1752 and 1644).
+    // 1544: 547 us from X, 536 from the copy; the gradients 1856 and 1805).
     q.always = T > 128 && (c.ldx % 64 != 0 || misaligned(q.X, 128));
     q.gathered = reinterpret_cast<uint16_t*>(c.ws + p.gathered);
     q.index = reinterpret_cast<int32_t*>(c.ws + p.index);

@@ -6,11 +6,12 @@
 //   kStats   per row and tile: m = max z, s = sum 2^(c (z - m)),
 //            t = sum of q z over the wanted words among them        (no z is kept)
 //   kGrad    G[t, v] = a_t (2^(c z - log2(e) lse_t) - sum of q of the wanted word v)
-//            over a piece of the vocabulary, rounded to the 16-bit type
+//            over a piece of the vocabulary, rounded to the 16-bit type; kGradLow, up to
+//            32 rows: in two parts, the rounded value and the rounded rest
 //   kSum     dX += G W over the piece, in 32 bits, split along the piece
 //   kWeight  dW[piece] = G^T X
 //
-// One kernel, four epilogues: D = A B^T in tiles of 128 rows x `width` columns
+// One kernel, five epilogues: D = A B^T in tiles of 128 rows x `width` columns
 // per CTA, or 256 x `width` per CTA pair, over k-blocks of 64 or 128.  An operand's
 // reduction index is contiguous ("k-major": boxes of 64 k x rows) or its rows'
 // index is ("mn-major": chunks of 64 rows x the k-block), as the matrices are
@@ -34,15 +35,16 @@
 //     162 us, 6.6 TB/s of weights; 16 rows, 65536 of 2048: 45 us; one row, 32000
 //     of 1024: 16.0 us, of which 6.4 are left with next to no words.  (Boxes of 256
 //     k: 5-15% slower; tiles of 64 to 112 words 5-60%.)  The gradients pass the
-//     weights three times (G, dX, dW): 16 rows, 65536 of 2048: 150 us.
+//     weights three times (G, dX, dW): 16 rows, 65536 of 2048: 132 us, 6.1 TB/s of
+//     those; 128 rows, 131072 of 4096: 522 us, 6.2 TB/s.
 //   many rows, alone: bytes from L2 into the multiprocessors, 13.4-14.2 TB/s in
 //     every product (a pair takes in 64 KB per 512 clocks of the tensor core, which
 //     at 1.8 GHz would be 17.5 TB/s): the tensor pipe is active 72-81% of the time.
 //   many rows, back to back: the power cap.  8192 rows, 131072 words of 4096: 5.1-
 //     5.3 ms, 1660-1730 TFLOP/s at 1.5 GHz, what the library product sustains; the
-//     gradients of 4096 rows 7.7-7.9 ms.
+//     gradients of 4096 rows 7.7-8.0 ms.
 //   rows whose pitch is not a multiple of 128 bytes cost a second line per box
-//     row: 50021 words of 2056, 1800 of 3000 rows in use, 262 (bfloat16) - 280 us.
+//     row: 50021 words of 2056, 1800 of 3000 rows in use, 266-290 us.
 #pragma once
 
 #include "ragged_kernel.cuh"
@@ -464,8 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (!kPair && kMode != kWeight) {
         // Few rows: the weights' way from memory is all there is, so the first item's
         // are asked for in L2 before the kernel before is waited for (a line that it
-        // still writes is current there): one row, 32000 words of 1024, 19.0 us without,
-        // 17.6 with.
+        // still writes is current there): 1.4 us less for one row, 32000 words of 1024.
         if (warp == 6 && lane == 0) {
             const uint32_t split = worker / (uint32_t)q.n_tiles, nt = worker - split * (uint32_t)q.n_tiles;
             const int32_t blocks = (q.K + q.bk - 1) / q.bk;

@@ -335,14 +335,14 @@ __device__ __forceinline__ double some_products(const RowsParams& p, int32_t t, 
 // * a copy of X with zeros in the rows that are not in use, for dW, and the scale;
 // * the gradient at the row's main word, if that is all but certain.  Little is
 //   left of p - q there, while the tensor core's z, whose sums it truncates, is off
-//   by up to 1e-4.  So z is summed once more, 1/2048 of the products in each number
+//   by 2e-5 (z = 19 over 576; more over more).  So z is summed once more, 1/2048 of the products in each number
 //   of 32 bits and those in 64, and 1 + expm1(z / tau - lse) taken for p; that goes
 //   over G's entry when the kernel of G is done.  (One row of 576, binary16, 1 - p =
 //   0.003: dX off by 2.4e-4, its own rounding; 6.7e-3 without.)
 //
-// Of more rows the certain ones have little part in dX's and dW's size, and no
-// kernel runs beside G's: 300 rows, 32008 words of 1000, 83 us without, 94 with one
-// in front of it.
+// Of more rows the certain ones have little part in dX's and dW's size, and G's
+// kernel leaves no room beside it: 300 rows, 32008 words of 1000 by columns, 83 us
+// without, 94 with a kernel in front of it.
 __global__ void __launch_bounds__(kRowsThreads) loss_mask_kernel(const __grid_constant__ RowsParams p) {
     __shared__ double part[kRowsThreads / 32];
     __shared__ int32_t main;
