@@ -372,7 +372,8 @@ typedef enum {
  * overlap (two streams, two captured graphs) need one each.  Nothing in it has to
  * be set, and nothing is kept in it.  gemm_relu_loss_workspace (host only) returns
  * bytes, or minus a gemm_status_t; k = 0 for targets.  The gradients' is about
- * T V 2 bytes or 512 MiB, whichever is less, + T D 4 (once or for up to 16 shares).
+ * T V 2 bytes (up to 32 rows, rounded up to eights, twice that) or 512 MiB,
+ * whichever is less, + T D 4 (once or for up to 64 shares).
  * Asynchronous on `stream`; bounded waits and the error word as gemm_relu.
  */
 int64_t gemm_relu_loss_workspace(int64_t T, int64_t V, int64_t D, int64_t k, int gradient);
