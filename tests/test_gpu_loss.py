@@ -264,6 +264,25 @@ def test_pitches_and_given_outputs():
     binding.check_device_error()
 
 
+@pytest.mark.parametrize("T", [1, 20, 32, 33, 100, 300])
+@pytest.mark.parametrize("layout", ["nk", "kn"])
+def test_one_gradient_alone(T, layout):
+    """dX or dW without the other: the same bits."""
+    V, D, k = 2000, 200, 4
+    x, w = normal((T, D), T, "f16"), head(V, D, layout, 2, "f16")
+    y, (ids, logits), d = ref.make_targets(T, V, 3, 0.2).to(DEV), ref.make_words(T, V, k, 4, 0.2), dloss_of(T, 5)
+    ids, logits = ids.to(DEV), logits.to(DEV)
+    _, lse = binding.gemm_relu_xent(x, w, y, b_layout=layout)
+    _, lse2 = binding.gemm_relu_distill(x, w, ids, logits, 2.0, b_layout=layout)
+    for call in (lambda **a: binding.gemm_relu_xent_grad(x, w, y, lse, d, b_layout=layout, **a),
+                 lambda **a: binding.gemm_relu_distill_grad(x, w, ids, logits, lse2, d, 2.0, b_layout=layout, **a)):
+        dx, dw = call()
+        one, none = call(want_dw=False)
+        none2, two = call(want_dx=False)
+        assert none is none2 is None and torch.equal(one, dx) and torch.equal(two, dw)
+    binding.check_device_error()
+
+
 def test_gradient_of_broadcast_losses():
     """One value for all rows (a mean's gradient): one element, or an expanded view, as that value in each row."""
     T, V, D = 200, 300, 64
