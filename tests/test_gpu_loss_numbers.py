@@ -1,0 +1,89 @@
+"""How exact the losses over a vocabulary are, where their own rounding shows:
+words that are all but certain, long reductions, small temperatures.
+
+Every case has logits, or sums, whose error is known: either all products and
+sums are exact in 32 bits (few bits each), or the tensor core's truncation is
+bounded.  It cuts products and sums to 24 bits of the largest at least, so n
+products of one sign and s in sum lose at most n 2^-23 s (about a sixteenth to a
+tenth of that measured); a reduction in parts of n, added up in registers, at
+most (n + number of parts) 2^-23 s.
+
+Softmax, up to 256 words (E32 = 2^-23, half of it per rounding):
+
+    s = sum 2^(c (z - max))   the maximum's own term is 1; a term of the sum goes through at most 16 additions in its
+                              group of columns, 2 that join the groups, 1 from chunk to chunk, 3 from half to half and
+                              3 per tile (4 at most): 34 roundings, 17 E32; twice that is allowed
+    2^x                       2 units of 2^-23 and what x is off by, which is 3 roundings of it
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import loss_ref as ref
+from tiled_dense_gemm_gb300 import binding
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda", 0)
+DT = {"f16": torch.float16, "bf16": torch.bfloat16}
+BOTH = [("nk", "f16"), ("kn", "f16"), ("nk", "bf16"), ("kn", "bf16")]
+E32 = ref.E32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from tiled_dense_gemm_gb300 import build
+    build.build()
+    torch.cuda.set_device(DEV)
+    yield
+    torch.cuda.synchronize()
+
+
+def laid_out(w, layout):
+    return w if layout == "nk" else w.t().contiguous()
+
+
+def exact_logits(T, V, dtype, best):
+    """Rows, weights (V, 16) and their logits, of few bits each so that every sum of products is exact: word `best`
+    at 40 to 104, the others 12 to 16 below it."""
+    x, w = torch.zeros(T, 16), torch.zeros(V, 16)
+    t, v = torch.arange(T), torch.arange(V)
+    x[:, 0], x[:, 1], x[:, 2] = (40 + (t * 37) % 64).float(), ((t * 5) % 8).float() / 8, 1.0
+    w[:, 0], w[:, 1], w[:, 2] = 1.0, 1.0, -(12 + ((v * 7) % 32).float() / 8)
+    w[best, 2] = 0.0
+    x, w = x.to(DT[dtype]), w.to(DT[dtype])
+    return x.to(DEV), w.to(DEV), (x.double() @ w.double().t()).numpy()
+
+
+def logsumexp(z):
+    top = z.max(axis=1, keepdims=True)
+    rest = np.exp(z - top)
+    rest[np.arange(len(z)), z.argmax(axis=1)] = 0.0
+    return top[:, 0] + np.log1p(rest.sum(axis=1)), np.log1p(rest.sum(axis=1))  # lse, lse - max
+
+
+@pytest.mark.parametrize("tau", [1.0, 0.5])
+@pytest.mark.parametrize("layout,dtype", BOTH)
+@pytest.mark.parametrize("T", [1, 20, 128, 129, 300])
+def test_loss_of_a_certain_word(T, layout, dtype, tau):
+    """The wanted word is the maximum: its loss is the logarithm of a sum that is at least 1, so never negative, and
+    off by that sum's roundings alone, however large the logits are."""
+    V = 200
+    for best in (0, 70, V - 1):
+        x, w, z = exact_logits(T, V, dtype, best)
+        lse, loss = logsumexp(z / tau)
+        if tau == 1.0:
+            y = torch.full((T,), best, dtype=torch.int32, device=DEV)
+            got, got_lse = binding.gemm_relu_xent(x, laid_out(w, layout), y, b_layout=layout)
+        else:
+            ids = torch.full((T, 3), -1, dtype=torch.int32, device=DEV)
+            ids[:, 1] = best
+            got, got_lse = binding.gemm_relu_distill(x, laid_out(w, layout), ids, torch.zeros(T, 3, device=DEV), tau, b_layout=layout)
+        binding.check_device_error()
+        got, got_lse = got.double().cpu().numpy(), got_lse.double().cpu().numpy()
+        e = 34 * E32
+        assert (got >= 0).all(), f"{(got < 0).sum()} negative losses, least {got.min()}"
+        assert (np.abs(got - tau ** 2 * loss) <= tau ** 2 * (e + 64 * E32 * loss)).all(), np.abs(got - tau ** 2 * loss).max()
+        assert (np.abs(got_lse - lse) <= e + E32 * lse).all(), np.abs(got_lse - lse).max()

@@ -766,12 +766,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 4; j < 64; ++j) top[j % 4] = fmaxf(top[j % 4], v[j]);
                     const float m_new = fmaxf(fmaxf(m_run, fmaxf(top[0], top[1])), fmaxf(top[2], top[3]));
-                    // (infinite maxima: the terms are taken as they are, so that the sum says what the row holds)
-                    const float off = fabsf(m_new) == INFINITY ? 0.0f : -m_new * c;
+                    // (infinite maxima: the terms are taken as they are, so that the sum says what the row holds.
+                    // The difference before the product: the maximum's own term is then 1, where v c - m c, its
+                    // second product rounded, was off by half a unit of m c: at z = 100 5e-6 of a sum that a nearly
+                    // certain word leaves at 1, so that half of such losses came out negative)
+                    const float ref = fabsf(m_new) == INFINITY ? 0.0f : m_new;
                     float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) sum[j % 4] += exp2_fast(fmaf(v[j], c, off));
-                    s_run = fmaf(s_run, exp2_fast(fmaf(m_run, c, off)), (sum[0] + sum[1]) + (sum[2] + sum[3]));
+                    for (int j = 0; j < 64; ++j) sum[j % 4] += exp2_fast((v[j] - ref) * c);
+                    s_run = fmaf(s_run, exp2_fast((m_run - ref) * c), (sum[0] + sum[1]) + (sum[2] + sum[3]));
                     m_run = m_new;
                 }
                 // The two halves' as one: the second hands its numbers to the first in one
