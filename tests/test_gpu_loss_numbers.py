@@ -41,6 +41,11 @@ def _built():
     torch.cuda.synchronize()
 
 
+def dloss_of(T, seed):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.rand(T, generator=g) + 0.25).mul_(1.0 / max(T, 1)).to(DEV)
+
+
 def laid_out(w, layout):
     return w if layout == "nk" else w.t().contiguous()
 
@@ -87,3 +92,44 @@ def test_loss_of_a_certain_word(T, layout, dtype, tau):
         assert (got >= 0).all(), f"{(got < 0).sum()} negative losses, least {got.min()}"
         assert (np.abs(got - tau ** 2 * loss) <= tau ** 2 * (e + 64 * E32 * loss)).all(), np.abs(got - tau ** 2 * loss).max()
         assert (np.abs(got_lse - lse) <= e + E32 * lse).all(), np.abs(got_lse - lse).max()
+
+
+def check_gradients(got, g, e, x, w, layout, dtype, T, dw_steps, dx_steps, a):
+    """dX and dW of g (T, V), each entry off by e before it is rounded to the type."""
+    u, dt = ref.UNIT[DT[dtype]], DT[dtype]
+    tiny = 2.0 ** -39 * np.abs(a).max() if dtype == "f16" else ref.TINY[dt]
+    e = e + u ** (2 if T <= 32 else 1) * (np.abs(g) + e) + tiny
+    n, X, W = np.abs(g) + e, x.double().cpu().numpy(), w.double().cpu().numpy()
+    done = lambda v, b: (v, b + u * (np.abs(v) + b) + ref.TINY[dt])  # noqa: E731
+    dx, dw = got
+    ref.check(dx, done(g @ W, e @ np.abs(W) + dx_steps * E32 * (n @ np.abs(W))), "dx")
+    value, bound = done(g.T @ X, e.T @ np.abs(X) + dw_steps * E32 * (n.T @ np.abs(X)))
+    ref.check(dw if layout == "nk" else dw.t(), (value, bound), "dw")
+
+
+@pytest.mark.parametrize("tau", [1.0, 0.5])
+@pytest.mark.parametrize("layout,dtype", BOTH)
+@pytest.mark.parametrize("T", [20, 100, 129, 300])
+def test_gradient_of_a_certain_word(T, layout, dtype, tau):
+    """exp(z / tau - lse) - 1 for a given lse: z and the difference are exact in 32 bits, so what is left of the
+    gradient is off by the exponential's own error, not by roundings of z and lse (up to 2^-17 of 104)."""
+    V, best = 200, 70
+    x, w, z = exact_logits(T, V, dtype, best)
+    lse = torch.from_numpy(logsumexp(z / tau)[0]).float()
+    d = dloss_of(T, 3) * (256 * T)
+    if tau == 1.0:
+        y = torch.full((T,), best, dtype=torch.int32, device=DEV)
+        got = binding.gemm_relu_xent_grad(x, laid_out(w, layout), y, lse.to(DEV), d, b_layout=layout)
+    else:
+        ids = torch.full((T, 2), best, dtype=torch.int32, device=DEV)
+        ids[:, 1] = -1
+        got = binding.gemm_relu_distill_grad(x, laid_out(w, layout), ids, torch.zeros(T, 2, device=DEV), lse.to(DEV), d, tau, b_layout=layout)
+    binding.check_device_error()
+    arg = z / tau - lse.double().numpy()[:, None]
+    p, a = np.exp(arg), d.double().cpu().numpy()[:, None] * tau
+    g = p.copy()
+    g[:, best] = np.expm1(arg[:, best])
+    # (two roundings of the factor, one each of the product and the difference)
+    e = np.abs(a) * (p * (2 + 3 * np.abs(arg) + 2) * E32)
+    e[:, best] += np.abs(a)[:, 0] * 2 * E32
+    check_gradients(got, a * g, e, x, w, layout, dtype, T, T, V + 32, a)

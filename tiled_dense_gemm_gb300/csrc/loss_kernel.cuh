@@ -5,7 +5,7 @@
 //
 //   kStats   per row and tile: m = max z, s = sum 2^(c (z - m)),
 //            t = sum of q z over the wanted words among them        (no z is kept)
-//   kGrad    G[t, v] = a_t (2^(c z - log2(e) lse_t) - sum of q of the wanted word v)
+//   kGrad    G[t, v] = a_t (2^(c (z - tau lse_t)) - sum of q of the wanted word v)
 //            over a piece of the vocabulary, rounded to the 16-bit type; kGradLow, up to
 //            32 rows: in two parts, the rounded value and the rounded rest
 //   kSum     dX += G W over the piece, in 32 bits, split along the piece
@@ -690,7 +690,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (live && !q.ids) y = __ldcg(q.targets + t);
                 if constexpr (kAnyGrad) {
                     if (live) {
-                        shift = -1.4426950408889634f * q.lse[t];
+                        // (what a logit is less, so that the difference comes before the product with c: next to
+                        // 1, p is off by roundings of the difference, not of lse log2(e), 5e-6 for an lse of 100)
+                        shift = q.grad_scale * q.lse[t];
                         coef = q.dloss[(int64_t)t * q.dloss_stride] * q.grad_scale * scale;
                     }
                 }
@@ -835,7 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     while (want.next < c0) want.advance(q);  // (of the other half's chunk)
 #pragma unroll
                     for (int j = 0; j < 64; ++j) {
-                        const float p = coef * exp2_fast(fmaf(v[j], c, shift));
+                        const float p = coef * exp2_fast((v[j] - shift) * c);
                         v[j] = live && col + j < q.N ? p : 0.0f;
                     }
                     if (here < 64 || kLow) {
