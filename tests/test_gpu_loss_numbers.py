@@ -133,3 +133,50 @@ def test_gradient_of_a_certain_word(T, layout, dtype, tau):
     e = np.abs(a) * (p * (2 + 3 * np.abs(arg) + 2) * E32)
     e[:, best] += np.abs(a)[:, 0] * 2 * E32
     check_gradients(got, a * g, e, x, w, layout, dtype, T, T, V + 32, a)
+
+
+def nearly_certain(T, D, V, dtype, seed, size=24.0):
+    """Rows along the weights of a word each, whose logit is about `size`; another word's is half of that.  All
+    products of the largest logits have one sign, where truncation takes most."""
+    gen = torch.Generator().manual_seed(seed)
+    w = (torch.randn(V, D, generator=gen) * 2 * D ** -0.5).to(DT[dtype])
+    half = V // 2
+    w[half:] = (0.5 * w[:half].float()).to(DT[dtype])
+    y = torch.randint(0, half, (T,), generator=gen, dtype=torch.int32)
+    rows = w[y.long()].float()
+    lift = size + 8 * torch.rand(T, 1, generator=gen)
+    x = (lift * rows / rows.pow(2).sum(dim=1, keepdim=True)).to(DT[dtype])
+    return x.to(DEV), w.to(DEV), y.to(DEV)
+
+
+def truncated(T, x, w, parts_of):
+    """What z may be off by, z summed in parts of so many products."""
+    D = x.shape[1]
+    size = x.double().cpu().numpy(), w.double().cpu().numpy()
+    return np.abs(size[0]) @ np.abs(size[1]).T * E32 * (min(D, parts_of) + math.ceil(D / parts_of))
+
+
+@pytest.mark.parametrize("layout,dtype", BOTH)
+@pytest.mark.parametrize("T,D", [(129, 2056), (300, 4096), (300, 1544)])
+def test_gradients_of_certain_words_with_the_forward_pass_own_lse(T, D, layout, dtype):
+    """The true gradient, with lse as the forward call returned it: both passes sum a logit alike (or exactly), so
+    what the tensor core truncates of it takes the same part of 1 - p, not of p."""
+    V = 64
+    x, w, y = nearly_certain(T, D, V, dtype, T + D)
+    z = x.double().cpu().numpy() @ w.double().cpu().numpy().T
+    lse, loss = logsumexp(z)
+    d = dloss_of(T, 3) * (256 * T)
+    _, got_lse = binding.gemm_relu_xent(x, laid_out(w, layout), y, b_layout=layout)
+    got = binding.gemm_relu_xent_grad(x, laid_out(w, layout), y, got_lse, d, b_layout=layout)
+    binding.check_device_error()
+    at, a = (np.arange(T), y.cpu().numpy()), d.double().cpu().numpy()[:, None]
+    p = np.exp(z - lse[:, None])
+    g, rest = p.copy(), -np.expm1(-loss)  # 1 - p of the wanted word
+    g[at] = -rest
+    b = truncated(T, x, w, 256 if T <= 128 else 1024).max(axis=1)
+    arg = np.abs(z - lse[:, None])
+    # lse: its own rounding and its sum's; the exponential's argument and value
+    shift = E32 / 2 * lse + 25 * E32 / 2
+    e = p * (2 * b[:, None] + shift[:, None] + (4 + 3 * arg) * E32)
+    e[at] = rest * 2 * b + shift + 8 * E32
+    check_gradients(got, a * g, a * e, x, w, layout, dtype, T, T, V + 32, a)

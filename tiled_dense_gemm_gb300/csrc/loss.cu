@@ -57,10 +57,10 @@ static int encode_sums(CUtensorMap* map, void* ptr, int64_t D, int64_t T, int64_
     return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_INVALID_ARG;
 }
 
-template <bool kPair, int kMode>
-static int launch_tiles(DeviceState& d, const TilePlan& t, const LossMaps& m, const LossParams& q, cudaStream_t st) {
-    auto fn = loss_kernel<kPair, kMode>;
-    bool& set = d.ls_attr_set[2 * kMode + (kPair ? 1 : 0)];
+template <bool kPair, int kMode, bool kMany>
+static int launch_kernel(DeviceState& d, const TilePlan& t, const LossMaps& m, const LossParams& q, cudaStream_t st) {
+    auto fn = loss_kernel<kPair, kMode, kMany>;
+    bool& set = d.ls_attr_set[4 * kMode + 2 * kMany + kPair];
     if (!set) {
         if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, rt::kMaxDynSmem) != cudaSuccess) {
             cudaGetLastError();
@@ -69,6 +69,13 @@ static int launch_tiles(DeviceState& d, const TilePlan& t, const LossMaps& m, co
         set = true;
     }
     return launch(fn, t.grid, kThreads, (size_t)t.smem_bytes, kPair ? 2 : 1, st, m, q);
+}
+
+template <bool kPair, int kMode>
+static int launch_tiles(DeviceState& d, const TilePlan& t, const LossMaps& m, const LossParams& q, cudaStream_t st) {
+    if constexpr (kMode == kGrad || kMode == kGradLow)
+        if (q.K <= Parts<kPair, kMode, true>::kPart) return launch_kernel<kPair, kMode, false>(d, t, m, q, st);
+    return launch_kernel<kPair, kMode, true>(d, t, m, q, st);
 }
 
 // Up to so many rows (four row tiles of a pair) the weights are read from memory,

@@ -234,16 +234,16 @@ __device__ __forceinline__ void reduce_add_3d(const CUtensorMap* m, uint32_t src
 // 1024: 34 us from L2, 29 so, the gradients 70 and 61; 4096 rows of 65536 of 2048:
 // 645 and 632).
 struct Wanted {
-    int64_t at;      // place of the word after `next` in the lists
-    int64_t end;
-    int32_t next;    // word, kNone: no more
-    float weight;    // its
+    int32_t row, at;  // row of the lists, place of the word after `next2` in it
+    int32_t next;     // word, kNone: no more
+    float weight;     // its
     int32_t next2;
     float weight2;
 
     // `y`: the row's target where there is no teacher
-    __device__ __forceinline__ void start(const LossParams& q, int32_t row, int32_t y, bool live, int32_t col) {
-        at = end = 0;
+    __device__ __forceinline__ void start(const LossParams& q, int32_t t, int32_t y, bool live, int32_t col) {
+        row = t;
+        at = q.k;
         next = next2 = kNone;
         weight = weight2 = 1.0f;
         if (!live) return;
@@ -260,17 +260,17 @@ struct Wanted {
             else
                 hi = mid;
         }
-        at = (int64_t)row * q.k + lo;
-        end = (int64_t)(row + 1) * q.k;
+        at = lo;
         fetch(q, next, weight);
         fetch(q, next2, weight2);
     }
 
     __device__ __forceinline__ void fetch(const LossParams& q, int32_t& id, float& w) {
         id = kNone;
-        if (at < end) {
-            id = q.ids[at];
-            w = q.weights[at];
+        if (at < q.k) {
+            const int64_t i = (int64_t)row * q.k + at;
+            id = q.ids[i];
+            w = q.weights[i];
             ++at;
         }
     }
@@ -293,22 +293,35 @@ __device__ __forceinline__ float pick(const float (&v)[kSize], int32_t at) {
     }
 }
 
-// kStats: the reduction in parts of at most this many k, each in an accumulator
-// of its own, added up in registers.  The tensor core truncates its sums in 32
-// bits, 16 products at a time, always towards zero: over 4096 that was 2.4e-6 of
-// the losses (6e-7 for a sum that rounds).  Pairs: 5.4e-7 in parts of 1024, which
-// cost nothing; parts of 512 3e-7, at 4096 rows, 65536 words of 2048 682 us for
-// 645.  Single CTAs, which wait for memory: 1.3e-7 in parts of 256 (64 rows, 131072
-// words of 4096: 162.1 -> 163.5 us), 9e-8 in parts of 128 (169.4).
+// The logits' reduction in parts of at most this many k, each in an accumulator of
+// its own, added up in registers.  The tensor core truncates its sums in 32 bits, 16
+// products at a time, always towards zero: over 4096 that was 2.4e-6 of the losses
+// (6e-7 for a sum that rounds).  Pairs: 5.4e-7 in parts of 1024, which cost
+// nothing; parts of 512 3e-7, at 4096 rows, 65536 words of 2048 682 us for 645.
+// Single CTAs, which wait for memory: 1.3e-7 in parts of 256 (64 rows, 131072 words
+// of 4096: 162.1 -> 163.5 us), 9e-8 in parts of 128 (169.4).  The gradients take the
+// same parts, so that what is left of the truncation is the same in z and in lse and
+// drops out of their difference.
 constexpr int32_t kPartPair = 1024, kPartSingle = 256;
+constexpr int32_t kPartSum = 1 << 30;  // (the gradients' sums: one part)
 
-template <bool kPair>
-__device__ __forceinline__ int32_t part_count(const LossParams& q) {
-    constexpr int32_t kPart = kPair ? kPartPair : kPartSingle;
-    return (q.K + kPart - 1) / kPart;
-}
+// In steps of 128 k, whatever a stage holds.  kMany: there may be several.
+template <bool kPair, int kMode, bool kMany>
+struct Parts {
+    static constexpr bool kLogits = kMode == kStats || kMode == kGrad || kMode == kGradLow;
+    static constexpr int32_t kPart = !kMany ? 1 << 30 : !kLogits ? kPartSum : kPair ? kPartPair : kPartSingle;
+    int32_t first, last, steps, count, two;
 
-__device__ __forceinline__ int32_t part_end(int32_t blocks, int32_t part, int32_t parts) { return part * blocks / parts; }
+    // blocks [kb0, kb1) of `bk` k
+    __device__ __forceinline__ Parts(int32_t kb0, int32_t kb1, int32_t bk) : first(kb0), last(kb1), two(bk == 64 ? 1 : 0) {
+        steps = (kb1 - kb0 + two) >> two;
+        count = (steps + kPart / 128 - 1) / (kPart / 128);
+    }
+    // one behind the last block of part `part` - 1
+    __device__ __forceinline__ int32_t end(int32_t part) const {
+        return min(last, first + ((int32_t)((int64_t)part * steps / count) << two));
+    }
+};
 
 // Division by a number that many items share.
 struct Divider {
@@ -327,25 +340,51 @@ struct Divider {
     }
 };
 
-// 64 numbers times a factor, rounded to the 16-bit type.
-__device__ __forceinline__ void pack_64(uint32_t (&x)[32], const float (&v)[64], float u, int32_t bf16) {
+// Eight columns of a row times a factor, rounded to the 16-bit type; kRest: what that
+// rounding left of them (u 1), rounded.
+template <int kBf16, bool kRest>
+__device__ __forceinline__ uint4 pack_8(const float (&v)[64], int at, float u) {
+    uint32_t x[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float a = u * v[at + 2 * j], b = u * v[at + 2 * j + 1];
+        x[j] = pack16(a, b, kBf16);
+        if (kRest) x[j] = rg::rest16x2(a, b, x[j], kBf16);
+    }
+    return make_uint4(x[0], x[1], x[2], x[3]);
+}
+
+// A chunk of 64 columns to a row of the staging buffer, and the first `here` of them
+// (a multiple of 8) to memory: one branch on the type per chunk.
+template <bool kRest>
+__device__ __forceinline__ void stage_64(uint32_t row, uint32_t lane, const float (&v)[64], float u, int32_t bf16) {
     if (bf16) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) x[j] = pack16(u * v[2 * j], u * v[2 * j + 1], 1);
+        for (uint32_t i = 0; i < 8; ++i) rg::st_shared_v4(row + ((i ^ (lane & 7u)) << 4), pack_8<1, kRest>(v, 8 * i, u));
     } else {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) x[j] = pack16(u * v[2 * j], u * v[2 * j + 1], 0);
+        for (uint32_t i = 0; i < 8; ++i) rg::st_shared_v4(row + ((i ^ (lane & 7u)) << 4), pack_8<0, kRest>(v, 8 * i, u));
     }
 }
 
-// What that rounding left of them, rounded.
-__device__ __forceinline__ void rest_64(uint32_t (&x)[32], const float (&v)[64], int32_t bf16) {
+__device__ __forceinline__ void stage_32(uint32_t row, uint32_t lane, const float (&v)[64], int at) {
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i)
+        rg::st_shared_v4(row + ((i ^ (lane & 7u)) << 4),
+                         make_uint4(__float_as_uint(v[at + 4 * i]), __float_as_uint(v[at + 4 * i + 1]),
+                                    __float_as_uint(v[at + 4 * i + 2]), __float_as_uint(v[at + 4 * i + 3])));
+}
+
+template <bool kRest>
+__device__ __forceinline__ void store_64(uint16_t* dst, const float (&v)[64], int32_t here, int32_t bf16) {
     if (bf16) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) x[j] = rg::rest16x2(v[2 * j], v[2 * j + 1], x[j], 1);
+        for (int i = 0; i < 8; ++i)
+            if (8 * i < here) reinterpret_cast<uint4*>(dst)[i] = pack_8<1, kRest>(v, 8 * i, 1.0f);
     } else {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) x[j] = rg::rest16x2(v[2 * j], v[2 * j + 1], x[j], 0);
+        for (int i = 0; i < 8; ++i)
+            if (8 * i < here) reinterpret_cast<uint4*>(dst)[i] = pack_8<0, kRest>(v, 8 * i, 1.0f);
     }
 }
 
@@ -417,7 +456,10 @@ __device__ __forceinline__ void finish_dx(const FinishParams& p, int32_t threads
         finish_lanes<1>(p, threads);
 }
 
-template <bool kPair, int kMode>
+// kMany false: reductions of one part (kGrad, whose epilogue is slower by 1.4 us a tile
+// with room for several parts' sums: 300 rows, 32008 words of 1000 by columns, 82.8 us
+// without, 85.5 with).
+template <bool kPair, int kMode, bool kMany>
 __global__ void __launch_bounds__(kThreads, 1)
     loss_kernel(const __grid_constant__ LossMaps maps, const __grid_constant__ LossParams q) {
     constexpr int kCG = kPair ? 2 : 1;
@@ -602,14 +644,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t a_step = q.a_mn ? 128u : 2u, b_step = q.b_mn ? 128u : 2u;
             const uint64_t a_next = q.a_mn ? 512u : (q.a_bytes / 2) >> 4, b_next = q.b_mn ? 512u : (b_rows * 128u) >> 4;
             const bool two = q.bk == 128;
-            const int32_t parts = kMode == kStats ? part_count<kPair>(q) : 1;
             uint32_t s = 0, ph = 0, local = 0;
             bool ok = true;
             while (ok && next(k)) {
-                if (k.kb0 == k.kb1) continue;
+                const Parts<kPair, kMode, kMany> parts(k.kb0, k.kb1, q.bk);
                 int32_t kb = k.kb0;
-                for (int32_t part = 1; ok && part <= parts; ++part) {
-                    const int32_t begin = kb, end = kMode == kStats ? part_end(k.kb1, part, parts) : k.kb1;
+                for (int32_t part = 1; ok && part <= parts.count; ++part) {
+                    const int32_t begin = kb, end = parts.end(part);
                     const uint32_t buf = local & 1u, bph = (local >> 1) & 1u;
                     if (!wait_phase(tempty0 + 8u * buf, bph ^ 1u, ctrl, w, rg::kErrAccum)) {
                         ok = false;
@@ -674,7 +715,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
         };
         while (next(k)) {
-            const bool some = k.kb1 > k.kb0;
             const int32_t row0 = k.mt * kTileM + 128 * (int32_t)rank + 32 * (int32_t)quarter;
             const int32_t r = row0 + (int32_t)lane, n0 = k.nt * q.width;
             bool live = r < M;
@@ -708,39 +748,49 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             };
             const float c = q.log2_scale;
-            if constexpr (kMode == kStats) {
-                // z of this warp's chunks, summed over the parts of the reduction
-                float z[2][64];
+            // This warp's chunks of the tile, summed over the parts of the reduction: kStats all of
+            // them, elsewhere the last part is added chunk by chunk as they are written (mostly
+            // it is the only one).
+            float z[2][64];
+            const Parts<kPair, kMode, kMany> parts(k.kb0, k.kb1, q.bk);
+            uint32_t taddr = 0;
+            auto filled = [&]() {  // the accumulator of the next part
+                const uint32_t buf = local & 1u, bph = (local >> 1) & 1u;
+                taddr = tmem_base + ((quarter * 32u) << 16) + buf * buf_cols;
+                if (!__all_sync(0xffffffffu, wait_phase(smem_u32(&ctrl->tmem_full[buf]), bph, ctrl, w, rg::kErrEpi))) return false;
+                tc_fence_after();
+                return true;
+            };
+            auto add = [&](float(&sum)[64], int32_t ch) {
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    float v[16];
+                    __syncwarp();
+                    tmem_load_16cols(taddr + 64u * (uint32_t)ch + 16u * h, v);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) sum[16 * h + j] += v[j];
+                }
+            };
+            bool ok = true;
+            if (kMode == kStats || (kMany && parts.count > 1)) {
 #pragma unroll
                 for (int j = 0; j < 64; ++j) z[0][j] = z[1][j] = 0.0f;
-                const int32_t parts = part_count<kPair>(q);
-                bool ok = true;
 #pragma unroll 1
-                for (int32_t part = 0; part < parts; ++part) {
-                    const uint32_t buf = local & 1u, bph = (local >> 1) & 1u;
-                    if (!__all_sync(0xffffffffu, wait_phase(smem_u32(&ctrl->tmem_full[buf]), bph, ctrl, w, rg::kErrEpi))) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t taddr = tmem_base + ((quarter * 32u) << 16) + buf * buf_cols;
+                for (int32_t part = 0; part < parts.count - (kMode == kStats ? 0 : 1); ++part) {
+                    ok = filled();
+                    if (!ok) break;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const int32_t ch = (int32_t)half + 2 * i;
-                        if (ch >= chunks) break;
-#pragma unroll
-                        for (int h = 0; h < 4; ++h) {
-                            float v[16];
-                            __syncwarp();
-                            tmem_load_16cols(taddr + 64u * (uint32_t)ch + 16u * h, v);
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) z[i][16 * h + j] += v[j];
-                        }
+                        if (ch >= chunks || row0 >= row_end) break;  // (uniform over the warp)
+                        add(z[i], ch);
                     }
-                    release(buf);
+                    release(local & 1u);
                     ++local;
                 }
-                if (!ok) break;
+            }
+            if (!ok) break;
+            if constexpr (kMode == kStats) {
                 Wanted want;
                 want.start(q, t, y, live, n0);
                 const int32_t n_end = min(q.N, n0 + q.width);
@@ -812,27 +862,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             Wanted want;
             if constexpr (kAnyGrad) want.start(q, t, y, live, n0 + q.w_row);
-            const uint32_t buf = local & 1u, bph = (local >> 1) & 1u;
-            if (some) {
-                if (!__all_sync(0xffffffffu, wait_phase(smem_u32(&ctrl->tmem_full[buf]), bph, ctrl, w, rg::kErrEpi))) break;
-                tc_fence_after();
-            }
-            const uint32_t taddr = tmem_base + ((quarter * 32u) << 16) + buf * buf_cols;
+            if (parts.count > 0 && !filled()) break;
             // kGrad: the last tile's zeros go on to the end of a chunk of 64 columns of G,
             // the others stop where the next one begins, inside a chunk perhaps
             const int32_t stop = !kAnyGrad ? min(q.N, n0 + 64 * chunks) : n0 + q.width >= q.N ? (q.N + 63) & ~63 : n0 + q.width;
-            for (int32_t ch = (int32_t)half;; ch += 2) {
-                const int32_t col = n0 + 64 * ch, c0 = col + q.w_row;  // (c0: its first word)
-                if (col >= stop || row0 >= row_end) break;             // (uniform over the warp)
+            auto chunk = [&](float(&v)[64], int32_t ch) {
+                const int32_t col = n0 + 64 * ch, c0 = col + q.w_row;         // (c0: its first word)
+                if (ch >= chunks || col >= stop || row0 >= row_end) return;  // (uniform over the warp)
                 const int32_t here = kAnyGrad ? min(64, stop - col) : 64;
-                float v[64];
-                if (some && ch < chunks) {
-                    __syncwarp();
-                    tmem_load_64cols(taddr + 64u * (uint32_t)ch, v);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 64; ++j) v[j] = 0.0f;
-                }
                 if constexpr (kAnyGrad) {
                     while (want.next < c0) want.advance(q);  // (of the other half's chunk)
 #pragma unroll
@@ -854,72 +891,60 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (here < 64) {
                         // part of a chunk (the tile's last): straight from the registers
-                        uint32_t x[32];
-                        pack_64(x, v, 1.0f, q.bf16);
-                        uint16_t* dst = q.grad + (int64_t)r * q.grad_pitch + col;
-                        const bool write = r < (kLow ? q.low : q.M);
-                        for (int part = 0;; ++part) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                if (8 * i < here && write)
-                                    reinterpret_cast<uint4*>(dst)[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-                            if (part == 1 || !kLow) break;
-                            dst += (int64_t)q.low * q.grad_pitch;
-                            rest_64(x, v, q.bf16);
+                        uint16_t* const dst = q.grad + (int64_t)r * q.grad_pitch + col;
+                        if (r < (kLow ? q.low : q.M)) {
+                            store_64<false>(dst, v, here, q.bf16);
+                            if constexpr (kLow) store_64<true>(dst + (int64_t)q.low * q.grad_pitch, v, here, q.bf16);
                         }
-                        break;
+                        return;
                     }
                 }
                 if constexpr (kAnyGrad || kMode == kWeight) {
-                    uint32_t x[32];
-                    pack_64(x, v, kMode == kWeight ? scale : 1.0f, q.bf16);
-                    for (int part = 0;; ++part) {
-                        turn();
-#pragma unroll
-                        for (uint32_t i = 0; i < 8; ++i)
-                            rg::st_shared_v4(staging + lane * 128u + ((i ^ (lane & 7u)) << 4),
-                                             make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]));
-                        if constexpr (kMode == kGrad) {
-                            // the wanted words, over what the row's thread has just written
-                            int32_t last = kNone;
-                            float g = 0.0f;
-                            while (__any_sync(0xffffffffu, want.next - c0 < 64)) {
-                                const int32_t at = want.next - c0;
-                                const float p = pick<0, 64>(v, at);
-                                if (at < 64) {
-                                    g = (at == last ? g : p) - coef * want.weight;  // (a word may come twice)
-                                    last = at;
-                                    st_shared_u16(staging + lane * 128u + ((((uint32_t)at >> 3) ^ (lane & 7u)) << 4) + ((uint32_t)at & 7u) * 2u,
-                                                  rg::round16(g, q.bf16));
-                                    want.advance(q);
-                                }
+                    turn();
+                    stage_64<false>(staging + lane * 128u, lane, v, kMode == kWeight ? scale : 1.0f, q.bf16);
+                    if constexpr (kMode == kGrad) {
+                        // the wanted words, over what the row's thread has just written
+                        int32_t last = kNone;
+                        float g = 0.0f;
+                        while (__any_sync(0xffffffffu, want.next - c0 < 64)) {
+                            const int32_t at = want.next - c0;
+                            const float p = pick<0, 64>(v, at);
+                            if (at < 64) {
+                                g = (at == last ? g : p) - coef * want.weight;  // (a word may come twice)
+                                last = at;
+                                st_shared_u16(staging + lane * 128u + ((((uint32_t)at >> 3) ^ (lane & 7u)) << 4) + ((uint32_t)at & 7u) * 2u,
+                                              rg::round16(g, q.bf16));
+                                want.advance(q);
                             }
                         }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (kMode == kWeight && q.once)
+                            store_2d_hint(&maps.d, staging, col + q.d_col, row0 + q.d_row, l2_policy_evict_first());
+                        else
+                            tma_store_2d(&maps.d, staging, col + q.d_col, row0 + q.d_row);
+                        bulk_commit_group();
+                    }
+                    if constexpr (kLow) {
+                        turn();
+                        stage_64<true>(staging + lane * 128u, lane, v, 1.0f, q.bf16);
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
-                            if (kMode == kWeight && q.once)
-                                store_2d_hint(&maps.d, staging, col + q.d_col, row0 + q.d_row, l2_policy_evict_first());
-                            else
-                                tma_store_2d(kLow && part == 1 ? &maps.low : &maps.d, staging, col + q.d_col, row0 + q.d_row);
+                            tma_store_2d(&maps.low, staging, col + q.d_col, row0 + q.d_row);
                             bulk_commit_group();
                         }
-                        if (!kLow || part == 1) break;
-                        rest_64(x, v, q.bf16);
                     }
                 }
                 if constexpr (kMode == kSum) {
-                    if (!some && !q.first) break;
+                    if (k.kb0 == k.kb1 && !q.first) return;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         if (col + 32 * h >= q.N) break;
                         turn();
-#pragma unroll
-                        for (uint32_t i = 0; i < 8; ++i)
-                            rg::st_shared_v4(staging + lane * 128u + ((i ^ (lane & 7u)) << 4),
-                                             make_uint4(__float_as_uint(v[32 * h + 4 * i]), __float_as_uint(v[32 * h + 4 * i + 1]),
-                                                        __float_as_uint(v[32 * h + 4 * i + 2]),
-                                                        __float_as_uint(v[32 * h + 4 * i + 3])));
+                        stage_32(staging + lane * 128u, lane, v, 32 * h);
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
@@ -931,10 +956,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
+            };
+#pragma unroll 1
+            for (int32_t ch = (int32_t)half; ch < chunks; ch += 2) {
+                if (kMany && parts.count > 1 && row0 < row_end) {
+                    add(z[0], ch);
+                } else if (parts.count > 0 && row0 < row_end) {
+                    __syncwarp();
+                    tmem_load_64cols(taddr + 64u * (uint32_t)ch, z[0]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) z[0][j] = 0.0f;
+                }
+                chunk(z[0], ch);
+                if (kMany && parts.count > 1) {
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) z[0][j] = z[1][j];
+                }
             }
-            if (some) {
-                release(buf);
+            if (parts.count > 0) {
+                release(local & 1u);
                 ++local;
+            }
+            // zeros of the last tile beyond its last chunk
+            if constexpr (kAnyGrad) {
+                const int32_t from = n0 + 64 * chunks;
+                if (half == 0 && from < stop && r < (kLow ? q.low : q.M)) {
+                    uint16_t* const dst = q.grad + (int64_t)r * q.grad_pitch;
+                    for (int32_t col = from; col < stop; col += 8) {
+                        *reinterpret_cast<uint4*>(dst + col) = make_uint4(0, 0, 0, 0);
+                        if constexpr (kLow) *reinterpret_cast<uint4*>(dst + (int64_t)q.low * q.grad_pitch + col) = make_uint4(0, 0, 0, 0);
+                    }
+                }
             }
         }
         if (lane == 0) bulk_wait_group_all();

@@ -56,7 +56,7 @@ struct DeviceState {
     bool attr_set[6] = {false, false, false, false, false, false};  // per kernel mode
     bool rg_carveout_set[2] = {};  // per kernel that runs beside a ragged one
     bool rg_attr_set[6] = {};  // per ragged kernel
-    bool ls_attr_set[10] = {};  // per kernel of the losses
+    bool ls_attr_set[20] = {};  // per kernel of the losses
     std::vector<StreamBuffers> streams;
 };
 
