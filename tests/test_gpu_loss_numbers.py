@@ -180,3 +180,66 @@ def test_gradients_of_certain_words_with_the_forward_pass_own_lse(T, D, layout, 
     e = p * (2 * b[:, None] + shift[:, None] + (4 + 3 * arg) * E32)
     e[at] = rest * 2 * b + shift + 8 * E32
     check_gradients(got, a * g, a * e, x, w, layout, dtype, T, T, V + 32, a)
+
+
+@pytest.mark.parametrize("layout", ["nk", "kn"])
+@pytest.mark.parametrize("ignored", [False, True])
+def test_weight_gradient_of_many_rows(layout, ignored):
+    """Sums over a million rows of terms of one sign: of two words with a logit of 0 and six far below, g is +-a / 2
+    exactly, and the rows are positive: in one accumulator the sum lost 1.07% of itself.  In parts of 4096 rows it
+    loses at most 2^-23 * (4096 + 256), beside its own rounding."""
+    T, V, D = 1 << 20, 8, 64
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    x = (torch.randint(64, 128, (T, D), generator=gen, device=DEV).float() / 128).half()
+    x[:, D - 1] = 1.0
+    w = torch.zeros((V, D), dtype=torch.float16, device=DEV)
+    w[2:, D - 1] = -200.0
+    y = torch.zeros(T, dtype=torch.int32, device=DEV)
+    if ignored:
+        y[torch.rand(T, generator=gen, device=DEV) < 0.3] = -1
+    a = torch.full((1,), 2.0 ** -20, device=DEV)
+    loss, lse = binding.gemm_relu_xent(x, laid_out(w, layout), y, b_layout=layout)
+    dx, dw = binding.gemm_relu_xent_grad(x, laid_out(w, layout), y, lse, a, b_layout=layout)
+    binding.check_device_error()
+    total = 2.0 ** -21 * x[y >= 0].double().sum(0)
+    dw = dw if layout == "nk" else dw.t()
+    bound = total * (2.0 ** -11 + 1.001 * (4096 + T / 4096) * E32)
+    for row, want in ((0, -total), (1, total)):
+        off = (dw[row].double() - want).abs()
+        assert (off <= bound).all(), (off / total).max().item()
+    assert not dw[2:].any() and not dx[:, :-1].any()
+
+
+@pytest.mark.parametrize("T,V", [(1, 16000000), (100, 4200008), (200, 2200008)])
+def test_row_gradient_of_many_words(T, V):
+    """Sums over millions of words of terms of one sign: the words' logits are 0, so g is a / V at every word but the
+    target (G's own rounding is the same at all of them), and their weights are positive.  In one accumulator per
+    share dX lost 0.2%; in parts of 4096 words it loses at most 2^-23 * (4096 + V / 4096)."""
+    D = 16
+    gen = torch.Generator(device=DEV).manual_seed(6)
+    w = (torch.randint(64, 128, (V, D), generator=gen, device=DEV).float() / 128).half()
+    x = torch.zeros((T, D), dtype=torch.float16, device=DEV)
+    y = torch.zeros(T, dtype=torch.int32, device=DEV)
+    w[0] = 0
+    lse = torch.full((T,), math.log(V), device=DEV)
+    d = torch.full((T,), 1.0, device=DEV)
+    dx, _ = binding.gemm_relu_xent_grad(x, w, y, lse, d, want_dw=False, b_layout="nk")
+    binding.check_device_error()
+    p = math.exp(-lse[0].double().item())
+    # G is p times 2047 / 1024 * 2^14, rounded (twice up to 32 rows: to its rest's half unit)
+    scale = 2047.0 / 1024.0 * 2 ** 14
+    g = torch.tensor(p * scale, dtype=torch.float64)
+    held = g.half().double()
+    if T <= 32:
+        held = held + (g - held).half().double()
+    want = w.double().sum(0) * held / scale
+    # the exponential: 2 units, its argument of 16.6 three roundings, the factor two; a step of G (of its rest: 2^-24)
+    # more where that crosses a border of its rounding
+    e, step = (4 + 3 * 16.6) * E32, 2.0 ** (math.floor(math.log2(g.item())) - 10)
+    if T <= 32:
+        unit = 2.0 ** -24 / g.item()
+    else:
+        unit = step / g.item() if abs((g - held).item()) > step / 2 - 2 * e * g.item() else 0.0
+    bound = want * (e + unit + 2.0 ** -11 + 1.001 * (4096 + V / 4096) * E32)
+    off = (dx.double() - want).abs()
+    assert (off <= bound).all(), (off / want).max().item()

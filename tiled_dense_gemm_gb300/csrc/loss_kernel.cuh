@@ -303,7 +303,10 @@ __device__ __forceinline__ float pick(const float (&v)[kSize], int32_t at) {
 // same parts, so that what is left of the truncation is the same in z and in lse and
 // drops out of their difference.
 constexpr int32_t kPartPair = 1024, kPartSingle = 256;
-constexpr int32_t kPartSum = 1 << 30;  // (the gradients' sums: one part)
+// dX's and dW's sums, whose terms may all have one sign: in one accumulator they lost
+// 1.07% over 2^20 rows and 0.08% over 94000 words; in parts of 4096 4e-5, a tenth of
+// binary16's rounding.
+constexpr int32_t kPartSum = 4096;
 
 // In steps of 128 k, whatever a stage holds.  kMany: there may be several.
 template <bool kPair, int kMode, bool kMany>
