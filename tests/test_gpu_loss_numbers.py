@@ -243,3 +243,37 @@ def test_row_gradient_of_many_words(T, V):
     bound = want * (e + unit + 2.0 ** -11 + 1.001 * (4096 + V / 4096) * E32)
     off = (dx.double() - want).abs()
     assert (off <= bound).all(), (off / want).max().item()
+
+
+@pytest.mark.parametrize("layout", ["nk", "kn"])
+@pytest.mark.parametrize("T", [20, 100])
+def test_gradient_of_a_main_word_in_several_entries(T, layout):
+    """A word whose weight of 0.6 comes in four entries of 0.15 beside one of 0.4: it is the row's main word all the
+    same, so p - q there, next to nothing, comes from the exact sum of z."""
+    V, D, tau = 64, 2048, 1.0
+    gen = torch.Generator().manual_seed(T)
+    w = (torch.randn(V, D, generator=gen) * 2 * D ** -0.5).half()
+    a, b = w[3].float(), w[40].float()
+    pair = torch.stack([a, b])
+    for_both = torch.linalg.solve((pair @ pair.t()).double(), torch.tensor([1.0, 1.0], dtype=torch.float64))
+    only_a = torch.linalg.solve((pair @ pair.t()).double(), torch.tensor([1.0, 0.0], dtype=torch.float64))
+    both, first = (for_both @ pair.double()), (only_a @ pair.double())
+    x = ((20 + 8 * torch.rand(T, 1, generator=gen)).double() * both + math.log(1.5) * first).half()
+    ids = torch.tensor([3, 40, 3, 3, 3], dtype=torch.int32).repeat(T, 1).to(DEV)
+    logits = torch.log(torch.tensor([0.15, 0.4, 0.15, 0.15, 0.15])).repeat(T, 1).to(DEV)
+    q = 4 * torch.softmax(logits[0].double(), 0)[0].item()
+    z = x.double() @ w.double().t()
+    lse = torch.logsumexp(z, 1).float()
+    d = dloss_of(T, 3) * (256 * T)
+    _, dw = binding.gemm_relu_distill_grad(x.to(DEV), laid_out(w.to(DEV), layout), ids, logits, lse.to(DEV), d, tau, b_layout=layout)
+    binding.check_device_error()
+    p = torch.exp(z[:, 3] - lse.double())
+    s = d.double().cpu()
+    g = s * (p - q)
+    # the exponential and the argument's rounding; four weights, their logits' and the softmax's roundings
+    e = s * (8 * E32 + q * (4 * 2 + 8 + 5 + 4) * E32)
+    e = e + 2.0 ** (-22 if T <= 32 else -11) * (g.abs() + e) + 2.0 ** -39 * s.max()
+    value, bound = x.double().t() @ g, x.double().abs().t() @ e + T * E32 * (x.double().abs().t() @ (g.abs() + e))
+    bound += 2.0 ** -11 * (value.abs() + bound) + 2.0 ** -25
+    off = ((dw[3] if layout == "nk" else dw[:, 3]).double().cpu() - value).abs()
+    assert (off <= bound).all(), ((off / bound).max().item(), (p - q).abs().max().item())

@@ -140,7 +140,14 @@ static int run_teacher(const Call& c, const LossPlan& p, int64_t b0, int64_t T, 
         q.entropy = reinterpret_cast<float*>(c.ws + p.entropy);
         q.err = d.d_err;
         const int grid = (int)std::min<int64_t>((T + kTeacherWarps - 1) / kTeacherWarps, 16 * d.sm_count);
-        rc = launch(loss_teacher_kernel, grid, 32 * kTeacherWarps, (size_t)kTeacherWarps * ((c.k + 3) / 4 * 4) * 8, 1, c.st, q);
+        const size_t smem = (size_t)kTeacherWarps * ((c.k + 3) / 4 * 4) * 8;
+        if (p.gather) {
+            rc = launch(loss_teacher_kernel<false>, grid, 32 * kTeacherWarps, smem, 1, c.st, q);
+        } else {
+            q.main = reinterpret_cast<int32_t*>(c.ws + p.main);
+            q.main_weight = reinterpret_cast<float*>(c.ws + p.main_weight);
+            rc = launch(loss_teacher_kernel<true>, grid, 32 * kTeacherWarps, smem, 1, c.st, q);
+        }
         if (rc != GEMM_OK) return rc;
     }
     return GEMM_OK;
@@ -181,9 +188,8 @@ static int run_rows(const Call& c, const LossPlan& p, int64_t b0, int64_t T, Dev
         q.w_word = c.nk ? c.D : 1;
         q.w_depth = c.nk ? 1 : c.V;
         if (c.ids) {
-            q.ids = reinterpret_cast<const int32_t*>(c.ws + p.sorted);
-            q.weights = reinterpret_cast<const float*>(c.ws + p.weights);
-            q.k = (int32_t)c.k;
+            q.main = reinterpret_cast<const int32_t*>(c.ws + p.main);
+            q.main_weight = reinterpret_cast<const float*>(c.ws + p.main_weight);
         }
         q.bf16 = c.bf16 ? 1 : 0;
         q.tau = c.ids ? c.tau : 1.0f;

@@ -140,6 +140,10 @@ LossPlan plan_loss(int64_t T, int64_t V, int64_t D, int64_t k, bool gradient) {
         p.entropy = take(4 * rows);
         p.sorted = take(4 * rows * k);
         p.weights = take(4 * rows * k);
+        if (!p.gather) {
+            p.main = take(4 * rows);
+            p.main_weight = take(4 * rows);
+        }
     }
     // The copy's rows start at multiples of 128 bytes, so that a box row lies in one
     // line (1800 of 3000 rows, 50021 words of 2056: 280 us at X's pitch, 266 so; the

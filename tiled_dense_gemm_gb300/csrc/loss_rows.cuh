@@ -23,6 +23,8 @@ struct TeacherParams {
     float* weights;        // (T, k) q
     int32_t* flags;        // per row: 0, or -1: no word
     float* entropy;        // per row: sum of q log q
+    int32_t* main;         // per row: the word that weighs most, kNone: no word, and its weight
+    float* main_weight;
     int32_t* err;
 };
 
@@ -43,7 +45,8 @@ constexpr int kTeacherWarps = 4;
 // One warp per row: the softmax over its k words in 32 bits, and the words in
 // rising order by counting, for each, the smaller ones (k^2 comparisons out of
 // shared memory; ties in their given order, so that a word given twice is two
-// entries).
+// entries).  kMain: the row's main word too, its weight that of all its entries.
+template <bool kMain>
 __global__ void __launch_bounds__(32 * kTeacherWarps) loss_teacher_kernel(const __grid_constant__ TeacherParams p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const int32_t warp = (int32_t)threadIdx.x / 32, lane = (int32_t)threadIdx.x % 32;
@@ -87,24 +90,54 @@ __global__ void __launch_bounds__(32 * kTeacherWarps) loss_teacher_kernel(const 
         const float log_sum = logf(sum), inv = 1.0f / sum;
         float h = 0.0f;
         __syncwarp();
+        for (int32_t j = lane; j < padded; j += 32) {
+            const float x = j < p.k ? e[j] : -INFINITY, q = expf(x) * inv;
+            if (j < p.k && q != 0.0f) h += q * (x - log_sum);
+            e[j] = j < p.k && key[j] != kNone && some ? q : 0.0f;
+        }
+        __syncwarp();
+        float most = 0.0f;
+        int32_t word = kNone;
         for (int32_t j = lane; j < p.k; j += 32) {
-            const float x = e[j], q = expf(x) * inv;
-            if (q != 0.0f) h += q * (x - log_sum);
             const int32_t mine = key[j];
             int32_t at = 0;
+            float all = 0.0f;
 #pragma unroll 4
             for (int32_t i = 0; i < padded; i += 4) {
                 const int4 o = *reinterpret_cast<const int4*>(key + i);
                 at += (o.x < mine || (o.x == mine && i < j)) + (o.y < mine || (o.y == mine && i + 1 < j)) +
                       (o.z < mine || (o.z == mine && i + 2 < j)) + (o.w < mine || (o.w == mine && i + 3 < j));
+                if constexpr (kMain) {
+                    const float4 q = *reinterpret_cast<const float4*>(e + i);
+                    all += ((o.x == mine ? q.x : 0.0f) + (o.y == mine ? q.y : 0.0f)) + ((o.z == mine ? q.z : 0.0f) + (o.w == mine ? q.w : 0.0f));
+                }
             }
             p.sorted[t * p.k + at] = some ? mine : kNone;
-            p.weights[t * p.k + at] = mine == kNone || !some ? 0.0f : q;
+            p.weights[t * p.k + at] = e[j];
+            if (kMain && (all > most || (all == most && mine < word))) {
+                most = all;
+                word = mine;
+            }
         }
         h = warp_sum(h);
+        if constexpr (kMain) {
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) {
+                const float all = __shfl_xor_sync(0xffffffffu, most, d);
+                const int32_t other = __shfl_xor_sync(0xffffffffu, word, d);
+                if (all > most || (all == most && other < word)) {
+                    most = all;
+                    word = other;
+                }
+            }
+        }
         if (lane == 0) {
             p.flags[t] = some ? 0 : -1;
             p.entropy[t] = h;
+            if constexpr (kMain) {
+                p.main[t] = most > 0.0f ? word : kNone;
+                p.main_weight[t] = most;
+            }
         }
         __syncwarp();
     }
@@ -132,9 +165,9 @@ struct RowsParams {
     int32_t rows_of, period;
     const uint16_t* W;
     int64_t w_word, w_depth;  // from one word to the next, and from one k: one of them 1
-    const int32_t* ids;       // (T, k) of a teacher; null: the flags
-    const float* weights;
-    int32_t k, bf16;
+    const int32_t* main;      // of a teacher; null: the flags, of weight 1
+    const float* main_weight;
+    int32_t bf16;
     float tau;
     const float* lse;
     uint16_t* grad;           // G
@@ -267,38 +300,6 @@ __global__ void __launch_bounds__(kRowsThreads) loss_rows_kernel(const __grid_co
     if (i == 0) write_header(p, total, gather ? 1 : 0, top);
 }
 
-// The wanted word of a row that weighs most, and its weight, by one warp.
-__device__ __forceinline__ int32_t main_word(const RowsParams& p, int32_t t, int32_t flag, float& weight) {
-    weight = 1.0f;
-    if (!p.ids) return flag;
-    const int32_t lane = (int32_t)threadIdx.x % 32;
-    const int32_t* const ids = p.ids + (int64_t)t * p.k;
-    const float* const weights = p.weights + (int64_t)t * p.k;
-    float most = 0.0f;
-    int32_t word = kNone;
-    for (int32_t j = lane; j < p.k; j += 32) {
-        const float q = __ldcg(weights + j);
-        if (q > most) {
-            most = q;
-            word = __ldcg(ids + j);
-        }
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        const float q = __shfl_xor_sync(0xffffffffu, most, d);
-        const int32_t y = __shfl_xor_sync(0xffffffffu, word, d);
-        if (q > most || (q == most && y < word)) {
-            most = q;
-            word = y;
-        }
-    }
-    float all = 0.0f;  // (it may come more than once)
-    for (int32_t j = lane; j < p.k; j += 32)
-        if (__ldcg(ids + j) == word) all += __ldcg(weights + j);
-    weight = warp_sum(all);
-    return word;
-}
-
 // This thread's products of X's row with a word's weights, of all the block's.
 __device__ __forceinline__ double some_products(const RowsParams& p, int32_t t, int32_t word) {
     const uint16_t* const x = p.X + (int64_t)t * p.ldx;
@@ -345,17 +346,18 @@ __device__ __forceinline__ double some_products(const RowsParams& p, int32_t t, 
 // without, 94 with a kernel in front of it.
 __global__ void __launch_bounds__(kRowsThreads) loss_mask_kernel(const __grid_constant__ RowsParams p) {
     __shared__ double part[kRowsThreads / 32];
-    __shared__ int32_t main;
     const int32_t i = (int32_t)threadIdx.x, r = (int32_t)blockIdx.x, warp = i / 32, lane = i % 32;
     grid_launch_dependents();
     const int32_t t = r % p.period;
     const int32_t y = t < p.T ? __ldcg(p.flags + t) : -1;
     if (y >= p.limit && i == 0) atomicCAS(p.err + 1, 0, (int32_t)rg::kBadIds);
     const bool in = y >= 0 && y < p.limit;
-    float weight = 0.0f;
-    if (warp == 0) {
-        const int32_t word = in && r < p.T ? main_word(p, t, y, weight) : kNone;
-        if (lane == 0) main = word - p.from >= 0 && word - p.from < p.words ? word : kNone;
+    int32_t word = kNone;
+    float weight = 1.0f;
+    if (in && r < p.T) {
+        word = p.main ? __ldcg(p.main + t) : y;
+        if (p.main) weight = __ldcg(p.main_weight + t);
+        if (word < p.from || word - p.from >= p.words) word = kNone;
     }
     const int32_t vecs = p.D / 8;
     if (in) {
@@ -366,8 +368,6 @@ __global__ void __launch_bounds__(kRowsThreads) loss_mask_kernel(const __grid_co
         uint4* const dst = reinterpret_cast<uint4*>(p.gathered + (int64_t)r * p.pitch);
         for (int32_t c = i; c < vecs; c += kRowsThreads) dst[c] = make_uint4(0, 0, 0, 0);
     }
-    __syncthreads();
-    const int32_t word = main;
     if (word != kNone) {
         double z = some_products(p, t, word);
 #pragma unroll
