@@ -157,7 +157,37 @@ def truncated(T, x, w, parts_of):
 
 
 @pytest.mark.parametrize("layout,dtype", BOTH)
-@pytest.mark.parametrize("T,D", [(129, 2056), (300, 4096), (300, 1544)])
+@pytest.mark.parametrize("T", [1, 20, 128])
+def test_lse_of_up_to_128_rows_with_a_certain_word(T, layout, dtype):
+    """The logit of the wanted word is summed exactly (2048 products in 256 threads' numbers), so lse is off by its
+    own rounding, the sum's, and what truncation makes of the words that have little part in it."""
+    V, D = 64, 2048
+    x, w, y = nearly_certain(T, D, V, dtype, T)
+    z = x.double().cpu().numpy() @ w.double().cpu().numpy().T
+    lse, loss = logsumexp(z)
+    small = 2 * truncated(T, x, w, 256).max(axis=1) * loss
+    got, got_lse = binding.gemm_relu_xent(x, laid_out(w, layout), y, b_layout=layout)
+    binding.check_device_error()
+    off, off_lse = np.abs(got.double().cpu().numpy() - loss), np.abs(got_lse.double().cpu().numpy() - lse)
+    # (64 words are one chunk: 16 additions, 2 that join, 1, 3 and 3)
+    e = 25 * E32 / 2 + small + 4 * E32 * loss
+    assert (off_lse <= e + E32 / 2 * lse).all(), (off_lse / lse).max()
+    assert (off <= e).all(), off.max()
+    for tau in (1.0, 1.5):
+        # q in two places of the same word, and a little elsewhere
+        ids = torch.stack([y, y, (y + 1) % V, torch.full_like(y, -1)], dim=1).contiguous()
+        logits = torch.tensor([9.0, 9.5, -9.0, 50.0], device=DEV).expand(T, 4).contiguous()
+        lse = logsumexp(z / tau)[0]
+        _, got_lse = binding.gemm_relu_distill(x, laid_out(w, layout), ids, logits, tau, b_layout=layout)
+        binding.check_device_error()
+        rest = logsumexp(z / tau)[1]
+        e = 25 * E32 / 2 + 2 * truncated(T, x, w, 256).max(axis=1) / tau * rest + 4 * E32 * rest + E32 / 2 * lse
+        off_lse = np.abs(got_lse.double().cpu().numpy() - lse)
+        assert (off_lse <= e).all(), (off_lse / lse).max()
+
+
+@pytest.mark.parametrize("layout,dtype", BOTH)
+@pytest.mark.parametrize("T,D", [(1, 2048), (20, 2048), (100, 2048), (129, 2056), (300, 4096), (300, 1544)])
 def test_gradients_of_certain_words_with_the_forward_pass_own_lse(T, D, layout, dtype):
     """The true gradient, with lse as the forward call returned it: both passes sum a logit alike (or exactly), so
     what the tensor core truncates of it takes the same part of 1 - p, not of p."""

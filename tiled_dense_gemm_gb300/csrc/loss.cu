@@ -159,6 +159,21 @@ static int run_teacher(const Call& c, const LossPlan& p, int64_t b0, int64_t T, 
 // what it can of small ones.
 static float top_of(const Call& c) { return c.bf16 ? 255.0f / 128.0f : 2047.0f / 1024.0f * 16384.0f; }
 
+// What the logits of single words are summed from (up to 128 rows).
+static WordSums word_sums(const Call& c, const LossPlan& p) {
+    WordSums s;
+    memset(&s, 0, sizeof(s));
+    s.X = reinterpret_cast<const uint16_t*>(c.X);
+    s.ldx = c.ldx;
+    s.W = reinterpret_cast<const uint16_t*>(c.W);
+    s.w_word = c.nk ? c.D : 1;
+    s.w_depth = c.nk ? 1 : c.V;
+    s.word = c.ids ? reinterpret_cast<const int32_t*>(c.ws + p.main) : c.targets;
+    s.D = (int32_t)c.D;
+    s.bf16 = c.bf16 ? 1 : 0;
+    return s;
+}
+
 // Which rows [b0, b0 + T) are in use, and a copy of those.
 static int run_rows(const Call& c, const LossPlan& p, int64_t b0, int64_t T, DeviceState& d, int64_t p0 = 0) {
     RowsParams q;
@@ -184,14 +199,8 @@ static int run_rows(const Call& c, const LossPlan& p, int64_t b0, int64_t T, Dev
     if (p.masked) {
         q.rows_of = (int32_t)p.g_rows;
         q.period = p.low ? p.low : (int32_t)T;
-        q.W = reinterpret_cast<const uint16_t*>(c.W);
-        q.w_word = c.nk ? c.D : 1;
-        q.w_depth = c.nk ? 1 : c.V;
-        if (c.ids) {
-            q.main = reinterpret_cast<const int32_t*>(c.ws + p.main);
-            q.main_weight = reinterpret_cast<const float*>(c.ws + p.main_weight);
-        }
-        q.bf16 = c.bf16 ? 1 : 0;
+        q.sums = word_sums(c, p);
+        if (c.ids) q.main_weight = reinterpret_cast<const float*>(c.ws + p.main_weight);
         q.tau = c.ids ? c.tau : 1.0f;
         q.lse = c.lse;
         q.grad = reinterpret_cast<uint16_t*>(c.ws + p.grad);
@@ -270,7 +279,7 @@ static int run_forward(const Call& c, const LossPlan& p, DeviceState& d) {
         int rc = run_teacher(c, p, b0, T, d);
         if (rc == GEMM_OK && p.gather) rc = run_rows(c, p, b0, T, d);
         if (rc != GEMM_OK) return rc;
-        const TilePlan t = plan_logits(T, c.V, c.D, !c.nk, true, d.sm_count, d.max_pairs);
+        TilePlan t = plan_logits(T, c.V, c.D, !c.nk, true, d.sm_count, d.max_pairs);
         LossMaps m;
         LossParams q;
         memset(&q, 0, sizeof(q));
@@ -281,6 +290,11 @@ static int run_forward(const Call& c, const LossPlan& p, DeviceState& d) {
         wanted(c, p, b0, q);
         q.stats = reinterpret_cast<float*>(c.ws + p.stats);
         q.stats_pitch = (p.rows + 31) / 32 * 32;
+        if (!p.gather) {  // (one block of rows)
+            q.exact = reinterpret_cast<double*>(c.ws + p.exact);
+            q.sums = word_sums(c, p);
+            t.grid = std::max(t.grid, std::min((int32_t)T, (int32_t)d.sm_count));  // (a row of those sums per CTA)
+        }
         rc = encode_rows_of_x(m, c, p, b0, T, t, q);
         if (rc == GEMM_OK) rc = encode_words(m, c, t, q);
         if (rc != GEMM_OK) return rc;
@@ -298,6 +312,8 @@ static int run_forward(const Call& c, const LossPlan& p, DeviceState& d) {
         o.flags = flags_of(c, p, b0);
         o.limit = limit_of(c);
         o.entropy = c.ids ? reinterpret_cast<const float*>(c.ws + p.entropy) : nullptr;
+        o.exact = q.exact;
+        o.main_weight = c.ids && !p.gather ? reinterpret_cast<const float*>(c.ws + p.main_weight) : nullptr;
         o.tau = c.tau;
         o.log2_scale = q.log2_scale;
         o.loss = c.loss + b0;

@@ -91,6 +91,17 @@ struct FinishParams {
     int64_t ld_dx;
 };
 
+// What the logit of a single word is summed from, by so many threads.
+struct WordSums {
+    const uint16_t* X;
+    int64_t ldx;
+    const uint16_t* W;
+    int64_t w_word, w_depth;  // from one word to the next, and from one k: one of them 1
+    const int32_t* word;      // per row: its target, or a teacher's main word
+    int32_t D, bf16;
+};
+constexpr int32_t kSumThreads = 256;
+
 struct LossParams {
     int32_t M, N, K;       // D is M x N, K the reduction (bounds, where the rows' count replaces them)
     int32_t rows_m;        // M is the rows' count
@@ -137,6 +148,8 @@ struct LossParams {
     float log2_scale;        // c
     float* stats;            // kStats: [tile][3][stats_pitch]
     int64_t stats_pitch;
+    WordSums sums;
+    double* exact;           // kStats, up to 128 rows: the logit of a row's main word, in eight parts
     const float* lse;        // kGrad
     const float* dloss;
     int64_t dloss_stride;    // 0 or 1
@@ -281,6 +294,37 @@ struct Wanted {
         fetch(q, next2, weight2);
     }
 };
+
+// Thread i's of kSumThreads' products of X's row with a word's weights: 1/2048 of them in
+// each number of 32 bits, and those in 64.
+__device__ __forceinline__ double some_products(const WordSums& p, int32_t t, int32_t word, int32_t i) {
+    const uint16_t* const x = p.X + (int64_t)t * p.ldx;
+    const uint16_t* const w = p.W + (int64_t)word * p.w_word;
+    float sum[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    for (int32_t d = 8 * i; d < p.D; d += 8 * kSumThreads) {  // (D a multiple of 8)
+        const uint4 a = __ldg(reinterpret_cast<const uint4*>(x + d));
+        uint4 b;
+        if (p.w_depth == 1) {
+            b = __ldg(reinterpret_cast<const uint4*>(w + d));
+        } else {
+            uint32_t e[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) e[j] = __ldg(w + (int64_t)(d + j) * p.w_depth);
+            b = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+        }
+        const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 m = rg::unpack16(av[j], p.bf16), n = rg::unpack16(bv[j], p.bf16);
+            sum[2 * j] = fmaf(m.x, n.x, sum[2 * j]);
+            sum[2 * j + 1] = fmaf(m.y, n.y, sum[2 * j + 1]);
+        }
+    }
+    double z = 0.0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) z += (double)sum[j];
+    return z;
+}
 
 // v[at], halving.
 template <int kFrom, int kCount, int kSize>
@@ -712,6 +756,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         float scale = 1.0f;
         if constexpr (kAnyGrad) scale = q.scale ? __ldcg(&q.scale->scale) : scale_of(q.top, q.grad_scale, largest_dloss(q.flags, q.limit, q.dloss, q.dloss_stride, q.M));
         if constexpr (kMode == kWeight) scale = __ldcg(&q.scale->unscale);
+        if constexpr (!kPair && kMode == kStats) {
+            // The logit of a row's main word, summed exactly (see the joining kernel): a row
+            // per CTA, an eighth of its products per warp, while the first tile's weights
+            // are on their way.
+            const int32_t e = (int32_t)(quarter + 4u * half);
+            for (int32_t t = (int32_t)blockIdx.x; q.exact && t < q.M; t += (int32_t)gridDim.x) {
+                const int32_t word = __ldcg(q.sums.word + t);
+                const bool is = word >= 0 && word < q.V;
+                double y = is ? some_products(q.sums, t, word, 32 * e + (int32_t)lane) : -INFINITY;
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) y += __shfl_xor_sync(0xffffffffu, y, d);
+                if (lane == 0) q.exact[8 * (int64_t)t + e] = y;
+            }
+        }
         // the copy issued from the staging buffer before must have read it
         auto turn = [&]() {
             if (lane == 0) bulk_wait_group_read<0>();

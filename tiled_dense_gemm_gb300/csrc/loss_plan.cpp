@@ -153,6 +153,7 @@ LossPlan plan_loss(int64_t T, int64_t V, int64_t D, int64_t k, bool gradient) {
     if (!gradient) {
         if (parts * ceil_div(rows, 128) > 2000000000ll) p.status = GEMM_ERR_TOO_LARGE;
         p.stats = take(12 * round_up(rows, 32) * parts);
+        if (!p.gather) p.exact = take(64 * rows);
     } else {
         const int64_t most = std::max<int64_t>(256, kGradBytes / (2 * p.g_rows) / 256 * 256);
         p.piece = round_up(ceil_div(V, ceil_div(V, most)), 256);

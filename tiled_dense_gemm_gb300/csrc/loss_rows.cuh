@@ -163,11 +163,8 @@ struct RowsParams {
     // masked: rows of the copy, X's over and over after so many (of G's two parts), and
     // what the gradient at a certain word is found from
     int32_t rows_of, period;
-    const uint16_t* W;
-    int64_t w_word, w_depth;  // from one word to the next, and from one k: one of them 1
-    const int32_t* main;      // of a teacher; null: the flags, of weight 1
-    const float* main_weight;
-    int32_t bf16;
+    WordSums sums;
+    const float* main_weight; // of a teacher's main words; null: 1
     float tau;
     const float* lse;
     uint16_t* grad;           // G
@@ -177,7 +174,7 @@ struct RowsParams {
     int32_t* err;
 };
 
-constexpr int kRowsThreads = 256;
+constexpr int kRowsThreads = kSumThreads;
 
 // top: the largest |dloss|
 __device__ __forceinline__ void write_header(const RowsParams& p, int32_t valid, int32_t compact, float top) {
@@ -300,36 +297,6 @@ __global__ void __launch_bounds__(kRowsThreads) loss_rows_kernel(const __grid_co
     if (i == 0) write_header(p, total, gather ? 1 : 0, top);
 }
 
-// This thread's products of X's row with a word's weights, of all the block's.
-__device__ __forceinline__ double some_products(const RowsParams& p, int32_t t, int32_t word) {
-    const uint16_t* const x = p.X + (int64_t)t * p.ldx;
-    const uint16_t* const w = p.W + (int64_t)word * p.w_word;
-    float sum[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    for (int32_t d = 8 * (int32_t)threadIdx.x; d < p.D; d += 8 * kRowsThreads) {  // (D a multiple of 8)
-        const uint4 a = __ldg(reinterpret_cast<const uint4*>(x + d));
-        uint4 b;
-        if (p.w_depth == 1) {
-            b = __ldg(reinterpret_cast<const uint4*>(w + d));
-        } else {
-            uint32_t e[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) e[j] = __ldg(w + (int64_t)(d + j) * p.w_depth);
-            b = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
-        }
-        const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 m = rg::unpack16(av[j], p.bf16), n = rg::unpack16(bv[j], p.bf16);
-            sum[2 * j] = fmaf(m.x, n.x, sum[2 * j]);
-            sum[2 * j + 1] = fmaf(m.y, n.y, sum[2 * j + 1]);
-        }
-    }
-    double z = 0.0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) z += (double)sum[j];
-    return z;
-}
-
 // Up to 128 rows: nothing is gathered (there is one row tile).  Beside the kernel of
 // G (`late`, as there: that one has waited for X and the flags), a block per row:
 //
@@ -355,8 +322,8 @@ __global__ void __launch_bounds__(kRowsThreads) loss_mask_kernel(const __grid_co
     int32_t word = kNone;
     float weight = 1.0f;
     if (in && r < p.T) {
-        word = p.main ? __ldcg(p.main + t) : y;
-        if (p.main) weight = __ldcg(p.main_weight + t);
+        word = __ldcg(p.sums.word + t);
+        if (p.main_weight) weight = __ldcg(p.main_weight + t);
         if (word < p.from || word - p.from >= p.words) word = kNone;
     }
     const int32_t vecs = p.D / 8;
@@ -369,7 +336,7 @@ __global__ void __launch_bounds__(kRowsThreads) loss_mask_kernel(const __grid_co
         for (int32_t c = i; c < vecs; c += kRowsThreads) dst[c] = make_uint4(0, 0, 0, 0);
     }
     if (word != kNone) {
-        double z = some_products(p, t, word);
+        double z = some_products(p.sums, t, word, i);
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
         if (lane == 0) part[warp] = z;
@@ -392,9 +359,9 @@ __global__ void __launch_bounds__(kRowsThreads) loss_mask_kernel(const __grid_co
     grid_dependency_wait();
     if (sure) {
         uint16_t* const at = p.grad + (int64_t)t * p.grad_pitch + (word - p.from);
-        const uint32_t x = rg::pack16(g, 0.0f, p.bf16);
+        const uint32_t x = rg::pack16(g, 0.0f, p.sums.bf16);
         at[0] = (uint16_t)x;
-        if (p.low) at[(int64_t)p.low * p.grad_pitch] = (uint16_t)rg::rest16x2(g, 0.0f, x, p.bf16);
+        if (p.low) at[(int64_t)p.low * p.grad_pitch] = (uint16_t)rg::rest16x2(g, 0.0f, x, p.sums.bf16);
     }
 }
 
@@ -410,6 +377,8 @@ struct CombineParams {
     int32_t limit;
     const float* entropy;   // teacher; null: targets
     float tau, log2_scale;
+    const double* exact;       // up to 128 rows: the logit of a row's main word, in eight parts,
+    const float* main_weight;  // ... and that word's weight; null: 1
     float* loss;
     float* lse;
     int32_t* err;
@@ -429,6 +398,13 @@ __global__ void __launch_bounds__(32 * kWarps) loss_combine_kernel(const __grid_
     const int32_t r = (int32_t)blockIdx.x * kRows + row;
     const int32_t valid = p.rows ? __ldcg(&p.rows->valid) : p.T;
     const float c = p.log2_scale;
+    double exact[8] = {};
+    float weight = 1.0f;
+    if (p.exact && warp == 0 && lane < kRows && r < p.T) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) exact[j] = __ldcg(p.exact + 8 * (int64_t)r + j);
+        if (p.main_weight) weight = __ldcg(p.main_weight + r);
+    }
     float m = -INFINITY, s = 0.0f, z = 0.0f;
     if (r < valid) {
         const float* const at = p.stats + r;
@@ -478,9 +454,25 @@ __global__ void __launch_bounds__(32 * kWarps) loss_combine_kernel(const __grid_
     if (in) {
         // (the maximum meets the wanted logit before the logarithm is added: where a
         // word is nearly certain they are equal, and the loss is the logarithm)
-        const float ref = fabsf(m) == INFINITY ? 0.0f : m, log_s = logf(s);
+        const float ref = fabsf(m) == INFINITY ? 0.0f : m;
+        float log_s = logf(s), gap = ref - z;  // (gap: to the wanted logits' mean)
         lse = ref / p.tau + log_s;
-        loss = p.entropy ? p.tau * p.tau * (__ldcg(p.entropy + t) + (ref - z) / p.tau + log_s) : (ref - z) + log_s;
+        if (p.exact) {
+            // Up to 128 rows, a main word of more than 1/2 (it is the maximum then): its
+            // logit from the exact sum, the others' share, s - 1, against that.  The
+            // gradients take p - 1 there from that sum and lse, which from the truncated
+            // one was off by up to 3e-5 (z = 28 over 2048).
+            double y = 0.0;
+            for (int j = 0; j < 8; ++j) y += exact[j];
+            const double over = y - (double)ref;
+            const float d = (float)(over / (double)p.tau);
+            if (fabsf(m) != INFINITY && expf(d) > 0.501f * s) {
+                log_s = log1pf((s - 1.0f) * expf(-d));
+                lse = (float)(y / (double)p.tau + (double)log_s);
+                gap = (float)((double)gap + over - (double)weight * over);
+            }
+        }
+        loss = p.entropy ? p.tau * p.tau * (__ldcg(p.entropy + t) + gap / p.tau + log_s) : gap + log_s;
     }
     p.loss[t] = loss;
     p.lse[t] = lse;
