@@ -339,8 +339,10 @@ typedef enum {
  * (T, k) of logits_type, pitch ld_logits >= k; a logit of -infinity has weight 0.
  * A target or id of V or more counts as none and is reported as GEMM_ERR_INDEX
  * by the next gemm_relu_check_device_error.  1 <= k <=
- * GEMM_RELU_MAX_TEACHER_WORDS; temperature is positive, and it and its inverse
- * are finite.
+ * GEMM_RELU_MAX_TEACHER_WORDS; temperature is positive, and it and log2(e) /
+ * temperature are finite in fp32.  (The loss carries tau^2 times the rounding of
+ * its terms, about 1e-7 of log V: at temperatures far above the logits' spread
+ * nothing is left of it.)
  *
  * A row with no target, or no word of a weight, has loss and lse +0 and a dX of
  * +0, and enters dW in no way, whatever X holds there.  Such rows are left out of

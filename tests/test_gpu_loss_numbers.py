@@ -307,3 +307,18 @@ def test_gradient_of_a_main_word_in_several_entries(T, layout):
     bound += 2.0 ** -11 * (value.abs() + bound) + 2.0 ** -25
     off = ((dw[3] if layout == "nk" else dw[:, 3]).double().cpu() - value).abs()
     assert (off <= bound).all(), ((off / bound).max().item(), (p - q).abs().max().item())
+
+
+@pytest.mark.parametrize("tau", [2.0 ** -20, 2.0 ** -70, 1e-22])
+@pytest.mark.parametrize("T", [20, 300])
+def test_small_temperatures(T, tau):
+    """tau^2 may leave 32 bits where tau times the gap between the logits does not."""
+    V, best, word = 200, 70, 3
+    tau = float(np.float32(tau))
+    x, w, z = exact_logits(T, V, "f16", best)
+    ids = torch.full((T, 1), word, dtype=torch.int32, device=DEV)
+    loss, lse = binding.gemm_relu_distill(x, w, ids, torch.zeros(T, 1, device=DEV), tau, b_layout="nk")
+    binding.check_device_error()
+    want = tau * (z[:, best] - z[:, word])
+    assert (np.abs(loss.double().cpu().numpy() - want) <= 4 * E32 * want).all()
+    assert (np.abs(lse.double().cpu().numpy() - z[:, best] / tau) <= 4 * E32 * z[:, best] / tau).all()

@@ -214,6 +214,8 @@ static int run_rows(const Call& c, const LossPlan& p, int64_t b0, int64_t T, Dev
     return launch(loss_rows_kernel, grid, kRowsThreads, 0, 1, c.st, q);
 }
 
+static float log2_scale(float tau) { return 1.4426950408889634f / tau; }
+
 // The wanted words and the rows, for kStats and kGrad.
 static void wanted(const Call& c, const LossPlan& p, int64_t b0, LossParams& q) {
     q.rows = p.gather ? reinterpret_cast<const RowsHeader*>(c.ws + p.header) : nullptr;
@@ -227,7 +229,7 @@ static void wanted(const Call& c, const LossPlan& p, int64_t b0, LossParams& q) 
         q.targets = c.targets + b0;
     }
     q.V = (int32_t)c.V;
-    q.log2_scale = 1.4426950408889634f / c.tau;
+    q.log2_scale = log2_scale(c.tau);
 }
 
 // An mn-major operand of `rows` x `width` (k and its rows' index): the chunks of a
@@ -492,7 +494,7 @@ static int check_call(const Call& c, int b_layout, int dtype) {
 }
 
 static int check_teacher(const Call& c) {
-    if (c.k < 1 || !(c.tau > 0.0f) || !isfinite(c.tau) || !isfinite(1.0f / c.tau)) return GEMM_ERR_INVALID_ARG;
+    if (c.k < 1 || !(c.tau > 0.0f) || !isfinite(c.tau) || !isfinite(log2_scale(c.tau))) return GEMM_ERR_INVALID_ARG;
     if (c.logits_type != GEMM_LOGITS_F16 && c.logits_type != GEMM_LOGITS_BF16 && c.logits_type != GEMM_LOGITS_F32)
         return GEMM_ERR_INVALID_ARG;
     if (c.T == 0) return GEMM_OK;

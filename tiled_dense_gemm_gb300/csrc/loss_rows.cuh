@@ -472,7 +472,8 @@ __global__ void __launch_bounds__(32 * kWarps) loss_combine_kernel(const __grid_
                 gap = (float)((double)gap + over - (double)weight * over);
             }
         }
-        loss = p.entropy ? p.tau * p.tau * (__ldcg(p.entropy + t) + gap / p.tau + log_s) : gap + log_s;
+        // (tau^2 (entropy + gap / tau + log s), without a square that leaves 32 bits)
+        loss = p.entropy ? p.tau * (gap + p.tau * (__ldcg(p.entropy + t) + log_s)) : gap + log_s;
     }
     p.loss[t] = loss;
     p.lse[t] = lse;
