@@ -373,9 +373,18 @@ typedef enum {
  * 256-byte aligned, that belongs to this call until it has run: calls that may
  * overlap (two streams, two captured graphs) need one each.  Nothing in it has to
  * be set, and nothing is kept in it.  gemm_relu_loss_workspace (host only) returns
- * bytes, or minus a gemm_status_t; k = 0 for targets.  The gradients' is about
- * T V 2 bytes (up to 32 rows, rounded up to eights, twice that) or 512 MiB,
- * whichever is less, + T D 4 (once or for up to 64 shares).
+ * bytes, or minus a gemm_status_t; k = 0 for targets.  It holds (w: D rounded up to
+ * a multiple of 64; besides, less than 128 bytes per row and 16 KiB):
+ *
+ *   losses     a block of R rows at a time: 12 R bytes per 64 words, R the most rows
+ *              of which that is at most 384 MiB, but 2048 at least (beyond 2^20 words it
+ *              is more: 6.4 GB at 2^24) and 16384 at most; from more than 128 rows on a
+ *              copy of the rows, 2 R w; a teacher's words, 8 R k
+ *   gradients  a piece of P words of g at a time: 2 T P bytes (up to 32 rows, rounded up
+ *              to eights, twice that), P the most words of which that is at most 512 MiB,
+ *              but 256 at least (beyond 2^20 rows it is more: 8.6 GB at 2^24); dX in fp32,
+ *              4 T D (up to 32 rows twice) for each of 1 to 64 shares of its reduction; a
+ *              copy of the rows, 2 T w (up to 32 rows twice); a teacher's words, 8 T k
  * Asynchronous on `stream`; bounded waits and the error word as gemm_relu.
  */
 int64_t gemm_relu_loss_workspace(int64_t T, int64_t V, int64_t D, int64_t k, int gradient);
