@@ -56,9 +56,14 @@ inline int launch(void (*fn)(P...), int grid, int threads, size_t smem, int clus
     cfg.blockDim = dim3((unsigned)threads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    // set-up may overlap the previous kernel of the stream (every kernel here
-    // waits for it before it touches global memory; the adapters' main one goes
-    // by the wait of the launch before it)
+    // Set-up may overlap the previous kernel of the stream.  Every kernel here waits for
+    // it before it touches global memory, but for four that go by an earlier wait:
+    // the adapters' main one, the losses' mask kernel, and their products with `late`
+    // or `early`.  (The losses' products also ask for weights in L2 ahead of their
+    // wait, which reads nothing into the kernel.)  Such a launch needs two things: its
+    // predecessor lets dependents start only behind its own wait (and writes nothing
+    // that the launch reads, nor reads what it writes), and the launch waits before it
+    // ends, so that its end says that all before it is done.
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     unsigned n = 1;

@@ -576,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (kMode == kStats) grid_launch_dependents();
     const bool early = kAnyGrad && q.early;
     if (!q.late && !early) grid_dependency_wait();
-    if (kMode != kStats && !early) grid_launch_dependents();  // (what follows may go by this wait)
+    if (kMode != kStats && !early) grid_launch_dependents();  // (behind the wait: what follows may go by it)
     const uint32_t tmem_base = ctrl->tmem_addr;
     const uint32_t S = (uint32_t)q.num_stages, stride = q.stage_bytes;
     const uint32_t full0 = smem_u32(&ctrl->full[0]), empty0 = smem_u32(&ctrl->empty[0]);
@@ -751,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t local = 0, tile = 0;
         if (early) {
             grid_dependency_wait();
-            grid_launch_dependents();
+            grid_launch_dependents();  // (behind the wait: the mask kernel goes by it)
         }
         float scale = 1.0f;
         if constexpr (kAnyGrad) scale = q.scale ? __ldcg(&q.scale->scale) : scale_of(q.top, q.grad_scale, largest_dloss(q.flags, q.limit, q.dloss, q.dloss_stride, q.M));

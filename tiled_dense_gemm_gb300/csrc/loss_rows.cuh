@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(32 * kTeacherWarps) loss_teacher_kernel(const 
     float* const e = reinterpret_cast<float*>(key + padded);
     if (!p.before) grid_launch_dependents();
     grid_dependency_wait();
-    if (p.before) grid_launch_dependents();
+    if (p.before) grid_launch_dependents();  // (a G kernel with `early` follows, which goes by that wait)
     for (int64_t t = (int64_t)blockIdx.x * kTeacherWarps + warp; t < p.T; t += (int64_t)gridDim.x * kTeacherWarps) {
         float top = -INFINITY;
         bool some = false;
