@@ -212,6 +212,50 @@ def test_gradients_of_certain_words_with_the_forward_pass_own_lse(T, D, layout, 
     check_gradients(got, a * g, a * e, x, w, layout, dtype, T, T, V + 32, a)
 
 
+@pytest.mark.parametrize("ignored", [0.0, 0.4])
+@pytest.mark.parametrize("layout,dtype", BOTH)
+@pytest.mark.parametrize("D", [1032, 2056, 4096])
+@pytest.mark.parametrize("T", [100, 129, 300, 513])
+def test_reductions_in_parts(T, D, layout, dtype, ignored):
+    """Logits of spread 2 over widths that are summed in several parts: within the bounds row by row, and over all
+    rows as exact as the parts make them.  Sixteen products at a time lose up to a unit of 2^-23 of the sum so far, low: over n about
+    n / 16 * 2^-23 of its size, which for a spread of 2 is about 4, a third of the loss.  Parts of 256 (up to 128
+    rows): 3e-7 would take 7 of such steps' units; of 1024: 1e-6; one part of 4096 measured 2.4e-6."""
+    V = 1000
+    gen = torch.Generator(device=DEV).manual_seed(D + T)
+    x = torch.randn((T, D), generator=gen, device=DEV).to(DT[dtype])
+    w = (torch.randn((V, D), generator=gen, device=DEV) * 2 * D ** -0.5).to(DT[dtype])
+    y = ref.make_targets(T, V, T, ignored).to(DEV)
+    y[0] = 1
+    valid = y >= 0
+    z = x.double() @ w.double().t()
+    lse = torch.where(valid, torch.logsumexp(z, 1), 0.0)
+    loss = torch.where(valid, lse - z.gather(1, y.clamp(min=0).long()[:, None])[:, 0], 0.0)
+    got, got_lse = binding.gemm_relu_xent(x, laid_out(w, layout), y, b_layout=layout)
+    ids, logits = (t.to(DEV) for t in ref.make_words(T, V, 7, T, ignored))
+    soft, soft_lse = binding.gemm_relu_distill(x, laid_out(w, layout), ids, logits, 2.0, b_layout=layout)
+    binding.check_device_error()
+    rms = 3e-7 if T <= 128 else 1e-6
+    rel = ((got_lse.double() - lse)[valid] / lse[valid]).pow(2).mean().sqrt().item()
+    assert rel <= rms, rel
+    off = ((got.double() - loss)[valid].pow(2).mean() / loss[valid].pow(2).mean()).sqrt().item()
+    assert off <= rms, off
+    assert not got[~valid].any() and not got_lse[~valid].any()
+    has = (ids >= 0).any(1)
+    lse2 = torch.logsumexp(z / 2, 1)
+    rel = ((soft_lse.double() - lse2)[has] / lse2[has]).pow(2).mean().sqrt().item()
+    assert rel <= rms, rel
+    want, _ = ref.losses(x, laid_out(w, layout), ref.words_of(ids=ids, logits=logits, tau=2.0), layout, 2.0, False)
+    ref.check(soft, want, "distill")
+    # the gradients' z in the same parts
+    d = dloss_of(T, 5)
+    dx, dw = binding.gemm_relu_xent_grad(x, laid_out(w, layout), y, got_lse, d, b_layout=layout)
+    binding.check_device_error()
+    rx, rw = ref.gradients(x, laid_out(w, layout), ref.words_of(targets=y), got_lse, d, layout)
+    ref.check(dx, rx, "dx")
+    ref.check(dw, rw, "dw")
+
+
 @pytest.mark.parametrize("layout", ["nk", "kn"])
 @pytest.mark.parametrize("ignored", [False, True])
 def test_weight_gradient_of_many_rows(layout, ignored):
@@ -273,6 +317,100 @@ def test_row_gradient_of_many_words(T, V):
     bound = want * (e + unit + 2.0 ** -11 + 1.001 * (4096 + V / 4096) * E32)
     off = (dx.double() - want).abs()
     assert (off <= bound).all(), (off / want).max().item()
+
+
+@pytest.mark.parametrize("T,V,k", [(2100, 140003, 5), (31, 4200008, 3), (128, 2200008, 3)])
+def test_several_pieces_with_a_teacher(T, V, k):
+    """A teacher's words in every piece of the vocabulary, at both sides of the pieces' borders, some certain."""
+    D, tau = 16, 2.0
+    gen = torch.Generator(device=DEV).manual_seed(7)
+    w = (torch.randn((V, D), generator=gen, device=DEV) * 2 * D ** -0.5).bfloat16()
+    x = torch.randn((T, D), generator=gen, device=DEV).bfloat16()
+    ids = torch.randint(0, V, (T, k), generator=gen, device=DEV, dtype=torch.int32)
+    rows = max(T, 1) if T > 32 else 2 * ((T + 7) // 8 * 8)
+    most = max(256, (1 << 29) // (2 * rows) // 256 * 256)
+    piece = -(-(-(-V // -(-V // most))) // 256) * 256
+    assert piece < V
+    edge = torch.tensor([piece - 1, piece, 0, V - 1], device=DEV, dtype=torch.int32)
+    ids[:, 0] = edge[torch.arange(T, device=DEV) % 4]
+    ids[::5, 1] = -1
+    ids[3::7] = -1
+    sure = torch.arange(T, device=DEV) % 3 == 1
+    word = w[ids[:, 0].clamp(min=0).long()].float()
+    x[sure] = (60 * word / word.pow(2).sum(dim=1, keepdim=True)).to(x.dtype)[sure]
+    logits = torch.randn((T, k), generator=gen, device=DEV)
+    logits[sure, 0] = 12.0
+    d = dloss_of(T, 8)
+    has = ids >= 0
+    live = has.any(1)
+    q = torch.softmax(torch.where(has, logits.double() / tau, -1e30), 1) * has
+    lse = torch.zeros(T, device=DEV)
+    rows = torch.arange(T, device=DEV)
+    u = 2.0 ** -8
+    W, X = w.double(), torch.where(live[:, None], x.double(), 0.0)
+    dx, ex = torch.zeros((T, D), dtype=torch.float64, device=DEV), torch.zeros((T, D), dtype=torch.float64, device=DEV)
+    dw, ew = torch.zeros((V, D), dtype=torch.float64, device=DEV), torch.zeros((V, D), dtype=torch.float64, device=DEV)
+    for at in rows.split(256):
+        z = x[at].double() @ W.t() / tau
+        lse[at] = torch.where(live[at], torch.logsumexp(z, 1), 0.0).float()
+        a = (torch.where(live[at], d[at], torch.zeros(()).to(DEV)) * tau).double()[:, None]
+        r = lse[at].double()[:, None]
+        p = torch.exp(z - r)
+        ez = D * E32 * (x[at].double().abs() @ W.abs().t()) / tau
+        e = p * (ez + 2 * E32 * (z.abs() + r.abs()) + 2 * E32)
+        here = torch.arange(len(at), device=DEV)
+        # (a row's first word, of p above a half, from a sum in 64 bits)
+        top = ids[at, 0].clamp(min=0).long()
+        if T <= 128:
+            exact = p[here, top] * (ez[here, top] / D + 2 * E32)
+            e[here, top] = torch.where((p[here, top] > 0.501) & has[at, 0], exact, e[here, top])
+        size = p.clone()
+        for j in range(k):
+            i = ids[at, j].clamp(min=0).long()
+            p.index_put_((here, i), -q[at, j], accumulate=True)
+            size.index_put_((here, i), q[at, j], accumulate=True)
+            e.index_put_((here, i), q[at, j] * (40 + k) * E32, accumulate=True)
+        g, e = a * p, a * (e + 4 * E32 * size)
+        e = e + u ** (2 if T <= 32 else 1) * (g.abs() + e) + (2.0 ** -134) * live[at].double()[:, None]
+        n = g.abs() + e
+        dx[at], ex[at] = g @ W, e @ W.abs() + V / 16 * E32 * (n @ W.abs())
+        dw += g.t() @ X[at]
+        ew += e.t() @ X[at].abs() + T * E32 * (n.t() @ X[at].abs())
+        del z, p, ez, e, size, g, n
+    got_dx, got_dw = binding.gemm_relu_distill_grad(x, w, ids, logits, lse, d, tau, b_layout="nk")
+    binding.check_device_error()
+    for out, value, bound in ((got_dw, dw, ew), (got_dx, dx, ex)):
+        off = (out.double() - value).abs() - (bound + u * (value.abs() + bound) + 2.0 ** -134)
+        assert off.max().item() <= 0.0
+    assert not got_dx[~live].any()
+
+
+@pytest.mark.parametrize("layout,dtype", BOTH)
+@pytest.mark.parametrize("T", [7, 32, 90, 300])
+def test_gradients_of_losses_of_both_signs_and_many_sizes(T, layout, dtype):
+    """dloss below zero, of both signs among the rows, and over eleven orders of magnitude: binary16's G keeps
+    2^-29 of the largest in full and loses what is below 2^-40 of it."""
+    V, D, k, tau = 504, 136, 4, 1.5
+    gen = torch.Generator().manual_seed(T)
+    x = torch.randn(T, D, generator=gen).to(DT[dtype]).to(DEV)
+    w = laid_out((torch.randn(V, D, generator=gen) * 2 * D ** -0.5).to(DT[dtype]).to(DEV), layout)
+    y = ref.make_targets(T, V, T, 0.2).to(DEV)
+    ids, logits = (t.to(DEV) for t in ref.make_words(T, V, k, T + 1, 0.2))
+    base = dloss_of(T, T + 2)
+    sign = torch.where(torch.arange(T, device=DEV) % 3 == 0, -1.0, 1.0)
+    size = 10.0 ** -(torch.arange(T, device=DEV) % 12).float()
+    _, lse = binding.gemm_relu_xent(x, w, y, b_layout=layout)
+    _, soft = binding.gemm_relu_distill(x, w, ids, logits, tau, b_layout=layout)
+    for d in (-base, base * sign, base * sign * size, torch.full((1,), -0.01, device=DEV)):
+        got = binding.gemm_relu_xent_grad(x, w, y, lse, d, b_layout=layout)
+        want = ref.gradients(x, w, ref.words_of(targets=y), lse, d, layout)
+        for name, o, r in zip(("dx", "dw"), got, want):
+            ref.check(o, r, name)
+        got = binding.gemm_relu_distill_grad(x, w, ids, logits, soft, d, tau, b_layout=layout)
+        want = ref.gradients(x, w, ref.words_of(ids=ids, logits=logits, tau=tau), soft, d, layout, tau, cross=False)
+        for name, o, r in zip(("dx", "dw"), got, want):
+            ref.check(o, r, f"{name} with a teacher")
+    binding.check_device_error()
 
 
 @pytest.mark.parametrize("layout", ["nk", "kn"])
