@@ -140,14 +140,7 @@ static int run_teacher(const Call& c, const LossPlan& p, int64_t b0, int64_t T, 
         q.entropy = reinterpret_cast<float*>(c.ws + p.entropy);
         q.err = d.d_err;
         const int grid = (int)std::min<int64_t>((T + kTeacherWarps - 1) / kTeacherWarps, 16 * d.sm_count);
-        const size_t smem = (size_t)kTeacherWarps * ((c.k + 3) / 4 * 4) * 8;
-        if (p.gather) {
-            rc = launch(loss_teacher_kernel<false>, grid, 32 * kTeacherWarps, smem, 1, c.st, q);
-        } else {
-            q.main = reinterpret_cast<int32_t*>(c.ws + p.main);
-            q.main_weight = reinterpret_cast<float*>(c.ws + p.main_weight);
-            rc = launch(loss_teacher_kernel<true>, grid, 32 * kTeacherWarps, smem, 1, c.st, q);
-        }
+        rc = launch(loss_teacher_kernel, grid, 32 * kTeacherWarps, (size_t)kTeacherWarps * ((c.k + 3) / 4 * 4) * 8, 1, c.st, q);
         if (rc != GEMM_OK) return rc;
     }
     return GEMM_OK;
@@ -168,7 +161,12 @@ static WordSums word_sums(const Call& c, const LossPlan& p) {
     s.W = reinterpret_cast<const uint16_t*>(c.W);
     s.w_word = c.nk ? c.D : 1;
     s.w_depth = c.nk ? 1 : c.V;
-    s.word = c.ids ? reinterpret_cast<const int32_t*>(c.ws + p.main) : c.targets;
+    s.targets = c.targets;
+    if (c.ids) {
+        s.ids = reinterpret_cast<const int32_t*>(c.ws + p.sorted);
+        s.weights = reinterpret_cast<const float*>(c.ws + p.weights);
+        s.k = (int32_t)c.k;
+    }
     s.D = (int32_t)c.D;
     s.bf16 = c.bf16 ? 1 : 0;
     return s;
@@ -200,7 +198,6 @@ static int run_rows(const Call& c, const LossPlan& p, int64_t b0, int64_t T, Dev
         q.rows_of = (int32_t)p.g_rows;
         q.period = p.low ? p.low : (int32_t)T;
         q.sums = word_sums(c, p);
-        if (c.ids) q.main_weight = reinterpret_cast<const float*>(c.ws + p.main_weight);
         q.tau = c.ids ? c.tau : 1.0f;
         q.lse = c.lse;
         q.grad = reinterpret_cast<uint16_t*>(c.ws + p.grad);
@@ -294,6 +291,7 @@ static int run_forward(const Call& c, const LossPlan& p, DeviceState& d) {
         q.stats_pitch = (p.rows + 31) / 32 * 32;
         if (!p.gather) {  // (one block of rows)
             q.exact = reinterpret_cast<double*>(c.ws + p.exact);
+            q.main_weight = reinterpret_cast<float*>(c.ws + p.main_weight);
             q.sums = word_sums(c, p);
             t.grid = std::max(t.grid, std::min((int32_t)T, (int32_t)d.sm_count));  // (a row of those sums per CTA)
         }
@@ -315,14 +313,16 @@ static int run_forward(const Call& c, const LossPlan& p, DeviceState& d) {
         o.limit = limit_of(c);
         o.entropy = c.ids ? reinterpret_cast<const float*>(c.ws + p.entropy) : nullptr;
         o.exact = q.exact;
-        o.main_weight = c.ids && !p.gather ? reinterpret_cast<const float*>(c.ws + p.main_weight) : nullptr;
+        o.main_weight = q.main_weight;
         o.tau = c.tau;
         o.log2_scale = q.log2_scale;
         o.loss = c.loss + b0;
         o.lse = c.lse_out + b0;
         o.err = d.d_err;
-        rc = T <= 1024 ? launch(loss_combine_kernel<32>, (int)((T + 7) / 8), 1024, 0, 1, c.st, o)
-                       : launch(loss_combine_kernel<16>, (int)((T + 7) / 8), 512, 0, 1, c.st, o);
+        const int grid = (int)((T + 7) / 8);
+        rc = !p.gather ? launch(loss_combine_kernel<32, true>, grid, 1024, 0, 1, c.st, o)
+             : T <= 1024 ? launch(loss_combine_kernel<32, false>, grid, 1024, 0, 1, c.st, o)
+                         : launch(loss_combine_kernel<16, false>, grid, 512, 0, 1, c.st, o);
         if (rc != GEMM_OK) return rc;
     }
     return GEMM_OK;

@@ -97,8 +97,10 @@ struct WordSums {
     int64_t ldx;
     const uint16_t* W;
     int64_t w_word, w_depth;  // from one word to the next, and from one k: one of them 1
-    const int32_t* word;      // per row: its target, or a teacher's main word
-    int32_t D, bf16;
+    const int32_t* targets;   // a row's word, or
+    const int32_t* ids;       // a teacher's (T, k), sorted, with weights: its main word
+    const float* weights;
+    int32_t k, D, bf16;
 };
 constexpr int32_t kSumThreads = 256;
 
@@ -149,7 +151,8 @@ struct LossParams {
     float* stats;            // kStats: [tile][3][stats_pitch]
     int64_t stats_pitch;
     WordSums sums;
-    double* exact;           // kStats, up to 128 rows: the logit of a row's main word, in eight parts
+    double* exact;           // kStats, up to 128 rows: the logit of a row's main word, in eight parts,
+    float* main_weight;      // ... and that word's weight
     const float* lse;        // kGrad
     const float* dloss;
     int64_t dloss_stride;    // 0 or 1
@@ -294,6 +297,49 @@ struct Wanted {
         fetch(q, next2, weight2);
     }
 };
+
+// A row's main word, the wanted one that weighs most, and its weight, by one warp.  A
+// word that comes several times weighs as all of its entries: the sorted list goes
+// by in 32 entries at once, each with the sum of its word's entries so far, whose
+// maximum is that of the whole sums.
+__device__ __forceinline__ int32_t main_word(const WordSums& p, int32_t t, float& weight) {
+    weight = 1.0f;
+    if (!p.ids) return __ldcg(p.targets + t);
+    const int32_t lane = (int32_t)threadIdx.x % 32;
+    const int32_t* const ids = p.ids + (int64_t)t * p.k;
+    const float* const weights = p.weights + (int64_t)t * p.k;
+    float most = 0.0f, carry = 0.0f;
+    int32_t word = kNone, before = kNone;  // (carry: the last word's sum before this entry)
+#pragma unroll 2
+    for (int32_t j0 = 0; j0 < p.k; j0 += 32) {
+        const int32_t id = j0 + lane < p.k ? __ldcg(ids + j0 + lane) : kNone;
+        float all = j0 + lane < p.k ? __ldcg(weights + j0 + lane) : 0.0f;
+        if (lane == 0 && id == before) all += carry;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const float x = __shfl_up_sync(0xffffffffu, all, d);
+            const int32_t y = __shfl_up_sync(0xffffffffu, id, d);
+            if (lane >= d && y == id) all += x;
+        }
+        carry = __shfl_sync(0xffffffffu, all, 31);
+        before = __shfl_sync(0xffffffffu, id, 31);
+        if (id != kNone && all > most) {  // (of equal ones the first, which is the lowest)
+            most = all;
+            word = id;
+        }
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        const float x = __shfl_xor_sync(0xffffffffu, most, d);
+        const int32_t y = __shfl_xor_sync(0xffffffffu, word, d);
+        if (x > most || (x == most && y < word)) {
+            most = x;
+            word = y;
+        }
+    }
+    weight = most;
+    return word;
+}
 
 // Thread i's of kSumThreads' products of X's row with a word's weights: 1/2048 of them in
 // each number of 32 bits, and those in 64.
@@ -762,12 +808,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             // are on their way.
             const int32_t e = (int32_t)(quarter + 4u * half);
             for (int32_t t = (int32_t)blockIdx.x; q.exact && t < q.M; t += (int32_t)gridDim.x) {
-                const int32_t word = __ldcg(q.sums.word + t);
+                float weight;
+                const int32_t word = main_word(q.sums, t, weight);
                 const bool is = word >= 0 && word < q.V;
                 double y = is ? some_products(q.sums, t, word, 32 * e + (int32_t)lane) : -INFINITY;
 #pragma unroll
                 for (int d = 16; d > 0; d >>= 1) y += __shfl_xor_sync(0xffffffffu, y, d);
                 if (lane == 0) q.exact[8 * (int64_t)t + e] = y;
+                if (lane == 0 && e == 0 && q.ids) q.main_weight[t] = weight;
             }
         }
         // the copy issued from the staging buffer before must have read it

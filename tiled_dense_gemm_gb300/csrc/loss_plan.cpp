@@ -140,10 +140,6 @@ LossPlan plan_loss(int64_t T, int64_t V, int64_t D, int64_t k, bool gradient) {
         p.entropy = take(4 * rows);
         p.sorted = take(4 * rows * k);
         p.weights = take(4 * rows * k);
-        if (!p.gather) {
-            p.main = take(4 * rows);
-            p.main_weight = take(4 * rows);
-        }
     }
     // The copy's rows start at multiples of 128 bytes, so that a box row lies in one
     // line (1800 of 3000 rows, 50021 words of 2056: 280 us at X's pitch, 266 so; the
@@ -153,7 +149,10 @@ LossPlan plan_loss(int64_t T, int64_t V, int64_t D, int64_t k, bool gradient) {
     if (!gradient) {
         if (parts * ceil_div(rows, 128) > 2000000000ll) p.status = GEMM_ERR_TOO_LARGE;
         p.stats = take(12 * round_up(rows, 32) * parts);
-        if (!p.gather) p.exact = take(64 * rows);
+        if (!p.gather) {
+            p.exact = take(64 * rows);
+            p.main_weight = take(4 * rows);
+        }
     } else {
         const int64_t most = std::max<int64_t>(256, kGradBytes / (2 * p.g_rows) / 256 * 256);
         p.piece = round_up(ceil_div(V, ceil_div(V, most)), 256);

@@ -33,7 +33,7 @@ struct LossPlan {
     int32_t sum_width;   // ... and its tiles' columns
     int64_t pitch;       // of the rows' copy
     // workspace, in bytes from its start
-    int64_t header, index, flags, entropy, sorted, weights, main, main_weight, gathered, stats, exact, grad, sums, bytes;
+    int64_t header, index, flags, entropy, sorted, weights, gathered, stats, exact, main_weight, grad, sums, bytes;
 };
 
 // The logits (T x N, reduction K): `stats` of the forward pass, else G.  b_mn: B

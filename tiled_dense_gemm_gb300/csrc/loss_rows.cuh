@@ -23,8 +23,6 @@ struct TeacherParams {
     float* weights;        // (T, k) q
     int32_t* flags;        // per row: 0, or -1: no word
     float* entropy;        // per row: sum of q log q
-    int32_t* main;         // per row: the word that weighs most, kNone: no word, and its weight
-    float* main_weight;
     int32_t* err;
 };
 
@@ -45,8 +43,7 @@ constexpr int kTeacherWarps = 4;
 // One warp per row: the softmax over its k words in 32 bits, and the words in
 // rising order by counting, for each, the smaller ones (k^2 comparisons out of
 // shared memory; ties in their given order, so that a word given twice is two
-// entries).  kMain: the row's main word too, its weight that of all its entries.
-template <bool kMain>
+// entries).
 __global__ void __launch_bounds__(32 * kTeacherWarps) loss_teacher_kernel(const __grid_constant__ TeacherParams p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const int32_t warp = (int32_t)threadIdx.x / 32, lane = (int32_t)threadIdx.x % 32;
@@ -90,54 +87,24 @@ __global__ void __launch_bounds__(32 * kTeacherWarps) loss_teacher_kernel(const 
         const float log_sum = logf(sum), inv = 1.0f / sum;
         float h = 0.0f;
         __syncwarp();
-        for (int32_t j = lane; j < padded; j += 32) {
-            const float x = j < p.k ? e[j] : -INFINITY, q = expf(x) * inv;
-            if (j < p.k && q != 0.0f) h += q * (x - log_sum);
-            e[j] = j < p.k && key[j] != kNone && some ? q : 0.0f;
-        }
-        __syncwarp();
-        float most = 0.0f;
-        int32_t word = kNone;
         for (int32_t j = lane; j < p.k; j += 32) {
+            const float x = e[j], q = expf(x) * inv;
+            if (q != 0.0f) h += q * (x - log_sum);
             const int32_t mine = key[j];
             int32_t at = 0;
-            float all = 0.0f;
 #pragma unroll 4
             for (int32_t i = 0; i < padded; i += 4) {
                 const int4 o = *reinterpret_cast<const int4*>(key + i);
                 at += (o.x < mine || (o.x == mine && i < j)) + (o.y < mine || (o.y == mine && i + 1 < j)) +
                       (o.z < mine || (o.z == mine && i + 2 < j)) + (o.w < mine || (o.w == mine && i + 3 < j));
-                if constexpr (kMain) {
-                    const float4 q = *reinterpret_cast<const float4*>(e + i);
-                    all += ((o.x == mine ? q.x : 0.0f) + (o.y == mine ? q.y : 0.0f)) + ((o.z == mine ? q.z : 0.0f) + (o.w == mine ? q.w : 0.0f));
-                }
             }
             p.sorted[t * p.k + at] = some ? mine : kNone;
-            p.weights[t * p.k + at] = e[j];
-            if (kMain && (all > most || (all == most && mine < word))) {
-                most = all;
-                word = mine;
-            }
+            p.weights[t * p.k + at] = mine == kNone || !some ? 0.0f : q;
         }
         h = warp_sum(h);
-        if constexpr (kMain) {
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) {
-                const float all = __shfl_xor_sync(0xffffffffu, most, d);
-                const int32_t other = __shfl_xor_sync(0xffffffffu, word, d);
-                if (all > most || (all == most && other < word)) {
-                    most = all;
-                    word = other;
-                }
-            }
-        }
         if (lane == 0) {
             p.flags[t] = some ? 0 : -1;
             p.entropy[t] = h;
-            if constexpr (kMain) {
-                p.main[t] = most > 0.0f ? word : kNone;
-                p.main_weight[t] = most;
-            }
         }
         __syncwarp();
     }
@@ -164,7 +131,6 @@ struct RowsParams {
     // what the gradient at a certain word is found from
     int32_t rows_of, period;
     WordSums sums;
-    const float* main_weight; // of a teacher's main words; null: 1
     float tau;
     const float* lse;
     uint16_t* grad;           // G
@@ -313,18 +279,17 @@ __global__ void __launch_bounds__(kRowsThreads) loss_rows_kernel(const __grid_co
 // without, 94 with a kernel in front of it.
 __global__ void __launch_bounds__(kRowsThreads) loss_mask_kernel(const __grid_constant__ RowsParams p) {
     __shared__ double part[kRowsThreads / 32];
+    __shared__ int32_t main;
     const int32_t i = (int32_t)threadIdx.x, r = (int32_t)blockIdx.x, warp = i / 32, lane = i % 32;
     grid_launch_dependents();
     const int32_t t = r % p.period;
     const int32_t y = t < p.T ? __ldcg(p.flags + t) : -1;
     if (y >= p.limit && i == 0) atomicCAS(p.err + 1, 0, (int32_t)rg::kBadIds);
     const bool in = y >= 0 && y < p.limit;
-    int32_t word = kNone;
     float weight = 1.0f;
-    if (in && r < p.T) {
-        word = __ldcg(p.sums.word + t);
-        if (p.main_weight) weight = __ldcg(p.main_weight + t);
-        if (word < p.from || word - p.from >= p.words) word = kNone;
+    if (warp == 0) {
+        const int32_t word = in && r < p.T ? main_word(p.sums, t, weight) : kNone;
+        if (lane == 0) main = word >= p.from && word - p.from < p.words ? word : kNone;
     }
     const int32_t vecs = p.D / 8;
     if (in) {
@@ -335,6 +300,8 @@ __global__ void __launch_bounds__(kRowsThreads) loss_mask_kernel(const __grid_co
         uint4* const dst = reinterpret_cast<uint4*>(p.gathered + (int64_t)r * p.pitch);
         for (int32_t c = i; c < vecs; c += kRowsThreads) dst[c] = make_uint4(0, 0, 0, 0);
     }
+    __syncthreads();
+    const int32_t word = main;
     if (word != kNone) {
         double z = some_products(p.sums, t, word, i);
 #pragma unroll
@@ -377,8 +344,8 @@ struct CombineParams {
     int32_t limit;
     const float* entropy;   // teacher; null: targets
     float tau, log2_scale;
-    const double* exact;       // up to 128 rows: the logit of a row's main word, in eight parts,
-    const float* main_weight;  // ... and that word's weight; null: 1
+    const double* exact;       // kExact (up to 128 rows): the logit of a row's main word, in eight parts,
+    const float* main_weight;  // ... and that word's weight
     float* loss;
     float* lse;
     int32_t* err;
@@ -387,7 +354,7 @@ struct CombineParams {
 // A block for eight rows (a sector of the statistics), so that a row's parts are
 // in flight at once: its threads take them in turn and are merged in a fixed
 // order.
-template <int kWarps>
+template <int kWarps, bool kExact>
 __global__ void __launch_bounds__(32 * kWarps) loss_combine_kernel(const __grid_constant__ CombineParams p) {
     constexpr int kRows = 8, kLanes = 32 / kRows;  // lanes of a warp per row
     __shared__ float part[3][kWarps][kRows];
@@ -400,10 +367,10 @@ __global__ void __launch_bounds__(32 * kWarps) loss_combine_kernel(const __grid_
     const float c = p.log2_scale;
     double exact[8] = {};
     float weight = 1.0f;
-    if (p.exact && warp == 0 && lane < kRows && r < p.T) {
+    if (kExact && warp == 0 && lane < kRows && r < p.T) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) exact[j] = __ldcg(p.exact + 8 * (int64_t)r + j);
-        if (p.main_weight) weight = __ldcg(p.main_weight + r);
+        if (p.entropy) weight = __ldcg(p.main_weight + r);
     }
     float m = -INFINITY, s = 0.0f, z = 0.0f;
     if (r < valid) {
@@ -457,7 +424,7 @@ __global__ void __launch_bounds__(32 * kWarps) loss_combine_kernel(const __grid_
         const float ref = fabsf(m) == INFINITY ? 0.0f : m;
         float log_s = logf(s), gap = ref - z;  // (gap: to the wanted logits' mean)
         lse = ref / p.tau + log_s;
-        if (p.exact) {
+        if constexpr (kExact) {
             // Up to 128 rows, a main word of more than 1/2 (it is the maximum then): its
             // logit from the exact sum, the others' share, s - 1, against that.  The
             // gradients take p - 1 there from that sum and lse, which from the truncated
