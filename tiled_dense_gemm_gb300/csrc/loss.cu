@@ -73,7 +73,7 @@ static int launch_kernel(DeviceState& d, const TilePlan& t, const LossMaps& m, c
 
 template <bool kPair, int kMode>
 static int launch_tiles(DeviceState& d, const TilePlan& t, const LossMaps& m, const LossParams& q, cudaStream_t st) {
-    if constexpr (kMode == kGrad || kMode == kGradLow)
+    if constexpr (kMode != kStats)
         if (q.K <= Parts<kPair, kMode, true>::kPart) return launch_kernel<kPair, kMode, false>(d, t, m, q, st);
     return launch_kernel<kPair, kMode, true>(d, t, m, q, st);
 }

@@ -234,6 +234,40 @@ __device__ __forceinline__ void store_2d_hint(const CUtensorMap* m, uint32_t src
         : "memory");
 }
 
+// 64 numbers of 32 bits per lane into tensor memory.
+__device__ __forceinline__ void tmem_store_64cols(uint32_t taddr, const float (&v)[64]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x64.b32 [%0],"
+        " {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16,"
+        " %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32,"
+        " %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48,"
+        " %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63, %64};\n\t"
+        "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+        "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+        "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
+        "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])), "r"(__float_as_uint(v[8])),
+        "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])),
+        "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])),
+        "r"(__float_as_uint(v[15])), "r"(__float_as_uint(v[16])), "r"(__float_as_uint(v[17])),
+        "r"(__float_as_uint(v[18])), "r"(__float_as_uint(v[19])), "r"(__float_as_uint(v[20])),
+        "r"(__float_as_uint(v[21])), "r"(__float_as_uint(v[22])), "r"(__float_as_uint(v[23])),
+        "r"(__float_as_uint(v[24])), "r"(__float_as_uint(v[25])), "r"(__float_as_uint(v[26])),
+        "r"(__float_as_uint(v[27])), "r"(__float_as_uint(v[28])), "r"(__float_as_uint(v[29])),
+        "r"(__float_as_uint(v[30])), "r"(__float_as_uint(v[31])), "r"(__float_as_uint(v[32])),
+        "r"(__float_as_uint(v[33])), "r"(__float_as_uint(v[34])), "r"(__float_as_uint(v[35])),
+        "r"(__float_as_uint(v[36])), "r"(__float_as_uint(v[37])), "r"(__float_as_uint(v[38])),
+        "r"(__float_as_uint(v[39])), "r"(__float_as_uint(v[40])), "r"(__float_as_uint(v[41])),
+        "r"(__float_as_uint(v[42])), "r"(__float_as_uint(v[43])), "r"(__float_as_uint(v[44])),
+        "r"(__float_as_uint(v[45])), "r"(__float_as_uint(v[46])), "r"(__float_as_uint(v[47])),
+        "r"(__float_as_uint(v[48])), "r"(__float_as_uint(v[49])), "r"(__float_as_uint(v[50])),
+        "r"(__float_as_uint(v[51])), "r"(__float_as_uint(v[52])), "r"(__float_as_uint(v[53])),
+        "r"(__float_as_uint(v[54])), "r"(__float_as_uint(v[55])), "r"(__float_as_uint(v[56])),
+        "r"(__float_as_uint(v[57])), "r"(__float_as_uint(v[58])), "r"(__float_as_uint(v[59])),
+        "r"(__float_as_uint(v[60])), "r"(__float_as_uint(v[61])), "r"(__float_as_uint(v[62])),
+        "r"(__float_as_uint(v[63]))
+        : "memory");
+}
+
 // 3-D tiled add shared -> global (bulk-group completion).
 __device__ __forceinline__ void reduce_add_3d(const CUtensorMap* m, uint32_t src, int32_t x, int32_t y, int32_t z) {
     asm volatile(
@@ -389,10 +423,16 @@ __device__ __forceinline__ float pick(const float (&v)[kSize], int32_t at) {
 // (6e-7 for a sum that rounds).  Pairs: 5.4e-7 in parts of 1024, which cost
 // nothing; parts of 512 3e-7, at 4096 rows, 65536 words of 2048 682 us for 645.
 // Single CTAs, which wait for memory: 1.3e-7 in parts of 256 (64 rows, 131072 words
-// of 4096: 162.1 -> 163.5 us), 9e-8 in parts of 128 (169.4).  The gradients take the
-// same parts, so that what is left of the truncation is the same in z and in lse and
-// drops out of their difference.
-constexpr int32_t kPartPair = 1024, kPartSingle = 256;
+// of 4096: 162.1 -> 163.5 us), 9e-8 in parts of 128 (169.4).
+//
+// The gradients take the pairs' parts.  So beyond 128 rows what truncation leaves is the
+// same in z and in the forward pass's lse, and drops out of their difference: at 1 - p =
+// 1e-6 and z = 27, binary16, p - 1 is off by 1e-6, the rounding of lse; by 1.7e-4 from
+// an exact lse.  Up to 128 rows words of p > 1/2 are summed exactly in both passes, and
+// the other words' p is off by 1.7e-4 of itself at most there; parts of 256, as the
+// forward pass's, cost 100 rows with a teacher, 32768 words of 1024, 69 -> 74 us (the
+// product stops two parts ahead of the epilogue, which waits for the teacher).
+constexpr int32_t kPartLogits = 1024, kPartFew = 256;
 // dX's and dW's sums, whose terms may all have one sign: in one accumulator they lost
 // 1.07% over 2^20 rows and 0.08% over 94000 words; in parts of 4096 4e-5, a tenth of
 // binary16's rounding.
@@ -402,7 +442,7 @@ constexpr int32_t kPartSum = 4096;
 template <bool kPair, int kMode, bool kMany>
 struct Parts {
     static constexpr bool kLogits = kMode == kStats || kMode == kGrad || kMode == kGradLow;
-    static constexpr int32_t kPart = !kMany ? 1 << 30 : !kLogits ? kPartSum : kPair ? kPartPair : kPartSingle;
+    static constexpr int32_t kPart = !kMany ? 1 << 30 : !kLogits ? kPartSum : kMode == kStats && !kPair ? kPartFew : kPartLogits;
     int32_t first, last, steps, count, two;
 
     // blocks [kb0, kb1) of `bk` k
@@ -433,51 +473,25 @@ struct Divider {
     }
 };
 
-// Eight columns of a row times a factor, rounded to the 16-bit type; kRest: what that
-// rounding left of them (u 1), rounded.
-template <int kBf16, bool kRest>
-__device__ __forceinline__ uint4 pack_8(const float (&v)[64], int at, float u) {
-    uint32_t x[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float a = u * v[at + 2 * j], b = u * v[at + 2 * j + 1];
-        x[j] = pack16(a, b, kBf16);
-        if (kRest) x[j] = rg::rest16x2(a, b, x[j], kBf16);
-    }
-    return make_uint4(x[0], x[1], x[2], x[3]);
-}
-
-// A chunk of 64 columns to a row of the staging buffer, and the first `here` of them
-// (a multiple of 8) to memory: one branch on the type per chunk.
-template <bool kRest>
-__device__ __forceinline__ void stage_64(uint32_t row, uint32_t lane, const float (&v)[64], float u, int32_t bf16) {
+// 64 numbers times a factor, rounded to the 16-bit type.
+__device__ __forceinline__ void pack_64(uint32_t (&x)[32], const float (&v)[64], float u, int32_t bf16) {
     if (bf16) {
 #pragma unroll
-        for (uint32_t i = 0; i < 8; ++i) rg::st_shared_v4(row + ((i ^ (lane & 7u)) << 4), pack_8<1, kRest>(v, 8 * i, u));
+        for (int j = 0; j < 32; ++j) x[j] = pack16(u * v[2 * j], u * v[2 * j + 1], 1);
     } else {
 #pragma unroll
-        for (uint32_t i = 0; i < 8; ++i) rg::st_shared_v4(row + ((i ^ (lane & 7u)) << 4), pack_8<0, kRest>(v, 8 * i, u));
+        for (int j = 0; j < 32; ++j) x[j] = pack16(u * v[2 * j], u * v[2 * j + 1], 0);
     }
 }
 
-__device__ __forceinline__ void stage_32(uint32_t row, uint32_t lane, const float (&v)[64], int at) {
-#pragma unroll
-    for (uint32_t i = 0; i < 8; ++i)
-        rg::st_shared_v4(row + ((i ^ (lane & 7u)) << 4),
-                         make_uint4(__float_as_uint(v[at + 4 * i]), __float_as_uint(v[at + 4 * i + 1]),
-                                    __float_as_uint(v[at + 4 * i + 2]), __float_as_uint(v[at + 4 * i + 3])));
-}
-
-template <bool kRest>
-__device__ __forceinline__ void store_64(uint16_t* dst, const float (&v)[64], int32_t here, int32_t bf16) {
+// What that rounding left of them, rounded.
+__device__ __forceinline__ void rest_64(uint32_t (&x)[32], const float (&v)[64], int32_t bf16) {
     if (bf16) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (8 * i < here) reinterpret_cast<uint4*>(dst)[i] = pack_8<1, kRest>(v, 8 * i, 1.0f);
+        for (int j = 0; j < 32; ++j) x[j] = rg::rest16x2(v[2 * j], v[2 * j + 1], x[j], 1);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (8 * i < here) reinterpret_cast<uint4*>(dst)[i] = pack_8<0, kRest>(v, 8 * i, 1.0f);
+        for (int j = 0; j < 32; ++j) x[j] = rg::rest16x2(v[2 * j], v[2 * j + 1], x[j], 0);
     }
 }
 
@@ -549,9 +563,9 @@ __device__ __forceinline__ void finish_dx(const FinishParams& p, int32_t threads
         finish_lanes<1>(p, threads);
 }
 
-// kMany false: reductions of one part (kGrad, whose epilogue is slower by 1.4 us a tile
-// with room for several parts' sums: 300 rows, 32008 words of 1000 by columns, 82.8 us
-// without, 85.5 with).
+// kMany false: reductions of one part.  (The gradients with room for several parts in
+// all three kernels: 64 rows, 65536 words of 2048, 140.4 us for 137.2, 300 rows, 32008 of
+// 1000 by columns, 85.5 for 81.5.)
 template <bool kPair, int kMode, bool kMany>
 __global__ void __launch_bounds__(kThreads, 1)
     loss_kernel(const __grid_constant__ LossMaps maps, const __grid_constant__ LossParams q) {
@@ -857,10 +871,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             };
             const float c = q.log2_scale;
-            // This warp's chunks of the tile, summed over the parts of the reduction: kStats all of
-            // them, elsewhere the last part is added chunk by chunk as they are written (mostly
-            // it is the only one).
-            float z[2][64];
             const Parts<kPair, kMode, kMany> parts(k.kb0, k.kb1, q.bk);
             uint32_t taddr = 0;
             auto filled = [&]() {  // the accumulator of the next part
@@ -870,36 +880,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 return true;
             };
-            auto add = [&](float(&sum)[64], int32_t ch) {
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    float v[16];
-                    __syncwarp();
-                    tmem_load_16cols(taddr + 64u * (uint32_t)ch + 16u * h, v);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) sum[16 * h + j] += v[j];
-                }
-            };
-            bool ok = true;
-            if (kMode == kStats || (kMany && parts.count > 1)) {
+            // This warp's chunks of the tile, summed over the parts of the reduction; the last
+            // part's accumulator is still held if `keep`.
+            auto sum_parts = [&](float(&z)[2][64], bool keep) {
 #pragma unroll
                 for (int j = 0; j < 64; ++j) z[0][j] = z[1][j] = 0.0f;
 #pragma unroll 1
-                for (int32_t part = 0; part < parts.count - (kMode == kStats ? 0 : 1); ++part) {
-                    ok = filled();
-                    if (!ok) break;
+                for (int32_t part = 0; part < parts.count; ++part) {
+                    if (!filled()) return false;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const int32_t ch = (int32_t)half + 2 * i;
                         if (ch >= chunks || row0 >= row_end) break;  // (uniform over the warp)
-                        add(z[i], ch);
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            float v[16];
+                            __syncwarp();
+                            tmem_load_16cols(taddr + 64u * (uint32_t)ch + 16u * h, v);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) z[i][16 * h + j] += v[j];
+                        }
                     }
+                    if (keep && part == parts.count - 1) break;
                     release(local & 1u);
                     ++local;
                 }
-            }
-            if (!ok) break;
+                return true;
+            };
             if constexpr (kMode == kStats) {
+                float z[2][64];
+                if (!sum_parts(z, false)) break;
                 Wanted want;
                 want.start(q, t, y, live, n0);
                 const int32_t n_end = min(q.N, n0 + q.width);
@@ -971,7 +981,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             Wanted want;
             if constexpr (kAnyGrad) want.start(q, t, y, live, n0 + q.w_row);
-            if (parts.count > 0 && !filled()) break;
+            if (kMany && parts.count > 1) {
+                // (back into the last accumulator, from where each chunk is taken as if it were
+                // the only part: held in registers beside what the epilogue needs, the gradients
+                // of 16 rows, 65536 words of 2048, in parts of 256 were 145.5 us for 143.4)
+                float z[2][64];
+                if (!sum_parts(z, true)) break;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int32_t ch = (int32_t)half + 2 * i;
+                    if (ch >= chunks || row0 >= row_end) break;  // (uniform over the warp)
+                    __syncwarp();
+                    tmem_store_64cols(taddr + 64u * (uint32_t)ch, z[i]);
+                }
+            } else if (parts.count > 0 && !filled()) {
+                break;
+            }
             // kGrad: the last tile's zeros go on to the end of a chunk of 64 columns of G,
             // the others stop where the next one begins, inside a chunk perhaps
             const int32_t stop = !kAnyGrad ? min(q.N, n0 + 64 * chunks) : n0 + q.width >= q.N ? (q.N + 63) & ~63 : n0 + q.width;
@@ -1000,51 +1025,58 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (here < 64) {
                         // part of a chunk (the tile's last): straight from the registers
-                        uint16_t* const dst = q.grad + (int64_t)r * q.grad_pitch + col;
-                        if (r < (kLow ? q.low : q.M)) {
-                            store_64<false>(dst, v, here, q.bf16);
-                            if constexpr (kLow) store_64<true>(dst + (int64_t)q.low * q.grad_pitch, v, here, q.bf16);
+                        uint32_t x[32];
+                        pack_64(x, v, 1.0f, q.bf16);
+                        uint16_t* dst = q.grad + (int64_t)r * q.grad_pitch + col;
+                        const bool write = r < (kLow ? q.low : q.M);
+                        for (int part = 0;; ++part) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                if (8 * i < here && write)
+                                    reinterpret_cast<uint4*>(dst)[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                            if (part == 1 || !kLow) break;
+                            dst += (int64_t)q.low * q.grad_pitch;
+                            rest_64(x, v, q.bf16);
                         }
                         return;
                     }
                 }
                 if constexpr (kAnyGrad || kMode == kWeight) {
-                    turn();
-                    stage_64<false>(staging + lane * 128u, lane, v, kMode == kWeight ? scale : 1.0f, q.bf16);
-                    if constexpr (kMode == kGrad) {
-                        // the wanted words, over what the row's thread has just written
-                        int32_t last = kNone;
-                        float g = 0.0f;
-                        while (__any_sync(0xffffffffu, want.next - c0 < 64)) {
-                            const int32_t at = want.next - c0;
-                            const float p = pick<0, 64>(v, at);
-                            if (at < 64) {
-                                g = (at == last ? g : p) - coef * want.weight;  // (a word may come twice)
-                                last = at;
-                                st_shared_u16(staging + lane * 128u + ((((uint32_t)at >> 3) ^ (lane & 7u)) << 4) + ((uint32_t)at & 7u) * 2u,
-                                              rg::round16(g, q.bf16));
-                                want.advance(q);
+                    uint32_t x[32];
+                    pack_64(x, v, kMode == kWeight ? scale : 1.0f, q.bf16);
+                    for (int part = 0;; ++part) {
+                        turn();
+#pragma unroll
+                        for (uint32_t i = 0; i < 8; ++i)
+                            rg::st_shared_v4(staging + lane * 128u + ((i ^ (lane & 7u)) << 4),
+                                             make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]));
+                        if constexpr (kMode == kGrad) {
+                            // the wanted words, over what the row's thread has just written
+                            int32_t last = kNone;
+                            float g = 0.0f;
+                            while (__any_sync(0xffffffffu, want.next - c0 < 64)) {
+                                const int32_t at = want.next - c0;
+                                const float p = pick<0, 64>(v, at);
+                                if (at < 64) {
+                                    g = (at == last ? g : p) - coef * want.weight;  // (a word may come twice)
+                                    last = at;
+                                    st_shared_u16(staging + lane * 128u + ((((uint32_t)at >> 3) ^ (lane & 7u)) << 4) + ((uint32_t)at & 7u) * 2u,
+                                                  rg::round16(g, q.bf16));
+                                    want.advance(q);
+                                }
                             }
                         }
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (kMode == kWeight && q.once)
-                            store_2d_hint(&maps.d, staging, col + q.d_col, row0 + q.d_row, l2_policy_evict_first());
-                        else
-                            tma_store_2d(&maps.d, staging, col + q.d_col, row0 + q.d_row);
-                        bulk_commit_group();
-                    }
-                    if constexpr (kLow) {
-                        turn();
-                        stage_64<true>(staging + lane * 128u, lane, v, 1.0f, q.bf16);
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
-                            tma_store_2d(&maps.low, staging, col + q.d_col, row0 + q.d_row);
+                            if (kMode == kWeight && q.once)
+                                store_2d_hint(&maps.d, staging, col + q.d_col, row0 + q.d_row, l2_policy_evict_first());
+                            else
+                                tma_store_2d(kLow && part == 1 ? &maps.low : &maps.d, staging, col + q.d_col, row0 + q.d_row);
                             bulk_commit_group();
                         }
+                        if (!kLow || part == 1) break;
+                        rest_64(x, v, q.bf16);
                     }
                 }
                 if constexpr (kMode == kSum) {
@@ -1053,7 +1085,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int h = 0; h < 2; ++h) {
                         if (col + 32 * h >= q.N) break;
                         turn();
-                        stage_32(staging + lane * 128u, lane, v, 32 * h);
+#pragma unroll
+                        for (uint32_t i = 0; i < 8; ++i)
+                            rg::st_shared_v4(staging + lane * 128u + ((i ^ (lane & 7u)) << 4),
+                                             make_uint4(__float_as_uint(v[32 * h + 4 * i]), __float_as_uint(v[32 * h + 4 * i + 1]),
+                                                        __float_as_uint(v[32 * h + 4 * i + 2]),
+                                                        __float_as_uint(v[32 * h + 4 * i + 3])));
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
@@ -1068,20 +1105,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
 #pragma unroll 1
             for (int32_t ch = (int32_t)half; ch < chunks; ch += 2) {
-                if (kMany && parts.count > 1 && row0 < row_end) {
-                    add(z[0], ch);
-                } else if (parts.count > 0 && row0 < row_end) {
+                float v[64];
+                if (parts.count > 0 && row0 < row_end) {
                     __syncwarp();
-                    tmem_load_64cols(taddr + 64u * (uint32_t)ch, z[0]);
+                    tmem_load_64cols(taddr + 64u * (uint32_t)ch, v);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) z[0][j] = 0.0f;
+                    for (int j = 0; j < 64; ++j) v[j] = 0.0f;
                 }
-                chunk(z[0], ch);
-                if (kMany && parts.count > 1) {
-#pragma unroll
-                    for (int j = 0; j < 64; ++j) z[0][j] = z[1][j];
-                }
+                chunk(v, ch);
             }
             if (parts.count > 0) {
                 release(local & 1u);
