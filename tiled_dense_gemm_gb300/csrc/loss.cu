@@ -73,8 +73,10 @@ static int launch_kernel(DeviceState& d, const TilePlan& t, const LossMaps& m, c
 
 template <bool kPair, int kMode>
 static int launch_tiles(DeviceState& d, const TilePlan& t, const LossMaps& m, const LossParams& q, cudaStream_t st) {
-    if constexpr (kMode != kStats)
-        if (q.K <= Parts<kPair, kMode, true>::kPart) return launch_kernel<kPair, kMode, false>(d, t, m, q, st);
+    if constexpr (kMode != kStats) {
+        const int64_t blocks = ((int64_t)q.K + q.bk - 1) / q.bk, share = (blocks + q.splits - 1) / q.splits;
+        if (share * q.bk <= Parts<kPair, kMode, true>::kPart) return launch_kernel<kPair, kMode, false>(d, t, m, q, st);
+    }
     return launch_kernel<kPair, kMode, true>(d, t, m, q, st);
 }
 
