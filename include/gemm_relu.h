@@ -357,12 +357,23 @@ typedef enum {
  * of the losses); 0: dloss[0] for all.  dX or dW null: not computed.  Outputs must
  * not overlap inputs (not checked).  T == 0: nothing but dW = +0.
  *
- * Arithmetic: z, the softmax and both sums in fp32; g is rounded to `dtype` once
- * before the gradients' products (up to 32 rows the rest that this leaves, rounded,
- * is kept beside it), dX and dW once at the end.  Where a row gives a wanted word
- * more than 1/2, little may be left of g there: up to 128 rows it is found from a
- * sum of z in 64 bits, beyond it carries dloss times what the tensor core's sum is
- * off by (2e-5 at z = 19, D = 576; more with D).  g is held times a
+ * Arithmetic: z, the softmax and both sums in fp32, on the tensor core, which cuts
+ * what it adds to about 24 bits of the sum, always towards zero.  So sums are made in
+ * parts, added up in fp32: of 1024 products of z (256 in the losses of up to 128
+ * rows), of 4096 rows or words in dW and dX.  That leaves z up to 6e-6 of itself low
+ * in binary16, 3e-6 in bfloat16, where all its products have one sign (1.7e-4 and 7e-5
+ * at z = 27), and sums of one sign 4e-5.  Next to that:
+ *  - A loss is made of differences from the row's largest logit, so it is never below 0
+ *    (targets), and at a nearly certain word it has the digits of a sum that is 1 + the
+ *    rest, in fp32.
+ *  - Where a row gives its wanted word (a teacher's: the one of the largest weight in
+ *    all its entries) more than 1/2, little may be left of g there.  Up to 128 rows
+ *    that word's z is summed exactly, in the losses, lse and gradients alike.  Beyond,
+ *    the gradients sum z as the losses do, and what is cut from z drops out against the
+ *    lse of a forward call that had more than 128 rows too; with another lse g is off by
+ *    dloss p times what is cut from z.
+ * g is rounded to `dtype` once before the gradients' products (up to 32 rows the rest
+ * that this leaves, rounded, is kept beside it), dX and dW once at the end.  g is held times a
  * factor that brings the largest |dloss tau| to the top of a binade, in binary16
  * just below 2^15: there terms below 2^-40 of that are lost, and those below
  * 2^-29 lose bits.  (Outside 1e-30 .. 1e30 the factor is 1.)  Results do not
@@ -374,7 +385,7 @@ typedef enum {
  * overlap (two streams, two captured graphs) need one each.  Nothing in it has to
  * be set, and nothing is kept in it.  gemm_relu_loss_workspace (host only) returns
  * bytes, or minus a gemm_status_t; k = 0 for targets.  It holds (w: D rounded up to
- * a multiple of 64; besides, less than 128 bytes per row and 16 KiB):
+ * a multiple of 64; besides, less than 128 bytes per row and 24 KiB):
  *
  *   losses     a block of R rows at a time: 12 R bytes per 64 words, R the most rows
  *              of which that is at most 384 MiB, but 2048 at least (beyond 2^20 words it

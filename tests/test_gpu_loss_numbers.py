@@ -186,6 +186,25 @@ def test_lse_of_up_to_128_rows_with_a_certain_word(T, layout, dtype):
         assert (off_lse <= e).all(), (off_lse / lse).max()
 
 
+@pytest.mark.parametrize("layout", ["nk", "kn"])
+@pytest.mark.parametrize("D", [8, 72, 264, 1000, 8200, 40008])
+@pytest.mark.parametrize("T", [1, 7, 128])
+def test_lse_of_certain_words_of_any_width(T, D, layout):
+    """The exact logits are summed in shares over warps and CTAs, as many as the width and the rows give."""
+    V = 64
+    x, w, y = nearly_certain(T, D, V, "f16", T + D)
+    z = x.double().cpu().numpy() @ w.double().cpu().numpy().T
+    best, (lse, loss) = z.argmax(axis=1), logsumexp(z)
+    ok = loss < 0.6  # (p > 1/2: 8 numbers at random may lie closer than the words' halves)
+    got, got_lse = binding.gemm_relu_xent(x, laid_out(w, layout), torch.from_numpy(best).int().to(DEV), b_layout=layout)
+    binding.check_device_error()
+    e = 25 * E32 / 2 + 2 * truncated(T, x, w, 256).max(axis=1) * loss + 4 * E32 * loss
+    off, off_lse = np.abs(got.double().cpu().numpy() - loss), np.abs(got_lse.double().cpu().numpy() - lse)
+    assert ok.any()
+    assert (off_lse <= e + E32 / 2 * lse)[ok].all(), (off_lse / lse)[ok].max()
+    assert (off <= e)[ok].all(), off[ok].max()
+
+
 @pytest.mark.parametrize("layout,dtype", BOTH)
 @pytest.mark.parametrize("T,D", [(1, 2048), (20, 2048), (100, 2048), (129, 2056), (300, 4096), (300, 1544)])
 def test_gradients_of_certain_words_with_the_forward_pass_own_lse(T, D, layout, dtype):

@@ -29,7 +29,7 @@ def test_workspace_is_what_the_header_says(gemm_lib, T, V, D, k):
     stats = 12 * up(V, 64) // 64
     most = max(2048, min(16384, (384 << 20) // stats // 256 * 256))
     R = T if T <= most else up(-(-T // -(-T // most)), 256)
-    rest = 128 * R + (16 << 10)
+    rest = 128 * R + (24 << 10)
     need = size(T, V, D, k, 0)
     told = stats * R + (2 * R * w if T > 128 else 0) + 8 * R * k
     assert told <= need <= told + rest + 32 * stats, (need, told)
@@ -39,7 +39,7 @@ def test_workspace_is_what_the_header_says(gemm_lib, T, V, D, k):
     need = size(T, V, D, k, 1)
     told = 2 * rows * P + 2 * rows * w + 8 * T * k
     share = 4 * rows * D
-    assert told + share <= need <= told + 64 * share + 128 * T + (16 << 10), (need, told, share)
+    assert told + share <= need <= told + 64 * share + 128 * T + (24 << 10), (need, told, share)
     assert (need - told) // share <= 64 or T < 32
 
 

@@ -295,7 +295,10 @@ static int run_forward(const Call& c, const LossPlan& p, DeviceState& d) {
             q.exact = reinterpret_cast<double*>(c.ws + p.exact);
             q.main_weight = reinterpret_cast<float*>(c.ws + p.main_weight);
             q.sums = word_sums(c, p);
-            t.grid = std::max(t.grid, std::min((int32_t)T, (int32_t)d.sm_count));  // (a row of those sums per CTA)
+            // a share per warp of the tiles' CTAs, and of others where those are few
+            const int64_t most = (c.D + 255) / 256;
+            t.grid = (int32_t)std::max<int64_t>(t.grid, std::min<int64_t>(d.sm_count, (T * most + 7) / 8));
+            q.shares = (int32_t)std::max<int64_t>(1, std::min(most, std::min<int64_t>(8 * t.grid, kMostShares) / T));
         }
         rc = encode_rows_of_x(m, c, p, b0, T, t, q);
         if (rc == GEMM_OK) rc = encode_words(m, c, t, q);
@@ -315,6 +318,7 @@ static int run_forward(const Call& c, const LossPlan& p, DeviceState& d) {
         o.limit = limit_of(c);
         o.entropy = c.ids ? reinterpret_cast<const float*>(c.ws + p.entropy) : nullptr;
         o.exact = q.exact;
+        o.shares = q.shares;
         o.main_weight = q.main_weight;
         o.tau = c.tau;
         o.log2_scale = q.log2_scale;

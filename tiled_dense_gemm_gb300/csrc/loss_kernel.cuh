@@ -32,17 +32,17 @@
 // What bounds it, and what it measured (the GPU's time alone, in a CUDA graph
 // whose inputs rotate beyond L2):
 //   up to 128 rows: the weights' way from memory.  64 rows, 131072 words of 4096:
-//     162 us, 6.6 TB/s of weights; 16 rows, 65536 of 2048: 45 us; one row, 32000
-//     of 1024: 16.0 us, of which 6.4 are left with next to no words.  (Boxes of 256
+//     158-162 us, 6.6-6.8 TB/s of weights; 16 rows, 65536 of 2048: 45 us; one row, 32000
+//     of 1024: 16.1 us, of which 6.4 are left with next to no words.  (Boxes of 256
 //     k: 5-15% slower; tiles of 64 to 112 words 5-60%.)  The gradients pass the
-//     weights three times (G, dX, dW): 16 rows, 65536 of 2048: 132 us, 6.1 TB/s of
-//     those; 128 rows, 131072 of 4096: 522 us, 6.2 TB/s.
-//   many rows, alone: bytes from L2 into the multiprocessors, 13.4-14.2 TB/s in
+//     weights three times (G, dX, dW): 16 rows, 65536 of 2048: 137 us, 5.9 TB/s of
+//     those; 128 rows, 131072 of 4096: 525 us, 6.1 TB/s.
+//   many rows, alone: bytes from L2 into the multiprocessors, 12.7-15.6 TB/s in
 //     every product (a pair takes in 64 KB per 512 clocks of the tensor core, which
-//     at 1.8 GHz would be 17.5 TB/s): the tensor pipe is active 72-81% of the time.
+//     at 1.8 GHz would be 17.5 TB/s): the tensor pipe is active 65-87% of the time.
 //   many rows, back to back: the power cap.  8192 rows, 131072 words of 4096: 5.1-
 //     5.3 ms, 1660-1730 TFLOP/s at 1.5 GHz, what the library product sustains; the
-//     gradients of 4096 rows 7.7-8.0 ms.
+//     gradients of 4096 rows 7.8-8.3 ms.
 //   rows whose pitch is not a multiple of 128 bytes cost a second line per box
 //     row: 50021 words of 2056, 1800 of 3000 rows in use, 266-290 us.
 #pragma once
@@ -151,7 +151,8 @@ struct LossParams {
     float* stats;            // kStats: [tile][3][stats_pitch]
     int64_t stats_pitch;
     WordSums sums;
-    double* exact;           // kStats, up to 128 rows: the logit of a row's main word, in eight parts,
+    int32_t shares;          // kStats, up to 128 rows: so many shares of each row's
+    double* exact;           // ... main word's logit,
     float* main_weight;      // ... and that word's weight
     const float* lse;        // kGrad
     const float* dloss;
@@ -390,34 +391,83 @@ __device__ __forceinline__ int32_t main_word(const WordSums& p, int32_t t, float
     return word;
 }
 
-// Thread i's of kSumThreads' products of X's row with a word's weights: 1/2048 of them in
-// each number of 32 bits, and those in 64.
+// Eight of the products of X's row with a word's weights, from k = d on (D is a
+// multiple of 8); each is exact in 32 bits.
+__device__ __forceinline__ void products_8(const WordSums& p, const uint16_t* x, const uint16_t* w, int32_t d, float (&o)[8]) {
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(x + d));
+    uint4 b;
+    if (p.w_depth == 1) {
+        b = __ldg(reinterpret_cast<const uint4*>(w + d));
+    } else {
+        uint32_t e[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) e[j] = __ldg(w + (int64_t)(d + j) * p.w_depth);
+        b = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+    }
+    const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 m = rg::unpack16(av[j], p.bf16), n = rg::unpack16(bv[j], p.bf16);
+        o[2 * j] = m.x * n.x;
+        o[2 * j + 1] = m.y * n.y;
+    }
+}
+
+// Thread i's of kSumThreads' share of that logit: 1/2048 of the products in each number
+// of 32 bits, and those in 64.
 __device__ __forceinline__ double some_products(const WordSums& p, int32_t t, int32_t word, int32_t i) {
-    const uint16_t* const x = p.X + (int64_t)t * p.ldx;
-    const uint16_t* const w = p.W + (int64_t)word * p.w_word;
+    const uint16_t *const x = p.X + (int64_t)t * p.ldx, *const w = p.W + (int64_t)word * p.w_word;
     float sum[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    for (int32_t d = 8 * i; d < p.D; d += 8 * kSumThreads) {  // (D a multiple of 8)
-        const uint4 a = __ldg(reinterpret_cast<const uint4*>(x + d));
-        uint4 b;
-        if (p.w_depth == 1) {
-            b = __ldg(reinterpret_cast<const uint4*>(w + d));
-        } else {
-            uint32_t e[8];
+    for (int32_t d = 8 * i; d < p.D; d += 8 * kSumThreads) {
+        float o[8];
+        products_8(p, x, w, d, o);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) e[j] = __ldg(w + (int64_t)(d + j) * p.w_depth);
-            b = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
-        }
-        const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 m = rg::unpack16(av[j], p.bf16), n = rg::unpack16(bv[j], p.bf16);
-            sum[2 * j] = fmaf(m.x, n.x, sum[2 * j]);
-            sum[2 * j + 1] = fmaf(m.y, n.y, sum[2 * j + 1]);
-        }
+        for (int j = 0; j < 8; ++j) sum[j] += o[j];
     }
     double z = 0.0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) z += (double)sum[j];
+    return z;
+}
+
+// A sum in two numbers of 32 bits, the second what rounding left of the first (Knuth's
+// exact sum of two): as exact as 64 bits here, whose additions take the GPU 64 clocks a
+// warp.
+struct Wide {
+    float hi, lo;
+
+    __device__ __forceinline__ void add(float b) {
+        const float s = __fadd_rn(hi, b), t = __fsub_rn(s, hi);
+        lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, t)), __fsub_rn(b, t)));
+        hi = s;
+    }
+    __device__ __forceinline__ void add_lane(int d) {  // another lane's
+        const float h = __shfl_xor_sync(0xffffffffu, hi, d), l = __shfl_xor_sync(0xffffffffu, lo, d);
+        add(h);
+        lo = __fadd_rn(lo, l);
+    }
+};
+
+// One of `shares` shares of that logit by one warp.
+__device__ __forceinline__ Wide exact_share(const WordSums& p, int32_t t, int32_t word, int32_t share, int32_t shares) {
+    const uint16_t *const x = p.X + (int64_t)t * p.ldx, *const w = p.W + (int64_t)word * p.w_word;
+    const int64_t vecs = p.D / 8;
+    const int32_t end = 8 * (int32_t)((share + 1) * vecs / shares);
+    Wide z = {0.0f, 0.0f}, z2 = z;
+#pragma unroll 2
+    for (int32_t d = 8 * ((int32_t)(share * vecs / shares) + (int32_t)threadIdx.x % 32); d < end; d += 256) {
+        float o[8];
+        products_8(p, x, w, d, o);
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            z.add(o[j]);
+            z2.add(o[j + 1]);
+        }
+    }
+    z.add(z2.hi);
+    z.lo = __fadd_rn(z.lo, z2.lo);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) z.add_lane(d);
     return z;
 }
 
@@ -832,19 +882,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (kAnyGrad) scale = q.scale ? __ldcg(&q.scale->scale) : scale_of(q.top, q.grad_scale, largest_dloss(q.flags, q.limit, q.dloss, q.dloss_stride, q.M));
         if constexpr (kMode == kWeight) scale = __ldcg(&q.scale->unscale);
         if constexpr (!kPair && kMode == kStats) {
-            // The logit of a row's main word, summed exactly (see the joining kernel): a row
-            // per CTA, an eighth of its products per warp, while the first tile's weights
-            // are on their way.
-            const int32_t e = (int32_t)(quarter + 4u * half);
-            for (int32_t t = (int32_t)blockIdx.x; q.exact && t < q.M; t += (int32_t)gridDim.x) {
+            // The exact logits of the rows' main words (see the joining kernel), while the
+            // first tile's weights are on their way: a share of a row per warp, over all CTAs.
+            // (A column of W by words is a line per k, and soon a page: with a row per CTA 8
+            // rows, 128000 words of 8192 by columns, took 384 us, 313 so, 310 without these
+            // sums; with a CTA beside the others for eight rows 430.)
+            for (int32_t i = (int32_t)(blockIdx.x + gridDim.x * (quarter + 4u * half)); i < q.M * q.shares; i += 8 * (int32_t)gridDim.x) {
+                const int32_t t = i / q.shares, share = i - t * q.shares;
                 float weight;
                 const int32_t word = main_word(q.sums, t, weight);
                 const bool is = word >= 0 && word < q.V;
-                double y = is ? some_products(q.sums, t, word, 32 * e + (int32_t)lane) : -INFINITY;
-#pragma unroll
-                for (int d = 16; d > 0; d >>= 1) y += __shfl_xor_sync(0xffffffffu, y, d);
-                if (lane == 0) q.exact[8 * (int64_t)t + e] = y;
-                if (lane == 0 && e == 0 && q.ids) q.main_weight[t] = weight;
+                const Wide y = is ? exact_share(q.sums, t, word, share, q.shares) : Wide{-INFINITY, 0.0f};
+                if (lane == 0) q.exact[i] = (double)y.hi + (double)y.lo;
+                if (lane == 0 && share == 0 && q.ids) q.main_weight[t] = weight;
             }
         }
         // the copy issued from the staging buffer before must have read it

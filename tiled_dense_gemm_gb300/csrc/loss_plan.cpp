@@ -150,7 +150,7 @@ LossPlan plan_loss(int64_t T, int64_t V, int64_t D, int64_t k, bool gradient) {
         if (parts * ceil_div(rows, 128) > 2000000000ll) p.status = GEMM_ERR_TOO_LARGE;
         p.stats = take(12 * round_up(rows, 32) * parts);
         if (!p.gather) {
-            p.exact = take(64 * rows);
+            p.exact = take(8 * kMostShares);
             p.main_weight = take(4 * rows);
         }
     } else {

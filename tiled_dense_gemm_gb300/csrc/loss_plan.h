@@ -20,6 +20,9 @@ struct TilePlan {
     int32_t a_bytes, stage_bytes, num_stages, smem_bytes, tmem_cols, grid;
 };
 
+// Shares of exact logits of a call (eight warps on each of 152 SMs).
+constexpr int64_t kMostShares = 1216;
+
 struct LossPlan {
     int32_t status;
     int64_t rows;        // forward: rows of a block; backward: all

@@ -268,11 +268,11 @@ __global__ void __launch_bounds__(kRowsThreads) loss_rows_kernel(const __grid_co
 //
 // * a copy of X with zeros in the rows that are not in use, for dW, and the scale;
 // * the gradient at the row's main word, if that is all but certain.  Little is
-//   left of p - q there, while the tensor core's z, whose sums it truncates, is off
-//   by 2e-5 (z = 19 over 576; more over more).  So z is summed once more, 1/2048 of the products in each number
-//   of 32 bits and those in 64, and 1 + expm1(z / tau - lse) taken for p; that goes
-//   over G's entry when the kernel of G is done.  (One row of 576, binary16, 1 - p =
-//   0.003: dX off by 2.4e-4, its own rounding; 6.7e-3 without.)
+//   left of p - q there, while the tensor core's z is off by up to 6e-6 of itself.  So z
+//   is summed once more, 1/2048 of the products in each number of 32 bits and those in
+//   64, as the forward pass has done for its lse, and 1 + expm1(z / tau - lse) taken for
+//   p; that goes over G's entry when the kernel of G is done.  (One row of 576, binary16,
+//   1 - p = 0.003, from an exact lse: dX off by 2.4e-4, its own rounding; 6.7e-3 without.)
 //
 // Of more rows the certain ones have little part in dX's and dW's size, and G's
 // kernel leaves no room beside it: 300 rows, 32008 words of 1000 by columns, 83 us
@@ -344,7 +344,8 @@ struct CombineParams {
     int32_t limit;
     const float* entropy;   // teacher; null: targets
     float tau, log2_scale;
-    const double* exact;       // kExact (up to 128 rows): the logit of a row's main word, in eight parts,
+    int32_t shares;            // kExact (up to 128 rows): so many shares of
+    const double* exact;       // ... the logit of a row's main word,
     const float* main_weight;  // ... and that word's weight
     float* loss;
     float* lse;
@@ -365,11 +366,11 @@ __global__ void __launch_bounds__(32 * kWarps) loss_combine_kernel(const __grid_
     const int32_t r = (int32_t)blockIdx.x * kRows + row;
     const int32_t valid = p.rows ? __ldcg(&p.rows->valid) : p.T;
     const float c = p.log2_scale;
-    double exact[8] = {};
+    double exact = 0.0;
     float weight = 1.0f;
-    if (kExact && warp == 0 && lane < kRows && r < p.T) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) exact[j] = __ldcg(p.exact + 8 * (int64_t)r + j);
+    if (kExact && warp == 0 && r < p.T) {
+#pragma unroll 8
+        for (int32_t j = lane / kRows; j < p.shares; j += kLanes) exact += __ldcg(p.exact + (int64_t)r * p.shares + j);
         if (p.entropy) weight = __ldcg(p.main_weight + r);
     }
     float m = -INFINITY, s = 0.0f, z = 0.0f;
@@ -409,6 +410,10 @@ __global__ void __launch_bounds__(32 * kWarps) loss_combine_kernel(const __grid_
         z += part[2][j][row];
     }
     across();
+    if constexpr (kExact) {
+#pragma unroll
+        for (int d = kRows; d < 32; d <<= 1) exact += __shfl_xor_sync(0xffffffffu, exact, d);
+    }
     if (r >= p.T || lane >= kRows) return;
     const int32_t t = p.rows ? __ldcg(p.index + r) : r;
     bool in = r < valid;
@@ -429,13 +434,11 @@ __global__ void __launch_bounds__(32 * kWarps) loss_combine_kernel(const __grid_
             // logit from the exact sum, the others' share, s - 1, against that.  The
             // gradients take p - 1 there from that sum and lse, which from the truncated
             // one was off by up to 3e-5 (z = 28 over 2048).
-            double y = 0.0;
-            for (int j = 0; j < 8; ++j) y += exact[j];
-            const double over = y - (double)ref;
+            const double over = exact - (double)ref;
             const float d = (float)(over / (double)p.tau);
             if (fabsf(m) != INFINITY && expf(d) > 0.501f * s) {
                 log_s = log1pf((s - 1.0f) * expf(-d));
-                lse = (float)(y / (double)p.tau + (double)log_s);
+                lse = (float)(exact / (double)p.tau + (double)log_s);
                 gap = (float)((double)gap + over - (double)weight * over);
             }
         }
