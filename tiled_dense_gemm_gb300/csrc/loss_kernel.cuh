@@ -413,23 +413,6 @@ __device__ __forceinline__ void products_8(const WordSums& p, const uint16_t* x,
     }
 }
 
-// Thread i's of kSumThreads' share of that logit: 1/2048 of the products in each number
-// of 32 bits, and those in 64.
-__device__ __forceinline__ double some_products(const WordSums& p, int32_t t, int32_t word, int32_t i) {
-    const uint16_t *const x = p.X + (int64_t)t * p.ldx, *const w = p.W + (int64_t)word * p.w_word;
-    float sum[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    for (int32_t d = 8 * i; d < p.D; d += 8 * kSumThreads) {
-        float o[8];
-        products_8(p, x, w, d, o);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum[j] += o[j];
-    }
-    double z = 0.0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) z += (double)sum[j];
-    return z;
-}
-
 // A sum in two numbers of 32 bits, the second what rounding left of the first (Knuth's
 // exact sum of two): as exact as 64 bits here, whose additions take the GPU 64 clocks a
 // warp.
@@ -448,27 +431,42 @@ struct Wide {
     }
 };
 
+// Eight products more.
+__device__ __forceinline__ void add_8(Wide (&z)[2], const float (&o)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) z[j & 1].add(o[j]);
+}
+
+// Thread i's of kSumThreads' products of that logit.
+__device__ __forceinline__ double some_products(const WordSums& p, int32_t t, int32_t word, int32_t i) {
+    const uint16_t *const x = p.X + (int64_t)t * p.ldx, *const w = p.W + (int64_t)word * p.w_word;
+    Wide z[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+    for (int32_t d = 8 * i; d < p.D; d += 8 * kSumThreads) {
+        float o[8];
+        products_8(p, x, w, d, o);
+        add_8(z, o);
+    }
+    z[0].add(z[1].hi);
+    return (double)z[0].hi + (double)__fadd_rn(z[0].lo, z[1].lo);
+}
+
 // One of `shares` shares of that logit by one warp.
 __device__ __forceinline__ Wide exact_share(const WordSums& p, int32_t t, int32_t word, int32_t share, int32_t shares) {
     const uint16_t *const x = p.X + (int64_t)t * p.ldx, *const w = p.W + (int64_t)word * p.w_word;
     const int64_t vecs = p.D / 8;
     const int32_t end = 8 * (int32_t)((share + 1) * vecs / shares);
-    Wide z = {0.0f, 0.0f}, z2 = z;
+    Wide z[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
 #pragma unroll 2
     for (int32_t d = 8 * ((int32_t)(share * vecs / shares) + (int32_t)threadIdx.x % 32); d < end; d += 256) {
         float o[8];
         products_8(p, x, w, d, o);
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            z.add(o[j]);
-            z2.add(o[j + 1]);
-        }
+        add_8(z, o);
     }
-    z.add(z2.hi);
-    z.lo = __fadd_rn(z.lo, z2.lo);
+    z[0].add(z[1].hi);
+    z[0].lo = __fadd_rn(z[0].lo, z[1].lo);
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) z.add_lane(d);
-    return z;
+    for (int d = 16; d > 0; d >>= 1) z[0].add_lane(d);
+    return z[0];
 }
 
 // v[at], halving.

@@ -269,10 +269,10 @@ __global__ void __launch_bounds__(kRowsThreads) loss_rows_kernel(const __grid_co
 // * a copy of X with zeros in the rows that are not in use, for dW, and the scale;
 // * the gradient at the row's main word, if that is all but certain.  Little is
 //   left of p - q there, while the tensor core's z is off by up to 6e-6 of itself.  So z
-//   is summed once more, 1/2048 of the products in each number of 32 bits and those in
-//   64, as the forward pass has done for its lse, and 1 + expm1(z / tau - lse) taken for
-//   p; that goes over G's entry when the kernel of G is done.  (One row of 576, binary16,
-//   1 - p = 0.003, from an exact lse: dX off by 2.4e-4, its own rounding; 6.7e-3 without.)
+//   is summed once more, without loss, as the forward pass has done for its lse, and 1 +
+//   expm1(z / tau - lse) taken for p; that goes over G's entry when the kernel of G is
+//   done.  (One row of 576, binary16, 1 - p = 0.003, from an exact lse: dX off by 2.4e-4,
+//   its own rounding; 6.7e-3 without.)
 //
 // Of more rows the certain ones have little part in dX's and dW's size, and G's
 // kernel leaves no room beside it: 300 rows, 32008 words of 1000 by columns, 83 us
